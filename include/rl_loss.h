@@ -48,6 +48,7 @@
 #ifndef RL_LOSS_H
 #define RL_LOSS_H
 
+#include <stddef.h>
 #include <stdint.h>
 
 #ifdef __cplusplus
@@ -380,6 +381,146 @@ RL_LOSS_API int32_t rl_topk_max_k(void);
 RL_LOSS_API rl_status rl_topk(const rl_topk_config *config, int32_t rows, const float *scores, int64_t ld,
                               const int32_t *lengths, int32_t *out_idx, float *out_val, int64_t ldo,
                               uint32_t *device_status, void *stream);
+
+/* ---- Post-training losses over the whole vocabulary ---------------------------
+ * Operators next to the loss above that read the same packed rows of logits:
+ * the log-prob of the sampled tokens without a gradient (the pass of a
+ * reference or old policy), the loss with a KL term to a reference policy,
+ * distillation from a teacher known by its top logits, and a preference loss
+ * over pairs of responses. Shared rules: logits rows are logits_dtype, 16-byte
+ * aligned with ld * elem_size % 16 == 0, read up to V rounded up to 16 bytes; a
+ * -inf logit has probability 0; dlogits may alias logits when the strides are
+ * equal, its columns >= V are not written; rows with mask = 0 are not read (NaN
+ * or inf in them changes nothing) and get zero gradients. Softmax statistics
+ * are held in fp32, sums over tokens in fp64, all in an order that depends only
+ * on the sizes, so results repeat bit for bit. Nothing is allocated and no call
+ * synchronises; every call can be captured into a CUDA graph. Argument errors
+ * are returned before anything is launched. `device_status` (optional, device
+ * uint32) receives RL_ERR_TARGET_RANGE, RL_ERR_NONFINITE, RL_ERR_EMPTY_SEQ and
+ * RL_ERR_SEQLENS bits as rl_loss_get_device_status reports them, and
+ * RL_ERR_TIMEOUT if a bounded wait inside a kernel ran out (results are then not
+ * valid). */
+
+/* logp[t] = log softmax(z_t)[y_t] and, if entropy is non-NULL, the entropy of
+ * softmax(z_t) in nats. mask [T] u8 may be NULL (every token counts); logp and
+ * entropy of mask = 0 tokens are 0. A target outside [0, V): logp = NaN.
+ * RL_ERR_DTYPE, RL_ERR_SHAPE (T < 0, V outside [1, 2^24), ld < V),
+ * RL_ERR_INVALID_ARG (NULL pointer), RL_ERR_ALIGNMENT. One launch. */
+RL_LOSS_API rl_status rl_loss_token_logp(int32_t logits_dtype, int32_t num_tokens, int32_t vocab_size,
+                                         const void *logits, int64_t ld_logits, const int32_t *targets,
+                                         const uint8_t *mask, float *logp, float *entropy, uint32_t *device_status,
+                                         void *stream);
+
+/* Estimators of KL(pi_theta || pi_ref) from the sampled token, d_t = logp_t - logp_ref_t. */
+typedef enum rl_kl_estimator {
+    RL_KL_K1 = 0, /* d */
+    RL_KL_K2 = 1, /* d^2 / 2 */
+    RL_KL_K3 = 2  /* e^{-d} - 1 + d */
+} rl_kl_estimator;
+
+typedef struct rl_loss_kl {
+    const float *logp_ref; /* [T] log pi_ref(y_t) */
+    float coef;            /* weight of the KL term, finite, >= 0 */
+    int32_t estimator;     /* rl_kl_estimator */
+    float *kl;             /* [T] the estimate k_t (0 for mask = 0, NaN for a bad target), or NULL */
+    float *mean_kl;        /* [1] mean of k_t over mask = 1 tokens, or NULL */
+} rl_loss_kl;
+
+/* rl_loss_forward_backward with the KL term added to every mask = 1 token
+ * (popped and clipped ones too):
+ *   L = -sum_t w_t m_t (policy term)_t + coef * sum_t w_t m_t k_t,
+ * w_t the weight of loss_norm, k_t differentiated through logp_t. Inputs,
+ * outputs and the handle's configuration mean what they mean there, except that
+ * the logits of mask = 0 tokens are read only when outputs->logp or
+ * outputs->entropy is given (and count towards RL_ERR_NONFINITE only then).
+ * Errors as there, and RL_ERR_INVALID_ARG for a NULL kl or kl->logp_ref, an
+ * unknown estimator or a coefficient that is negative or not finite. Two
+ * launches (three with RL_NORM_PER_TOKEN). */
+RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t handle, const rl_loss_inputs *inputs,
+                                                  const rl_loss_kl *kl, const rl_loss_outputs *outputs, void *stream);
+
+/* Distillation from a teacher's top logits. Of the teacher, each row has the
+ * vocabulary positions of K entries (id -1: padding) and a value for each; the
+ * student is p = softmax(z / temperature) over the whole vocabulary. */
+typedef enum rl_distill_mode {
+    RL_DISTILL_RENORM = 0, /* q = softmax of the values over the entries: logits already divided by the
+                              temperature, or log-probs */
+    RL_DISTILL_TAIL = 1    /* values are log-probs at the temperature; what they leave of the mass,
+                              q_o = max(1 - sum q, tail_floor), is one more outcome, as is the student's
+                              mass outside the entries */
+} rl_distill_mode;
+
+typedef struct rl_loss_distill_config {
+    int32_t logits_dtype; /* rl_dtype of logits and dlogits */
+    int32_t vocab_size;   /* V, 1 <= V < 2^24 */
+    int32_t k;            /* entries per row, 1 <= k <= rl_loss_distill_max_k() */
+    int32_t mode;         /* rl_distill_mode */
+    int32_t reverse;      /* 0: KL(q || p), 1: KL(p || q) (RL_DISTILL_TAIL only: without a remaining mass the
+                             divergence from p to a truncated q is infinite) */
+    int32_t loss_norm;    /* rl_loss_norm */
+    float temperature;    /* > 0 */
+    float scale;          /* factor of the loss, e.g. temperature^2; finite */
+    float tail_floor;     /* in [0, 1): lower bound of q_o (RL_DISTILL_TAIL) */
+} rl_loss_distill_config;
+
+/* Largest k (1024). */
+RL_LOSS_API int32_t rl_loss_distill_max_k(void);
+RL_LOSS_API size_t rl_loss_distill_workspace_bytes(int32_t num_tokens, int32_t num_seqs);
+
+/* L = scale * sum_t w_t m_t KL_t and dlogits = dL/dz. teacher_ids, teacher_vals
+ * [T x ldk], cu_seqlens [S + 1]; kl [T] (optional) receives KL_t (0 for mask =
+ * 0). The ids of a row are distinct and in [0, V) or -1; a row where they are
+ * not is excluded (zero gradient, kl = NaN, RL_ERR_TARGET_RANGE). A row whose
+ * entries are all padding, or all -inf with RL_DISTILL_RENORM, contributes 0.
+ * 0 log 0 = 0. `workspace`: device, 256-byte aligned, at least
+ * rl_loss_distill_workspace_bytes(T, S), any contents, one per stream. Errors:
+ * RL_ERR_INVALID_ARG (NULL pointer, bad mode, norm or number), RL_ERR_DTYPE,
+ * RL_ERR_SHAPE (T < 0, S < 1, V, a stride), RL_ERR_UNSUPPORTED (k, reverse
+ * without a tail), RL_ERR_CAPACITY (workspace), RL_ERR_ALIGNMENT. Two launches. */
+RL_LOSS_API rl_status rl_loss_distill(const rl_loss_distill_config *config, int32_t num_tokens, int32_t num_seqs,
+                                      const void *logits, int64_t ld_logits, const int32_t *teacher_ids,
+                                      const float *teacher_vals, int64_t ldk, const uint8_t *mask,
+                                      const int32_t *cu_seqlens, float *loss, double *loss_f64, void *dlogits,
+                                      int64_t ld_dlogits, float *kl, void *workspace, size_t workspace_bytes,
+                                      uint32_t *device_status, void *stream);
+
+/* Preference loss over pairs: response 2j is preferred to response 2j + 1. With
+ *   s_i = sum_{t in i} m_t (logp_t - logp_ref_t)   (divided by |y_i| with length_norm),
+ *   D_j = s_{2j} - s_{2j+1},  h_j = beta D_j - margin:
+ *   RL_PREF_SIGMOID  -(1 - label_smoothing) log sigma(h) - label_smoothing log sigma(-h)
+ *   RL_PREF_HINGE    max(0, 1 - h)
+ *   RL_PREF_IPO      (D - 1 / (2 beta))^2
+ * each plus nll_coef times the mean negative log-prob of the preferred
+ * response's mask = 1 tokens; L is the mean over the pairs. A response without
+ * mask = 1 tokens has s_i = 0 (RL_ERR_EMPTY_SEQ); a token whose target is
+ * outside [0, V) is left out of the sums (logp = NaN, RL_ERR_TARGET_RANGE). */
+typedef enum rl_pref_loss { RL_PREF_SIGMOID = 0, RL_PREF_HINGE = 1, RL_PREF_IPO = 2 } rl_pref_loss;
+
+typedef struct rl_loss_pref_config {
+    int32_t logits_dtype;  /* rl_dtype of logits and dlogits */
+    int32_t vocab_size;    /* V, 1 <= V < 2^24 */
+    int32_t loss_type;     /* rl_pref_loss */
+    int32_t length_norm;   /* 0: sums, 1: means over the response's mask = 1 tokens */
+    float beta;            /* > 0 */
+    float margin;          /* finite (sigmoid and hinge) */
+    float label_smoothing; /* in [0, 1/2) (sigmoid) */
+    float nll_coef;        /* >= 0 */
+} rl_loss_pref_config;
+
+RL_LOSS_API size_t rl_loss_preference_workspace_bytes(int32_t num_tokens, int32_t num_seqs);
+
+/* targets [T], logp_ref [T] (NULL: 0, a loss without a reference), mask [T],
+ * cu_seqlens [S + 1], S even. Writes loss, dlogits and, where non-NULL, loss_f64,
+ * logp [T] (0 for mask = 0), seq_logratio [S] = s_i and pair_loss [S / 2].
+ * `workspace` as for rl_loss_distill, of rl_loss_preference_workspace_bytes.
+ * Errors: RL_ERR_INVALID_ARG, RL_ERR_DTYPE, RL_ERR_SHAPE (S < 2 or odd, T < 0, V,
+ * a stride), RL_ERR_CAPACITY, RL_ERR_ALIGNMENT. */
+RL_LOSS_API rl_status rl_loss_preference(const rl_loss_pref_config *config, int32_t num_tokens, int32_t num_seqs,
+                                         const void *logits, int64_t ld_logits, const int32_t *targets,
+                                         const float *logp_ref, const uint8_t *mask, const int32_t *cu_seqlens,
+                                         float *loss, double *loss_f64, void *dlogits, int64_t ld_dlogits, float *logp,
+                                         float *seq_logratio, float *pair_loss, void *workspace,
+                                         size_t workspace_bytes, uint32_t *device_status, void *stream);
 
 /* Synchronises `stream`, returns the accumulated device status bits
  * (1u << code for each rl_status code raised) in *bits and clears them. */

@@ -70,6 +70,31 @@ class rl_topk_config(ctypes.Structure):
 RL_TOPK_BY_SCORE, RL_TOPK_BY_POSITION = 0, 1
 
 
+class rl_loss_kl(ctypes.Structure):
+    _fields_ = [("logp_ref", ctypes.c_void_p), ("coef", ctypes.c_float), ("estimator", ctypes.c_int32),
+                ("kl", ctypes.c_void_p), ("mean_kl", ctypes.c_void_p)]
+
+
+class rl_loss_distill_config(ctypes.Structure):
+    _fields_ = [("logits_dtype", ctypes.c_int32), ("vocab_size", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("mode", ctypes.c_int32), ("reverse", ctypes.c_int32), ("loss_norm", ctypes.c_int32),
+                ("temperature", ctypes.c_float), ("scale", ctypes.c_float), ("tail_floor", ctypes.c_float)]
+
+
+class rl_loss_pref_config(ctypes.Structure):
+    _fields_ = [("logits_dtype", ctypes.c_int32), ("vocab_size", ctypes.c_int32), ("loss_type", ctypes.c_int32),
+                ("length_norm", ctypes.c_int32), ("beta", ctypes.c_float), ("margin", ctypes.c_float),
+                ("label_smoothing", ctypes.c_float), ("nll_coef", ctypes.c_float)]
+
+
+RL_KL_K1, RL_KL_K2, RL_KL_K3 = 0, 1, 2
+RL_DISTILL_RENORM, RL_DISTILL_TAIL = 0, 1
+RL_PREF_SIGMOID, RL_PREF_HINGE, RL_PREF_IPO = 0, 1, 2
+KL_ESTIMATORS = {"k1": RL_KL_K1, "k2": RL_KL_K2, "k3": RL_KL_K3}
+DISTILL_MODES = {"renorm": RL_DISTILL_RENORM, "tail": RL_DISTILL_TAIL}
+PREF_LOSSES = {"sigmoid": RL_PREF_SIGMOID, "hinge": RL_PREF_HINGE, "ipo": RL_PREF_IPO}
+
+
 class rl_loss_profile(ctypes.Structure):
     _fields_ = [("num_kernels", ctypes.c_int32), ("names", (ctypes.c_char * 32) * 12),
                 ("launches", ctypes.c_int64 * 12), ("total_ms", ctypes.c_double * 12)]
@@ -114,6 +139,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "rl_topk_max_k": ([], ctypes.c_int32),
         "rl_topk": ([ctypes.POINTER(rl_topk_config), ctypes.c_int32, P, ctypes.c_int64, P, P, P, ctypes.c_int64, P, P],
                     st),
+        "rl_loss_token_logp": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int64, P, P, P, P, P, P], st),
+        "rl_loss_forward_backward_kl": ([P, ctypes.POINTER(rl_loss_inputs), ctypes.POINTER(rl_loss_kl),
+                                         ctypes.POINTER(rl_loss_outputs), P], st),
+        "rl_loss_distill_max_k": ([], ctypes.c_int32),
+        "rl_loss_distill_workspace_bytes": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+        "rl_loss_distill": ([ctypes.POINTER(rl_loss_distill_config), ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int64,
+                             P, P, ctypes.c_int64, P, P, P, P, P, ctypes.c_int64, P, P, ctypes.c_size_t, P, P], st),
+        "rl_loss_preference_workspace_bytes": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+        "rl_loss_preference": ([ctypes.POINTER(rl_loss_pref_config), ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int64,
+                                P, P, P, P, P, P, P, ctypes.c_int64, P, P, P, P, ctypes.c_size_t, P, P], st),
         "rl_loss_projection_logits": ([P, P, ctypes.c_int64, P, ctypes.c_int64, ctypes.c_int32, P, ctypes.c_int64,
                                        P], st),
         "rl_loss_fused_projection_forward_backward": ([P, P, ctypes.c_int64, P, ctypes.c_int64,
@@ -300,6 +335,173 @@ def topk(scores, k: int, lengths=None, order: str = "score", out_idx=None, out_v
     return out_idx, out_val
 
 
+# ------------------------------------------------------------------ post-training losses without a handle
+
+def rl_loss_distill_max_k() -> int:
+    return int(load().rl_loss_distill_max_k())
+
+
+def rl_loss_distill_workspace_bytes(num_tokens: int, num_seqs: int) -> int:
+    return int(load().rl_loss_distill_workspace_bytes(int(num_tokens), int(num_seqs)))
+
+
+def rl_loss_preference_workspace_bytes(num_tokens: int, num_seqs: int) -> int:
+    return int(load().rl_loss_preference_workspace_bytes(int(num_tokens), int(num_seqs)))
+
+
+_POST_WORKSPACE: dict = {}
+
+
+def _post_workspace(need: int, device, stream: int):
+    """A workspace of this device and stream, grown when a call needs more and kept between calls. During a
+    graph capture the caller passes its own: one allocated here would belong to the graph's memory pool."""
+    import torch
+    ws = _POST_WORKSPACE.get((device, stream))
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("pass workspace= while a CUDA graph is captured (any torch.uint8 tensor of the size "
+                         "rl_loss_*_workspace_bytes gives, kept as long as the graph)")
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
+        _POST_WORKSPACE[(device, stream)] = ws
+    return ws
+
+
+def _logits_code(logits, vocab, dlogits=None):
+    """(dtype code, V, row stride) of a logits tensor, and the row stride of its gradient."""
+    import torch
+    code = {torch.float32: RL_F32, torch.bfloat16: RL_BF16}.get(logits.dtype)
+    if code is None or logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits is a CUDA tensor [tokens, vocabulary] of torch.float32 or torch.bfloat16")
+    if logits.stride(1) != 1 or (dlogits is not None and (dlogits.dim() != 2 or dlogits.stride(1) != 1)):
+        raise ValueError("the rows of logits and dlogits are contiguous")
+    V = logits.shape[1] if vocab is None else int(vocab)
+    if V > logits.shape[1]:
+        raise ValueError("vocab is larger than the logits' rows")
+    if dlogits is not None and (dlogits.dtype != logits.dtype or dlogits.shape[0] < logits.shape[0]
+                                or dlogits.shape[1] < V):
+        raise ValueError("dlogits has the type of logits and at least its rows and vocabulary")
+    return code, V
+
+
+def _vector(name: str, t, n: int, dtype, device, optional: bool = False):
+    """The pointer of a 1-D tensor argument after checking its type, length, place and layout."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype or t.numel() < n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} is a contiguous {dtype} tensor of at least {n} values on {device}")
+    return t.data_ptr()
+
+
+def token_logp(logits, targets, mask=None, *, vocab: int | None = None, logp=None, entropy=None,
+               want_entropy: bool = False, device_status=None, stream=None):
+    """Log-probs (and entropies) of the target tokens on the GPU, without a gradient: the pass of a reference
+    or old policy. Returns (logp [T], entropy [T] or None); mask = 0 tokens get 0 and their logits are not read."""
+    import torch
+    code, V = _logits_code(logits, vocab)
+    T, dev = logits.shape[0], logits.device
+    if logp is None:
+        logp = torch.empty(T, dtype=torch.float32, device=dev)
+    if entropy is None and want_entropy:
+        entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(logits.device).cuda_stream
+    f32 = torch.float32
+    _check(load().rl_loss_token_logp(code, T, V, logits.data_ptr(), logits.stride(0) if T else V,
+                                     _vector("targets", targets, T, torch.int32, dev),
+                                     _vector("mask", mask, T, torch.uint8, dev, True), _vector("logp", logp, T, f32, dev),
+                                     _vector("entropy", entropy, T, f32, dev, True), _ptr(device_status), stream),
+           "rl_loss_token_logp")
+    return logp, entropy
+
+
+def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: int | None = None, mode: str = "renorm",
+                 direction: str = "forward", temperature: float = 1.0, scale: float = 1.0, tail_floor: float = 0.0,
+                 loss_norm: int = RL_NORM_PER_RESPONSE, loss=None, loss_f64=None, dlogits=None, kl=None, workspace=None,
+                 device_status=None, stream=None) -> dict:
+    """Distillation from a teacher's top logits, forward and backward: teacher_ids / teacher_vals [T, K] hold
+    each row's entries (id -1: padding). mode "renorm" takes logits already divided by the temperature or
+    log-probs, "tail" log-probs at the temperature (what they leave of the mass is one more outcome);
+    direction "forward" is KL(teacher || student), "reverse" KL(student || teacher) ("tail" only). Returns
+    loss [1], kl [T] and dlogits (allocated where not given; dlogits may be logits itself)."""
+    import torch
+    if mode not in DISTILL_MODES or direction not in ("forward", "reverse"):
+        raise ValueError("mode is 'renorm' or 'tail', direction 'forward' or 'reverse'")
+    if dlogits is None:
+        dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
+    code, V = _logits_code(logits, vocab, dlogits)
+    T, S, dev, f32 = logits.shape[0], cu_seqlens.shape[0] - 1, logits.device, torch.float32
+    for name, t, dt in (("teacher_ids", teacher_ids, torch.int32), ("teacher_vals", teacher_vals, f32)):
+        if t.dtype != dt or t.dim() != 2 or t.shape[0] < T or t.device != dev or t.stride(1) != 1:
+            raise ValueError(f"{name} is a {dt} tensor [tokens, entries] with contiguous rows on {dev}")
+    if teacher_ids.shape != teacher_vals.shape or teacher_ids.stride(0) != teacher_vals.stride(0):
+        raise ValueError("teacher_ids and teacher_vals have one shape and layout")
+    if loss is None:
+        loss = torch.empty(1, dtype=f32, device=dev)
+    if kl is None:
+        kl = torch.empty(T, dtype=f32, device=dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(logits.device).cuda_stream
+    if workspace is None:
+        workspace = _post_workspace(rl_loss_distill_workspace_bytes(T, S), dev, stream)
+    cfg = rl_loss_distill_config(code, V, teacher_ids.shape[1], DISTILL_MODES[mode], int(direction == "reverse"),
+                                 loss_norm, temperature, scale, tail_floor)
+    _check(load().rl_loss_distill(ctypes.byref(cfg), T, S, logits.data_ptr(), logits.stride(0), teacher_ids.data_ptr(),
+                                  teacher_vals.data_ptr(), teacher_ids.stride(0),
+                                  _vector("mask", mask, T, torch.uint8, dev),
+                                  _vector("cu_seqlens", cu_seqlens, S + 1, torch.int32, dev),
+                                  _vector("loss", loss, 1, f32, dev),
+                                  _vector("loss_f64", loss_f64, 1, torch.float64, dev, True), dlogits.data_ptr(),
+                                  dlogits.stride(0), _vector("kl", kl, T, f32, dev), workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _ptr(device_status), stream),
+           "rl_loss_distill")
+    return {"loss": loss, "kl": kl, "dlogits": dlogits}
+
+
+def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int | None = None,
+                    loss_type: str = "sigmoid", length_norm: bool = False, beta: float = 0.1, margin: float = 0.0,
+                    label_smoothing: float = 0.0, nll_coef: float = 0.0, loss=None, loss_f64=None, dlogits=None,
+                    logp=None, seq_logratio=None, pair_loss=None, workspace=None, device_status=None,
+                    stream=None) -> dict:
+    """Preference loss over pairs of responses (2j preferred to 2j + 1), forward and backward. logp_ref [T] are
+    the reference policy's log-probs (None: no reference). Returns loss [1], logp [T], seq_logratio [S],
+    pair_loss [S / 2] and dlogits (allocated where not given; dlogits may be logits itself)."""
+    import torch
+    if loss_type not in PREF_LOSSES:
+        raise ValueError("loss_type is 'sigmoid', 'hinge' or 'ipo'")
+    if dlogits is None:
+        dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
+    code, V = _logits_code(logits, vocab, dlogits)
+    T, S, dev, f32 = logits.shape[0], cu_seqlens.shape[0] - 1, logits.device, torch.float32
+    if loss is None:
+        loss = torch.empty(1, dtype=f32, device=dev)
+    if logp is None:
+        logp = torch.empty(T, dtype=f32, device=dev)
+    if seq_logratio is None:
+        seq_logratio = torch.empty(max(S, 0), dtype=f32, device=dev)
+    if pair_loss is None:
+        pair_loss = torch.empty(max(S // 2, 0), dtype=f32, device=dev)
+    if stream is None:
+        stream = torch.cuda.current_stream(logits.device).cuda_stream
+    if workspace is None:
+        workspace = _post_workspace(rl_loss_preference_workspace_bytes(T, S), dev, stream)
+    cfg = rl_loss_pref_config(code, V, PREF_LOSSES[loss_type], int(length_norm), beta, margin, label_smoothing, nll_coef)
+    _check(load().rl_loss_preference(ctypes.byref(cfg), T, S, logits.data_ptr(), logits.stride(0),
+                                     _vector("targets", targets, T, torch.int32, dev),
+                                     _vector("logp_ref", logp_ref, T, f32, dev, True),
+                                     _vector("mask", mask, T, torch.uint8, dev),
+                                     _vector("cu_seqlens", cu_seqlens, S + 1, torch.int32, dev),
+                                     _vector("loss", loss, 1, f32, dev),
+                                     _vector("loss_f64", loss_f64, 1, torch.float64, dev, True), dlogits.data_ptr(),
+                                     dlogits.stride(0), _vector("logp", logp, T, f32, dev),
+                                     _vector("seq_logratio", seq_logratio, S, f32, dev),
+                                     _vector("pair_loss", pair_loss, S // 2, f32, dev), workspace.data_ptr(),
+                                     workspace.numel() * workspace.element_size(), _ptr(device_status), stream),
+           "rl_loss_preference")
+    return {"loss": loss, "logp": logp, "seq_logratio": seq_logratio, "pair_loss": pair_loss, "dlogits": dlogits}
+
+
 def rl_loss_version() -> int:
     return int(load().rl_loss_version())
 
@@ -375,6 +577,30 @@ class RlLoss:
             stream = torch.cuda.current_stream().cuda_stream
         self._raise(rl_loss_forward_backward_from_host(self.handle, inputs(host), inputs(device), out, num_chunks,
                                                        stream), "rl_loss_forward_backward_from_host")
+
+    def forward_backward_kl(self, logits, targets, logp_old, logp_infer, mask, cu_seqlens, rewards_or_adv, logp_ref, *,
+                            kl_coef: float, kl_estimator: str = "k3", loss, dlogits, loss_f64=None, logp=None,
+                            entropy=None, flags=None, seq_adv=None, counts=None, mean_entropy=None, kl=None,
+                            mean_kl=None, stream=None) -> None:
+        """forward_backward with a KL term to a reference policy (its log-probs logp_ref [T]): kl_coef times the
+        "k1", "k2" or "k3" estimate of every mask = 1 token. kl [T] and mean_kl [1] receive the estimates."""
+        import torch
+        if kl_estimator not in KL_ESTIMATORS:
+            raise ValueError("kl_estimator is 'k1', 'k2' or 'k3'")
+        T = int(targets.shape[0])
+        dev, f32 = targets.device, torch.float32
+        inp = rl_loss_inputs(T, int(cu_seqlens.shape[0]) - 1, int(logits.stride(0)) if logits.dim() == 2 else 0,
+                             _ptr(logits), _ptr(targets), _ptr(logp_old), _ptr(logp_infer), _ptr(mask),
+                             _ptr(cu_seqlens), _ptr(rewards_or_adv))
+        out = rl_loss_outputs(_ptr(loss), _ptr(loss_f64), _ptr(dlogits),
+                              int(dlogits.stride(0)) if dlogits.dim() == 2 else 0, _ptr(logp), _ptr(entropy),
+                              _ptr(flags), _ptr(seq_adv), _ptr(counts), _ptr(mean_entropy))
+        term = rl_loss_kl(_vector("logp_ref", logp_ref, T, f32, dev), kl_coef, KL_ESTIMATORS[kl_estimator],
+                          _vector("kl", kl, T, f32, dev, True), _vector("mean_kl", mean_kl, 1, f32, dev, True))
+        if stream is None:
+            stream = torch.cuda.current_stream().cuda_stream
+        self._raise(load().rl_loss_forward_backward_kl(self.handle, ctypes.byref(inp), ctypes.byref(term),
+                                                       ctypes.byref(out), stream), "rl_loss_forward_backward_kl")
 
     def _raise(self, code: int, what: str):
         if code == CODES["RL_ERR_CUDA"]:

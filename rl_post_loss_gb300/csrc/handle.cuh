@@ -6,6 +6,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "post.cuh"
 
 // Kernel classes timed by rl_loss_profile_start / rl_loss_profile_read.
 enum RlKernelClass {
@@ -18,11 +19,12 @@ enum RlKernelClass {
     kProjRows,
     kProjBwd,     // both products of the projection backward (one tcgen05 launch per chunk)
     kEntropyFix,  // the entropy of rows holding -inf logits
+    kPolicyKl,    // the row kernel of the loss with a KL term
     kNumKernels
 };
 static const char *const kKernelNames[kNumKernels] = {"seg_prep",  "token_prep", "row_loss", "seg_reduce",
                                                       "final_reduce", "proj_gemm", "proj_rows", "proj_bwd",
-                                                      "entropy_fix"};
+                                                      "entropy_fix",  "policy_kl"};
 constexpr size_t kProfSlotsPerCall = 160;  // enough for a projection call of 32 chunks (or a host call of 64 blocks)
 constexpr int kMaxCopyChunks = 64;         // logits blocks of rl_loss_forward_backward_from_host
 
@@ -45,6 +47,8 @@ struct rl_loss_handle_s {
     float4 *tok_rec;
     uint32_t *tok_meta;
     float *loss_scratch;
+    rlk::PostPartial *post_partials;  // [kPostMaxBlocks], of the loss with a KL term
+    uint32_t *post_done;              // blocks that filled their slot (zero between calls)
     // bookkeeping
     int64_t launches;
     cudaError_t last_cuda_error;  // the CUDA error behind the last RL_ERR_CUDA of this handle

@@ -1,0 +1,460 @@
+// The vocabulary-wide post-training operators: parameters and per-row mathematics shared by their
+// kernels (sm_103a).
+//
+//   logp     logp_t = z_y - log sum_v exp z_v and the entropy, forward only
+//   policy   Eq. (1) (or DIS) plus a KL term to a reference policy
+//   distill  KL between a teacher known by its top entries and the student softmax(z / tau)
+//   pref     a preference loss over pairs of responses
+//
+// Every gradient row is one coefficient times the row's exponentials, plus a few entries of its own
+// (the sampled token, or the teacher's entries). Exponentials are taken in base 2 against the row's
+// own maximum, 2^{c (z_v - m)} with c = log2(e) / tau and m = max z_v, and the sum S is kept apart
+// from m: ln p_v = (c (z_v - m) - log2 S) ln 2 has no large term to cancel, so a log-prob near 0
+// keeps its digits, and p_v = 2^{c (z_v - m)} / S costs one multiplication by a per-row constant.
+// The difference is taken before the factor c: it is exact for entries near the maximum, and 0 at
+// it, whatever the size of the logits.
+#pragma once
+
+#include <cfloat>
+
+#include "common.cuh"
+
+namespace rlk {
+
+// ---------------------------------------------------------------- logits of either type
+
+template <typename T>
+struct PostVec;
+
+template <>
+struct PostVec<float> {
+    static constexpr int kElems = 4;
+    __device__ __forceinline__ static void decode(const uint4 &v, float (&x)[4]) {
+        x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+    __device__ __forceinline__ static uint4 encode(const float (&x)[4]) {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    __device__ __forceinline__ static float load1(const void *p, int64_t v) { return reinterpret_cast<const float *>(p)[v]; }
+    __device__ __forceinline__ static void store1(void *p, int64_t v, float x) { reinterpret_cast<float *>(p)[v] = x; }
+};
+
+template <>
+struct PostVec<__nv_bfloat16> {
+    static constexpr int kElems = 8;
+    __device__ __forceinline__ static void decode(const uint4 &v, float (&x)[8]) {
+        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
+        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+    }
+    __device__ __forceinline__ static uint4 encode(const float (&x)[8]) {
+        return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+    }
+    __device__ __forceinline__ static float load1(const void *p, int64_t v) {
+        return __uint_as_float((uint32_t) reinterpret_cast<const unsigned short *>(p)[v] << 16);
+    }
+    __device__ __forceinline__ static void store1(void *p, int64_t v, float x) {
+        reinterpret_cast<__nv_bfloat16 *>(p)[v] = __float2bfloat16_rn(x);
+    }
+};
+
+// ---------------------------------------------------------------- running statistics
+
+// Running softmax statistics of part of a row: the reference m (its maximum), s = sum 2^d and
+// u = sum 2^d d with d = c (z - m). They start from a finite reference point, so that a -inf logit
+// is 2^-inf = 0 against it; merging a start that saw nothing scales its zero sums by 0.
+struct PostStats {
+    float m, s, u;
+};
+constexpr PostStats kPostStart{-FLT_MAX, 0.f, 0.f};
+
+// Where d is below this, 2^d is 0 in fp32: products 2^d d hold d here, so that they are 0 and not
+// 0 times infinity.
+constexpr float kNoWeight = -1024.f;
+
+// Moves partial statistics to the reference M >= st.m.
+template <bool kEnt>
+__device__ __forceinline__ void post_rescale(PostStats &st, float M, float c) {
+    const float dm = __fmul_rn(__fsub_rn(st.m, M), c);
+    const float f = ex2_approx(dm);
+    if (kEnt) st.u = __fmul_rn(f, __fadd_rn(st.u, __fmul_rn(fmaxf(dm, kNoWeight), st.s)));
+    st.s = __fmul_rn(st.s, f);
+    st.m = M;
+}
+
+// Folds a group of logits into the statistics (one rescale at most). A logit of -inf adds 0 to u
+// (0 log 0 = 0), while e comes from d itself, so that a NaN reaches s.
+template <bool kEnt, int N>
+__device__ __forceinline__ void post_fold(PostStats &st, const float (&x)[N], float c) {
+    float mv = x[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) mv = fmaxf(mv, x[k]);
+    if (mv > st.m) post_rescale<kEnt>(st, mv, c);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const float d = (x[k] - st.m) * c;
+        const float e = ex2_approx(d);
+        st.s += e;
+        if (kEnt) st.u = fmaf(e, fmaxf(d, kNoWeight), st.u);
+    }
+}
+
+// Merges two partial statistics; symmetric in its arguments, so a butterfly leaves the same bits in
+// every lane.
+template <bool kEnt>
+__device__ __forceinline__ PostStats post_merge(PostStats a, PostStats b, float c) {
+    const float M = fmaxf(a.m, b.m);
+    post_rescale<kEnt>(a, M, c);
+    post_rescale<kEnt>(b, M, c);
+    return PostStats{M, __fadd_rn(a.s, b.s), kEnt ? __fadd_rn(a.u, b.u) : 0.f};
+}
+
+template <bool kEnt>
+__device__ __forceinline__ PostStats post_warp_merge(PostStats r, float c) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        PostStats o{__shfl_xor_sync(0xffffffffu, r.m, off), __shfl_xor_sync(0xffffffffu, r.s, off),
+                    kEnt ? __shfl_xor_sync(0xffffffffu, r.u, off) : 0.f};
+        r = post_merge<kEnt>(r, o, c);
+    }
+    return r;
+}
+
+__device__ __forceinline__ void post_raise(uint32_t *status, rl_status code) {
+    if (status) raise_status(status, code);  // the status word is optional for the entry points without a handle
+}
+
+// ---------------------------------------------------------------- parameters
+
+// What one block adds to the batch's sums (blocks take rows in a fixed stride, in increasing order).
+struct PostPartial {
+    double loss, ent, kl;
+    int32_t n, popped, clipped, masked;
+};
+
+struct PostRows {
+    const void *logits;
+    int64_t ld;
+    void *dlogits;
+    int64_t ldd;
+    int32_t T, V, S;
+    const int32_t *targets;
+    const uint8_t *mask;         // may be null (logp): every row counts
+    const int32_t *cu_seqlens;
+    float *logp;                 // optional for policy and pref
+    float *entropy;              // optional
+    uint32_t *status;            // optional
+    // sums of the batch: one slot per block, and the count of blocks that have filled theirs
+    PostPartial *partials;
+    uint32_t *blocks_done;
+    float *loss;
+    double *loss_f64;
+};
+
+// pref: the statistics of every row (m, S), kept from the log-prob pass for the gradient pass
+struct LogpParams {
+    PostRows r;
+    float2 *stats;               // optional [T]
+    uint32_t *zero;              // optional: a word this launch sets to 0 for the next one
+};
+
+struct KlTerm {
+    const float *logp_ref;       // [T]
+    float coef;
+    int32_t estimator;           // rl_kl_estimator
+    float *kl;                   // optional [T]
+    float *mean_kl;              // optional [1]
+};
+
+struct PolicyParams {
+    PostRows r;
+    LossConsts c;
+    const float *logp_old, *logp_infer;
+    const float *token_adv;      // RL_ADV_PER_TOKEN, else null
+    const float *teacher;        // RL_ADV_TEACHER_LOGP, else null
+    const float *seq_adv, *seq_w;
+    const double *seq_w64;
+    const int32_t *seq_n;
+    uint8_t *flags;              // optional
+    int32_t *counts;             // optional
+    float *mean_entropy;         // optional
+    int32_t read_masked;         // the log-probs or entropies of masked tokens are wanted
+    KlTerm kl;
+};
+
+struct DistillParams {
+    PostRows r;
+    const int32_t *ids;          // [T, ldk]
+    const float *vals;           // [T, ldk]
+    int64_t ldk;
+    int32_t K, tail, reverse, per_token;
+    float c;                     // log2(e) / tau
+    float inv_tau, scale;
+    const float4 *rec;           // [T] {m, ln sum, q_rest, Q} of the teacher's row (distill_prep)
+    const int32_t *seq_n;        // [S]
+    float *kl;                   // optional [T]
+};
+
+struct DistillPrepParams {
+    const int32_t *ids;
+    const float *vals;
+    int64_t ldk;
+    int32_t K, T, S, tail;
+    float floor;
+    const uint8_t *mask;
+    const int32_t *cu_seqlens;
+    float4 *rec;
+    int32_t *seq_n;
+    uint32_t *blocks_done;       // set to 0
+    uint32_t *status;
+};
+
+struct PrefPairParams {
+    int32_t T, S, V;
+    const int32_t *targets;
+    const uint8_t *mask;
+    const int32_t *cu_seqlens;
+    const float *logp, *logp_ref;
+    int32_t kind, mean;
+    float beta, smoothing, margin, nll;
+    float *coef;                 // [S] dL/dlogp of the response's tokens
+    double *pair64;              // [S/2]
+    float *seq_logratio, *pair_loss;  // optional
+    uint32_t *pairs_done;
+    float *loss;
+    double *loss_f64;
+    uint32_t *status;
+};
+
+struct ScaleParams {
+    PostRows r;
+    const float2 *stats;         // [T] (m, S)
+    const float *coef;           // [S]
+};
+
+cudaError_t launch_post_logp(const LogpParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_post_policy(const PolicyParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_distill_prep(const DistillPrepParams &p, cudaStream_t stream);
+cudaError_t launch_post_distill(const DistillParams &p, int dtype, cudaStream_t stream);
+cudaError_t launch_pref_pairs(const PrefPairParams &p, cudaStream_t stream);
+cudaError_t launch_post_scale(const ScaleParams &p, int dtype, cudaStream_t stream);
+
+constexpr int kPostMaxBlocks = 4096;  // slots of PostRows::partials
+constexpr int kDistillMaxK = 1024;    // the teacher's entries of a row stay in shared memory
+
+// ---------------------------------------------------------------- the sampled token
+
+// The statistics of a row are finite: no NaN or +inf logit, and not every logit -inf.
+__device__ __forceinline__ bool post_finite(PostStats st) { return st.s > 0.f && st.s < INFINITY && fabsf(st.m) < INFINITY; }
+
+// The row's statistics leave the sampled entry out: `rest` are those of the others, zy its logit.
+// With x = sum_{v != y} 2^d 2^{c (m_rest - z_y)} = (1 - p_y) / p_y, ln p_y = -log1p(x) keeps its
+// relative accuracy as p_y nears 1, which 1 + x has lost. Returns ln p_y (NaN where the row is not
+// finite) and the whole row's statistics in `all`.
+template <bool kEnt>
+__device__ __forceinline__ float post_target(PostStats rest, float zy, float c, PostStats &all) {
+    PostStats y = kPostStart;
+    const float one[1] = {zy};
+    post_fold<kEnt>(y, one, c);
+    all = post_merge<kEnt>(rest, y, c);
+    if (!post_finite(all)) return __int_as_float(0x7fc00000);
+    if (zy >= rest.m) return -log1pf(rest.s * ex2_approx((rest.m - zy) * c));
+    return ((zy - rest.m) * c - log2f(all.s)) * kLn2;
+}
+
+__device__ __forceinline__ float post_entropy(PostStats st) { return (log2f(st.s) - st.u / st.s) * kLn2; }
+
+// Estimators of KL(pi || pi_ref) from the sampled token, d = logp - logp_ref, and their derivative
+// in logp: d; d^2 / 2; e^{-d} - 1 + d, whose first two terms cancel near 0, where its series is
+// summed instead (|d| < 1/4: kl / d^2 = 1/2 - d/6 + ..., the first term left out is d^8 / 10! < 5e-12).
+__device__ __forceinline__ void post_kl(int estimator, float d, float &kl, float &grad) {
+    if (estimator == RL_KL_K1) {
+        kl = d;
+        grad = 1.f;
+    } else if (estimator == RL_KL_K2) {
+        kl = 0.5f * d * d;
+        grad = d;
+    } else {
+        const float em1 = expm1f(-d);
+        grad = -em1;
+        if (fabsf(d) < 0.25f) {
+            float q = 1.f / 362880.f;
+            q = fmaf(-d, q, 1.f / 40320.f);
+            q = fmaf(-d, q, 1.f / 5040.f);
+            q = fmaf(-d, q, 1.f / 720.f);
+            q = fmaf(-d, q, 1.f / 120.f);
+            q = fmaf(-d, q, 1.f / 24.f);
+            q = fmaf(-d, q, 1.f / 6.f);
+            q = fmaf(-d, q, 0.5f);
+            kl = d * d * q;
+        } else {
+            kl = em1 + d;
+        }
+    }
+}
+
+// What pass 2 of a row needs: dz_v = a 2^{c (z_v - m)}, and dz_y = gy at the sampled token.
+struct RowGrad {
+    float a, m, gy;
+    int32_t y;  // -1: no entry of its own
+};
+
+__device__ __forceinline__ RowGrad post_row_grad(float g, PostStats st, float logp, int y) {
+    return RowGrad{-g / st.s, st.m, -g * expm1f(logp), y};
+}
+
+// The token objective, its KL term and every per-token output of a policy row; adds the row to
+// `sum` and returns its gradient. `st` are the
+// whole row's statistics, `logp` its ln p_y (0 where the row was not read). `write` false: another
+// block writes the row's outputs and sums.
+__device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, PostStats st, float logp, bool write,
+                                              PostPartial &sum) {
+    const int i = find_seq(p.r.cu_seqlens, p.r.S, t);
+    if (i < 0 && write) post_raise(p.r.status, RL_ERR_SEQLENS);
+    const float A = p.token_adv ? __ldg(p.token_adv + t) : (i >= 0 ? p.seq_adv[i] : 0.f);
+    const float w = i >= 0 ? p.seq_w[i] : 0.f;
+    const int y = __ldg(p.r.targets + t);
+    const bool ok = y >= 0 && y < p.r.V;
+    const bool m = i >= 0 && __ldg(p.r.mask + t) != 0;
+    const bool read = m || p.read_masked;
+    const float lo = __ldg(p.logp_old + t);
+    const float d = __fsub_rn(lo, __ldg(p.logp_infer + t));  // ln rho, one fp32 subtraction
+    const bool in_bounds = (-p.c.ln_beta <= d) && (d <= p.c.ln_beta);
+    uint32_t pre = (m ? 0u : RL_FLAG_MASKED) | (ok ? 0u : RL_FLAG_BAD_TARGET) | (A > 0.f ? kPreAPos : 0u) |
+                   (A < 0.f ? kPreANeg : 0u);
+    float cf = 0.f, lref = lo;
+    if (p.c.objective == RL_OBJ_DIS) {
+        lref = __ldg(p.logp_infer + t);
+        if (m && ok) cf = A;
+    } else {
+        pre |= in_bounds ? RL_FLAG_POP_IN_BOUNDS : 0u;
+        const float pop = (m && ok && in_bounds) ? (p.c.pop_indicator ? 1.f : expf(d)) : 0.f;
+        cf = p.c.adv_teacher ? pop : pop * A;
+    }
+    const float4 rec = make_float4(0.f, lref, cf, w * cf);
+    const uint32_t meta = (ok ? (uint32_t)y : 0u) | (pre << 24);
+    RowOut o = finish_row(RowStats2{0.f, st.s, st.u}, rec, meta, p.c, p.teacher ? __ldg(p.teacher + t) : 0.f, &logp);
+    if (!read) {  // nothing of the row was read: no log-prob, and the clip test has nothing to test
+        o.H = 0.f;
+        o.flags &= ~(RL_FLAG_CLIP_ACTIVE | (p.c.objective == RL_OBJ_DIS ? RL_FLAG_POP_IN_BOUNDS : 0u));
+    }
+    float kl = 0.f, dkl = 0.f;
+    const bool counts = m && ok;
+    if (counts) post_kl(p.kl.estimator, __fsub_rn(o.logp, __ldg(p.kl.logp_ref + t)), kl, dkl);
+    const float g = counts ? fmaf(w * p.kl.coef, dkl, o.g) : 0.f;
+    if (write) {
+        if (!ok) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
+        if (read && !post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
+        if (p.r.logp) p.r.logp[t] = ok ? o.logp : __int_as_float(0x7fc00000);
+        if (p.r.entropy) p.r.entropy[t] = o.H;
+        if (p.flags) p.flags[t] = (uint8_t)o.flags;
+        if (p.kl.kl) p.kl.kl[t] = m && !ok ? __int_as_float(0x7fc00000) : kl;
+        if (i >= 0) sum.loss += p.seq_w64[i] * ((double)p.kl.coef * (double)kl - (double)o.obj);
+        if (m) {
+            sum.n += 1;
+            sum.ent += (double)o.H;
+            sum.kl += (double)kl;
+            sum.popped += !(o.flags & RL_FLAG_POP_IN_BOUNDS);
+            sum.clipped += (o.flags & RL_FLAG_CLIP_ACTIVE) != 0;
+        } else {
+            sum.masked += 1;
+        }
+    }
+    return g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : post_row_grad(g, st, o.logp, y);
+}
+
+// ---------------------------------------------------------------- the teacher's entries
+
+// One row of distillation after its statistics: dz_v = ct 2^{c (z_v - m)} outside the teacher's
+// entries, and distill_entry() at them.
+struct DistillRow {
+    float ct, m;           // tail: coefficient and reference
+    float M, l2s;          // the whole row: reference and log2 S
+    float kl, w;           // the row's divergence; its weight * scale / tau
+    float Q;               // total mass of the teacher's distribution
+};
+
+// Statistics of the student over the teacher's entries, by one warp. s_z[k] holds the student's
+// logit at entry k (-inf where the entry is padding).
+__device__ __forceinline__ void distill_entry_stats(const float *s_z, int K, float c, float &M, float &S) {
+    const int lane = threadIdx.x & 31;
+    float m = -FLT_MAX;
+    for (int k = lane; k < K; k += 32) m = fmaxf(m, s_z[k]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float s = 0.f;
+    for (int k = lane; k < K; k += 32) s += ex2_approx((s_z[k] - m) * c);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
+    M = m;
+    S = s;
+}
+
+// The row's divergence and coefficients, by one warp. `tail` are the statistics of the vocabulary
+// outside the teacher's entries, s_lq[k] the teacher's log-prob of entry k, rec of distill_prep,
+// w the row's weight * scale / tau, n_rest the number of vocabulary entries outside the teacher's.
+//
+// With q_o = rec.z the teacher's remaining mass and p_o the student's (forward, the remaining mass
+// being one more outcome):
+//   KL = sum_k q_k ln(q_k / p_k) + q_o ln(q_o / p_o),  dKL/dz'_v = Q p_v - q_v  (an entry),
+//                                                                  Q p_v - q_o p_v / p_o  (outside)
+// renormalised: q_o = 0, Q = 1. Reverse:
+//   KL = sum_k p_k a_k + p_o a_o,  a = ln(p / q),  dKL/dz'_v = p_v (a_v - KL), a_v = a_o outside.
+// p_o is the sum of the entries outside, not 1 - sum_k p_k, which would cancel.
+__device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, PostStats tail, float Mk, float Sk,
+                                                     const float *s_z, const float *s_lq, float4 rec, float w, int n_rest) {
+    const int lane = threadIdx.x & 31;
+    DistillRow r;
+    r.w = w;
+    r.Q = rec.w;
+    r.m = tail.m;
+    r.M = fmaxf(Mk, tail.m);
+    const float dt = (tail.m - r.M) * p.c;
+    const float ft = ex2_approx(dt);
+    const float S = __fadd_rn(__fmul_rn(Sk, ex2_approx((Mk - r.M) * p.c)), __fmul_rn(tail.s, ft));
+    r.l2s = log2f(S);
+    float kl = 0.f;
+    for (int k = lane; k < p.K; k += 32) {
+        const float lp2 = (s_z[k] - r.M) * p.c - r.l2s;
+        const float lq = s_lq[k];
+        if (p.reverse) {
+            const float pk = ex2_approx(lp2);
+            if (pk > 0.f) kl = fmaf(pk, fmaf(lp2, kLn2, -lq), kl);
+        } else {
+            const float q = expf(lq);
+            if (q > 0.f) kl = fmaf(q, lq - lp2 * kLn2, kl);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) kl = __fadd_rn(kl, __shfl_xor_sync(0xffffffffu, kl, off));
+    const float inv_s = 1.f / S;
+    float ct;
+    if (p.tail && n_rest > 0) {
+        // ln p_o from the tail's own reference, so that a tail far below the row's maximum keeps its log
+        const float lpo = (dt + (log2f(tail.s) - r.l2s)) * kLn2;
+        const float qo = rec.z, lqo = logf(qo);
+        if (p.reverse) {
+            const float po = tail.s * ft * inv_s;
+            const float ao = lpo - lqo;
+            if (po > 0.f) kl = fmaf(po, ao, kl);
+            ct = tail.s > 0.f ? (ao - kl) * ft * inv_s : 0.f;
+        } else {
+            if (qo > 0.f) kl = fmaf(qo, lqo - lpo, kl);
+            ct = tail.s > 0.f ? r.Q * ft * inv_s - qo / tail.s : 0.f;
+        }
+    } else {
+        ct = p.reverse ? -kl * ft * inv_s : r.Q * ft * inv_s;
+    }
+    r.kl = kl;
+    r.ct = w * ct;
+    return r;
+}
+
+// dL/dz of one of the teacher's entries.
+__device__ __forceinline__ float distill_entry(const DistillParams &p, const DistillRow &r, float z, float lq) {
+    const float lp2 = (z - r.M) * p.c - r.l2s;
+    const float pk = ex2_approx(lp2);
+    if (!p.reverse) return r.w * fmaf(r.Q, pk, -expf(lq));
+    return pk == 0.f ? 0.f : r.w * pk * (fmaf(lp2, kLn2, -lq) - r.kl);
+}
+
+}  // namespace rlk

@@ -1,0 +1,170 @@
+// The small kernels around the post-training operators' row kernels: the teacher's normalisers and
+// the responses' token counts (distill), and the pairs' losses and coefficients (pref).
+#include <algorithm>
+
+#include "post.cuh"
+
+namespace rlk {
+
+namespace {
+
+constexpr int kPrepThreads = 256;
+
+// The token range of response i, clamped into [0, T]; raises RL_ERR_SEQLENS where it is malformed.
+__device__ __forceinline__ int2 seq_range(const int32_t *cu, int S, int T, int i, uint32_t *status) {
+    int b = __ldg(cu + i), e = __ldg(cu + i + 1);
+    if ((b < 0) || (e < b) || (e > T) || (i == 0 && b != 0) || (i == S - 1 && e != T)) {
+        if (threadIdx.x == 0) post_raise(status, RL_ERR_SEQLENS);
+        b = min(max(b, 0), T);
+        e = min(max(e, b), T);
+    }
+    return make_int2(b, e);
+}
+
+// Blocks [0, S) count the mask=1 tokens of one response each; the others take eight rows each, a
+// warp per row: ln of the teacher's normaliser, its remaining mass and its total mass. A teacher
+// given by log-probs keeps them (m = ln sum = 0) and its remaining mass is 1 - sum q in fp64: with
+// most of the mass in the entries, fp32 would leave it no digits.
+__global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepParams p) {
+    __shared__ int s_i[32];
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.blocks_done = 0;
+    if ((int)blockIdx.x < p.S) {
+        const int i = blockIdx.x;
+        const int2 r = seq_range(p.cu_seqlens, p.S, p.T, i, p.status);
+        int n = 0;
+#pragma unroll 4
+        for (int t = r.x + threadIdx.x; t < r.y; t += kPrepThreads) n += __ldg(p.mask + t) ? 1 : 0;
+        n = block_sum_i32(n, s_i);
+        if (threadIdx.x == 0) {
+            p.seq_n[i] = n;
+            if (n == 0) post_raise(p.status, RL_ERR_EMPTY_SEQ);
+        }
+        return;
+    }
+    const int lane = threadIdx.x & 31;
+    const int64_t t = ((int64_t)blockIdx.x - p.S) * (kPrepThreads / 32) + (threadIdx.x >> 5);
+    if (t >= p.T || !__ldg(p.mask + t)) return;
+    const int32_t *ids = p.ids + t * p.ldk;
+    const float *vals = p.vals + t * p.ldk;
+    float4 rec = make_float4(0.f, 0.f, 0.f, 1.f);
+    if (p.tail) {
+        double q = 0.0;
+        for (int k = lane; k < p.K; k += 32)
+            if (__ldg(ids + k) >= 0) q += exp((double)__ldg(vals + k));
+        q = warp_sum_f64(q);
+        const double rest = fmax(1.0 - q, (double)p.floor);
+        rec.z = (float)rest;
+        rec.w = (float)(q + rest);
+    } else {
+        float m = -INFINITY;
+        bool nan = false;
+        for (int k = lane; k < p.K; k += 32) {
+            if (__ldg(ids + k) < 0) continue;
+            const float v = __ldg(vals + k);
+            nan |= isnan(v);
+            m = fmaxf(m, v);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        nan = __any_sync(0xffffffffu, nan);
+        double s = 0.0;
+        if (m > -INFINITY)
+            for (int k = lane; k < p.K; k += 32)
+                if (__ldg(ids + k) >= 0) s += (double)expf(__ldg(vals + k) - m);
+        s = warp_sum_f64(s);
+        rec.x = m;
+        rec.y = (float)log(s);
+        rec.w = nan ? __int_as_float(0x7fc00000) : m > -INFINITY ? 1.f : 0.f;  // no entry with mass: 0
+    }
+    if (lane == 0) p.rec[t] = rec;
+}
+
+// One block per pair (responses 2j and 2j + 1): the log ratios of both in fp64 in token order, the
+// pair's loss and the coefficients dL/dlogp of their tokens. The last block sums the losses in pair
+// order.
+__global__ void __launch_bounds__(kPrepThreads) pref_pairs_kernel(PrefPairParams p) {
+    __shared__ double s_d[32];
+    __shared__ int s_i[32];
+    __shared__ int s_last;
+    const int j = blockIdx.x, P = p.S / 2;
+    double ratio[2], like = 0.0;
+    int n[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int2 r = seq_range(p.cu_seqlens, p.S, p.T, 2 * j + h, p.status);
+        double lp = 0.0, lr = 0.0;
+        int c = 0;
+#pragma unroll 4
+        for (int t = r.x + threadIdx.x; t < r.y; t += kPrepThreads) {
+            if (!__ldg(p.mask + t)) continue;
+            c += 1;
+            if ((uint32_t)__ldg(p.targets + t) >= (uint32_t)p.V) continue;  // the token is excluded
+            lp += (double)p.logp[t];
+            if (p.logp_ref) lr += (double)__ldg(p.logp_ref + t);
+        }
+        lp = block_sum_f64(lp, s_d);
+        lr = block_sum_f64(lr, s_d);
+        n[h] = block_sum_i32(c, s_i);
+        const double per = p.mean ? (n[h] > 0 ? 1.0 / n[h] : 0.0) : 1.0;
+        ratio[h] = (lp - lr) * per;
+        if (h == 0) like = n[0] > 0 ? -lp / n[0] : 0.0;
+    }
+    if (threadIdx.x == 0) {
+        if (n[0] == 0 || n[1] == 0) post_raise(p.status, RL_ERR_EMPTY_SEQ);
+        const double beta = p.beta, eps = p.smoothing, diff = ratio[0] - ratio[1];
+        double loss, slope;  // of the pair's loss in ratio[0] - ratio[1]
+        if (p.kind == RL_PREF_SIGMOID) {
+            const double h = beta * diff - (double)p.margin;
+            const double soft = log1p(exp(-fabs(h)));  // -ln sigma(|h|)
+            loss = (1.0 - eps) * (soft + fmax(-h, 0.0)) + eps * (soft + fmax(h, 0.0));
+            slope = beta * (eps / (1.0 + exp(-h)) - (1.0 - eps) / (1.0 + exp(h)));
+        } else if (p.kind == RL_PREF_HINGE) {
+            const double h = beta * diff - (double)p.margin;
+            loss = isnan(h) ? h : fmax(1.0 - h, 0.0);
+            slope = h < 1.0 ? -beta : 0.0;
+        } else {
+            const double d = diff - 0.5 / beta;
+            loss = d * d;
+            slope = 2.0 * d;
+        }
+        loss += (double)p.nll * like;
+        double per[2];
+        for (int h = 0; h < 2; ++h) per[h] = p.mean ? (n[h] > 0 ? 1.0 / n[h] : 0.0) : 1.0;
+        p.coef[2 * j] = (float)((slope * per[0] - (n[0] > 0 ? (double)p.nll / n[0] : 0.0)) / P);
+        p.coef[2 * j + 1] = (float)(-slope * per[1] / P);
+        p.pair64[j] = loss;
+        if (p.pair_loss) p.pair_loss[j] = (float)loss;
+        if (p.seq_logratio) {
+            p.seq_logratio[2 * j] = (float)ratio[0];
+            p.seq_logratio[2 * j + 1] = (float)ratio[1];
+        }
+        __threadfence();
+        s_last = atomicAdd(p.pairs_done, 1u) == (uint32_t)P - 1;
+    }
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    double L = 0.0;
+    for (int k = threadIdx.x; k < P; k += kPrepThreads) L += p.pair64[k];
+    L = block_sum_f64(L, s_d) / P;
+    if (threadIdx.x == 0) {
+        p.loss[0] = (float)L;
+        if (p.loss_f64) p.loss_f64[0] = L;
+        if (!isfinite(L)) post_raise(p.status, RL_ERR_NONFINITE);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_distill_prep(const DistillPrepParams &p, cudaStream_t stream) {
+    const int rows_per = kPrepThreads / 32;
+    distill_prep_kernel<<<p.S + (p.T + rows_per - 1) / rows_per, kPrepThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pref_pairs(const PrefPairParams &p, cudaStream_t stream) {
+    pref_pairs_kernel<<<p.S / 2, kPrepThreads, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace rlk

@@ -38,6 +38,8 @@ static size_t workspace_layout(const rl_loss_config &c, rl_loss_handle_s *h, cha
     char *tok_rec = carve(T * sizeof(float4));
     char *tok_meta = carve(T * sizeof(uint32_t));
     char *loss_scratch = carve(4 * sizeof(float));
+    char *post_partials = carve(rlk::kPostMaxBlocks * sizeof(rlk::PostPartial));
+    char *post_done = carve(sizeof(uint32_t));
     if (h) {
         h->status = reinterpret_cast<uint32_t *>(status);
         h->seq_adv = reinterpret_cast<float *>(seq_adv);
@@ -54,6 +56,8 @@ static size_t workspace_layout(const rl_loss_config &c, rl_loss_handle_s *h, cha
         h->tok_rec = reinterpret_cast<float4 *>(tok_rec);
         h->tok_meta = reinterpret_cast<uint32_t *>(tok_meta);
         h->loss_scratch = reinterpret_cast<float *>(loss_scratch);
+        h->post_partials = reinterpret_cast<rlk::PostPartial *>(post_partials);
+        h->post_done = reinterpret_cast<uint32_t *>(post_done);
     }
     return align_up(off, 256);
 }
@@ -342,6 +346,7 @@ RL_LOSS_API rl_status rl_loss_create(const rl_loss_config *config, rl_loss_t *ou
     }
     workspace_layout(c, h, reinterpret_cast<char *>(h->ws));
     if (cudaMemset(h->status, 0, sizeof(uint32_t)) != cudaSuccess ||
+        cudaMemset(h->post_done, 0, sizeof(uint32_t)) != cudaSuccess ||
         cudaMemset(h->tok_fix, 0, (size_t)c.max_tokens) != cudaSuccess) {
         cudaFree(h->ws);
         delete h;
@@ -374,6 +379,65 @@ RL_LOSS_API rl_status rl_loss_forward_backward(rl_loss_t h, const rl_loss_inputs
     const rl_status st = prepare_call(h, in, out, L);
     if (st != RL_OK) return st;
     return launch_loss(h, L, nullptr, 0, reinterpret_cast<cudaStream_t>(stream_ptr));
+}
+
+RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inputs *in, const rl_loss_kl *kl,
+                                                  const rl_loss_outputs *out, void *stream_ptr) {
+    if (!kl || kl->estimator < RL_KL_K1 || kl->estimator > RL_KL_K3 || !(kl->coef >= 0.f) || !std::isfinite(kl->coef))
+        return RL_ERR_INVALID_ARG;
+    LossLaunch L;
+    const rl_status st = prepare_call(h, in, out, L);
+    if (st != RL_OK) return st;
+    if (L.T > 0 && !kl->logp_ref) return RL_ERR_INVALID_ARG;
+    const rl_loss_config &c = h->cfg;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_ptr);
+    rlk::PolicyParams p{};
+    p.r.logits = in->logits;
+    p.r.ld = in->ld_logits;
+    p.r.dlogits = out->dlogits;
+    p.r.ldd = out->ld_dlogits;
+    p.r.T = L.T;
+    p.r.V = c.vocab_size;
+    p.r.S = in->num_seqs;
+    p.r.targets = in->targets;
+    p.r.mask = in->mask;
+    p.r.cu_seqlens = in->cu_seqlens;
+    p.r.logp = out->logp;
+    p.r.entropy = out->entropy;
+    p.r.status = h->status;
+    p.r.partials = h->post_partials;
+    p.r.blocks_done = h->post_done;
+    p.r.loss = out->loss;
+    p.r.loss_f64 = out->loss_f64;
+    p.c = h->consts;
+    p.logp_old = in->logp_old;
+    p.logp_infer = in->logp_infer;
+    p.token_adv = c.adv_mode == RL_ADV_PER_TOKEN ? in->rewards_or_adv : nullptr;
+    p.teacher = c.adv_mode == RL_ADV_TEACHER_LOGP ? in->rewards_or_adv : nullptr;
+    p.seq_adv = h->seq_adv;
+    p.seq_w = h->seq_w;
+    p.seq_w64 = h->seq_w64;
+    p.seq_n = h->seq_n;
+    p.flags = out->flags;
+    p.counts = out->counts;
+    p.mean_entropy = out->mean_entropy;
+    p.read_masked = out->logp || out->entropy;
+    p.kl = rlk::KlTerm{kl->logp_ref, kl->coef, kl->estimator, kl->kl, kl->mean_kl};
+    auto failed = [&](cudaError_t e) {
+        h->last_cuda_error = e;
+        return RL_ERR_CUDA;
+    };
+    int slot = h->prof_begin(kSegPrep, stream);
+    cudaError_t err = rlk::launch_seg_prep(L.sp, stream);
+    if (err == cudaSuccess && c.loss_norm == RL_NORM_PER_TOKEN) err = rlk::launch_seg_token_norm(L.sp, stream);
+    h->prof_end(slot, stream);
+    if (err != cudaSuccess) return failed(err);
+    slot = h->prof_begin(kPolicyKl, stream);
+    err = rlk::launch_post_policy(p, c.logits_dtype, stream);
+    h->prof_end(slot, stream);
+    if (err != cudaSuccess) return failed(err);
+    h->launches += 2 + (c.loss_norm == RL_NORM_PER_TOKEN ? 1 : 0);
+    return RL_OK;
 }
 
 RL_LOSS_API rl_status rl_loss_forward_backward_from_host(rl_loss_t h, const rl_loss_inputs *host,
