@@ -9,7 +9,7 @@
 // Every gradient row is one coefficient times the row's exponentials, plus a few entries of its own
 // (the sampled token, or the teacher's entries). Exponentials are taken in base 2 against the row's
 // own maximum, 2^{c (z_v - m)} with c = log2(e) / tau and m = max z_v, and the sum S is kept apart
-// from m: ln p_v = (c (z_v - m) - log2 S) ln 2 has no large term to cancel, so a log-prob near 0
+// from m: ln p_v = (z_v - m) / tau - ln S has no large term to cancel, so a log-prob near 0
 // keeps its digits, and p_v = 2^{c (z_v - m)} / S costs one multiplication by a per-row constant.
 // The difference is taken before the factor c: it is exact for entries near the maximum, and 0 at
 // it, whatever the size of the logits.
@@ -71,14 +71,25 @@ constexpr PostStats kPostStart{-FLT_MAX, 0.f, 0.f};
 // 0 times infinity.
 constexpr float kNoWeight = -1024.f;
 
-// Moves partial statistics to the reference M >= st.m.
-template <bool kEnt>
+// Moves partial statistics to the reference M >= st.m. ex2.approx truncates (its results are 5e-8
+// low on average), which a chain of merges would add up: the factor of a merge is exp2f's.
+template <bool kEnt, bool kExact = true>
 __device__ __forceinline__ void post_rescale(PostStats &st, float M, float c) {
     const float dm = __fmul_rn(__fsub_rn(st.m, M), c);
-    const float f = ex2_approx(dm);
+    const float f = kExact ? exp2f(dm) : ex2_approx(dm);
     if (kEnt) st.u = __fmul_rn(f, __fadd_rn(st.u, __fmul_rn(fmaxf(dm, kNoWeight), st.s)));
     st.s = __fmul_rn(st.s, f);
     st.m = M;
+}
+
+// The sum of a group, in pairs.
+template <int N>
+__device__ __forceinline__ float group_sum(float (&e)[N]) {
+#pragma unroll
+    for (int h = N / 2; h > 0; h >>= 1)
+#pragma unroll
+        for (int k = 0; k < h; ++k) e[k] += e[k + h];
+    return e[0];
 }
 
 // Folds a group of logits into the statistics (one rescale at most). A logit of -inf adds 0 to u
@@ -88,18 +99,20 @@ __device__ __forceinline__ void post_fold(PostStats &st, const float (&x)[N], fl
     float mv = x[0];
 #pragma unroll
     for (int k = 1; k < N; ++k) mv = fmaxf(mv, x[k]);
-    if (mv > st.m) post_rescale<kEnt>(st, mv, c);
+    if (mv > st.m) post_rescale<kEnt, false>(st, mv, c);
+    float e[N], u[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
         const float d = (x[k] - st.m) * c;
-        const float e = ex2_approx(d);
-        st.s += e;
-        if (kEnt) st.u = fmaf(e, fmaxf(d, kNoWeight), st.u);
+        e[k] = ex2_approx(d);
+        if (kEnt) u[k] = e[k] * fmaxf(d, kNoWeight);
     }
+    // the group is summed by itself: single terms below half a step of s would all be lost
+    st.s += group_sum(e);
+    if (kEnt) st.u += group_sum(u);
 }
 
-// Merges two partial statistics; symmetric in its arguments, so a butterfly leaves the same bits in
-// every lane.
+// Merges two partial statistics.
 template <bool kEnt>
 __device__ __forceinline__ PostStats post_merge(PostStats a, PostStats b, float c) {
     const float M = fmaxf(a.m, b.m);
@@ -108,13 +121,18 @@ __device__ __forceinline__ PostStats post_merge(PostStats a, PostStats b, float 
     return PostStats{M, __fadd_rn(a.s, b.s), kEnt ? __fadd_rn(a.u, b.u) : 0.f};
 }
 
+// Merges the lanes' statistics: their maximum first, so that each is rescaled once; sums in a
+// butterfly, which leaves the same bits in every lane.
 template <bool kEnt>
 __device__ __forceinline__ PostStats post_warp_merge(PostStats r, float c) {
+    float M = r.m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    post_rescale<kEnt>(r, M, c);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
-        PostStats o{__shfl_xor_sync(0xffffffffu, r.m, off), __shfl_xor_sync(0xffffffffu, r.s, off),
-                    kEnt ? __shfl_xor_sync(0xffffffffu, r.u, off) : 0.f};
-        r = post_merge<kEnt>(r, o, c);
+        r.s = __fadd_rn(r.s, __shfl_xor_sync(0xffffffffu, r.s, off));
+        if (kEnt) r.u = __fadd_rn(r.u, __shfl_xor_sync(0xffffffffu, r.u, off));
     }
     return r;
 }
@@ -251,17 +269,18 @@ __device__ __forceinline__ bool post_finite(PostStats st) { return st.s > 0.f &&
 // relative accuracy as p_y nears 1, which 1 + x has lost. Returns ln p_y (NaN where the row is not
 // finite) and the whole row's statistics in `all`.
 template <bool kEnt>
-__device__ __forceinline__ float post_target(PostStats rest, float zy, float c, PostStats &all) {
+__device__ __forceinline__ float post_target(PostStats rest, float zy, PostStats &all) {
+    constexpr float c = kLog2e;
     PostStats y = kPostStart;
     const float one[1] = {zy};
     post_fold<kEnt>(y, one, c);
     all = post_merge<kEnt>(rest, y, c);
     if (!post_finite(all)) return __int_as_float(0x7fc00000);
     if (zy >= rest.m) return -log1pf(rest.s * ex2_approx((rest.m - zy) * c));
-    return ((zy - rest.m) * c - log2f(all.s)) * kLn2;
+    return (zy - rest.m) - logf(all.s);
 }
 
-__device__ __forceinline__ float post_entropy(PostStats st) { return (log2f(st.s) - st.u / st.s) * kLn2; }
+__device__ __forceinline__ float post_entropy(PostStats st) { return logf(st.s) - st.u / st.s * kLn2; }
 
 // Estimators of KL(pi || pi_ref) from the sampled token, d = logp - logp_ref, and their derivative
 // in logp: d; d^2 / 2; e^{-d} - 1 + d, whose first two terms cancel near 0, where its series is
@@ -302,53 +321,70 @@ __device__ __forceinline__ RowGrad post_row_grad(float g, PostStats st, float lo
     return RowGrad{-g / st.s, st.m, -g * expm1f(logp), y};
 }
 
+// Everything a policy row needs besides its logits.
+struct PolicyTok {
+    int32_t seq, y;  // seq < 0: outside every response
+    int32_t m, ok;   // loss mask; the target is in the vocabulary
+    float A, w, lo, li, ref, teacher;
+    double w64;
+};
+
+__device__ __forceinline__ PolicyTok policy_load(const PolicyParams &p, int t, int i) {
+    PolicyTok k;
+    k.seq = i;
+    k.y = __ldg(p.r.targets + t);
+    k.ok = k.y >= 0 && k.y < p.r.V;
+    k.m = i >= 0 && __ldg(p.r.mask + t) != 0;
+    k.A = p.token_adv ? __ldg(p.token_adv + t) : (i >= 0 ? p.seq_adv[i] : 0.f);
+    k.w = i >= 0 ? p.seq_w[i] : 0.f;
+    k.w64 = i >= 0 ? p.seq_w64[i] : 0.0;
+    k.lo = __ldg(p.logp_old + t);
+    k.li = __ldg(p.logp_infer + t);
+    k.ref = __ldg(p.kl.logp_ref + t);
+    k.teacher = p.teacher ? __ldg(p.teacher + t) : 0.f;
+    return k;
+}
+
 // The token objective, its KL term and every per-token output of a policy row; adds the row to
-// `sum` and returns its gradient. `st` are the
-// whole row's statistics, `logp` its ln p_y (0 where the row was not read). `write` false: another
-// block writes the row's outputs and sums.
-__device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, PostStats st, float logp, bool write,
-                                              PostPartial &sum) {
-    const int i = find_seq(p.r.cu_seqlens, p.r.S, t);
-    if (i < 0 && write) post_raise(p.r.status, RL_ERR_SEQLENS);
-    const float A = p.token_adv ? __ldg(p.token_adv + t) : (i >= 0 ? p.seq_adv[i] : 0.f);
-    const float w = i >= 0 ? p.seq_w[i] : 0.f;
-    const int y = __ldg(p.r.targets + t);
-    const bool ok = y >= 0 && y < p.r.V;
-    const bool m = i >= 0 && __ldg(p.r.mask + t) != 0;
+// `sum` and returns its gradient. `st` are the whole row's statistics, `logp` its ln p_y (0 where
+// the row was not read). `write` false: another block writes the row's outputs and sums.
+__device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, const PolicyTok &k, PostStats st, float logp,
+                                              bool write, PostPartial &sum) {
+    const bool ok = k.ok, m = k.m;
     const bool read = m || p.read_masked;
-    const float lo = __ldg(p.logp_old + t);
-    const float d = __fsub_rn(lo, __ldg(p.logp_infer + t));  // ln rho, one fp32 subtraction
+    const float d = __fsub_rn(k.lo, k.li);  // ln rho, one fp32 subtraction
     const bool in_bounds = (-p.c.ln_beta <= d) && (d <= p.c.ln_beta);
-    uint32_t pre = (m ? 0u : RL_FLAG_MASKED) | (ok ? 0u : RL_FLAG_BAD_TARGET) | (A > 0.f ? kPreAPos : 0u) |
-                   (A < 0.f ? kPreANeg : 0u);
-    float cf = 0.f, lref = lo;
+    uint32_t pre = (m ? 0u : RL_FLAG_MASKED) | (ok ? 0u : RL_FLAG_BAD_TARGET) | (k.A > 0.f ? kPreAPos : 0u) |
+                   (k.A < 0.f ? kPreANeg : 0u);
+    float cf = 0.f, lref = k.lo;
     if (p.c.objective == RL_OBJ_DIS) {
-        lref = __ldg(p.logp_infer + t);
-        if (m && ok) cf = A;
+        lref = k.li;
+        if (m && ok) cf = k.A;
     } else {
         pre |= in_bounds ? RL_FLAG_POP_IN_BOUNDS : 0u;
         const float pop = (m && ok && in_bounds) ? (p.c.pop_indicator ? 1.f : expf(d)) : 0.f;
-        cf = p.c.adv_teacher ? pop : pop * A;
+        cf = p.c.adv_teacher ? pop : pop * k.A;
     }
-    const float4 rec = make_float4(0.f, lref, cf, w * cf);
-    const uint32_t meta = (ok ? (uint32_t)y : 0u) | (pre << 24);
-    RowOut o = finish_row(RowStats2{0.f, st.s, st.u}, rec, meta, p.c, p.teacher ? __ldg(p.teacher + t) : 0.f, &logp);
+    const float4 rec = make_float4(0.f, lref, cf, k.w * cf);
+    const uint32_t meta = (ok ? (uint32_t)k.y : 0u) | (pre << 24);
+    RowOut o = finish_row(RowStats2{0.f, st.s, st.u}, rec, meta, p.c, k.teacher, &logp);
     if (!read) {  // nothing of the row was read: no log-prob, and the clip test has nothing to test
         o.H = 0.f;
         o.flags &= ~(RL_FLAG_CLIP_ACTIVE | (p.c.objective == RL_OBJ_DIS ? RL_FLAG_POP_IN_BOUNDS : 0u));
     }
     float kl = 0.f, dkl = 0.f;
     const bool counts = m && ok;
-    if (counts) post_kl(p.kl.estimator, __fsub_rn(o.logp, __ldg(p.kl.logp_ref + t)), kl, dkl);
-    const float g = counts ? fmaf(w * p.kl.coef, dkl, o.g) : 0.f;
+    if (counts) post_kl(p.kl.estimator, __fsub_rn(o.logp, k.ref), kl, dkl);
+    const float g = counts ? fmaf(k.w * p.kl.coef, dkl, o.g) : 0.f;
     if (write) {
+        if (k.seq < 0) post_raise(p.r.status, RL_ERR_SEQLENS);
         if (!ok) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
         if (read && !post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
         if (p.r.logp) p.r.logp[t] = ok ? o.logp : __int_as_float(0x7fc00000);
         if (p.r.entropy) p.r.entropy[t] = o.H;
         if (p.flags) p.flags[t] = (uint8_t)o.flags;
         if (p.kl.kl) p.kl.kl[t] = m && !ok ? __int_as_float(0x7fc00000) : kl;
-        if (i >= 0) sum.loss += p.seq_w64[i] * ((double)p.kl.coef * (double)kl - (double)o.obj);
+        sum.loss += k.w64 * ((double)p.kl.coef * (double)kl - (double)o.obj);
         if (m) {
             sum.n += 1;
             sum.ent += (double)o.H;
@@ -359,7 +395,7 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, Post
             sum.masked += 1;
         }
     }
-    return g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : post_row_grad(g, st, o.logp, y);
+    return g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : post_row_grad(g, st, o.logp, k.y);
 }
 
 // ---------------------------------------------------------------- the teacher's entries
@@ -368,7 +404,7 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, Post
 // entries, and distill_entry() at them.
 struct DistillRow {
     float ct, m;           // tail: coefficient and reference
-    float M, l2s;          // the whole row: reference and log2 S
+    float M, ls, inv_s;    // the whole row: reference, ln S and 1 / S
     float kl, w;           // the row's divergence; its weight * scale / tau
     float Q;               // total mass of the teacher's distribution
 };
@@ -408,42 +444,45 @@ __device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, Pos
     r.Q = rec.w;
     r.m = tail.m;
     r.M = fmaxf(Mk, tail.m);
-    const float dt = (tail.m - r.M) * p.c;
-    const float ft = ex2_approx(dt);
-    const float S = __fadd_rn(__fmul_rn(Sk, ex2_approx((Mk - r.M) * p.c)), __fmul_rn(tail.s, ft));
-    r.l2s = log2f(S);
-    float kl = 0.f;
+    const float ft = exp2f((tail.m - r.M) * p.c);
+    // KL's terms nearly cancel for a student near its teacher. An error of S_tail or of the entries'
+    // sum alone enters only times p - q, as long as S is their sum and the logarithms are of these
+    // same numbers: S, the logarithms, the differences and the sum are taken in 64 bits.
+    const double St = (double)tail.s * (double)ft;
+    const double S = (double)Sk * (double)exp2f((Mk - r.M) * p.c) + St;
+    const double both = log(lane == 0 ? S : St);  // one logarithm's time for two
+    const double lnS = __shfl_sync(0xffffffffu, both, 0);
+    const float inv_s = r.inv_s = 1.f / (float)S;
+    r.ls = (float)lnS;
+    double sum = 0.0;
     for (int k = lane; k < p.K; k += 32) {
-        const float lp2 = (s_z[k] - r.M) * p.c - r.l2s;
+        const double d = ((double)s_z[k] - (double)r.M) * (double)p.inv_tau;
         const float lq = s_lq[k];
-        if (p.reverse) {
-            const float pk = ex2_approx(lp2);
-            if (pk > 0.f) kl = fmaf(pk, fmaf(lp2, kLn2, -lq), kl);
-        } else {
-            const float q = expf(lq);
-            if (q > 0.f) kl = fmaf(q, lq - lp2 * kLn2, kl);
-        }
+        const float head = p.reverse ? ex2_approx((s_z[k] - r.M) * p.c) * inv_s : expf(lq);
+        const double diff = (double)lq - (d - lnS);
+        if (head != 0.f) sum += (double)head * (p.reverse ? -diff : diff);
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) kl = __fadd_rn(kl, __shfl_xor_sync(0xffffffffu, kl, off));
-    const float inv_s = 1.f / S;
+    sum = warp_sum_f64(sum);
     float ct;
     if (p.tail && n_rest > 0) {
-        // ln p_o from the tail's own reference, so that a tail far below the row's maximum keeps its log
-        const float lpo = (dt + (log2f(tail.s) - r.l2s)) * kLn2;
-        const float qo = rec.z, lqo = logf(qo);
+        // a tail far below the row's maximum keeps its logarithm by its own reference
+        double lpo = __shfl_sync(0xffffffffu, both, 1) - lnS;
+        if (ft < 1e-30f) lpo = ((double)tail.m - (double)r.M) * (double)p.inv_tau + ((double)logf(tail.s) - lnS);
+        const float qo = rec.z;
+        const double lqo = log((double)qo);
         if (p.reverse) {
             const float po = tail.s * ft * inv_s;
-            const float ao = lpo - lqo;
-            if (po > 0.f) kl = fmaf(po, ao, kl);
-            ct = tail.s > 0.f ? (ao - kl) * ft * inv_s : 0.f;
+            const double ao = lpo - lqo;
+            if (po > 0.f) sum += (double)po * ao;
+            ct = tail.s > 0.f ? (float)(ao - sum) * ft * inv_s : 0.f;
         } else {
-            if (qo > 0.f) kl = fmaf(qo, lqo - lpo, kl);
+            if (qo > 0.f) sum += (double)qo * (lqo - lpo);
             ct = tail.s > 0.f ? r.Q * ft * inv_s - qo / tail.s : 0.f;
         }
     } else {
-        ct = p.reverse ? -kl * ft * inv_s : r.Q * ft * inv_s;
+        ct = p.reverse ? -(float)sum * ft * inv_s : r.Q * ft * inv_s;
     }
+    const float kl = (float)sum;
     r.kl = kl;
     r.ct = w * ct;
     return r;
@@ -451,10 +490,9 @@ __device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, Pos
 
 // dL/dz of one of the teacher's entries.
 __device__ __forceinline__ float distill_entry(const DistillParams &p, const DistillRow &r, float z, float lq) {
-    const float lp2 = (z - r.M) * p.c - r.l2s;
-    const float pk = ex2_approx(lp2);
+    const float pk = ex2_approx((z - r.M) * p.c) * r.inv_s;
     if (!p.reverse) return r.w * fmaf(r.Q, pk, -expf(lq));
-    return pk == 0.f ? 0.f : r.w * pk * (fmaf(lp2, kLn2, -lq) - r.kl);
+    return pk == 0.f ? 0.f : r.w * pk * (((z - r.M) * p.inv_tau - r.ls) - lq - r.kl);
 }
 
 }  // namespace rlk

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) logp_rows_kernel(LogpParams p) {
         PostStats st = block_merge<kEnt>(row_stats<T, kEnt>(z, p.r.V, kLog2e, ok ? y : -1), s_warp, kLog2e);
         if (threadIdx.x == 0) {
             float logp = __int_as_float(0x7fc00000);
-            if (ok) logp = post_target<kEnt>(st, PostVec<T>::load1(z, y), kLog2e, st);
+            if (ok) logp = post_target<kEnt>(st, PostVec<T>::load1(z, y), st);
             if (!ok) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
             if (!post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
             p.r.logp[t] = logp;
@@ -172,8 +172,8 @@ __global__ void __launch_bounds__(kThreads) policy_rows_kernel(PolicyParams p) {
         PostStats st{0.f, 1.f, 0.f};
         if (read) st = block_merge<kEnt>(row_stats<T, kEnt>(z, p.r.V, kLog2e, ok ? y : -1), s_warp, kLog2e);
         if (threadIdx.x == 0) {
-            const float logp = ok && read ? post_target<kEnt>(st, PostVec<T>::load1(z, y), kLog2e, st) : 0.f;
-            s_grad = policy_row(p, t, st, logp, true, sum);
+            const float logp = ok && read ? post_target<kEnt>(st, PostVec<T>::load1(z, y), st) : 0.f;
+            s_grad = policy_row(p, t, policy_load(p, t, find_seq(p.r.cu_seqlens, p.r.S, t)), st, logp, true, sum);
         }
         __syncthreads();
         const RowGrad gr = s_grad;
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) distill_rows_kernel(DistillParams p)
             const DistillRow r = distill_finish(p, st, Mk, Sk, s_z, s_lq, rec, (float)w * p.scale * p.inv_tau, V - have);
             if (threadIdx.x == 0) {
                 s_row = r;
-                if (!isfinite(r.l2s)) post_raise(p.r.status, RL_ERR_NONFINITE);
+                if (!isfinite(r.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
                 if (p.kl) p.kl[t] = r.kl;
                 sum.loss += w * (double)p.scale * (double)r.kl;
             }
