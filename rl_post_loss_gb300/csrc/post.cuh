@@ -29,8 +29,14 @@ struct PostVec;
 template <>
 struct PostVec<float> {
     static constexpr int kElems = 4;
+    using Tag = uint32_t;
+    static constexpr Tag kNegInf = 0xff800000u;
     __device__ __forceinline__ static void decode(const uint4 &v, float (&x)[4]) {
         x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+    // The largest of the group (NaN counts as missing).
+    __device__ __forceinline__ static float max_of(const uint4 &v) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
     __device__ __forceinline__ static uint4 encode(const float (&x)[4]) {
         return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
@@ -42,9 +48,16 @@ struct PostVec<float> {
 template <>
 struct PostVec<__nv_bfloat16> {
     static constexpr int kElems = 8;
+    using Tag = uint16_t;
+    static constexpr Tag kNegInf = 0xff80u;
     __device__ __forceinline__ static void decode(const uint4 &v, float (&x)[8]) {
         x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
         x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+    }
+    __device__ __forceinline__ static float max_of(const uint4 &v) {
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
+        const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        return fmaxf(__low2float(m), __high2float(m));
     }
     __device__ __forceinline__ static uint4 encode(const float (&x)[8]) {
         return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
@@ -92,14 +105,10 @@ __device__ __forceinline__ float group_sum(float (&e)[N]) {
     return e[0];
 }
 
-// Folds a group of logits into the statistics (one rescale at most). A logit of -inf adds 0 to u
+// Adds the terms of a group to the statistics; no entry exceeds st.m. A logit of -inf adds 0 to u
 // (0 log 0 = 0), while e comes from d itself, so that a NaN reaches s.
 template <bool kEnt, int N>
-__device__ __forceinline__ void post_fold(PostStats &st, const float (&x)[N], float c) {
-    float mv = x[0];
-#pragma unroll
-    for (int k = 1; k < N; ++k) mv = fmaxf(mv, x[k]);
-    if (mv > st.m) post_rescale<kEnt, false>(st, mv, c);
+__device__ __forceinline__ void post_add(PostStats &st, const float (&x)[N], float c) {
     float e[N], u[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) {
@@ -110,6 +119,33 @@ __device__ __forceinline__ void post_fold(PostStats &st, const float (&x)[N], fl
     // the group is summed by itself: single terms below half a step of s would all be lost
     st.s += group_sum(e);
     if (kEnt) st.u += group_sum(u);
+}
+
+// Folds a group of logits into the statistics (one rescale at most).
+template <bool kEnt, int N>
+__device__ __forceinline__ void post_fold(PostStats &st, const float (&x)[N], float c) {
+    float mv = x[0];
+#pragma unroll
+    for (int k = 1; k < N; ++k) mv = fmaxf(mv, x[k]);
+    if (mv > st.m) post_rescale<kEnt, false>(st, mv, c);
+    post_add<kEnt>(st, x, c);
+}
+
+// Folds M 16-byte groups: one comparison with the reference for all of them, so that their
+// exponentials overlap.
+template <typename T, bool kEnt, int M>
+__device__ __forceinline__ void post_fold_groups(PostStats &st, const uint4 (&v)[M], float c) {
+    using VT = PostVec<T>;
+    float mv = VT::max_of(v[0]);
+#pragma unroll
+    for (int i = 1; i < M; ++i) mv = fmaxf(mv, VT::max_of(v[i]));
+    if (mv > st.m) post_rescale<kEnt, false>(st, mv, c);
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+        float x[VT::kElems];
+        VT::decode(v[i], x);
+        post_add<kEnt>(st, x, c);
+    }
 }
 
 // Merges two partial statistics.

@@ -55,7 +55,7 @@ def close(got, want, tol, what):
 # ---------------------------------------------------------------- token log-probs
 
 LOGP = [(1, 1, 0), (3, 7, 1), (5, 8, 0), (4, 9, 0), (2, 1000, 3), (70, 4097, 0), (700, 1003, 0), (1, 32768, 0), (9, 32003, 0),
-        (1, 151552, 0), (5, 151553, 1), (40, 50257, 0)]
+        (1, 151552, 0), (5, 151553, 1), (40, 50257, 0), (460, 5003, 0), (2, 1000003, 0), (1500, 64, 1)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -126,7 +126,8 @@ KLC = [(0, [5, 17, 1, 64, 33, 0, 16, 128], 4096, {}), (1, [40, 3, 0, 90, 11, 25,
        (0, [9, 12, 1, 3, 8, 0, 6, 7], 151552, dict(loss_norm=1)),
        (0, [20, 31, 7, 9, 8, 11, 6, 7], 517, dict(objective=1, loss_norm=1)),
        (1, [20, 31, 7, 9, 8, 11, 6, 7], 2048, dict(token_adv="normal")),
-       (1, [20, 31, 7, 9, 8, 11, 6, 7], 2048, dict(token_adv="teacher"))]
+       (1, [20, 31, 7, 9, 8, 11, 6, 7], 2048, dict(token_adv="teacher")),
+       (0, [1, 0, 1, 0, 1, 0, 0, 1], 1000001, {}), (1, [1, 0, 0, 1, 1, 0, 0, 1], 2000003, {})]
 
 
 @pytest.mark.parametrize("estimator", ["k1", "k2", "k3"])
@@ -249,7 +250,8 @@ def distill_case(T, V, K, dtype, seed, mode, tau, pad=0, lengths=None):
 
 
 DISTILL = [(1, 1, 1), (1, 9, 4), (4, 7, 16), (5, 64, 64), (9, 1000, 1), (30, 4097, 64), (6, 32003, 33), (3, 151552, 128),
-           (4, 5000, 1024), (70, 1001, 8), (300, 517, 5)]
+           (4, 5000, 1024), (70, 1001, 8), (300, 517, 5), (2, 2000003, 16), (3, 600001, 7),
+           (500, 2048, 3)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -365,7 +367,7 @@ def test_distill_gradient_against_differences_of_the_loss(mode, reverse):
 # ---------------------------------------------------------------- preference
 
 PREF = [([1, 1], 1), ([3, 0], 9), ([5, 2, 1, 7], 1000), ([40, 33, 0, 0, 12, 1], 4097), ([9, 30], 32003), ([3, 2], 151552),
-        ([200, 340, 90, 7], 517)]
+        ([200, 340, 90, 7], 517), ([1, 2], 1000003)]
 
 
 def check_pref(lengths, V, dtype, kind, mean, use_ref, seed=0, nll=0.2, smoothing=0.1):
