@@ -21,6 +21,27 @@
 
 namespace rlk {
 
+// ---------------------------------------------------------------- pairs of fp32
+
+// Two fp32 values in a 64-bit register pair: one instruction adds or multiplies both.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f32x2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // ---------------------------------------------------------------- logits of either type
 
 template <typename T>
@@ -31,8 +52,21 @@ struct PostVec<float> {
     static constexpr int kElems = 4;
     using Tag = uint32_t;
     static constexpr Tag kNegInf = 0xff800000u;
+    // a group of -inf
+    __device__ __forceinline__ static uint4 none() { return make_uint4(kNegInf, kNegInf, kNegInf, kNegInf); }
     __device__ __forceinline__ static void decode(const uint4 &v, float (&x)[4]) {
         x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+    }
+    static constexpr int kPairs = 2;
+    __device__ __forceinline__ static void pairs(const uint4 &v, f32x2 (&x)[2]) {
+        x[0] = pack2(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[1] = pack2(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
+    __device__ __forceinline__ static uint4 from_pairs(const f32x2 (&x)[2]) {
+        float a, b, c, d;
+        unpack2(x[0], a, b);
+        unpack2(x[1], c, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
     }
     // The largest of the group (NaN counts as missing).
     __device__ __forceinline__ static float max_of(const uint4 &v) {
@@ -50,9 +84,25 @@ struct PostVec<__nv_bfloat16> {
     static constexpr int kElems = 8;
     using Tag = uint16_t;
     static constexpr Tag kNegInf = 0xff80u;
+    __device__ __forceinline__ static uint4 none() { return make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u); }
     __device__ __forceinline__ static void decode(const uint4 &v, float (&x)[8]) {
         x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
         x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+    }
+    static constexpr int kPairs = 4;
+    __device__ __forceinline__ static void pairs(const uint4 &v, f32x2 (&x)[4]) {
+        x[0] = pack2(bf16_lo(v.x), bf16_hi(v.x));
+        x[1] = pack2(bf16_lo(v.y), bf16_hi(v.y));
+        x[2] = pack2(bf16_lo(v.z), bf16_hi(v.z));
+        x[3] = pack2(bf16_lo(v.w), bf16_hi(v.w));
+    }
+    __device__ __forceinline__ static uint32_t from_pair(f32x2 x) {
+        float a, b;
+        unpack2(x, a, b);
+        return pack_bf16x2(a, b);
+    }
+    __device__ __forceinline__ static uint4 from_pairs(const f32x2 (&x)[4]) {
+        return make_uint4(from_pair(x[0]), from_pair(x[1]), from_pair(x[2]), from_pair(x[3]));
     }
     __device__ __forceinline__ static float max_of(const uint4 &v) {
         const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&v);
@@ -131,21 +181,80 @@ __device__ __forceinline__ void post_fold(PostStats &st, const float (&x)[N], fl
     post_add<kEnt>(st, x, c);
 }
 
+// A thread's running statistics with the sums held as two halves (even and odd entries).
+struct PostAcc {
+    float m;
+    f32x2 s, u;
+    __device__ __forceinline__ PostStats stats() const {
+        float a, b, x, y;
+        unpack2(s, a, b);
+        unpack2(u, x, y);
+        return PostStats{m, a + b, x + y};
+    }
+};
+__device__ __forceinline__ PostAcc post_acc() { return PostAcc{-FLT_MAX, 0ull, 0ull}; }
+
 // Folds M 16-byte groups: one comparison with the reference for all of them, so that their
-// exponentials overlap.
+// exponentials overlap, and one addition to the running sums.
 template <typename T, bool kEnt, int M>
-__device__ __forceinline__ void post_fold_groups(PostStats &st, const uint4 (&v)[M], float c) {
+__device__ __forceinline__ void post_fold_groups(PostAcc &st, const uint4 (&v)[M], float c) {
     using VT = PostVec<T>;
+    constexpr int P = VT::kPairs;
     float mv = VT::max_of(v[0]);
 #pragma unroll
     for (int i = 1; i < M; ++i) mv = fmaxf(mv, VT::max_of(v[i]));
-    if (mv > st.m) post_rescale<kEnt, false>(st, mv, c);
+    if (mv > st.m) {
+        const float dm = (st.m - mv) * c;
+        const float f = ex2_approx(dm);
+        if (kEnt) {
+            const float h = fmaxf(dm, kNoWeight);
+            st.u = mul2(pack2(f, f), add2(st.u, mul2(pack2(h, h), st.s)));
+        }
+        st.s = mul2(st.s, pack2(f, f));
+        st.m = mv;
+    }
+    const f32x2 nm = pack2(-st.m, -st.m), cc = pack2(c, c);
+    f32x2 es = 0ull, us = 0ull;
 #pragma unroll
     for (int i = 0; i < M; ++i) {
-        float x[VT::kElems];
-        VT::decode(v[i], x);
-        post_add<kEnt>(st, x, c);
+        f32x2 x[P], u[P];
+        VT::pairs(v[i], x);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            float a, b;
+            unpack2(mul2(add2(x[k], nm), cc), a, b);
+            x[k] = pack2(ex2_approx(a), ex2_approx(b));
+            if (kEnt) u[k] = mul2(x[k], pack2(fmaxf(a, kNoWeight), fmaxf(b, kNoWeight)));
+        }
+#pragma unroll
+        for (int h = P / 2; h > 0; h >>= 1)
+#pragma unroll
+            for (int k = 0; k < h; ++k) {
+                x[k] = add2(x[k], x[k + h]);
+                if (kEnt) u[k] = add2(u[k], u[k + h]);
+            }
+        es = i == 0 ? x[0] : add2(es, x[0]);
+        if (kEnt) us = i == 0 ? u[0] : add2(us, u[0]);
     }
+    st.s = add2(st.s, es);
+    if (kEnt) st.u = add2(st.u, us);
+}
+
+// dz of a 16-byte group: a 2^{c (z - m)}.
+template <typename T>
+__device__ __forceinline__ uint4 post_grad_group(const uint4 &v, float a, float m, float c) {
+    using VT = PostVec<T>;
+    constexpr int P = VT::kPairs;
+    const f32x2 nm = pack2(-m, -m), cc = pack2(c, c), aa = pack2(a, a);
+    f32x2 x[P];
+    VT::pairs(v, x);
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        float p, q;
+        unpack2(mul2(add2(x[k], nm), cc), p, q);
+        x[k] = mul2(pack2(ex2_approx(p), ex2_approx(q)), aa);
+    }
+    return VT::from_pairs(x);
 }
 
 // Merges two partial statistics.
@@ -441,7 +550,7 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, cons
 struct DistillRow {
     float ct, m;           // tail: coefficient and reference
     float M, ls, inv_s;    // the whole row: reference, ln S and 1 / S
-    float kl, w;           // the row's divergence; its weight * scale / tau
+    float kl, w;           // the row's divergence (reverse); its weight * scale / tau
     float Q;               // total mass of the teacher's distribution
 };
 
@@ -461,7 +570,7 @@ __device__ __forceinline__ void distill_entry_stats(const float *s_z, int K, flo
     S = s;
 }
 
-// The row's divergence and coefficients, by one warp. `tail` are the statistics of the vocabulary
+// The row's coefficients, by one warp. `tail` are the statistics of the vocabulary
 // outside the teacher's entries, s_lq[k] the teacher's log-prob of entry k, rec of distill_prep,
 // w the row's weight * scale / tau, n_rest the number of vocabulary entries outside the teacher's.
 //
@@ -481,47 +590,63 @@ __device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, Pos
     r.m = tail.m;
     r.M = fmaxf(Mk, tail.m);
     const float ft = exp2f((tail.m - r.M) * p.c);
-    // KL's terms nearly cancel for a student near its teacher. An error of S_tail or of the entries'
-    // sum alone enters only times p - q, as long as S is their sum and the logarithms are of these
-    // same numbers: S, the logarithms, the differences and the sum are taken in 64 bits.
+    const float S = __fadd_rn(__fmul_rn(Sk, exp2f((Mk - r.M) * p.c)), __fmul_rn(tail.s, ft));
+    const float inv_s = r.inv_s = 1.f / S;
+    r.ls = logf(S);
+    const bool rest = p.tail && n_rest > 0;
+    const float lqo = rest ? logf(rec.z) : 0.f;
+    // a tail far below the row's maximum keeps its logarithm by its own reference
+    const float lpo = (tail.m - r.M) * p.inv_tau + (logf(tail.s) - r.ls);
+    const float po = tail.s * ft * inv_s;
+    r.kl = 0.f;
+    if (p.reverse) {  // the gradient needs the divergence
+        float kl = 0.f;
+        for (int k = lane; k < p.K; k += 32) {
+            const float pk = ex2_approx((s_z[k] - r.M) * p.c) * inv_s;
+            if (pk != 0.f) kl = fmaf(pk, ((s_z[k] - r.M) * p.inv_tau - r.ls) - s_lq[k], kl);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) kl = __fadd_rn(kl, __shfl_xor_sync(0xffffffffu, kl, off));
+        if (rest && po > 0.f) kl = fmaf(po, lpo - lqo, kl);
+        r.kl = kl;
+        r.ct = rest ? (tail.s > 0.f ? (lpo - lqo - kl) * ft * inv_s : 0.f) : -kl * ft * inv_s;
+    } else {
+        r.ct = r.Q * ft * inv_s;
+        if (rest) r.ct = tail.s > 0.f ? r.ct - rec.z / tail.s : 0.f;
+    }
+    r.ct *= w;
+    return r;
+}
+
+// The row's divergence for the caller, by one warp, from the same sums. Its terms nearly cancel for
+// a student near its teacher. An error of the sum over the tail or over the entries enters only times
+// p - q, as long as S is their sum and the logarithms are of these same numbers: S, the logarithms,
+// the differences and the sum are taken in 64 bits.
+__device__ __forceinline__ float distill_kl(const DistillParams &p, const DistillRow &r, PostStats tail, float Mk, float Sk,
+                                            const float *s_z, const float *s_lq, float4 rec, int n_rest) {
+    const int lane = threadIdx.x & 31;
+    const float ft = exp2f((tail.m - r.M) * p.c);
     const double St = (double)tail.s * (double)ft;
     const double S = (double)Sk * (double)exp2f((Mk - r.M) * p.c) + St;
-    const double both = log(lane == 0 ? S : St);  // one logarithm's time for two
-    const double lnS = __shfl_sync(0xffffffffu, both, 0);
-    const float inv_s = r.inv_s = 1.f / (float)S;
-    r.ls = (float)lnS;
+    // one logarithm's time for all three
+    const double logs = log(lane == 0 ? S : lane == 1 ? St : (double)rec.z);
+    const double lnS = __shfl_sync(0xffffffffu, logs, 0);
+    double lpo = __shfl_sync(0xffffffffu, logs, 1) - lnS;
+    const double lqo = __shfl_sync(0xffffffffu, logs, 2);
+    if (ft < 1e-30f) lpo = ((double)tail.m - (double)r.M) * (double)p.inv_tau + ((double)logf(tail.s) - lnS);
     double sum = 0.0;
     for (int k = lane; k < p.K; k += 32) {
-        const double d = ((double)s_z[k] - (double)r.M) * (double)p.inv_tau;
         const float lq = s_lq[k];
-        const float head = p.reverse ? ex2_approx((s_z[k] - r.M) * p.c) * inv_s : expf(lq);
-        const double diff = (double)lq - (d - lnS);
+        const float head = p.reverse ? ex2_approx((s_z[k] - r.M) * p.c) * r.inv_s : expf(lq);
+        const double diff = (double)lq - (((double)s_z[k] - (double)r.M) * (double)p.inv_tau - lnS);
         if (head != 0.f) sum += (double)head * (p.reverse ? -diff : diff);
     }
     sum = warp_sum_f64(sum);
-    float ct;
     if (p.tail && n_rest > 0) {
-        // a tail far below the row's maximum keeps its logarithm by its own reference
-        double lpo = __shfl_sync(0xffffffffu, both, 1) - lnS;
-        if (ft < 1e-30f) lpo = ((double)tail.m - (double)r.M) * (double)p.inv_tau + ((double)logf(tail.s) - lnS);
-        const float qo = rec.z;
-        const double lqo = log((double)qo);
-        if (p.reverse) {
-            const float po = tail.s * ft * inv_s;
-            const double ao = lpo - lqo;
-            if (po > 0.f) sum += (double)po * ao;
-            ct = tail.s > 0.f ? (float)(ao - sum) * ft * inv_s : 0.f;
-        } else {
-            if (qo > 0.f) sum += (double)qo * (lqo - lpo);
-            ct = tail.s > 0.f ? r.Q * ft * inv_s - qo / tail.s : 0.f;
-        }
-    } else {
-        ct = p.reverse ? -(float)sum * ft * inv_s : r.Q * ft * inv_s;
+        const float ho = p.reverse ? tail.s * ft * r.inv_s : rec.z;
+        if (ho > 0.f) sum += (double)ho * (p.reverse ? lpo - lqo : lqo - lpo);
     }
-    const float kl = (float)sum;
-    r.kl = kl;
-    r.ct = w * ct;
-    return r;
+    return (float)sum;
 }
 
 // dL/dz of one of the teacher's entries.

@@ -1,18 +1,22 @@
 // Row kernels of the vocabulary-wide post-training operators (post.cuh has their mathematics).
 //
-// A row is cut over the CTAs of a cluster (one to eight). In each CTA a producer warp copies its
-// slice of the next rows into a ring of shared-memory tiles (bulk copies completing on mbarriers)
-// and gathers what the row needs besides its logits (the token's record, or the teacher's entries);
-// the consumer warps fold the tiles into softmax statistics as they land. The CTAs exchange their
-// statistics through distributed shared memory, every CTA finishes the row for itself, and the
-// consumers walk the tiles, still in shared memory, a second time for the gradient: each logit is
-// read from memory once. A tile is refilled with the next row's as soon as its second walk is done,
-// so copies, folds and stores of consecutive rows overlap, and two or three CTAs on an SM fill each
-// other's exchanges.
+// A row is cut over the CTAs of a cluster (one to eight), and a CTA's slice over its consumer warps. In
+// each CTA
+//  - a producer warp copies every consumer warp's segments of the next rows into a ring of that warp's
+//    own (bulk copies completing on mbarriers) and gathers what a row needs besides its logits: the
+//    token's record, for 32 rows at a time, or the teacher's entries, whose places it marks;
+//  - each consumer warp folds its segment into softmax statistics (A) and later walks it, still in shared
+//    memory, for the gradient (B): each logit is read from memory once. Warps wait for their own copies
+//    alone, never for one another;
+//  - a finisher warp merges the warps' statistics, exchanges them with the other CTAs through distributed
+//    shared memory and works out the row's results.
+// Three CTAs on an SM fill each other's waits for the finisher; where a ring holds two slices the warps
+// also fold row r + 1 before they write row r.
 //
 // Rows too long for the rings of a cluster (above about 1.8 MB with eight CTAs) take the block-per-row
 // kernels at the end, which read a row twice.
 #include <algorithm>
+#include <cstddef>
 #include <mutex>
 
 #include "post.cuh"
@@ -97,66 +101,81 @@ __device__ __forceinline__ char *row_out(const PostRows &r, int t) {
 enum RowOp { kOpLogp, kOpPolicy, kOpDistill, kOpScale };
 
 constexpr int kWarps = 8;                      // consumer warps
-constexpr int kCons = 32 * kWarps;             // consumer threads
-constexpr int kRowThreads = kCons + 32;        // and the producer warp
+constexpr int kRowThreads = 32 * (kWarps + 2); // and the producer and the finisher
+constexpr int kRowBlocks = 3;                  // CTAs on an SM
 constexpr int kMaxCluster = 8;
-constexpr int kMaxSlots = 8;
-constexpr int kMeta = 2;                       // rows whose records are held
+constexpr int kMaxDepth = 4;
+constexpr int kBatch = 4;                      // 16-byte groups a lane takes at once
+
+// Rows whose records are held. A ring of one slice has use for the next row's record alone; a distilled
+// row's record takes two dependent loads to gather and starts a row earlier; the others have room.
+constexpr int kMetaOf(int op) { return op == kOpPolicy ? 2 : op == kOpDistill ? 3 : 4; }
 
 // How a launch cuts its rows.
 struct RowPlan {
     int32_t cluster;    // CTAs per row
     int32_t slice;      // 16-byte groups per CTA
-    int32_t tile;       // 16-byte groups per tile
-    int32_t slots;      // tiles in the ring
+    int32_t parts;      // segments of a warp's share of the slice
+    int32_t seg;        // 16-byte groups per segment
+    int32_t depth;      // segments in a warp's ring
+    int32_t lag;        // rows folded ahead of the row that is written: 1 where the ring holds two slices, else 0
 };
 
 template <int OP>
 struct RowMeta;
 template <>
 struct RowMeta<kOpLogp> {
-    int32_t copied, read;  // the row's logits are in the ring; they are needed
+    int32_t read;          // the row's logits are needed (and copied)
     int32_t y;             // the sampled entry, -1: none
     float zy;
 };
 template <>
 struct RowMeta<kOpPolicy> {
-    int32_t copied, read, y;
+    int32_t read, y;
     float zy;
     PolicyTok tok;
 };
 template <>
 struct RowMeta<kOpDistill> {
-    int32_t copied, read;
+    int32_t read, copied;  // its logits are needed; they were copied (its entries then turned out bad)
     int32_t bad, have;     // an id outside the vocabulary; entries that are not padding
+    int32_t dup;           // an entry of this slice is listed twice
+    uint32_t tail_mark;    // the teacher's among the last V mod VEC entries
     float4 rec;
     double w;              // the row's weight
 };
 template <>
 struct RowMeta<kOpScale> {
-    int32_t copied, read;
+    int32_t read;
     RowGrad grad;
 };
 
-struct RowMsg {
+struct alignas(16) RowMsg {  // sent by one 16-byte store
     float m, s, u;
     int32_t bad;
 };
 
+// What a row's finisher publishes.
+struct RowFin {
+    RowGrad grad;
+};
+
 template <int OP>
 struct RowShared {
-    uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t mfull[kMeta], mempty[kMeta];
-    uint64_t xbar[2];
+    static constexpr int kMeta = kMetaOf(OP);
+    uint64_t mfull[kMeta], mempty[kMeta];         // records: gathered; no longer needed
+    uint64_t part_full[kMeta];                    // the warps' statistics of a row
+    uint64_t fin_full[kMeta];                     // a row's results
+    uint64_t written[kMeta];                      // distill: the warps have written the row
+    uint64_t xbar[2];  // the cluster's statistics: two in turn, as another CTA's next ones may come before the last of these
     RowMsg xmsg[2][kMaxCluster];
-    RowMsg warp[2][kWarps];
+    RowMsg part[kMeta][kWarps];
     RowMeta<OP> meta[kMeta];
-    RowGrad grad[2];    // of the last two rows: a row without logits passes one barrier only
-    DistillRow drow[2];
-    int32_t dead;       // a wait ran out: nothing waits any more
-    int32_t dup;        // distill: an entry is listed twice
-    uint32_t tail_mark; // distill: marks of the last V mod VEC entries
+    RowFin fin[kMeta];
+    int32_t dead;                                 // a wait ran out: nothing waits any more
 };
+static_assert(offsetof(RowShared<kOpLogp>, xmsg) % 16 == 0 && offsetof(RowShared<kOpPolicy>, xmsg) % 16 == 0 &&
+              offsetof(RowShared<kOpDistill>, xmsg) % 16 == 0 && sizeof(RowMsg) == 16, "st.async takes 16-byte boundaries");
 
 // A bounded wait that gives up for good once any wait of the block has.
 template <int OP>
@@ -170,10 +189,27 @@ __device__ __forceinline__ void row_wait(RowShared<OP> &sh, uint64_t *bar, uint3
     }
 }
 
-// A barrier of the consumer warps.
-__device__ __forceinline__ void cons_sync() {
-    __syncwarp();
-    asm volatile("bar.sync 1, %0;" ::"n"(kCons) : "memory");
+// A bounded wait for one barrier per lane (null: none): `act` runs for a lane as soon as its barrier is
+// through.
+template <int OP, typename Act>
+__device__ __forceinline__ void lanes_wait(RowShared<OP> &sh, bool mine, uint64_t *bar, uint32_t parity, uint32_t *status, Act act) {
+    uint64_t t0 = 0;
+    bool pending = mine;
+    while (true) {
+        if (pending && (bar == nullptr || ptx::mbar_try_wait(ptx::smem_u32(bar), parity))) {
+            act();
+            pending = false;
+        }
+        if (!__any_sync(0xffffffffu, pending)) return;
+        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&sh.dead) != 0)) return;
+        uint64_t now;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+        if (t0 == 0) t0 = now;
+        if (now - t0 > 2000000000ull) {
+            *reinterpret_cast<volatile int32_t *>(&sh.dead) = 1;
+            post_raise(status, RL_ERR_TIMEOUT);
+        }
+    }
 }
 
 // 16 bytes into the shared memory of a CTA of the cluster, counted on its mbarrier.
@@ -181,21 +217,6 @@ __device__ __forceinline__ void st_async16(uint32_t dst, uint32_t bar, const Row
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
                  "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(__float_as_uint(v.u)), "r"(v.bad), "r"(bar)
                  : "memory");
-}
-
-// find_seq by a warp: each step narrows 32-fold.
-__device__ __forceinline__ int warp_find_seq(const int32_t *__restrict__ cu, int S, int t) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = S;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + lane * step;
-        const bool le = lane == 0 || (at < hi && __ldg(cu + at) <= t);
-        const int l = 31 - __clz(__ballot_sync(0xffffffffu, le));
-        lo += l * step;
-        hi = min(hi, lo + step);
-    }
-    return (__ldg(cu + lo) <= t && t < __ldg(cu + lo + 1)) ? lo : -1;
 }
 
 template <int OP>
@@ -209,127 +230,176 @@ struct OpParams<kOpDistill> { using type = DistillParams; };
 template <>
 struct OpParams<kOpScale> { using type = ScaleParams; };
 
-// Whether row t is copied into the ring.
-template <int OP>
-__device__ __forceinline__ bool row_wanted(const typename OpParams<OP>::type &p, int t) {
-    if constexpr (OP == kOpLogp) return !p.r.mask || __ldg(p.r.mask + t);
-    if constexpr (OP == kOpPolicy) return p.read_masked || __ldg(p.r.mask + t);
-    return __ldg(p.r.mask + t) != 0;
+// The record of row t, by one lane (the producer's lanes gather those of 32 rows at once).
+template <typename T, int OP>
+__device__ __forceinline__ RowMeta<OP> load_meta(const typename OpParams<OP>::type &p, int t, int N) {
+    using VT = PostVec<T>;
+    RowMeta<OP> m{};
+    const char *z = row_in<T>(p.r, t);
+    if constexpr (OP == kOpLogp) {
+        const int y = __ldg(p.r.targets + t);
+        m.read = !p.r.mask || __ldg(p.r.mask + t);
+        m.y = y >= 0 && y < p.r.V ? y : -1;
+        m.zy = m.read && m.y >= 0 ? VT::load1(z, y) : 0.f;
+    } else if constexpr (OP == kOpPolicy) {
+        m.tok = policy_load(p, t, find_seq(p.r.cu_seqlens, p.r.S, t));
+        m.read = m.tok.m || p.read_masked;
+        m.y = m.tok.ok ? m.tok.y : -1;
+        m.zy = m.read && m.tok.ok ? VT::load1(z, m.tok.y) : 0.f;
+    } else if constexpr (OP == kOpScale) {
+        const int i = find_seq(p.r.cu_seqlens, p.r.S, t);
+        const int y = __ldg(p.r.targets + t);
+        m.grad = RowGrad{0.f, 0.f, 0.f, -1};
+        if (i >= 0 && __ldg(p.r.mask + t) && y >= 0 && y < p.r.V) {
+            const float2 st = p.stats[t];
+            const float g = p.coef[i];
+            if (g != 0.f) m.grad = post_row_grad(g, PostStats{st.x, st.y, 0.f}, p.r.logp[t], y);
+        }
+        m.read = m.grad.y >= 0;
+    } else {
+        const int i = find_seq(p.r.cu_seqlens, p.r.S, t);
+        m.read = i >= 0 && __ldg(p.r.mask + t);
+        if (m.read) {
+            m.rec = p.rec[t];
+            m.w = p.per_token ? 1.0 / (double)N : 1.0 / ((double)p.r.S * (double)p.seq_n[i]);
+            // a teacher that gives the row no mass: it contributes nothing
+            if (!(m.rec.w > 0.f || isnan(m.rec.w))) m.read = 0;
+        }
+        m.copied = m.read;
+    }
+    return m;
 }
 
-// The record of row t, by the producer warp.
-template <typename T, int OP>
-__device__ __forceinline__ void load_meta(const typename OpParams<OP>::type &p, int t, int N, RowMeta<OP> &m, float *s_z,
-                                          float *s_lq, int *s_id) {
+// distill: the teacher's entries of row t and the student's logits there, by the producer warp.
+template <typename T>
+__device__ __forceinline__ void load_entries(const DistillParams &p, int t, RowMeta<kOpDistill> &m, float *s_z, float *s_lq, int *s_id) {
     using VT = PostVec<T>;
     const int lane = threadIdx.x & 31;
     const char *z = row_in<T>(p.r, t);
-    const bool copied = row_wanted<OP>(p, t);
-    if constexpr (OP == kOpLogp) {
-        if (lane == 0) {
-            const int y = __ldg(p.r.targets + t);
-            m.copied = m.read = copied;
-            m.y = y >= 0 && y < p.r.V ? y : -1;
-            m.zy = copied && m.y >= 0 ? VT::load1(z, y) : 0.f;
-        }
-    } else if constexpr (OP == kOpPolicy) {
-        const int i = warp_find_seq(p.r.cu_seqlens, p.r.S, t);
-        if (lane == 0) {
-            m.tok = policy_load(p, t, i);
-            m.copied = copied;
-            m.read = m.tok.m || p.read_masked;
-            m.y = m.tok.ok ? m.tok.y : -1;
-            m.zy = copied && m.tok.ok ? VT::load1(z, m.tok.y) : 0.f;
-        }
-    } else if constexpr (OP == kOpScale) {
-        const int i = warp_find_seq(p.r.cu_seqlens, p.r.S, t);
-        if (lane == 0) {
-            const int y = __ldg(p.r.targets + t);
-            RowGrad gr{0.f, 0.f, 0.f, -1};
-            if (i >= 0 && copied && y >= 0 && y < p.r.V) {
-                const float2 st = p.stats[t];
-                const float g = p.coef[i];
-                if (g != 0.f) gr = post_row_grad(g, PostStats{st.x, st.y, 0.f}, p.r.logp[t], y);
-            }
-            m.copied = copied;
-            m.read = gr.y >= 0;
-            m.grad = gr;
-        }
-    } else {
-        const int i = warp_find_seq(p.r.cu_seqlens, p.r.S, t);
-        const bool on = i >= 0 && copied;
-        int bad = 0, have = 0;
-        float4 rec = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (on) {
+    const float4 rec = m.rec;
+    int bad = 0, have = 0;
 #pragma unroll 4
-            for (int k = lane; k < p.K; k += 32) {
-                const int id = __ldg(p.ids + (int64_t)t * p.ldk + k);
-                const float val = __ldg(p.vals + (int64_t)t * p.ldk + k);
-                const bool real = id >= 0 && id < p.r.V;
-                bad |= id < -1 || id >= p.r.V;
-                have += real;
-                s_id[k] = real ? id : -1;
-                s_z[k] = real ? VT::load1(z, id) : -INFINITY;
-                s_lq[k] = val;
-            }
-            rec = p.rec[t];
-            for (int k = lane; k < p.K; k += 32) s_lq[k] = s_id[k] >= 0 ? (s_lq[k] - rec.x) - rec.y : -INFINITY;
-            have = warp_sum_i32(have);
-            bad = __any_sync(0xffffffffu, bad);
+    for (int k = lane; k < p.K; k += 32) {
+        const int id = __ldg(p.ids + (int64_t)t * p.ldk + k);
+        const float val = __ldg(p.vals + (int64_t)t * p.ldk + k);
+        const bool real = id >= 0 && id < p.r.V;
+        bad |= id < -1 || id >= p.r.V;
+        have += real;
+        s_id[k] = real ? id : -1;
+        s_z[k] = real ? VT::load1(z, id) : -INFINITY;
+        s_lq[k] = real ? (val - rec.x) - rec.y : -INFINITY;
+    }
+    have = warp_sum_i32(have);
+    bad = __any_sync(0xffffffffu, bad);
+    __syncwarp();
+    if (lane == 0) {
+        m.bad = bad;
+        m.have = have;
+        if (bad || have == 0) m.read = 0;
+    }
+    __syncwarp();
+}
+
+// Takes the teacher's entries out of the row's slice in the rings, by the producer warp: each becomes
+// -inf, so that the fold leaves it out. It first gets its index as a tag: an entry listed twice finds
+// another's tag, or -inf, in its place. The row's segments are at place d of their rings, one per warp.
+template <typename T>
+__device__ __forceinline__ void mark_entries(const RowPlan &plan, uint4 *ring, int d, int v0, int v1, int nvec, bool last_rank,
+                                             const int *s_id, int K, RowMeta<kOpDistill> &m) {
+    using VT = PostVec<T>;
+    using Tag = typename VT::Tag;
+    constexpr int VEC = VT::kElems;
+    const int lane = threadIdx.x & 31;
+    auto place = [&](int id) -> volatile Tag * {
+        return reinterpret_cast<volatile Tag *>(ring + (size_t)d * kWarps * plan.seg + (id / VEC - v0)) + id % VEC;
+    };
+    int dup = 0;
+    uint32_t tail = 0;
+    for (int k = lane; k < K; k += 32) {
+        const int id = s_id[k];
+        if (id >= v0 * VEC && id < v1 * VEC) {
+            *place(id) = (Tag)k;
+        } else if (last_rank && id >= nvec * VEC) {
+            const uint32_t bit = 1u << (id - nvec * VEC);
+            dup |= (tail & bit) != 0;
+            tail |= bit;
         }
-        if (lane == 0) {
-            // a teacher that gives the row no mass contributes nothing; nor does a bad row
-            const bool none = have == 0 || !(rec.w > 0.f || isnan(rec.w));
-            m.copied = copied;
-            m.read = on && !bad && !none;
-            m.bad = bad;
-            m.have = have;
-            m.rec = rec;
-            m.w = !on ? 0.0 : p.per_token ? 1.0 / (double)N : 1.0 / ((double)p.r.S * (double)p.seq_n[i]);
-        }
+    }
+    // the last V mod VEC entries: a bit that two lanes hold was listed twice
+#pragma unroll
+    for (int b = 0; b < VEC - 1; ++b) {
+        const uint32_t who = __ballot_sync(0xffffffffu, (tail >> b) & 1);
+        dup |= __popc(who) > 1;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) tail |= __shfl_xor_sync(0xffffffffu, tail, off);
+    __syncwarp();
+    for (int k = lane; k < K; k += 32) {
+        const int id = s_id[k];
+        if (id < v0 * VEC || id >= v1 * VEC) continue;
+        if (*place(id) == (Tag)k) *place(id) = VT::kNegInf;
+        else dup = 1;
+    }
+    ptx::fence_proxy_async_smem();  // the next copies into these segments come after the marks
+    dup = __any_sync(0xffffffffu, dup);
+    if (lane == 0) {
+        m.dup = dup;
+        m.tail_mark = tail;
     }
 }
 
 template <typename T, int OP, bool kEnt>
-__global__ void __launch_bounds__(kRowThreads, 3)
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks)
 ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __grid_constant__ RowPlan plan, int nclusters) {
     using VT = PostVec<T>;
     constexpr int VEC = VT::kElems;
-    constexpr bool kStats = OP != kOpScale;   // a row is folded first
+    constexpr int kMeta = kMetaOf(OP);
+    constexpr bool kStats = OP != kOpScale;   // a row is folded
     constexpr bool kGrad = OP != kOpLogp;     // a row is written
-    extern __shared__ __align__(128) uint4 s_ring[];
+    extern __shared__ __align__(128) uint4 s_ring[];  // [depth][kWarps][seg]
     __shared__ RowShared<OP> sh;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = plan.cluster;
     const int rank = (int)blockIdx.x % C, q = (int)blockIdx.x / C;
     const int T_ = p.r.T, V = p.r.V, nvec = V / VEC;
     const int v0 = min(nvec, rank * plan.slice), v1 = min(nvec, v0 + plan.slice);  // this CTA's 16-byte groups
-    const int n_tiles = (v1 - v0 + plan.tile - 1) / plan.tile;
     const bool last_rank = rank == C - 1;    // has the last V mod VEC entries too
-    const int tail_v = nvec * VEC + tid;     // a consumer's entry of those
-    const bool has_tail = last_rank && tail_v < V;
     float c = kLog2e;
     int K = 0, N = 0;
     if constexpr (OP == kOpDistill) {
         c = p.c;
         K = p.K;
     }
-    float *s_meta = reinterpret_cast<float *>(s_ring + (size_t)plan.slots * plan.tile);  // [kMeta][3][K]
+    // after the ring: the segments' barriers (copied; free again), [depth][kWarps] each, and the teacher's
+    // entries, [kMeta][3][K]
+    uint64_t *s_full = reinterpret_cast<uint64_t *>(s_ring + (size_t)plan.depth * kWarps * plan.seg);
+    uint64_t *s_empty = s_full + plan.depth * kWarps;
+    float *s_meta = reinterpret_cast<float *>(s_empty + plan.depth * kWarps);
+    const int n_rows = q < T_ ? (T_ - 1 - q) / nclusters + 1 : 0;
+    // the r-th row of this cluster; scale: the rows read last are the likeliest in L2
+    auto row_of = [&](int r) {
+        const int t = q + r * nclusters;
+        return OP == kOpScale ? T_ - 1 - t : t;
+    };
+    auto use = [](int r) { return (uint32_t)(r / kMeta) & 1u; };  // the phase of row r's record
+    // groups of part j of warp w's share
+    auto seg_groups = [&](int w, int j) { return max(0, min(plan.seg, v1 - v0 - (j * kWarps + w) * plan.seg)); };
 
     if (tid == 0) {
-        for (int s = 0; s < plan.slots; ++s) {
-            ptx::mbar_init(ptx::smem_u32(&sh.full[s]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sh.empty[s]), kWarps);
+        for (int s = 0; s < plan.depth * kWarps; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&s_full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&s_empty[s]), 1);
         }
         for (int s = 0; s < kMeta; ++s) {
             ptx::mbar_init(ptx::smem_u32(&sh.mfull[s]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sh.mempty[s]), kWarps);
+            ptx::mbar_init(ptx::smem_u32(&sh.mempty[s]), kWarps + (kStats ? 1 : 0));
+            ptx::mbar_init(ptx::smem_u32(&sh.part_full[s]), kWarps);
+            ptx::mbar_init(ptx::smem_u32(&sh.fin_full[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh.written[s]), kWarps);
         }
         for (int s = 0; s < 2; ++s) ptx::mbar_init(ptx::smem_u32(&sh.xbar[s]), 1);
         ptx::fence_mbar_init();
         sh.dead = 0;
-        sh.dup = 0;
-        sh.tail_mark = 0;
     }
     if constexpr (OP == kOpLogp)
         if (p.zero && blockIdx.x == 0 && tid == 0) *p.zero = 0;
@@ -346,177 +416,109 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
 
     if (warp == kWarps) {
         // ------------------------------------------------ producer
-        int n = 0;  // tiles issued
-        int slot = 0;
+        int n = 0, d = 0;      // segments issued for each warp; their next place
         uint32_t phase = 0;
         const uint64_t pol = ptx::l2_evict_first_policy();
-        int r = 0;
-        for (int qt = q; qt < T_; qt += nclusters, ++r) {
-            const int t = OP == kOpScale ? T_ - 1 - qt : qt;  // scale: the rows read last are the likeliest in L2
-            const int tiles = row_wanted<OP>(p, t) ? n_tiles : 0;
+        RowMeta<OP> mine{};    // the record of row (r & ~31) + lane
+        for (int r = 0; r < n_rows; ++r) {
+            const int t = row_of(r), ms = r % kMeta;
+            if ((r & 31) == 0 && r + lane < n_rows) mine = load_meta<T, OP>(p, row_of(r + lane), N);
+            const int read = __shfl_sync(0xffffffffu, mine.read, r & 31);
             const char *src = row_in<T>(p.r, t) + (size_t)v0 * 16;
+            const int d0 = d;
+            const uint32_t phase0 = phase;
             auto record = [&] {
-                const int ms = r % kMeta;
-                if (r >= kMeta) row_wait(sh, &sh.mempty[ms], ((r / kMeta) & 1) ^ 1, p.r.status);
-                float *mz = s_meta + (size_t)ms * 3 * K;
-                load_meta<T, OP>(p, t, N, sh.meta[ms], mz, mz + K, reinterpret_cast<int *>(mz + 2 * K));
+                if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
+                if (lane == (r & 31)) sh.meta[ms] = mine;
                 __syncwarp();
+                if constexpr (OP == kOpDistill) {
+                    if (read) {
+                        float *mz = s_meta + (size_t)ms * 3 * K;
+                        int *s_id = reinterpret_cast<int *>(mz + 2 * K);
+                        load_entries<T>(p, t, sh.meta[ms], mz, mz + K, s_id);
+                        lanes_wait(sh, lane < kWarps, &s_full[d0 * kWarps + lane % kWarps], phase0, p.r.status, [] {});
+                        __syncwarp();
+                        if (sh.meta[ms].read) mark_entries<T>(plan, s_ring, d0, v0, v1, nvec, last_rank, s_id, K, sh.meta[ms]);
+                        __syncwarp();
+                    }
+                }
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mfull[ms]));
             };
-            if (tiles == 0) record();
-            for (int j = 0; j < tiles; ++j) {
-                const int g = min(plan.tile, v1 - v0 - j * plan.tile);
-                if (n >= plan.slots) row_wait(sh, &sh.empty[slot], phase ^ 1, p.r.status);
-                if (lane == 0 && !*reinterpret_cast<volatile int32_t *>(&sh.dead)) {
-                    const uint32_t bar = ptx::smem_u32(&sh.full[slot]);
-                    ptx::mbar_arrive_expect_tx(bar, (uint32_t)g * 16);
-                    const uint32_t dst = ptx::smem_u32(s_ring + (size_t)slot * plan.tile);
-                    const char *from = src + (size_t)j * plan.tile * 16;
-                    if (OP == kOpLogp && p.r.dlogits) ptx::bulk_g2s(dst, from, (uint32_t)g * 16, bar);  // read again
-                    else ptx::bulk_g2s_hint(dst, from, (uint32_t)g * 16, bar, pol);
-                }
-                __syncwarp();
-                ++n;
-                if (++slot == plan.slots) slot = 0, phase ^= 1;
-                // the record goes between the row's first copies and those that wait for tiles of the
-                // same row (a row longer than the ring): the consumers free none before they have it
-                if (j == min(tiles, plan.slots) - 1) record();
+            if (!read) {
+                record();
+                continue;
             }
+            for (int j = 0; j < plan.parts; ++j) {
+                const int w = lane % kWarps;
+                const int g = seg_groups(w, j);
+                uint64_t *bar = n >= plan.depth ? &s_empty[d * kWarps + w] : nullptr;
+                lanes_wait(sh, lane < kWarps, bar, phase ^ 1, p.r.status, [&] {
+                    const uint32_t full = ptx::smem_u32(&s_full[d * kWarps + w]);
+                    if (g == 0) {
+                        ptx::mbar_arrive(full);
+                        return;
+                    }
+                    ptx::mbar_arrive_expect_tx(full, (uint32_t)g * 16);
+                    const uint32_t dst = ptx::smem_u32(s_ring + ((size_t)d * kWarps + w) * plan.seg);
+                    const char *from = src + ((size_t)j * kWarps + w) * plan.seg * 16;
+                    if (OP == kOpLogp && p.r.dlogits) ptx::bulk_g2s(dst, from, (uint32_t)g * 16, full);  // read again
+                    else ptx::bulk_g2s_hint(dst, from, (uint32_t)g * 16, full, pol);
+                });
+                ++n;
+                if (++d == plan.depth) d = 0, phase ^= 1;
+                // the record goes between the row's first copies and those that wait for segments of the
+                // same row (a row longer than the ring): the consumers free none before they have it
+                if (j == min(plan.parts, plan.depth) - 1) record();
+                if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&sh.dead) != 0)) break;
+            }
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&sh.dead) != 0)) break;
         }
-        if (*reinterpret_cast<volatile int32_t *>(&sh.dead) && lane == 0) {
+        if (*reinterpret_cast<volatile int32_t *>(&sh.dead) && lane < kWarps) {
             // a wait ran out: no copy may be in flight when the block exits
-            for (int k = max(0, n - plan.slots); k < n; ++k)
-                ptx::mbar_wait(ptx::smem_u32(&sh.full[k % plan.slots]), (k / plan.slots) & 1, 100000000ull);
+            for (int k = max(0, n - plan.depth); k < n; ++k)
+                ptx::mbar_wait(ptx::smem_u32(&s_full[(k % plan.depth) * kWarps + lane]), (k / plan.depth) & 1, 100000000ull);
         }
-    } else {
-        // ------------------------------------------------ consumers
-        int slot = 0;
-        uint32_t phase = 0;
-        int r = 0, nr = 0;  // rows; rows folded
-        for (int qt = q; qt < T_; qt += nclusters, ++r) {
-            const int t = OP == kOpScale ? T_ - 1 - qt : qt;
-            const int ms = r % kMeta;
-            row_wait(sh, &sh.mfull[ms], (r / kMeta) & 1, p.r.status);
+    } else if (warp > kWarps) {
+        // ------------------------------------------------ finisher
+        int exchanges = 0;
+        for (int r = 0; kStats && r < n_rows; ++r) {
+            const int t = row_of(r), ms = r % kMeta;
+            row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
+            row_wait(sh, &sh.part_full[ms], use(r), p.r.status);
             const RowMeta<OP> &meta = sh.meta[ms];
-            const bool copied = meta.copied, read = meta.read;
-            const char *z = row_in<T>(p.r, t);
+            RowFin &fin = sh.fin[ms];
+            const bool read = meta.read;
             const float *s_z = s_meta + (size_t)ms * 3 * K, *s_lq = s_z + K;
             const int *s_id = reinterpret_cast<const int *>(s_z + 2 * K);
-            int y = -1;
-            if constexpr (OP == kOpLogp || OP == kOpPolicy) y = meta.y;
             PostStats st{0.f, 1.f, 0.f};
             int dup = 0;
-
-            if (kStats && read) {
-                if constexpr (OP == kOpDistill) {
-                    // marks: the teacher's entries of this slice become -inf in the ring, so that the
-                    // fold leaves them out. Each first gets its index as a tag: an entry listed twice
-                    // finds another's tag (or -inf) in its place.
-                    int sl = slot;
-                    uint32_t ph = phase;
-                    for (int j = 0; j < n_tiles; ++j) {
-                        row_wait(sh, &sh.full[sl], ph, p.r.status);
-                        if (++sl == plan.slots) sl = 0, ph ^= 1;
-                    }
-                    using Tag = typename VT::Tag;
-                    auto place = [&](int id) -> volatile Tag * {
-                        const int g = id / VEC - v0;
-                        int s = slot + g / plan.tile;
-                        if (s >= plan.slots) s -= plan.slots;
-                        return reinterpret_cast<volatile Tag *>(s_ring + (size_t)s * plan.tile + g % plan.tile) + id % VEC;
-                    };
-                    for (int k = tid; k < K; k += kCons) {
-                        const int id = s_id[k];
-                        if (id >= v0 * VEC && id < v1 * VEC) {
-                            *place(id) = (Tag)k;
-                        } else if (last_rank && id >= nvec * VEC) {
-                            const uint32_t bit = 1u << (id - nvec * VEC);
-                            if (atomicOr(&sh.tail_mark, bit) & bit) sh.dup = 1;
-                        }
-                    }
-                    cons_sync();
-                    for (int k = tid; k < K; k += kCons) {
-                        const int id = s_id[k];
-                        if (id < v0 * VEC || id >= v1 * VEC) continue;
-                        if (*place(id) == (Tag)k) *place(id) = VT::kNegInf;
-                        else sh.dup = 1;
-                    }
-                    ptx::fence_proxy_async_smem();  // the next copy into these tiles comes after the marks
-                    cons_sync();
-                }
-                st = kPostStart;
-                const int ky = y >= 0 ? y / VEC - v0 : -1;
-                int sl = slot;
-                uint32_t ph = phase;
-                for (int j = 0; j < n_tiles; ++j) {
-                    if (OP != kOpDistill) row_wait(sh, &sh.full[sl], ph, p.r.status);
-                    uint4 *tile = s_ring + (size_t)sl * plan.tile;
-                    const int g = min(plan.tile, v1 - v0 - j * plan.tile);
-                    if constexpr (OP != kOpDistill) {
-                        // the thread that folds the sampled entry's group takes the entry out of it
-                        const int kyt = ky - j * plan.tile;
-                        if (kyt >= 0 && kyt < g && kyt % kCons == tid) {
-                            reinterpret_cast<volatile typename VT::Tag *>(tile + kyt)[y % VEC] = VT::kNegInf;
-                            ptx::fence_proxy_async_smem();  // the next copy into the tile comes after this
-                        }
-                    }
-                    int k = tid;
-                    for (; k + 3 * kCons < g; k += 4 * kCons) {
-                        const uint4 v[4] = {tile[k], tile[k + kCons], tile[k + 2 * kCons], tile[k + 3 * kCons]};
-                        post_fold_groups<T, kEnt>(st, v, c);
-                    }
-                    for (; k < g; k += kCons) {
-                        const uint4 v[1] = {tile[k]};
-                        post_fold_groups<T, kEnt>(st, v, c);
-                    }
-                    if (!kGrad) {
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[sl]));
-                    }
-                    if (++sl == plan.slots) sl = 0, ph ^= 1;
-                }
-                if (!kGrad) slot = sl, phase = ph;
-                if (has_tail && tail_v != y && !(OP == kOpDistill && (sh.tail_mark >> tid) & 1)) {
-                    const float x[1] = {VT::load1(z, tail_v)};
-                    post_fold<kEnt>(st, x, c);
-                }
+            if (read) {
+                if constexpr (OP == kOpDistill) dup = meta.dup;
+                RowMsg w = sh.part[ms][lane < kWarps ? lane : 0];
+                st = lane < kWarps ? PostStats{w.m, w.s, w.u} : kPostStart;
                 st = post_warp_merge<kEnt>(st, c);
-                const int x = nr & 1;
-                if (lane == 0) sh.warp[x][warp] = RowMsg{st.m, st.s, st.u, 0};
-                cons_sync();
-                if (warp == 0) {
-                    RowMsg w = sh.warp[x][lane < kWarps ? lane : 0];
-                    st = lane < kWarps ? PostStats{w.m, w.s, w.u} : kPostStart;
+                if (C > 1) {
+                    const int x = exchanges & 1;
+                    const uint32_t bar = ptx::smem_u32(&sh.xbar[x]);
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(C * sizeof(RowMsg)));
+                    __syncwarp();
+                    if (lane < C)
+                        st_async16(ptx::mapa_shared(ptx::smem_u32(&sh.xmsg[x][rank]), lane), ptx::mapa_shared(bar, lane),
+                                   RowMsg{st.m, st.s, st.u, dup});
+                    row_wait(sh, &sh.xbar[x], (exchanges >> 1) & 1, p.r.status);
+                    w = sh.xmsg[x][lane < C ? lane : 0];
+                    ++exchanges;
+                    st = lane < C ? PostStats{w.m, w.s, w.u} : kPostStart;
+                    dup = __any_sync(0xffffffffu, lane < C && w.bad);
                     st = post_warp_merge<kEnt>(st, c);
-                    if constexpr (OP == kOpDistill) {
-                        dup = *reinterpret_cast<volatile int32_t *>(&sh.dup);
-                        __syncwarp();
-                        if (lane == 0) sh.dup = 0, sh.tail_mark = 0;
-                    }
-                    if (C > 1) {
-                        const uint32_t bar = ptx::smem_u32(&sh.xbar[x]);
-                        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(C * sizeof(RowMsg)));
-                        __syncwarp();
-                        if (lane < C)
-                            st_async16(ptx::mapa_shared(ptx::smem_u32(&sh.xmsg[x][rank]), lane), ptx::mapa_shared(bar, lane),
-                                       RowMsg{st.m, st.s, st.u, dup});
-                        row_wait(sh, &sh.xbar[x], (nr >> 1) & 1, p.r.status);
-                        w = sh.xmsg[x][lane < C ? lane : 0];
-                        st = lane < C ? PostStats{w.m, w.s, w.u} : kPostStart;
-                        dup = __any_sync(0xffffffffu, lane < C && w.bad);
-                        st = post_warp_merge<kEnt>(st, c);
-                    }
                 }
-                ++nr;
             }
-
-            // the row's results, by warp 0 of every CTA (rank 0 writes them)
             if constexpr (OP == kOpLogp) {
-                if (tid == 0 && rank == 0) {
+                if (lane == 0 && rank == 0) {
                     float logp = 0.f, ent = 0.f;
                     if (read) {
                         logp = __int_as_float(0x7fc00000);
-                        if (y >= 0) logp = post_target<kEnt>(st, meta.zy, st);
+                        if (meta.y >= 0) logp = post_target<kEnt>(st, meta.zy, st);
                         else post_raise(p.r.status, RL_ERR_TARGET_RANGE);
                         if (!post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
                         if (kEnt) ent = post_entropy(st);
@@ -526,92 +528,190 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                     if (p.stats) p.stats[t] = make_float2(st.m, st.s);
                 }
             } else if constexpr (OP == kOpPolicy) {
-                if (tid == 0) {
-                    const float logp = read && y >= 0 ? post_target<kEnt>(st, meta.zy, st) : 0.f;
-                    sh.grad[r & 1] = policy_row(p, t, meta.tok, st, logp, rank == 0, sum);
+                if (lane == 0) {
+                    const float logp = read && meta.y >= 0 ? post_target<kEnt>(st, meta.zy, st) : 0.f;
+                    fin.grad = policy_row(p, t, meta.tok, st, logp, rank == 0, sum);
+                    ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
                 }
-                cons_sync();
             } else if constexpr (OP == kOpDistill) {
-                if (warp == 0) {
-                    const bool live = read && !dup;
-                    DistillRow d{};
-                    if (live) {
-                        float Mk, Sk;
-                        distill_entry_stats(s_z, K, c, Mk, Sk);
-                        d = distill_finish(p, st, Mk, Sk, s_z, s_lq, meta.rec, (float)meta.w * p.scale * p.inv_tau, V - meta.have);
-                    }
+                const bool live = read && !dup;
+                float Mk = 0.f, Sk = 0.f;
+                DistillRow row{};
+                if (live) {
+                    distill_entry_stats(s_z, K, c, Mk, Sk);
+                    row = distill_finish(p, st, Mk, Sk, s_z, s_lq, meta.rec, (float)meta.w * p.scale * p.inv_tau, V - meta.have);
+                }
+                if (lane == 0) {
+                    fin.grad = RowGrad{live ? row.ct : 0.f, row.m, 0.f, live ? 0 : -1};
+                    ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
+                }
+                if (rank == 0) {
+                    const float kl = live ? distill_kl(p, row, st, Mk, Sk, s_z, s_lq, meta.rec, V - meta.have) : 0.f;
                     if (lane == 0) {
-                        sh.drow[r & 1] = d;
-                        sh.grad[r & 1] = RowGrad{live ? d.ct : 0.f, d.m, 0.f, live ? 0 : -1};
-                        if (rank == 0) {
-                            const bool bad = meta.bad || dup;
-                            if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
-                            if (live && !isfinite(d.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
-                            if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : d.kl;
-                            sum.loss += meta.w * (double)p.scale * (double)d.kl;
-                        }
+                        const bool bad = meta.bad || dup;
+                        if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
+                        if (live && !isfinite(row.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
+                        if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : kl;
+                        sum.loss += meta.w * (double)p.scale * (double)kl;
                     }
                 }
-                cons_sync();
-            }
-
-            if constexpr (kGrad) {
-                RowGrad gr;
-                if constexpr (OP == kOpScale) gr = meta.grad;
-                else gr = sh.grad[r & 1];
-                char *dz = row_out<T>(p.r, t);
-                const bool zero = gr.y < 0;
-                const int ky = OP == kOpDistill || zero ? -1 : gr.y / VEC - v0;
-                for (int j = 0; j < n_tiles; ++j) {
-                    const int g = min(plan.tile, v1 - v0 - j * plan.tile);
-                    char *to = dz + ((size_t)v0 + (size_t)j * plan.tile) * 16;
-                    const uint4 *tile = s_ring + (size_t)slot * plan.tile;
-                    if (copied && !(kStats && read)) row_wait(sh, &sh.full[slot], phase, p.r.status);
-                    if (zero) {
-                        for (int k = tid; k < g; k += kCons) __stcs(reinterpret_cast<uint4 *>(to) + k, make_uint4(0, 0, 0, 0));
-                    } else {
-                        const int kyt = ky - j * plan.tile;
-#pragma unroll 4
-                        for (int k = tid; k < g; k += kCons) {
-                            float x[VEC];
-                            VT::decode(tile[k], x);
-#pragma unroll
-                            for (int i = 0; i < VEC; ++i) x[i] = gr.a * ex2_approx((x[i] - gr.m) * c);
-                            __stcs(reinterpret_cast<uint4 *>(to) + k, VT::encode(x));
-                        }
-                        // by the thread that wrote the group, after it
-                        if (OP != kOpDistill && kyt >= 0 && kyt < g && kyt % kCons == tid) VT::store1(dz, gr.y, gr.gy);
-                    }
-                    if (copied) {
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.empty[slot]));
-                        if (++slot == plan.slots) slot = 0, phase ^= 1;
-                    }
-                }
-                if (has_tail) {
-                    const float e = zero ? 0.f : gr.a * ex2_approx((VT::load1(z, tail_v) - gr.m) * c);
-                    VT::store1(dz, tail_v, OP != kOpDistill && !zero && tail_v == gr.y ? gr.gy : e);
-                }
-                if constexpr (OP == kOpDistill) {
-                    if (!zero) {
-                        cons_sync();  // the entries are written after the rest of the row, whose value they replace
-                        const DistillRow d = sh.drow[r & 1];
-                        for (int k = tid; k < K; k += kCons) {
-                            const int id = s_id[k];
-                            if ((id >= v0 * VEC && id < v1 * VEC) || (last_rank && id >= nvec * VEC))
-                                VT::store1(dz, id, distill_entry(p, d, s_z[k], s_lq[k]));
-                        }
+                // the entries are written after the rest of the row, whose value they replace
+                row_wait(sh, &sh.written[ms], use(r), p.r.status);
+                if (live) {
+                    char *dz = row_out<T>(p.r, t);
+                    for (int k = lane; k < K; k += 32) {
+                        const int id = s_id[k];
+                        if ((id >= v0 * VEC && id < v1 * VEC) || (last_rank && id >= nvec * VEC))
+                            VT::store1(dz, id, distill_entry(p, row, s_z[k], s_lq[k]));
                     }
                 }
             }
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
         }
+    } else {
+        // ------------------------------------------------ consumers
+        const int tail_v = nvec * VEC + tid;     // this thread's entry of the last V mod VEC
+        const bool has_tail = last_rank && tail_v < V;
+        int da = 0, db = 0;                      // the next segments of the fold and of the write
+        uint32_t phase_a = 0, phase_b = 0;
+        auto next = [&](int &d, uint32_t &phase) {
+            if (++d == plan.depth) d = 0, phase ^= 1;
+        };
+        auto copied = [&](const RowMeta<OP> &m) {  // whether the row is in the ring
+            if constexpr (OP == kOpDistill) return m.copied != 0;
+            else return m.read != 0;
+        };
+        // A: the statistics of row r
+        auto fold = [&](int r) {
+            const int ms = r % kMeta;
+            row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
+            const RowMeta<OP> &meta = sh.meta[ms];
+            if (meta.read) {
+                int y = -1;
+                uint32_t marks = 0;
+                if constexpr (OP == kOpLogp || OP == kOpPolicy) y = meta.y;
+                if constexpr (OP == kOpDistill) marks = meta.tail_mark;
+                const int ky = y >= 0 && y < nvec * VEC ? y / VEC - v0 : -1;  // the sampled entry's group
+                PostAcc acc = post_acc();
+                for (int j = 0; j < plan.parts; ++j) {
+                    row_wait(sh, &s_full[da * kWarps + warp], phase_a, p.r.status);
+                    uint4 *seg = s_ring + ((size_t)da * kWarps + warp) * plan.seg;
+                    const int g = seg_groups(warp, j);
+                    if constexpr (OP != kOpDistill) {
+                        // the lane that folds the sampled entry's group takes the entry out of it
+                        const int ks = ky - (j * kWarps + warp) * plan.seg;
+                        if (ky >= 0 && ks >= 0 && ks < g && (ks & 31) == lane) {
+                            reinterpret_cast<volatile typename VT::Tag *>(seg + ks)[y % VEC] = VT::kNegInf;
+                            ptx::fence_proxy_async_smem();  // the next copy into the segment comes after this
+                        }
+                    }
+                    int k = lane;
+                    for (; k - lane + 32 * kBatch <= g; k += 32 * kBatch) {
+                        uint4 v[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) v[i] = seg[k + 32 * i];
+                        post_fold_groups<T, kEnt>(acc, v, c);
+                    }
+                    if (k - lane < g) {  // the rest of the segment, filled up with -inf
+                        uint4 v[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) v[i] = k + 32 * i < g ? seg[k + 32 * i] : VT::none();
+                        post_fold_groups<T, kEnt>(acc, v, c);
+                    }
+                    if (!kGrad) {
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&s_empty[da * kWarps + warp]));
+                    }
+                    next(da, phase_a);
+                }
+                PostStats st = acc.stats();
+                if (has_tail && tail_v != y && !((marks >> tid) & 1)) {
+                    const float x[1] = {VT::load1(row_in<T>(p.r, row_of(r)), tail_v)};
+                    post_fold<kEnt>(st, x, c);
+                }
+                st = post_warp_merge<kEnt>(st, c);
+                if (lane == 0) sh.part[ms][warp] = RowMsg{st.m, st.s, st.u, 0};
+            } else if (copied(meta)) {
+                for (int j = 0; j < plan.parts; ++j) next(da, phase_a);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive(ptx::smem_u32(&sh.part_full[ms]));
+                if (!kGrad) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
+            }
+        };
+        // B: the gradient of row r
+        auto write = [&](int r) {
+            const int t = row_of(r), ms = r % kMeta;
+            RowGrad gr;
+            if constexpr (OP == kOpScale) {
+                row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
+                gr = sh.meta[ms].grad;
+            } else {
+                row_wait(sh, &sh.fin_full[ms], use(r), p.r.status);
+                gr = sh.fin[ms].grad;
+            }
+            const bool in_ring = copied(sh.meta[ms]), zero = gr.y < 0;
+            char *dz = row_out<T>(p.r, t);
+            const int ky = OP == kOpDistill || zero || gr.y >= nvec * VEC ? -1 : gr.y / VEC - v0;
+            for (int j = 0; j < plan.parts; ++j) {
+                const int g = seg_groups(warp, j), at = (j * kWarps + warp) * plan.seg;
+                uint4 *to = reinterpret_cast<uint4 *>(dz) + v0 + at;
+                if (in_ring) row_wait(sh, &s_full[db * kWarps + warp], phase_b, p.r.status);  // a row that was not folded
+                if (zero) {
+                    for (int k = lane; k < g; k += 32) __stcs(to + k, make_uint4(0, 0, 0, 0));
+                } else {
+                    const uint4 *seg = s_ring + ((size_t)db * kWarps + warp) * plan.seg;
+                    int k = lane;
+                    for (; k - lane + 32 * kBatch <= g; k += 32 * kBatch) {
+                        uint4 v[kBatch];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) v[i] = seg[k + 32 * i];
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) __stcs(to + k + 32 * i, post_grad_group<T>(v[i], gr.a, gr.m, c));
+                    }
+                    for (; k < g; k += 32) __stcs(to + k, post_grad_group<T>(seg[k], gr.a, gr.m, c));
+                    // by the lane that wrote the group, after it
+                    const int ks = ky - at;
+                    if (OP != kOpDistill && ky >= 0 && ks >= 0 && ks < g && (ks & 31) == lane) VT::store1(dz, gr.y, gr.gy);
+                }
+                if (in_ring) {
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&s_empty[db * kWarps + warp]));
+                    next(db, phase_b);
+                }
+            }
+            if (has_tail) {
+                const float e = zero ? 0.f : gr.a * ex2_approx((VT::load1(row_in<T>(p.r, t), tail_v) - gr.m) * c);
+                VT::store1(dz, tail_v, OP != kOpDistill && !zero && tail_v == gr.y ? gr.gy : e);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                if (OP == kOpDistill) ptx::mbar_arrive(ptx::smem_u32(&sh.written[ms]));
+                ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
+            }
+        };
+        if constexpr (!kGrad) {
+            for (int r = 0; r < n_rows; ++r) fold(r);
+        } else if constexpr (!kStats) {
+            for (int r = 0; r < n_rows; ++r) write(r);
+        } else {
+            for (int r = 0; r < n_rows + plan.lag; ++r) {
+                if (r < n_rows) fold(r);
+                if (r >= plan.lag) write(r - plan.lag);
+            }
+        }
     }
     if constexpr (OP == kOpPolicy || OP == kOpDistill) {
         if (rank == 0) {
-            finish_sums(p.r, sum, q, nclusters, s_ring, [&](const PostPartial &a, int *s_i) {
-                if constexpr (OP == kOpPolicy) policy_finish(p, a, s_i);
+            // the finisher's sums go to thread 0; the ring is no longer in use
+            PostPartial *s_sum = reinterpret_cast<PostPartial *>(reinterpret_cast<char *>(s_ring) + 512);
+            __syncthreads();
+            if (tid == kRowThreads - 32) *s_sum = sum;
+            __syncthreads();
+            finish_sums(p.r, *s_sum, q, nclusters, s_ring, [&](const PostPartial &all, int *s_i) {
+                if constexpr (OP == kOpPolicy) policy_finish(p, all, s_i);
             });
         }
     }
@@ -805,11 +905,12 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
             float Mk, Sk;
             distill_entry_stats(s_z, p.K, p.c, Mk, Sk);
             const DistillRow r = distill_finish(p, st, Mk, Sk, s_z, s_lq, rec, (float)w * p.scale * p.inv_tau, V - have);
+            const float kl = distill_kl(p, r, st, Mk, Sk, s_z, s_lq, rec, V - have);
             if (threadIdx.x == 0) {
                 s_row = r;
                 if (!isfinite(r.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
-                if (p.kl) p.kl[t] = r.kl;
-                sum.loss += w * (double)p.scale * (double)r.kl;
+                if (p.kl) p.kl[t] = kl;
+                sum.loss += w * (double)p.scale * (double)kl;
             }
         }
         __syncthreads();
@@ -826,9 +927,9 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
 
 // ---------------------------------------------------------------- launches
 
-// The ring of one CTA: what three (two, one) CTAs on an SM leave each of its 228 KB, less the 1 KB the
-// system takes per CTA and the static state.
-constexpr size_t kRingBytes[3] = {76800, 115712, 231424};
+// Shared memory of a CTA: what three CTAs (two, one) on an SM leave each of its 228 KB, less the 1 KB that
+// the system takes per CTA.
+constexpr size_t kCtaBytes[3] = {76800, 115712, 231424};
 
 // How many clusters of this launch are resident at once; sets the kernel's shared-memory limit on its
 // first use on a device and size. Remembered for the last sizes asked for.
@@ -874,30 +975,37 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, cudaStream_
     auto kernel = ring_rows_kernel<T, OP, kEnt>;
     constexpr bool kStats = OP != kOpScale, kKeep = OP == kOpPolicy || OP == kOpDistill;
     const int nvec = p.r.V / PostVec<T>::kElems;
-    constexpr size_t kMaxDynamic = kRingBytes[2] - sizeof(RowShared<OP>);
-    const size_t fixed = sizeof(RowShared<OP>) + (size_t)kMeta * 12 * K + 16;
+    constexpr size_t kMaxDynamic = kCtaBytes[2] - sizeof(RowShared<OP>);
+    const size_t fixed = sizeof(RowShared<OP>) + (size_t)kMetaOf(OP) * 12 * K;
     RowPlan plan{};
-    size_t smem = 0;
     fits = false;
-    // the fewest CTAs per row whose slice stays in the ring of one of three CTAs on an SM; with eight,
-    // of one of two, or of one
+    // enough CTAs per row that the rows there are fill the SMs; then the fewest whose rings hold a slice
+    // with three CTAs on an SM; with eight, two or one on an SM
     int C = 1;
     for (int want = 456 / std::max(1, p.r.T); C < kMaxCluster && C * 2 <= want && nvec >= C * 2 * 256;) C *= 2;
-    for (int occ = 0; occ < 3 && !fits;) {
+    for (int occ = 0; !fits;) {
+        // groups in a warp's ring; a segment's two barriers take one group's room
+        const int room = (int)((kCtaBytes[occ] - fixed) / (16 * kWarps));
         plan.cluster = C;
         plan.slice = std::max(1, (nvec + C - 1) / C);
-        plan.tile = std::max(1, (plan.slice + 3) / 4);
-        const size_t room = kRingBytes[occ] - fixed;
-        if (!kKeep) plan.tile = std::min<int>(plan.tile, (int)(room / 16 / 4));
-        plan.slots = (int)std::min<size_t>(kMaxSlots, room / ((size_t)plan.tile * 16));
-        fits = kKeep ? (size_t)plan.slots * plan.tile >= (size_t)plan.slice : plan.slots >= 2;
+        const int share = (plan.slice + kWarps - 1) / kWarps;
+        if (kKeep) {
+            plan.parts = 1;
+            plan.seg = share;
+            plan.depth = std::min(kMaxDepth, room / (share + 1));
+            fits = plan.depth >= 1;
+            plan.lag = plan.depth >= 2;
+        } else {  // segments of a quarter of the ring, or less where the share is
+            plan.seg = std::min(share, room / kMaxDepth - 1);
+            plan.parts = (share + plan.seg - 1) / plan.seg;
+            plan.depth = kMaxDepth;
+            fits = true;
+        }
         if (fits) break;
         if (C < kMaxCluster) C *= 2;
-        else ++occ;
+        else if (++occ == 3) return cudaSuccess;
     }
-    if (!fits) return cudaSuccess;
-    smem = (size_t)plan.slots * plan.tile * 16 + (size_t)kMeta * 12 * K;
-    smem = std::max<size_t>(smem, 1024);
+    const size_t smem = std::max<size_t>((size_t)plan.depth * kWarps * (plan.seg + 1) * 16 + (size_t)kMetaOf(OP) * 12 * K, 1024);
 
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
