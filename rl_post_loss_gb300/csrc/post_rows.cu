@@ -427,15 +427,22 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             const char *src = row_in<T>(p.r, t) + (size_t)v0 * 16;
             const int d0 = d;
             const uint32_t phase0 = phase;
-            auto record = [&] {
+            float *mz = s_meta + (size_t)ms * 3 * K;
+            int *s_id = reinterpret_cast<int *>(mz + 2 * K);
+            if constexpr (OP == kOpDistill) {
+                // before the row's copies, which wait for segments: the gather takes two dependent loads
                 if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
                 if (lane == (r & 31)) sh.meta[ms] = mine;
                 __syncwarp();
-                if constexpr (OP == kOpDistill) {
+                if (read) load_entries<T>(p, t, sh.meta[ms], mz, mz + K, s_id);
+            }
+            auto record = [&] {
+                if constexpr (OP != kOpDistill) {
+                    if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
+                    if (lane == (r & 31)) sh.meta[ms] = mine;
+                    __syncwarp();
+                } else {
                     if (read) {
-                        float *mz = s_meta + (size_t)ms * 3 * K;
-                        int *s_id = reinterpret_cast<int *>(mz + 2 * K);
-                        load_entries<T>(p, t, sh.meta[ms], mz, mz + K, s_id);
                         lanes_wait(sh, lane < kWarps, &s_full[d0 * kWarps + lane % kWarps], phase0, p.r.status, [] {});
                         __syncwarp();
                         if (sh.meta[ms].read) mark_entries<T>(plan, s_ring, d0, v0, v1, nvec, last_rank, s_id, K, sh.meta[ms]);
@@ -995,10 +1002,11 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, cudaStream_
             plan.depth = std::min(kMaxDepth, room / (share + 1));
             fits = plan.depth >= 1;
             plan.lag = plan.depth >= 2;
-        } else {  // segments of a quarter of the ring, or less where the share is
-            plan.seg = std::min(share, room / kMaxDepth - 1);
+        } else {  // two segments of whole batches, or more shorter ones
+            const int batch = 32 * kBatch;
+            plan.seg = std::min(share, std::max(batch, (room / 2 - 1) / batch * batch));
             plan.parts = (share + plan.seg - 1) / plan.seg;
-            plan.depth = kMaxDepth;
+            plan.depth = std::min(kMaxDepth, room / (plan.seg + 1));
             fits = true;
         }
         if (fits) break;
