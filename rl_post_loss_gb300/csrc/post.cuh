@@ -490,13 +490,16 @@ __device__ __forceinline__ PolicyTok policy_load(const PolicyParams &p, int t, i
     return k;
 }
 
-// The token objective, its KL term and every per-token output of a policy row; adds the row to
-// `sum` and returns its gradient. `st` are the whole row's statistics, `logp` its ln p_y (0 where
-// the row was not read). `write` false: another block writes the row's outputs and sums.
-__device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, const PolicyTok &k, PostStats st, float logp,
-                                              bool write, PostPartial &sum) {
+// The token objective and its KL term of a policy row, and the row's gradient. `st` are the whole row's
+// statistics, `logp` its ln p_y (0 where the row was not read).
+struct PolicyRow {
+    RowOut o;
+    float kl;
+    RowGrad grad;
+};
+
+__device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const PolicyTok &k, PostStats st, float logp) {
     const bool ok = k.ok, m = k.m;
-    const bool read = m || p.read_masked;
     const float d = __fsub_rn(k.lo, k.li);  // ln rho, one fp32 subtraction
     const bool in_bounds = (-p.c.ln_beta <= d) && (d <= p.c.ln_beta);
     uint32_t pre = (m ? 0u : RL_FLAG_MASKED) | (ok ? 0u : RL_FLAG_BAD_TARGET) | (k.A > 0.f ? kPreAPos : 0u) |
@@ -512,35 +515,43 @@ __device__ __forceinline__ RowGrad policy_row(const PolicyParams &p, int t, cons
     }
     const float4 rec = make_float4(0.f, lref, cf, k.w * cf);
     const uint32_t meta = (ok ? (uint32_t)k.y : 0u) | (pre << 24);
-    RowOut o = finish_row(RowStats2{0.f, st.s, st.u}, rec, meta, p.c, k.teacher, &logp);
-    if (!read) {  // nothing of the row was read: no log-prob, and the clip test has nothing to test
-        o.H = 0.f;
-        o.flags &= ~(RL_FLAG_CLIP_ACTIVE | (p.c.objective == RL_OBJ_DIS ? RL_FLAG_POP_IN_BOUNDS : 0u));
+    PolicyRow r;
+    r.o = finish_row(RowStats2{0.f, st.s, st.u}, rec, meta, p.c, k.teacher, &logp);
+    if (!(m || p.read_masked)) {  // nothing of the row was read: no log-prob, and the clip test has nothing to test
+        r.o.H = 0.f;
+        r.o.flags &= ~(RL_FLAG_CLIP_ACTIVE | (p.c.objective == RL_OBJ_DIS ? RL_FLAG_POP_IN_BOUNDS : 0u));
     }
-    float kl = 0.f, dkl = 0.f;
+    float dkl = 0.f;
+    r.kl = 0.f;
     const bool counts = m && ok;
-    if (counts) post_kl(p.kl.estimator, __fsub_rn(o.logp, k.ref), kl, dkl);
-    const float g = counts ? fmaf(k.w * p.kl.coef, dkl, o.g) : 0.f;
-    if (write) {
-        if (k.seq < 0) post_raise(p.r.status, RL_ERR_SEQLENS);
-        if (!ok) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
-        if (read && !post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
-        if (p.r.logp) p.r.logp[t] = ok ? o.logp : __int_as_float(0x7fc00000);
-        if (p.r.entropy) p.r.entropy[t] = o.H;
-        if (p.flags) p.flags[t] = (uint8_t)o.flags;
-        if (p.kl.kl) p.kl.kl[t] = m && !ok ? __int_as_float(0x7fc00000) : kl;
-        sum.loss += k.w64 * ((double)p.kl.coef * (double)kl - (double)o.obj);
-        if (m) {
-            sum.n += 1;
-            sum.ent += (double)o.H;
-            sum.kl += (double)kl;
-            sum.popped += !(o.flags & RL_FLAG_POP_IN_BOUNDS);
-            sum.clipped += (o.flags & RL_FLAG_CLIP_ACTIVE) != 0;
-        } else {
-            sum.masked += 1;
-        }
+    if (counts) post_kl(p.kl.estimator, __fsub_rn(r.o.logp, k.ref), r.kl, dkl);
+    const float g = counts ? fmaf(k.w * p.kl.coef, dkl, r.o.g) : 0.f;
+    r.grad = g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : post_row_grad(g, st, r.o.logp, k.y);
+    return r;
+}
+
+// Every per-token output of a policy row; adds the row to `sum`.
+__device__ __forceinline__ void policy_write(const PolicyParams &p, int t, const PolicyTok &k, PostStats st, const PolicyRow &r,
+                                             PostPartial &sum) {
+    const bool ok = k.ok, m = k.m;
+    const float nan = __int_as_float(0x7fc00000);
+    if (k.seq < 0) post_raise(p.r.status, RL_ERR_SEQLENS);
+    if (!ok) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
+    if ((m || p.read_masked) && !post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
+    if (p.r.logp) p.r.logp[t] = ok ? r.o.logp : nan;
+    if (p.r.entropy) p.r.entropy[t] = r.o.H;
+    if (p.flags) p.flags[t] = (uint8_t)r.o.flags;
+    if (p.kl.kl) p.kl.kl[t] = m && !ok ? nan : r.kl;
+    sum.loss += k.w64 * ((double)p.kl.coef * (double)r.kl - (double)r.o.obj);
+    if (m) {
+        sum.n += 1;
+        sum.ent += (double)r.o.H;
+        sum.kl += (double)r.kl;
+        sum.popped += !(r.o.flags & RL_FLAG_POP_IN_BOUNDS);
+        sum.clipped += (r.o.flags & RL_FLAG_CLIP_ACTIVE) != 0;
+    } else {
+        sum.masked += 1;
     }
-    return g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : post_row_grad(g, st, o.logp, k.y);
 }
 
 // ---------------------------------------------------------------- the teacher's entries

@@ -488,15 +488,37 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
     } else if (warp > kWarps) {
         // ------------------------------------------------ finisher
         int exchanges = 0;
+        DistillRow last{};      // distill: the row before this one, whose entries are still to be written
+        bool last_live = false;
+        // The entries are written after the rest of the row, whose value they replace, and after the next
+        // row's results are out: nobody waits for them.
+        auto write_entries = [&](int r) {
+            if constexpr (OP == kOpDistill) {
+                const int ms = r % kMeta;
+                const float *s_z = s_meta + (size_t)ms * 3 * K, *s_lq = s_z + K;
+                const int *s_id = reinterpret_cast<const int *>(s_z + 2 * K);
+                row_wait(sh, &sh.written[ms], use(r), p.r.status);
+                if (last_live) {
+                    char *dz = row_out<T>(p.r, row_of(r));
+                    for (int k = lane; k < K; k += 32) {
+                        const int id = s_id[k];
+                        if ((id >= v0 * VEC && id < v1 * VEC) || (last_rank && id >= nvec * VEC))
+                            VT::store1(dz, id, distill_entry(p, last, s_z[k], s_lq[k]));
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
+            }
+        };
         for (int r = 0; kStats && r < n_rows; ++r) {
             const int t = row_of(r), ms = r % kMeta;
+            const bool writes = r % C == rank;  // the CTAs take turns in writing the rows' results
             row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
             row_wait(sh, &sh.part_full[ms], use(r), p.r.status);
             const RowMeta<OP> &meta = sh.meta[ms];
             RowFin &fin = sh.fin[ms];
             const bool read = meta.read;
             const float *s_z = s_meta + (size_t)ms * 3 * K, *s_lq = s_z + K;
-            const int *s_id = reinterpret_cast<const int *>(s_z + 2 * K);
             PostStats st{0.f, 1.f, 0.f};
             int dup = 0;
             if (read) {
@@ -521,7 +543,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 }
             }
             if constexpr (OP == kOpLogp) {
-                if (lane == 0 && rank == 0) {
+                if (lane == 0 && writes) {
                     float logp = 0.f, ent = 0.f;
                     if (read) {
                         logp = __int_as_float(0x7fc00000);
@@ -537,8 +559,10 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             } else if constexpr (OP == kOpPolicy) {
                 if (lane == 0) {
                     const float logp = read && meta.y >= 0 ? post_target<kEnt>(st, meta.zy, st) : 0.f;
-                    fin.grad = policy_row(p, t, meta.tok, st, logp, rank == 0, sum);
+                    const PolicyRow row = policy_row(p, meta.tok, st, logp);
+                    fin.grad = row.grad;
                     ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
+                    if (writes) policy_write(p, t, meta.tok, st, row, sum);
                 }
             } else if constexpr (OP == kOpDistill) {
                 const bool live = read && !dup;
@@ -552,7 +576,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                     fin.grad = RowGrad{live ? row.ct : 0.f, row.m, 0.f, live ? 0 : -1};
                     ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
                 }
-                if (rank == 0) {
+                if (writes) {
                     const float kl = live ? distill_kl(p, row, st, Mk, Sk, s_z, s_lq, meta.rec, V - meta.have) : 0.f;
                     if (lane == 0) {
                         const bool bad = meta.bad || dup;
@@ -562,20 +586,16 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                         sum.loss += meta.w * (double)p.scale * (double)kl;
                     }
                 }
-                // the entries are written after the rest of the row, whose value they replace
-                row_wait(sh, &sh.written[ms], use(r), p.r.status);
-                if (live) {
-                    char *dz = row_out<T>(p.r, t);
-                    for (int k = lane; k < K; k += 32) {
-                        const int id = s_id[k];
-                        if ((id >= v0 * VEC && id < v1 * VEC) || (last_rank && id >= nvec * VEC))
-                            VT::store1(dz, id, distill_entry(p, row, s_z[k], s_lq[k]));
-                    }
-                }
+                if (r > 0) write_entries(r - 1);
+                last = row;
+                last_live = live;
             }
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
+            if constexpr (OP != kOpDistill) {
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
+            }
         }
+        if (n_rows > 0) write_entries(n_rows - 1);
     } else {
         // ------------------------------------------------ consumers
         const int tail_v = nvec * VEC + tid;     // this thread's entry of the last V mod VEC
@@ -711,16 +731,14 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
         }
     }
     if constexpr (OP == kOpPolicy || OP == kOpDistill) {
-        if (rank == 0) {
-            // the finisher's sums go to thread 0; the ring is no longer in use
-            PostPartial *s_sum = reinterpret_cast<PostPartial *>(reinterpret_cast<char *>(s_ring) + 512);
-            __syncthreads();
-            if (tid == kRowThreads - 32) *s_sum = sum;
-            __syncthreads();
-            finish_sums(p.r, *s_sum, q, nclusters, s_ring, [&](const PostPartial &all, int *s_i) {
-                if constexpr (OP == kOpPolicy) policy_finish(p, all, s_i);
-            });
-        }
+        // the finisher's sums go to thread 0; the ring is no longer in use
+        PostPartial *s_sum = reinterpret_cast<PostPartial *>(reinterpret_cast<char *>(s_ring) + 512);
+        __syncthreads();
+        if (tid == kRowThreads - 32) *s_sum = sum;
+        __syncthreads();
+        finish_sums(p.r, *s_sum, (int)blockIdx.x, (int)gridDim.x, s_ring, [&](const PostPartial &all, int *s_i) {
+            if constexpr (OP == kOpPolicy) policy_finish(p, all, s_i);
+        });
     }
     if (kStats && C > 1) ptx::cluster_sync();  // no CTA leaves while another may still write to it
 }
@@ -811,7 +829,10 @@ __global__ void __launch_bounds__(kThreads) long_policy_kernel(PolicyParams p) {
         if (read) st = block_merge<kEnt>(row_stats<T, kEnt>(z, p.r.V, kLog2e, ok ? y : -1), s_warp, kLog2e);
         if (threadIdx.x == 0) {
             const float logp = ok && read ? post_target<kEnt>(st, PostVec<T>::load1(z, y), st) : 0.f;
-            s_grad = policy_row(p, t, policy_load(p, t, find_seq(p.r.cu_seqlens, p.r.S, t)), st, logp, true, sum);
+            const PolicyTok tok = policy_load(p, t, find_seq(p.r.cu_seqlens, p.r.S, t));
+            const PolicyRow row = policy_row(p, tok, st, logp);
+            policy_write(p, t, tok, st, row, sum);
+            s_grad = row.grad;
         }
         __syncthreads();
         const RowGrad gr = s_grad;
@@ -971,7 +992,7 @@ cudaError_t resident_clusters(const void *kernel, const cudaLaunchConfig_t &cfg,
         resident = sms * per / C;
     }
     if (e != cudaSuccess) return e;
-    *out = std::max(1, std::min(resident, kPostMaxBlocks));
+    *out = std::max(1, std::min(resident, kPostMaxBlocks / C));
     known[next] = Entry{kernel, dev, C, cfg.dynamicSmemBytes, *out};
     next = (next + 1) % kEntries;
     return cudaSuccess;
