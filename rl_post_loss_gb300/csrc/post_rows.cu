@@ -4,7 +4,7 @@
 // each CTA
 //  - a producer warp copies every consumer warp's segments of the next rows into a ring of that warp's
 //    own (bulk copies completing on mbarriers) and gathers what a row needs besides its logits: the
-//    token's record, for 32 rows at a time, or the teacher's entries, whose places it marks;
+//    token's record, for 32 rows at a time, or the teacher's entries;
 //  - each consumer warp folds its segment into softmax statistics (A) and later walks it, still in shared
 //    memory, for the gradient (B): each logit is read from memory once. Warps wait for their own copies
 //    alone, never for one another;
@@ -139,8 +139,6 @@ template <>
 struct RowMeta<kOpDistill> {
     int32_t read, copied;  // its logits are needed; they were copied (its entries then turned out bad)
     int32_t bad, have;     // an id outside the vocabulary; entries that are not padding
-    int32_t dup;           // an entry of this slice is listed twice
-    uint32_t tail_mark;    // the teacher's among the last V mod VEC entries
     float4 rec;
     double w;              // the row's weight
 };
@@ -300,52 +298,52 @@ __device__ __forceinline__ void load_entries(const DistillParams &p, int t, RowM
     __syncwarp();
 }
 
-// Takes the teacher's entries out of the row's slice in the rings, by the producer warp: each becomes
-// -inf, so that the fold leaves it out. It first gets its index as a tag: an entry listed twice finds
-// another's tag, or -inf, in its place. The row's segments are at place d of their rings, one per warp.
+// Takes the teacher's entries out of a warp's segment (groups v0 .. v0 + g of the row), by that warp: each
+// becomes -inf, so that the fold leaves it out. It first gets its index as a tag: an entry listed twice
+// finds another's tag, or -inf, in its place. `tail` receives the entries among the row's last V mod VEC
+// where `tail0` >= 0 is the first of them. Returns whether an entry is listed twice.
 template <typename T>
-__device__ __forceinline__ void mark_entries(const RowPlan &plan, uint4 *ring, int d, int v0, int v1, int nvec, bool last_rank,
-                                             const int *s_id, int K, RowMeta<kOpDistill> &m) {
+__device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail0, const int *s_id, int K, uint32_t &tail) {
     using VT = PostVec<T>;
     using Tag = typename VT::Tag;
     constexpr int VEC = VT::kElems;
     const int lane = threadIdx.x & 31;
-    auto place = [&](int id) -> volatile Tag * {
-        return reinterpret_cast<volatile Tag *>(ring + (size_t)d * kWarps * plan.seg + (id / VEC - v0)) + id % VEC;
-    };
-    int dup = 0;
-    uint32_t tail = 0;
+    volatile Tag *at = reinterpret_cast<volatile Tag *>(seg);
+    const int lo = v0 * VEC, hi = (v0 + g) * VEC;
+    bool dup = false, any = false;
+    uint32_t mine = 0;
     for (int k = lane; k < K; k += 32) {
         const int id = s_id[k];
-        if (id >= v0 * VEC && id < v1 * VEC) {
-            *place(id) = (Tag)k;
-        } else if (last_rank && id >= nvec * VEC) {
-            const uint32_t bit = 1u << (id - nvec * VEC);
-            dup |= (tail & bit) != 0;
-            tail |= bit;
+        if (id >= lo && id < hi) {
+            at[id - lo] = (Tag)k;
+            any = true;
+        } else if (tail0 >= 0 && id >= tail0) {
+            const uint32_t bit = 1u << (id - tail0);
+            dup |= (mine & bit) != 0;
+            mine |= bit;
         }
     }
-    // the last V mod VEC entries: a bit that two lanes hold was listed twice
+    tail = 0;
+    if (tail0 >= 0) {  // a bit that two lanes hold was listed twice
 #pragma unroll
-    for (int b = 0; b < VEC - 1; ++b) {
-        const uint32_t who = __ballot_sync(0xffffffffu, (tail >> b) & 1);
-        dup |= __popc(who) > 1;
+        for (int b = 0; b < VEC - 1; ++b) {
+            const uint32_t who = __ballot_sync(0xffffffffu, (mine >> b) & 1);
+            dup |= __popc(who) > 1;
+            tail |= who ? 1u << b : 0u;
+        }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) tail |= __shfl_xor_sync(0xffffffffu, tail, off);
-    __syncwarp();
-    for (int k = lane; k < K; k += 32) {
-        const int id = s_id[k];
-        if (id < v0 * VEC || id >= v1 * VEC) continue;
-        if (*place(id) == (Tag)k) *place(id) = VT::kNegInf;
-        else dup = 1;
+    if (__any_sync(0xffffffffu, any)) {
+        __syncwarp();
+        for (int k = lane; k < K; k += 32) {
+            const int id = s_id[k];
+            if (id < lo || id >= hi) continue;
+            if (at[id - lo] == (Tag)k) at[id - lo] = VT::kNegInf;
+            else dup = true;
+        }
+        ptx::fence_proxy_async_smem();  // the next copy into the segment comes after the marks
+        __syncwarp();
     }
-    ptx::fence_proxy_async_smem();  // the next copies into these segments come after the marks
-    dup = __any_sync(0xffffffffu, dup);
-    if (lane == 0) {
-        m.dup = dup;
-        m.tail_mark = tail;
-    }
+    return __any_sync(0xffffffffu, dup);
 }
 
 template <typename T, int OP, bool kEnt>
@@ -425,8 +423,6 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             if ((r & 31) == 0 && r + lane < n_rows) mine = load_meta<T, OP>(p, row_of(r + lane), N);
             const int read = __shfl_sync(0xffffffffu, mine.read, r & 31);
             const char *src = row_in<T>(p.r, t) + (size_t)v0 * 16;
-            const int d0 = d;
-            const uint32_t phase0 = phase;
             float *mz = s_meta + (size_t)ms * 3 * K;
             int *s_id = reinterpret_cast<int *>(mz + 2 * K);
             if constexpr (OP == kOpDistill) {
@@ -441,13 +437,6 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                     if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
                     if (lane == (r & 31)) sh.meta[ms] = mine;
                     __syncwarp();
-                } else {
-                    if (read) {
-                        lanes_wait(sh, lane < kWarps, &s_full[d0 * kWarps + lane % kWarps], phase0, p.r.status, [] {});
-                        __syncwarp();
-                        if (sh.meta[ms].read) mark_entries<T>(plan, s_ring, d0, v0, v1, nvec, last_rank, s_id, K, sh.meta[ms]);
-                        __syncwarp();
-                    }
                 }
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mfull[ms]));
             };
@@ -522,8 +511,8 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             PostStats st{0.f, 1.f, 0.f};
             int dup = 0;
             if (read) {
-                if constexpr (OP == kOpDistill) dup = meta.dup;
                 RowMsg w = sh.part[ms][lane < kWarps ? lane : 0];
+                dup = __any_sync(0xffffffffu, lane < kWarps && w.bad);
                 st = lane < kWarps ? PostStats{w.m, w.s, w.u} : kPostStart;
                 st = post_warp_merge<kEnt>(st, c);
                 if (C > 1) {
@@ -617,8 +606,8 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             if (meta.read) {
                 int y = -1;
                 uint32_t marks = 0;
+                bool dup = false;
                 if constexpr (OP == kOpLogp || OP == kOpPolicy) y = meta.y;
-                if constexpr (OP == kOpDistill) marks = meta.tail_mark;
                 const int ky = y >= 0 && y < nvec * VEC ? y / VEC - v0 : -1;  // the sampled entry's group
                 PostAcc acc = post_acc();
                 for (int j = 0; j < plan.parts; ++j) {
@@ -633,6 +622,9 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                             ptx::fence_proxy_async_smem();  // the next copy into the segment comes after this
                         }
                     }
+                    if constexpr (OP == kOpDistill)
+                        dup = mark_entries<T>(seg, v0 + warp * plan.seg, g, last_rank && warp == 0 ? nvec * VEC : -1,
+                                              reinterpret_cast<const int *>(s_meta + (size_t)ms * 3 * K + 2 * K), K, marks);
                     int k = lane;
                     for (; k - lane + 32 * kBatch <= g; k += 32 * kBatch) {
                         uint4 v[kBatch];
@@ -658,7 +650,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                     post_fold<kEnt>(st, x, c);
                 }
                 st = post_warp_merge<kEnt>(st, c);
-                if (lane == 0) sh.part[ms][warp] = RowMsg{st.m, st.s, st.u, 0};
+                if (lane == 0) sh.part[ms][warp] = RowMsg{st.m, st.s, st.u, dup};
             } else if (copied(meta)) {
                 for (int j = 0; j < plan.parts; ++j) next(da, phase_a);
             }
