@@ -427,9 +427,25 @@ __device__ __forceinline__ float post_target(PostStats rest, float zy, PostStats
 
 __device__ __forceinline__ float post_entropy(PostStats st) { return logf(st.s) - st.u / st.s * kLn2; }
 
+// e^{-d} - 1 + d >= 0. Its terms cancel near 0, where its series is summed instead (|d| < 1/4:
+// 1/2 - d/6 + ... times d^2, the first term left out is d^8 / 10! < 5e-12).
+__device__ __forceinline__ float post_k3(float d) {
+    if (fabsf(d) < 0.25f) {
+        float q = 1.f / 362880.f;
+        q = fmaf(-d, q, 1.f / 40320.f);
+        q = fmaf(-d, q, 1.f / 5040.f);
+        q = fmaf(-d, q, 1.f / 720.f);
+        q = fmaf(-d, q, 1.f / 120.f);
+        q = fmaf(-d, q, 1.f / 24.f);
+        q = fmaf(-d, q, 1.f / 6.f);
+        q = fmaf(-d, q, 0.5f);
+        return d * d * q;
+    }
+    return expm1f(-d) + d;
+}
+
 // Estimators of KL(pi || pi_ref) from the sampled token, d = logp - logp_ref, and their derivative
-// in logp: d; d^2 / 2; e^{-d} - 1 + d, whose first two terms cancel near 0, where its series is
-// summed instead (|d| < 1/4: kl / d^2 = 1/2 - d/6 + ..., the first term left out is d^8 / 10! < 5e-12).
+// in logp: d; d^2 / 2; e^{-d} - 1 + d.
 __device__ __forceinline__ void post_kl(int estimator, float d, float &kl, float &grad) {
     if (estimator == RL_KL_K1) {
         kl = d;
@@ -438,21 +454,8 @@ __device__ __forceinline__ void post_kl(int estimator, float d, float &kl, float
         kl = 0.5f * d * d;
         grad = d;
     } else {
-        const float em1 = expm1f(-d);
-        grad = -em1;
-        if (fabsf(d) < 0.25f) {
-            float q = 1.f / 362880.f;
-            q = fmaf(-d, q, 1.f / 40320.f);
-            q = fmaf(-d, q, 1.f / 5040.f);
-            q = fmaf(-d, q, 1.f / 720.f);
-            q = fmaf(-d, q, 1.f / 120.f);
-            q = fmaf(-d, q, 1.f / 24.f);
-            q = fmaf(-d, q, 1.f / 6.f);
-            q = fmaf(-d, q, 0.5f);
-            kl = d * d * q;
-        } else {
-            kl = em1 + d;
-        }
+        kl = post_k3(d);
+        grad = -expm1f(-d);
     }
 }
 
@@ -561,8 +564,10 @@ __device__ __forceinline__ void policy_write(const PolicyParams &p, int t, const
 struct DistillRow {
     float ct, m;           // tail: coefficient and reference
     float M, ls, inv_s;    // the whole row: reference, ln S and 1 / S
+    float po, lpo;         // the student's mass outside the teacher's entries, and its logarithm
     float kl, w;           // the row's divergence (reverse); its weight * scale / tau
     float Q;               // total mass of the teacher's distribution
+    bool rest;             // there are entries outside
 };
 
 // Statistics of the student over the teacher's entries, by one warp. s_z[k] holds the student's
@@ -581,12 +586,43 @@ __device__ __forceinline__ void distill_entry_stats(const float *s_z, int K, flo
     S = s;
 }
 
-// The row's coefficients, by one warp. `tail` are the statistics of the vocabulary
-// outside the teacher's entries, s_lq[k] the teacher's log-prob of entry k, rec of distill_prep,
-// w the row's weight * scale / tau, n_rest the number of vocabulary entries outside the teacher's.
+// The row's divergence, by one warp. Its terms h ln(h / o) (h the distribution the mean is over, o the
+// other one) nearly cancel for a student near its teacher. With the masses added and taken away,
+//   sum h ln(h / o) = sum [h ln(h / o) - h + o] + sum h - sum o = sum h k3(ln(h / o)) + sum h - sum o,
+// k3(d) = e^{-d} - 1 + d: no term is negative, and an error e of a logarithm enters as h (1 - o / h) e
+// and not as h e; a common one cancels. The difference of the masses is Q - 1, known in 64 bits; where
+// h = 0 the term is o.
+__device__ __forceinline__ float distill_kl(const DistillParams &p, const DistillRow &r, const float *s_z, const float *s_lq,
+                                            float4 rec) {
+    const int lane = threadIdx.x & 31;
+    float sum = 0.f;
+    for (int k = lane; k < p.K; k += 32) {
+        const float lp = (s_z[k] - r.M) * p.inv_tau - r.ls, lq = s_lq[k];
+        const float pk = ex2_approx((s_z[k] - r.M) * p.c) * r.inv_s, q = expf(lq);
+        const float h = p.reverse ? pk : q;
+        sum += h != 0.f ? h * post_k3(p.reverse ? lp - lq : lq - lp) : (p.reverse ? q : pk);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
+    float gap = rec.w;  // sum q - sum p
+    if (p.tail && r.rest) {
+        const float lqo = logf(rec.z), h = p.reverse ? r.po : rec.z;
+        sum += h != 0.f ? h * post_k3(p.reverse ? r.lpo - lqo : lqo - r.lpo) : (p.reverse ? rec.z : r.po);
+    } else if (p.tail) {
+        gap -= rec.z;  // the entries are the whole vocabulary: there is no further outcome
+    } else {
+        sum += r.po;   // outside, q = 0
+    }
+    return p.reverse ? sum - gap : sum + gap;
+}
+
+// The row's coefficients, by one warp. `tail` are the statistics of the vocabulary outside the
+// teacher's entries, Mk and Sk those of the entries (distill_entry_stats), s_lq[k] the teacher's
+// log-prob of entry k, rec of distill_prep, w the row's weight * scale / tau, n_rest the number of
+// vocabulary entries outside the teacher's.
 //
-// With q_o = rec.z the teacher's remaining mass and p_o the student's (forward, the remaining mass
-// being one more outcome):
+// With q_o = rec.z the teacher's remaining mass, p_o the student's and Q = sum q + q_o (forward, the
+// remaining mass being one more outcome):
 //   KL = sum_k q_k ln(q_k / p_k) + q_o ln(q_o / p_o),  dKL/dz'_v = Q p_v - q_v  (an entry),
 //                                                                  Q p_v - q_o p_v / p_o  (outside)
 // renormalised: q_o = 0, Q = 1. Reverse:
@@ -594,70 +630,31 @@ __device__ __forceinline__ void distill_entry_stats(const float *s_z, int K, flo
 // p_o is the sum of the entries outside, not 1 - sum_k p_k, which would cancel.
 __device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, PostStats tail, float Mk, float Sk,
                                                      const float *s_z, const float *s_lq, float4 rec, float w, int n_rest) {
-    const int lane = threadIdx.x & 31;
     DistillRow r;
     r.w = w;
-    r.Q = rec.w;
+    r.Q = 1.f + rec.w;
     r.m = tail.m;
     r.M = fmaxf(Mk, tail.m);
     const float ft = exp2f((tail.m - r.M) * p.c);
     const float S = __fadd_rn(__fmul_rn(Sk, exp2f((Mk - r.M) * p.c)), __fmul_rn(tail.s, ft));
-    const float inv_s = r.inv_s = 1.f / S;
+    r.inv_s = 1.f / S;
     r.ls = logf(S);
-    const bool rest = p.tail && n_rest > 0;
-    const float lqo = rest ? logf(rec.z) : 0.f;
+    r.rest = n_rest > 0;
+    r.po = tail.s * ft * r.inv_s;
     // a tail far below the row's maximum keeps its logarithm by its own reference
-    const float lpo = (tail.m - r.M) * p.inv_tau + (logf(tail.s) - r.ls);
-    const float po = tail.s * ft * inv_s;
+    r.lpo = (tail.m - r.M) * p.inv_tau + (logf(tail.s) - r.ls);
     r.kl = 0.f;
+    const bool bucket = p.tail && r.rest;
     if (p.reverse) {  // the gradient needs the divergence
-        float kl = 0.f;
-        for (int k = lane; k < p.K; k += 32) {
-            const float pk = ex2_approx((s_z[k] - r.M) * p.c) * inv_s;
-            if (pk != 0.f) kl = fmaf(pk, ((s_z[k] - r.M) * p.inv_tau - r.ls) - s_lq[k], kl);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) kl = __fadd_rn(kl, __shfl_xor_sync(0xffffffffu, kl, off));
-        if (rest && po > 0.f) kl = fmaf(po, lpo - lqo, kl);
-        r.kl = kl;
-        r.ct = rest ? (tail.s > 0.f ? (lpo - lqo - kl) * ft * inv_s : 0.f) : -kl * ft * inv_s;
+        r.kl = distill_kl(p, r, s_z, s_lq, rec);
+        const float a = bucket ? r.lpo - logf(rec.z) : 0.f;
+        r.ct = tail.s > 0.f ? (a - r.kl) * ft * r.inv_s : 0.f;
     } else {
-        r.ct = r.Q * ft * inv_s;
-        if (rest) r.ct = tail.s > 0.f ? r.ct - rec.z / tail.s : 0.f;
+        r.ct = r.Q * ft * r.inv_s;
+        if (bucket) r.ct = tail.s > 0.f ? r.ct - rec.z / tail.s : 0.f;
     }
     r.ct *= w;
     return r;
-}
-
-// The row's divergence for the caller, by one warp, from the same sums. Its terms nearly cancel for
-// a student near its teacher. An error of the sum over the tail or over the entries enters only times
-// p - q, as long as S is their sum and the logarithms are of these same numbers: S, the logarithms,
-// the differences and the sum are taken in 64 bits.
-__device__ __forceinline__ float distill_kl(const DistillParams &p, const DistillRow &r, PostStats tail, float Mk, float Sk,
-                                            const float *s_z, const float *s_lq, float4 rec, int n_rest) {
-    const int lane = threadIdx.x & 31;
-    const float ft = exp2f((tail.m - r.M) * p.c);
-    const double St = (double)tail.s * (double)ft;
-    const double S = (double)Sk * (double)exp2f((Mk - r.M) * p.c) + St;
-    // one logarithm's time for all three
-    const double logs = log(lane == 0 ? S : lane == 1 ? St : (double)rec.z);
-    const double lnS = __shfl_sync(0xffffffffu, logs, 0);
-    double lpo = __shfl_sync(0xffffffffu, logs, 1) - lnS;
-    const double lqo = __shfl_sync(0xffffffffu, logs, 2);
-    if (ft < 1e-30f) lpo = ((double)tail.m - (double)r.M) * (double)p.inv_tau + ((double)logf(tail.s) - lnS);
-    double sum = 0.0;
-    for (int k = lane; k < p.K; k += 32) {
-        const float lq = s_lq[k];
-        const float head = p.reverse ? ex2_approx((s_z[k] - r.M) * p.c) * r.inv_s : expf(lq);
-        const double diff = (double)lq - (((double)s_z[k] - (double)r.M) * (double)p.inv_tau - lnS);
-        if (head != 0.f) sum += (double)head * (p.reverse ? -diff : diff);
-    }
-    sum = warp_sum_f64(sum);
-    if (p.tail && n_rest > 0) {
-        const float ho = p.reverse ? tail.s * ft * r.inv_s : rec.z;
-        if (ho > 0.f) sum += (double)ho * (p.reverse ? lpo - lqo : lqo - lpo);
-    }
-    return (float)sum;
 }
 
 // dL/dz of one of the teacher's entries.

@@ -22,7 +22,7 @@ __device__ __forceinline__ int2 seq_range(const int32_t *cu, int S, int T, int i
 }
 
 // Blocks [0, S) count the mask=1 tokens of one response each; the others take eight rows each, a
-// warp per row: ln of the teacher's normaliser, its remaining mass and its total mass. A teacher
+// warp per row: ln of the teacher's normaliser, its remaining mass and its total mass less 1. A teacher
 // given by log-probs keeps them (m = ln sum = 0) and its remaining mass is 1 - sum q in fp64: with
 // most of the mass in the entries, fp32 would leave it no digits.
 __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepParams p) {
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepP
     if (t >= p.T || !__ldg(p.mask + t)) return;
     const int32_t *ids = p.ids + t * p.ldk;
     const float *vals = p.vals + t * p.ldk;
-    float4 rec = make_float4(0.f, 0.f, 0.f, 1.f);
+    float4 rec = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.tail) {
         double q = 0.0;
         for (int k = lane; k < p.K; k += 32)
@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepP
         q = warp_sum_f64(q);
         const double rest = fmax(1.0 - q, (double)p.floor);
         rec.z = (float)rest;
-        rec.w = (float)(q + rest);
+        rec.w = (float)(q + rest - 1.0);
     } else {
         float m = -INFINITY;
         bool nan = false;
@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepP
         s = warp_sum_f64(s);
         rec.x = m;
         rec.y = (float)log(s);
-        rec.w = nan ? __int_as_float(0x7fc00000) : m > -INFINITY ? 1.f : 0.f;  // no entry with mass: 0
+        rec.w = nan ? __int_as_float(0x7fc00000) : m > -INFINITY ? 0.f : -1.f;  // no entry with mass: Q = 0
     }
     if (lane == 0) p.rec[t] = rec;
 }

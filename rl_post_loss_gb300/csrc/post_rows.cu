@@ -261,7 +261,7 @@ __device__ __forceinline__ RowMeta<OP> load_meta(const typename OpParams<OP>::ty
             m.rec = p.rec[t];
             m.w = p.per_token ? 1.0 / (double)N : 1.0 / ((double)p.r.S * (double)p.seq_n[i]);
             // a teacher that gives the row no mass: it contributes nothing
-            if (!(m.rec.w > 0.f || isnan(m.rec.w))) m.read = 0;
+            if (m.rec.w == -1.f) m.read = 0;
         }
         m.copied = m.read;
     }
@@ -503,11 +503,14 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             const int t = row_of(r), ms = r % kMeta;
             const bool writes = r % C == rank;  // the CTAs take turns in writing the rows' results
             row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
-            row_wait(sh, &sh.part_full[ms], use(r), p.r.status);
             const RowMeta<OP> &meta = sh.meta[ms];
             RowFin &fin = sh.fin[ms];
             const bool read = meta.read;
             const float *s_z = s_meta + (size_t)ms * 3 * K, *s_lq = s_z + K;
+            float Mk = 0.f, Sk = 0.f;
+            if constexpr (OP == kOpDistill)
+                if (read) distill_entry_stats(s_z, K, c, Mk, Sk);
+            row_wait(sh, &sh.part_full[ms], use(r), p.r.status);
             PostStats st{0.f, 1.f, 0.f};
             int dup = 0;
             if (read) {
@@ -555,18 +558,14 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 }
             } else if constexpr (OP == kOpDistill) {
                 const bool live = read && !dup;
-                float Mk = 0.f, Sk = 0.f;
                 DistillRow row{};
-                if (live) {
-                    distill_entry_stats(s_z, K, c, Mk, Sk);
-                    row = distill_finish(p, st, Mk, Sk, s_z, s_lq, meta.rec, (float)meta.w * p.scale * p.inv_tau, V - meta.have);
-                }
+                if (live) row = distill_finish(p, st, Mk, Sk, s_z, s_lq, meta.rec, (float)meta.w * p.scale * p.inv_tau, V - meta.have);
                 if (lane == 0) {
                     fin.grad = RowGrad{live ? row.ct : 0.f, row.m, 0.f, live ? 0 : -1};
                     ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
                 }
                 if (writes) {
-                    const float kl = live ? distill_kl(p, row, st, Mk, Sk, s_z, s_lq, meta.rec, V - meta.have) : 0.f;
+                    const float kl = !live ? 0.f : p.reverse ? row.kl : distill_kl(p, row, s_z, s_lq, meta.rec);
                     if (lane == 0) {
                         const bool bad = meta.bad || dup;
                         if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
@@ -911,7 +910,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
         st = block_merge<false>(st, s_warp, p.c);
         const int n_i = p.seq_n[i];
         const double w = p.per_token ? 1.0 / (double)N : 1.0 / ((double)p.r.S * (double)n_i);
-        const bool none = have == 0 || !(rec.w > 0.f || isnan(rec.w));  // the teacher gives the row no mass
+        const bool none = have == 0 || rec.w == -1.f;  // the teacher gives the row no mass
         if (bad || none) {  // excluded: contributes nothing
             if (threadIdx.x == 0) {
                 if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
@@ -925,7 +924,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
             float Mk, Sk;
             distill_entry_stats(s_z, p.K, p.c, Mk, Sk);
             const DistillRow r = distill_finish(p, st, Mk, Sk, s_z, s_lq, rec, (float)w * p.scale * p.inv_tau, V - have);
-            const float kl = distill_kl(p, r, st, Mk, Sk, s_z, s_lq, rec, V - have);
+            const float kl = p.reverse ? r.kl : distill_kl(p, r, s_z, s_lq, rec);
             if (threadIdx.x == 0) {
                 s_row = r;
                 if (!isfinite(r.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
