@@ -21,10 +21,43 @@ __device__ __forceinline__ int2 seq_range(const int32_t *cu, int S, int T, int i
     return make_int2(b, e);
 }
 
+// A sum held as two fp32 values, |lo| a rounding of hi at most: about 48 bits at fp32's speed (the
+// device's fp64 units are some sixty times slower; a row of 128 entries took them 0.1 us of the whole GPU).
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float h, float l) {
+        const float s = __fadd_rn(hi, h), b = __fsub_rn(s, hi);
+        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(h, b));  // Knuth's exact error of hi + h
+        l = __fadd_rn(__fadd_rn(lo, l), err);
+        hi = __fadd_rn(s, l);
+        lo = __fsub_rn(l, __fsub_rn(hi, s));
+    }
+};
+
+// Adds e^v, v <= 88, to a sum, within about 1e-9 relative: v = n ln 2 + r in Cody and Waite's two parts of
+// ln 2 (the first has 10 bits, so that n times it is exact), then e^r = 1 + r + the rest of Taylor's series,
+// of which only the rest, below 0.07, is rounded to fp32.
+__device__ __forceinline__ void add_exp(Sum2 &sum, float v) {
+    if (v < -87.f) return;  // below 2e-38
+    const float n = rintf(v * kLog2e);
+    const float a = fmaf(-n, 0.693359375f, v), b = n * 2.12194440e-4f;
+    const float r = __fadd_rn(a, b), rl = __fsub_rn(b, __fsub_rn(r, a));
+    float q = 1.f / 40320.f;
+    q = fmaf(r, q, 1.f / 5040.f);
+    q = fmaf(r, q, 1.f / 720.f);
+    q = fmaf(r, q, 1.f / 120.f);
+    q = fmaf(r, q, 1.f / 24.f);
+    q = fmaf(r, q, 1.f / 6.f);
+    q = fmaf(r, q, 0.5f);
+    const float one = __fadd_rn(1.f, r), ol = __fsub_rn(r, __fsub_rn(one, 1.f));
+    const float scale = ex2_approx(n);  // a power of two: exact
+    sum.add(one * scale, (fmaf(r * r, q, rl) + ol) * scale);
+}
+
 // Blocks [0, S) count the mask=1 tokens of one response each; the others take eight rows each, a
 // warp per row: ln of the teacher's normaliser, its remaining mass and its total mass less 1. A teacher
-// given by log-probs keeps them (m = ln sum = 0) and its remaining mass is 1 - sum q in fp64: with
-// most of the mass in the entries, fp32 would leave it no digits.
+// given by log-probs keeps them (m = ln sum = 0) and its remaining mass is 1 - sum q, the sum held in two
+// parts: with most of the mass in the entries, fp32 would leave it no digits.
 __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepParams p) {
     __shared__ int s_i[32];
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.blocks_done = 0;
@@ -48,13 +81,24 @@ __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepP
     const float *vals = p.vals + t * p.ldk;
     float4 rec = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.tail) {
-        double q = 0.0;
-        for (int k = lane; k < p.K; k += 32)
-            if (__ldg(ids + k) >= 0) q += exp((double)__ldg(vals + k));
-        q = warp_sum_f64(q);
-        const double rest = fmax(1.0 - q, (double)p.floor);
-        rec.z = (float)rest;
-        rec.w = (float)(q + rest - 1.0);
+        Sum2 q{0.f, 0.f};
+        bool nan = false;
+#pragma unroll 4
+        for (int k = lane; k < p.K; k += 32) {
+            const float v = __ldg(vals + k);
+            if (__ldg(ids + k) < 0) continue;
+            nan |= isnan(v);
+            add_exp(q, v);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const float h = __shfl_xor_sync(0xffffffffu, q.hi, off), l = __shfl_xor_sync(0xffffffffu, q.lo, off);
+            q.add(h, l);
+        }
+        const float rest = fmaxf((1.f - q.hi) - q.lo, p.floor);
+        nan = __any_sync(0xffffffffu, nan);
+        rec.z = nan ? __int_as_float(0x7fc00000) : rest;
+        rec.w = ((q.hi - 1.f) + q.lo) + rest;
     } else {
         float m = -INFINITY;
         bool nan = false;
@@ -67,13 +111,14 @@ __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepP
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
         nan = __any_sync(0xffffffffu, nan);
-        double s = 0.0;
+        float s = 0.f;
         if (m > -INFINITY)
             for (int k = lane; k < p.K; k += 32)
-                if (__ldg(ids + k) >= 0) s += (double)expf(__ldg(vals + k) - m);
-        s = warp_sum_f64(s);
+                if (__ldg(ids + k) >= 0) s += expf(__ldg(vals + k) - m);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
         rec.x = m;
-        rec.y = (float)log(s);
+        rec.y = logf(s);
         rec.w = nan ? __int_as_float(0x7fc00000) : m > -INFINITY ? 0.f : -1.f;  // no entry with mass: Q = 0
     }
     if (lane == 0) p.rec[t] = rec;

@@ -1000,8 +1000,7 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, cudaStream_
     fits = false;
     // enough CTAs per row that the rows there are fill the SMs; then the fewest whose rings hold a slice
     // with three CTAs on an SM; with eight, two or one on an SM
-    int C = 1;
-    for (int want = 456 / std::max(1, p.r.T); C < kMaxCluster && C * 2 <= want && nvec >= C * 2 * 256;) C *= 2;
+    int C = std::max(1, std::min({(int)kMaxCluster, 456 / std::max(1, p.r.T), nvec / 256}));
     for (int occ = 0; !fits;) {
         // groups in a warp's ring; a segment's two barriers take one group's room
         const int room = (int)((kCtaBytes[occ] - fixed) / (16 * kWarps));
@@ -1022,7 +1021,7 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, cudaStream_
             fits = true;
         }
         if (fits) break;
-        if (C < kMaxCluster) C *= 2;
+        if (C < kMaxCluster) ++C;
         else if (++occ == 3) return cudaSuccess;
     }
     const size_t smem = std::max<size_t>((size_t)plan.depth * kWarps * (plan.seg + 1) * 16 + (size_t)kMetaOf(OP) * 12 * K, 1024);
