@@ -356,10 +356,10 @@ def _post_workspace(need: int, device, stream: int):
     """A workspace of this device and stream, grown when a call needs more and kept between calls. During a
     graph capture the caller passes its own: one allocated here would belong to the graph's memory pool."""
     import torch
-    ws = _POST_WORKSPACE.get((device, stream))
     if torch.cuda.is_current_stream_capturing():
         raise ValueError("pass workspace= while a CUDA graph is captured (any torch.uint8 tensor of the size "
                          "rl_loss_*_workspace_bytes gives, kept as long as the graph)")
+    ws = _POST_WORKSPACE.get((device, stream))
     if ws is None or ws.numel() < need:
         ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
         _POST_WORKSPACE[(device, stream)] = ws
@@ -394,6 +394,16 @@ def _vector(name: str, t, n: int, dtype, device, optional: bool = False):
     return t.data_ptr()
 
 
+def _current_stream(device) -> int:
+    """The current stream of a CUDA device as an address, without the Stream object around it."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def token_logp(logits, targets, mask=None, *, vocab: int | None = None, logp=None, entropy=None,
                want_entropy: bool = False, device_status=None, stream=None):
     """Log-probs (and entropies) of the target tokens on the GPU, without a gradient: the pass of a reference
@@ -406,12 +416,12 @@ def token_logp(logits, targets, mask=None, *, vocab: int | None = None, logp=Non
     if entropy is None and want_entropy:
         entropy = torch.empty(T, dtype=torch.float32, device=dev)
     if stream is None:
-        stream = torch.cuda.current_stream(logits.device).cuda_stream
+        stream = _current_stream(dev)
     f32 = torch.float32
     _check(load().rl_loss_token_logp(code, T, V, logits.data_ptr(), logits.stride(0) if T else V,
                                      _vector("targets", targets, T, torch.int32, dev),
                                      _vector("mask", mask, T, torch.uint8, dev, True), _vector("logp", logp, T, f32, dev),
-                                     _vector("entropy", entropy, T, f32, dev, True), _ptr(device_status), stream),
+                                     _vector("entropy", entropy, T, f32, dev, True), _addr(device_status), stream),
            "rl_loss_token_logp")
     return logp, entropy
 
@@ -442,7 +452,7 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
     if kl is None:
         kl = torch.empty(T, dtype=f32, device=dev)
     if stream is None:
-        stream = torch.cuda.current_stream(logits.device).cuda_stream
+        stream = _current_stream(dev)
     if workspace is None:
         workspace = _post_workspace(rl_loss_distill_workspace_bytes(T, S), dev, stream)
     cfg = rl_loss_distill_config(code, V, teacher_ids.shape[1], DISTILL_MODES[mode], int(direction == "reverse"),
@@ -454,7 +464,7 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
                                   _vector("loss", loss, 1, f32, dev),
                                   _vector("loss_f64", loss_f64, 1, torch.float64, dev, True), dlogits.data_ptr(),
                                   dlogits.stride(0), _vector("kl", kl, T, f32, dev), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _ptr(device_status), stream),
+                                  workspace.numel() * workspace.element_size(), _addr(device_status), stream),
            "rl_loss_distill")
     return {"loss": loss, "kl": kl, "dlogits": dlogits}
 
@@ -483,7 +493,7 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
     if pair_loss is None:
         pair_loss = torch.empty(max(S // 2, 0), dtype=f32, device=dev)
     if stream is None:
-        stream = torch.cuda.current_stream(logits.device).cuda_stream
+        stream = _current_stream(dev)
     if workspace is None:
         workspace = _post_workspace(rl_loss_preference_workspace_bytes(T, S), dev, stream)
     cfg = rl_loss_pref_config(code, V, PREF_LOSSES[loss_type], int(length_norm), beta, margin, label_smoothing, nll_coef)
@@ -497,7 +507,7 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
                                      dlogits.stride(0), _vector("logp", logp, T, f32, dev),
                                      _vector("seq_logratio", seq_logratio, S, f32, dev),
                                      _vector("pair_loss", pair_loss, S // 2, f32, dev), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _ptr(device_status), stream),
+                                     workspace.numel() * workspace.element_size(), _addr(device_status), stream),
            "rl_loss_preference")
     return {"loss": loss, "logp": logp, "seq_logratio": seq_logratio, "pair_loss": pair_loss, "dlogits": dlogits}
 
@@ -589,18 +599,20 @@ class RlLoss:
             raise ValueError("kl_estimator is 'k1', 'k2' or 'k3'")
         T = int(targets.shape[0])
         dev, f32 = targets.device, torch.float32
-        inp = rl_loss_inputs(T, int(cu_seqlens.shape[0]) - 1, int(logits.stride(0)) if logits.dim() == 2 else 0,
-                             _ptr(logits), _ptr(targets), _ptr(logp_old), _ptr(logp_infer), _ptr(mask),
-                             _ptr(cu_seqlens), _ptr(rewards_or_adv))
-        out = rl_loss_outputs(_ptr(loss), _ptr(loss_f64), _ptr(dlogits),
-                              int(dlogits.stride(0)) if dlogits.dim() == 2 else 0, _ptr(logp), _ptr(entropy),
-                              _ptr(flags), _ptr(seq_adv), _ptr(counts), _ptr(mean_entropy))
+        inp = rl_loss_inputs(T, cu_seqlens.shape[0] - 1, logits.stride(0) if logits.dim() == 2 else 0,
+                             logits.data_ptr(), targets.data_ptr(), logp_old.data_ptr(), logp_infer.data_ptr(),
+                             mask.data_ptr(), cu_seqlens.data_ptr(), rewards_or_adv.data_ptr())
+        out = rl_loss_outputs(loss.data_ptr(), _addr(loss_f64), dlogits.data_ptr(),
+                              dlogits.stride(0) if dlogits.dim() == 2 else 0, _addr(logp), _addr(entropy),
+                              _addr(flags), _addr(seq_adv), _addr(counts), _addr(mean_entropy))
         term = rl_loss_kl(_vector("logp_ref", logp_ref, T, f32, dev), kl_coef, KL_ESTIMATORS[kl_estimator],
                           _vector("kl", kl, T, f32, dev, True), _vector("mean_kl", mean_kl, 1, f32, dev, True))
         if stream is None:
-            stream = torch.cuda.current_stream().cuda_stream
-        self._raise(load().rl_loss_forward_backward_kl(self.handle, ctypes.byref(inp), ctypes.byref(term),
-                                                       ctypes.byref(out), stream), "rl_loss_forward_backward_kl")
+            stream = _current_stream(dev)
+        code = load().rl_loss_forward_backward_kl(self.handle, ctypes.byref(inp), ctypes.byref(term), ctypes.byref(out),
+                                                  stream)
+        if code:
+            self._raise(code, "rl_loss_forward_backward_kl")
 
     def _raise(self, code: int, what: str):
         if code == CODES["RL_ERR_CUDA"]:
