@@ -356,31 +356,32 @@ def _post_workspace(need: int, device, stream: int):
     """A workspace of this device and stream, grown when a call needs more and kept between calls. During a
     graph capture the caller passes its own: one allocated here would belong to the graph's memory pool."""
     import torch
-    if torch.cuda.is_current_stream_capturing():
+    if torch._C._cuda_isCurrentStreamCapturing():
         raise ValueError("pass workspace= while a CUDA graph is captured (any torch.uint8 tensor of the size "
                          "rl_loss_*_workspace_bytes gives, kept as long as the graph)")
-    ws = _POST_WORKSPACE.get((device, stream))
+    ws = _POST_WORKSPACE.get((device.index, stream))
     if ws is None or ws.numel() < need:
         ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        _POST_WORKSPACE[(device, stream)] = ws
+        _POST_WORKSPACE[(device.index, stream)] = ws
     return ws
 
 
 def _logits_code(logits, vocab, dlogits=None):
-    """(dtype code, V, row stride) of a logits tensor, and the row stride of its gradient."""
+    """(dtype code, V) of a logits tensor, checked together with its gradient's."""
     import torch
-    code = {torch.float32: RL_F32, torch.bfloat16: RL_BF16}.get(logits.dtype)
-    if code is None or logits.dim() != 2 or not logits.is_cuda:
+    dt = logits.dtype
+    if (dt != torch.bfloat16 and dt != torch.float32) or logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits is a CUDA tensor [tokens, vocabulary] of torch.float32 or torch.bfloat16")
+    T, W = logits.shape
     if logits.stride(1) != 1 or (dlogits is not None and (dlogits.dim() != 2 or dlogits.stride(1) != 1)):
         raise ValueError("the rows of logits and dlogits are contiguous")
-    V = logits.shape[1] if vocab is None else int(vocab)
-    if V > logits.shape[1]:
+    V = W if vocab is None else int(vocab)
+    if V > W:
         raise ValueError("vocab is larger than the logits' rows")
-    if dlogits is not None and (dlogits.dtype != logits.dtype or dlogits.shape[0] < logits.shape[0]
-                                or dlogits.shape[1] < V):
-        raise ValueError("dlogits has the type of logits and at least its rows and vocabulary")
-    return code, V
+    if dlogits is not None and (dlogits.dtype != dt or dlogits.shape[0] < T or dlogits.shape[1] < V
+                                or dlogits.device != logits.device):
+        raise ValueError("dlogits has the type of logits and at least its rows and vocabulary, on its device")
+    return (RL_BF16 if dt == torch.bfloat16 else RL_F32), V
 
 
 def _vector(name: str, t, n: int, dtype, device, optional: bool = False):

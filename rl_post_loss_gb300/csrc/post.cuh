@@ -380,7 +380,7 @@ struct PrefPairParams {
     int32_t kind, mean;
     float beta, smoothing, margin, nll;
     float *coef;                 // [S] dL/dlogp of the response's tokens
-    double *pair64;              // [S/2]
+    float *pair32;               // [S/2]
     float *seq_logratio, *pair_loss;  // optional
     uint32_t *pairs_done;
     float *loss;

@@ -56,7 +56,7 @@ struct PrefWork {
     float *logp;
     float2 *stats;
     float *coef;
-    double *pair64;
+    float *pair32;
 };
 size_t pref_layout(int32_t T, int32_t S, void *base, PrefWork &w) {
     Carve c{static_cast<char *>(base)};
@@ -64,7 +64,7 @@ size_t pref_layout(int32_t T, int32_t S, void *base, PrefWork &w) {
     w.logp = c.take<float>((size_t)T);
     w.stats = c.take<float2>((size_t)T);
     w.coef = c.take<float>((size_t)S);
-    w.pair64 = c.take<double>((size_t)S / 2);
+    w.pair32 = c.take<float>((size_t)S / 2);
     return align_up(c.off, 256);
 }
 
@@ -235,7 +235,7 @@ RL_LOSS_API rl_status rl_loss_preference(const rl_loss_pref_config *config, int3
     b.margin = c.margin;
     b.nll = c.nll_coef;
     b.coef = w.coef;
-    b.pair64 = w.pair64;
+    b.pair32 = w.pair32;
     b.seq_logratio = seq_logratio;
     b.pair_loss = pair_loss;
     b.pairs_done = w.done;

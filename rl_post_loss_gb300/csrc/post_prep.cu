@@ -124,64 +124,102 @@ __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepP
     if (lane == 0) p.rec[t] = rec;
 }
 
-// One block per pair (responses 2j and 2j + 1): the log ratios of both in fp64 in token order, the
-// pair's loss and the coefficients dL/dlogp of their tokens. The last block sums the losses in pair
-// order.
+// One block per pair (responses 2j and 2j + 1), half of its warps on each: the log ratios in token order
+// per thread and a fixed tree, held in two fp32 parts (tens of thousands of log-probs near -10 sum to
+// differences near 1), the pair's loss and the coefficients dL/dlogp of its tokens. The last block sums the
+// losses in pair order. The loss itself needs fp32 only: the device's fp64 exponentials and logarithms took
+// 14 us of a launch.
 __global__ void __launch_bounds__(kPrepThreads) pref_pairs_kernel(PrefPairParams p) {
-    __shared__ double s_d[32];
-    __shared__ int s_i[32];
+    constexpr int kHalf = kPrepThreads / 2, kHalfWarps = kHalf / 32;
+    __shared__ Sum2 s_ratio[2][kHalfWarps], s_lp[2][kHalfWarps];
+    __shared__ int s_n[2][kHalfWarps];
+    __shared__ Sum2 s_loss[kPrepThreads / 32];
     __shared__ int s_last;
     const int j = blockIdx.x, P = p.S / 2;
-    double ratio[2], like = 0.0;
-    int n[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int2 r = seq_range(p.cu_seqlens, p.S, p.T, 2 * j + h, p.status);
-        double lp = 0.0, lr = 0.0;
-        int c = 0;
+    const int h = threadIdx.x / kHalf, lane = threadIdx.x & 31, warp = (threadIdx.x % kHalf) / 32;
+    {
+        int b = __ldg(p.cu_seqlens + 2 * j + h), e = __ldg(p.cu_seqlens + 2 * j + h + 1);
+        const int i = 2 * j + h;
+        if ((b < 0) || (e < b) || (e > p.T) || (i == 0 && b != 0) || (i == p.S - 1 && e != p.T)) {
+            if (threadIdx.x % kHalf == 0) post_raise(p.status, RL_ERR_SEQLENS);
+            b = min(max(b, 0), p.T);
+            e = min(max(e, b), p.T);
+        }
+        Sum2 ratio{0.f, 0.f}, lp{0.f, 0.f};
+        int n = 0;
 #pragma unroll 4
-        for (int t = r.x + threadIdx.x; t < r.y; t += kPrepThreads) {
+        for (int t = b + threadIdx.x % kHalf; t < e; t += kHalf) {
+            const float x = p.logp[t], ref = p.logp_ref ? __ldg(p.logp_ref + t) : 0.f;
             if (!__ldg(p.mask + t)) continue;
-            c += 1;
+            n += 1;
             if ((uint32_t)__ldg(p.targets + t) >= (uint32_t)p.V) continue;  // the token is excluded
-            lp += (double)p.logp[t];
-            if (p.logp_ref) lr += (double)__ldg(p.logp_ref + t);
+            ratio.add(x, 0.f);
+            ratio.add(-ref, 0.f);
+            lp.add(x, 0.f);
         }
-        lp = block_sum_f64(lp, s_d);
-        lr = block_sum_f64(lr, s_d);
-        n[h] = block_sum_i32(c, s_i);
-        const double per = p.mean ? (n[h] > 0 ? 1.0 / n[h] : 0.0) : 1.0;
-        ratio[h] = (lp - lr) * per;
-        if (h == 0) like = n[0] > 0 ? -lp / n[0] : 0.0;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const float a = __shfl_xor_sync(0xffffffffu, ratio.hi, off), c = __shfl_xor_sync(0xffffffffu, ratio.lo, off);
+            const float d = __shfl_xor_sync(0xffffffffu, lp.hi, off), f = __shfl_xor_sync(0xffffffffu, lp.lo, off);
+            n += __shfl_xor_sync(0xffffffffu, n, off);
+            ratio.add(a, c);
+            lp.add(d, f);
+        }
+        if (lane == 0) {
+            s_ratio[h][warp] = ratio;
+            s_lp[h][warp] = lp;
+            s_n[h][warp] = n;
+        }
     }
+    __syncthreads();
     if (threadIdx.x == 0) {
-        if (n[0] == 0 || n[1] == 0) post_raise(p.status, RL_ERR_EMPTY_SEQ);
-        const double beta = p.beta, eps = p.smoothing, diff = ratio[0] - ratio[1];
-        double loss, slope;  // of the pair's loss in ratio[0] - ratio[1]
-        if (p.kind == RL_PREF_SIGMOID) {
-            const double h = beta * diff - (double)p.margin;
-            const double soft = log1p(exp(-fabs(h)));  // -ln sigma(|h|)
-            loss = (1.0 - eps) * (soft + fmax(-h, 0.0)) + eps * (soft + fmax(h, 0.0));
-            slope = beta * (eps / (1.0 + exp(-h)) - (1.0 - eps) / (1.0 + exp(h)));
-        } else if (p.kind == RL_PREF_HINGE) {
-            const double h = beta * diff - (double)p.margin;
-            loss = isnan(h) ? h : fmax(1.0 - h, 0.0);
-            slope = h < 1.0 ? -beta : 0.0;
-        } else {
-            const double d = diff - 0.5 / beta;
-            loss = d * d;
-            slope = 2.0 * d;
+        Sum2 r[2], lp{0.f, 0.f};
+        int n[2];
+        float per[2];
+        for (int k = 0; k < 2; ++k) {
+            r[k] = Sum2{0.f, 0.f};
+            n[k] = 0;
+            for (int w = 0; w < kHalfWarps; ++w) {
+                r[k].add(s_ratio[k][w].hi, s_ratio[k][w].lo);
+                if (k == 0) lp.add(s_lp[k][w].hi, s_lp[k][w].lo);
+                n[k] += s_n[k][w];
+            }
+            per[k] = p.mean ? (n[k] > 0 ? 1.f / (float)n[k] : 0.f) : 1.f;
+            if (p.mean && n[k] > 0) {  // the quotient of a two-part number: of its parts, with the first one's remainder
+                const float q = r[k].hi / (float)n[k];
+                r[k] = Sum2{q, (fmaf(-q, (float)n[k], r[k].hi) + r[k].lo) / (float)n[k]};
+            }
         }
-        loss += (double)p.nll * like;
-        double per[2];
-        for (int h = 0; h < 2; ++h) per[h] = p.mean ? (n[h] > 0 ? 1.0 / n[h] : 0.0) : 1.0;
-        p.coef[2 * j] = (float)((slope * per[0] - (n[0] > 0 ? (double)p.nll / n[0] : 0.0)) / P);
-        p.coef[2 * j + 1] = (float)(-slope * per[1] / P);
-        p.pair64[j] = loss;
-        if (p.pair_loss) p.pair_loss[j] = (float)loss;
+        if (n[0] == 0 || n[1] == 0) post_raise(p.status, RL_ERR_EMPTY_SEQ);
+        Sum2 diff = r[0];
+        diff.add(-r[1].hi, -r[1].lo);
+        const float D = diff.hi + diff.lo, beta = p.beta, eps = p.smoothing;
+        float loss, slope;  // of the pair's loss in D
+        if (p.kind == RL_PREF_SIGMOID) {
+            const float x = fmaf(beta, D, -p.margin);
+            const float soft = log1pf(expf(-fabsf(x)));  // -ln sigma(|x|)
+            loss = (1.f - eps) * (soft + fmaxf(-x, 0.f)) + eps * (soft + fmaxf(x, 0.f));
+            slope = beta * (eps / (1.f + expf(-x)) - (1.f - eps) / (1.f + expf(x)));
+        } else if (p.kind == RL_PREF_HINGE) {
+            const float x = fmaf(beta, D, -p.margin);
+            loss = isnan(x) ? x : fmaxf(1.f - x, 0.f);
+            slope = x < 1.f ? -beta : 0.f;
+        } else {
+            const float d = D - 0.5f / beta;
+            loss = d * d;
+            slope = 2.f * d;
+        }
+        if (isnan(D)) loss = slope = D;  // a row that is not finite: max() would hide it
+        const float like = n[0] > 0 ? -(lp.hi + lp.lo) / (float)n[0] : 0.f;
+        loss = fmaf(p.nll, like, loss);
+        const float inv_p = 1.f / (float)P;
+        p.coef[2 * j] = (slope * per[0] - (n[0] > 0 ? p.nll / (float)n[0] : 0.f)) * inv_p;
+        p.coef[2 * j + 1] = -slope * per[1] * inv_p;
+        p.pair32[j] = loss;
+        if (p.pair_loss) p.pair_loss[j] = loss;
         if (p.seq_logratio) {
-            p.seq_logratio[2 * j] = (float)ratio[0];
-            p.seq_logratio[2 * j + 1] = (float)ratio[1];
+            p.seq_logratio[2 * j] = r[0].hi + r[0].lo;
+            p.seq_logratio[2 * j + 1] = r[1].hi + r[1].lo;
         }
         __threadfence();
         s_last = atomicAdd(p.pairs_done, 1u) == (uint32_t)P - 1;
@@ -189,13 +227,22 @@ __global__ void __launch_bounds__(kPrepThreads) pref_pairs_kernel(PrefPairParams
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    double L = 0.0;
-    for (int k = threadIdx.x; k < P; k += kPrepThreads) L += p.pair64[k];
-    L = block_sum_f64(L, s_d) / P;
+    Sum2 L{0.f, 0.f};
+    for (int k = threadIdx.x; k < P; k += kPrepThreads) L.add(p.pair32[k], 0.f);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float a = __shfl_xor_sync(0xffffffffu, L.hi, off), c = __shfl_xor_sync(0xffffffffu, L.lo, off);
+        L.add(a, c);
+    }
+    if (lane == 0) s_loss[threadIdx.x / 32] = L;
+    __syncthreads();
     if (threadIdx.x == 0) {
-        p.loss[0] = (float)L;
-        if (p.loss_f64) p.loss_f64[0] = L;
-        if (!isfinite(L)) post_raise(p.status, RL_ERR_NONFINITE);
+        L = s_loss[0];
+        for (int w = 1; w < kPrepThreads / 32; ++w) L.add(s_loss[w].hi, s_loss[w].lo);
+        const double total = ((double)L.hi + (double)L.lo) / P;
+        p.loss[0] = (float)total;
+        if (p.loss_f64) p.loss_f64[0] = total;
+        if (!isfinite(total)) post_raise(p.status, RL_ERR_NONFINITE);
     }
 }
 
