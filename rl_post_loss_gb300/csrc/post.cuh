@@ -575,10 +575,12 @@ struct DistillRow {
 __device__ __forceinline__ void distill_entry_stats(const float *s_z, int K, float c, float &M, float &S) {
     const int lane = threadIdx.x & 31;
     float m = -FLT_MAX;
+#pragma unroll 4
     for (int k = lane; k < K; k += 32) m = fmaxf(m, s_z[k]);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float s = 0.f;
+#pragma unroll 4
     for (int k = lane; k < K; k += 32) s += ex2_approx((s_z[k] - m) * c);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
@@ -596,11 +598,18 @@ __device__ __forceinline__ float distill_kl(const DistillParams &p, const Distil
                                             float4 rec) {
     const int lane = threadIdx.x & 31;
     float sum = 0.f;
-    for (int k = lane; k < p.K; k += 32) {
-        const float lp = (s_z[k] - r.M) * p.inv_tau - r.ls, lq = s_lq[k];
-        const float pk = ex2_approx((s_z[k] - r.M) * p.c) * r.inv_s, q = expf(lq);
-        const float h = p.reverse ? pk : q;
-        sum += h != 0.f ? h * post_k3(p.reverse ? lp - lq : lq - lp) : (p.reverse ? q : pk);
+    if (p.reverse) {
+#pragma unroll 4
+        for (int k = lane; k < p.K; k += 32) {
+            const float d = s_z[k] - r.M, lq = s_lq[k], pk = ex2_approx(d * p.c) * r.inv_s;
+            sum += pk != 0.f ? pk * post_k3((d * p.inv_tau - r.ls) - lq) : expf(lq);
+        }
+    } else {
+#pragma unroll 4
+        for (int k = lane; k < p.K; k += 32) {
+            const float d = s_z[k] - r.M, lq = s_lq[k], q = expf(lq);
+            sum += q != 0.f ? q * post_k3(lq - (d * p.inv_tau - r.ls)) : ex2_approx(d * p.c) * r.inv_s;
+        }
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
