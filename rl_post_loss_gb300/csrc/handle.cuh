@@ -47,8 +47,8 @@ struct rl_loss_handle_s {
     float4 *tok_rec;
     uint32_t *tok_meta;
     float *loss_scratch;
-    rlk::PostPartial *post_partials;  // [kPostMaxBlocks], of the loss with a KL term
-    uint32_t *post_done;              // blocks that filled their slot (zero between calls)
+    rlk::PostPartial *post_partials;  // of the loss with a KL term (its terms lie in tok_rec)
+    uint32_t *post_counters;
     // bookkeeping
     int64_t launches;
     cudaError_t last_cuda_error;  // the CUDA error behind the last RL_ERR_CUDA of this handle

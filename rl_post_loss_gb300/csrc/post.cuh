@@ -288,11 +288,28 @@ __device__ __forceinline__ void post_raise(uint32_t *status, rl_status code) {
 
 // ---------------------------------------------------------------- parameters
 
-// What one block adds to the batch's sums (blocks take rows in a fixed stride, in increasing order).
+// What a row adds to the batch's sums, written by whichever block took the row, and sums of them: over
+// chunks of kSumRows consecutive rows, each by the block that finishes its last row, then over the chunks
+// by the block that finishes the last one. Rows go to blocks as these come for them; the order of the
+// additions depends on the sizes alone.
+struct alignas(16) PostTerm {
+    double loss;
+    float ent, kl;
+};
+constexpr int kSumRows = 256;
 struct PostPartial {
     double loss, ent, kl;
     int32_t n, popped, clipped, masked;
 };
+
+// Words of PostRows::counters.
+enum PostCount {
+    kCountTickets = 0,   // rows handed out; for the pref gradient one for each part of the rows
+    kCountDone = 8,      // chunks summed
+    kCountChunks = 16    // from here: finished rows of each chunk
+};
+inline size_t post_chunks(int64_t T) { return (size_t)((T + kSumRows - 1) / kSumRows); }
+inline size_t post_counters(int64_t T) { return (size_t)kCountChunks + post_chunks(T); }
 
 struct PostRows {
     const void *logits;
@@ -306,9 +323,11 @@ struct PostRows {
     float *logp;                 // optional for policy and pref
     float *entropy;              // optional
     uint32_t *status;            // optional
-    // sums of the batch: one slot per block, and the count of blocks that have filled theirs
+    // sums of the batch: a term per row, a partial sum per chunk, and counters, all zero at
+    // the launch (PostCount)
+    PostTerm *terms;
     PostPartial *partials;
-    uint32_t *blocks_done;
+    uint32_t *counters;
     float *loss;
     double *loss_f64;
 };
@@ -337,7 +356,7 @@ struct PolicyParams {
     const float *seq_adv, *seq_w;
     const double *seq_w64;
     const int32_t *seq_n;
-    uint8_t *flags;              // optional
+    uint8_t *flags;              // [T]
     int32_t *counts;             // optional
     float *mean_entropy;         // optional
     int32_t read_masked;         // the log-probs or entropies of masked tokens are wanted
@@ -367,7 +386,8 @@ struct DistillPrepParams {
     const int32_t *cu_seqlens;
     float4 *rec;
     int32_t *seq_n;
-    uint32_t *blocks_done;       // set to 0
+    uint32_t *counters;          // PostRows::counters, set to 0
+    int32_t n_counters;
     uint32_t *status;
 };
 
@@ -383,13 +403,14 @@ struct PrefPairParams {
     float *pair32;               // [S/2]
     float *seq_logratio, *pair_loss;  // optional
     uint32_t *pairs_done;
+    uint32_t *tickets;           // [8], set to 0 for the gradient's launch
     float *loss;
     double *loss_f64;
     uint32_t *status;
 };
 
 struct ScaleParams {
-    PostRows r;
+    PostRows r;  // counters: zeroed by the pairs' kernel
     const float2 *stats;         // [T] (m, S)
     const float *coef;           // [S]
 };
@@ -401,7 +422,6 @@ cudaError_t launch_post_distill(const DistillParams &p, int dtype, cudaStream_t 
 cudaError_t launch_pref_pairs(const PrefPairParams &p, cudaStream_t stream);
 cudaError_t launch_post_scale(const ScaleParams &p, int dtype, cudaStream_t stream);
 
-constexpr int kPostMaxBlocks = 4096;  // slots of PostRows::partials
 constexpr int kDistillMaxK = 1024;    // the teacher's entries of a row stay in shared memory
 
 // ---------------------------------------------------------------- the sampled token
@@ -533,9 +553,8 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const Pol
     return r;
 }
 
-// Every per-token output of a policy row; adds the row to `sum`.
-__device__ __forceinline__ void policy_write(const PolicyParams &p, int t, const PolicyTok &k, PostStats st, const PolicyRow &r,
-                                             PostPartial &sum) {
+// Every per-token output of a policy row; returns what it adds to the sums (its counts come from the flags).
+__device__ __forceinline__ PostTerm policy_write(const PolicyParams &p, int t, const PolicyTok &k, PostStats st, const PolicyRow &r) {
     const bool ok = k.ok, m = k.m;
     const float nan = __int_as_float(0x7fc00000);
     if (k.seq < 0) post_raise(p.r.status, RL_ERR_SEQLENS);
@@ -543,18 +562,9 @@ __device__ __forceinline__ void policy_write(const PolicyParams &p, int t, const
     if ((m || p.read_masked) && !post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
     if (p.r.logp) p.r.logp[t] = ok ? r.o.logp : nan;
     if (p.r.entropy) p.r.entropy[t] = r.o.H;
-    if (p.flags) p.flags[t] = (uint8_t)r.o.flags;
+    p.flags[t] = (uint8_t)r.o.flags;
     if (p.kl.kl) p.kl.kl[t] = m && !ok ? nan : r.kl;
-    sum.loss += k.w64 * ((double)p.kl.coef * (double)r.kl - (double)r.o.obj);
-    if (m) {
-        sum.n += 1;
-        sum.ent += (double)r.o.H;
-        sum.kl += (double)r.kl;
-        sum.popped += !(r.o.flags & RL_FLAG_POP_IN_BOUNDS);
-        sum.clipped += (r.o.flags & RL_FLAG_CLIP_ACTIVE) != 0;
-    } else {
-        sum.masked += 1;
-    }
+    return PostTerm{k.w64 * ((double)p.kl.coef * (double)r.kl - (double)r.o.obj), m ? r.o.H : 0.f, m ? r.kl : 0.f};
 }
 
 // ---------------------------------------------------------------- the teacher's entries

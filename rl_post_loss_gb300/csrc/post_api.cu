@@ -38,14 +38,16 @@ struct Carve {
 
 struct DistillWork {
     rlk::PostPartial *partials;
-    uint32_t *done;
+    rlk::PostTerm *terms;
+    uint32_t *counters;
     int32_t *seq_n;
     float4 *rec;
 };
 size_t distill_layout(int32_t T, int32_t S, void *base, DistillWork &w) {
     Carve c{static_cast<char *>(base)};
-    w.done = c.take<uint32_t>(1);
-    w.partials = c.take<rlk::PostPartial>(rlk::kPostMaxBlocks);
+    w.counters = c.take<uint32_t>(rlk::post_counters(T));
+    w.partials = c.take<rlk::PostPartial>(rlk::post_chunks(T) + 1);
+    w.terms = c.take<rlk::PostTerm>((size_t)T);
     w.seq_n = c.take<int32_t>((size_t)S);
     w.rec = c.take<float4>((size_t)T);
     return align_up(c.off, 256);
@@ -53,6 +55,7 @@ size_t distill_layout(int32_t T, int32_t S, void *base, DistillWork &w) {
 
 struct PrefWork {
     uint32_t *done;
+    uint32_t *counters;
     float *logp;
     float2 *stats;
     float *coef;
@@ -61,6 +64,7 @@ struct PrefWork {
 size_t pref_layout(int32_t T, int32_t S, void *base, PrefWork &w) {
     Carve c{static_cast<char *>(base)};
     w.done = c.take<uint32_t>(1);
+    w.counters = c.take<uint32_t>(rlk::kCountChunks);
     w.logp = c.take<float>((size_t)T);
     w.stats = c.take<float2>((size_t)T);
     w.coef = c.take<float>((size_t)S);
@@ -138,7 +142,8 @@ RL_LOSS_API rl_status rl_loss_distill(const rl_loss_distill_config *config, int3
     q.cu_seqlens = cu_seqlens;
     q.rec = w.rec;
     q.seq_n = w.seq_n;
-    q.blocks_done = w.done;
+    q.counters = w.counters;
+    q.n_counters = (int32_t)rlk::post_counters(T);
     q.status = device_status;
 
     rlk::DistillParams p{};
@@ -152,8 +157,9 @@ RL_LOSS_API rl_status rl_loss_distill(const rl_loss_distill_config *config, int3
     p.r.mask = mask;
     p.r.cu_seqlens = cu_seqlens;
     p.r.status = device_status;
+    p.r.terms = w.terms;
     p.r.partials = w.partials;
-    p.r.blocks_done = w.done;
+    p.r.counters = w.counters;
     p.r.loss = loss;
     p.r.loss_f64 = loss_f64;
     p.ids = ids;
@@ -239,12 +245,14 @@ RL_LOSS_API rl_status rl_loss_preference(const rl_loss_pref_config *config, int3
     b.seq_logratio = seq_logratio;
     b.pair_loss = pair_loss;
     b.pairs_done = w.done;
+    b.tickets = w.counters + rlk::kCountTickets;
     b.loss = loss;
     b.loss_f64 = loss_f64;
     b.status = device_status;
 
     rlk::ScaleParams g{};
     g.r = q.r;
+    g.r.counters = w.counters;
     g.stats = w.stats;
     g.coef = w.coef;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_ptr);

@@ -60,7 +60,8 @@ __device__ __forceinline__ void add_exp(Sum2 &sum, float v) {
 // parts: with most of the mass in the entries, fp32 would leave it no digits.
 __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepParams p) {
     __shared__ int s_i[32];
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.blocks_done = 0;
+    if (blockIdx.x == 0)
+        for (int k = threadIdx.x; k < p.n_counters; k += kPrepThreads) p.counters[k] = 0;
     if ((int)blockIdx.x < p.S) {
         const int i = blockIdx.x;
         const int2 r = seq_range(p.cu_seqlens, p.S, p.T, i, p.status);
@@ -136,6 +137,7 @@ __global__ void __launch_bounds__(kPrepThreads) pref_pairs_kernel(PrefPairParams
     __shared__ Sum2 s_loss[kPrepThreads / 32];
     __shared__ int s_last;
     const int j = blockIdx.x, P = p.S / 2;
+    if (j == 0 && threadIdx.x < 8) p.tickets[threadIdx.x] = 0;
     const int h = threadIdx.x / kHalf, lane = threadIdx.x & 31, warp = (threadIdx.x % kHalf) / 32;
     {
         int b = __ldg(p.cu_seqlens + 2 * j + h), e = __ldg(p.cu_seqlens + 2 * j + h + 1);

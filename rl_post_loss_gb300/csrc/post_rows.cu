@@ -28,55 +28,39 @@ namespace {
 
 // ---------------------------------------------------------------- sums of the batch
 
-// Fixed-order sums of the slots' partials by the last of `nslots` blocks to fill its slot; it leaves
-// the count at 0. Called by every thread of the block, with 512 bytes of shared memory.
-template <typename Finish>
-__device__ __forceinline__ void finish_sums(const PostRows &r, const PostPartial &mine, int slot, int nslots, void *scratch,
-                                            Finish finish) {
-    double *s_d = static_cast<double *>(scratch);      // [32]
-    int *s_i = reinterpret_cast<int *>(s_d + 32);      // [32]
-    int &s_last = s_i[32];
-    __syncthreads();  // the scratch may be the ring's memory
-    if (threadIdx.x == 0) {
-        r.partials[slot] = mine;
-        __threadfence();
-        s_last = atomicAdd(r.blocks_done, 1u) == (uint32_t)nslots - 1;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    PostPartial a{};
-    for (int b = threadIdx.x; b < nslots; b += blockDim.x) {
-        const PostPartial q = r.partials[b];
-        a.loss += q.loss;
-        a.ent += q.ent;
-        a.kl += q.kl;
-        a.n += q.n;
-        a.popped += q.popped;
-        a.clipped += q.clipped;
-        a.masked += q.masked;
-    }
-    a.loss = block_sum_f64(a.loss, s_d);
-    a.ent = block_sum_f64(a.ent, s_d);
-    a.kl = block_sum_f64(a.kl, s_d);
-    a.n = block_sum_i32(a.n, s_i);
-    a.popped = block_sum_i32(a.popped, s_i);
-    a.clipped = block_sum_i32(a.clipped, s_i);
-    a.masked = block_sum_i32(a.masked, s_i);
-    finish(a, s_i);
-    if (threadIdx.x == 0) {
-        *r.blocks_done = 0;
-        r.loss[0] = (float)a.loss;
-        if (r.loss_f64) r.loss_f64[0] = a.loss;
-        if (!isfinite(a.loss)) post_raise(r.status, RL_ERR_NONFINITE);
-    }
+__device__ __forceinline__ void add_partial(PostPartial &a, const PostPartial &q) {
+    a.loss += q.loss;
+    a.ent += q.ent;
+    a.kl += q.kl;
+    a.n += q.n;
+    a.popped += q.popped;
+    a.clipped += q.clipped;
+    a.masked += q.masked;
 }
 
-__device__ __forceinline__ void policy_finish(const PolicyParams &p, const PostPartial &a, int *s_i) {
+__device__ __forceinline__ PostPartial warp_sum(PostPartial a) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        PostPartial q;
+        q.loss = __shfl_xor_sync(0xffffffffu, a.loss, off);
+        q.ent = __shfl_xor_sync(0xffffffffu, a.ent, off);
+        q.kl = __shfl_xor_sync(0xffffffffu, a.kl, off);
+        q.n = __shfl_xor_sync(0xffffffffu, a.n, off);
+        q.popped = __shfl_xor_sync(0xffffffffu, a.popped, off);
+        q.clipped = __shfl_xor_sync(0xffffffffu, a.clipped, off);
+        q.masked = __shfl_xor_sync(0xffffffffu, a.masked, off);
+        add_partial(a, q);
+    }
+    return a;
+}
+
+// The batch's results from its sums, by one warp.
+__device__ __forceinline__ void write_sums(const PolicyParams &p, const PostPartial &a) {
+    const int lane = threadIdx.x & 31;
     int empty = 0;
-    for (int i = threadIdx.x; i < p.r.S; i += blockDim.x) empty += p.seq_n[i] == 0;
-    empty = block_sum_i32(empty, s_i);
-    if (threadIdx.x != 0) return;
+    for (int i = lane; i < p.r.S; i += 32) empty += p.seq_n[i] == 0;
+    empty = warp_sum_i32(empty);
+    if (lane != 0) return;
     if (p.counts) {
         p.counts[0] = a.popped;
         p.counts[1] = a.clipped;
@@ -85,6 +69,96 @@ __device__ __forceinline__ void policy_finish(const PolicyParams &p, const PostP
     }
     if (p.mean_entropy) p.mean_entropy[0] = a.n > 0 ? (float)(a.ent / a.n) : 0.f;
     if (p.kl.mean_kl) p.kl.mean_kl[0] = a.n > 0 ? (float)(a.kl / a.n) : 0.f;
+}
+__device__ __forceinline__ void write_sums(const DistillParams &, const PostPartial &) {}
+
+template <typename P>
+__device__ __forceinline__ void write_loss(const P &p, const PostPartial &a) {
+    write_sums(p, a);
+    if ((threadIdx.x & 31) == 0) {
+        p.r.loss[0] = (float)a.loss;
+        if (p.r.loss_f64) p.r.loss_f64[0] = a.loss;
+        if (!isfinite(a.loss)) post_raise(p.r.status, RL_ERR_NONFINITE);
+    }
+}
+
+__device__ __forceinline__ void count_flags(PostPartial &a, const PolicyParams &p, int t) {
+    const uint32_t f = __ldcg(p.flags + t);
+    const bool m = !(f & RL_FLAG_MASKED);
+    a.n += m;
+    a.masked += !m;
+    a.popped += m && !(f & RL_FLAG_POP_IN_BOUNDS);
+    a.clipped += m && (f & RL_FLAG_CLIP_ACTIVE);
+}
+__device__ __forceinline__ void count_flags(PostPartial &, const DistillParams &, int) {}
+
+// Counts `n` rows of a chunk whose terms this warp has written. The warp that counts a chunk's last row
+// sums the chunk, and the one that sums the last chunk writes the batch's results.
+template <typename P>
+__device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
+    const int lane = threadIdx.x & 31, T = p.r.T;
+    const int c0 = chunk * kSumRows, c1 = min(T, c0 + kSumRows), chunks = (T + kSumRows - 1) / kSumRows;
+    int last = 0;
+    if (lane == 0) {
+        __threadfence();
+        last = atomicAdd(p.r.counters + kCountChunks + chunk, (uint32_t)n) == (uint32_t)(c1 - c0 - n);
+    }
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
+    PostPartial a{};
+#pragma unroll
+    for (int i = 0; i < kSumRows / 32; ++i) {
+        const int k = c0 + lane + 32 * i;
+        if (k >= c1) continue;
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.r.terms + k));
+        a.loss += __hiloint2double(__float_as_int(v.y), __float_as_int(v.x));
+        a.ent += (double)v.z;
+        a.kl += (double)v.w;
+        count_flags(a, p, k);
+    }
+    a = warp_sum(a);
+    if (lane == 0) {
+        p.r.partials[chunk] = a;
+        __threadfence();
+        last = atomicAdd(p.r.counters + kCountDone, 1u) == (uint32_t)chunks - 1;
+    }
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
+    a = PostPartial{};
+    for (int k = lane; k < chunks; k += 32) {
+        const volatile PostPartial &q = p.r.partials[k];
+        add_partial(a, PostPartial{q.loss, q.ent, q.kl, q.n, q.popped, q.clipped, q.masked});
+    }
+    write_loss(p, warp_sum(a));
+}
+
+// The rows of one chunk that a warp has written and not yet counted: counting takes a fence and an atomic,
+// once for the rows of a ticket.
+struct PendingRows {
+    int chunk = 0, n = 0;
+};
+template <typename P>
+__device__ __forceinline__ void add_term(const P &p, PendingRows &pend, int t, const PostTerm &term) {
+    const int chunk = t / kSumRows;
+    if (pend.n > 0 && chunk != pend.chunk) {
+        count_rows(p, pend.chunk, pend.n);
+        pend.n = 0;
+    }
+    if ((threadIdx.x & 31) == 0) p.r.terms[t] = term;
+    pend.chunk = chunk;
+    pend.n += 1;
+}
+template <typename P>
+__device__ __forceinline__ void flush_rows(const P &p, PendingRows &pend) {
+    if (pend.n > 0) count_rows(p, pend.chunk, pend.n);
+    pend.n = 0;
+}
+
+template <typename P>
+__device__ __forceinline__ void one_term(const P &p, int t, const PostTerm &term) {
+    PendingRows pend;
+    add_term(p, pend, t, term);
+    flush_rows(p, pend);
 }
 
 template <typename T>
@@ -106,6 +180,7 @@ constexpr int kRowBlocks = 3;                  // CTAs on an SM
 constexpr int kMaxCluster = 8;
 constexpr int kMaxDepth = 4;
 constexpr int kBatch = 4;                      // 16-byte groups a lane takes at once
+constexpr int kTickets = 4;                    // tickets of a cluster in flight
 
 // Rows whose records are held. A ring of one slice has use for the next row's record alone; a distilled
 // row's record takes two dependent loads to gather and starts a row earlier; the others have room.
@@ -118,6 +193,7 @@ struct RowPlan {
     int32_t parts;      // segments of a warp's share of the slice
     int32_t seg;        // 16-byte groups per segment
     int32_t depth;      // segments in a warp's ring
+    int32_t rows;       // consecutive rows per ticket (at most 32)
     int32_t lag;        // rows folded ahead of the row that is written: 1 where the ring holds two slices, else 0
 };
 
@@ -125,18 +201,24 @@ template <int OP>
 struct RowMeta;
 template <>
 struct RowMeta<kOpLogp> {
+    int32_t t;             // the row, -1: there are no more
+    int32_t last;          // of its ticket
     int32_t read;          // the row's logits are needed (and copied)
     int32_t y;             // the sampled entry, -1: none
     float zy;
 };
 template <>
 struct RowMeta<kOpPolicy> {
+    int32_t t;             // the row, -1: there are no more
+    int32_t last;          // of its ticket
     int32_t read, y;
     float zy;
     PolicyTok tok;
 };
 template <>
 struct RowMeta<kOpDistill> {
+    int32_t t;             // the row, -1: there are no more
+    int32_t last;          // of its ticket
     int32_t read, copied;  // its logits are needed; they were copied (its entries then turned out bad)
     int32_t bad, have;     // an id outside the vocabulary; entries that are not padding
     float4 rec;
@@ -144,6 +226,8 @@ struct RowMeta<kOpDistill> {
 };
 template <>
 struct RowMeta<kOpScale> {
+    int32_t t;             // the row, -1: there are no more
+    int32_t last;          // of its ticket
     int32_t read;
     RowGrad grad;
 };
@@ -165,11 +249,13 @@ struct RowShared {
     uint64_t part_full[kMeta];                    // the warps' statistics of a row
     uint64_t fin_full[kMeta];                     // a row's results
     uint64_t written[kMeta];                      // distill: the warps have written the row
+    uint64_t tbar[kTickets], tfree[kTickets];     // the cluster's tickets: come; taken by every CTA (the first CTA's count)
     uint64_t xbar[2];  // the cluster's statistics: two in turn, as another CTA's next ones may come before the last of these
     RowMsg xmsg[2][kMaxCluster];
     RowMsg part[kMeta][kWarps];
     RowMeta<OP> meta[kMeta];
     RowFin fin[kMeta];
+    int32_t ticket[kTickets];
     int32_t dead;                                 // a wait ran out: nothing waits any more
 };
 static_assert(offsetof(RowShared<kOpLogp>, xmsg) % 16 == 0 && offsetof(RowShared<kOpPolicy>, xmsg) % 16 == 0 &&
@@ -187,6 +273,11 @@ __device__ __forceinline__ void row_wait(RowShared<OP> &sh, uint64_t *bar, uint3
     }
 }
 
+template <int OP>
+__device__ __forceinline__ bool any_dead(RowShared<OP> &sh) {
+    return __any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&sh.dead) != 0);
+}
+
 // A bounded wait for one barrier per lane (null: none): `act` runs for a lane as soon as its barrier is
 // through.
 template <int OP, typename Act>
@@ -199,7 +290,7 @@ __device__ __forceinline__ void lanes_wait(RowShared<OP> &sh, bool mine, uint64_
             pending = false;
         }
         if (!__any_sync(0xffffffffu, pending)) return;
-        if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&sh.dead) != 0)) return;
+        if (any_dead(sh)) return;
         uint64_t now;
         asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
         if (t0 == 0) t0 = now;
@@ -214,6 +305,12 @@ __device__ __forceinline__ void lanes_wait(RowShared<OP> &sh, bool mine, uint64_
 __device__ __forceinline__ void st_async16(uint32_t dst, uint32_t bar, const RowMsg &v) {
     asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(dst),
                  "r"(__float_as_uint(v.m)), "r"(__float_as_uint(v.s)), "r"(__float_as_uint(v.u)), "r"(v.bad), "r"(bar)
+                 : "memory");
+}
+
+// 4 bytes likewise.
+__device__ __forceinline__ void st_async4(uint32_t dst, uint32_t bar, int v) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(dst), "r"(v), "r"(bar)
                  : "memory");
 }
 
@@ -233,6 +330,7 @@ template <typename T, int OP>
 __device__ __forceinline__ RowMeta<OP> load_meta(const typename OpParams<OP>::type &p, int t, int N) {
     using VT = PostVec<T>;
     RowMeta<OP> m{};
+    m.t = t;
     const char *z = row_in<T>(p.r, t);
     if constexpr (OP == kOpLogp) {
         const int y = __ldg(p.r.targets + t);
@@ -373,12 +471,6 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
     uint64_t *s_full = reinterpret_cast<uint64_t *>(s_ring + (size_t)plan.depth * kWarps * plan.seg);
     uint64_t *s_empty = s_full + plan.depth * kWarps;
     float *s_meta = reinterpret_cast<float *>(s_empty + plan.depth * kWarps);
-    const int n_rows = q < T_ ? (T_ - 1 - q) / nclusters + 1 : 0;
-    // the r-th row of this cluster; scale: the rows read last are the likeliest in L2
-    auto row_of = [&](int r) {
-        const int t = q + r * nclusters;
-        return OP == kOpScale ? T_ - 1 - t : t;
-    };
     auto use = [](int r) { return (uint32_t)(r / kMeta) & 1u; };  // the phase of row r's record
     // groups of part j of warp w's share
     auto seg_groups = [&](int w, int j) { return max(0, min(plan.seg, v1 - v0 - (j * kWarps + w) * plan.seg)); };
@@ -396,6 +488,10 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             ptx::mbar_init(ptx::smem_u32(&sh.written[s]), kWarps);
         }
         for (int s = 0; s < 2; ++s) ptx::mbar_init(ptx::smem_u32(&sh.xbar[s]), 1);
+        for (int s = 0; s < kTickets; ++s) {
+            ptx::mbar_init(ptx::smem_u32(&sh.tbar[s]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh.tfree[s]), C);
+        }
         ptx::fence_mbar_init();
         sh.dead = 0;
     }
@@ -410,35 +506,93 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
     }
     __syncthreads();
     if (kStats && C > 1) ptx::cluster_sync();  // every CTA's mbarriers are ready
-    PostPartial sum{};
-
     if (warp == kWarps) {
         // ------------------------------------------------ producer
         int n = 0, d = 0;      // segments issued for each warp; their next place
         uint32_t phase = 0;
         const uint64_t pol = ptx::l2_evict_first_policy();
-        RowMeta<OP> mine{};    // the record of row (r & ~31) + lane
-        for (int r = 0; r < n_rows; ++r) {
-            const int t = row_of(r), ms = r % kMeta;
-            if ((r & 31) == 0 && r + lane < n_rows) mine = load_meta<T, OP>(p, row_of(r + lane), N);
-            const int read = __shfl_sync(0xffffffffu, mine.read, r & 31);
+        // The next rows: those of the log-prob pass go round the clusters in turn; the others are handed out
+        // by a counter, as the SMs do not run alike (the slowest clusters took 9% longer than the middle
+        // ones). The first CTA of a cluster asks, one ticket ahead, and tells the others.
+        constexpr bool kDynamic = OP != kOpLogp;
+        const bool shared = kStats && C > 1;
+        uint32_t *counter = p.r.counters + kCountTickets + (kStats ? 0 : rank);
+        int ahead = 0, n_tickets = -1;
+        auto take = [&]() -> int {
+            if (!kDynamic) return ahead++;
+            int v = ahead;
+            if (!shared || rank == 0)
+                if (lane == 0) ahead = nclusters + (int)atomicAdd(counter, 1u);
+            if (n_tickets < 0) {  // the first one is the cluster's own number
+                n_tickets = 0;
+                return q;
+            }
+            if (shared) {
+                const int s = n_tickets % kTickets;
+                const uint32_t phase_t = (uint32_t)(n_tickets / kTickets) & 1u;
+                const uint32_t bar = ptx::smem_u32(&sh.tbar[s]), at = ptx::smem_u32(&sh.ticket[s]);
+                if (rank == 0) {
+                    if (n_tickets >= kTickets) row_wait(sh, &sh.tfree[s], phase_t ^ 1, p.r.status);
+                    v = __shfl_sync(0xffffffffu, v, 0);
+                    if (lane < C) st_async4(ptx::mapa_shared(at, lane), ptx::mapa_shared(bar, lane), v);
+                }
+                if (lane == 0) ptx::mbar_arrive_expect_tx(bar, 4);
+                __syncwarp();
+                row_wait(sh, &sh.tbar[s], phase_t, p.r.status);
+                v = *reinterpret_cast<volatile int32_t *>(&sh.ticket[s]);
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh.tfree[s]), 0));
+                ++n_tickets;
+            }
+            return __shfl_sync(0xffffffffu, v, 0);
+        };
+        const int n_rows = kDynamic ? T_ : q < T_ ? (T_ - 1 - q) / nclusters + 1 : 0;
+        // the k-th row; scale: from the last row backwards, the rows read last being the likeliest in L2
+        auto row_of = [&](int k) { return OP == kOpScale ? T_ - 1 - k : kDynamic ? k : q + k * nclusters; };
+        RowMeta<OP> mine{};  // the record of the ticket's row `lane`
+        int row0 = 0, left = 0, at = 0;
+        auto fetch = [&] {
+            const int64_t first = (int64_t)take() * plan.rows;
+            left = first < n_rows ? min(plan.rows, n_rows - (int)first) : 0;
+            row0 = (int)first;
+            at = 0;
+            if (lane < left) mine = load_meta<T, OP>(p, row_of(row0 + lane), N);
+        };
+        fetch();
+        for (int r = 0;; ++r) {
+            const int ms = r % kMeta;
+            if (left == 0 || any_dead(sh)) {  // the end
+                if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
+                if (lane == 0) {
+                    sh.meta[ms].t = -1;
+                    ptx::mbar_arrive(ptx::smem_u32(&sh.mfull[ms]));
+                }
+                break;
+            }
+            const int i = at++, t = row_of(row0 + i);
+            const int read = __shfl_sync(0xffffffffu, mine.read, i);
             const char *src = row_in<T>(p.r, t) + (size_t)v0 * 16;
             float *mz = s_meta + (size_t)ms * 3 * K;
             int *s_id = reinterpret_cast<int *>(mz + 2 * K);
             if constexpr (OP == kOpDistill) {
                 // before the row's copies, which wait for segments: the gather takes two dependent loads
                 if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
-                if (lane == (r & 31)) sh.meta[ms] = mine;
+                if (lane == i) sh.meta[ms] = mine;
+                __syncwarp();
+                if (lane == 0) sh.meta[ms].last = at == left;
                 __syncwarp();
                 if (read) load_entries<T>(p, t, sh.meta[ms], mz, mz + K, s_id);
             }
             auto record = [&] {
                 if constexpr (OP != kOpDistill) {
                     if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
-                    if (lane == (r & 31)) sh.meta[ms] = mine;
+                    if (lane == i) sh.meta[ms] = mine;
                     __syncwarp();
+                    if (lane == 0) sh.meta[ms].last = at == left;
                 }
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mfull[ms]));
+                // the next ticket and its rows' records, a chain of dependent loads, come behind this row's copies
+                if (at == left) fetch();
             };
             if (!read) {
                 record();
@@ -465,9 +619,8 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 // the record goes between the row's first copies and those that wait for segments of the
                 // same row (a row longer than the ring): the consumers free none before they have it
                 if (j == min(plan.parts, plan.depth) - 1) record();
-                if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&sh.dead) != 0)) break;
+                if (any_dead(sh)) break;
             }
-            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int32_t *>(&sh.dead) != 0)) break;
         }
         if (*reinterpret_cast<volatile int32_t *>(&sh.dead) && lane < kWarps) {
             // a wait ran out: no copy may be in flight when the block exits
@@ -479,6 +632,8 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
         int exchanges = 0;
         DistillRow last{};      // distill: the row before this one, whose entries are still to be written
         bool last_live = false;
+        int last_t = 0;
+        PendingRows pend;
         // The entries are written after the rest of the row, whose value they replace, and after the next
         // row's results are out: nobody waits for them.
         auto write_entries = [&](int r) {
@@ -488,7 +643,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 const int *s_id = reinterpret_cast<const int *>(s_z + 2 * K);
                 row_wait(sh, &sh.written[ms], use(r), p.r.status);
                 if (last_live) {
-                    char *dz = row_out<T>(p.r, row_of(r));
+                    char *dz = row_out<T>(p.r, last_t);
                     for (int k = lane; k < K; k += 32) {
                         const int id = s_id[k];
                         if ((id >= v0 * VEC && id < v1 * VEC) || (last_rank && id >= nvec * VEC))
@@ -499,11 +654,14 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
             }
         };
-        for (int r = 0; kStats && r < n_rows; ++r) {
-            const int t = row_of(r), ms = r % kMeta;
+        int r = 0;
+        for (; kStats; ++r) {
+            const int ms = r % kMeta;
             const bool writes = r % C == rank;  // the CTAs take turns in writing the rows' results
             row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
             const RowMeta<OP> &meta = sh.meta[ms];
+            const int t = meta.t;
+            if (t < 0 || any_dead(sh)) break;
             RowFin &fin = sh.fin[ms];
             const bool read = meta.read;
             const float *s_z = s_meta + (size_t)ms * 3 * K, *s_lq = s_z + K;
@@ -549,13 +707,17 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                     if (p.stats) p.stats[t] = make_float2(st.m, st.s);
                 }
             } else if constexpr (OP == kOpPolicy) {
+                PostTerm term{};
                 if (lane == 0) {
                     const float logp = read && meta.y >= 0 ? post_target<kEnt>(st, meta.zy, st) : 0.f;
                     const PolicyRow row = policy_row(p, meta.tok, st, logp);
                     fin.grad = row.grad;
                     ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
-                    if (writes) policy_write(p, t, meta.tok, st, row, sum);
+                    if (writes) term = policy_write(p, t, meta.tok, st, row);
                 }
+                __syncwarp();
+                if (writes) add_term(p, pend, t, term);
+                if (meta.last) flush_rows(p, pend);
             } else if constexpr (OP == kOpDistill) {
                 const bool live = read && !dup;
                 DistillRow row{};
@@ -571,19 +733,22 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                         if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
                         if (live && !isfinite(row.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
                         if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : kl;
-                        sum.loss += meta.w * (double)p.scale * (double)kl;
                     }
+                    __syncwarp();
+                    add_term(p, pend, t, PostTerm{live ? meta.w * (double)p.scale * (double)kl : 0.0, 0.f, 0.f});
                 }
+                if (meta.last) flush_rows(p, pend);
                 if (r > 0) write_entries(r - 1);
                 last = row;
                 last_live = live;
+                last_t = t;
             }
             if constexpr (OP != kOpDistill) {
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
             }
         }
-        if (n_rows > 0) write_entries(n_rows - 1);
+        if (r > 0) write_entries(r - 1);
     } else {
         // ------------------------------------------------ consumers
         const int tail_v = nvec * VEC + tid;     // this thread's entry of the last V mod VEC
@@ -597,11 +762,12 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             if constexpr (OP == kOpDistill) return m.copied != 0;
             else return m.read != 0;
         };
-        // A: the statistics of row r
-        auto fold = [&](int r) {
+        // A: the statistics of row r; false where there are no more rows
+        auto fold = [&](int r) -> bool {
             const int ms = r % kMeta;
             row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
             const RowMeta<OP> &meta = sh.meta[ms];
+            if (meta.t < 0 || any_dead(sh)) return false;
             if (meta.read) {
                 int y = -1;
                 uint32_t marks = 0;
@@ -645,7 +811,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 }
                 PostStats st = acc.stats();
                 if (has_tail && tail_v != y && !((marks >> tid) & 1)) {
-                    const float x[1] = {VT::load1(row_in<T>(p.r, row_of(r)), tail_v)};
+                    const float x[1] = {VT::load1(row_in<T>(p.r, meta.t), tail_v)};
                     post_fold<kEnt>(st, x, c);
                 }
                 st = post_warp_merge<kEnt>(st, c);
@@ -658,18 +824,21 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 ptx::mbar_arrive(ptx::smem_u32(&sh.part_full[ms]));
                 if (!kGrad) ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
             }
+            return true;
         };
         // B: the gradient of row r
-        auto write = [&](int r) {
-            const int t = row_of(r), ms = r % kMeta;
+        auto write = [&](int r) -> bool {
+            const int ms = r % kMeta;
             RowGrad gr;
             if constexpr (OP == kOpScale) {
                 row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
+                if (sh.meta[ms].t < 0 || any_dead(sh)) return false;
                 gr = sh.meta[ms].grad;
             } else {
                 row_wait(sh, &sh.fin_full[ms], use(r), p.r.status);
                 gr = sh.fin[ms].grad;
             }
+            const int t = sh.meta[ms].t;
             const bool in_ring = copied(sh.meta[ms]), zero = gr.y < 0;
             char *dz = row_out<T>(p.r, t);
             const int ky = OP == kOpDistill || zero || gr.y >= nvec * VEC ? -1 : gr.y / VEC - v0;
@@ -709,27 +878,22 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 if (OP == kOpDistill) ptx::mbar_arrive(ptx::smem_u32(&sh.written[ms]));
                 ptx::mbar_arrive(ptx::smem_u32(&sh.mempty[ms]));
             }
+            return true;
         };
+        int r = 0;
         if constexpr (!kGrad) {
-            for (int r = 0; r < n_rows; ++r) fold(r);
+            while (fold(r)) ++r;
         } else if constexpr (!kStats) {
-            for (int r = 0; r < n_rows; ++r) write(r);
+            while (write(r)) ++r;
         } else {
-            for (int r = 0; r < n_rows + plan.lag; ++r) {
-                if (r < n_rows) fold(r);
+            for (; fold(r); ++r)
                 if (r >= plan.lag) write(r - plan.lag);
-            }
+            for (int k = max(0, r - plan.lag); k < r && !any_dead(sh); ++k) write(k);
         }
     }
     if constexpr (OP == kOpPolicy || OP == kOpDistill) {
-        // the finisher's sums go to thread 0; the ring is no longer in use
-        PostPartial *s_sum = reinterpret_cast<PostPartial *>(reinterpret_cast<char *>(s_ring) + 512);
-        __syncthreads();
-        if (tid == kRowThreads - 32) *s_sum = sum;
-        __syncthreads();
-        finish_sums(p.r, *s_sum, (int)blockIdx.x, (int)gridDim.x, s_ring, [&](const PostPartial &all, int *s_i) {
-            if constexpr (OP == kOpPolicy) policy_finish(p, all, s_i);
-        });
+        // an empty batch: there is no row whose term could be the last
+        if (T_ == 0 && blockIdx.x == 0 && warp == 0) write_loss(p, PostPartial{});
     }
     if (kStats && C > 1) ptx::cluster_sync();  // no CTA leaves while another may still write to it
 }
@@ -809,8 +973,7 @@ template <typename T, bool kEnt>
 __global__ void __launch_bounds__(kThreads) long_policy_kernel(PolicyParams p) {
     __shared__ PostStats s_warp[kThreads / 32];
     __shared__ RowGrad s_grad;
-    __shared__ double s_scratch[64];
-    PostPartial sum{};
+    __shared__ PostTerm s_term;
     for (int t = blockIdx.x; t < p.r.T; t += gridDim.x) {
         const char *z = row_in<T>(p.r, t);
         const bool read = p.read_masked || __ldg(p.r.mask + t);
@@ -822,15 +985,16 @@ __global__ void __launch_bounds__(kThreads) long_policy_kernel(PolicyParams p) {
             const float logp = ok && read ? post_target<kEnt>(st, PostVec<T>::load1(z, y), st) : 0.f;
             const PolicyTok tok = policy_load(p, t, find_seq(p.r.cu_seqlens, p.r.S, t));
             const PolicyRow row = policy_row(p, tok, st, logp);
-            policy_write(p, t, tok, st, row, sum);
+            s_term = policy_write(p, t, tok, st, row);
             s_grad = row.grad;
         }
         __syncthreads();
+        if (threadIdx.x < 32) one_term(p, t, s_term);
         const RowGrad gr = s_grad;
         write_row<T>(z, row_out<T>(p.r, t), p.r.V, kLog2e, gr);
         __syncthreads();
     }
-    finish_sums(p.r, sum, blockIdx.x, gridDim.x, s_scratch, [&](const PostPartial &a, int *s_i) { policy_finish(p, a, s_i); });
+    if (p.r.T == 0 && threadIdx.x < 32) write_loss(p, PostPartial{});
 }
 
 template <typename T>
@@ -844,9 +1008,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
     __shared__ PostStats s_warp[kThreads / 32];
     __shared__ DistillRow s_row;
     __shared__ int s_int[32];
-    __shared__ double s_scratch[64];
     const int V = p.r.V, nvec = V / VEC;
-    PostPartial sum{};
     int N = 0;
     if (p.per_token) {
         for (int i = threadIdx.x; i < p.r.S; i += kThreads) N += p.seq_n[i];
@@ -859,6 +1021,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
         const bool on = i >= 0 && __ldg(p.r.mask + t);
         if (!on) {
             if (threadIdx.x == 0 && p.kl) p.kl[t] = 0.f;
+            if (threadIdx.x < 32) one_term(p, t, PostTerm{});
             write_row<T>(z, dz, V, p.c, RowGrad{0.f, 0.f, 0.f, -1});
             continue;
         }
@@ -916,6 +1079,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
                 if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
                 if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : 0.f;
             }
+            if (threadIdx.x < 32) one_term(p, t, PostTerm{});
             write_row<T>(z, dz, V, p.c, RowGrad{0.f, 0.f, 0.f, -1});
             __syncthreads();
             continue;
@@ -929,8 +1093,9 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
                 s_row = r;
                 if (!isfinite(r.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
                 if (p.kl) p.kl[t] = kl;
-                sum.loss += w * (double)p.scale * (double)kl;
             }
+            __syncwarp();
+            one_term(p, t, PostTerm{w * (double)p.scale * (double)kl, 0.f, 0.f});
         }
         __syncthreads();
         const DistillRow r = s_row;
@@ -941,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
             if (s_id[k] >= 0) VT::store1(dz, s_id[k], distill_entry(p, r, s_z[k], s_lq[k]));
         __syncthreads();
     }
-    finish_sums(p.r, sum, blockIdx.x, gridDim.x, s_scratch, [](const PostPartial &, int *) {});
+    if (p.r.T == 0 && threadIdx.x < 32) write_loss(p, PostPartial{});
 }
 
 // ---------------------------------------------------------------- launches
@@ -983,7 +1148,7 @@ cudaError_t resident_clusters(const void *kernel, const cudaLaunchConfig_t &cfg,
         resident = sms * per / C;
     }
     if (e != cudaSuccess) return e;
-    *out = std::max(1, std::min(resident, kPostMaxBlocks / C));
+    *out = std::max(1, resident);
     known[next] = Entry{kernel, dev, C, cfg.dynamicSmemBytes, *out};
     next = (next + 1) % kEntries;
     return cudaSuccess;
@@ -1040,6 +1205,9 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, cudaStream_
     int resident = 0;
     const cudaError_t e = resident_clusters(reinterpret_cast<const void *>(kernel), cfg, C, (int)kMaxDynamic, &resident);
     if (e != cudaSuccess) return e;
+    // a ticket's rows: 128 KB of a CTA's share, so that the dozen dependent loads behind a ticket are spread
+    // over rows that take long enough, where that leaves every cluster four tickets
+    plan.rows = OP == kOpLogp ? 32 : std::max(1, std::min({32, 8192 / plan.slice, p.r.T / (4 * resident)}));
     const int nclusters = std::max(1, std::min(p.r.T, resident));
     cfg.gridDim = dim3((unsigned)(nclusters * C));
     return cudaLaunchKernelEx(&cfg, kernel, p, plan, nclusters);

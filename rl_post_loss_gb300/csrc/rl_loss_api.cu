@@ -38,8 +38,8 @@ static size_t workspace_layout(const rl_loss_config &c, rl_loss_handle_s *h, cha
     char *tok_rec = carve(T * sizeof(float4));
     char *tok_meta = carve(T * sizeof(uint32_t));
     char *loss_scratch = carve(4 * sizeof(float));
-    char *post_partials = carve(rlk::kPostMaxBlocks * sizeof(rlk::PostPartial));
-    char *post_done = carve(sizeof(uint32_t));
+    char *post_partials = carve((rlk::post_chunks((int64_t)T) + 1) * sizeof(rlk::PostPartial));
+    char *post_counters = carve(rlk::post_counters((int64_t)T) * sizeof(uint32_t));
     if (h) {
         h->status = reinterpret_cast<uint32_t *>(status);
         h->seq_adv = reinterpret_cast<float *>(seq_adv);
@@ -57,7 +57,7 @@ static size_t workspace_layout(const rl_loss_config &c, rl_loss_handle_s *h, cha
         h->tok_meta = reinterpret_cast<uint32_t *>(tok_meta);
         h->loss_scratch = reinterpret_cast<float *>(loss_scratch);
         h->post_partials = reinterpret_cast<rlk::PostPartial *>(post_partials);
-        h->post_done = reinterpret_cast<uint32_t *>(post_done);
+        h->post_counters = reinterpret_cast<uint32_t *>(post_counters);
     }
     return align_up(off, 256);
 }
@@ -346,7 +346,6 @@ RL_LOSS_API rl_status rl_loss_create(const rl_loss_config *config, rl_loss_t *ou
     }
     workspace_layout(c, h, reinterpret_cast<char *>(h->ws));
     if (cudaMemset(h->status, 0, sizeof(uint32_t)) != cudaSuccess ||
-        cudaMemset(h->post_done, 0, sizeof(uint32_t)) != cudaSuccess ||
         cudaMemset(h->tok_fix, 0, (size_t)c.max_tokens) != cudaSuccess) {
         cudaFree(h->ws);
         delete h;
@@ -405,8 +404,12 @@ RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inp
     p.r.logp = out->logp;
     p.r.entropy = out->entropy;
     p.r.status = h->status;
+    static_assert(sizeof(rlk::PostTerm) == sizeof(float4), "a row's term takes its token record's place");
+    p.r.terms = reinterpret_cast<rlk::PostTerm *>(h->tok_rec);
     p.r.partials = h->post_partials;
-    p.r.blocks_done = h->post_done;
+    p.r.counters = h->post_counters;
+    L.sp.zero = h->post_counters;
+    L.sp.n_zero = (int32_t)rlk::post_counters(L.T);
     p.r.loss = out->loss;
     p.r.loss_f64 = out->loss_f64;
     p.c = h->consts;
@@ -418,7 +421,7 @@ RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inp
     p.seq_w = h->seq_w;
     p.seq_w64 = h->seq_w64;
     p.seq_n = h->seq_n;
-    p.flags = out->flags;
+    p.flags = out->flags ? out->flags : h->tok_flags;
     p.counts = out->counts;
     p.mean_entropy = out->mean_entropy;
     p.read_masked = out->logp || out->entropy;

@@ -26,6 +26,8 @@ __global__ void __launch_bounds__(kPrepThreads) seg_prep_kernel(SeqPrepParams p)
     __shared__ int iscratch[32];
     const int i = blockIdx.x;
     const int T = p.num_tokens;
+    if (i == 0)
+        for (int k = threadIdx.x; k < p.n_zero; k += kPrepThreads) p.zero[k] = 0;
     int b = __ldg(p.cu_seqlens + i), e = __ldg(p.cu_seqlens + i + 1);
     const bool bad = (b < 0) || (e < b) || (e > T) || (i == 0 && b != 0) || (i == p.num_seqs - 1 && e != T);
     if (bad) {
