@@ -42,6 +42,21 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
     return r;
 }
 
+// ---------------------------------------------------------------- sums in two parts
+
+// A sum held as two fp32 values, |lo| a rounding of hi at most: about 48 bits at fp32's speed (the
+// device's fp64 units are some sixty times slower).
+struct Sum2 {
+    float hi, lo;
+    __device__ __forceinline__ void add(float h, float l) {
+        const float s = __fadd_rn(hi, h), b = __fsub_rn(s, hi);
+        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(h, b));  // Knuth's exact error of hi + h
+        l = __fadd_rn(__fadd_rn(lo, l), err);
+        hi = __fadd_rn(s, l);
+        lo = __fsub_rn(l, __fsub_rn(hi, s));
+    }
+};
+
 // ---------------------------------------------------------------- logits of either type
 
 template <typename T>
@@ -293,12 +308,12 @@ __device__ __forceinline__ void post_raise(uint32_t *status, rl_status code) {
 // by the block that finishes the last one. Rows go to blocks as these come for them; the order of the
 // additions depends on the sizes alone.
 struct alignas(16) PostTerm {
-    double loss;
-    float ent, kl;
+    float loss, ent, kl;
+    uint32_t flags;
 };
 constexpr int kSumRows = 256;
 struct PostPartial {
-    double loss, ent, kl;
+    Sum2 loss, ent, kl;
     int32_t n, popped, clipped, masked;
 };
 
@@ -354,9 +369,8 @@ struct PolicyParams {
     const float *token_adv;      // RL_ADV_PER_TOKEN, else null
     const float *teacher;        // RL_ADV_TEACHER_LOGP, else null
     const float *seq_adv, *seq_w;
-    const double *seq_w64;
     const int32_t *seq_n;
-    uint8_t *flags;              // [T]
+    uint8_t *flags;              // optional
     int32_t *counts;             // optional
     float *mean_entropy;         // optional
     int32_t read_masked;         // the log-probs or entropies of masked tokens are wanted
@@ -494,7 +508,6 @@ struct PolicyTok {
     int32_t seq, y;  // seq < 0: outside every response
     int32_t m, ok;   // loss mask; the target is in the vocabulary
     float A, w, lo, li, ref, teacher;
-    double w64;
 };
 
 __device__ __forceinline__ PolicyTok policy_load(const PolicyParams &p, int t, int i) {
@@ -505,7 +518,6 @@ __device__ __forceinline__ PolicyTok policy_load(const PolicyParams &p, int t, i
     k.m = i >= 0 && __ldg(p.r.mask + t) != 0;
     k.A = p.token_adv ? __ldg(p.token_adv + t) : (i >= 0 ? p.seq_adv[i] : 0.f);
     k.w = i >= 0 ? p.seq_w[i] : 0.f;
-    k.w64 = i >= 0 ? p.seq_w64[i] : 0.0;
     k.lo = __ldg(p.logp_old + t);
     k.li = __ldg(p.logp_infer + t);
     k.ref = __ldg(p.kl.logp_ref + t);
@@ -553,7 +565,7 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const Pol
     return r;
 }
 
-// Every per-token output of a policy row; returns what it adds to the sums (its counts come from the flags).
+// Every per-token output of a policy row; returns what it adds to the sums.
 __device__ __forceinline__ PostTerm policy_write(const PolicyParams &p, int t, const PolicyTok &k, PostStats st, const PolicyRow &r) {
     const bool ok = k.ok, m = k.m;
     const float nan = __int_as_float(0x7fc00000);
@@ -562,9 +574,9 @@ __device__ __forceinline__ PostTerm policy_write(const PolicyParams &p, int t, c
     if ((m || p.read_masked) && !post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
     if (p.r.logp) p.r.logp[t] = ok ? r.o.logp : nan;
     if (p.r.entropy) p.r.entropy[t] = r.o.H;
-    p.flags[t] = (uint8_t)r.o.flags;
+    if (p.flags) p.flags[t] = (uint8_t)r.o.flags;
     if (p.kl.kl) p.kl.kl[t] = m && !ok ? nan : r.kl;
-    return PostTerm{k.w64 * ((double)p.kl.coef * (double)r.kl - (double)r.o.obj), m ? r.o.H : 0.f, m ? r.kl : 0.f};
+    return PostTerm{k.w * fmaf(p.kl.coef, r.kl, -r.o.obj), m ? r.o.H : 0.f, m ? r.kl : 0.f, r.o.flags};
 }
 
 // ---------------------------------------------------------------- the teacher's entries

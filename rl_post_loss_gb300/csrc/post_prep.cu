@@ -21,19 +21,6 @@ __device__ __forceinline__ int2 seq_range(const int32_t *cu, int S, int T, int i
     return make_int2(b, e);
 }
 
-// A sum held as two fp32 values, |lo| a rounding of hi at most: about 48 bits at fp32's speed (the
-// device's fp64 units are some sixty times slower; a row of 128 entries took them 0.1 us of the whole GPU).
-struct Sum2 {
-    float hi, lo;
-    __device__ __forceinline__ void add(float h, float l) {
-        const float s = __fadd_rn(hi, h), b = __fsub_rn(s, hi);
-        const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(h, b));  // Knuth's exact error of hi + h
-        l = __fadd_rn(__fadd_rn(lo, l), err);
-        hi = __fadd_rn(s, l);
-        lo = __fsub_rn(l, __fsub_rn(hi, s));
-    }
-};
-
 // Adds e^v, v <= 88, to a sum, within about 1e-9 relative: v = n ln 2 + r in Cody and Waite's two parts of
 // ln 2 (the first has 10 bits, so that n times it is exact), then e^r = 1 + r + the rest of Taylor's series,
 // of which only the rest, below 0.07, is rounded to fp32.

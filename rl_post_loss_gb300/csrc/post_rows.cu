@@ -29,22 +29,25 @@ namespace {
 // ---------------------------------------------------------------- sums of the batch
 
 __device__ __forceinline__ void add_partial(PostPartial &a, const PostPartial &q) {
-    a.loss += q.loss;
-    a.ent += q.ent;
-    a.kl += q.kl;
+    a.loss.add(q.loss.hi, q.loss.lo);
+    a.ent.add(q.ent.hi, q.ent.lo);
+    a.kl.add(q.kl.hi, q.kl.lo);
     a.n += q.n;
     a.popped += q.popped;
     a.clipped += q.clipped;
     a.masked += q.masked;
 }
 
+__device__ __forceinline__ Sum2 shfl_xor(const Sum2 &s, int off) {
+    return Sum2{__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off)};
+}
 __device__ __forceinline__ PostPartial warp_sum(PostPartial a) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         PostPartial q;
-        q.loss = __shfl_xor_sync(0xffffffffu, a.loss, off);
-        q.ent = __shfl_xor_sync(0xffffffffu, a.ent, off);
-        q.kl = __shfl_xor_sync(0xffffffffu, a.kl, off);
+        q.loss = shfl_xor(a.loss, off);
+        q.ent = shfl_xor(a.ent, off);
+        q.kl = shfl_xor(a.kl, off);
         q.n = __shfl_xor_sync(0xffffffffu, a.n, off);
         q.popped = __shfl_xor_sync(0xffffffffu, a.popped, off);
         q.clipped = __shfl_xor_sync(0xffffffffu, a.clipped, off);
@@ -67,8 +70,8 @@ __device__ __forceinline__ void write_sums(const PolicyParams &p, const PostPart
         p.counts[2] = a.masked;
         p.counts[3] = empty;
     }
-    if (p.mean_entropy) p.mean_entropy[0] = a.n > 0 ? (float)(a.ent / a.n) : 0.f;
-    if (p.kl.mean_kl) p.kl.mean_kl[0] = a.n > 0 ? (float)(a.kl / a.n) : 0.f;
+    if (p.mean_entropy) p.mean_entropy[0] = a.n > 0 ? (a.ent.hi + a.ent.lo) / (float)a.n : 0.f;
+    if (p.kl.mean_kl) p.kl.mean_kl[0] = a.n > 0 ? (a.kl.hi + a.kl.lo) / (float)a.n : 0.f;
 }
 __device__ __forceinline__ void write_sums(const DistillParams &, const PostPartial &) {}
 
@@ -76,21 +79,12 @@ template <typename P>
 __device__ __forceinline__ void write_loss(const P &p, const PostPartial &a) {
     write_sums(p, a);
     if ((threadIdx.x & 31) == 0) {
-        p.r.loss[0] = (float)a.loss;
-        if (p.r.loss_f64) p.r.loss_f64[0] = a.loss;
-        if (!isfinite(a.loss)) post_raise(p.r.status, RL_ERR_NONFINITE);
+        const float loss = a.loss.hi + a.loss.lo;
+        p.r.loss[0] = loss;
+        if (p.r.loss_f64) p.r.loss_f64[0] = (double)a.loss.hi + (double)a.loss.lo;
+        if (!isfinite(loss)) post_raise(p.r.status, RL_ERR_NONFINITE);
     }
 }
-
-__device__ __forceinline__ void count_flags(PostPartial &a, const PolicyParams &p, int t) {
-    const uint32_t f = __ldcg(p.flags + t);
-    const bool m = !(f & RL_FLAG_MASKED);
-    a.n += m;
-    a.masked += !m;
-    a.popped += m && !(f & RL_FLAG_POP_IN_BOUNDS);
-    a.clipped += m && (f & RL_FLAG_CLIP_ACTIVE);
-}
-__device__ __forceinline__ void count_flags(PostPartial &, const DistillParams &, int) {}
 
 // Counts `n` rows of a chunk whose terms this warp has written. The warp that counts a chunk's last row
 // sums the chunk, and the one that sums the last chunk writes the batch's results.
@@ -111,10 +105,15 @@ __device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
         const int k = c0 + lane + 32 * i;
         if (k >= c1) continue;
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.r.terms + k));
-        a.loss += __hiloint2double(__float_as_int(v.y), __float_as_int(v.x));
-        a.ent += (double)v.z;
-        a.kl += (double)v.w;
-        count_flags(a, p, k);
+        const uint32_t f = __float_as_uint(v.w);
+        const bool m = !(f & RL_FLAG_MASKED);
+        a.loss.add(v.x, 0.f);
+        a.ent.add(v.y, 0.f);
+        a.kl.add(v.z, 0.f);
+        a.n += m;
+        a.masked += !m;
+        a.popped += m && !(f & RL_FLAG_POP_IN_BOUNDS);
+        a.clipped += m && (f & RL_FLAG_CLIP_ACTIVE);
     }
     a = warp_sum(a);
     if (lane == 0) {
@@ -127,7 +126,7 @@ __device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
     a = PostPartial{};
     for (int k = lane; k < chunks; k += 32) {
         const volatile PostPartial &q = p.r.partials[k];
-        add_partial(a, PostPartial{q.loss, q.ent, q.kl, q.n, q.popped, q.clipped, q.masked});
+        add_partial(a, PostPartial{{q.loss.hi, q.loss.lo}, {q.ent.hi, q.ent.lo}, {q.kl.hi, q.kl.lo}, q.n, q.popped, q.clipped, q.masked});
     }
     write_loss(p, warp_sum(a));
 }
@@ -222,7 +221,7 @@ struct RowMeta<kOpDistill> {
     int32_t read, copied;  // its logits are needed; they were copied (its entries then turned out bad)
     int32_t bad, have;     // an id outside the vocabulary; entries that are not padding
     float4 rec;
-    double w;              // the row's weight
+    float w;               // the row's weight
 };
 template <>
 struct RowMeta<kOpScale> {
@@ -357,7 +356,7 @@ __device__ __forceinline__ RowMeta<OP> load_meta(const typename OpParams<OP>::ty
         m.read = i >= 0 && __ldg(p.r.mask + t);
         if (m.read) {
             m.rec = p.rec[t];
-            m.w = p.per_token ? 1.0 / (double)N : 1.0 / ((double)p.r.S * (double)p.seq_n[i]);
+            m.w = 1.f / (p.per_token ? (float)N : (float)p.r.S * (float)p.seq_n[i]);
             // a teacher that gives the row no mass: it contributes nothing
             if (m.rec.w == -1.f) m.read = 0;
         }
@@ -444,6 +443,9 @@ __device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail
     return __any_sync(0xffffffffu, dup);
 }
 
+// Waits for the launches before this one where it began while they ran.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <typename T, int OP, bool kEnt>
 __global__ void __launch_bounds__(kRowThreads, kRowBlocks)
 ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __grid_constant__ RowPlan plan, int nclusters) {
@@ -495,6 +497,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
         ptx::fence_mbar_init();
         sh.dead = 0;
     }
+    grid_dependency_wait();  // what follows reads what the launches before this one wrote
     if constexpr (OP == kOpLogp)
         if (p.zero && blockIdx.x == 0 && tid == 0) *p.zero = 0;
     if constexpr (OP == kOpDistill) {
@@ -721,7 +724,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             } else if constexpr (OP == kOpDistill) {
                 const bool live = read && !dup;
                 DistillRow row{};
-                if (live) row = distill_finish(p, st, Mk, Sk, s_z, s_lq, meta.rec, (float)meta.w * p.scale * p.inv_tau, V - meta.have);
+                if (live) row = distill_finish(p, st, Mk, Sk, s_z, s_lq, meta.rec, meta.w * p.scale * p.inv_tau, V - meta.have);
                 if (lane == 0) {
                     fin.grad = RowGrad{live ? row.ct : 0.f, row.m, 0.f, live ? 0 : -1};
                     ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
@@ -735,7 +738,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                         if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : kl;
                     }
                     __syncwarp();
-                    add_term(p, pend, t, PostTerm{live ? meta.w * (double)p.scale * (double)kl : 0.0, 0.f, 0.f});
+                    add_term(p, pend, t, PostTerm{live ? meta.w * p.scale * kl : 0.f, 0.f, 0.f, 0u});
                 }
                 if (meta.last) flush_rows(p, pend);
                 if (r > 0) write_entries(r - 1);
@@ -1072,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
         bad = __syncthreads_or(bad);
         st = block_merge<false>(st, s_warp, p.c);
         const int n_i = p.seq_n[i];
-        const double w = p.per_token ? 1.0 / (double)N : 1.0 / ((double)p.r.S * (double)n_i);
+        const float w = 1.f / (p.per_token ? (float)N : (float)p.r.S * (float)n_i);
         const bool none = have == 0 || rec.w == -1.f;  // the teacher gives the row no mass
         if (bad || none) {  // excluded: contributes nothing
             if (threadIdx.x == 0) {
@@ -1087,7 +1090,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
         if (threadIdx.x < 32) {
             float Mk, Sk;
             distill_entry_stats(s_z, p.K, p.c, Mk, Sk);
-            const DistillRow r = distill_finish(p, st, Mk, Sk, s_z, s_lq, rec, (float)w * p.scale * p.inv_tau, V - have);
+            const DistillRow r = distill_finish(p, st, Mk, Sk, s_z, s_lq, rec, w * p.scale * p.inv_tau, V - have);
             const float kl = p.reverse ? r.kl : distill_kl(p, r, s_z, s_lq, rec);
             if (threadIdx.x == 0) {
                 s_row = r;
@@ -1095,7 +1098,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
                 if (p.kl) p.kl[t] = kl;
             }
             __syncwarp();
-            one_term(p, t, PostTerm{w * (double)p.scale * (double)kl, 0.f, 0.f});
+            one_term(p, t, PostTerm{w * p.scale * kl, 0.f, 0.f, 0u});
         }
         __syncthreads();
         const DistillRow r = s_row;
@@ -1139,7 +1142,7 @@ cudaError_t resident_clusters(const void *kernel, const cudaLaunchConfig_t &cfg,
         }
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_dynamic);
     int resident = 0;
-    if (e == cudaSuccess && cfg.numAttrs) {
+    if (e == cudaSuccess && cfg.numAttrs > 1) {
         e = cudaOccupancyMaxActiveClusters(&resident, kernel, &cfg);
     } else if (e == cudaSuccess) {
         int sms = 0, per = 0;
@@ -1155,7 +1158,7 @@ cudaError_t resident_clusters(const void *kernel, const cudaLaunchConfig_t &cfg,
 }
 
 template <typename T, int OP, bool kEnt>
-cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, cudaStream_t stream, bool &fits) {
+cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_own, cudaStream_t stream, bool &fits) {
     auto kernel = ring_rows_kernel<T, OP, kEnt>;
     constexpr bool kStats = OP != kOpScale, kKeep = OP == kOpPolicy || OP == kOpDistill;
     const int nvec = p.r.V / PostVec<T>::kElems;
@@ -1191,32 +1194,36 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, cudaStream_
     }
     const size_t smem = std::max<size_t>((size_t)plan.depth * kWarps * (plan.seg + 1) * 16 + (size_t)kMetaOf(OP) * 12 * K, 1024);
 
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)C;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)C);
     cfg.blockDim = dim3(kRowThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = kStats && C > 1 ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = kStats && C > 1 ? 2 : 1;
     int resident = 0;
-    const cudaError_t e = resident_clusters(reinterpret_cast<const void *>(kernel), cfg, C, (int)kMaxDynamic, &resident);
+    cudaError_t e = resident_clusters(reinterpret_cast<const void *>(kernel), cfg, C, (int)kMaxDynamic, &resident);
     if (e != cudaSuccess) return e;
     // a ticket's rows: 128 KB of a CTA's share, so that the dozen dependent loads behind a ticket are spread
     // over rows that take long enough, where that leaves every cluster four tickets
     plan.rows = OP == kOpLogp ? 32 : std::max(1, std::min({32, 8192 / plan.slice, p.r.T / (4 * resident)}));
     const int nclusters = std::max(1, std::min(p.r.T, resident));
     cfg.gridDim = dim3((unsigned)(nclusters * C));
+    // the launch may begin while the one before it ends (it waits before it reads anything of that one's)
+    if (!after_own) cfg.attrs = attr + 1, cfg.numAttrs -= 1;
     return cudaLaunchKernelEx(&cfg, kernel, p, plan, nclusters);
 }
 
 template <typename T>
 cudaError_t launch_logp(const LogpParams &p, cudaStream_t stream) {
     bool fits;
-    return p.r.entropy ? launch_ring<T, kOpLogp, true>(p, 0, stream, fits) : launch_ring<T, kOpLogp, false>(p, 0, stream, fits);
+    return p.r.entropy ? launch_ring<T, kOpLogp, true>(p, 0, false, stream, fits) : launch_ring<T, kOpLogp, false>(p, 0, false, stream, fits);
 }
 
 int long_grid(int T) { return std::max(1, std::min(T, 608)); }
@@ -1225,7 +1232,7 @@ template <typename T>
 cudaError_t launch_policy(const PolicyParams &p, cudaStream_t stream) {
     const bool ent = p.r.entropy || p.mean_entropy;
     bool fits;
-    const cudaError_t e = ent ? launch_ring<T, kOpPolicy, true>(p, 0, stream, fits) : launch_ring<T, kOpPolicy, false>(p, 0, stream, fits);
+    const cudaError_t e = ent ? launch_ring<T, kOpPolicy, true>(p, 0, true, stream, fits) : launch_ring<T, kOpPolicy, false>(p, 0, true, stream, fits);
     if (fits) return e;
     if (ent) long_policy_kernel<T, true><<<long_grid(p.r.T), kThreads, 0, stream>>>(p);
     else long_policy_kernel<T, false><<<long_grid(p.r.T), kThreads, 0, stream>>>(p);
@@ -1235,7 +1242,7 @@ cudaError_t launch_policy(const PolicyParams &p, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_distill(const DistillParams &p, cudaStream_t stream) {
     bool fits;
-    const cudaError_t e = launch_ring<T, kOpDistill, false>(p, p.K, stream, fits);
+    const cudaError_t e = launch_ring<T, kOpDistill, false>(p, p.K, true, stream, fits);
     if (fits) return e;
     long_distill_kernel<T><<<long_grid(p.r.T), kThreads, (size_t)p.K * 12, stream>>>(p);
     return cudaGetLastError();
@@ -1244,7 +1251,7 @@ cudaError_t launch_distill(const DistillParams &p, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_scale(const ScaleParams &p, cudaStream_t stream) {
     bool fits;
-    return launch_ring<T, kOpScale, false>(p, 0, stream, fits);
+    return launch_ring<T, kOpScale, false>(p, 0, true, stream, fits);
 }
 
 }  // namespace

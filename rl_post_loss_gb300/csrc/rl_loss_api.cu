@@ -419,9 +419,8 @@ RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inp
     p.teacher = c.adv_mode == RL_ADV_TEACHER_LOGP ? in->rewards_or_adv : nullptr;
     p.seq_adv = h->seq_adv;
     p.seq_w = h->seq_w;
-    p.seq_w64 = h->seq_w64;
     p.seq_n = h->seq_n;
-    p.flags = out->flags ? out->flags : h->tok_flags;
+    p.flags = out->flags;
     p.counts = out->counts;
     p.mean_entropy = out->mean_entropy;
     p.read_masked = out->logp || out->entropy;
