@@ -282,15 +282,15 @@ __device__ __forceinline__ PostStats post_merge(PostStats a, PostStats b, float 
 }
 
 // Merges the lanes' statistics: their maximum first, so that each is rescaled once; sums in a
-// butterfly, which leaves the same bits in every lane.
-template <bool kEnt>
+// butterfly, which leaves the same bits in every lane. (kLanes: within groups of so many lanes.)
+template <bool kEnt, int kLanes = 32>
 __device__ __forceinline__ PostStats post_warp_merge(PostStats r, float c) {
     float M = r.m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    for (int off = kLanes / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     post_rescale<kEnt>(r, M, c);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
+    for (int off = kLanes / 2; off > 0; off >>= 1) {
         r.s = __fadd_rn(r.s, __shfl_xor_sync(0xffffffffu, r.s, off));
         if (kEnt) r.u = __fadd_rn(r.u, __shfl_xor_sync(0xffffffffu, r.u, off));
     }

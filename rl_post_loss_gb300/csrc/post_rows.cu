@@ -409,19 +409,23 @@ __device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail
     const int lo = v0 * VEC, hi = (v0 + g) * VEC;
     bool dup = false, any = false;
     uint32_t mine = 0;
+#pragma unroll 4
     for (int k = lane; k < K; k += 32) {
         const int id = s_id[k];
         if (id >= lo && id < hi) {
             at[id - lo] = (Tag)k;
             any = true;
-        } else if (tail0 >= 0 && id >= tail0) {
-            const uint32_t bit = 1u << (id - tail0);
-            dup |= (mine & bit) != 0;
-            mine |= bit;
         }
     }
     tail = 0;
-    if (tail0 >= 0) {  // a bit that two lanes hold was listed twice
+    if (tail0 >= 0) {
+        for (int k = lane; k < K; k += 32) {
+            const int id = s_id[k];
+            if (id < tail0) continue;
+            const uint32_t bit = 1u << (id - tail0);
+            dup |= (mine & bit) != 0;
+            mine |= bit;
+        }  // a bit that two lanes hold was listed twice
 #pragma unroll
         for (int b = 0; b < VEC - 1; ++b) {
             const uint32_t who = __ballot_sync(0xffffffffu, (mine >> b) & 1);
@@ -431,6 +435,7 @@ __device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail
     }
     if (__any_sync(0xffffffffu, any)) {
         __syncwarp();
+#pragma unroll 4
         for (int k = lane; k < K; k += 32) {
             const int id = s_id[k];
             if (id < lo || id >= hi) continue;
@@ -577,28 +582,19 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             const char *src = row_in<T>(p.r, t) + (size_t)v0 * 16;
             float *mz = s_meta + (size_t)ms * 3 * K;
             int *s_id = reinterpret_cast<int *>(mz + 2 * K);
+            // the record goes out before the row's copies, which wait for segments
+            if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
+            if (lane == i) sh.meta[ms] = mine;
+            __syncwarp();
+            if (lane == 0) sh.meta[ms].last = at == left;
             if constexpr (OP == kOpDistill) {
-                // before the row's copies, which wait for segments: the gather takes two dependent loads
-                if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
-                if (lane == i) sh.meta[ms] = mine;
-                __syncwarp();
-                if (lane == 0) sh.meta[ms].last = at == left;
                 __syncwarp();
                 if (read) load_entries<T>(p, t, sh.meta[ms], mz, mz + K, s_id);
             }
-            auto record = [&] {
-                if constexpr (OP != kOpDistill) {
-                    if (r >= kMeta) row_wait(sh, &sh.mempty[ms], use(r) ^ 1, p.r.status);
-                    if (lane == i) sh.meta[ms] = mine;
-                    __syncwarp();
-                    if (lane == 0) sh.meta[ms].last = at == left;
-                }
-                if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mfull[ms]));
-                // the next ticket and its rows' records, a chain of dependent loads, come behind this row's copies
-                if (at == left) fetch();
-            };
+            if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mfull[ms]));
+            const bool more = at == left;
             if (!read) {
-                record();
+                if (more) fetch();
                 continue;
             }
             for (int j = 0; j < plan.parts; ++j) {
@@ -619,9 +615,9 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 });
                 ++n;
                 if (++d == plan.depth) d = 0, phase ^= 1;
-                // the record goes between the row's first copies and those that wait for segments of the
-                // same row (a row longer than the ring): the consumers free none before they have it
-                if (j == min(plan.parts, plan.depth) - 1) record();
+                // the next ticket and its rows' records, a chain of dependent loads, come behind the copies that
+                // need not wait for segments of this row
+                if (more && j == min(plan.parts, plan.depth) - 1) fetch();
                 if (any_dead(sh)) break;
             }
         }
@@ -675,10 +671,10 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             PostStats st{0.f, 1.f, 0.f};
             int dup = 0;
             if (read) {
-                RowMsg w = sh.part[ms][lane < kWarps ? lane : 0];
-                dup = __any_sync(0xffffffffu, lane < kWarps && w.bad);
-                st = lane < kWarps ? PostStats{w.m, w.s, w.u} : kPostStart;
-                st = post_warp_merge<kEnt>(st, c);
+                static_assert(kWarps == 8 && kMaxCluster == 8, "the merges go over groups of eight lanes");
+                RowMsg w = sh.part[ms][lane & 7];
+                dup = __any_sync(0xffffffffu, w.bad);
+                st = post_warp_merge<kEnt, 8>(PostStats{w.m, w.s, w.u}, c);
                 if (C > 1) {
                     const int x = exchanges & 1;
                     const uint32_t bar = ptx::smem_u32(&sh.xbar[x]);
@@ -688,11 +684,11 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                         st_async16(ptx::mapa_shared(ptx::smem_u32(&sh.xmsg[x][rank]), lane), ptx::mapa_shared(bar, lane),
                                    RowMsg{st.m, st.s, st.u, dup});
                     row_wait(sh, &sh.xbar[x], (exchanges >> 1) & 1, p.r.status);
-                    w = sh.xmsg[x][lane < C ? lane : 0];
+                    const bool in = (lane & 7) < C;
+                    w = sh.xmsg[x][in ? lane & 7 : 0];
                     ++exchanges;
-                    st = lane < C ? PostStats{w.m, w.s, w.u} : kPostStart;
-                    dup = __any_sync(0xffffffffu, lane < C && w.bad);
-                    st = post_warp_merge<kEnt>(st, c);
+                    dup = __any_sync(0xffffffffu, w.bad);
+                    st = post_warp_merge<kEnt, 8>(in ? PostStats{w.m, w.s, w.u} : kPostStart, c);
                 }
             }
             if constexpr (OP == kOpLogp) {
@@ -791,7 +787,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                         }
                     }
                     if constexpr (OP == kOpDistill)
-                        dup = mark_entries<T>(seg, v0 + warp * plan.seg, g, last_rank && warp == 0 ? nvec * VEC : -1,
+                        dup = mark_entries<T>(seg, v0 + warp * plan.seg, g, last_rank && warp == 0 && nvec * VEC < V ? nvec * VEC : -1,
                                               reinterpret_cast<const int *>(s_meta + (size_t)ms * 3 * K + 2 * K), K, marks);
                     int k = lane;
                     for (; k - lane + 32 * kBatch <= g; k += 32 * kBatch) {
@@ -1166,32 +1162,37 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_
     const size_t fixed = sizeof(RowShared<OP>) + (size_t)kMetaOf(OP) * 12 * K;
     RowPlan plan{};
     fits = false;
-    // enough CTAs per row that the rows there are fill the SMs; then the fewest whose rings hold a slice
-    // with three CTAs on an SM; with eight, two or one on an SM
-    int C = std::max(1, std::min({(int)kMaxCluster, 456 / std::max(1, p.r.T), nvec / 256}));
-    for (int occ = 0; !fits;) {
-        // groups in a warp's ring; a segment's two barriers take one group's room
-        const int room = (int)((kCtaBytes[occ] - fixed) / (16 * kWarps));
-        plan.cluster = C;
-        plan.slice = std::max(1, (nvec + C - 1) / C);
-        const int share = (plan.slice + kWarps - 1) / kWarps;
-        if (kKeep) {
-            plan.parts = 1;
-            plan.seg = share;
-            plan.depth = std::min(kMaxDepth, room / (share + 1));
-            fits = plan.depth >= 1;
-            plan.lag = plan.depth >= 2;
-        } else {  // two segments of whole batches, or more shorter ones
-            const int batch = 32 * kBatch;
-            plan.seg = std::min(share, std::max(batch, (room / 2 - 1) / batch * batch));
-            plan.parts = (share + plan.seg - 1) / plan.seg;
-            plan.depth = std::min(kMaxDepth, room / (plan.seg + 1));
-            fits = true;
+    // enough CTAs per row that the rows there are fill the SMs
+    const int least = std::max(1, std::min({(int)kMaxCluster, 456 / std::max(1, p.r.T), nvec / 256}));
+    if (kKeep) {
+        // A row's stay in the rings is set by its chain of steps, so the rate goes by the bytes of rows that an
+        // SM holds: the plan that holds most of them, of those within 5% the one with more CTAs on an SM, then
+        // the one with fewer per row. (2048 x 151552 bf16, k = 128: five CTAs a row, three on an SM, 182 KB,
+        // 282 us; three a row, two on an SM, 202 KB, 272 us.)
+        int64_t best = 0;
+        for (int occ = 0; occ < 3; ++occ) {
+            const int room = (int)((kCtaBytes[occ] - fixed) / (16 * kWarps));  // groups in a warp's ring
+            for (int C = least; C <= kMaxCluster; ++C) {
+                const int slice = std::max(1, (nvec + C - 1) / C), share = (slice + kWarps - 1) / kWarps;
+                // a segment's two barriers take one group's room
+                const int depth = std::min(kMaxDepth, room / (share + 1));
+                if (depth < 1) continue;
+                const int64_t held = (int64_t)(3 - occ) * std::min(depth, 2) * slice;
+                if (held * 20 <= best * 21) continue;
+                best = held;
+                plan = RowPlan{C, slice, 1, share, depth, 1, depth >= 2};
+                fits = true;
+            }
         }
-        if (fits) break;
-        if (C < kMaxCluster) ++C;
-        else if (++occ == 3) return cudaSuccess;
+        if (!fits) return cudaSuccess;
+    } else {  // two segments of whole batches in a warp's ring, or more shorter ones
+        const int room = (int)((kCtaBytes[0] - fixed) / (16 * kWarps)), batch = 32 * kBatch;
+        const int slice = std::max(1, (nvec + least - 1) / least), share = (slice + kWarps - 1) / kWarps;
+        const int seg = std::min(share, std::max(batch, (room / 2 - 1) / batch * batch));
+        plan = RowPlan{least, slice, (share + seg - 1) / seg, seg, std::min(kMaxDepth, room / (seg + 1)), 1, 0};
+        fits = true;
     }
+    const int C = plan.cluster;
     const size_t smem = std::max<size_t>((size_t)plan.depth * kWarps * (plan.seg + 1) * 16 + (size_t)kMetaOf(OP) * 12 * K, 1024);
 
     cudaLaunchAttribute attr[2] = {};
