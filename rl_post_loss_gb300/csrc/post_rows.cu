@@ -1165,10 +1165,11 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_
     // enough CTAs per row that the rows there are fill the SMs
     const int least = std::max(1, std::min({(int)kMaxCluster, 456 / std::max(1, p.r.T), nvec / 256}));
     if (kKeep) {
-        // A row's stay in the rings is set by its chain of steps, so the rate goes by the bytes of rows that an
-        // SM holds: the plan that holds most of them, of those within 5% the one with more CTAs on an SM, then
-        // the one with fewer per row. (2048 x 151552 bf16, k = 128: five CTAs a row, three on an SM, 182 KB,
-        // 282 us; three a row, two on an SM, 202 KB, 272 us.)
+        // A row's stay in the rings is set by its chain of steps, so the rate goes by the bytes that an SM's rings
+        // hold, a slice for each CTA: the plan that holds most, and of those within 5% the one with the fewest
+        // CTAs per row. (50257 bf16: one a row, two on an SM, 201 KB, 82% of the copy rate; two and three,
+        // 151 KB, 73%. 128256 bf16: four and three, 192 KB, 84%; three and two, 171 KB, 77%; seven and three
+        // with two slices each, 73%.)
         int64_t best = 0;
         for (int occ = 0; occ < 3; ++occ) {
             const int room = (int)((kCtaBytes[occ] - fixed) / (16 * kWarps));  // groups in a warp's ring
@@ -1177,8 +1178,8 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_
                 // a segment's two barriers take one group's room
                 const int depth = std::min(kMaxDepth, room / (share + 1));
                 if (depth < 1) continue;
-                const int64_t held = (int64_t)(3 - occ) * std::min(depth, 2) * slice;
-                if (held * 20 <= best * 21) continue;
+                const int64_t held = (int64_t)(3 - occ) * slice;
+                if (fits && !(held * 20 > best * 21 || (held * 20 >= best * 19 && C < plan.cluster))) continue;
                 best = held;
                 plan = RowPlan{C, slice, 1, share, depth, 1, depth >= 2};
                 fits = true;
