@@ -109,10 +109,9 @@ struct RowOut {
     uint32_t flags;
 };
 
-// `teacher` is log pi_teacher(y_t) when c.adv_teacher (ignored otherwise). With `logp` the token's
-// log-prob is taken from there (a caller that has it more exactly) instead of z_y - logZ.
+// `teacher` is log pi_teacher(y_t) when c.adv_teacher (ignored otherwise).
 __device__ __forceinline__ RowOut finish_row(RowStats2 st, float4 rec, uint32_t meta, const LossConsts &c,
-                                             float teacher = 0.f, const float *logp = nullptr) {
+                                             float teacher = 0.f) {
     RowOut o;
     const float log2S = log2f(st.s);
     o.logZ2 = st.m2 + log2S;
@@ -121,7 +120,7 @@ __device__ __forceinline__ RowOut finish_row(RowStats2 st, float4 rec, uint32_t 
     uint32_t pre = meta >> 24;
     o.y = meta & kMetaYMask;
     const bool ok = !(pre & RL_FLAG_BAD_TARGET);
-    o.logp = ok ? (logp ? *logp : __fsub_rn(rec.x, logZ)) : __int_as_float(0x7fc00000);
+    o.logp = ok ? __fsub_rn(rec.x, logZ) : __int_as_float(0x7fc00000);
     const float e = __fsub_rn(o.logp, rec.y);  // ln r, one fp32 subtraction
     o.obj = 0.f;
     o.g = 0.f;

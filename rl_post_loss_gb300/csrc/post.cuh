@@ -308,8 +308,7 @@ __device__ __forceinline__ void post_raise(uint32_t *status, rl_status code) {
 // by the block that finishes the last one. Rows go to blocks as these come for them; the order of the
 // additions depends on the sizes alone.
 struct alignas(16) PostTerm {
-    float loss, ent, kl;
-    uint32_t flags;
+    float loss, loss_lo, ent, kl;
 };
 constexpr int kSumRows = 256;
 struct PostPartial {
@@ -341,6 +340,7 @@ struct PostRows {
     // sums of the batch: a term per row, a partial sum per chunk, and counters, all zero at
     // the launch (PostCount)
     PostTerm *terms;
+    uint32_t *term_flags;        // [T] flags of the rows (policy; else null)
     PostPartial *partials;
     uint32_t *counters;
     float *loss;
@@ -369,6 +369,7 @@ struct PolicyParams {
     const float *token_adv;      // RL_ADV_PER_TOKEN, else null
     const float *teacher;        // RL_ADV_TEACHER_LOGP, else null
     const float *seq_adv, *seq_w;
+    const double *seq_w64;
     const int32_t *seq_n;
     uint8_t *flags;              // optional
     int32_t *counts;             // optional
@@ -445,18 +446,30 @@ __device__ __forceinline__ bool post_finite(PostStats st) { return st.s > 0.f &&
 
 // The row's statistics leave the sampled entry out: `rest` are those of the others, zy its logit.
 // With x = sum_{v != y} 2^d 2^{c (m_rest - z_y)} = (1 - p_y) / p_y, ln p_y = -log1p(x) keeps its
-// relative accuracy as p_y nears 1, which 1 + x has lost. Returns ln p_y (NaN where the row is not
-// finite) and the whole row's statistics in `all`.
+// relative accuracy as p_y nears 1, which 1 + x has lost, and so does 1 - p_y = (the others' sum) / S.
+struct PostToken {
+    PostStats all;   // the whole row
+    float others;    // the others' sum against the whole row's reference
+    float logp;      // ln p_y (NaN where the row is not finite)
+};
 template <bool kEnt>
-__device__ __forceinline__ float post_target(PostStats rest, float zy, PostStats &all) {
-    constexpr float c = kLog2e;
-    PostStats y = kPostStart;
-    const float one[1] = {zy};
-    post_fold<kEnt>(y, one, c);
-    all = post_merge<kEnt>(rest, y, c);
-    if (!post_finite(all)) return __int_as_float(0x7fc00000);
-    if (zy >= rest.m) return -log1pf(rest.s * ex2_approx((rest.m - zy) * c));
-    return (zy - rest.m) - logf(all.s);
+__device__ __forceinline__ PostToken post_target(PostStats rest, float zy) {
+    PostToken r;
+    if (zy >= rest.m) {
+        const float dm = (rest.m - zy) * kLog2e, f = exp2f(dm);
+        r.others = rest.s * f;
+        r.all = PostStats{zy, r.others + ((zy - zy) + 1.f), 0.f};  // 1, or NaN for an infinite logit
+        if (kEnt) r.all.u = f * fmaf(fmaxf(dm, kNoWeight), rest.s, rest.u);
+        r.logp = -log1pf(r.others);
+    } else {
+        const float d = (zy - rest.m) * kLog2e, e = exp2f(d);
+        r.others = rest.s;
+        r.all = PostStats{rest.m, rest.s + e, 0.f};
+        if (kEnt) r.all.u = fmaf(e, fmaxf(d, kNoWeight), rest.u);
+        r.logp = (zy - rest.m) - logf(r.all.s);
+    }
+    if (!post_finite(r.all)) r.logp = __int_as_float(0x7fc00000);
+    return r;
 }
 
 __device__ __forceinline__ float post_entropy(PostStats st) { return logf(st.s) - st.u / st.s * kLn2; }
@@ -499,15 +512,21 @@ struct RowGrad {
     int32_t y;  // -1: no entry of its own
 };
 
+// From kept statistics (pref): 1 - p_y from the log-prob.
 __device__ __forceinline__ RowGrad post_row_grad(float g, PostStats st, float logp, int y) {
     return RowGrad{-g / st.s, st.m, -g * expm1f(logp), y};
 }
 
-// Everything a policy row needs besides its logits.
+// Everything a policy row needs besides its logits: what of the objective does not depend on the row's
+// softmax is worked out with the record, as in the token records of the loss without a KL term.
 struct PolicyTok {
-    int32_t seq, y;  // seq < 0: outside every response
-    int32_t m, ok;   // loss mask; the target is in the vocabulary
-    float A, w, lo, li, ref, teacher;
+    int32_t seq, y;        // seq < 0: outside every response
+    int32_t m, ok;         // loss mask; the target is in the vocabulary
+    uint32_t pre;          // flags and the advantage's sign
+    float w, w_lo;         // weight, and what its rounding left of it
+    float lref;            // logp_old, or the rollout log-prob (DIS)
+    float cf, wcf;         // m pop A (m pop with the distillation advantage, m A for DIS), times w
+    float ref, teacher;
 };
 
 __device__ __forceinline__ PolicyTok policy_load(const PolicyParams &p, int t, int i) {
@@ -516,67 +535,96 @@ __device__ __forceinline__ PolicyTok policy_load(const PolicyParams &p, int t, i
     k.y = __ldg(p.r.targets + t);
     k.ok = k.y >= 0 && k.y < p.r.V;
     k.m = i >= 0 && __ldg(p.r.mask + t) != 0;
-    k.A = p.token_adv ? __ldg(p.token_adv + t) : (i >= 0 ? p.seq_adv[i] : 0.f);
+    const float A = p.token_adv ? __ldg(p.token_adv + t) : (i >= 0 ? p.seq_adv[i] : 0.f);
     k.w = i >= 0 ? p.seq_w[i] : 0.f;
-    k.lo = __ldg(p.logp_old + t);
-    k.li = __ldg(p.logp_infer + t);
+    k.w_lo = i >= 0 ? (float)(p.seq_w64[i] - (double)k.w) : 0.f;
+    const float lo = __ldg(p.logp_old + t), li = __ldg(p.logp_infer + t);
     k.ref = __ldg(p.kl.logp_ref + t);
     k.teacher = p.teacher ? __ldg(p.teacher + t) : 0.f;
+    k.pre = (k.m ? 0u : RL_FLAG_MASKED) | (k.ok ? 0u : RL_FLAG_BAD_TARGET) | (A > 0.f ? kPreAPos : 0u) | (A < 0.f ? kPreANeg : 0u);
+    const bool in = k.m && k.ok;
+    if (p.c.objective == RL_OBJ_DIS) {
+        k.lref = li;
+        k.cf = in ? A : 0.f;
+    } else {
+        const float d = __fsub_rn(lo, li);  // ln rho, one fp32 subtraction
+        const bool in_bounds = (-p.c.ln_beta <= d) && (d <= p.c.ln_beta);
+        k.pre |= in_bounds ? RL_FLAG_POP_IN_BOUNDS : 0u;
+        k.lref = lo;
+        const float pop = in && in_bounds ? (p.c.pop_indicator ? 1.f : expf(d)) : 0.f;
+        k.cf = p.c.adv_teacher ? pop : pop * A;
+    }
+    k.wcf = k.w * k.cf;
     return k;
 }
 
-// The token objective and its KL term of a policy row, and the row's gradient. `st` are the whole row's
-// statistics, `logp` its ln p_y (0 where the row was not read).
+// The token objective of Eq. (1) or DIS with its KL term, and the row's gradient.
 struct PolicyRow {
-    RowOut o;
-    float kl;
+    float logp, obj, kl;
+    uint32_t flags;
     RowGrad grad;
 };
 
-__device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const PolicyTok &k, PostStats st, float logp) {
-    const bool ok = k.ok, m = k.m;
-    const float d = __fsub_rn(k.lo, k.li);  // ln rho, one fp32 subtraction
-    const bool in_bounds = (-p.c.ln_beta <= d) && (d <= p.c.ln_beta);
-    uint32_t pre = (m ? 0u : RL_FLAG_MASKED) | (ok ? 0u : RL_FLAG_BAD_TARGET) | (k.A > 0.f ? kPreAPos : 0u) |
-                   (k.A < 0.f ? kPreANeg : 0u);
-    float cf = 0.f, lref = k.lo;
-    if (p.c.objective == RL_OBJ_DIS) {
-        lref = k.li;
-        if (m && ok) cf = k.A;
-    } else {
-        pre |= in_bounds ? RL_FLAG_POP_IN_BOUNDS : 0u;
-        const float pop = (m && ok && in_bounds) ? (p.c.pop_indicator ? 1.f : expf(d)) : 0.f;
-        cf = p.c.adv_teacher ? pop : pop * k.A;
-    }
-    const float4 rec = make_float4(0.f, lref, cf, k.w * cf);
-    const uint32_t meta = (ok ? (uint32_t)k.y : 0u) | (pre << 24);
+__device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const PolicyTok &k, const PostToken &tok, bool read) {
     PolicyRow r;
-    r.o = finish_row(RowStats2{0.f, st.s, st.u}, rec, meta, p.c, k.teacher, &logp);
-    if (!(m || p.read_masked)) {  // nothing of the row was read: no log-prob, and the clip test has nothing to test
-        r.o.H = 0.f;
-        r.o.flags &= ~(RL_FLAG_CLIP_ACTIVE | (p.c.objective == RL_OBJ_DIS ? RL_FLAG_POP_IN_BOUNDS : 0u));
-    }
-    float dkl = 0.f;
+    const LossConsts &c = p.c;
+    const float logp = tok.logp, e = __fsub_rn(logp, k.lref);  // ln r, one fp32 subtraction
+    const bool ok = k.ok && read;
+    float g = 0.f;
+    r.logp = logp;
+    r.obj = 0.f;
     r.kl = 0.f;
-    const bool counts = m && ok;
-    if (counts) post_kl(p.kl.estimator, __fsub_rn(r.o.logp, k.ref), r.kl, dkl);
-    const float g = counts ? fmaf(k.w * p.kl.coef, dkl, r.o.g) : 0.f;
-    r.grad = g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : post_row_grad(g, st, r.o.logp, k.y);
+    if (c.objective == RL_OBJ_DIS) {
+        const bool gate = ok && e > c.clip_lo && e < c.clip_hi;
+        r.flags = (k.pre & (RL_FLAG_MASKED | RL_FLAG_BAD_TARGET)) | (gate ? RL_FLAG_POP_IN_BOUNDS : 0u);
+        if (gate && k.cf != 0.f) {
+            const float ratio = expf(e);
+            r.obj = k.cf * ratio * logp;
+            g = c.dis_stopgrad ? -k.wcf * ratio : -k.wcf * ratio * (1.f + logp);
+        }
+    } else {
+        uint32_t pre = k.pre;
+        float A = 1.f;  // cf and wcf carry it, unless it comes from the teacher
+        if (c.adv_teacher) {
+            A = ok ? __fsub_rn(k.teacher, logp) : 0.f;
+            pre = (pre & ~(kPreAPos | kPreANeg)) | (A > 0.f ? kPreAPos : 0u) | (A < 0.f ? kPreANeg : 0u);
+        }
+        const bool clip = ok && (((pre & kPreAPos) && e > c.clip_hi) || ((pre & kPreANeg) && e < c.clip_lo));
+        r.flags = (pre & kPreOut) | (clip ? RL_FLAG_CLIP_ACTIVE : 0u);
+        if (k.cf != 0.f && A != 0.f) {
+            const float ratio = expf(e);
+            r.obj = k.cf * A * (clip ? ((pre & kPreAPos) ? c.one_plus_eps_high : c.one_minus_eps_low) : ratio);
+            g = clip ? 0.f : -k.wcf * A * ratio;
+        }
+    }
+    if (k.m && k.ok) {
+        float dkl;
+        post_kl(p.kl.estimator, __fsub_rn(logp, k.ref), r.kl, dkl);
+        g = fmaf(k.w * p.kl.coef, dkl, g);
+    }
+    const float inv = 1.f / tok.all.s;
+    r.grad = g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : RowGrad{-g * inv, tok.all.m, g * (tok.others * inv), k.y};
     return r;
 }
 
 // Every per-token output of a policy row; returns what it adds to the sums.
-__device__ __forceinline__ PostTerm policy_write(const PolicyParams &p, int t, const PolicyTok &k, PostStats st, const PolicyRow &r) {
+template <bool kEnt>
+__device__ __forceinline__ PostTerm policy_write(const PolicyParams &p, int t, const PolicyTok &k, const PostToken &tok, const PolicyRow &r,
+                                                 bool read) {
     const bool ok = k.ok, m = k.m;
     const float nan = __int_as_float(0x7fc00000);
+    const float H = kEnt && read ? post_entropy(tok.all) : 0.f;
     if (k.seq < 0) post_raise(p.r.status, RL_ERR_SEQLENS);
     if (!ok) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
-    if ((m || p.read_masked) && !post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
-    if (p.r.logp) p.r.logp[t] = ok ? r.o.logp : nan;
-    if (p.r.entropy) p.r.entropy[t] = r.o.H;
-    if (p.flags) p.flags[t] = (uint8_t)r.o.flags;
+    if (read && !post_finite(tok.all)) post_raise(p.r.status, RL_ERR_NONFINITE);
+    if (p.r.logp) p.r.logp[t] = ok ? r.logp : nan;
+    if (p.r.entropy) p.r.entropy[t] = H;
+    if (p.flags) p.flags[t] = (uint8_t)r.flags;
     if (p.kl.kl) p.kl.kl[t] = m && !ok ? nan : r.kl;
-    return PostTerm{k.w * fmaf(p.kl.coef, r.kl, -r.o.obj), m ? r.o.H : 0.f, m ? r.kl : 0.f, r.o.flags};
+    // w x in two parts: the same weight for a whole response, its rounding would not average out
+    const float x = fmaf(p.kl.coef, r.kl, -r.obj), wx = k.w * x;
+    p.r.term_flags[t] = r.flags;
+    return PostTerm{wx, fmaf(k.w_lo, x, fmaf(k.w, x, -wx)), m ? H : 0.f, m ? r.kl : 0.f};
 }
 
 // ---------------------------------------------------------------- the teacher's entries

@@ -105,11 +105,11 @@ __device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
         const int k = c0 + lane + 32 * i;
         if (k >= c1) continue;
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.r.terms + k));
-        const uint32_t f = __float_as_uint(v.w);
+        const uint32_t f = p.r.term_flags ? __ldcg(p.r.term_flags + k) : RL_FLAG_MASKED;
         const bool m = !(f & RL_FLAG_MASKED);
-        a.loss.add(v.x, 0.f);
-        a.ent.add(v.y, 0.f);
-        a.kl.add(v.z, 0.f);
+        a.loss.add(v.x, v.y);
+        a.ent.add(v.z, 0.f);
+        a.kl.add(v.w, 0.f);
         a.n += m;
         a.masked += !m;
         a.popped += m && !(f & RL_FLAG_POP_IN_BOUNDS);
@@ -696,8 +696,13 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                     float logp = 0.f, ent = 0.f;
                     if (read) {
                         logp = __int_as_float(0x7fc00000);
-                        if (meta.y >= 0) logp = post_target<kEnt>(st, meta.zy, st);
-                        else post_raise(p.r.status, RL_ERR_TARGET_RANGE);
+                        if (meta.y >= 0) {
+                            const PostToken tok = post_target<kEnt>(st, meta.zy);
+                            st = tok.all;
+                            logp = tok.logp;
+                        } else {
+                            post_raise(p.r.status, RL_ERR_TARGET_RANGE);
+                        }
                         if (!post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
                         if (kEnt) ent = post_entropy(st);
                     }
@@ -708,11 +713,12 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             } else if constexpr (OP == kOpPolicy) {
                 PostTerm term{};
                 if (lane == 0) {
-                    const float logp = read && meta.y >= 0 ? post_target<kEnt>(st, meta.zy, st) : 0.f;
-                    const PolicyRow row = policy_row(p, meta.tok, st, logp);
+                    PostToken tok{st, 0.f, 0.f};
+                    if (read && meta.y >= 0) tok = post_target<kEnt>(st, meta.zy);
+                    const PolicyRow row = policy_row(p, meta.tok, tok, read);
                     fin.grad = row.grad;
                     ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
-                    if (writes) term = policy_write(p, t, meta.tok, st, row);
+                    if (writes) term = policy_write<kEnt>(p, t, meta.tok, tok, row, read);
                 }
                 __syncwarp();
                 if (writes) add_term(p, pend, t, term);
@@ -734,7 +740,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                         if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : kl;
                     }
                     __syncwarp();
-                    add_term(p, pend, t, PostTerm{live ? meta.w * p.scale * kl : 0.f, 0.f, 0.f, 0u});
+                    add_term(p, pend, t, PostTerm{live ? meta.w * p.scale * kl : 0.f, 0.f, 0.f, 0.f});
                 }
                 if (meta.last) flush_rows(p, pend);
                 if (r > 0) write_entries(r - 1);
@@ -981,10 +987,11 @@ __global__ void __launch_bounds__(kThreads) long_policy_kernel(PolicyParams p) {
         PostStats st{0.f, 1.f, 0.f};
         if (read) st = block_merge<kEnt>(row_stats<T, kEnt>(z, p.r.V, kLog2e, ok ? y : -1), s_warp, kLog2e);
         if (threadIdx.x == 0) {
-            const float logp = ok && read ? post_target<kEnt>(st, PostVec<T>::load1(z, y), st) : 0.f;
-            const PolicyTok tok = policy_load(p, t, find_seq(p.r.cu_seqlens, p.r.S, t));
-            const PolicyRow row = policy_row(p, tok, st, logp);
-            s_term = policy_write(p, t, tok, st, row);
+            PostToken tok{st, 0.f, 0.f};
+            if (ok && read) tok = post_target<kEnt>(st, PostVec<T>::load1(z, y));
+            const PolicyTok k = policy_load(p, t, find_seq(p.r.cu_seqlens, p.r.S, t));
+            const PolicyRow row = policy_row(p, k, tok, read);
+            s_term = policy_write<kEnt>(p, t, k, tok, row, read);
             s_grad = row.grad;
         }
         __syncthreads();
@@ -1094,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
                 if (p.kl) p.kl[t] = kl;
             }
             __syncwarp();
-            one_term(p, t, PostTerm{w * p.scale * kl, 0.f, 0.f, 0u});
+            one_term(p, t, PostTerm{w * p.scale * kl, 0.f, 0.f, 0.f});
         }
         __syncthreads();
         const DistillRow r = s_row;
@@ -1166,8 +1173,8 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_
     const int least = std::max(1, std::min({(int)kMaxCluster, 456 / std::max(1, p.r.T), nvec / 256}));
     if (kKeep) {
         // A row's stay in the rings is set by its chain of steps, so the rate goes by the bytes that an SM's rings
-        // hold, a slice for each CTA: the plan that holds most, and of those within 5% the one with the fewest
-        // CTAs per row. (50257 bf16: one a row, two on an SM, 201 KB, 82% of the copy rate; two and three,
+        // hold, a slice for each CTA: the plan that holds most, and of those within 5% with two or three CTAs on an SM
+        // the one with the fewest per row. (50257 bf16: one a row, two on an SM, 201 KB, 82% of the copy rate; two and three,
         // 151 KB, 73%. 128256 bf16: four and three, 192 KB, 84%; three and two, 171 KB, 77%; seven and three
         // with two slices each, 73%.)
         int64_t best = 0;
@@ -1179,7 +1186,7 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_
                 const int depth = std::min(kMaxDepth, room / (share + 1));
                 if (depth < 1) continue;
                 const int64_t held = (int64_t)(3 - occ) * slice;
-                if (fits && !(held * 20 > best * 21 || (held * 20 >= best * 19 && C < plan.cluster))) continue;
+                if (fits && !(held * 20 > best * 21 || (occ < 2 && held * 20 >= best * 19 && C < plan.cluster))) continue;
                 best = held;
                 plan = RowPlan{C, slice, 1, share, depth, 1, depth >= 2};
                 fits = true;

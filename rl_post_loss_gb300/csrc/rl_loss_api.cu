@@ -404,8 +404,9 @@ RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inp
     p.r.logp = out->logp;
     p.r.entropy = out->entropy;
     p.r.status = h->status;
-    static_assert(sizeof(rlk::PostTerm) == sizeof(float4), "a row's term takes its token record's place");
+    static_assert(sizeof(rlk::PostTerm) == sizeof(float4), "a row's term and flags take its token record's place");
     p.r.terms = reinterpret_cast<rlk::PostTerm *>(h->tok_rec);
+    p.r.term_flags = h->tok_meta;
     p.r.partials = h->post_partials;
     p.r.counters = h->post_counters;
     L.sp.zero = h->post_counters;
@@ -419,6 +420,7 @@ RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inp
     p.teacher = c.adv_mode == RL_ADV_TEACHER_LOGP ? in->rewards_or_adv : nullptr;
     p.seq_adv = h->seq_adv;
     p.seq_w = h->seq_w;
+    p.seq_w64 = h->seq_w64;
     p.seq_n = h->seq_n;
     p.flags = out->flags;
     p.counts = out->counts;
