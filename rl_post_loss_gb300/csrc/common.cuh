@@ -227,8 +227,6 @@ struct SeqPrepParams {
     int32_t *seq_n;      // workspace [S]
     float *seq_adv_out;  // optional user output [S]
     uint32_t *status;
-    uint32_t *zero;      // optional: words this launch sets to 0 for a later one
-    int32_t n_zero;
 };
 
 struct TokenPrepParams {

@@ -431,6 +431,8 @@ struct ScaleParams {
 };
 
 cudaError_t launch_post_logp(const LogpParams &p, int dtype, cudaStream_t stream);
+// launch_seg_prep that also sets the words of `zero` (the loss's counters) to 0.
+cudaError_t launch_seg_prep(const SeqPrepParams &p, uint32_t *zero, int n_zero, cudaStream_t stream);
 cudaError_t launch_post_policy(const PolicyParams &p, int dtype, cudaStream_t stream);
 cudaError_t launch_distill_prep(const DistillPrepParams &p, cudaStream_t stream);
 cudaError_t launch_post_distill(const DistillParams &p, int dtype, cudaStream_t stream);

@@ -1176,7 +1176,7 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_
         // hold, a slice for each CTA: the plan that holds most, and of those within 5% with two or three CTAs on an SM
         // the one with the fewest per row. (50257 bf16: one a row, two on an SM, 201 KB, 82% of the copy rate; two and three,
         // 151 KB, 73%. 128256 bf16: four and three, 192 KB, 84%; three and two, 171 KB, 77%; seven and three
-        // with two slices each, 73%.)
+        // with two slices each, 73%. 100000 bf16: two and two, 200 KB, 89%; one and one, 200 KB, 80%.)
         int64_t best = 0;
         for (int occ = 0; occ < 3; ++occ) {
             const int room = (int)((kCtaBytes[occ] - fixed) / (16 * kWarps));  // groups in a warp's ring

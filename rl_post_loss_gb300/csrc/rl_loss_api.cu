@@ -409,8 +409,6 @@ RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inp
     p.r.term_flags = h->tok_meta;
     p.r.partials = h->post_partials;
     p.r.counters = h->post_counters;
-    L.sp.zero = h->post_counters;
-    L.sp.n_zero = (int32_t)rlk::post_counters(L.T);
     p.r.loss = out->loss;
     p.r.loss_f64 = out->loss_f64;
     p.c = h->consts;
@@ -432,7 +430,7 @@ RL_LOSS_API rl_status rl_loss_forward_backward_kl(rl_loss_t h, const rl_loss_inp
         return RL_ERR_CUDA;
     };
     int slot = h->prof_begin(kSegPrep, stream);
-    cudaError_t err = rlk::launch_seg_prep(L.sp, stream);
+    cudaError_t err = rlk::launch_seg_prep(L.sp, h->post_counters, (int)rlk::post_counters(L.T), stream);
     if (err == cudaSuccess && c.loss_norm == RL_NORM_PER_TOKEN) err = rlk::launch_seg_token_norm(L.sp, stream);
     h->prof_end(slot, stream);
     if (err != cudaSuccess) return failed(err);

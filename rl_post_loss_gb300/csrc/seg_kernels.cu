@@ -12,6 +12,7 @@
 // never on timing or on how many SMs are free, so results are bit-identical
 // from run to run. No float atomics.
 #include "common.cuh"
+#include "post.cuh"
 
 namespace rlk {
 
@@ -21,13 +22,13 @@ constexpr int kPrepThreads = 256;
 constexpr int kTokenThreads = 256;
 constexpr int kReduceThreads = 256;
 
-// One block per response.
-__global__ void __launch_bounds__(kPrepThreads) seg_prep_kernel(SeqPrepParams p) {
+// One block per response. The first one also sets the n_zero counters of a later launch to 0.
+__global__ void __launch_bounds__(kPrepThreads) seg_prep_kernel(SeqPrepParams p, uint32_t *zero, int n_zero) {
     __shared__ int iscratch[32];
     const int i = blockIdx.x;
     const int T = p.num_tokens;
     if (i == 0)
-        for (int k = threadIdx.x; k < p.n_zero; k += kPrepThreads) p.zero[k] = 0;
+        for (int k = threadIdx.x; k < n_zero; k += kPrepThreads) zero[k] = 0;
     int b = __ldg(p.cu_seqlens + i), e = __ldg(p.cu_seqlens + i + 1);
     const bool bad = (b < 0) || (e < b) || (e > T) || (i == 0 && b != 0) || (i == p.num_seqs - 1 && e != T);
     if (bad) {
@@ -208,10 +209,12 @@ __global__ void __launch_bounds__(kReduceThreads) final_reduce_kernel(ReducePara
 
 }  // namespace
 
-cudaError_t launch_seg_prep(const SeqPrepParams &p, cudaStream_t stream) {
-    seg_prep_kernel<<<p.num_seqs, kPrepThreads, 0, stream>>>(p);
+cudaError_t launch_seg_prep(const SeqPrepParams &p, uint32_t *zero, int n_zero, cudaStream_t stream) {
+    seg_prep_kernel<<<p.num_seqs, kPrepThreads, 0, stream>>>(p, zero, n_zero);
     return cudaGetLastError();
 }
+
+cudaError_t launch_seg_prep(const SeqPrepParams &p, cudaStream_t stream) { return launch_seg_prep(p, nullptr, 0, stream); }
 
 cudaError_t launch_seg_token_norm(const SeqPrepParams &p, cudaStream_t stream) {
     seg_token_norm_kernel<<<1, kReduceThreads, 0, stream>>>(p);
