@@ -8,6 +8,7 @@ error: there is no other code path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -395,6 +396,18 @@ def _vector(name: str, t, n: int, dtype, device, optional: bool = False):
     return t.data_ptr()
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
+def _allocations_of(stream, device):
+    """The context in which a call on `stream` (None: the current one) allocates what its caller left out: the
+    memory then belongs to the stream that uses it, and is not handed to another one while that still does."""
+    import torch
+    if stream is None or device.type != "cuda" or stream == _current_stream(device):
+        return _NO_CONTEXT
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+
+
 def _current_stream(device) -> int:
     """The current stream of a CUDA device as an address, without the Stream object around it."""
     import torch
@@ -412,10 +425,11 @@ def token_logp(logits, targets, mask=None, *, vocab: int | None = None, logp=Non
     import torch
     code, V = _logits_code(logits, vocab)
     T, dev = logits.shape[0], logits.device
-    if logp is None:
-        logp = torch.empty(T, dtype=torch.float32, device=dev)
-    if entropy is None and want_entropy:
-        entropy = torch.empty(T, dtype=torch.float32, device=dev)
+    with _allocations_of(stream, dev):
+        if logp is None:
+            logp = torch.empty(T, dtype=torch.float32, device=dev)
+        if entropy is None and want_entropy:
+            entropy = torch.empty(T, dtype=torch.float32, device=dev)
     if stream is None:
         stream = _current_stream(dev)
     f32 = torch.float32
@@ -440,7 +454,8 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
     if mode not in DISTILL_MODES or direction not in ("forward", "reverse"):
         raise ValueError("mode is 'renorm' or 'tail', direction 'forward' or 'reverse'")
     if dlogits is None:
-        dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
+        with _allocations_of(stream, logits.device):
+            dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
     code, V = _logits_code(logits, vocab, dlogits)
     T, S, dev, f32 = logits.shape[0], cu_seqlens.shape[0] - 1, logits.device, torch.float32
     for name, t, dt in (("teacher_ids", teacher_ids, torch.int32), ("teacher_vals", teacher_vals, f32)):
@@ -448,14 +463,15 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
             raise ValueError(f"{name} is a {dt} tensor [tokens, entries] with contiguous rows on {dev}")
     if teacher_ids.shape != teacher_vals.shape or teacher_ids.stride(0) != teacher_vals.stride(0):
         raise ValueError("teacher_ids and teacher_vals have one shape and layout")
-    if loss is None:
-        loss = torch.empty(1, dtype=f32, device=dev)
-    if kl is None:
-        kl = torch.empty(T, dtype=f32, device=dev)
-    if stream is None:
-        stream = _current_stream(dev)
-    if workspace is None:
-        workspace = _post_workspace(rl_loss_distill_workspace_bytes(T, S), dev, stream)
+    with _allocations_of(stream, dev):
+        if loss is None:
+            loss = torch.empty(1, dtype=f32, device=dev)
+        if kl is None:
+            kl = torch.empty(T, dtype=f32, device=dev)
+        if stream is None:
+            stream = _current_stream(dev)
+        if workspace is None:
+            workspace = _post_workspace(rl_loss_distill_workspace_bytes(T, S), dev, stream)
     cfg = rl_loss_distill_config(code, V, teacher_ids.shape[1], DISTILL_MODES[mode], int(direction == "reverse"),
                                  loss_norm, temperature, scale, tail_floor)
     _check(load().rl_loss_distill(ctypes.byref(cfg), T, S, logits.data_ptr(), logits.stride(0), teacher_ids.data_ptr(),
@@ -482,21 +498,23 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
     if loss_type not in PREF_LOSSES:
         raise ValueError("loss_type is 'sigmoid', 'hinge' or 'ipo'")
     if dlogits is None:
-        dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
+        with _allocations_of(stream, logits.device):
+            dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
     code, V = _logits_code(logits, vocab, dlogits)
     T, S, dev, f32 = logits.shape[0], cu_seqlens.shape[0] - 1, logits.device, torch.float32
-    if loss is None:
-        loss = torch.empty(1, dtype=f32, device=dev)
-    if logp is None:
-        logp = torch.empty(T, dtype=f32, device=dev)
-    if seq_logratio is None:
-        seq_logratio = torch.empty(max(S, 0), dtype=f32, device=dev)
-    if pair_loss is None:
-        pair_loss = torch.empty(max(S // 2, 0), dtype=f32, device=dev)
-    if stream is None:
-        stream = _current_stream(dev)
-    if workspace is None:
-        workspace = _post_workspace(rl_loss_preference_workspace_bytes(T, S), dev, stream)
+    with _allocations_of(stream, dev):
+        if loss is None:
+            loss = torch.empty(1, dtype=f32, device=dev)
+        if logp is None:
+            logp = torch.empty(T, dtype=f32, device=dev)
+        if seq_logratio is None:
+            seq_logratio = torch.empty(max(S, 0), dtype=f32, device=dev)
+        if pair_loss is None:
+            pair_loss = torch.empty(max(S // 2, 0), dtype=f32, device=dev)
+        if stream is None:
+            stream = _current_stream(dev)
+        if workspace is None:
+            workspace = _post_workspace(rl_loss_preference_workspace_bytes(T, S), dev, stream)
     cfg = rl_loss_pref_config(code, V, PREF_LOSSES[loss_type], int(length_norm), beta, margin, label_smoothing, nll_coef)
     _check(load().rl_loss_preference(ctypes.byref(cfg), T, S, logits.data_ptr(), logits.stride(0),
                                      _vector("targets", targets, T, torch.int32, dev),
