@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 
@@ -342,10 +343,12 @@ def rl_loss_distill_max_k() -> int:
     return int(load().rl_loss_distill_max_k())
 
 
+@functools.lru_cache(maxsize=256)
 def rl_loss_distill_workspace_bytes(num_tokens: int, num_seqs: int) -> int:
     return int(load().rl_loss_distill_workspace_bytes(int(num_tokens), int(num_seqs)))
 
 
+@functools.lru_cache(maxsize=256)
 def rl_loss_preference_workspace_bytes(num_tokens: int, num_seqs: int) -> int:
     return int(load().rl_loss_preference_workspace_bytes(int(num_tokens), int(num_seqs)))
 
@@ -391,7 +394,7 @@ def _vector(name: str, t, n: int, dtype, device, optional: bool = False):
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype or t.numel() < n or t.device != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.numel() < n or t.get_device() != device.index or not t.is_contiguous():
         raise ValueError(f"{name} is a contiguous {dtype} tensor of at least {n} values on {device}")
     return t.data_ptr()
 
@@ -406,6 +409,13 @@ def _allocations_of(stream, device):
     if stream is None or device.type != "cuda" or stream == _current_stream(device):
         return _NO_CONTEXT
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
+
+
+def _missing(tensors: tuple, sizes: tuple, device) -> list:
+    """The fp32 tensors as they were given, new ones in the place of those that were not. (An allocation takes
+    1.5 us of host time; one for all of them takes 10, as a tensor is then split.)"""
+    import torch
+    return [torch.empty(n, dtype=torch.float32, device=device) if t is None else t for t, n in zip(tensors, sizes)]
 
 
 def _current_stream(device) -> int:
@@ -464,10 +474,7 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
     if teacher_ids.shape != teacher_vals.shape or teacher_ids.stride(0) != teacher_vals.stride(0):
         raise ValueError("teacher_ids and teacher_vals have one shape and layout")
     with _allocations_of(stream, dev):
-        if loss is None:
-            loss = torch.empty(1, dtype=f32, device=dev)
-        if kl is None:
-            kl = torch.empty(T, dtype=f32, device=dev)
+        loss, kl = _missing((loss, kl), (1, T), dev)
         if stream is None:
             stream = _current_stream(dev)
         if workspace is None:
@@ -503,14 +510,8 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
     code, V = _logits_code(logits, vocab, dlogits)
     T, S, dev, f32 = logits.shape[0], cu_seqlens.shape[0] - 1, logits.device, torch.float32
     with _allocations_of(stream, dev):
-        if loss is None:
-            loss = torch.empty(1, dtype=f32, device=dev)
-        if logp is None:
-            logp = torch.empty(T, dtype=f32, device=dev)
-        if seq_logratio is None:
-            seq_logratio = torch.empty(max(S, 0), dtype=f32, device=dev)
-        if pair_loss is None:
-            pair_loss = torch.empty(max(S // 2, 0), dtype=f32, device=dev)
+        P = max(S // 2, 0)
+        loss, logp, seq_logratio, pair_loss = _missing((loss, logp, seq_logratio, pair_loss), (1, T, max(S, 0), P), dev)
         if stream is None:
             stream = _current_stream(dev)
         if workspace is None:

@@ -301,6 +301,9 @@ __device__ __forceinline__ void post_raise(uint32_t *status, rl_status code) {
     if (status) raise_status(status, code);  // the status word is optional for the entry points without a handle
 }
 
+// Waits for the launches before this one where it began while they ran.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- parameters
 
 // What a row adds to the batch's sums, written by whichever block took the row, and sums of them: over

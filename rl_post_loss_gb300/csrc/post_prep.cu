@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kPrepThreads) pref_pairs_kernel(PrefPairParams
     __shared__ Sum2 s_loss[kPrepThreads / 32];
     __shared__ int s_last;
     const int j = blockIdx.x, P = p.S / 2;
+    grid_dependency_wait();  // the log-probs
     if (j == 0 && threadIdx.x < 8) p.tickets[threadIdx.x] = 0;
     const int h = threadIdx.x / kHalf, lane = threadIdx.x & 31, warp = (threadIdx.x % kHalf) / 32;
     {
@@ -244,8 +245,17 @@ cudaError_t launch_distill_prep(const DistillPrepParams &p, cudaStream_t stream)
 }
 
 cudaError_t launch_pref_pairs(const PrefPairParams &p, cudaStream_t stream) {
-    pref_pairs_kernel<<<p.S / 2, kPrepThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    // begins while the log-prob pass of the same call ends
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.S / 2));
+    cfg.blockDim = dim3(kPrepThreads);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pref_pairs_kernel, p);
 }
 
 }  // namespace rlk

@@ -448,9 +448,6 @@ __device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail
     return __any_sync(0xffffffffu, dup);
 }
 
-// Waits for the launches before this one where it began while they ran.
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 template <typename T, int OP, bool kEnt>
 __global__ void __launch_bounds__(kRowThreads, kRowBlocks)
 ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __grid_constant__ RowPlan plan, int nclusters) {
