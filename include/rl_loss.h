@@ -392,8 +392,8 @@ RL_LOSS_API rl_status rl_topk(const rl_topk_config *config, int32_t rows, const 
  * -inf logit has probability 0; dlogits may alias logits when the strides are
  * equal, its columns >= V are not written; rows with mask = 0 are not read (NaN
  * or inf in them changes nothing) and get zero gradients. Softmax statistics
- * are held in fp32, sums over tokens in fp64, all in an order that depends only
- * on the sizes, so results repeat bit for bit. Nothing is allocated and no call
+ * are held in fp32, sums over tokens in two fp32 parts (about 48 bits), all in an
+ * order that depends only on the sizes, so results repeat bit for bit. Nothing is allocated and no call
  * synchronises; every call can be captured into a CUDA graph. Argument errors
  * are returned before anything is launched. `device_status` (optional, device
  * uint32) receives RL_ERR_TARGET_RANGE, RL_ERR_NONFINITE, RL_ERR_EMPTY_SEQ and
@@ -514,7 +514,8 @@ RL_LOSS_API size_t rl_loss_preference_workspace_bytes(int32_t num_tokens, int32_
  * logp [T] (0 for mask = 0), seq_logratio [S] = s_i and pair_loss [S / 2].
  * `workspace` as for rl_loss_distill, of rl_loss_preference_workspace_bytes.
  * Errors: RL_ERR_INVALID_ARG, RL_ERR_DTYPE, RL_ERR_SHAPE (S < 2 or odd, T < 0, V,
- * a stride), RL_ERR_CAPACITY, RL_ERR_ALIGNMENT. */
+ * a stride), RL_ERR_CAPACITY, RL_ERR_ALIGNMENT. Three launches; the logits are
+ * read twice, as a pair's coefficients need all of its tokens. */
 RL_LOSS_API rl_status rl_loss_preference(const rl_loss_pref_config *config, int32_t num_tokens, int32_t num_seqs,
                                          const void *logits, int64_t ld_logits, const int32_t *targets,
                                          const float *logp_ref, const uint8_t *mask, const int32_t *cu_seqlens,
