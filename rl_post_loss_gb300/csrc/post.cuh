@@ -645,10 +645,18 @@ struct DistillRow {
     bool rest;             // there are entries outside
 };
 
-// Statistics of the student over the teacher's entries, by one warp. s_z[k] holds the student's
-// logit at entry k (-inf where the entry is padding).
-__device__ __forceinline__ void distill_entry_stats(const float *s_z, int K, float c, float &M, float &S) {
-    const int lane = threadIdx.x & 31;
+// What a row's entries give before the rest of the row is known, by one warp.
+struct DistillEntries {
+    float m, s;            // the student's statistics over the teacher's entries
+    float shift;           // reverse: ln of the mass that they are taken to have, see distill_reverse
+    float f, mass, a;      // reverse: sums of p k3(x), p and p x at that mass
+    float lqo;             // ln q_o
+};
+
+// s_z[k] holds the student's logit at entry k (-inf where the entry is padding), s_lq[k] the teacher's log-prob.
+__device__ __forceinline__ DistillEntries distill_entries(const DistillParams &p, const float *s_z, const float *s_lq, float4 rec) {
+    const int lane = threadIdx.x & 31, K = p.K;
+    DistillEntries e{};
     float m = -FLT_MAX;
 #pragma unroll 4
     for (int k = lane; k < K; k += 32) m = fmaxf(m, s_z[k]);
@@ -656,53 +664,92 @@ __device__ __forceinline__ void distill_entry_stats(const float *s_z, int K, flo
     for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
     float s = 0.f;
 #pragma unroll 4
-    for (int k = lane; k < K; k += 32) s += ex2_approx((s_z[k] - m) * c);
+    for (int k = lane; k < K; k += 32) s += ex2_approx((s_z[k] - m) * p.c);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, off));
-    M = m;
-    S = s;
+    e.m = m;
+    e.s = s;
+    if (!p.reverse) return e;
+    e.lqo = logf(rec.z);
+    e.mass = s != 0.f ? fmaxf(1.f + rec.w - rec.z, 1e-6f) : 0.f;
+    e.shift = s != 0.f ? logf(e.mass) : 0.f;
+    const float ls = logf(s) - e.shift, r = e.mass / s;
+    float f = 0.f, a = 0.f;
+#pragma unroll 4
+    for (int k = lane; k < K; k += 32) {
+        const float d = s_z[k] - m, lq = s_lq[k], pk = s != 0.f ? ex2_approx(d * p.c) * r : 0.f;
+        if (pk != 0.f) {  // (a NaN too)
+            const float x = (d * p.inv_tau - ls) - lq;
+            f += pk * post_k3(x);
+            a += pk * x;
+        } else {
+            f += expf(lq);
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        f = __fadd_rn(f, __shfl_xor_sync(0xffffffffu, f, off));
+        a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
+    }
+    e.f = f;
+    e.a = a;
+    return e;
 }
 
-// The row's divergence, by one warp. Its terms h ln(h / o) (h the distribution the mean is over, o the
-// other one) nearly cancel for a student near its teacher. With the masses added and taken away,
+// The row's divergence: its terms h ln(h / o) (h the distribution the mean is over, o the other one) nearly
+// cancel for a student near its teacher. With the masses added and taken away,
 //   sum h ln(h / o) = sum [h ln(h / o) - h + o] + sum h - sum o = sum h k3(ln(h / o)) + sum h - sum o,
 // k3(d) = e^{-d} - 1 + d: no term is negative, and an error e of a logarithm enters as h (1 - o / h) e
 // and not as h e; a common one cancels. The difference of the masses is Q - 1, known in 64 bits; where
 // h = 0 the term is o.
-__device__ __forceinline__ float distill_kl(const DistillParams &p, const DistillRow &r, const float *s_z, const float *s_lq,
-                                            float4 rec) {
+
+// Forward, by one warp.
+__device__ __forceinline__ float distill_forward(const DistillParams &p, const DistillRow &r, const float *s_z, const float *s_lq,
+                                                 float4 rec) {
     const int lane = threadIdx.x & 31;
     float sum = 0.f;
-    if (p.reverse) {
 #pragma unroll 4
-        for (int k = lane; k < p.K; k += 32) {
-            const float d = s_z[k] - r.M, lq = s_lq[k], pk = ex2_approx(d * p.c) * r.inv_s;
-            sum += pk != 0.f ? pk * post_k3((d * p.inv_tau - r.ls) - lq) : expf(lq);
-        }
-    } else {
-#pragma unroll 4
-        for (int k = lane; k < p.K; k += 32) {
-            const float d = s_z[k] - r.M, lq = s_lq[k], q = expf(lq);
-            sum += q != 0.f ? q * post_k3(lq - (d * p.inv_tau - r.ls)) : ex2_approx(d * p.c) * r.inv_s;
-        }
+    for (int k = lane; k < p.K; k += 32) {
+        const float d = s_z[k] - r.M, lq = s_lq[k], q = expf(lq);
+        sum += q != 0.f ? q * post_k3(lq - (d * p.inv_tau - r.ls)) : ex2_approx(d * p.c) * r.inv_s;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
     float gap = rec.w;  // sum q - sum p
     if (p.tail && r.rest) {
-        const float lqo = logf(rec.z), h = p.reverse ? r.po : rec.z;
-        sum += h != 0.f ? h * post_k3(p.reverse ? r.lpo - lqo : lqo - r.lpo) : (p.reverse ? rec.z : r.po);
+        const float lqo = logf(rec.z);
+        sum += rec.z != 0.f ? rec.z * post_k3(lqo - r.lpo) : r.po;
     } else if (p.tail) {
         gap -= rec.z;  // the entries are the whole vocabulary: there is no further outcome
     } else {
         sum += r.po;   // outside, q = 0
     }
-    return p.reverse ? sum - gap : sum + gap;
+    return sum + gap;
+}
+
+// Reverse, which the gradient waits for. The sum over the entries is made before the rest of the row is known,
+// as if the student gave them the mass that the teacher does, p' (x' = ln(p' / q)). With their true mass
+// p = p' e^{-y}, x = x' - y:
+//   sum p k3(x) = sum p' k3(x') + (sum p') (y (1 - e^{-y}) - k3(y)) - (sum p' x') (1 - e^{-y}).
+// y is near 0 where the student is near its teacher, so there the two last terms are small of second order, as
+// the first one is. in, out: the student's sums over the entries and outside, to one reference.
+__device__ __forceinline__ float distill_reverse(const DistillRow &r, const DistillEntries &e, float in, float out, float4 rec) {
+    float sum;
+    const float y = e.shift + log1pf(out / in);
+    if (in == 0.f || y > 80.f) {  // e^{-y} = 0
+        sum = e.f + e.mass - e.a;
+    } else {
+        const float u = -expm1f(-y);
+        sum = e.f + (e.mass * (y * u - post_k3(y)) - e.a * u);
+    }
+    float gap = rec.w;
+    if (r.rest) sum += r.po != 0.f ? r.po * post_k3(r.lpo - e.lqo) : rec.z;
+    else gap -= rec.z;
+    return sum - gap;
 }
 
 // The row's coefficients, by one warp. `tail` are the statistics of the vocabulary outside the
-// teacher's entries, Mk and Sk those of the entries (distill_entry_stats), s_lq[k] the teacher's
-// log-prob of entry k, rec of distill_prep, w the row's weight * scale / tau, n_rest the number of
+// teacher's entries, e what the entries give, rec of distill_prep, w the row's weight * scale / tau, n_rest the number of
 // vocabulary entries outside the teacher's.
 //
 // With q_o = rec.z the teacher's remaining mass, p_o the student's and Q = sum q + q_o (forward, the
@@ -712,15 +759,15 @@ __device__ __forceinline__ float distill_kl(const DistillParams &p, const Distil
 // renormalised: q_o = 0, Q = 1. Reverse:
 //   KL = sum_k p_k a_k + p_o a_o,  a = ln(p / q),  dKL/dz'_v = p_v (a_v - KL), a_v = a_o outside.
 // p_o is the sum of the entries outside, not 1 - sum_k p_k, which would cancel.
-__device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, PostStats tail, float Mk, float Sk,
-                                                     const float *s_z, const float *s_lq, float4 rec, float w, int n_rest) {
+__device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, PostStats tail, const DistillEntries &e, float4 rec,
+                                                     float w, int n_rest) {
     DistillRow r;
     r.w = w;
     r.Q = 1.f + rec.w;
     r.m = tail.m;
-    r.M = fmaxf(Mk, tail.m);
+    r.M = fmaxf(e.m, tail.m);
     const float ft = exp2f((tail.m - r.M) * p.c);
-    const float S = __fadd_rn(__fmul_rn(Sk, exp2f((Mk - r.M) * p.c)), __fmul_rn(tail.s, ft));
+    const float in = __fmul_rn(e.s, exp2f((e.m - r.M) * p.c)), out = __fmul_rn(tail.s, ft), S = __fadd_rn(in, out);
     r.inv_s = 1.f / S;
     r.ls = logf(S);
     r.rest = n_rest > 0;
@@ -730,8 +777,8 @@ __device__ __forceinline__ DistillRow distill_finish(const DistillParams &p, Pos
     r.kl = 0.f;
     const bool bucket = p.tail && r.rest;
     if (p.reverse) {  // the gradient needs the divergence
-        r.kl = distill_kl(p, r, s_z, s_lq, rec);
-        const float a = bucket ? r.lpo - logf(rec.z) : 0.f;
+        r.kl = distill_reverse(r, e, in, out, rec);
+        const float a = bucket ? r.lpo - e.lqo : 0.f;
         r.ct = tail.s > 0.f ? (a - r.kl) * ft * r.inv_s : 0.f;
     } else {
         r.ct = r.Q * ft * r.inv_s;

@@ -661,9 +661,9 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             RowFin &fin = sh.fin[ms];
             const bool read = meta.read;
             const float *s_z = s_meta + (size_t)ms * 3 * K, *s_lq = s_z + K;
-            float Mk = 0.f, Sk = 0.f;
+            DistillEntries entries{};
             if constexpr (OP == kOpDistill)
-                if (read) distill_entry_stats(s_z, K, c, Mk, Sk);
+                if (read) entries = distill_entries(p, s_z, s_lq, meta.rec);
             row_wait(sh, &sh.part_full[ms], use(r), p.r.status);
             PostStats st{0.f, 1.f, 0.f};
             int dup = 0;
@@ -723,13 +723,13 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             } else if constexpr (OP == kOpDistill) {
                 const bool live = read && !dup;
                 DistillRow row{};
-                if (live) row = distill_finish(p, st, Mk, Sk, s_z, s_lq, meta.rec, meta.w * p.scale * p.inv_tau, V - meta.have);
+                if (live) row = distill_finish(p, st, entries, meta.rec, meta.w * p.scale * p.inv_tau, V - meta.have);
                 if (lane == 0) {
                     fin.grad = RowGrad{live ? row.ct : 0.f, row.m, 0.f, live ? 0 : -1};
                     ptx::mbar_arrive(ptx::smem_u32(&sh.fin_full[ms]));
                 }
                 if (writes) {
-                    const float kl = !live ? 0.f : p.reverse ? row.kl : distill_kl(p, row, s_z, s_lq, meta.rec);
+                    const float kl = !live ? 0.f : p.reverse ? row.kl : distill_forward(p, row, s_z, s_lq, meta.rec);
                     if (lane == 0) {
                         const bool bad = meta.bad || dup;
                         if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
@@ -1088,10 +1088,8 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
             continue;
         }
         if (threadIdx.x < 32) {
-            float Mk, Sk;
-            distill_entry_stats(s_z, p.K, p.c, Mk, Sk);
-            const DistillRow r = distill_finish(p, st, Mk, Sk, s_z, s_lq, rec, w * p.scale * p.inv_tau, V - have);
-            const float kl = p.reverse ? r.kl : distill_kl(p, r, s_z, s_lq, rec);
+            const DistillRow r = distill_finish(p, st, distill_entries(p, s_z, s_lq, rec), rec, w * p.scale * p.inv_tau, V - have);
+            const float kl = p.reverse ? r.kl : distill_forward(p, r, s_z, s_lq, rec);
             if (threadIdx.x == 0) {
                 s_row = r;
                 if (!isfinite(r.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
