@@ -442,7 +442,6 @@ __device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail
             if (at[id - lo] == (Tag)k) at[id - lo] = VT::kNegInf;
             else dup = true;
         }
-        ptx::fence_proxy_async_smem();  // the next copy into the segment comes after the marks
         __syncwarp();
     }
     return __any_sync(0xffffffffu, dup);
@@ -786,7 +785,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                         const int ks = ky - (j * kWarps + warp) * plan.seg;
                         if (ky >= 0 && ks >= 0 && ks < g && (ks & 31) == lane) {
                             reinterpret_cast<volatile typename VT::Tag *>(seg + ks)[y % VEC] = VT::kNegInf;
-                            ptx::fence_proxy_async_smem();  // the next copy into the segment comes after this
+                            if (!kGrad) ptx::fence_proxy_async_smem();  // the next copy into the segment comes after this
                         }
                     }
                     if constexpr (OP == kOpDistill)
@@ -866,6 +865,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                     if (OP != kOpDistill && ky >= 0 && ks >= 0 && ks < g && (ks & 31) == lane) VT::store1(dz, gr.y, gr.gy);
                 }
                 if (in_ring) {
+                    if (kStats) ptx::fence_proxy_async_smem();  // the next copy comes after the fold's marks in the segment
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&s_empty[db * kWarps + warp]));
                     next(db, phase_b);
