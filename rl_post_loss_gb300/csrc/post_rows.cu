@@ -405,17 +405,28 @@ __device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail
     using Tag = typename VT::Tag;
     constexpr int VEC = VT::kElems;
     const int lane = threadIdx.x & 31;
-    volatile Tag *at = reinterpret_cast<volatile Tag *>(seg);
+    Tag *at = reinterpret_cast<Tag *>(seg);
     const int lo = v0 * VEC, hi = (v0 + g) * VEC;
+    constexpr int U = 4;  // entries of a lane at once: their loads and stores go out together
+    // the places of this lane's entries k, k + 32, ... in the segment, -1: none
+    auto places = [&](int k, int (&at_k)[U]) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int id = k + 32 * i < K ? s_id[k + 32 * i] : -1;
+            at_k[i] = id >= lo && id < hi ? id - lo : -1;
+        }
+    };
     bool dup = false, any = false;
     uint32_t mine = 0;
-#pragma unroll 4
-    for (int k = lane; k < K; k += 32) {
-        const int id = s_id[k];
-        if (id >= lo && id < hi) {
-            at[id - lo] = (Tag)k;
-            any = true;
-        }
+    for (int k = lane; k < K; k += 32 * U) {
+        int at_k[U];
+        places(k, at_k);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (at_k[i] >= 0) {
+                at[at_k[i]] = (Tag)(k + 32 * i);
+                any = true;
+            }
     }
     tail = 0;
     if (tail0 >= 0) {
@@ -435,12 +446,17 @@ __device__ __forceinline__ bool mark_entries(uint4 *seg, int v0, int g, int tail
     }
     if (__any_sync(0xffffffffu, any)) {
         __syncwarp();
-#pragma unroll 4
-        for (int k = lane; k < K; k += 32) {
-            const int id = s_id[k];
-            if (id < lo || id >= hi) continue;
-            if (at[id - lo] == (Tag)k) at[id - lo] = VT::kNegInf;
-            else dup = true;
+        for (int k = lane; k < K; k += 32 * U) {
+            int at_k[U];
+            bool lost[U];
+            places(k, at_k);
+#pragma unroll
+            for (int i = 0; i < U; ++i) lost[i] = at_k[i] >= 0 && at[at_k[i]] != (Tag)(k + 32 * i);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (at_k[i] >= 0 && !lost[i]) at[at_k[i]] = VT::kNegInf;
+                dup |= lost[i];
+            }
         }
         __syncwarp();
     }
