@@ -479,21 +479,23 @@ __device__ __forceinline__ PostToken post_target(PostStats rest, float zy) {
 
 __device__ __forceinline__ float post_entropy(PostStats st) { return logf(st.s) - st.u / st.s * kLn2; }
 
-// e^{-d} - 1 + d >= 0. Its terms cancel near 0, where its series is summed instead (|d| < 1/4:
-// 1/2 - d/6 + ... times d^2, the first term left out is d^8 / 10! < 5e-12).
+// e^{-d} - 1 + d >= 0. Its terms cancel near 0, where its series is summed instead (|d| < 1:
+// 1/2 - d/6 + ... times d^2, the first term left out is below 2 d / 13! of it). Both are worked out, without a
+// branch, so that calls for several entries overlap.
 __device__ __forceinline__ float post_k3(float d) {
-    if (fabsf(d) < 0.25f) {
-        float q = 1.f / 362880.f;
-        q = fmaf(-d, q, 1.f / 40320.f);
-        q = fmaf(-d, q, 1.f / 5040.f);
-        q = fmaf(-d, q, 1.f / 720.f);
-        q = fmaf(-d, q, 1.f / 120.f);
-        q = fmaf(-d, q, 1.f / 24.f);
-        q = fmaf(-d, q, 1.f / 6.f);
-        q = fmaf(-d, q, 0.5f);
-        return d * d * q;
-    }
-    return expm1f(-d) + d;
+    float q = 1.f / 479001600.f;
+    q = fmaf(-d, q, 1.f / 39916800.f);
+    q = fmaf(-d, q, 1.f / 3628800.f);
+    q = fmaf(-d, q, 1.f / 362880.f);
+    q = fmaf(-d, q, 1.f / 40320.f);
+    q = fmaf(-d, q, 1.f / 5040.f);
+    q = fmaf(-d, q, 1.f / 720.f);
+    q = fmaf(-d, q, 1.f / 120.f);
+    q = fmaf(-d, q, 1.f / 24.f);
+    q = fmaf(-d, q, 1.f / 6.f);
+    q = fmaf(-d, q, 0.5f);
+    const float far = (expf(-d) - 1.f) + d;
+    return fabsf(d) < 1.f ? d * d * q : far;
 }
 
 // Estimators of KL(pi || pi_ref) from the sampled token, d = logp - logp_ref, and their derivative
@@ -678,13 +680,9 @@ __device__ __forceinline__ DistillEntries distill_entries(const DistillParams &p
 #pragma unroll 4
     for (int k = lane; k < K; k += 32) {
         const float d = s_z[k] - m, lq = s_lq[k], pk = s != 0.f ? ex2_approx(d * p.c) * r : 0.f;
-        if (pk != 0.f) {  // (a NaN too)
-            const float x = (d * p.inv_tau - ls) - lq;
-            f += pk * post_k3(x);
-            a += pk * x;
-        } else {
-            f += expf(lq);
-        }
+        const float x = (d * p.inv_tau - ls) - lq, q = expf(lq), k3 = pk * post_k3(x), px = pk * x;
+        f += pk != 0.f ? k3 : q;  // (a NaN too)
+        a += pk != 0.f ? px : 0.f;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
@@ -711,7 +709,8 @@ __device__ __forceinline__ float distill_forward(const DistillParams &p, const D
 #pragma unroll 4
     for (int k = lane; k < p.K; k += 32) {
         const float d = s_z[k] - r.M, lq = s_lq[k], q = expf(lq);
-        sum += q != 0.f ? q * post_k3(lq - (d * p.inv_tau - r.ls)) : ex2_approx(d * p.c) * r.inv_s;
+        const float k3 = q * post_k3(lq - (d * p.inv_tau - r.ls)), pk = ex2_approx(d * p.c) * r.inv_s;
+        sum += q != 0.f ? k3 : pk;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));

@@ -38,6 +38,18 @@ __device__ __forceinline__ void add_partial(PostPartial &a, const PostPartial &q
     a.masked += q.masked;
 }
 
+// A row's term, with its flags.
+__device__ __forceinline__ void add_row(PostPartial &a, const PostTerm &v, uint32_t f) {
+    const bool m = !(f & RL_FLAG_MASKED);
+    a.loss.add(v.loss, v.loss_lo);
+    a.ent.add(v.ent, 0.f);
+    a.kl.add(v.kl, 0.f);
+    a.n += m;
+    a.masked += !m;
+    a.popped += m && !(f & RL_FLAG_POP_IN_BOUNDS);
+    a.clipped += m && (f & RL_FLAG_CLIP_ACTIVE);
+}
+
 __device__ __forceinline__ Sum2 shfl_xor(const Sum2 &s, int off) {
     return Sum2{__shfl_xor_sync(0xffffffffu, s.hi, off), __shfl_xor_sync(0xffffffffu, s.lo, off)};
 }
@@ -86,18 +98,12 @@ __device__ __forceinline__ void write_loss(const P &p, const PostPartial &a) {
     }
 }
 
-// Counts `n` rows of a chunk whose terms this warp has written. The warp that counts a chunk's last row
-// sums the chunk, and the one that sums the last chunk writes the batch's results.
+// Sums a chunk whose terms are all written. The warp that sums the last chunk writes the batch's results.
 template <typename P>
-__device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
+__device__ __forceinline__ void sum_chunk(const P &p, int chunk) {
     const int lane = threadIdx.x & 31, T = p.r.T;
     const int c0 = chunk * kSumRows, c1 = min(T, c0 + kSumRows), chunks = (T + kSumRows - 1) / kSumRows;
     int last = 0;
-    if (lane == 0) {
-        __threadfence();
-        last = atomicAdd(p.r.counters + kCountChunks + chunk, (uint32_t)n) == (uint32_t)(c1 - c0 - n);
-    }
-    if (!__shfl_sync(0xffffffffu, last, 0)) return;
     __threadfence();
     PostPartial a{};
 #pragma unroll
@@ -106,14 +112,7 @@ __device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
         if (k >= c1) continue;
         const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.r.terms + k));
         const uint32_t f = p.r.term_flags ? __ldcg(p.r.term_flags + k) : RL_FLAG_MASKED;
-        const bool m = !(f & RL_FLAG_MASKED);
-        a.loss.add(v.x, v.y);
-        a.ent.add(v.z, 0.f);
-        a.kl.add(v.w, 0.f);
-        a.n += m;
-        a.masked += !m;
-        a.popped += m && !(f & RL_FLAG_POP_IN_BOUNDS);
-        a.clipped += m && (f & RL_FLAG_CLIP_ACTIVE);
+        add_row(a, PostTerm{v.x, v.y, v.z, v.w}, f);
     }
     a = warp_sum(a);
     if (lane == 0) {
@@ -129,6 +128,18 @@ __device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
         add_partial(a, PostPartial{{q.loss.hi, q.loss.lo}, {q.ent.hi, q.ent.lo}, {q.kl.hi, q.kl.lo}, q.n, q.popped, q.clipped, q.masked});
     }
     write_loss(p, warp_sum(a));
+}
+
+// Counts `n` rows of a chunk whose terms this warp has written; the warp that counts a chunk's last row sums it.
+template <typename P>
+__device__ __forceinline__ void count_rows(const P &p, int chunk, int n) {
+    const int rows = min(p.r.T, (chunk + 1) * kSumRows) - chunk * kSumRows;
+    int last = 0;
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence();
+        last = atomicAdd(p.r.counters + kCountChunks + chunk, (uint32_t)n) == (uint32_t)(rows - n);
+    }
+    if (__shfl_sync(0xffffffffu, last, 0)) sum_chunk(p, chunk);
 }
 
 // The rows of one chunk that a warp has written and not yet counted: counting takes a fence and an atomic,
@@ -230,6 +241,40 @@ struct RowMeta<kOpScale> {
     int32_t read;
     RowGrad grad;
 };
+
+// The results of row t of the log-prob pass, by one thread.
+template <bool kEnt>
+__device__ __forceinline__ void logp_write(const LogpParams &p, const RowMeta<kOpLogp> &meta, PostStats st, int t) {
+    float logp = 0.f, ent = 0.f;
+    if (meta.read) {
+        logp = __int_as_float(0x7fc00000);
+        if (meta.y >= 0) {
+            const PostToken tok = post_target<kEnt>(st, meta.zy);
+            st = tok.all;
+            logp = tok.logp;
+        } else {
+            post_raise(p.r.status, RL_ERR_TARGET_RANGE);
+        }
+        if (!post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
+        if (kEnt) ent = post_entropy(st);
+    }
+    p.r.logp[t] = logp;
+    if (kEnt) p.r.entropy[t] = ent;
+    if (p.stats) p.stats[t] = make_float2(st.m, st.s);
+}
+
+// The results of a distilled row t, by one warp, and its term of the loss.
+__device__ __forceinline__ PostTerm distill_write(const DistillParams &p, const RowMeta<kOpDistill> &meta, int t, bool live, bool dup,
+                                                  const DistillRow &row, float kl) {
+    if ((threadIdx.x & 31) == 0) {
+        const bool bad = meta.bad || dup;
+        if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
+        if (live && !isfinite(row.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
+        if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : kl;
+    }
+    __syncwarp();
+    return PostTerm{live ? meta.w * p.scale * kl : 0.f, 0.f, 0.f, 0.f};
+}
 
 struct alignas(16) RowMsg {  // sent by one 16-byte store
     float m, s, u;
@@ -365,24 +410,52 @@ __device__ __forceinline__ RowMeta<OP> load_meta(const typename OpParams<OP>::ty
     return m;
 }
 
+// distill: a row's first entries in registers, loaded while the row before is gathered: the ids and the logits
+// there are two dependent loads.
+struct NextEntries {
+    static constexpr int kLane = 4;
+    int id[kLane];
+    float val[kLane];
+};
+__device__ __forceinline__ void next_entries(const DistillParams &p, int t, NextEntries &e) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < NextEntries::kLane; ++i) {
+        const int k = lane + 32 * i;
+        e.id[i] = k < p.K ? __ldg(p.ids + (int64_t)t * p.ldk + k) : -1;
+        e.val[i] = k < p.K ? __ldg(p.vals + (int64_t)t * p.ldk + k) : 0.f;
+    }
+}
+
 // distill: the teacher's entries of row t and the student's logits there, by the producer warp.
 template <typename T>
-__device__ __forceinline__ void load_entries(const DistillParams &p, int t, RowMeta<kOpDistill> &m, float *s_z, float *s_lq, int *s_id) {
+__device__ __forceinline__ void load_entries(const DistillParams &p, int t, const NextEntries &e, RowMeta<kOpDistill> &m, float *s_z,
+                                             float *s_lq, int *s_id) {
     using VT = PostVec<T>;
+    constexpr int U = NextEntries::kLane;
     const int lane = threadIdx.x & 31;
     const char *z = row_in<T>(p.r, t);
     const float4 rec = m.rec;
     int bad = 0, have = 0;
-#pragma unroll 4
-    for (int k = lane; k < p.K; k += 32) {
-        const int id = __ldg(p.ids + (int64_t)t * p.ldk + k);
-        const float val = __ldg(p.vals + (int64_t)t * p.ldk + k);
+    auto put = [&](int k, int id, float val, float zk) {
         const bool real = id >= 0 && id < p.r.V;
         bad |= id < -1 || id >= p.r.V;
         have += real;
         s_id[k] = real ? id : -1;
-        s_z[k] = real ? VT::load1(z, id) : -INFINITY;
+        s_z[k] = zk;
         s_lq[k] = real ? (val - rec.x) - rec.y : -INFINITY;
+    };
+    auto logit = [&](int id) { return id >= 0 && id < p.r.V ? VT::load1(z, id) : -INFINITY; };
+    float zk[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) zk[i] = logit(e.id[i]);
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+        if (lane + 32 * i < p.K) put(lane + 32 * i, e.id[i], e.val[i], zk[i]);
+#pragma unroll 4
+    for (int k = lane + 32 * U; k < p.K; k += 32) {
+        const int id = __ldg(p.ids + (int64_t)t * p.ldk + k);
+        put(k, id, __ldg(p.vals + (int64_t)t * p.ldk + k), logit(id));
     }
     have = warp_sum_i32(have);
     bad = __any_sync(0xffffffffu, bad);
@@ -571,11 +644,17 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
         auto row_of = [&](int k) { return OP == kOpScale ? T_ - 1 - k : kDynamic ? k : q + k * nclusters; };
         RowMeta<OP> mine{};  // the record of the ticket's row `lane`
         int row0 = 0, left = 0, at = 0;
+        NextEntries entries;
+        auto entries_ahead = [&] {  // of the ticket's next row
+            if constexpr (OP == kOpDistill)
+                if (at < left) next_entries(p, row_of(row0 + at), entries);
+        };
         auto fetch = [&] {
             const int64_t first = (int64_t)take() * plan.rows;
             left = first < n_rows ? min(plan.rows, n_rows - (int)first) : 0;
             row0 = (int)first;
             at = 0;
+            entries_ahead();
             if (lane < left) mine = load_meta<T, OP>(p, row_of(row0 + lane), N);
         };
         fetch();
@@ -601,7 +680,8 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
             if (lane == 0) sh.meta[ms].last = at == left;
             if constexpr (OP == kOpDistill) {
                 __syncwarp();
-                if (read) load_entries<T>(p, t, sh.meta[ms], mz, mz + K, s_id);
+                if (read) load_entries<T>(p, t, entries, sh.meta[ms], mz, mz + K, s_id);
+                entries_ahead();
             }
             if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.mfull[ms]));
             const bool more = at == left;
@@ -704,24 +784,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 }
             }
             if constexpr (OP == kOpLogp) {
-                if (lane == 0 && writes) {
-                    float logp = 0.f, ent = 0.f;
-                    if (read) {
-                        logp = __int_as_float(0x7fc00000);
-                        if (meta.y >= 0) {
-                            const PostToken tok = post_target<kEnt>(st, meta.zy);
-                            st = tok.all;
-                            logp = tok.logp;
-                        } else {
-                            post_raise(p.r.status, RL_ERR_TARGET_RANGE);
-                        }
-                        if (!post_finite(st)) post_raise(p.r.status, RL_ERR_NONFINITE);
-                        if (kEnt) ent = post_entropy(st);
-                    }
-                    p.r.logp[t] = logp;
-                    if (kEnt) p.r.entropy[t] = ent;
-                    if (p.stats) p.stats[t] = make_float2(st.m, st.s);
-                }
+                if (lane == 0 && writes) logp_write<kEnt>(p, meta, st, t);
             } else if constexpr (OP == kOpPolicy) {
                 PostTerm term{};
                 if (lane == 0) {
@@ -745,14 +808,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 }
                 if (writes) {
                     const float kl = !live ? 0.f : p.reverse ? row.kl : distill_forward(p, row, s_z, s_lq, meta.rec);
-                    if (lane == 0) {
-                        const bool bad = meta.bad || dup;
-                        if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);
-                        if (live && !isfinite(row.ls)) post_raise(p.r.status, RL_ERR_NONFINITE);
-                        if (p.kl) p.kl[t] = bad ? __int_as_float(0x7fc00000) : kl;
-                    }
-                    __syncwarp();
-                    add_term(p, pend, t, PostTerm{live ? meta.w * p.scale * kl : 0.f, 0.f, 0.f, 0.f});
+                    add_term(p, pend, t, distill_write(p, meta, t, live, dup, row, kl));
                 }
                 if (meta.last) flush_rows(p, pend);
                 if (r > 0) write_entries(r - 1);
@@ -914,6 +970,224 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
         if (T_ == 0 && blockIdx.x == 0 && warp == 0) write_loss(p, PostPartial{});
     }
     if (kStats && C > 1) ptx::cluster_sync();  // no CTA leaves while another may still write to it
+}
+
+// ---------------------------------------------------------------- short rows
+
+constexpr int kLineWarps = 4;                   // rows of a block at once
+constexpr int kLineBlocks = 6;                  // blocks on an SM
+constexpr int kLineBytes = 24576;               // the longest row that takes this way
+
+// The batch's sums from those of the warps: of a block's in their order, then of the blocks' by the block that
+// comes last. A block's takes the place of three rows' terms, of which there are as many. (Chunks of rows as in
+// the ring kernel would each be summed by the warp that comes last there: one slow warp, for all its rows. They
+// took 45 us of 140.)
+template <typename P>
+__device__ __forceinline__ void line_sums(const P &p, const PostPartial &mine) {
+    __shared__ PostPartial s_sum[kLineWarps];
+    __shared__ int s_last;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = gridDim.x;
+    static_assert(sizeof(PostPartial) <= 3 * sizeof(PostTerm), "");
+    auto block_total = [&](const PostPartial &a) {  // in the first thread
+        if (lane == 0) s_sum[warp] = a;
+        __syncthreads();
+        PostPartial b{};
+        if (threadIdx.x == 0)
+            for (int w = 0; w < kLineWarps; ++w) add_partial(b, s_sum[w]);
+        return b;
+    };
+    PostPartial a = block_total(mine);
+    if (blocks > 1) {
+        auto place = [&](int b) { return reinterpret_cast<PostPartial *>(p.r.terms + 3 * (size_t)b); };
+        if (threadIdx.x == 0) {
+            *place(blockIdx.x) = a;
+            __threadfence();
+            s_last = atomicAdd(p.r.counters + kCountDone, 1u) == (uint32_t)blocks - 1;
+        }
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+        a = PostPartial{};
+        for (int b = threadIdx.x; b < blocks; b += 32 * kLineWarps) {
+            const volatile PostPartial &q = *place(b);
+            add_partial(a, PostPartial{{q.loss.hi, q.loss.lo}, {q.ent.hi, q.ent.lo}, {q.kl.hi, q.kl.lo}, q.n, q.popped, q.clipped, q.masked});
+        }
+        a = block_total(warp_sum(a));
+    }
+    if (warp == 0) write_loss(p, a);
+}
+
+// A row per warp, in shared memory: for short rows the steps between a row's warps, its finisher and its
+// producer take longer than its bytes. Two dozen warps on an SM cover one another's copies and chains.
+template <typename T, int OP, bool kEnt>
+__global__ void __launch_bounds__(32 * kLineWarps, kLineBlocks)
+line_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, int stride) {
+    using VT = PostVec<T>;
+    constexpr int VEC = VT::kElems;
+    constexpr bool kGrad = OP != kOpLogp, kFold = OP != kOpScale;
+    extern __shared__ __align__(128) uint4 s_lines[];  // [kLineWarps][stride]: a row, then the teacher's entries, [3][K]
+    __shared__ uint64_t s_bar[kLineWarps];
+    __shared__ RowMeta<OP> s_meta[kLineWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int T_ = p.r.T, V = p.r.V, nvec = V / VEC;
+    float c = kLog2e;
+    int K = 0, N = 0;
+    if constexpr (OP == kOpDistill) {
+        c = p.c;
+        K = p.K;
+    }
+    uint4 *line = s_lines + (size_t)warp * stride;
+    float *s_z = reinterpret_cast<float *>(line + nvec), *s_lq = s_z + K;
+    int *s_id = reinterpret_cast<int *>(s_z + 2 * K);
+    const uint32_t bar = ptx::smem_u32(&s_bar[warp]);
+    if (lane == 0) {
+        ptx::mbar_init(bar, 1);
+        ptx::fence_mbar_init();
+    }
+    __syncwarp();
+    grid_dependency_wait();
+    if constexpr (OP == kOpLogp)
+        if (p.zero && blockIdx.x == 0 && threadIdx.x == 0) *p.zero = 0;
+    if constexpr (OP == kOpDistill) {
+        if (p.per_token) {
+            for (int i = lane; i < p.r.S; i += 32) N += p.seq_n[i];
+            N = warp_sum_i32(N);
+        }
+    }
+    // Rows go to the warps in turn; the lanes hold the records of a warp's next 32.
+    const int W = gridDim.x * kLineWarps;
+    int64_t first = (int64_t)warp * gridDim.x + blockIdx.x;
+    auto row_of = [&](int i) { return (int)(OP == kOpScale ? T_ - 1 - (first + (int64_t)i * W) : first + (int64_t)i * W); };
+    auto count_of = [&] { return first < T_ ? (int)min((int64_t)32, (T_ - 1 - first) / W + 1) : 0; };
+    int n = count_of();
+    RowMeta<OP> mine{};
+    if (lane < n) mine = load_meta<T, OP>(p, row_of(lane), N);
+    NextEntries entries;
+    const uint64_t pol = ptx::l2_evict_first_policy();
+    auto start = [&](int i) {
+        const int t = row_of(i);
+        if constexpr (OP == kOpDistill) next_entries(p, t, entries);
+        if (nvec > 0 && __shfl_sync(0xffffffffu, mine.read, i) && lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar, (uint32_t)nvec * 16);
+            if (OP == kOpLogp && p.r.dlogits) ptx::bulk_g2s(ptx::smem_u32(line), row_in<T>(p.r, t), (uint32_t)nvec * 16, bar);  // read again
+            else ptx::bulk_g2s_hint(ptx::smem_u32(line), row_in<T>(p.r, t), (uint32_t)nvec * 16, bar, pol);
+        }
+    };
+    const int tail_v = nvec * VEC + lane;  // this lane's entry of the last V mod VEC
+    const bool has_tail = tail_v < V;
+    PostPartial sum{};  // of this warp's rows
+    uint32_t phase = 0;
+    int i = 0;
+    if (n > 0) start(0);
+    while (n > 0) {
+        const int t = row_of(i), in_line = __shfl_sync(0xffffffffu, mine.read, i);
+        RowMeta<OP> &meta = s_meta[warp];
+        if (lane == i) meta = mine;
+        __syncwarp();
+        DistillEntries de{};
+        if constexpr (OP == kOpDistill) {
+            if (meta.read) load_entries<T>(p, t, entries, meta, s_z, s_lq, s_id);
+            if (meta.read) de = distill_entries(p, s_z, s_lq, meta.rec);
+        }
+        const bool read = meta.read;
+        if (in_line && nvec > 0) {
+            const bool there = ptx::mbar_wait(bar, phase);
+            phase ^= 1;
+            if (!__all_sync(0xffffffffu, there)) {
+                if (lane == 0) {
+                    post_raise(p.r.status, RL_ERR_TIMEOUT);
+                    ptx::mbar_wait(bar, phase ^ 1);  // no copy may be in flight when the warp leaves
+                }
+                break;
+            }
+        }
+        // the statistics
+        PostStats st{0.f, 1.f, 0.f};
+        bool dup = false;
+        uint32_t marks = 0;
+        int y = -1;
+        if constexpr (OP == kOpLogp || OP == kOpPolicy) y = meta.y;
+        if (kFold && read) {
+            const int ky = y >= 0 && y < nvec * VEC ? y / VEC : -1;
+            if (ky >= 0 && (ky & 31) == lane)  // the lane that folds the sampled entry's group takes the entry out of it
+                reinterpret_cast<volatile typename VT::Tag *>(line + ky)[y % VEC] = VT::kNegInf;
+            if constexpr (OP == kOpDistill) dup = mark_entries<T>(line, 0, nvec, nvec * VEC < V ? nvec * VEC : -1, s_id, K, marks);
+            PostAcc acc = post_acc();
+            for (int k = lane; k - lane < nvec; k += 32 * kBatch) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) v[b] = k + 32 * b < nvec ? line[k + 32 * b] : VT::none();
+                post_fold_groups<T, kEnt>(acc, v, c);
+            }
+            st = acc.stats();
+            if (has_tail && tail_v != y && !((marks >> lane) & 1)) {
+                const float x[1] = {VT::load1(row_in<T>(p.r, t), tail_v)};
+                post_fold<kEnt>(st, x, c);
+            }
+            st = post_warp_merge<kEnt>(st, c);
+        }
+        // the row's results
+        RowGrad gr{0.f, 0.f, 0.f, -1};
+        DistillRow row{};
+        const bool live = read && !dup;
+        if constexpr (OP == kOpLogp) {
+            if (lane == 0) logp_write<kEnt>(p, meta, st, t);
+        } else if constexpr (OP == kOpPolicy) {
+            PostToken tok{st, 0.f, 0.f};
+            if (read && y >= 0) tok = post_target<kEnt>(st, meta.zy);
+            const PolicyRow pr = policy_row(p, meta.tok, tok, read);
+            gr = pr.grad;
+            if (lane == 0) add_row(sum, policy_write<kEnt>(p, t, meta.tok, tok, pr, read), pr.flags);
+        } else if constexpr (OP == kOpDistill) {
+            if (live) row = distill_finish(p, st, de, meta.rec, meta.w * p.scale * p.inv_tau, V - meta.have);
+            gr = RowGrad{live ? row.ct : 0.f, row.m, 0.f, live ? 0 : -1};
+            const float kl = !live ? 0.f : p.reverse ? row.kl : distill_forward(p, row, s_z, s_lq, meta.rec);
+            const PostTerm term = distill_write(p, meta, t, live, dup, row, kl);
+            if (lane == 0) add_row(sum, term, 0);
+        } else {
+            gr = meta.grad;
+        }
+        // the gradient
+        if (kGrad) {
+            char *dz = row_out<T>(p.r, t);
+            uint4 *to = reinterpret_cast<uint4 *>(dz);
+            const bool zero = gr.y < 0;
+            if (zero) {
+                for (int k = lane; k < nvec; k += 32) __stcs(to + k, make_uint4(0, 0, 0, 0));
+            } else {
+                int k = lane;
+                for (; k - lane + 32 * kBatch <= nvec; k += 32 * kBatch) {
+                    uint4 v[kBatch];
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) v[b] = line[k + 32 * b];
+#pragma unroll
+                    for (int b = 0; b < kBatch; ++b) __stcs(to + k + 32 * b, post_grad_group<T>(v[b], gr.a, gr.m, c));
+                }
+                for (; k < nvec; k += 32) __stcs(to + k, post_grad_group<T>(line[k], gr.a, gr.m, c));
+                if (OP != kOpDistill && gr.y < nvec * VEC && ((gr.y / VEC) & 31) == lane) VT::store1(dz, gr.y, gr.gy);
+            }
+            if (has_tail) {
+                const float e = zero ? 0.f : gr.a * ex2_approx((VT::load1(row_in<T>(p.r, t), tail_v) - gr.m) * c);
+                VT::store1(dz, tail_v, OP != kOpDistill && !zero && tail_v == gr.y ? gr.gy : e);
+            }
+            if constexpr (OP == kOpDistill) {
+                __syncwarp();  // the entries replace what the row's other lanes have written there
+                if (live)
+                    for (int k = lane; k < K; k += 32)
+                        if (s_id[k] >= 0) VT::store1(dz, s_id[k], distill_entry(p, row, s_z[k], s_lq[k]));
+            }
+        }
+        ptx::fence_proxy_async_smem();  // the next copy comes after the marks
+        __syncwarp();
+        if (++i == n) {
+            i = 0;
+            first += (int64_t)32 * W;
+            n = count_of();
+            if (lane < n) mine = load_meta<T, OP>(p, row_of(lane), N);
+        }
+        if (n > 0) start(i);
+    }
+    if constexpr (OP == kOpPolicy || OP == kOpDistill) line_sums(p, sum);
 }
 
 // ---------------------------------------------------------------- rows too long for the rings
@@ -1161,7 +1435,7 @@ cudaError_t resident_clusters(const void *kernel, const cudaLaunchConfig_t &cfg,
     } else if (e == cudaSuccess) {
         int sms = 0, per = 0;
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kRowThreads, cfg.dynamicSmemBytes);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, (int)cfg.blockDim.x, cfg.dynamicSmemBytes);
         resident = sms * per / C;
     }
     if (e != cudaSuccess) return e;
@@ -1172,11 +1446,36 @@ cudaError_t resident_clusters(const void *kernel, const cudaLaunchConfig_t &cfg,
 }
 
 template <typename T, int OP, bool kEnt>
+cudaError_t launch_lines(const typename OpParams<OP>::type &p, int K, bool after_own, cudaStream_t stream) {
+    auto kernel = line_rows_kernel<T, OP, kEnt>;
+    const int stride = p.r.V / PostVec<T>::kElems + (3 * K + 3) / 4;  // 16-byte groups of a warp
+    constexpr size_t kStatic = kLineWarps * (sizeof(RowMeta<OP>) + 16);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1);
+    cfg.blockDim = dim3(32 * kLineWarps);
+    cfg.dynamicSmemBytes = (size_t)kLineWarps * stride * 16;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = after_own ? 1 : 0;
+    int resident = 0;
+    const cudaError_t e = resident_clusters(reinterpret_cast<const void *>(kernel), cfg, 1, (int)(kCtaBytes[2] - kStatic), &resident);
+    if (e != cudaSuccess) return e;
+    // blocks without a row to spare, and no more than their sums have room for
+    cfg.gridDim = dim3((unsigned)std::max(1, std::min(resident, p.r.T / kLineWarps)));
+    return cudaLaunchKernelEx(&cfg, kernel, p, stride);
+}
+
+template <typename T, int OP, bool kEnt>
 cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_own, cudaStream_t stream, bool &fits) {
     auto kernel = ring_rows_kernel<T, OP, kEnt>;
     constexpr bool kStats = OP != kOpScale, kKeep = OP == kOpPolicy || OP == kOpDistill;
     const int nvec = p.r.V / PostVec<T>::kElems;
     constexpr size_t kMaxDynamic = kCtaBytes[2] - sizeof(RowShared<OP>);
+    fits = true;
+    if (p.r.T > 0 && nvec <= kLineBytes / 16) return launch_lines<T, OP, kEnt>(p, K, after_own, stream);
     const size_t fixed = sizeof(RowShared<OP>) + (size_t)kMetaOf(OP) * 12 * K;
     RowPlan plan{};
     fits = false;
