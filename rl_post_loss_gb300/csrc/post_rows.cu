@@ -13,8 +13,12 @@
 // Three CTAs on an SM fill each other's waits for the finisher; where a ring holds two slices the warps
 // also fold row r + 1 before they write row r.
 //
-// Rows too long for the rings of a cluster (above about 1.8 MB with eight CTAs) take the block-per-row
-// kernels at the end, which read a row twice.
+// Short rows (up to 24 KB) are a warp's each (line_rows_kernel). Rows too long for the rings of a cluster (above
+// about 1.8 MB with eight CTAs) take the block-per-row kernels at the end, which read a row twice.
+//
+// Bounds: HBM for long rows. 6000 x 151552 bf16: the loss with a KL term 570 us, 94% of the copy rate; log-probs
+// of 16000 rows 102-107%; distillation (128 entries) 691 us, 78%, bounded by a row's stay in the rings (9.4 us, of
+// which 4.4 copy and write).
 #include <algorithm>
 #include <cstddef>
 #include <mutex>
@@ -1018,7 +1022,10 @@ __device__ __forceinline__ void line_sums(const P &p, const PostPartial &mine) {
 }
 
 // A row per warp, in shared memory: for short rows the steps between a row's warps, its finisher and its
-// producer take longer than its bytes. Two dozen warps on an SM cover one another's copies and chains.
+// producer take longer than its bytes. Two dozen warps on an SM cover one another's copies and chains. Bytes of a
+// row here and on the rings, rows of bf16 (us): 8 KB, 30000 rows: the loss 105 and 264, distillation (K = 128) 172
+// and 430, log-probs 44 and 115; 24 KB, 15000: 140 and 191, 226 and 267, 68 and 80; 32 KB, 15000: 233 and 207, 347
+// and 284, 116 and 81.
 template <typename T, int OP, bool kEnt>
 __global__ void __launch_bounds__(32 * kLineWarps, kLineBlocks)
 line_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, int stride) {
