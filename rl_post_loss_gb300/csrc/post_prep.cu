@@ -44,7 +44,8 @@ __device__ __forceinline__ void add_exp(Sum2 &sum, float v) {
 // Blocks [0, S) count the mask=1 tokens of one response each; the others take eight rows each, a
 // warp per row: ln of the teacher's normaliser, its remaining mass and its total mass less 1. A teacher
 // given by log-probs keeps them (m = ln sum = 0) and its remaining mass is 1 - sum q, the sum held in two
-// parts: with most of the mass in the entries, fp32 would leave it no digits.
+// parts: with most of the mass in the entries, fp32 would leave it no digits. 6000 rows of 128 entries:
+// 6.7 us, a launch and two dependent loads (6 MB would take 1); the rows' launch begins as it ends.
 __global__ void __launch_bounds__(kPrepThreads) distill_prep_kernel(DistillPrepParams p) {
     __shared__ int s_i[32];
     if (blockIdx.x == 0)
