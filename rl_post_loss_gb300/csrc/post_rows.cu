@@ -830,6 +830,8 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
         // ------------------------------------------------ consumers
         const int tail_v = nvec * VEC + tid;     // this thread's entry of the last V mod VEC
         const bool has_tail = last_rank && tail_v < V;
+        // asked for before the waits of a fold or a write, which its latency would lengthen
+        auto tail_of = [&](int t) { return has_tail ? VT::load1(row_in<T>(p.r, t), tail_v) : 0.f; };
         int da = 0, db = 0;                      // the next segments of the fold and of the write
         uint32_t phase_a = 0, phase_b = 0;
         auto next = [&](int &d, uint32_t &phase) {
@@ -851,6 +853,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 bool dup = false;
                 if constexpr (OP == kOpLogp || OP == kOpPolicy) y = meta.y;
                 const int ky = y >= 0 && y < nvec * VEC ? y / VEC - v0 : -1;  // the sampled entry's group
+                const float tail_z = tail_of(meta.t);
                 PostAcc acc = post_acc();
                 for (int j = 0; j < plan.parts; ++j) {
                     row_wait(sh, &s_full[da * kWarps + warp], phase_a, p.r.status);
@@ -888,7 +891,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 }
                 PostStats st = acc.stats();
                 if (has_tail && tail_v != y && !((marks >> tid) & 1)) {
-                    const float x[1] = {VT::load1(row_in<T>(p.r, meta.t), tail_v)};
+                    const float x[1] = {tail_z};
                     post_fold<kEnt>(st, x, c);
                 }
                 st = post_warp_merge<kEnt>(st, c);
@@ -907,11 +910,14 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
         auto write = [&](int r) -> bool {
             const int ms = r % kMeta;
             RowGrad gr;
+            float tail_z;
             if constexpr (OP == kOpScale) {
                 row_wait(sh, &sh.mfull[ms], use(r), p.r.status);
                 if (sh.meta[ms].t < 0 || any_dead(sh)) return false;
                 gr = sh.meta[ms].grad;
+                tail_z = tail_of(sh.meta[ms].t);
             } else {
+                tail_z = tail_of(sh.meta[ms].t);
                 row_wait(sh, &sh.fin_full[ms], use(r), p.r.status);
                 gr = sh.fin[ms].grad;
             }
@@ -948,7 +954,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 }
             }
             if (has_tail) {
-                const float e = zero ? 0.f : gr.a * ex2_approx((VT::load1(row_in<T>(p.r, t), tail_v) - gr.m) * c);
+                const float e = zero ? 0.f : gr.a * ex2_approx((tail_z - gr.m) * c);
                 VT::store1(dz, tail_v, OP != kOpDistill && !zero && tail_v == gr.y ? gr.gy : e);
             }
             __syncwarp();
@@ -1097,6 +1103,7 @@ line_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, int stri
             if (meta.read) de = distill_entries(p, s_z, s_lq, meta.rec);
         }
         const bool read = meta.read;
+        const float tail_z = has_tail && in_line ? VT::load1(row_in<T>(p.r, t), tail_v) : 0.f;  // before the wait
         if (in_line && nvec > 0) {
             const bool there = ptx::mbar_wait(bar, phase);
             phase ^= 1;
@@ -1128,7 +1135,7 @@ line_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, int stri
             }
             st = acc.stats();
             if (has_tail && tail_v != y && !((marks >> lane) & 1)) {
-                const float x[1] = {VT::load1(row_in<T>(p.r, t), tail_v)};
+                const float x[1] = {tail_z};
                 post_fold<kEnt>(st, x, c);
             }
             st = post_warp_merge<kEnt>(st, c);
@@ -1174,7 +1181,7 @@ line_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, int stri
                 if (OP != kOpDistill && gr.y < nvec * VEC && ((gr.y / VEC) & 31) == lane) VT::store1(dz, gr.y, gr.gy);
             }
             if (has_tail) {
-                const float e = zero ? 0.f : gr.a * ex2_approx((VT::load1(row_in<T>(p.r, t), tail_v) - gr.m) * c);
+                const float e = zero ? 0.f : gr.a * ex2_approx((tail_z - gr.m) * c);
                 VT::store1(dz, tail_v, OP != kOpDistill && !zero && tail_v == gr.y ? gr.gy : e);
             }
             if constexpr (OP == kOpDistill) {
