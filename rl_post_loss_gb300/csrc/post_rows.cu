@@ -17,7 +17,7 @@
 // about 1.8 MB with eight CTAs) take the block-per-row kernels at the end, which read a row twice.
 //
 // Bounds: HBM for long rows. 6000 x 151552 bf16: the loss with a KL term 570 us, 94% of the copy rate; log-probs
-// of 16000 rows 102-107%; distillation (128 entries) 691 us, 78%, bounded by a row's stay in the rings (9.4 us, of
+// of 16000 rows 102-107%; distillation (128 entries) 681 us, 79%, bounded by a row's stay in the rings (9.4 us, of
 // which 4.4 copy and write).
 #include <algorithm>
 #include <cstddef>
