@@ -57,6 +57,46 @@ struct Sum2 {
     }
 };
 
+// e^v = hi + lo for |v| < 88, within about 1e-8 relative: v = n ln 2 + r in Cody and Waite's two parts of
+// ln 2 (the first has 10 bits, so that n times it is exact), then e^r = 1 + r + the rest of Taylor's series,
+// of which only the rest, below 0.07, is rounded to fp32.
+__device__ __forceinline__ void exp_parts(float v, float &hi, float &lo) {
+    const float n = rintf(v * kLog2e);
+    const float a = fmaf(-n, 0.693359375f, v), b = n * 2.12194440e-4f;
+    const float r = __fadd_rn(a, b), rl = __fsub_rn(b, __fsub_rn(r, a));
+    float q = 1.f / 40320.f;
+    q = fmaf(r, q, 1.f / 5040.f);
+    q = fmaf(r, q, 1.f / 720.f);
+    q = fmaf(r, q, 1.f / 120.f);
+    q = fmaf(r, q, 1.f / 24.f);
+    q = fmaf(r, q, 1.f / 6.f);
+    q = fmaf(r, q, 0.5f);
+    const float one = __fadd_rn(1.f, r), ol = __fsub_rn(r, __fsub_rn(one, 1.f));
+    const float scale = ex2_approx(n);  // a power of two: exact
+    hi = one * scale;
+    lo = (fmaf(r * r, q, rl) + ol) * scale;
+}
+
+// What rounding left of ln(x + x_lo), l = ln x in fp32: Newton's step (x + x_lo) e^{-l} - 1, to about 1e-8 (half a
+// step of l itself is 2.4e-7 from 4 to 8).
+__device__ __forceinline__ float log_rest(float x, float x_lo, float l) {
+    float hi, lo;
+    exp_parts(-l, hi, lo);
+    return fmaf(x_lo, hi, fmaf(x, lo, fmaf(x, hi, -1.f)));
+}
+
+// The rounding error of s = a - b (Knuth), for finite values.
+__device__ __forceinline__ float diff_rest(float a, float b, float s) {
+    const float t = __fsub_rn(s, a);
+    return __fsub_rn(__fsub_rn(a, __fsub_rn(s, t)), __fadd_rn(b, t));
+}
+
+// (a + lo) - b, rounded once where it is finite.
+__device__ __forceinline__ float diff_of(float a, float lo, float b) {
+    const float s = __fsub_rn(a, b);
+    return fabsf(s) < INFINITY ? __fadd_rn(s, __fadd_rn(diff_rest(a, b, s), lo)) : s;
+}
+
 // ---------------------------------------------------------------- logits of either type
 
 template <typename T>
@@ -456,6 +496,7 @@ struct PostToken {
     PostStats all;   // the whole row
     float others;    // the others' sum against the whole row's reference
     float logp;      // ln p_y (NaN where the row is not finite)
+    float logp_lo;   // what rounding left of it: the loss takes its differences from near values
 };
 template <bool kEnt>
 __device__ __forceinline__ PostToken post_target(PostStats rest, float zy) {
@@ -465,15 +506,22 @@ __device__ __forceinline__ PostToken post_target(PostStats rest, float zy) {
         r.others = rest.s * f;
         r.all = PostStats{zy, r.others + ((zy - zy) + 1.f), 0.f};  // 1, or NaN for an infinite logit
         if (kEnt) r.all.u = f * fmaf(fmaxf(dm, kNoWeight), rest.s, rest.u);
-        r.logp = -log1pf(r.others);
+        const float l = log1pf(r.others), s = r.all.s;
+        r.logp = -l;
+        // below 1/8 log1pf's own error is the smaller one
+        r.logp_lo = r.others > 0.125f ? -log_rest(s, diff_rest(1.f, -r.others, s), l) : 0.f;
     } else {
         const float d = (zy - rest.m) * kLog2e, e = exp2f(d);
         r.others = rest.s;
         r.all = PostStats{rest.m, rest.s + e, 0.f};
         if (kEnt) r.all.u = fmaf(e, fmaxf(d, kNoWeight), rest.u);
-        r.logp = (zy - rest.m) - logf(r.all.s);
+        const float l = logf(r.all.s), dz = zy - rest.m;
+        r.logp = dz - l;
+        r.logp_lo = diff_rest(zy, rest.m, dz) + diff_rest(dz, l, r.logp) -
+                    log_rest(r.all.s, diff_rest(rest.s, -e, r.all.s), l);
     }
     if (!post_finite(r.all)) r.logp = __int_as_float(0x7fc00000);
+    if (!(fabsf(r.logp) < INFINITY)) r.logp_lo = 0.f;
     return r;
 }
 
@@ -575,7 +623,8 @@ struct PolicyRow {
 __device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const PolicyTok &k, const PostToken &tok, bool read) {
     PolicyRow r;
     const LossConsts &c = p.c;
-    const float logp = tok.logp, e = __fsub_rn(logp, k.lref);  // ln r, one fp32 subtraction
+    // ln r: the branches go by one fp32 subtraction, its exponential by the difference before the log-prob was rounded
+    const float logp = tok.logp, e = __fsub_rn(logp, k.lref), ln_r = diff_of(logp, tok.logp_lo, k.lref);
     const bool ok = k.ok && read;
     float g = 0.f;
     r.logp = logp;
@@ -585,7 +634,7 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const Pol
         const bool gate = ok && e > c.clip_lo && e < c.clip_hi;
         r.flags = (k.pre & (RL_FLAG_MASKED | RL_FLAG_BAD_TARGET)) | (gate ? RL_FLAG_POP_IN_BOUNDS : 0u);
         if (gate && k.cf != 0.f) {
-            const float ratio = expf(e);
+            const float ratio = expf(ln_r);
             r.obj = k.cf * ratio * logp;
             g = c.dis_stopgrad ? -k.wcf * ratio : -k.wcf * ratio * (1.f + logp);
         }
@@ -599,14 +648,14 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const Pol
         const bool clip = ok && (((pre & kPreAPos) && e > c.clip_hi) || ((pre & kPreANeg) && e < c.clip_lo));
         r.flags = (pre & kPreOut) | (clip ? RL_FLAG_CLIP_ACTIVE : 0u);
         if (k.cf != 0.f && A != 0.f) {
-            const float ratio = expf(e);
+            const float ratio = expf(ln_r);
             r.obj = k.cf * A * (clip ? ((pre & kPreAPos) ? c.one_plus_eps_high : c.one_minus_eps_low) : ratio);
             g = clip ? 0.f : -k.wcf * A * ratio;
         }
     }
     if (k.m && k.ok) {
         float dkl;
-        post_kl(p.kl.estimator, __fsub_rn(logp, k.ref), r.kl, dkl);
+        post_kl(p.kl.estimator, diff_of(logp, tok.logp_lo, k.ref), r.kl, dkl);
         g = fmaf(k.w * p.kl.coef, dkl, g);
     }
     const float inv = 1.f / tok.all.s;
@@ -628,10 +677,12 @@ __device__ __forceinline__ PostTerm policy_write(const PolicyParams &p, int t, c
     if (p.r.entropy) p.r.entropy[t] = H;
     if (p.flags) p.flags[t] = (uint8_t)r.flags;
     if (p.kl.kl) p.kl.kl[t] = m && !ok ? nan : r.kl;
-    // w x in two parts: the same weight for a whole response, its rounding would not average out
-    const float x = fmaf(p.kl.coef, r.kl, -r.obj), wx = k.w * x;
+    // x = coef k - obj and w x in two parts each: a loss of centred advantages is a small difference of large sums,
+    // and the same weight for a whole response, rounded, would not average out
+    const float ck = p.kl.coef * r.kl, x = ck - r.obj, wx = k.w * x;
+    const float x_lo = diff_rest(ck, r.obj, x) + fmaf(p.kl.coef, r.kl, -ck);
     p.r.term_flags[t] = r.flags;
-    return PostTerm{wx, fmaf(k.w_lo, x, fmaf(k.w, x, -wx)), m ? H : 0.f, m ? r.kl : 0.f};
+    return PostTerm{wx, fmaf(k.w_lo, x, fmaf(k.w, x, -wx)) + k.w * x_lo, m ? H : 0.f, m ? r.kl : 0.f};
 }
 
 // ---------------------------------------------------------------- the teacher's entries

@@ -21,24 +21,12 @@ __device__ __forceinline__ int2 seq_range(const int32_t *cu, int S, int T, int i
     return make_int2(b, e);
 }
 
-// Adds e^v, v <= 88, to a sum, within about 1e-9 relative: v = n ln 2 + r in Cody and Waite's two parts of
-// ln 2 (the first has 10 bits, so that n times it is exact), then e^r = 1 + r + the rest of Taylor's series,
-// of which only the rest, below 0.07, is rounded to fp32.
+// Adds e^v, v <= 88, to a sum.
 __device__ __forceinline__ void add_exp(Sum2 &sum, float v) {
     if (v < -87.f) return;  // below 2e-38
-    const float n = rintf(v * kLog2e);
-    const float a = fmaf(-n, 0.693359375f, v), b = n * 2.12194440e-4f;
-    const float r = __fadd_rn(a, b), rl = __fsub_rn(b, __fsub_rn(r, a));
-    float q = 1.f / 40320.f;
-    q = fmaf(r, q, 1.f / 5040.f);
-    q = fmaf(r, q, 1.f / 720.f);
-    q = fmaf(r, q, 1.f / 120.f);
-    q = fmaf(r, q, 1.f / 24.f);
-    q = fmaf(r, q, 1.f / 6.f);
-    q = fmaf(r, q, 0.5f);
-    const float one = __fadd_rn(1.f, r), ol = __fsub_rn(r, __fsub_rn(one, 1.f));
-    const float scale = ex2_approx(n);  // a power of two: exact
-    sum.add(one * scale, (fmaf(r * r, q, rl) + ol) * scale);
+    float hi, lo;
+    exp_parts(v, hi, lo);
+    sum.add(hi, lo);
 }
 
 // Blocks [0, S) count the mask=1 tokens of one response each; the others take eight rows each, a
