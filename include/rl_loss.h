@@ -473,7 +473,9 @@ RL_LOSS_API size_t rl_loss_distill_workspace_bytes(int32_t num_tokens, int32_t n
  * not is excluded (zero gradient, kl = NaN, RL_ERR_TARGET_RANGE). A row whose
  * entries are all padding, or all -inf with RL_DISTILL_RENORM, contributes 0.
  * 0 log 0 = 0. `workspace`: device, 256-byte aligned, at least
- * rl_loss_distill_workspace_bytes(T, S), any contents, one per stream. Errors:
+ * rl_loss_distill_workspace_bytes(T, S), any contents, one per stream and per
+ * host thread: a call's launches hand results on in it, and another call's that
+ * go between them on the same stream would overwrite these. Errors:
  * RL_ERR_INVALID_ARG (NULL pointer, bad mode, norm or number), RL_ERR_DTYPE,
  * RL_ERR_SHAPE (T < 0, S < 1, V, a stride), RL_ERR_UNSUPPORTED (k, reverse
  * without a tail), RL_ERR_CAPACITY (workspace), RL_ERR_ALIGNMENT. Two launches. */

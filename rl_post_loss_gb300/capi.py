@@ -13,6 +13,7 @@ import ctypes
 import functools
 import os
 import re
+import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "librl_loss.so")
@@ -353,20 +354,22 @@ def rl_loss_preference_workspace_bytes(num_tokens: int, num_seqs: int) -> int:
     return int(load().rl_loss_preference_workspace_bytes(int(num_tokens), int(num_seqs)))
 
 
-_POST_WORKSPACE: dict = {}
+_POST_WORKSPACE = threading.local()
 
 
 def _post_workspace(need: int, device, stream: int):
-    """A workspace of this device and stream, grown when a call needs more and kept between calls. During a
+    """A workspace of this thread, device and stream, grown when a call needs more and kept between calls. (By
+    thread: a call is two or three launches, between which another thread's on the same stream may go.) During a
     graph capture the caller passes its own: one allocated here would belong to the graph's memory pool."""
     import torch
     if torch._C._cuda_isCurrentStreamCapturing():
         raise ValueError("pass workspace= while a CUDA graph is captured (any torch.uint8 tensor of the size "
                          "rl_loss_*_workspace_bytes gives, kept as long as the graph)")
-    ws = _POST_WORKSPACE.get((device.index, stream))
+    kept = _POST_WORKSPACE.__dict__
+    ws = kept.get((device.index, stream))
     if ws is None or ws.numel() < need:
         ws = torch.empty(max(need, 1 << 16), dtype=torch.uint8, device=device)
-        _POST_WORKSPACE[(device.index, stream)] = ws
+        kept[(device.index, stream)] = ws
     return ws
 
 
@@ -459,7 +462,8 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
     each row's entries (id -1: padding). mode "renorm" takes logits already divided by the temperature or
     log-probs, "tail" log-probs at the temperature (what they leave of the mass is one more outcome);
     direction "forward" is KL(teacher || student), "reverse" KL(student || teacher) ("tail" only). Returns
-    loss [1], kl [T] and dlogits (allocated where not given; dlogits may be logits itself)."""
+    loss [1], kl [T] and dlogits (allocated where not given; dlogits may be logits itself). A workspace that is
+    passed serves one call at a time: threads pass one each."""
     import torch
     if mode not in DISTILL_MODES or direction not in ("forward", "reverse"):
         raise ValueError("mode is 'renorm' or 'tail', direction 'forward' or 'reverse'")
@@ -500,7 +504,8 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
                     stream=None) -> dict:
     """Preference loss over pairs of responses (2j preferred to 2j + 1), forward and backward. logp_ref [T] are
     the reference policy's log-probs (None: no reference). Returns loss [1], logp [T], seq_logratio [S],
-    pair_loss [S / 2] and dlogits (allocated where not given; dlogits may be logits itself)."""
+    pair_loss [S / 2] and dlogits (allocated where not given; dlogits may be logits itself). A workspace that is
+    passed serves one call at a time: threads pass one each."""
     import torch
     if loss_type not in PREF_LOSSES:
         raise ValueError("loss_type is 'sigmoid', 'hinge' or 'ipo'")

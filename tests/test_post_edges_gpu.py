@@ -87,3 +87,44 @@ def test_differences_are_taken_before_the_log_prob_is_rounded(V, dtype, low):
     out, bits = policy(z, V, y, [0, T], [-1.0], full(ref), full(old), coef=64.0, estimator="k1", adv_mode=capi.RL_ADV_PER_SEQ)
     assert bits == 0 and abs(64 * d + r) < 0.1
     assert abs(out["loss_f64"].item() - (64 * d + r)) <= 64 * d_tol + r * (r_tol + 6 * ph.U)
+
+
+# ---------------------------------------------------------------- threads
+
+@pytest.mark.parametrize("V", [4099, 40001])
+def test_two_threads_on_one_stream(V):
+    """Each thread's calls, without a workspace of their own, give what they give alone, bit for bit."""
+    import threading
+
+    def job(seed, T, K):
+        g = torch.Generator().manual_seed(seed)
+        z = rows_of(T, V, "bf16")
+        z[:, :V] = (torch.randn(T, V, generator=g) * 2).bfloat16().cuda()
+        ids = torch.stack([torch.randperm(V, generator=g)[:K] for _ in range(T)])
+        vals = torch.log_softmax(torch.randn(T, K, generator=g), 1) - 0.2
+        ids, vals, y = dev(ids, torch.int32), dev(vals), dev(torch.randint(0, V, (T,), generator=g), torch.int32)
+        mask, cu = dev(np.ones(T), torch.uint8), dev([0, T // 3, T], torch.int32)
+
+        def run():
+            a = capi.distill_loss(z, ids, vals, mask, cu, vocab=V, mode="tail", tail_floor=1e-6)
+            b = capi.preference_loss(z, y, None, mask, cu, vocab=V)
+            return [a["loss"], a["kl"], a["dlogits"][:, :V], b["loss"], b["seq_logratio"], b["dlogits"][:, :V]]
+        return run
+
+    jobs = [job(1, 60, 9), job(2, 201, 24)]
+    want = [[t.clone() for t in run()] for run in jobs]
+    torch.cuda.synchronize()
+    wrong, start = [], threading.Barrier(2, timeout=60)
+
+    def work(run, expected):
+        start.wait()
+        for i in range(40):
+            if not all(torch.equal(a, b) for a, b in zip(run(), expected)):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(jobs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not wrong and not any(t.is_alive() for t in threads)
