@@ -389,7 +389,10 @@ RL_LOSS_API rl_status rl_topk(const rl_topk_config *config, int32_t rows, const 
  * distillation from a teacher known by its top logits, and a preference loss
  * over pairs of responses. Shared rules: logits rows are logits_dtype, 16-byte
  * aligned with ld * elem_size % 16 == 0, read up to V rounded up to 16 bytes; a
- * -inf logit has probability 0; dlogits may alias logits when the strides are
+ * -inf logit has probability 0 (where it is the sampled token's, logp is -inf and
+ * a loss is what its formula tends to: an infinite loss raises RL_ERR_NONFINITE,
+ * and a gradient whose coefficient is infinite holds infinities and NaN);
+ * dlogits may alias logits when the strides are
  * equal, its columns >= V are not written; rows with mask = 0 are not read (NaN
  * or inf in them changes nothing) and get zero gradients. Softmax statistics
  * are held in fp32, sums over tokens in two fp32 parts (about 48 bits), all in an

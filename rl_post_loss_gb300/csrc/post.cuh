@@ -45,15 +45,17 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
 // ---------------------------------------------------------------- sums in two parts
 
 // A sum held as two fp32 values, |lo| a rounding of hi at most: about 48 bits at fp32's speed (the
-// device's fp64 units are some sixty times slower).
+// device's fp64 units are some sixty times slower). An infinite term makes an infinite sum.
 struct Sum2 {
     float hi, lo;
     __device__ __forceinline__ void add(float h, float l) {
         const float s = __fadd_rn(hi, h), b = __fsub_rn(s, hi);
         const float err = __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(h, b));  // Knuth's exact error of hi + h
         l = __fadd_rn(__fadd_rn(lo, l), err);
-        hi = __fadd_rn(s, l);
-        lo = __fsub_rn(l, __fsub_rn(hi, s));
+        const float t = __fadd_rn(s, l);
+        const bool fin = fabsf(t) < INFINITY;  // else err is inf - inf where s is infinite: s itself is the sum
+        lo = fin ? __fsub_rn(l, __fsub_rn(t, s)) : 0.f;
+        hi = fin ? t : s;
     }
 };
 
@@ -542,7 +544,7 @@ __device__ __forceinline__ float post_k3(float d) {
     q = fmaf(-d, q, 1.f / 24.f);
     q = fmaf(-d, q, 1.f / 6.f);
     q = fmaf(-d, q, 0.5f);
-    const float far = (expf(-d) - 1.f) + d;
+    const float e = expf(-d), far = e < INFINITY ? (e - 1.f) + d : e;  // d = -inf: inf, not inf - inf
     return fabsf(d) < 1.f ? d * d * q : far;
 }
 
@@ -656,7 +658,7 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyParams &p, const Pol
     if (k.m && k.ok) {
         float dkl;
         post_kl(p.kl.estimator, diff_of(logp, tok.logp_lo, k.ref), r.kl, dkl);
-        g = fmaf(k.w * p.kl.coef, dkl, g);
+        if (p.kl.coef != 0.f) g = fmaf(k.w * p.kl.coef, dkl, g);  // no 0 times infinity
     }
     const float inv = 1.f / tok.all.s;
     r.grad = g == 0.f ? RowGrad{0.f, 0.f, 0.f, -1} : RowGrad{-g * inv, tok.all.m, g * (tok.others * inv), k.y};
@@ -679,10 +681,11 @@ __device__ __forceinline__ PostTerm policy_write(const PolicyParams &p, int t, c
     if (p.kl.kl) p.kl.kl[t] = m && !ok ? nan : r.kl;
     // x = coef k - obj and w x in two parts each: a loss of centred advantages is a small difference of large sums,
     // and the same weight for a whole response, rounded, would not average out
-    const float ck = p.kl.coef * r.kl, x = ck - r.obj, wx = k.w * x;
+    const float ck = p.kl.coef != 0.f ? p.kl.coef * r.kl : 0.f, x = ck - r.obj, wx = k.w * x;
     const float x_lo = diff_rest(ck, r.obj, x) + fmaf(p.kl.coef, r.kl, -ck);
+    const float lo = fabsf(wx) < INFINITY ? fmaf(k.w_lo, x, fmaf(k.w, x, -wx)) + k.w * x_lo : 0.f;
     p.r.term_flags[t] = r.flags;
-    return PostTerm{wx, fmaf(k.w_lo, x, fmaf(k.w, x, -wx)) + k.w * x_lo, m ? H : 0.f, m ? r.kl : 0.f};
+    return PostTerm{wx, lo, m ? H : 0.f, m ? r.kl : 0.f};
 }
 
 // ---------------------------------------------------------------- the teacher's entries

@@ -166,18 +166,19 @@ __global__ void __launch_bounds__(kPrepThreads) pref_pairs_kernel(PrefPairParams
             per[k] = p.mean ? (n[k] > 0 ? 1.f / (float)n[k] : 0.f) : 1.f;
             if (p.mean && n[k] > 0) {  // the quotient of a two-part number: of its parts, with the first one's remainder
                 const float q = r[k].hi / (float)n[k];
-                r[k] = Sum2{q, (fmaf(-q, (float)n[k], r[k].hi) + r[k].lo) / (float)n[k]};
+                r[k] = Sum2{q, fabsf(q) < INFINITY ? (fmaf(-q, (float)n[k], r[k].hi) + r[k].lo) / (float)n[k] : 0.f};
             }
         }
         if (n[0] == 0 || n[1] == 0) post_raise(p.status, RL_ERR_EMPTY_SEQ);
         Sum2 diff = r[0];
         diff.add(-r[1].hi, -r[1].lo);
         const float D = diff.hi + diff.lo, beta = p.beta, eps = p.smoothing;
+        // D is infinite where a token of probability 0 was sampled: each kind's limit, and no 0 times infinity
         float loss, slope;  // of the pair's loss in D
         if (p.kind == RL_PREF_SIGMOID) {
             const float x = fmaf(beta, D, -p.margin);
             const float soft = log1pf(expf(-fabsf(x)));  // -ln sigma(|x|)
-            loss = (1.f - eps) * (soft + fmaxf(-x, 0.f)) + eps * (soft + fmaxf(x, 0.f));
+            loss = (1.f - eps) * (soft + fmaxf(-x, 0.f)) + (eps != 0.f ? eps * (soft + fmaxf(x, 0.f)) : 0.f);
             slope = beta * (eps / (1.f + expf(-x)) - (1.f - eps) / (1.f + expf(x)));
         } else if (p.kind == RL_PREF_HINGE) {
             const float x = fmaf(beta, D, -p.margin);
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kPrepThreads) pref_pairs_kernel(PrefPairParams
         }
         if (isnan(D)) loss = slope = D;  // a row that is not finite: max() would hide it
         const float like = n[0] > 0 ? -(lp.hi + lp.lo) / (float)n[0] : 0.f;
-        loss = fmaf(p.nll, like, loss);
+        if (p.nll != 0.f) loss = fmaf(p.nll, like, loss);
         const float inv_p = 1.f / (float)P;
         p.coef[2 * j] = (slope * per[0] - (n[0] > 0 ? p.nll / (float)n[0] : 0.f)) * inv_p;
         p.coef[2 * j + 1] = -slope * per[1] * inv_p;

@@ -128,3 +128,111 @@ def test_two_threads_on_one_stream(V):
     for t in threads:
         t.join(120)
     assert not wrong and not any(t.is_alive() for t in threads)
+
+
+# ---------------------------------------------------------------- sampled tokens of probability 0
+
+EVERY = [(1003, "bf16"), (1003, "f32"), (20011, "bf16"), (600001, "f32")]  # a warp per row, rings, rows too long for them
+NAN = float("nan")
+
+
+def random_rows(T, V, dtype, seed):
+    z = rows_of(T, V, dtype, NAN)
+    g = torch.Generator().manual_seed(seed)
+    z[:, :V] = (torch.randn(T, V, generator=g) * 2).to(DT[dtype]).cuda()
+    return z
+
+
+@pytest.mark.parametrize("kind,mean,eps", [("sigmoid", 0, 0.0), ("sigmoid", 1, 0.1), ("hinge", 0, 0.0), ("ipo", 1, 0.0)])
+@pytest.mark.parametrize("V,dtype", EVERY)
+def test_preference_of_an_impossible_token(V, dtype, kind, mean, eps):
+    """One token of the rejected (or the preferred) response has a -inf logit. D is +inf (-inf), so the pair's loss
+    and slope are their limits; the other pair's values are as ever. Tolerances as elsewhere, from the error model."""
+    cu, beta, P = np.array([0, 3, 5, 9, 12]), 0.3, 2
+    T = int(cu[-1])
+    y = (np.arange(T) * 37 + 5) % V
+    mask = np.ones(T, np.uint8)
+    for t, D in ((4, np.inf), (1, -np.inf)):
+        z = random_rows(T, V, dtype, V + t)
+        z[t, int(y[t])] = -math.inf
+        zf = z[:, :V].double().cpu().numpy()
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = capi.preference_loss(z, dev(y, torch.int32), None, dev(mask), dev(cu, torch.int32), vocab=V, loss_type=kind,
+                                   length_norm=bool(mean), beta=beta, label_smoothing=eps, device_status=st)
+        torch.cuda.synchronize()
+        r = ph.Rows(zf)
+        lp = r.lp[np.arange(T), y]
+        tol = r.logp_tol(lp)
+        x = beta * D
+        if kind == "sigmoid":
+            loss = np.inf if x < 0 or eps > 0 else 0.0
+            slope = -beta * (1 - eps) if x < 0 else beta * eps
+        elif kind == "hinge":
+            loss, slope = (np.inf, -beta) if x < 0 else (0.0, 0.0)
+        else:
+            loss, slope = np.inf, 2 * D
+        got = out["logp"].double().cpu().numpy()
+        assert got[t] == -np.inf
+        fin = np.arange(T) != t
+        assert np.abs(got[fin] - lp[fin]).max() <= (tol[fin] + ph.U * np.abs(lp[fin])).max()
+        s = out["seq_logratio"].cpu().numpy()
+        assert s[1 if t == 4 else 0] == -np.inf and np.isfinite(np.delete(s, 1 if t == 4 else 0)).all()
+        pair = out["pair_loss"].cpu().numpy()
+        assert pair[0] == loss
+        rest = slice(5, 12)
+        want = ph.preference(zf[rest], y[rest], None, mask[rest], cu[2:] - 5, kind, mean, beta, 0.0, eps, 0.0)
+        s_tol = (tol[rest] + ph.U * np.abs(lp[rest])).sum()
+        curve = {"sigmoid": beta * beta / 4, "hinge": 0.0, "ipo": 2.0}[kind]
+        pair_tol = abs(want["slope"][0]) * s_tol + curve * s_tol ** 2 + 4 * ph.U * abs(want["pair"][0])
+        assert abs(pair[1] - want["pair"][0]) <= pair_tol
+        if np.isinf(loss):
+            assert out["loss"].item() == np.inf and st.item() == BIT["RL_ERR_NONFINITE"]
+        else:
+            assert abs(out["loss"].item() - want["pair"][0] / P) <= pair_tol and st.item() == 0
+        dz = out["dlogits"][:, :V].double().cpu().numpy()
+        per = np.array([1 / 3, 1 / 2]) if mean else np.ones(2)
+        g = np.concatenate([np.repeat([slope * per[0], -slope * per[1]], [3, 2]), want["g"]]) / P
+        if kind == "ipo":  # an infinite coefficient
+            assert not np.isfinite(dz[:5]).any(1).all()
+            g[:5] = 0
+        dg = np.concatenate([np.zeros(5), np.full(7, curve * s_tol / P)]) + 4 * ph.U * np.abs(g)
+        d, d_tol = ph.onehot_grad(r, g, y, dg, np.where(fin, tol, 0), dtype)
+        on = np.arange(T) >= (5 if kind == "ipo" else 0)
+        assert (np.abs(dz - d)[on] <= d_tol[on]).all()
+
+
+@pytest.mark.parametrize("estimator,limit", [("k1", -np.inf), ("k2", np.inf), ("k3", np.inf)])
+@pytest.mark.parametrize("V,dtype", EVERY)
+def test_loss_with_kl_of_an_impossible_token(V, dtype, estimator, limit):
+    """The token's ratio is 0 and its estimate infinite: with a coefficient the loss is infinite, without one it is
+    the policy term's. Other rows keep their gradients."""
+    T, t = 6, 2
+    z = random_rows(T, V, dtype, V)
+    y = (np.arange(T) * 31 + 4) % V
+    z[t, int(y[t])] = -math.inf
+    zf = z[:, :V].double().cpu().numpy()
+    r = ph.Rows(zf)
+    lp = r.lp[np.arange(T), y]
+    tol = r.logp_tol(lp)
+    base = np.where(np.isfinite(lp), lp, -9.0).astype(np.float32)
+    w = 1 / T
+    ratio = np.exp(lp - base.astype(np.float64))
+    rel = tol + 12 * ph.U * (1 + np.abs(base))
+    for coef in (0.0, 0.5):
+        out, bits = policy(z, V, y, [0, T], [1.0], base + np.float32(0.25), base, coef=coef, estimator=estimator,
+                           adv_mode=capi.RL_ADV_PER_SEQ)
+        kl = out["kl"].cpu().numpy()
+        assert kl[t] == limit and np.isfinite(np.delete(kl, t)).all() and out["mean_kl"].item() == limit
+        assert out["logp"][t].item() == -np.inf
+        if coef:
+            assert out["loss"].item() == limit and bits == BIT["RL_ERR_NONFINITE"]
+        else:
+            assert bits == 0 and abs(out["loss_f64"].item() + w * ratio.sum()) <= w * (ratio * rel).sum()
+        _, dk = ph.kl_terms(estimator, np.where(np.isfinite(lp), lp, 0) - (base + np.float32(0.25)))
+        g = w * (coef * dk - ratio)
+        g[t] = 0.0
+        dg = w * (ratio * rel + coef * (tol + 8 * ph.U * 9) * (1 + np.abs(dk)))
+        d, d_tol = ph.onehot_grad(r, g, y, dg, np.where(np.isfinite(lp), tol, 0), dtype)
+        dz = out["dlogits"][:, :V].double().cpu().numpy()
+        on = np.arange(T) != t if coef else np.ones(T, bool)
+        assert (np.abs(dz - d)[on] <= d_tol[on]).all()
