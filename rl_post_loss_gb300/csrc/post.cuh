@@ -548,6 +548,13 @@ __device__ __forceinline__ float post_k3(float d) {
     return fabsf(d) < 1.f ? d * d * q : far;
 }
 
+// h k3(d), d = ln(h / o). Its part h e^{-d} is o: taken as such where h is 0, and where e^{-d} nears fp32's end,
+// beyond which a subnormal h times infinity would stand for a term of at most o.
+__device__ __forceinline__ float post_k3_term(float h, float o, float d) {
+    const float near = h * post_k3(d), far = o + h * (d - 1.f);
+    return h != 0.f ? (d > -80.f ? near : far) : o;  // (a NaN too)
+}
+
 // Estimators of KL(pi || pi_ref) from the sampled token, d = logp - logp_ref, and their derivative
 // in logp: d; d^2 / 2; e^{-d} - 1 + d.
 __device__ __forceinline__ void post_kl(int estimator, float d, float &kl, float &grad) {
@@ -734,8 +741,8 @@ __device__ __forceinline__ DistillEntries distill_entries(const DistillParams &p
 #pragma unroll 4
     for (int k = lane; k < K; k += 32) {
         const float d = s_z[k] - m, lq = s_lq[k], pk = s != 0.f ? ex2_approx(d * p.c) * r : 0.f;
-        const float x = (d * p.inv_tau - ls) - lq, q = expf(lq), k3 = pk * post_k3(x), px = pk * x;
-        f += pk != 0.f ? k3 : q;  // (a NaN too)
+        const float x = (d * p.inv_tau - ls) - lq, px = pk * x;
+        f += post_k3_term(pk, expf(lq), x);
         a += pk != 0.f ? px : 0.f;
     }
 #pragma unroll
@@ -752,8 +759,7 @@ __device__ __forceinline__ DistillEntries distill_entries(const DistillParams &p
 // cancel for a student near its teacher. With the masses added and taken away,
 //   sum h ln(h / o) = sum [h ln(h / o) - h + o] + sum h - sum o = sum h k3(ln(h / o)) + sum h - sum o,
 // k3(d) = e^{-d} - 1 + d: no term is negative, and an error e of a logarithm enters as h (1 - o / h) e
-// and not as h e; a common one cancels. The difference of the masses is Q - 1, known in 64 bits; where
-// h = 0 the term is o.
+// and not as h e; a common one cancels. The difference of the masses is Q - 1, known to 1e-8 (distill_prep).
 
 // Forward, by one warp.
 __device__ __forceinline__ float distill_forward(const DistillParams &p, const DistillRow &r, const float *s_z, const float *s_lq,
@@ -763,15 +769,13 @@ __device__ __forceinline__ float distill_forward(const DistillParams &p, const D
 #pragma unroll 4
     for (int k = lane; k < p.K; k += 32) {
         const float d = s_z[k] - r.M, lq = s_lq[k], q = expf(lq);
-        const float k3 = q * post_k3(lq - (d * p.inv_tau - r.ls)), pk = ex2_approx(d * p.c) * r.inv_s;
-        sum += q != 0.f ? k3 : pk;
+        sum += post_k3_term(q, ex2_approx(d * p.c) * r.inv_s, lq - (d * p.inv_tau - r.ls));
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, off));
     float gap = rec.w;  // sum q - sum p
     if (p.tail && r.rest) {
-        const float lqo = logf(rec.z);
-        sum += rec.z != 0.f ? rec.z * post_k3(lqo - r.lpo) : r.po;
+        sum += post_k3_term(rec.z, r.po, logf(rec.z) - r.lpo);
     } else if (p.tail) {
         gap -= rec.z;  // the entries are the whole vocabulary: there is no further outcome
     } else {
@@ -796,7 +800,7 @@ __device__ __forceinline__ float distill_reverse(const DistillRow &r, const Dist
         sum = e.f + (e.mass * (y * u - post_k3(y)) - e.a * u);
     }
     float gap = rec.w;
-    if (r.rest) sum += r.po != 0.f ? r.po * post_k3(r.lpo - e.lqo) : rec.z;
+    if (r.rest) sum += post_k3_term(r.po, rec.z, r.lpo - e.lqo);
     else gap -= rec.z;
     return sum - gap;
 }

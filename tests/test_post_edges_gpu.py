@@ -236,3 +236,76 @@ def test_loss_with_kl_of_an_impossible_token(V, dtype, estimator, limit):
         dz = out["dlogits"][:, :V].double().cpu().numpy()
         on = np.arange(T) != t if coef else np.ones(T, bool)
         assert (np.abs(dz - d)[on] <= d_tol[on]).all()
+
+
+# ---------------------------------------------------------------- masses at the end of fp32's range
+
+DEEP = [60, 87, 89, 92, 95, 99, 102]  # -ln of a mass: the last ones are subnormal
+
+
+def deep_rows(V, what):
+    """Logits, teacher ids and log-probs of a row for each of DEEP, whose one mass is about e^-L."""
+    z, ids, vals = np.zeros((len(DEEP), V)), [], []
+    for row, L in zip(z, DEEP):
+        gap = L + round(math.log(V - 1))
+        if what == "po":        # the student's mass outside the teacher's entries
+            row[3] = gap
+            e = [(3, math.log(0.5)), (-1, -np.inf)]
+        elif what == "pk":      # the student's mass at one of them
+            row[5], row[7] = round(math.log(V)), round(math.log(V)) - L
+            e = [(5, math.log(0.3)), (7, math.log(0.3))]
+        elif what == "qk":      # the teacher's mass at one of them
+            row[5], row[7] = round(math.log(V)), round(math.log(V)) + 1
+            e = [(5, math.log(0.6)), (7, -float(L))]
+        else:                   # the teacher's remaining mass (its floor is that of the test)
+            row[5] = round(math.log(V))
+            e = [(5, 0.0), (-1, -np.inf)]
+        ids.append([i for i, _ in e])
+        vals.append([v for _, v in e])
+    return z, np.array(ids, np.int32), np.array(vals, np.float32)
+
+
+@pytest.mark.parametrize("what,mode,reverse", [("po", "tail", 1), ("pk", "tail", 1), ("qk", "tail", 0), ("qk", "renorm", 0),
+                                               ("qo", "tail", 0), ("po", "tail", 0), ("qk", "tail", 1)])
+@pytest.mark.parametrize("V,dtype", EVERY + [(9, "f32")])
+def test_distill_with_masses_at_the_end_of_the_range(V, dtype, what, mode, reverse):
+    """A term h ln(h / o) - h + o with h near 0 is near o: the divergence and the gradient stay finite."""
+    zn, ids, vals = deep_rows(V, what)
+    for floor in ([math.exp(-float(L)) for L in DEEP] if what == "qo" else [1e-6]):
+        check_distill(zn, ids, vals, dtype, mode, reverse, float(np.float32(floor)))
+
+
+@pytest.mark.parametrize("V,dtype", EVERY)
+def test_distill_with_a_mass_scaled_below_the_range(V, dtype):
+    """Reverse, where one of 300 entries has a mass whose exponential is in range and whose share of the sum is not."""
+    steps = [80, 84, 85, 86, 87]
+    zn = np.zeros((len(steps), V))
+    ids = np.tile(np.arange(300, dtype=np.int32), (len(steps), 1))
+    vals = np.full(ids.shape, math.log(0.4 / 299), np.float32)
+    vals[:, 299] = math.log(0.3)
+    for row, L in zip(zn, steps):
+        row[:299], row[299] = 4, 4 - L
+    check_distill(zn, ids, vals, dtype, "tail", 1, 1e-6)
+
+
+def check_distill(zn, ids, vals, dtype, mode, reverse, floor):
+    """One call, every row on, against 64 bits and the error model's bounds, which are finite."""
+    T, V = zn.shape
+    z = rows_of(T, V, dtype, NAN)
+    z[:, :V] = torch.from_numpy(zn).cuda().to(DT[dtype])
+    zf = z[:, :V].double().cpu().numpy()
+    assert np.array_equal(zf, zn)  # the steps are representable
+    mask, cu = np.ones(T, np.uint8), np.array([0, T], np.int32)
+    args = (ids, vals, mask, cu, mode, reverse, 1.0, 1.0, floor, True)
+    loss, kl, d = ph.distill(zf, *args)
+    loss_tol, kl_tol, d_tol = ph.distill_tol(zf, *args, dtype, kl, d)
+    assert np.isfinite(kl).all() and np.isfinite(d).all()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = capi.distill_loss(z, dev(ids), dev(vals), dev(mask), dev(cu), vocab=V, mode=mode,
+                            direction="reverse" if reverse else "forward", tail_floor=floor,
+                            loss_norm=capi.RL_NORM_PER_TOKEN, device_status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert (np.abs(out["kl"].double().cpu().numpy() - kl) <= kl_tol).all()
+    assert abs(out["loss"].item() - loss) <= loss_tol + ph.U * abs(loss)
+    assert (np.abs(out["dlogits"][:, :V].double().cpu().numpy() - d) <= d_tol).all()
