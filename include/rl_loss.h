@@ -463,7 +463,8 @@ typedef struct rl_loss_distill_config {
     int32_t loss_norm;    /* rl_loss_norm */
     float temperature;    /* > 0 */
     float scale;          /* factor of the loss, e.g. temperature^2; finite */
-    float tail_floor;     /* in [0, 1): lower bound of q_o (RL_DISTILL_TAIL) */
+    float tail_floor;     /* in [0, 1): lower bound of q_o (RL_DISTILL_TAIL). With reverse, pass one above 0 (1e-9):
+                             entries that sum to 1 in fp32 leave q_o = 0, and KL(p || q) is then infinite */
 } rl_loss_distill_config;
 
 /* Largest k (1024). */

@@ -95,6 +95,7 @@ RL_DISTILL_RENORM, RL_DISTILL_TAIL = 0, 1
 RL_PREF_SIGMOID, RL_PREF_HINGE, RL_PREF_IPO = 0, 1, 2
 KL_ESTIMATORS = {"k1": RL_KL_K1, "k2": RL_KL_K2, "k3": RL_KL_K3}
 DISTILL_MODES = {"renorm": RL_DISTILL_RENORM, "tail": RL_DISTILL_TAIL}
+REVERSE_TAIL_FLOOR = 1e-9  # distill_loss's default; 1 - sum q of fp32 log-probs is known to some 1e-8
 PREF_LOSSES = {"sigmoid": RL_PREF_SIGMOID, "hinge": RL_PREF_HINGE, "ipo": RL_PREF_IPO}
 
 
@@ -455,18 +456,22 @@ def token_logp(logits, targets, mask=None, *, vocab: int | None = None, logp=Non
 
 
 def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: int | None = None, mode: str = "renorm",
-                 direction: str = "forward", temperature: float = 1.0, scale: float = 1.0, tail_floor: float = 0.0,
+                 direction: str = "forward", temperature: float = 1.0, scale: float = 1.0, tail_floor: float | None = None,
                  loss_norm: int = RL_NORM_PER_RESPONSE, loss=None, loss_f64=None, dlogits=None, kl=None, workspace=None,
                  device_status=None, stream=None) -> dict:
     """Distillation from a teacher's top logits, forward and backward: teacher_ids / teacher_vals [T, K] hold
     each row's entries (id -1: padding). mode "renorm" takes logits already divided by the temperature or
     log-probs, "tail" log-probs at the temperature (what they leave of the mass is one more outcome);
-    direction "forward" is KL(teacher || student), "reverse" KL(student || teacher) ("tail" only). Returns
+    direction "forward" is KL(teacher || student), "reverse" KL(student || teacher) ("tail" only). tail_floor
+    bounds the teacher's remaining mass from below: 1e-9 in the reverse direction unless given, as an entry's
+    log-prob of -0.0, or entries that sum to 1 in fp32, leave 0 and the divergence would be infinite; else 0. Returns
     loss [1], kl [T] and dlogits (allocated where not given; dlogits may be logits itself). A workspace that is
     passed serves one call at a time: threads pass one each."""
     import torch
     if mode not in DISTILL_MODES or direction not in ("forward", "reverse"):
         raise ValueError("mode is 'renorm' or 'tail', direction 'forward' or 'reverse'")
+    if tail_floor is None:
+        tail_floor = REVERSE_TAIL_FLOOR if direction == "reverse" else 0.0
     if dlogits is None:
         with _allocations_of(stream, logits.device):
             dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)

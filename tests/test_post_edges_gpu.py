@@ -309,3 +309,22 @@ def check_distill(zn, ids, vals, dtype, mode, reverse, floor):
     assert (np.abs(out["kl"].double().cpu().numpy() - kl) <= kl_tol).all()
     assert abs(out["loss"].item() - loss) <= loss_tol + ph.U * abs(loss)
     assert (np.abs(out["dlogits"][:, :V].double().cpu().numpy() - d) <= d_tol).all()
+
+
+@pytest.mark.parametrize("V,dtype", EVERY)
+def test_reverse_distillation_of_a_certain_teacher(V, dtype):
+    """Teacher rows whose entries sum to 1 or more in fp32, under the defaults: finite, and the floor's values."""
+    T, K = 4, 3
+    z = random_rows(T, V, dtype, V)
+    ids = np.array([[5, 1, 2], [7, -1, -1], [0, 3, 4], [8, 6, 2]], np.int32)
+    vals = np.array([[0.0, -30.0, -40.0], [0.0, -np.inf, -np.inf], np.log([0.5, 0.25, 0.25]), np.log([0.6, 0.2, 0.1])], np.float32)
+    mask, cu = np.ones(T, np.uint8), np.array([0, T], np.int32)
+    call = lambda **kw: capi.distill_loss(z, dev(ids), dev(vals), dev(mask), dev(cu), vocab=V, mode="tail",
+                                          loss_norm=capi.RL_NORM_PER_TOKEN, **kw)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = call(direction="reverse", device_status=st)
+    assert st.item() == 0 and torch.isfinite(out["loss"]).all()
+    assert torch.isfinite(out["kl"]).all() and torch.isfinite(out["dlogits"][:, :V].float()).all()
+    same = call(direction="reverse", tail_floor=1e-9)
+    assert torch.equal(out["kl"], same["kl"]) and torch.equal(out["dlogits"][:, :V], same["dlogits"][:, :V])
+    assert torch.equal(call()["kl"], call(tail_floor=0.0)["kl"])  # forward: no floor
