@@ -267,6 +267,10 @@ __device__ __forceinline__ void logp_write(const LogpParams &p, const RowMeta<kO
     if (p.stats) p.stats[t] = make_float2(st.m, st.s);
 }
 
+// The teacher gives the row no mass: it contributes nothing, once its ids have been looked at like any row's.
+constexpr float kNoMass = -1.f;  // Q - 1 of such a row (distill_prep)
+__device__ __forceinline__ bool no_mass(const RowMeta<kOpDistill> &m) { return m.rec.w == kNoMass; }
+
 // The results of a distilled row t, by one warp, and its term of the loss.
 __device__ __forceinline__ PostTerm distill_write(const DistillParams &p, const RowMeta<kOpDistill> &meta, int t, bool live, bool dup,
                                                   const DistillRow &row, float kl) {
@@ -406,8 +410,6 @@ __device__ __forceinline__ RowMeta<OP> load_meta(const typename OpParams<OP>::ty
         if (m.read) {
             m.rec = p.rec[t];
             m.w = 1.f / (p.per_token ? (float)N : (float)p.r.S * (float)p.seq_n[i]);
-            // a teacher that gives the row no mass: it contributes nothing
-            if (m.rec.w == -1.f) m.read = 0;
         }
         m.copied = m.read;
     }
@@ -803,7 +805,7 @@ ring_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, const __
                 if (writes) add_term(p, pend, t, term);
                 if (meta.last) flush_rows(p, pend);
             } else if constexpr (OP == kOpDistill) {
-                const bool live = read && !dup;
+                const bool live = read && !dup && !no_mass(meta);
                 DistillRow row{};
                 if (live) row = distill_finish(p, st, entries, meta.rec, meta.w * p.scale * p.inv_tau, V - meta.have);
                 if (lane == 0) {
@@ -1143,7 +1145,8 @@ line_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, int stri
         // the row's results
         RowGrad gr{0.f, 0.f, 0.f, -1};
         DistillRow row{};
-        const bool live = read && !dup;
+        bool live = read && !dup;
+        if constexpr (OP == kOpDistill) live = live && !no_mass(meta);
         if constexpr (OP == kOpLogp) {
             if (lane == 0) logp_write<kEnt>(p, meta, st, t);
         } else if constexpr (OP == kOpPolicy) {
@@ -1380,7 +1383,7 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
         st = block_merge<false>(st, s_warp, p.c);
         const int n_i = p.seq_n[i];
         const float w = 1.f / (p.per_token ? (float)N : (float)p.r.S * (float)n_i);
-        const bool none = have == 0 || rec.w == -1.f;  // the teacher gives the row no mass
+        const bool none = have == 0 || rec.w == kNoMass;
         if (bad || none) {  // excluded: contributes nothing
             if (threadIdx.x == 0) {
                 if (bad) post_raise(p.r.status, RL_ERR_TARGET_RANGE);

@@ -328,3 +328,31 @@ def test_reverse_distillation_of_a_certain_teacher(V, dtype):
     same = call(direction="reverse", tail_floor=1e-9)
     assert torch.equal(out["kl"], same["kl"]) and torch.equal(out["dlogits"][:, :V], same["dlogits"][:, :V])
     assert torch.equal(call()["kl"], call(tail_floor=0.0)["kl"])  # forward: no floor
+
+
+@pytest.mark.parametrize("mode", ["renorm", "tail"])
+@pytest.mark.parametrize("V,dtype", EVERY)
+def test_distill_bad_ids_of_rows_without_mass(V, dtype, mode):
+    """A bad id is reported whatever its row's values are: also where these leave the row no mass."""
+    ids = np.array([[-2, -1, -1], [V, -1, -1], [4, 9, 4], [V - 1, -1, V - 1], [-1, -1, -1], [3, 1, V - 1], [2, 7, 1]], np.int32)
+    vals = np.full(ids.shape, -np.inf, np.float32)
+    vals[6] = np.log([0.5, 0.2, 0.1])
+    T = len(ids)
+    mask, cu = np.ones(T, np.uint8), np.array([0, T], np.int32)
+    z = random_rows(T, V, dtype, V)
+    for rows, bits in (([0, 5, 6], BIT["RL_ERR_TARGET_RANGE"]), ([1, 6], BIT["RL_ERR_TARGET_RANGE"]),
+                       ([2, 6], BIT["RL_ERR_TARGET_RANGE"]), ([3, 6], BIT["RL_ERR_TARGET_RANGE"]), ([4, 5, 6], 0)):
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        n = len(rows)
+        out = capi.distill_loss(z[rows].contiguous(), dev(ids[rows]), dev(vals[rows]), dev(mask[:n]),
+                                dev([0, n], torch.int32), vocab=V, mode=mode, device_status=st)
+        kl, dz = out["kl"].cpu(), out["dlogits"][:, :V]
+        assert st.item() == bits, rows
+        for i, t in enumerate(rows):
+            if t < 4:
+                assert math.isnan(kl[i].item()) and not dz[i].any()
+            elif t == 4 or (t == 5 and mode == "renorm"):
+                assert kl[i].item() == 0.0 and not dz[i].any()
+            else:
+                assert math.isfinite(kl[i].item()) and dz[i].any()
+        assert torch.isfinite(out["loss"]).all()
