@@ -616,7 +616,7 @@ __device__ __forceinline__ PolicyTok policy_load(const PolicyParams &p, int t, i
         k.pre |= in_bounds ? RL_FLAG_POP_IN_BOUNDS : 0u;
         k.lref = lo;
         const float pop = in && in_bounds ? (p.c.pop_indicator ? 1.f : expf(d)) : 0.f;
-        k.cf = p.c.adv_teacher ? pop : pop * A;
+        k.cf = p.c.adv_teacher || pop == 0.f ? pop : pop * A;  // what a token left out has for an advantage does not matter
     }
     k.wcf = k.w * k.cf;
     return k;

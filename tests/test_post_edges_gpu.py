@@ -356,3 +356,53 @@ def test_distill_bad_ids_of_rows_without_mass(V, dtype, mode):
             else:
                 assert math.isfinite(kl[i].item()) and dz[i].any()
         assert torch.isfinite(out["loss"]).all()
+
+
+# ---------------------------------------------------------------- what masked and popped tokens hold
+
+@pytest.mark.parametrize("V,dtype", EVERY)
+@pytest.mark.parametrize("adv_mode", [capi.RL_ADV_PER_TOKEN, capi.RL_ADV_TEACHER_LOGP])
+@pytest.mark.parametrize("objective", [capi.RL_OBJ_GRPO_ICEPOP, capi.RL_OBJ_DIS])
+def test_loss_with_kl_of_masked_tokens_that_hold_nan(V, dtype, adv_mode, objective):
+    """Masked tokens' inputs, and advantages of tokens that are popped or have a bad target, may be NaN or infinite."""
+    if objective == capi.RL_OBJ_DIS and adv_mode == capi.RL_ADV_TEACHER_LOGP:
+        pytest.skip("not a configuration")
+    T = 8
+    z = random_rows(T, V, dtype, V)
+    y = (np.arange(T) * 31 + 4) % V
+    y[6] = V
+    mask = np.array([1, 0, 1, 0, 1, 1, 1, 0], np.uint8)
+    logp = torch.log_softmax(z[:, :V].double(), 1).cpu().numpy()[np.arange(T), np.minimum(y, V - 1)].astype(np.float32)
+    old, infer, ref, adv = (x.copy() for x in (logp + 0.1, logp + 0.1, logp - 0.2, np.linspace(-1, 1, T).astype(np.float32)))
+    if adv_mode == capi.RL_ADV_TEACHER_LOGP:
+        adv += logp
+    infer[5] = infer[5] + 3.0  # popped (outside the interval with the other objective)
+    code = capi.RL_BF16 if dtype == "bf16" else capi.RL_F32
+    rl = capi.RlLoss(V, 1, T, 1, code, adv_mode=adv_mode, objective=objective)
+
+    def call(old, infer, ref, adv, z):
+        out = dict(loss=torch.empty(1, device="cuda"), loss_f64=torch.empty(1, dtype=torch.float64, device="cuda"),
+                   dlogits=torch.zeros_like(z), kl=torch.empty(T, device="cuda"), mean_kl=torch.empty(1, device="cuda"),
+                   counts=torch.empty(4, dtype=torch.int32, device="cuda"))
+        rl.forward_backward_kl(z, dev(y, torch.int32), dev(old), dev(infer), dev(mask), dev([0, T], torch.int32), dev(adv),
+                               dev(ref), kl_coef=0.1, kl_estimator="k3", **out)
+        torch.cuda.synchronize()
+        assert rl.device_status() == BIT["RL_ERR_TARGET_RANGE"]
+        return out
+
+    want = call(old, infer, ref, adv, z)
+    off = mask == 0
+    for bad in (NAN, math.inf, -math.inf):
+        a = [x.copy() for x in (old, infer, ref, adv)]
+        for x in a:
+            x[off] = bad
+        a[3][[5, 6]] = bad
+        zb = z.clone()
+        zb[torch.from_numpy(off).cuda()] = bad
+        got = call(*a, zb)
+        on = torch.arange(T) != 6  # the bad target's estimate is NaN
+        assert torch.isfinite(want["loss"]).all()
+        for name in want:
+            pick = (lambda x: x[on.cuda()]) if name == "kl" else lambda x: x
+            assert torch.equal(pick(got[name]), pick(want[name])), (name, bad)
+    rl.close()
