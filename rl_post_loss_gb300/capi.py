@@ -403,6 +403,30 @@ def _vector(name: str, t, n: int, dtype, device, optional: bool = False):
     return t.data_ptr()
 
 
+def _rows(name: str, t, rows: int, cols: int, dtype, device):
+    """The pointer and row stride of a 2-D tensor argument after checking its type, shape, place and layout."""
+    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != device.index or t.shape[0] < rows \
+            or t.shape[1] < cols or t.stride(1) != 1:
+        raise ValueError(f"{name} is a {dtype} tensor [at least {rows}, at least {cols}] with contiguous rows on {device}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _status_word(t, device):
+    """The pointer of a call's optional status word, 32 bits on the device."""
+    if t is None:
+        return None
+    if t.is_floating_point() or t.element_size() != 4 or t.numel() < 1 or t.get_device() != device.index:
+        raise ValueError(f"device_status is a torch.int32 or torch.uint32 tensor of one value on {device}")
+    return t.data_ptr()
+
+
+def _workspace_of(t, device):
+    """The pointer and bytes of a workspace that the caller passed."""
+    if t.get_device() != device.index or not t.is_contiguous():
+        raise ValueError(f"workspace is a contiguous tensor on {device}, of any type")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 _NO_CONTEXT = contextlib.nullcontext()
 
 
@@ -428,10 +452,6 @@ def _current_stream(device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
 def token_logp(logits, targets, mask=None, *, vocab: int | None = None, logp=None, entropy=None,
                want_entropy: bool = False, device_status=None, stream=None):
     """Log-probs (and entropies) of the target tokens on the GPU, without a gradient: the pass of a reference
@@ -450,7 +470,8 @@ def token_logp(logits, targets, mask=None, *, vocab: int | None = None, logp=Non
     _check(load().rl_loss_token_logp(code, T, V, logits.data_ptr(), logits.stride(0) if T else V,
                                      _vector("targets", targets, T, torch.int32, dev),
                                      _vector("mask", mask, T, torch.uint8, dev, True), _vector("logp", logp, T, f32, dev),
-                                     _vector("entropy", entropy, T, f32, dev, True), _addr(device_status), stream),
+                                     _vector("entropy", entropy, T, f32, dev, True), _status_word(device_status, dev),
+                                     stream),
            "rl_loss_token_logp")
     return logp, entropy
 
@@ -496,8 +517,8 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
                                   _vector("cu_seqlens", cu_seqlens, S + 1, torch.int32, dev),
                                   _vector("loss", loss, 1, f32, dev),
                                   _vector("loss_f64", loss_f64, 1, torch.float64, dev, True), dlogits.data_ptr(),
-                                  dlogits.stride(0), _vector("kl", kl, T, f32, dev), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _addr(device_status), stream),
+                                  dlogits.stride(0), _vector("kl", kl, T, f32, dev), *_workspace_of(workspace, dev),
+                                  _status_word(device_status, dev), stream),
            "rl_loss_distill")
     return {"loss": loss, "kl": kl, "dlogits": dlogits}
 
@@ -536,8 +557,8 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
                                      _vector("loss_f64", loss_f64, 1, torch.float64, dev, True), dlogits.data_ptr(),
                                      dlogits.stride(0), _vector("logp", logp, T, f32, dev),
                                      _vector("seq_logratio", seq_logratio, S, f32, dev),
-                                     _vector("pair_loss", pair_loss, S // 2, f32, dev), workspace.data_ptr(),
-                                     workspace.numel() * workspace.element_size(), _addr(device_status), stream),
+                                     _vector("pair_loss", pair_loss, S // 2, f32, dev), *_workspace_of(workspace, dev),
+                                     _status_word(device_status, dev), stream),
            "rl_loss_preference")
     return {"loss": loss, "logp": logp, "seq_logratio": seq_logratio, "pair_loss": pair_loss, "dlogits": dlogits}
 
@@ -627,14 +648,23 @@ class RlLoss:
         import torch
         if kl_estimator not in KL_ESTIMATORS:
             raise ValueError("kl_estimator is 'k1', 'k2' or 'k3'")
-        T = int(targets.shape[0])
-        dev, f32 = targets.device, torch.float32
-        inp = rl_loss_inputs(T, cu_seqlens.shape[0] - 1, logits.stride(0) if logits.dim() == 2 else 0,
-                             logits.data_ptr(), targets.data_ptr(), logp_old.data_ptr(), logp_infer.data_ptr(),
-                             mask.data_ptr(), cu_seqlens.data_ptr(), rewards_or_adv.data_ptr())
-        out = rl_loss_outputs(loss.data_ptr(), _addr(loss_f64), dlogits.data_ptr(),
-                              dlogits.stride(0) if dlogits.dim() == 2 else 0, _addr(logp), _addr(entropy),
-                              _addr(flags), _addr(seq_adv), _addr(counts), _addr(mean_entropy))
+        if not logits.is_cuda:
+            raise ValueError("logits is a CUDA tensor [tokens, vocabulary] of the handle's type")
+        T, S, V = int(targets.shape[0]), cu_seqlens.shape[0] - 1, self.config.vocab_size
+        dev, f32, i32, u8 = logits.device, torch.float32, torch.int32, torch.uint8
+        dt = torch.bfloat16 if self.config.logits_dtype == RL_BF16 else f32
+        z, ld = _rows("logits", logits, T, V, dt, dev)
+        dz, ldd = _rows("dlogits", dlogits, T, V, dt, dev)
+        inp = rl_loss_inputs(T, S, ld, z, _vector("targets", targets, T, i32, dev), _vector("logp_old", logp_old, T, f32, dev),
+                             _vector("logp_infer", logp_infer, T, f32, dev), _vector("mask", mask, T, u8, dev),
+                             _vector("cu_seqlens", cu_seqlens, S + 1, i32, dev),
+                             _vector("rewards_or_adv", rewards_or_adv, T if self.config.adv_mode >= RL_ADV_PER_TOKEN else S,
+                                     f32, dev))
+        out = rl_loss_outputs(_vector("loss", loss, 1, f32, dev), _vector("loss_f64", loss_f64, 1, torch.float64, dev, True),
+                              dz, ldd, _vector("logp", logp, T, f32, dev, True),
+                              _vector("entropy", entropy, T, f32, dev, True), _vector("flags", flags, T, u8, dev, True),
+                              _vector("seq_adv", seq_adv, S, f32, dev, True), _vector("counts", counts, 4, i32, dev, True),
+                              _vector("mean_entropy", mean_entropy, 1, f32, dev, True))
         term = rl_loss_kl(_vector("logp_ref", logp_ref, T, f32, dev), kl_coef, KL_ESTIMATORS[kl_estimator],
                           _vector("kl", kl, T, f32, dev, True), _vector("mean_kl", mean_kl, 1, f32, dev, True))
         if stream is None:

@@ -406,3 +406,61 @@ def test_loss_with_kl_of_masked_tokens_that_hold_nan(V, dtype, adv_mode, objecti
             pick = (lambda x: x[on.cuda()]) if name == "kl" else lambda x: x
             assert torch.equal(pick(got[name]), pick(want[name])), (name, bad)
     rl.close()
+
+
+# ---------------------------------------------------------------- arguments
+
+def test_wrong_status_words_and_workspaces_are_refused():
+    z = torch.zeros(4, 64, device="cuda")
+    y = torch.zeros(4, dtype=torch.int32, device="cuda")
+    m = torch.ones(4, dtype=torch.uint8, device="cuda")
+    cu = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    ids, vals = y.view(4, 1), torch.zeros(4, 1, device="cuda")
+    calls = [lambda **kw: capi.token_logp(z, y, m, **kw), lambda **kw: capi.distill_loss(z, ids, vals, m, cu, **kw),
+             lambda **kw: capi.preference_loss(z, y, None, m, cu, **kw)]
+    for call in calls:
+        for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"),
+                    torch.zeros(1, dtype=torch.int64, device="cuda")):
+            with pytest.raises(ValueError, match="device_status"):
+                call(device_status=bad)
+        call(device_status=torch.zeros(1, dtype=torch.uint32, device="cuda"))
+    for call in calls[1:]:
+        big = torch.zeros(1 << 17, dtype=torch.uint8, device="cuda")
+        for bad in (torch.zeros(1 << 16, dtype=torch.uint8), big[::2]):
+            with pytest.raises(ValueError, match="workspace"):
+                call(workspace=bad)
+        call(workspace=big.view(torch.float32))
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("adv_mode", [capi.RL_ADV_GROUP_REWARDS, capi.RL_ADV_PER_TOKEN])
+def test_loss_with_kl_refuses_wrong_tensors(adv_mode):
+    T, S, V = 6, 2, 64
+    f = lambda n: torch.zeros(n, device="cuda")
+    rl = capi.RlLoss(V, 2, T, S, capi.RL_F32, adv_mode=adv_mode)
+    good = dict(logits=torch.zeros(T, V, device="cuda"), targets=torch.zeros(T, dtype=torch.int32, device="cuda"), logp_old=f(T),
+                logp_infer=f(T), mask=torch.ones(T, dtype=torch.uint8, device="cuda"),
+                cu_seqlens=torch.tensor([0, 2, T], dtype=torch.int32, device="cuda"),
+                rewards_or_adv=f(T if adv_mode >= capi.RL_ADV_PER_TOKEN else S), logp_ref=f(T), loss=f(1),
+                loss_f64=torch.zeros(1, dtype=torch.float64, device="cuda"), dlogits=torch.zeros(T, V, device="cuda"), logp=f(T),
+                entropy=f(T), flags=torch.zeros(T, dtype=torch.uint8, device="cuda"), seq_adv=f(S),
+                counts=torch.zeros(4, dtype=torch.int32, device="cuda"), mean_entropy=f(1), kl=f(T), mean_kl=f(1))
+    call = lambda **over: rl.forward_backward_kl(**{**good, **over}, kl_coef=0.1)
+    call()
+    for name, t in good.items():
+        flat = t.dim() == 1
+        bad = [t.cpu(), t.double() if t.dtype != torch.float64 else t.float()]
+        if name not in ("targets", "cu_seqlens"):  # these say how many tokens and responses there are
+            bad.append(t[:-1])
+        bad.append(torch.zeros(2 * len(t), dtype=t.dtype, device="cuda")[::2] if flat and len(t) > 1 else t[:0])
+        if not flat:
+            bad += [t[:, :V - 1], torch.zeros(V, T, device="cuda").t(), t.bfloat16()]
+        if name in ("targets", "mask"):
+            bad.append(t.long() if name == "targets" else t.bool())
+        for b in bad:
+            with pytest.raises(ValueError, match=name if name != "logits" else "logits|CUDA"):
+                call(**{name: b})
+    call()
+    torch.cuda.synchronize()
+    assert rl.device_status() == 0
+    rl.close()
