@@ -439,6 +439,17 @@ def _allocations_of(stream, device):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device))
 
 
+def _gradient_of(logits, V: int, stream):
+    """A gradient laid out like the logits. Calls do not write its columns past the vocabulary, which a product with
+    the whole of it reads: they are 0."""
+    import torch
+    with _allocations_of(stream, logits.device):
+        dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
+        if V < logits.shape[1]:
+            dlogits[:, V:].zero_()
+    return dlogits
+
+
 def _missing(tensors: tuple, sizes: tuple, device) -> list:
     """The fp32 tensors as they were given, new ones in the place of those that were not. (An allocation takes
     1.5 us of host time; one for all of them takes 10, as a tensor is then split.)"""
@@ -486,17 +497,17 @@ def distill_loss(logits, teacher_ids, teacher_vals, mask, cu_seqlens, *, vocab: 
     direction "forward" is KL(teacher || student), "reverse" KL(student || teacher) ("tail" only). tail_floor
     bounds the teacher's remaining mass from below: 1e-9 in the reverse direction unless given, as an entry's
     log-prob of -0.0, or entries that sum to 1 in fp32, leave 0 and the divergence would be infinite; else 0. Returns
-    loss [1], kl [T] and dlogits (allocated where not given; dlogits may be logits itself). A workspace that is
-    passed serves one call at a time: threads pass one each."""
+    loss [1], kl [T] and dlogits (allocated where not given; a new dlogits is 0 past the vocabulary, one that is given
+    is not written there; dlogits may be logits itself). A workspace that is passed serves one call at a time:
+    threads pass one each."""
     import torch
     if mode not in DISTILL_MODES or direction not in ("forward", "reverse"):
         raise ValueError("mode is 'renorm' or 'tail', direction 'forward' or 'reverse'")
     if tail_floor is None:
         tail_floor = REVERSE_TAIL_FLOOR if direction == "reverse" else 0.0
-    if dlogits is None:
-        with _allocations_of(stream, logits.device):
-            dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
     code, V = _logits_code(logits, vocab, dlogits)
+    if dlogits is None:
+        dlogits = _gradient_of(logits, V, stream)
     T, S, dev, f32 = logits.shape[0], cu_seqlens.shape[0] - 1, logits.device, torch.float32
     for name, t, dt in (("teacher_ids", teacher_ids, torch.int32), ("teacher_vals", teacher_vals, f32)):
         if t.dtype != dt or t.dim() != 2 or t.shape[0] < T or t.device != dev or t.stride(1) != 1:
@@ -530,15 +541,15 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
                     stream=None) -> dict:
     """Preference loss over pairs of responses (2j preferred to 2j + 1), forward and backward. logp_ref [T] are
     the reference policy's log-probs (None: no reference). Returns loss [1], logp [T], seq_logratio [S],
-    pair_loss [S / 2] and dlogits (allocated where not given; dlogits may be logits itself). A workspace that is
-    passed serves one call at a time: threads pass one each."""
+    pair_loss [S / 2] and dlogits (allocated where not given; a new dlogits is 0 past the vocabulary, one that is given
+    is not written there; dlogits may be logits itself). A workspace that is passed serves one call at a time:
+    threads pass one each."""
     import torch
     if loss_type not in PREF_LOSSES:
         raise ValueError("loss_type is 'sigmoid', 'hinge' or 'ipo'")
-    if dlogits is None:
-        with _allocations_of(stream, logits.device):
-            dlogits = torch.empty_strided(logits.shape, logits.stride(), dtype=logits.dtype, device=logits.device)
     code, V = _logits_code(logits, vocab, dlogits)
+    if dlogits is None:
+        dlogits = _gradient_of(logits, V, stream)
     T, S, dev, f32 = logits.shape[0], cu_seqlens.shape[0] - 1, logits.device, torch.float32
     with _allocations_of(stream, dev):
         P = max(S // 2, 0)

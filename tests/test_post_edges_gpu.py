@@ -464,3 +464,26 @@ def test_loss_with_kl_refuses_wrong_tensors(adv_mode):
     torch.cuda.synchronize()
     assert rl.device_status() == 0
     rl.close()
+
+
+@pytest.mark.parametrize("V,dtype", EVERY)
+def test_a_new_gradient_is_zero_past_the_vocabulary(V, dtype):
+    """Where the memory it is given held NaN, also on a stream that is not the current one."""
+    T = 6
+    z = random_rows(T, V, dtype, V)
+    assert z.shape[1] > V
+    y, m = dev((np.arange(T) * 7) % V, torch.int32), dev(np.ones(T), torch.uint8)
+    cu, ids, vals = dev([0, 2, T], torch.int32), dev(np.ones((T, 1)), torch.int32), dev(np.full((T, 1), -1.0), torch.float32)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side.cuda_stream):
+        for call in (lambda: capi.distill_loss(z, ids, vals, m, cu, vocab=V, mode="tail", stream=stream),
+                     lambda: capi.preference_loss(z, y, None, m, cu, vocab=V, stream=stream)):
+            with torch.cuda.stream(side if stream else torch.cuda.current_stream()):
+                held = torch.full_like(z, NAN)
+            at = held.data_ptr()
+            del held
+            out = call()
+            torch.cuda.synchronize()
+            assert out["dlogits"].data_ptr() == at
+            assert not out["dlogits"][:, V:].any() and torch.isfinite(out["dlogits"].float()).all()
