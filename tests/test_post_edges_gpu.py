@@ -487,3 +487,81 @@ def test_a_new_gradient_is_zero_past_the_vocabulary(V, dtype):
             torch.cuda.synchronize()
             assert out["dlogits"].data_ptr() == at
             assert not out["dlogits"][:, V:].any() and torch.isfinite(out["dlogits"].float()).all()
+
+
+# ---------------------------------------------------------------- accuracy
+
+@pytest.mark.parametrize("gap", [20.0, 30.0, 40.0])
+@pytest.mark.parametrize("V,dtype", EVERY)
+def test_confident_rows_keep_their_digits(V, dtype, gap):
+    """One logit above V - 1 zeros: ln p = -log1p((V - 1) e^-gap), down to -e^-30. The others' sum is exact and the
+    exponential's argument rounded twice, 2 U gap relative, and its result and the logarithm's 8 U; the gradient at
+    the sampled entry is that times a coefficient of a dozen more roundings."""
+    T = 2
+    y = np.array([17, V - 3])
+    z = rows_of(T, V, dtype)
+    z[torch.arange(T), torch.from_numpy(y)] = gap
+    lp = -math.log1p((V - 1) * math.exp(-gap))
+    rel = (2 * gap + 8) * ph.U
+    logp, _ = capi.token_logp(z, dev(y, torch.int32), vocab=V)
+    assert np.abs(logp.double().cpu().numpy() / lp - 1).max() <= rel
+    rest = -math.expm1(lp)  # 1 - p
+    half = ph.half_step(dtype)
+
+    def at(dz):
+        return dz[torch.arange(T), torch.from_numpy(y)].double().cpu().numpy()
+
+    out, bits = policy(z, V, y, [0, T], [1.0], np.zeros(T), np.zeros(T), coef=0.0, adv_mode=capi.RL_ADV_PER_SEQ)
+    assert bits == 0
+    assert np.abs(out["logp"].double().cpu().numpy() / lp - 1).max() <= rel
+    assert np.abs(at(out["dlogits"]) / (-math.exp(lp) / T * rest) - 1).max() <= rel + 12 * ph.U + half
+    out = capi.preference_loss(z, dev(y, torch.int32), None, dev(np.ones(T), torch.uint8), dev([0, 1, 2], torch.int32),
+                               vocab=V, beta=0.3)
+    assert np.abs(at(out["dlogits"]) / (0.15 * rest * np.array([-1, 1])) - 1).max() <= rel + 12 * ph.U + half
+
+
+@pytest.mark.parametrize("T,V,dtype", [(64, 1003, "bf16"), (64, 6144, "f32"), (64, 12288, "bf16"), (64, 20011, "bf16"),
+                                       (600, 32003, "f32"), (64, 151552, "bf16"), (700, 151552, "bf16"), (40, 600001, "f32")])
+def test_token_logp_error_is_that_of_a_tree(T, V, dtype):
+    """A lane folds at most 20 batches in sequence (a ring's slice is at most 20 batches of 1024 entries for each of
+    eight warps), and the rest are trees: 36 additions on a term's way, up to eight moves of the reference and three
+    merges of 6 U each, 4 U for an exponential and 2 U of its argument's size. So no row is off by more than
+    (100 + 2 mean|d|) U and its own rounding; and where the roundings are independent (0.6 U each) the rms is below
+    4 U, with the result's rounding at |logp| of 8 to 16 (4.6 U) and the exponential's bias (1 U) below 8 U: 16 U
+    leaves a factor of two."""
+    z = random_rows(T, V, dtype, T + V)
+    z[:, :V] -= (1.1 * torch.log(torch.arange(1.0, V + 1, device="cuda"))).to(z.dtype)
+    y = np.random.default_rng(V).integers(0, V, T)
+    logp, ent = capi.token_logp(z, dev(y, torch.int32), vocab=V, want_entropy=True)
+    r = ph.Rows(z[:, :V].double().cpu().numpy())
+    lp = r.lp[np.arange(T), y]
+    err = logp.double().cpu().numpy() - lp
+    assert (np.abs(err) <= (100 + 2 * r.mean_d + np.abs(lp)) * ph.U).all()
+    assert math.sqrt((err ** 2).mean()) <= 16 * ph.U * max(1.0, np.abs(lp).max() / 16)
+    err = ent.double().cpu().numpy() - r.entropy
+    assert (np.abs(err) <= (100 + 2 * r.mean_d) * (1 + r.mean_d) * ph.U).all()
+    assert math.sqrt((err ** 2).mean()) <= 16 * ph.U * (1 + r.mean_d.max())
+
+
+# ---------------------------------------------------------------- graphs
+
+@pytest.mark.parametrize("T,V,dtype", [(40, 40001, "bf16"), (8, 151552, "bf16"), (1200, 32768, "bf16"), (4, 600001, "f32"),
+                                       (60, 20011, "f32")])
+def test_long_rows_captured_in_a_graph(T, V, dtype):
+    """Rows over rings, one CTA or a cluster each, with the launches that begin while the one before ends."""
+    import test_post_ops_gpu as ops
+    for name, op in ops._everything(2, T, V, dtype):
+        want = op()
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = op()
+        for _ in range(3):
+            for t in got.values():
+                t.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert ops._same(want, got), name
+        del graph
