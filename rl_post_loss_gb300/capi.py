@@ -405,10 +405,11 @@ def _vector(name: str, t, n: int, dtype, device, optional: bool = False):
 
 def _rows(name: str, t, rows: int, cols: int, dtype, device):
     """The pointer and row stride of a 2-D tensor argument after checking its type, shape, place and layout."""
-    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != device.index or t.shape[0] < rows \
-            or t.shape[1] < cols or t.stride(1) != 1:
-        raise ValueError(f"{name} is a {dtype} tensor [at least {rows}, at least {cols}] with contiguous rows on {device}")
-    return t.data_ptr(), t.stride(0)
+    if t.dtype is dtype and t.dim() == 2 and t.get_device() == device.index:
+        (have, width), (ld, step) = t.shape, t.stride()
+        if have >= rows and width >= cols and step == 1:
+            return t.data_ptr(), ld
+    raise ValueError(f"{name} is a {dtype} tensor [at least {rows}, at least {cols}] with contiguous rows on {device}")
 
 
 def _status_word(t, device):
@@ -661,7 +662,7 @@ class RlLoss:
             raise ValueError("kl_estimator is 'k1', 'k2' or 'k3'")
         if not logits.is_cuda:
             raise ValueError("logits is a CUDA tensor [tokens, vocabulary] of the handle's type")
-        T, S, V = int(targets.shape[0]), cu_seqlens.shape[0] - 1, self.config.vocab_size
+        T, S, V = targets.numel(), cu_seqlens.numel() - 1, self.config.vocab_size
         dev, f32, i32, u8 = logits.device, torch.float32, torch.int32, torch.uint8
         dt = torch.bfloat16 if self.config.logits_dtype == RL_BF16 else f32
         z, ld = _rows("logits", logits, T, V, dt, dev)
