@@ -394,9 +394,12 @@ RL_LOSS_API rl_status rl_topk(const rl_topk_config *config, int32_t rows, const 
  * and a gradient whose coefficient is infinite holds infinities and NaN);
  * dlogits may alias logits when the strides are
  * equal, its columns >= V are not written; rows with mask = 0 are not read (NaN
- * or inf in them changes nothing) and get zero gradients. Softmax statistics
- * are held in fp32, sums over tokens in two fp32 parts (about 48 bits), all in an
- * order that depends only on the sizes, so results repeat bit for bit. Nothing is allocated and no call
+ * or inf in them changes nothing) and get zero gradients. Softmax statistics and
+ * a token's share of a loss are fp32 (the loss with a KL term takes differences of
+ * log-probs before these are rounded, and holds its tokens' shares in two parts);
+ * shares are added in two fp32 parts (about 48 bits). The order of all additions
+ * depends on the sizes and, for rows of up to 24 KB, on how many blocks the device
+ * holds at once, so results repeat bit for bit on one device. Nothing is allocated and no call
  * synchronises; every call can be captured into a CUDA graph. Argument errors
  * are returned before anything is launched. `device_status` (optional, device
  * uint32) receives RL_ERR_TARGET_RANGE, RL_ERR_NONFINITE, RL_ERR_EMPTY_SEQ and

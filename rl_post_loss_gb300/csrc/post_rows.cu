@@ -991,7 +991,8 @@ constexpr int kLineBlocks = 6;                  // blocks on an SM
 constexpr int kLineBytes = 24576;               // the longest row that takes this way
 
 // The batch's sums from those of the warps: of a block's in their order, then of the blocks' by the block that
-// comes last. A block's takes the place of three rows' terms, of which there are as many. (Chunks of rows as in
+// comes last. The order of the additions goes by how many blocks the launch has, which is by the sizes and by how many
+// the device holds at once. A block's takes the place of three rows' terms, of which there are as many. (Chunks of rows as in
 // the ring kernel would each be summed by the warp that comes last there: one slow warp, for all its rows. They
 // took 45 us of 140.)
 template <typename P>
@@ -1030,10 +1031,10 @@ __device__ __forceinline__ void line_sums(const P &p, const PostPartial &mine) {
 }
 
 // A row per warp, in shared memory: for short rows the steps between a row's warps, its finisher and its
-// producer take longer than its bytes. Two dozen warps on an SM cover one another's copies and chains. Bytes of a
-// row here and on the rings, rows of bf16 (us): 8 KB, 30000 rows: the loss 105 and 264, distillation (K = 128) 172
-// and 430, log-probs 44 and 115; 24 KB, 15000: 140 and 191, 226 and 267, 68 and 80; 32 KB, 15000: 233 and 207, 347
-// and 284, 116 and 81.
+// producer take longer than its bytes. The warps on an SM cover one another's copies and chains: 24 of them for rows
+// up to 9 KB (distillation of 128 entries at 8 KB: 20), 8 at 24 KB. Bytes of a row here and on the rings, rows of bf16
+// (us): 8 KB, 30000 rows: the loss 106 and 261, distillation (K = 128) 171 and 443, log-probs 44 and 116; 24 KB, 15000:
+// 142 and 189, 226 and 271, 69 and 80; 32 KB, 15000: 234 and 206, 346 and 289, 115 and 81.
 template <typename T, int OP, bool kEnt>
 __global__ void __launch_bounds__(32 * kLineWarps, kLineBlocks)
 line_rows_kernel(const __grid_constant__ typename OpParams<OP>::type p, int stride) {
@@ -1423,6 +1424,9 @@ __global__ void __launch_bounds__(kThreads) long_distill_kernel(DistillParams p)
 // the system takes per CTA.
 constexpr size_t kCtaBytes[3] = {76800, 115712, 231424};
 
+// A GB300's SMs. A cut goes by this number and not by the device's, as the order of a row's additions goes by its cut.
+constexpr int kSms = 152;
+
 // How many clusters of this launch are resident at once; sets the kernel's shared-memory limit on its
 // first use on a device and size. Remembered for the last sizes asked for.
 cudaError_t resident_clusters(const void *kernel, const cudaLaunchConfig_t &cfg, int C, int max_dynamic, int *out) {
@@ -1497,7 +1501,7 @@ cudaError_t launch_ring(const typename OpParams<OP>::type &p, int K, bool after_
     RowPlan plan{};
     fits = false;
     // enough CTAs per row that the rows there are fill the SMs
-    const int least = std::max(1, std::min({(int)kMaxCluster, 456 / std::max(1, p.r.T), nvec / 256}));
+    const int least = std::max(1, std::min({(int)kMaxCluster, kRowBlocks * kSms / std::max(1, p.r.T), nvec / 256}));
     if (kKeep) {
         // A row's stay in the rings is set by its chain of steps, so the rate goes by the bytes that an SM's rings
         // hold, a slice for each CTA: the plan that holds most, and of those within 5% with two or three CTAs on an SM
