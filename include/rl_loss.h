@@ -532,6 +532,107 @@ RL_LOSS_API rl_status rl_loss_preference(const rl_loss_pref_config *config, int3
                                          float *seq_logratio, float *pair_loss, void *workspace,
                                          size_t workspace_bytes, uint32_t *device_status, void *stream);
 
+/* ---- The norm before the output projection, and activations kept in 8 bits -----
+ * The model's last norm gives the projection's hidden states and takes their
+ * gradient back; the same norms stand in every layer before it, and their inputs
+ * are the activations that a trainer keeps from the forward pass to the backward
+ * pass. Per row of C columns:
+ *   forward   h = x (+ residual, rounded to the type of x), y = (h - mean) rstd w + b,
+ *             mean = sum h / C, rstd = (sum (h - mean)^2 / C + eps)^(-1/2)
+ *   backward  xh = (h - mean) rstd, g = dy w,
+ *             dx = rstd (g - mean(g) - xh mean(g xh)) + dsummed,
+ *             dweight = sum over rows of dy xh, dbias = sum over rows of dy
+ * (RL_LN_RMS: mean = 0, and dx without mean(g)). With a residual, h continues along
+ * the residual stream: `summed` receives it, `dsummed` is the gradient that comes
+ * back along it, and dx is the gradient of x and of the residual alike.
+ * Statistics, sums and products are fp32 (the mean is corrected by the sum of the
+ * differences from it), outputs are rounded once; sums over rows go through fp32
+ * sums of each block's rows, added in a fixed order that depends on the sizes
+ * alone, so results repeat bit for bit.
+ * Shared rules: rows of any element-aligned address and stride >= C (16-byte
+ * aligned ones are read by vectors, up to C rounded up to 16 bytes); nothing past a
+ * row's C columns is written. A row whose mask is 0 is not read, its outputs are 0
+ * (dx too: dsummed of such a row is not read) and it takes no part in dweight and
+ * dbias; mask may be NULL. Outputs may be the same matrix as an input (same
+ * address, stride and type), except that y is never summed, dx or dsummed. Nothing is
+ * allocated, no call synchronises, every call can be captured into a CUDA graph;
+ * argument errors are returned before anything is launched. `device_status`
+ * (optional, device uint32) receives RL_ERR_NONFINITE when a row's statistics, or
+ * the sums of its backward pass, are not finite. */
+typedef enum rl_ln_kind { RL_LN_LAYER = 0, RL_LN_RMS = 1 } rl_ln_kind;
+
+typedef struct rl_ln_config {
+    int32_t kind;        /* rl_ln_kind */
+    int32_t cols;        /* C, 1 <= C <= rl_loss_layer_norm_max_cols() */
+    int32_t x_dtype;     /* rl_dtype of x, residual, summed, dsummed and dx */
+    int32_t y_dtype;     /* rl_dtype of y and dy */
+    int32_t param_dtype; /* rl_dtype of weight and bias */
+    float eps;           /* > 0, finite (forward only) */
+} rl_ln_config;
+
+/* A matrix of activations kept in 8 bits: per block of 32 columns of a row (the
+ * last one may be shorter) a scale byte b for 2^(b - 127), 255 for "not a number",
+ * and a code for each column. The writer takes the smallest power of two that leaves
+ * no value out of range (max |x| <= 127 2^e or 448 2^e, e >= -126) and rounds
+ * x / 2^e to the nearest code, ties to even; the values that codes stand for are
+ * exact in fp32 and in bf16 (a value that rounding takes past the largest finite one
+ * reads as that one). A block that holds NaN or infinity reads back as NaN. 33 bytes
+ * for 32 values. */
+typedef enum rl_act8_format {
+    RL_ACT8_INT8 = 0, /* two's complement, -127 .. 127: steps of one size in a block */
+    RL_ACT8_E4M3 = 1  /* 4 exponent and 3 mantissa bits, up to 448: steps relative to the value */
+} rl_act8_format;
+
+typedef struct rl_act8 {
+    void *codes;       /* [rows x ld_codes] bytes; 16-byte aligned rows are read by vectors */
+    void *scales;      /* [rows x ld_scales] bytes */
+    int64_t ld_codes;  /* >= C */
+    int64_t ld_scales; /* >= (C + 31) / 32 */
+    int32_t format;    /* rl_act8_format */
+} rl_act8;
+
+/* Largest number of columns of a norm (16384). */
+RL_LOSS_API int32_t rl_loss_layer_norm_max_cols(void);
+
+/* weight and bias [C] may be NULL (1 and 0); residual, summed (h; allowed without
+ * a residual), checkpoint (h in 8 bits), mean [rows] and rstd [rows] (fp32) may be
+ * NULL. RL_ERR_INVALID_ARG (NULL pointer, kind, eps, outputs that are one
+ * matrix), RL_ERR_DTYPE, RL_ERR_SHAPE (rows < 0, C < 1, a stride),
+ * RL_ERR_UNSUPPORTED (C), RL_ERR_ALIGNMENT. One launch. */
+RL_LOSS_API rl_status rl_loss_layer_norm(const rl_ln_config *config, int32_t rows, const void *x, int64_t ld_x,
+                                         const void *residual, int64_t ld_residual, const void *weight,
+                                         const void *bias, const uint8_t *mask, void *y, int64_t ld_y, void *summed,
+                                         int64_t ld_summed, const rl_act8 *checkpoint, float *mean, float *rstd,
+                                         uint32_t *device_status, void *stream);
+
+RL_LOSS_API size_t rl_loss_layer_norm_workspace_bytes(int32_t rows, int32_t cols);
+
+/* h comes from x (with a residual: the summed rows) or from `checkpoint`, one of
+ * the two; mean (RL_LN_LAYER) and rstd are the forward pass's. dsummed, dweight,
+ * dbias [C] fp32 and y (the forward's output made again from h, for the gradient of
+ * a product that took it; needs bias if there was one) may be NULL. accumulate = 1
+ * adds to dweight and dbias. `workspace` (device, 256-byte aligned, at least
+ * rl_loss_layer_norm_workspace_bytes(rows, C), any contents, one per stream and per
+ * host thread) is needed for dweight or dbias. With rows = 0 dweight and dbias are
+ * 0. Errors as for rl_loss_layer_norm, and RL_ERR_CAPACITY (workspace). Two
+ * launches. */
+RL_LOSS_API rl_status rl_loss_layer_norm_backward(const rl_ln_config *config, int32_t rows, const void *dy,
+                                                  int64_t ld_dy, const void *x, int64_t ld_x,
+                                                  const rl_act8 *checkpoint, const void *weight, const void *bias,
+                                                  const uint8_t *mask, const float *mean, const float *rstd,
+                                                  const void *dsummed, int64_t ld_dsummed, void *dx, int64_t ld_dx,
+                                                  float *dweight, float *dbias, int32_t accumulate, void *y,
+                                                  int64_t ld_y, void *workspace, size_t workspace_bytes,
+                                                  uint32_t *device_status, void *stream);
+
+/* x [rows x ld_x] (x_dtype) packed into 8 bits, and the values of a checkpoint
+ * read back. RL_ERR_DTYPE, RL_ERR_SHAPE (rows < 0, C outside [1, 2^30], a stride),
+ * RL_ERR_INVALID_ARG (NULL pointer, format), RL_ERR_ALIGNMENT. One launch. */
+RL_LOSS_API rl_status rl_loss_act8_pack(int32_t x_dtype, int32_t rows, int32_t cols, const void *x, int64_t ld_x,
+                                        const rl_act8 *out, void *stream);
+RL_LOSS_API rl_status rl_loss_act8_unpack(int32_t x_dtype, int32_t rows, int32_t cols, const rl_act8 *in, void *x,
+                                          int64_t ld_x, void *stream);
+
 /* Synchronises `stream`, returns the accumulated device status bits
  * (1u << code for each rl_status code raised) in *bits and clears them. */
 RL_LOSS_API rl_status rl_loss_get_device_status(rl_loss_t handle, void *stream, uint32_t *bits);

@@ -90,6 +90,21 @@ class rl_loss_pref_config(ctypes.Structure):
                 ("label_smoothing", ctypes.c_float), ("nll_coef", ctypes.c_float)]
 
 
+class rl_ln_config(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("cols", ctypes.c_int32), ("x_dtype", ctypes.c_int32),
+                ("y_dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class rl_act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("ld_codes", ctypes.c_int64),
+                ("ld_scales", ctypes.c_int64), ("format", ctypes.c_int32)]
+
+
+RL_LN_LAYER, RL_LN_RMS = 0, 1
+RL_ACT8_INT8, RL_ACT8_E4M3 = 0, 1
+LN_KINDS = {"layer": RL_LN_LAYER, "rms": RL_LN_RMS}
+ACT8_FORMATS = {"int8": RL_ACT8_INT8, "e4m3": RL_ACT8_E4M3}
+ACT8_BLOCK = 32  # columns that share a scale
 RL_KL_K1, RL_KL_K2, RL_KL_K3 = 0, 1, 2
 RL_DISTILL_RENORM, RL_DISTILL_TAIL = 0, 1
 RL_PREF_SIGMOID, RL_PREF_HINGE, RL_PREF_IPO = 0, 1, 2
@@ -153,6 +168,17 @@ def load(path: str | None = None) -> ctypes.CDLL:
         "rl_loss_preference_workspace_bytes": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
         "rl_loss_preference": ([ctypes.POINTER(rl_loss_pref_config), ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int64,
                                 P, P, P, P, P, P, P, ctypes.c_int64, P, P, P, P, ctypes.c_size_t, P, P], st),
+        "rl_loss_layer_norm_max_cols": ([], ctypes.c_int32),
+        "rl_loss_layer_norm": ([ctypes.POINTER(rl_ln_config), ctypes.c_int32, P, ctypes.c_int64, P, ctypes.c_int64, P, P, P,
+                                P, ctypes.c_int64, P, ctypes.c_int64, ctypes.POINTER(rl_act8), P, P, P, P], st),
+        "rl_loss_layer_norm_workspace_bytes": ([ctypes.c_int32, ctypes.c_int32], ctypes.c_size_t),
+        "rl_loss_layer_norm_backward": ([ctypes.POINTER(rl_ln_config), ctypes.c_int32, P, ctypes.c_int64, P, ctypes.c_int64,
+                                         ctypes.POINTER(rl_act8), P, P, P, P, P, P, ctypes.c_int64, P, ctypes.c_int64, P, P,
+                                         ctypes.c_int32, P, ctypes.c_int64, P, ctypes.c_size_t, P, P], st),
+        "rl_loss_act8_pack": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, ctypes.c_int64, ctypes.POINTER(rl_act8), P],
+                              st),
+        "rl_loss_act8_unpack": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(rl_act8), P, ctypes.c_int64,
+                                 P], st),
         "rl_loss_projection_logits": ([P, P, ctypes.c_int64, P, ctypes.c_int64, ctypes.c_int32, P, ctypes.c_int64,
                                        P], st),
         "rl_loss_fused_projection_forward_backward": ([P, P, ctypes.c_int64, P, ctypes.c_int64,
@@ -573,6 +599,231 @@ def preference_loss(logits, targets, logp_ref, mask, cu_seqlens, *, vocab: int |
                                      _status_word(device_status, dev), stream),
            "rl_loss_preference")
     return {"loss": loss, "logp": logp, "seq_logratio": seq_logratio, "pair_loss": pair_loss, "dlogits": dlogits}
+
+
+# ------------------------------------------------------------------ norms and 8-bit activation checkpoints
+
+class Act8:
+    """A matrix of activations kept in 8 bits: ``codes`` [rows, columns] and ``scales`` [rows, ceil(columns / 32)], both
+    torch.uint8, in the format "int8" or "e4m3" (rl_act8 in the header says what they hold)."""
+
+    __slots__ = ("codes", "scales", "format")
+
+    def __init__(self, codes, scales, format: str):
+        if format not in ACT8_FORMATS:
+            raise ValueError("format is 'int8' or 'e4m3'")
+        self.codes, self.scales, self.format = codes, scales, format
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+
+def act8_empty(rows: int, cols: int, format: str = "int8", device="cuda") -> Act8:
+    """Room for rows x cols activations in 8 bits, rows on 16-byte boundaries."""
+    import torch
+    if format not in ACT8_FORMATS:
+        raise ValueError("format is 'int8' or 'e4m3'")
+    codes = torch.empty((rows, (cols + 15) & ~15), dtype=torch.uint8, device=device)
+    scales = torch.empty((rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8, device=device)
+    return Act8(codes if cols % 16 == 0 else codes[:, :cols], scales, format)
+
+
+def _act8_struct(a: Act8, rows: int, cols: int, device) -> rl_act8:
+    import torch
+    if not isinstance(a, Act8):
+        raise ValueError("an 8-bit checkpoint is a capi.Act8")
+    codes, ld_codes = _rows("codes", a.codes, rows, cols, torch.uint8, device)
+    scales, ld_scales = _rows("scales", a.scales, rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, torch.uint8, device)
+    return rl_act8(codes, scales, ld_codes, ld_scales, ACT8_FORMATS[a.format])
+
+
+def _float_code(name: str, dtype) -> int:
+    import torch
+    if dtype is torch.bfloat16:
+        return RL_BF16
+    if dtype is torch.float32:
+        return RL_F32
+    raise ValueError(f"{name} is torch.float32 or torch.bfloat16")
+
+
+def _matrix(name: str, t):
+    """(rows, cols, dtype code, pointer, row stride) of a CUDA matrix with contiguous rows."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} is a CUDA tensor [rows, columns]")
+    (rows, cols), (ld, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"the rows of {name} are contiguous")
+    return rows, cols, _float_code(name, t.dtype), t.data_ptr(), max(ld, cols)
+
+
+def _like(name: str, t, rows: int, cols: int, dtype, device):
+    """The pointer and row stride of a matrix of exactly this shape and type (None: no matrix)."""
+    if t is None:
+        return None, 0
+    if t.dtype is dtype and t.dim() == 2 and t.get_device() == device.index:
+        (have, width), (ld, step) = t.shape, t.stride()
+        if have == rows and width == cols and (step == 1 or cols == 1):
+            return t.data_ptr(), max(ld, cols)
+    raise ValueError(f"{name} is a {dtype} tensor [{rows}, {cols}] with contiguous rows on {device}")
+
+
+def _params(weight, bias, cols: int, device):
+    """(dtype code, pointer of weight, pointer of bias) of a norm's parameters."""
+    p = weight if weight is not None else bias
+    if p is None:
+        return RL_F32, None, None
+    code, dt = _float_code("weight", p.dtype), p.dtype
+    return (code, _vector("weight", weight, cols, dt, device, True),
+            _vector("bias, of the weight's type", bias, cols, dt, device, True))
+
+
+def _on_device(device):
+    """The context that makes a tensor's device the current one for a launch."""
+    import torch
+    return _NO_CONTEXT if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+
+
+def rl_loss_layer_norm_max_cols() -> int:
+    return int(load().rl_loss_layer_norm_max_cols())
+
+
+@functools.lru_cache(maxsize=256)
+def rl_loss_layer_norm_workspace_bytes(rows: int, cols: int) -> int:
+    return int(load().rl_loss_layer_norm_workspace_bytes(int(rows), int(cols)))
+
+
+def layer_norm(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1e-5, residual=None, mask=None, y=None,
+               dtype=None, summed=None, checkpoint=None, mean=None, rstd=None, want_stats: bool = False,
+               device_status=None, stream=None) -> dict:
+    """Layer norm (or, with kind "rms", RMS norm) of the rows of x [rows, columns] on the GPU, after adding `residual`
+    where there is one. Returns y (of type `dtype`, that of x unless given), summed (x + residual; None without a
+    residual unless a tensor is passed), mean and rstd [rows] (with want_stats; no mean for "rms") and checkpoint: `checkpoint`
+    is an Act8, or "int8" or "e4m3" for a new one, that receives the norm's input in 8 bits for layer_norm_backward. Rows whose mask
+    is 0 are not read and give 0. y may be x or the residual, and so may summed."""
+    import torch
+    if kind not in LN_KINDS:
+        raise ValueError("kind is 'layer' or 'rms'")
+    rows, cols, xt, px, ldx = _matrix("x", x)
+    dev, f32 = x.device, torch.float32
+    pt, pw, pb = _params(weight, bias, cols, dev)
+    with _allocations_of(stream, dev):
+        if y is None:
+            y = torch.empty((rows, cols), dtype=dtype or x.dtype, device=dev)
+        elif dtype is not None and y.dtype is not dtype:
+            raise ValueError("y has the type that dtype names")
+        if summed is None and residual is not None:
+            summed = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        if want_stats:
+            if rstd is None:
+                rstd = torch.empty(rows, dtype=f32, device=dev)
+            if mean is None and kind == "layer":
+                mean = torch.empty(rows, dtype=f32, device=dev)
+        if isinstance(checkpoint, str):
+            checkpoint = act8_empty(rows, cols, checkpoint, dev)
+        if stream is None:
+            stream = _current_stream(dev)
+    kept = None if checkpoint is None else ctypes.byref(_act8_struct(checkpoint, rows, cols, dev))
+    cfg = rl_ln_config(LN_KINDS[kind], cols, xt, _float_code("y", y.dtype), pt, eps)
+    with _on_device(dev):
+        _check(load().rl_loss_layer_norm(ctypes.byref(cfg), rows, px, ldx, *_like("residual", residual, rows, cols, x.dtype, dev),
+                                         pw, pb, _vector("mask", mask, rows, torch.uint8, dev, True),
+                                         *_like("y", y, rows, cols, y.dtype, dev),
+                                         *_like("summed", summed, rows, cols, x.dtype, dev), kept,
+                                         _vector("mean", mean, rows, f32, dev, True), _vector("rstd", rstd, rows, f32, dev, True),
+                                         _status_word(device_status, dev), stream),
+               "rl_loss_layer_norm")
+    return {"y": y, "summed": summed, "mean": mean, "rstd": rstd, "checkpoint": checkpoint}
+
+
+def layer_norm_backward(dy, weight, mean, rstd, *, x=None, checkpoint=None, kind: str = "layer", dtype=None, mask=None,
+                        dsummed=None, dx=None, dweight=None, dbias=None, want_dweight: bool = True, want_dbias: bool = False,
+                        accumulate: bool = False, bias=None, y=None, workspace=None, device_status=None,
+                        stream=None) -> dict:
+    """The backward pass of layer_norm: gradients of its input (dx, and of the residual, which is the same), weight and
+    bias from dy. The input comes as x (with a residual: `summed`) or as the 8-bit `checkpoint`; mean (None for "rms") and rstd are the
+    forward pass's. dsummed is the gradient that comes along the residual stream, added to dx. dx has the type of x (from a checkpoint: `dtype`, that of dy unless given). dweight (unless
+    want_dweight is False) and dbias (with want_dbias, or where it is passed) are fp32; with accumulate they are
+    added to. A tensor y receives the forward pass's output made again (with `bias`, if there was one). Rows whose mask is 0 are not
+    read and give 0. dx may be dy, x or dsummed. A workspace that is passed serves one call at a time."""
+    import torch
+    if kind not in LN_KINDS:
+        raise ValueError("kind is 'layer' or 'rms'")
+    if (x is None) == (checkpoint is None):
+        raise ValueError("the norm's input comes as x or as a checkpoint")
+    rows, cols, yt, pdy, lddy = _matrix("dy", dy)
+    dev, f32 = dy.device, torch.float32
+    if x is not None:
+        if dtype is not None and dtype is not x.dtype:
+            raise ValueError("dx has the type of x")
+        dtype = x.dtype
+    elif dtype is None:
+        dtype = dx.dtype if dx is not None else dy.dtype
+    pt, pw, pb = _params(weight, bias, cols, dev)
+    if accumulate and ((want_dweight and dweight is None) or (want_dbias and dbias is None)):
+        raise ValueError("pass the dweight and dbias that are added to")
+    with _allocations_of(stream, dev):
+        if dx is None:
+            dx = torch.empty((rows, cols), dtype=dtype, device=dev)
+        if dweight is None and want_dweight:
+            dweight = torch.empty(cols, dtype=f32, device=dev)
+        if dbias is None and want_dbias:
+            dbias = torch.empty(cols, dtype=f32, device=dev)
+        if stream is None:
+            stream = _current_stream(dev)
+        if workspace is None and (dweight is not None or dbias is not None):
+            workspace = _post_workspace(rl_loss_layer_norm_workspace_bytes(rows, cols), dev, stream)
+    kept = None if checkpoint is None else ctypes.byref(_act8_struct(checkpoint, rows, cols, dev))
+    cfg = rl_ln_config(LN_KINDS[kind], cols, _float_code("dx", dtype), yt, pt, 0.0)
+    with _on_device(dev):
+        _check(load().rl_loss_layer_norm_backward(
+            ctypes.byref(cfg), rows, pdy, lddy, *_like("x", x, rows, cols, dtype, dev), kept, pw, pb,
+            _vector("mask", mask, rows, torch.uint8, dev, True), _vector("mean", mean, rows, f32, dev, kind == "rms"),
+            _vector("rstd", rstd, rows, f32, dev), *_like("dsummed", dsummed, rows, cols, dtype, dev),
+            *_like("dx", dx, rows, cols, dtype, dev), _vector("dweight", dweight, cols, f32, dev, True),
+            _vector("dbias", dbias, cols, f32, dev, True), int(accumulate), *_like("y", y, rows, cols, dy.dtype, dev),
+            *((None, 0) if workspace is None else _workspace_of(workspace, dev)), _status_word(device_status, dev), stream),
+            "rl_loss_layer_norm_backward")
+    return {"dx": dx, "dweight": dweight, "dbias": dbias, "y": y}
+
+
+def act8_pack(x, *, format: str = "int8", out: Act8 | None = None, stream=None) -> Act8:
+    """The activations x [rows, columns] in 8 bits, in a new Act8 or in `out`."""
+    rows, cols, xt, px, ldx = _matrix("x", x)
+    dev = x.device
+    if out is None:
+        with _allocations_of(stream, dev):
+            out = act8_empty(rows, cols, format, dev)
+    if stream is None:
+        stream = _current_stream(dev)
+    with _on_device(dev):
+        _check(load().rl_loss_act8_pack(xt, rows, cols, px, ldx, ctypes.byref(_act8_struct(out, rows, cols, dev)), stream),
+               "rl_loss_act8_pack")
+    return out
+
+
+def act8_unpack(a: Act8, *, dtype=None, out=None, stream=None):
+    """The activations that an Act8 stands for, as torch.bfloat16 (or `dtype`), in a new tensor or in `out`."""
+    import torch
+    rows, cols = a.codes.shape
+    dev = a.codes.device
+    if out is None:
+        with _allocations_of(stream, dev):
+            out = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=dev)
+    elif dtype is not None and out.dtype is not dtype:
+        raise ValueError("out has the type that dtype names")
+    if stream is None:
+        stream = _current_stream(dev)
+    with _on_device(dev):
+        _check(load().rl_loss_act8_unpack(_float_code("out", out.dtype), rows, cols,
+                                          ctypes.byref(_act8_struct(a, rows, cols, dev)),
+                                          *_like("out", out, rows, cols, out.dtype, dev), stream),
+               "rl_loss_act8_unpack")
+    return out
 
 
 def rl_loss_version() -> int:

@@ -1,0 +1,249 @@
+// Activations kept in 8 bits: blocks of 32 columns of a row under one power of two.
+//
+// A block's scale byte b stands for 2^(b - 127) (255: not a number), its codes are int8 or e4m3 values. The
+// writer takes the smallest power of two with max |x| <= 127 2^e (int8) or 448 2^e (e4m3), e >= -126, and
+// rounds x / 2^e to the nearest code, ties to even. Scaling by a power of two is exact, so a code does not
+// depend on the precision it is computed in, and no division is needed. A block that holds an infinity or a
+// NaN gets b = 255 and reads back as NaN throughout.
+#pragma once
+
+#include "common.cuh"
+
+namespace rlk {
+
+constexpr int kAct8Block = 32;
+
+// Eight neighbouring columns of a thread; a block is four neighbouring lanes.
+constexpr int kVec = 8;
+
+// The scale byte of a block from the bits of its largest |x| (as integers, so that NaN is above infinity).
+// For 127 = 1.984375 2^6 and 448 = 1.75 2^8 the test is one on the mantissa.
+__device__ __forceinline__ uint32_t act8_scale(uint32_t amax, bool e4m3) {
+    const int man = (int)(amax & 0x7fffffu);
+    const int b = (int)(amax >> 23) - (e4m3 ? 8 : 6) + (man > (e4m3 ? 0x600000 : 0x7e0000) ? 1 : 0);
+    return amax >= 0x7f800000u ? 255u : (uint32_t)max(b, 1);
+}
+
+__device__ __forceinline__ uint32_t act8_amax(const float (&v)[kVec]) {
+    uint32_t a = 0;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) a = max(a, __float_as_uint(v[j]) & 0x7fffffffu);
+    return a;
+}
+
+// The largest of the four lanes that share a block (every lane of the warp takes part).
+__device__ __forceinline__ uint32_t act8_block_max(uint32_t a) {
+    a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+    return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+
+// Codes of eight values under scale byte b. int8: adding 1.5 2^23 rounds to a whole number (to nearest even)
+// and leaves it in the low byte.
+__device__ __forceinline__ uint2 act8_encode(const float (&v)[kVec], uint32_t b, bool e4m3) {
+    if (b == 255u) return make_uint2(0u, 0u);
+    const float inv = __uint_as_float((254u - b) << 23);
+    uint32_t w[2];
+    if (e4m3) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            uint16_t lo, hi;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[4 * k + 1] * inv), "f"(v[4 * k] * inv));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[4 * k + 3] * inv), "f"(v[4 * k + 2] * inv));
+            w[k] = (uint32_t)lo | ((uint32_t)hi << 16);
+        }
+    } else {
+        uint32_t t[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) t[j] = __float_as_uint(fmaf(v[j], inv, 12582912.f));
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            w[k] = __byte_perm(__byte_perm(t[4 * k], t[4 * k + 1], 0x0040), __byte_perm(t[4 * k + 2], t[4 * k + 3], 0x0040), 0x5410);
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// What eight codes stand for. Beyond b = 230 products may pass fp32's range (64 2^122 stands for a value that
+// was rounded up to 2^128): they end at +-`most`, the largest finite value of the type that is read back.
+__device__ __forceinline__ void act8_decode(uint2 c, uint32_t b, bool e4m3, float most, float (&v)[kVec]) {
+    const float s = __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
+    const uint32_t w[2] = {c.x, c.y};
+    if (e4m3) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t h;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
+            float lo, hi;
+            asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
+                : "=f"(lo), "=f"(hi)
+                : "r"(h));
+            v[2 * k] = lo * s;
+            v[2 * k + 1] = hi * s;
+        }
+    } else {
+        // a code plus 128 in the low byte of 2^23 is 2^23 + 128 + code; times s the difference is exact
+        const float off = b <= 230u ? -8388736.f * s : -8388736.f, mul = b <= 230u ? s : 1.f;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            v[j] = fmaf(__uint_as_float(__byte_perm(w[j >> 2] ^ 0x80808080u, 0x4b000000u, 0x7440u | (j & 3))), mul, off);
+        if (b > 230u) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j] *= s;
+        }
+    }
+    if (b > 230u && b != 255u) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (fabsf(v[j]) > most) v[j] = copysignf(most, v[j]);
+    }
+}
+
+// ---------------------------------------------------------------- eight columns of a row in memory
+//
+// `fast` (one flag per matrix, from its address and row stride): rows start on 16-byte boundaries (8-byte
+// ones for codes) and are read up to their length rounded up to those; otherwise element by element.
+
+struct Raw16 { uint4 a; };
+struct Raw32 { uint4 a, b; };
+struct Raw8 { uint2 a; };
+
+__device__ __forceinline__ uint4 ld16(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+__device__ __forceinline__ void load_raw(Raw16 &r, const __nv_bfloat16 *row, int col, int cols, bool fast) {
+    if (fast) {
+        r.a = ld16(row + col);
+        return;
+    }
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + col;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = col + 2 * k < cols ? p[2 * k] : 0u, hi = col + 2 * k + 1 < cols ? p[2 * k + 1] : 0u;
+        w[k] = lo | (hi << 16);
+    }
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load_raw(Raw32 &r, const float *row, int col, int cols, bool fast) {
+    if (fast) {
+        r.a = *reinterpret_cast<const uint4 *>(row + col);
+        r.b = col + 4 < cols ? *reinterpret_cast<const uint4 *>(row + col + 4) : make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    const uint32_t *p = reinterpret_cast<const uint32_t *>(row) + col;
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = col + k < cols ? p[k] : 0u;
+    r.a = make_uint4(w[0], w[1], w[2], w[3]);
+    r.b = make_uint4(w[4], w[5], w[6], w[7]);
+}
+__device__ __forceinline__ void load_raw(Raw8 &r, const uint8_t *row, int col, int cols, bool fast) {
+    if (fast) {
+        r.a = *reinterpret_cast<const uint2 *>(row + col);
+        return;
+    }
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (col + k < cols) w[k >> 2] |= (uint32_t)row[col + k] << (8 * (k & 3));
+    r.a = make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void to_float(const Raw16 &r, float (&v)[kVec]) {
+    const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = bf16_lo(w[k]);
+        v[2 * k + 1] = bf16_hi(w[k]);
+    }
+}
+__device__ __forceinline__ void to_float(const Raw32 &r, float (&v)[kVec]) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __uint_as_float(w[k]);
+}
+
+// Sets what lies past the row's end to 0.
+__device__ __forceinline__ void clip_row(float (&v)[kVec], int col, int cols) {
+    if (col + kVec > cols) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (col + j >= cols) v[j] = 0.f;
+    }
+}
+
+// Eight values rounded once to the matrix's type; nothing past the row's end is written.
+__device__ __forceinline__ void store_vec(__nv_bfloat16 *row, int col, int cols, bool fast, const float (&v)[kVec]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+    if (fast && col + kVec <= cols) {
+        *reinterpret_cast<uint4 *>(row + col) = make_uint4(w[0], w[1], w[2], w[3]);
+        return;
+    }
+    uint16_t *p = reinterpret_cast<uint16_t *>(row) + col;
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        if (col + j < cols) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+}
+__device__ __forceinline__ void store_vec(float *row, int col, int cols, bool fast, const float (&v)[kVec]) {
+    if (fast && col + kVec <= cols) {
+        *reinterpret_cast<float4 *>(row + col) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4 *>(row + col + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        if (col + j < cols) row[col + j] = v[j];
+}
+__device__ __forceinline__ void store_codes(uint8_t *row, int col, int cols, bool fast, uint2 c) {
+    if (fast && col + kVec <= cols) {
+        *reinterpret_cast<uint2 *>(row + col) = c;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j)
+        if (col + j < cols) row[col + j] = (uint8_t)((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+}
+
+// ---------------------------------------------------------------- parameters
+
+// A matrix: its first element, the row stride in elements, and whether vector accesses are allowed.
+struct RowMat {
+    void *p;
+    int64_t ld;
+    int32_t bf16;
+    int32_t fast;
+};
+
+struct Act8Mat {
+    uint8_t *codes, *scales;
+    int64_t ld_codes, ld_scales;
+    int32_t e4m3;
+    int32_t fast;
+};
+
+struct Act8Params {
+    RowMat x;
+    Act8Mat a;
+    int64_t rows;
+    int32_t cols;
+    int32_t row_vecs;       // vectors of a row, whole blocks
+    int64_t step_rows;      // rows and vectors that the grid's threads step over
+    int32_t step_vecs;
+};
+
+cudaError_t launch_act8_pack(Act8Params p, cudaStream_t stream);
+cudaError_t launch_act8_unpack(Act8Params p, cudaStream_t stream);
+
+// A row of a matrix of either type.
+__device__ __forceinline__ void store_row(const RowMat &m, int64_t row, int col, int cols, const float (&v)[kVec]) {
+    if (m.bf16)
+        store_vec(static_cast<__nv_bfloat16 *>(m.p) + row * m.ld, col, cols, m.fast, v);
+    else
+        store_vec(static_cast<float *>(m.p) + row * m.ld, col, cols, m.fast, v);
+}
+
+}  // namespace rlk

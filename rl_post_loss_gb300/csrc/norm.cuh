@@ -1,0 +1,121 @@
+// Layer norm and RMS norm over rows of activations, forward and backward (internal).
+//
+//   forward   h = x (+ residual, rounded to the type of x);  y = (h - mean) rstd w + b
+//             mean = sum h / C,  rstd = (sum (h - mean)^2 / C + eps)^-1/2;  RMS: mean = 0
+//   backward  xh = (h - mean) rstd,  g = dy w
+//             dx = rstd (g - mean(g) - xh mean(g xh)) + dsummed     (RMS: without mean(g))
+//             dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// All arithmetic is fp32. A row's columns lie over `lanes` threads in vectors of eight; thread t has vectors
+// t, t + lanes, ... . Rows of up to 256 columns share a warp or take one, longer ones take the 1 to 16 warps
+// of a block.
+#pragma once
+
+#include "act8.cuh"
+
+namespace rlk {
+
+constexpr int kNormMaxCols = 16384;
+constexpr int kNormSMs = 152;
+
+struct NormForwardParams {
+    RowMat x, residual, y, h;  // p = nullptr where there is none
+    Act8Mat ckpt;              // codes = nullptr: none
+    const void *w, *b;         // [cols] or nullptr
+    int32_t params_bf16, params_fast;
+    const uint8_t *mask;
+    float *mean, *rstd;        // or nullptr
+    int32_t rows, cols, rms, lanes;
+    float eps, inv_cols;
+    uint32_t *status;
+};
+
+struct NormBackwardParams {
+    RowMat dy, x, dsummed, dx, y;  // x.p = nullptr: from ckpt
+    Act8Mat ckpt;
+    const void *w, *b;
+    int32_t params_bf16, params_fast;
+    const uint8_t *mask;
+    const float *mean, *rstd;
+    int32_t rows, cols, rms, lanes;
+    float inv_cols;
+    float *partials;   // [parts][1 or 2][ld_part]: dw, then db
+    int64_t ld_part;
+    int32_t want_dw, want_db;
+    float *dw, *db;
+    int32_t accumulate;  // dw and db are added to
+    uint32_t *status;
+};
+
+// How a norm's rows are laid over threads.
+struct NormShape {
+    int lanes;    // threads of a row
+    int vecs;     // vectors of a thread
+    int threads;  // of a block
+    int groups;   // rows that a block works on at a time
+};
+NormShape norm_shape(int cols);
+
+// Blocks of the backward pass, which is also the number of partial sums of dw and db.
+int norm_backward_parts(int rows, int cols);
+
+cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream);
+cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- device helpers
+
+// Sums over the threads of a row. Inside a warp a butterfly, so that every lane has the same bits; over a
+// block's warps one exchange through shared memory (two buffers in turn: a thread may still read the last
+// one while another writes the next), added in the order of the warps.
+template <int LANES>
+struct RowSum {
+    float (*buf)[2][16];
+    int turn;
+    __device__ __forceinline__ RowSum(float (*b)[2][16]) : buf(b), turn(0) {}
+
+    template <int N>
+    __device__ __forceinline__ void run(float (&v)[N]) {
+        static_assert(N <= 2, "two sums at most");
+#pragma unroll
+        for (int off = (LANES < 32 ? LANES : 32) / 2; off > 0; off >>= 1)
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] = __fadd_rn(v[n], __shfl_xor_sync(0xffffffffu, v[n], off));
+        if (LANES <= 32) return;
+        const int warps = blockDim.x >> 5;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n) buf[turn][n][threadIdx.x >> 5] = v[n];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float s = buf[turn][n][0];
+            for (int w = 1; w < warps; ++w) s = __fadd_rn(s, buf[turn][n][w]);
+            v[n] = s;
+        }
+        turn ^= 1;
+    }
+};
+
+__device__ __forceinline__ void load_params(const void *p, int bf16, int fast, int col, int cols, float (&v)[kVec]) {
+    if (bf16) {
+        const uint16_t *q = static_cast<const uint16_t *>(p) + col;
+        if (fast && col + kVec <= cols) {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(q));
+            to_float(Raw16{a}, v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j] = col + j < cols ? __uint_as_float((uint32_t)__ldg(q + j) << 16) : 0.f;
+        }
+    } else {
+        const float *q = static_cast<const float *>(p) + col;
+        if (fast && col + kVec <= cols) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(q)), b = __ldg(reinterpret_cast<const float4 *>(q) + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) v[j] = col + j < cols ? __ldg(q + j) : 0.f;
+        }
+    }
+}
+
+}  // namespace rlk
