@@ -12,6 +12,7 @@
 #pragma once
 
 #include "act8.cuh"
+#include "post.cuh"
 
 namespace rlk {
 
@@ -62,7 +63,61 @@ int norm_backward_parts(int rows, int cols);
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream);
 
+// The backward pass of rows that bulk copies can take (16-byte aligned ones): how many blocks of how many warps,
+// and how many rows' room each block has in shared memory. depth = 0: the rows do not fit.
+struct NormRing {
+    int warps, vecs, blocks_per_sm, depth;
+    size_t h_bytes, dy_bytes, ds_bytes, w_bytes, smem;  // of a row, of the weight, of a block
+};
+
 // ---------------------------------------------------------------- device helpers
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Eight neighbouring columns as four pairs.
+struct V8 {
+    f32x2 p[4];
+};
+__device__ __forceinline__ V8 pairs_of(const float (&v)[kVec]) {
+    V8 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.p[k] = pack2(v[2 * k], v[2 * k + 1]);
+    return r;
+}
+__device__ __forceinline__ void floats_of(const V8 &a, float (&v)[kVec]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpack2(a.p[k], v[2 * k], v[2 * k + 1]);
+}
+__device__ __forceinline__ V8 bf16_pairs(uint4 a) {
+    V8 r;
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.p[k] = pack2(bf16_lo(w[k]), bf16_hi(w[k]));
+    return r;
+}
+__device__ __forceinline__ V8 f32_pairs(uint4 a, uint4 b) {
+    V8 r;
+    r.p[0] = pack2(__uint_as_float(a.x), __uint_as_float(a.y));
+    r.p[1] = pack2(__uint_as_float(a.z), __uint_as_float(a.w));
+    r.p[2] = pack2(__uint_as_float(b.x), __uint_as_float(b.y));
+    r.p[3] = pack2(__uint_as_float(b.z), __uint_as_float(b.w));
+    return r;
+}
+__device__ __forceinline__ V8 clipped(const V8 &a, int col, int cols) {
+    float v[kVec];
+    floats_of(a, v);
+    clip_row(v, col, cols);
+    return pairs_of(v);
+}
+__device__ __forceinline__ float sum_of(f32x2 a) {
+    float x, y;
+    unpack2(a, x, y);
+    return x + y;
+}
 
 // Sums over the threads of a row. Inside a warp a butterfly, so that every lane has the same bits; over a
 // block's warps one exchange through shared memory (two buffers in turn: a thread may still read the last
