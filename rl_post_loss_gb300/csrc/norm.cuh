@@ -62,6 +62,11 @@ int norm_backward_parts(int rows, int cols);
 
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream);
+cudaError_t launch_norm_ring_bf16(const NormBackwardParams &p, const struct NormRing &r, int parts, cudaStream_t stream);
+cudaError_t launch_norm_ring_f32(const NormBackwardParams &p, const struct NormRing &r, int parts, cudaStream_t stream);
+cudaError_t launch_norm_ring_act8(const NormBackwardParams &p, const struct NormRing &r, int parts, cudaStream_t stream);
+
+constexpr size_t kNormRingSmem = 226 * 1024;  // of a block
 
 // The backward pass of rows that bulk copies can take (16-byte aligned ones): how many blocks of how many warps,
 // and how many rows' room each block has in shared memory. depth = 0: the rows do not fit.
@@ -111,6 +116,25 @@ __device__ __forceinline__ V8 clipped(const V8 &a, int col, int cols) {
     float v[kVec];
     floats_of(a, v);
     clip_row(v, col, cols);
+    return pairs_of(v);
+}
+// act8_decode for fp32, as pairs.
+__device__ __forceinline__ V8 act8_pairs(uint2 c, uint32_t b, bool e4m3) {
+    float v[kVec];
+    if (!e4m3 && b <= 230u) {
+        const float s = __uint_as_float(b ? b << 23 : 0x00400000u);
+        const f32x2 mul = pack2(s, s), off = pack2(-8388736.f * s, -8388736.f * s);
+        const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+        V8 r;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x = w[k >> 1];
+            r.p[k] = fma2(pack2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440u | (2 * k & 3))),
+                                __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440u | ((2 * k + 1) & 3)))), mul, off);
+        }
+        return r;
+    }
+    act8_decode(c, b, e4m3, __uint_as_float(0x7f7fffffu), v);
     return pairs_of(v);
 }
 __device__ __forceinline__ float sum_of(f32x2 a) {
