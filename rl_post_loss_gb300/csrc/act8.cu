@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kThreads) act8_unpack_kernel(Act8Params p) {
         load_raw(r, p.a.codes + at.row * p.a.ld_codes, col, p.cols, p.a.fast);
         const uint32_t b = p.a.scales[at.row * p.a.ld_scales + (at.vec >> 2)];
         float v[kVec];
-        act8_decode(r.a, b, p.a.e4m3, most, v);
+        floats_of(act8_decode(r.a, b, p.a.e4m3, most), v);
         store_row(p.x, at.row, col, p.cols, v);
     }
 }

@@ -7,7 +7,7 @@
 // NaN gets b = 255 and reads back as NaN throughout.
 #pragma once
 
-#include "common.cuh"
+#include "post.cuh"
 
 namespace rlk {
 
@@ -16,6 +16,41 @@ constexpr int kAct8Block = 32;
 // Eight neighbouring columns of a thread; a block is four neighbouring lanes.
 constexpr int kVec = 8;
 
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Eight neighbouring columns as four pairs.
+struct V8 {
+    f32x2 p[4];
+};
+__device__ __forceinline__ V8 pairs_of(const float (&v)[kVec]) {
+    V8 r;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.p[k] = pack2(v[2 * k], v[2 * k + 1]);
+    return r;
+}
+__device__ __forceinline__ void floats_of(const V8 &a, float (&v)[kVec]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) unpack2(a.p[k], v[2 * k], v[2 * k + 1]);
+}
+__device__ __forceinline__ V8 bf16_pairs(uint4 a) {
+    V8 r;
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) r.p[k] = pack2(bf16_lo(w[k]), bf16_hi(w[k]));
+    return r;
+}
+__device__ __forceinline__ V8 f32_pairs(uint4 a, uint4 b) {
+    V8 r;
+    r.p[0] = pack2(__uint_as_float(a.x), __uint_as_float(a.y));
+    r.p[1] = pack2(__uint_as_float(a.z), __uint_as_float(a.w));
+    r.p[2] = pack2(__uint_as_float(b.x), __uint_as_float(b.y));
+    r.p[3] = pack2(__uint_as_float(b.z), __uint_as_float(b.w));
+    return r;
+}
 // The scale byte of a block from the bits of its largest |x| (as integers, so that NaN is above infinity).
 // For 127 = 1.984375 2^6 and 448 = 1.75 2^8 the test is one on the mantissa.
 __device__ __forceinline__ uint32_t act8_scale(uint32_t amax, bool e4m3) {
@@ -62,39 +97,83 @@ __device__ __forceinline__ uint2 act8_encode(const float (&v)[kVec], uint32_t b,
     return make_uint2(w[0], w[1]);
 }
 
-// What eight codes stand for. Beyond b = 230 products may pass fp32's range (64 2^122 stands for a value that
-// was rounded up to 2^128): they end at +-`most`, the largest finite value of the type that is read back.
-__device__ __forceinline__ void act8_decode(uint2 c, uint32_t b, bool e4m3, float most, float (&v)[kVec]) {
+// What eight codes stand for, as pairs. An int8 code plus 128 in the low byte of 2^23 is 2^23 + 128 + code, and
+// times s the difference is exact. An e4m3 code's 7 low bits, put where fp32 has its exponent and mantissa, are the
+// value times 2^-120 (subnormal codes included). Where products may pass fp32's range (a code can stand for a
+// value that was rounded up to 2^128), they end at +-`most`, the largest finite value of the type that is read back.
+__device__ __forceinline__ V8 act8_decode(uint2 c, uint32_t b, bool e4m3, float most) {
     const float s = __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
-    const uint32_t w[2] = {c.x, c.y};
+    const bool plain = b <= (e4m3 ? 134u : 230u);
+    V8 r;
     if (e4m3) {
+        const float k = plain ? s * 0x1p120f : 0x1p120f;
+        const f32x2 mul = pack2(k, k);
+        const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t h;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)(w[k >> 1] >> (16 * (k & 1)))));
-            float lo, hi;
-            asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;}"
-                : "=f"(lo), "=f"(hi)
-                : "r"(h));
-            v[2 * k] = lo * s;
-            v[2 * k + 1] = hi * s;
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[j] = (uint32_t)((int32_t)__byte_perm(w[i >> 1], 0u, 0x0444u | (uint32_t)((2 * i + j) & 3) << 12) >> 4) & 0x87f00000u;
+            r.p[i] = mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), mul);
         }
     } else {
-        // a code plus 128 in the low byte of 2^23 is 2^23 + 128 + code; times s the difference is exact
-        const float off = b <= 230u ? -8388736.f * s : -8388736.f, mul = b <= 230u ? s : 1.f;
+        const float m = plain ? s : 1.f;
+        const f32x2 mul = pack2(m, m), off = pack2(-8388736.f * m, -8388736.f * m);
+        const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            v[j] = fmaf(__uint_as_float(__byte_perm(w[j >> 2] ^ 0x80808080u, 0x4b000000u, 0x7440u | (j & 3))), mul, off);
-        if (b > 230u) {
+        for (int i = 0; i < 4; ++i)
+            r.p[i] = fma2(pack2(__uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | (2 * i & 3))),
+                                __uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | ((2 * i + 1) & 3)))), mul, off);
+    }
+    if (!plain) {
+        float v[kVec];
+        floats_of(r, v);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) v[j] *= s;
+        for (int j = 0; j < kVec; ++j) {
+            v[j] *= s;
+            if (fabsf(v[j]) > most) v[j] = copysignf(most, v[j]);  // (NaN stays)
         }
+        r = pairs_of(v);
     }
-    if (b > 230u && b != 255u) {
+    return r;
+}
+
+// act8_decode without branches, right for b <= 198 (and NaN for 255): beyond, values are above 1e21, whose squares
+// pass fp32's range, and a norm's statistics are not finite whatever it reads. (The e4m3 factor 2^120 s comes in
+// two steps, as s may be above 2^7.)
+template <bool E4M3>
+__device__ __forceinline__ V8 act8_decode_norm(uint2 c, uint32_t b) {
+    const float s = __uint_as_float(b << 23);
+    V8 r;
+    if (E4M3) {
+        const f32x2 up = pack2(0x1p64f, 0x1p64f), mul = pack2(s * 0x1p56f, s * 0x1p56f);
+        const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (fabsf(v[j]) > most) v[j] = copysignf(most, v[j]);
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[j] = (uint32_t)((int32_t)__byte_perm(w[i >> 1], 0u, 0x0444u | (uint32_t)((2 * i + j) & 3) << 12) >> 4) & 0x87f00000u;
+            r.p[i] = mul2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), up), mul);
+        }
+    } else {
+        const f32x2 mul = pack2(s, s), off = pack2(-8388736.f * s, -8388736.f * s);
+        const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r.p[i] = fma2(pack2(__uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | (2 * i & 3))),
+                                __uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | ((2 * i + 1) & 3)))), mul, off);
     }
+    return r;
+}
+
+// What one code stands for, in fp32.
+__device__ __forceinline__ float act8_value(uint32_t c, uint32_t b, bool e4m3) {
+    const float s = __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
+    const float q = e4m3 ? __uint_as_float((uint32_t)((int32_t)(c << 24) >> 4) & 0x87f00000u) * 0x1p120f : (float)(int8_t)c;
+    const float v = q * s, most = __uint_as_float(0x7f7fffffu);
+    return fabsf(v) > most ? copysignf(most, v) : v;
 }
 
 // ---------------------------------------------------------------- eight columns of a row in memory

@@ -6,18 +6,19 @@
 //             dx = rstd (g - mean(g) - xh mean(g xh)) + dsummed     (RMS: without mean(g))
 //             dw = sum over rows of dy xh,  db = sum over rows of dy
 //
-// All arithmetic is fp32. A row's columns lie over `lanes` threads in vectors of eight; thread t has vectors
-// t, t + lanes, ... . Rows of up to 256 columns share a warp or take one, longer ones take the 1 to 16 warps
-// of a block.
+// All arithmetic is fp32. The backward pass works with r = dy rstd, u = r w, d = h - mean, so that dw += r d,
+// rstd mean(g) = mean(u), mean(g xh) = mean(u d), dx = u - mean(u) - d k + dsummed with k = rstd^2 mean(u d).
+// A block of the backward pass keeps the sums of dw and db over its rows and leaves them as one partial sum
+// of a column; a second launch adds the partial sums.
 #pragma once
 
 #include "act8.cuh"
-#include "post.cuh"
 
 namespace rlk {
 
 constexpr int kNormMaxCols = 16384;
 constexpr int kNormSMs = 152;
+constexpr int kNormWarps = 16;  // of a block of the backward pass, which has an SM for itself
 
 struct NormForwardParams {
     RowMat x, residual, y, h;  // p = nullptr where there is none
@@ -38,9 +39,9 @@ struct NormBackwardParams {
     int32_t params_bf16, params_fast;
     const uint8_t *mask;
     const float *mean, *rstd;
-    int32_t rows, cols, rms, lanes;
+    int32_t rows, cols, rms;
     float inv_cols;
-    float *partials;   // [parts][1 or 2][ld_part]: dw, then db
+    float *partials;   // [parts][2][ld_part]: dw, then db
     int64_t ld_part;
     int32_t want_dw, want_db;
     float *dw, *db;
@@ -57,84 +58,41 @@ struct NormShape {
 };
 NormShape norm_shape(int cols);
 
-// Blocks of the backward pass, which is also the number of partial sums of dw and db.
+// How the backward pass lays rows over blocks (norm_ring.cuh).
+constexpr int kNormDepth = 8;
+constexpr size_t kNormRingSmem = 225 * 1024;  // of a block, beside its barriers and sums
+struct NormTeams {
+    int mode;                                    // RowMode
+    int warps, vecs, blocks_per_sm;              // of a row; vectors of eight columns of a thread
+    int depth;                                   // rows' room of a team in shared memory
+    int w_in_smem;                               // the weight beside them, where registers have no room for it
+    int at_dy, at_ds, at_scales, stage_bytes;    // of a row
+    size_t smem;
+};
+
+// Partial sums of dw and db, at most.
 int norm_backward_parts(int rows, int cols);
 
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream);
-cudaError_t launch_norm_ring_bf16(const NormBackwardParams &p, const struct NormRing &r, int parts, cudaStream_t stream);
-cudaError_t launch_norm_ring_f32(const NormBackwardParams &p, const struct NormRing &r, int parts, cudaStream_t stream);
-cudaError_t launch_norm_ring_act8(const NormBackwardParams &p, const struct NormRing &r, int parts, cudaStream_t stream);
-
-constexpr size_t kNormRingSmem = 226 * 1024;  // of a block
-
-// The backward pass of rows that bulk copies can take (16-byte aligned ones): how many blocks of how many warps,
-// and how many rows' room each block has in shared memory. depth = 0: the rows do not fit.
-struct NormRing {
-    int warps, vecs, blocks_per_sm, depth;
-    size_t h_bytes, dy_bytes, ds_bytes, w_bytes, smem;  // of a row, of the weight, of a block
-};
+// The backward pass's kernels by the types of h and dy.
+#define RLK_NORM_ROWS(H, DY) cudaError_t launch_norm_rows_##H##_##DY(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream)
+RLK_NORM_ROWS(bf16, bf16);
+RLK_NORM_ROWS(bf16, f32);
+RLK_NORM_ROWS(f32, bf16);
+RLK_NORM_ROWS(f32, f32);
+RLK_NORM_ROWS(int8, bf16);
+RLK_NORM_ROWS(int8, f32);
+RLK_NORM_ROWS(e4m3, bf16);
+RLK_NORM_ROWS(e4m3, f32);
+#undef RLK_NORM_ROWS
 
 // ---------------------------------------------------------------- device helpers
 
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-// Eight neighbouring columns as four pairs.
-struct V8 {
-    f32x2 p[4];
-};
-__device__ __forceinline__ V8 pairs_of(const float (&v)[kVec]) {
-    V8 r;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r.p[k] = pack2(v[2 * k], v[2 * k + 1]);
-    return r;
-}
-__device__ __forceinline__ void floats_of(const V8 &a, float (&v)[kVec]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) unpack2(a.p[k], v[2 * k], v[2 * k + 1]);
-}
-__device__ __forceinline__ V8 bf16_pairs(uint4 a) {
-    V8 r;
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) r.p[k] = pack2(bf16_lo(w[k]), bf16_hi(w[k]));
-    return r;
-}
-__device__ __forceinline__ V8 f32_pairs(uint4 a, uint4 b) {
-    V8 r;
-    r.p[0] = pack2(__uint_as_float(a.x), __uint_as_float(a.y));
-    r.p[1] = pack2(__uint_as_float(a.z), __uint_as_float(a.w));
-    r.p[2] = pack2(__uint_as_float(b.x), __uint_as_float(b.y));
-    r.p[3] = pack2(__uint_as_float(b.z), __uint_as_float(b.w));
-    return r;
-}
 __device__ __forceinline__ V8 clipped(const V8 &a, int col, int cols) {
     float v[kVec];
     floats_of(a, v);
     clip_row(v, col, cols);
-    return pairs_of(v);
-}
-// act8_decode for fp32, as pairs.
-__device__ __forceinline__ V8 act8_pairs(uint2 c, uint32_t b, bool e4m3) {
-    float v[kVec];
-    if (!e4m3 && b <= 230u) {
-        const float s = __uint_as_float(b ? b << 23 : 0x00400000u);
-        const f32x2 mul = pack2(s, s), off = pack2(-8388736.f * s, -8388736.f * s);
-        const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
-        V8 r;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t x = w[k >> 1];
-            r.p[k] = fma2(pack2(__uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440u | (2 * k & 3))),
-                                __uint_as_float(__byte_perm(x, 0x4b000000u, 0x7440u | ((2 * k + 1) & 3)))), mul, off);
-        }
-        return r;
-    }
-    act8_decode(c, b, e4m3, __uint_as_float(0x7f7fffffu), v);
     return pairs_of(v);
 }
 __device__ __forceinline__ float sum_of(f32x2 a) {
@@ -142,38 +100,47 @@ __device__ __forceinline__ float sum_of(f32x2 a) {
     unpack2(a, x, y);
     return x + y;
 }
+__device__ __forceinline__ V8 zeros() {
+    V8 r;
+    r.p[0] = r.p[1] = r.p[2] = r.p[3] = 0ull;
+    return r;
+}
 
-// Sums over the threads of a row. Inside a warp a butterfly, so that every lane has the same bits; over a
-// block's warps one exchange through shared memory (two buffers in turn: a thread may still read the last
-// one while another writes the next), added in the order of the warps.
-template <int LANES>
-struct RowSum {
-    float (*buf)[2][16];
-    int turn;
-    __device__ __forceinline__ RowSum(float (*b)[2][16]) : buf(b), turn(0) {}
-
-    template <int N>
-    __device__ __forceinline__ void run(float (&v)[N]) {
-        static_assert(N <= 2, "two sums at most");
+// The sums over a block's warps (or, with WARP, over the warp) of two values (BOTH) or of the second one: a
+// butterfly in each warp, which for two values first gives each half of the warp one of them; then the warps'
+// sums, in their order, from shared memory (`buf`: 16 places, the unused ones 0; two buffers in turn, as a
+// thread may still read the last one while another writes the next). Every thread gets the same bits.
+template <bool BOTH, bool WARP>
+__device__ __forceinline__ void team_sums(float &a, float &b, float2 *buf, int warps) {
+    const int lane = threadIdx.x & 31;
+    float v;
+    if (BOTH) {
+        const float give = lane < 16 ? b : a, keep = lane < 16 ? a : b;
+        v = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, 16));
 #pragma unroll
-        for (int off = (LANES < 32 ? LANES : 32) / 2; off > 0; off >>= 1)
+        for (int off = 8; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
+    } else {
+        v = b;
 #pragma unroll
-            for (int n = 0; n < N; ++n) v[n] = __fadd_rn(v[n], __shfl_xor_sync(0xffffffffu, v[n], off));
-        if (LANES <= 32) return;
-        const int warps = blockDim.x >> 5;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int n = 0; n < N; ++n) buf[turn][n][threadIdx.x >> 5] = v[n];
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float s = buf[turn][n][0];
-            for (int w = 1; w < warps; ++w) s = __fadd_rn(s, buf[turn][n][w]);
-            v[n] = s;
-        }
-        turn ^= 1;
+        for (int off = 16; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
     }
-};
+    if (WARP) {
+        if (BOTH) a = __shfl_sync(0xffffffffu, v, 0);
+        b = BOTH ? __shfl_sync(0xffffffffu, v, 16) : v;
+        return;
+    }
+    if (BOTH ? (lane & 15) == 0 : lane == 0) reinterpret_cast<float *>(buf + (threadIdx.x >> 5))[BOTH ? lane >> 4 : 1] = v;
+    __syncthreads();
+    const float4 *q = reinterpret_cast<const float4 *>(buf);
+    a = b = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k == 4 && warps <= 8) break;
+        const float4 x = q[k];
+        if (BOTH) a += x.x + x.z;
+        b += x.y + x.w;
+    }
+}
 
 __device__ __forceinline__ void load_params(const void *p, int bf16, int fast, int col, int cols, float (&v)[kVec]) {
     if (bf16) {
@@ -194,6 +161,18 @@ __device__ __forceinline__ void load_params(const void *p, int bf16, int fast, i
 #pragma unroll
             for (int j = 0; j < kVec; ++j) v[j] = col + j < cols ? __ldg(q + j) : 0.f;
         }
+    }
+}
+__device__ __forceinline__ float load_param(const void *p, int bf16, int col) {
+    return bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(p) + col) << 16) : __ldg(static_cast<const float *>(p) + col);
+}
+
+// A block's partial sum of dw or db: the teams' sums, which they left in shared memory, added in their order.
+__device__ __forceinline__ void join_teams(const float *sums, int teams, int ld, int cols, float *part) {
+    for (int c = threadIdx.x; c < cols; c += blockDim.x) {
+        float s = 0.f;
+        for (int k = 0; k < teams; ++k) s += sums[k * ld + c];
+        part[c] = s;
     }
 }
 

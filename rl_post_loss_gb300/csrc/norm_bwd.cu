@@ -1,200 +1,187 @@
-// The backward pass of the norms (mathematics and layout: norm.cuh).
+// The backward pass of the norms (mathematics: norm.cuh): the kernels for short rows and for rows that start
+// anywhere, the sum of the blocks' partial sums, and which kernel takes a call.
 #include <algorithm>
 
 #include "norm.cuh"
+#include "norm_ring.cuh"
 
 namespace rlk {
 
 namespace {
 
+constexpr int kThreads = kNormWarps * 32;
 constexpr int kJoinCols = 32, kJoinRows = 8;
 
-struct Bf16Rows {
-    using Raw = Raw16;
-    static __device__ __forceinline__ void load(Raw &r, const RowMat &m, int64_t row, int col, int cols) {
-        load_raw(r, static_cast<const __nv_bfloat16 *>(m.p) + row * m.ld, col, cols, m.fast);
-    }
-};
-struct F32Rows {
-    using Raw = Raw32;
-    static __device__ __forceinline__ void load(Raw &r, const RowMat &m, int64_t row, int col, int cols) {
-        load_raw(r, static_cast<const float *>(m.p) + row * m.ld, col, cols, m.fast);
-    }
-};
+// ---------------------------------------------------------------- short rows
+//
+// Rows on 16-byte boundaries that fit `lanes` threads of a warp (4 to 32) with VPT vectors each, so that a warp
+// works on several rows and a row's sums take few steps; rows are held in registers from one load to the store.
 
-// h from where the forward pass left it.
-struct FromBf16 {
-    Raw16 r;
-    __device__ __forceinline__ void load(const NormBackwardParams &p, int64_t row, int col) { Bf16Rows::load(r, p.x, row, col, p.cols); }
-    __device__ __forceinline__ void get(const NormBackwardParams &, float (&v)[kVec]) const { to_float(r, v); }
+template <bool BF16>
+struct RawMat {
+    using type = Raw16;
 };
-struct FromF32 {
-    Raw32 r;
-    __device__ __forceinline__ void load(const NormBackwardParams &p, int64_t row, int col) { F32Rows::load(r, p.x, row, col, p.cols); }
-    __device__ __forceinline__ void get(const NormBackwardParams &, float (&v)[kVec]) const { to_float(r, v); }
+template <>
+struct RawMat<false> {
+    using type = Raw32;
 };
-struct FromAct8 {
-    Raw8 r;
-    uint32_t b;
-    __device__ __forceinline__ void load(const NormBackwardParams &p, int64_t row, int col) {
-        load_raw(r, p.ckpt.codes + row * p.ckpt.ld_codes, col, p.cols, p.ckpt.fast);
-        b = p.ckpt.scales[row * p.ckpt.ld_scales + col / kAct8Block];
-    }
-    __device__ __forceinline__ void get(const NormBackwardParams &p, float (&v)[kVec]) const {
-        act8_decode(r.a, b, p.ckpt.e4m3, __uint_as_float(0x7f7fffffu), v);
-    }
-};
+template <bool BF16>
+__device__ __forceinline__ void load_mat(typename RawMat<BF16>::type &r, const RowMat &m, int64_t row, int col, int cols) {
+    if constexpr (BF16)
+        load_raw(r, static_cast<const __nv_bfloat16 *>(m.p) + row * m.ld, col, cols, true);
+    else
+        load_raw(r, static_cast<const float *>(m.p) + row * m.ld, col, cols, true);
+}
+__device__ __forceinline__ V8 pairs(const Raw16 &r) { return bf16_pairs(r.a); }
+__device__ __forceinline__ V8 pairs(const Raw32 &r) { return f32_pairs(r.a, r.b); }
 
-// A block takes rows in turn and keeps, in every thread, the sums of dw (and db) over them for that thread's
-// columns; it leaves them as one of the partial sums that norm_join_kernel adds.
-template <typename From, typename Dy, int VPT, int LANES, bool DB>
-__global__ void __launch_bounds__(512) norm_backward_kernel(NormBackwardParams p) {
-    __shared__ float s_buf[2][2][16];
-    RowSum<LANES> sums(s_buf);
-    const int lanes = p.lanes, groups = blockDim.x / lanes, group = threadIdx.x / lanes, t = threadIdx.x - group * lanes;
-    float dw[VPT][kVec], db[DB ? VPT : 1][kVec];
+template <int SRC, bool XBF16, bool DYBF16, int VPT, bool FULL>
+__global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBackwardParams p, int lanes) {
+    extern __shared__ __align__(16) float smem_short[];
+    float *w_smem = smem_short;  // [lanes VPT 8]
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & (lanes - 1), per_warp = 32 / lanes;
+    const int width = lanes * VPT * kVec;
+    for (int c = threadIdx.x; c < width; c += kThreads) w_smem[c] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
+    __syncthreads();
+    V8 dw[VPT], db[FULL ? VPT : 1];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            dw[i][j] = 0.f;
-            if (DB) db[i][j] = 0.f;
-        }
-    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += (int64_t)gridDim.x * groups) {
-        const int64_t row = r0 + group;
-        const bool mine = row < p.rows;
-        const bool on = mine && (!p.mask || p.mask[row]);
-        From h[VPT];
-        typename Dy::Raw dy[VPT];
+    for (int i = 0; i < VPT; ++i) {
+        dw[i] = zeros();
+        if (FULL) db[i] = zeros();
+    }
+    const int64_t step = (int64_t)gridDim.x * kNormWarps * per_warp;
+    for (int64_t base = (blockIdx.x + (int64_t)warp * gridDim.x) * per_warp; base < p.rows; base += step) {
+        const int64_t row = base + lane / lanes;
+        const bool mine = row < p.rows, on = mine && (!p.mask || p.mask[row]);
+        typename RawMat<DYBF16>::type dy[VPT];
+        typename RawMat<XBF16>::type hx[VPT], ds[VPT];
+        Raw8 h8[VPT];
+        uint32_t scale[VPT];
         float mean = 0.f, rstd = 0.f;
         if (on) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int col = (t + i * lanes) * kVec;
+                const int vec = t + i * lanes, col = vec * kVec;
                 if (col < p.cols) {
-                    h[i].load(p, row, col);
-                    Dy::load(dy[i], p.dy, row, col, p.cols);
+                    if (from_act8(SRC)) {
+                        load_raw(h8[i], p.ckpt.codes + row * p.ckpt.ld_codes, col, p.cols, true);
+                        scale[i] = p.ckpt.scales[row * p.ckpt.ld_scales + (vec >> 2)];
+                    } else {
+                        load_mat<XBF16>(hx[i], p.x, row, col, p.cols);
+                    }
+                    load_mat<DYBF16>(dy[i], p.dy, row, col, p.cols);
+                    if (p.dsummed.p) load_mat<XBF16>(ds[i], p.dsummed, row, col, p.cols);
                 }
             }
             rstd = p.rstd[row];
-            if (!p.rms) mean = p.mean[row];
+            if (FULL && !p.rms) mean = p.mean[row];
         }
-        float s[2] = {0.f, 0.f};
-        float xh[VPT][kVec], g[VPT][kVec];
+        const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
+        const auto get_h = [&](int i) -> V8 {
+            if constexpr (from_act8(SRC))
+                return act8_decode_norm<SRC == kHE4M3>(h8[i].a, scale[i]);
+            else
+                return pairs(hx[i]);
+        };
+        f32x2 s0 = 0ull, s1 = 0ull;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int col = (t + i * lanes) * kVec;
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) xh[i][j] = g[i][j] = 0.f;
             if (!on || col >= p.cols) continue;
-            h[i].get(p, xh[i]);
-            to_float(dy[i], g[i]);
+            V8 g = pairs(dy[i]), h = get_h(i);
+            if (col + kVec > p.cols) h = clipped(h, col, p.cols), g = clipped(g, col, p.cols);
+            const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), t + i * lanes);
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) xh[i][j] = (xh[i][j] - mean) * rstd;
-            if (col + kVec > p.cols) {
-                clip_row(xh[i], col, p.cols);
-                clip_row(g[i], col, p.cols);
-            }
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                dw[i][j] = fmaf(g[i][j], xh[i][j], dw[i][j]);
-                if (DB) db[i][j] += g[i][j];
-            }
-            if (p.w) {
-                float w[kVec];
-                load_params(p.w, p.params_bf16, p.params_fast, col, p.cols, w);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) g[i][j] *= w[j];
-            }
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                s[0] += g[i][j];
-                s[1] = fmaf(g[i][j], xh[i][j], s[1]);
+            for (int k = 0; k < 4; ++k) {
+                const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, w.p[k]);
+                dw[i].p[k] = fma2(r, d, dw[i].p[k]);
+                if (FULL) {
+                    db[i].p[k] = add2(db[i].p[k], g.p[k]);
+                    s0 = add2(s0, u);
+                }
+                s1 = fma2(u, d, s1);
             }
         }
-        sums.run(s);
-        const float c1 = p.rms ? 0.f : s[0] * p.inv_cols, c2 = s[1] * p.inv_cols;
+        float c1 = sum_of(s0), c2 = sum_of(s1);
+        for (int off = lanes >> 1; off > 0; off >>= 1) {
+            if (FULL) c1 = __fadd_rn(c1, __shfl_xor_sync(0xffffffffu, c1, off));
+            c2 = __fadd_rn(c2, __shfl_xor_sync(0xffffffffu, c2, off));
+        }
         if (!mine) continue;
-        if (t == 0 && on && p.status && !(fabsf(s[0]) < INFINITY && fabsf(s[1]) < INFINITY)) raise_status(p.status, RL_ERR_NONFINITE);
+        if (t == 0 && p.status && !(fabsf(c1) < INFINITY && fabsf(c2) < INFINITY)) raise_status(p.status, RL_ERR_NONFINITE);
+        c1 = FULL && !p.rms ? c1 * p.inv_cols : 0.f;
+        c2 = c2 * p.inv_cols * rstd * rstd;
+        const f32x2 o1 = pack2(-c1, -c1), nk = pack2(-c2, -c2);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int col = (t + i * lanes) * kVec;
             if (col >= p.cols) continue;
-            float o[kVec];
-            if (p.y.p) {
-                float w[kVec];
+            float o[kVec] = {};
+            if (on) {
+                const V8 g = pairs(dy[i]), h = get_h(i), w = read_vec<false>(reinterpret_cast<const char *>(w_smem), t + i * lanes);
+                V8 r;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) o[j] = xh[i][j];
-                if (p.w) {
-                    load_params(p.w, p.params_bf16, p.params_fast, col, p.cols, w);
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) o[j] *= w[j];
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 rr = mul2(g.p[k], rs), u = FULL ? fma2(rr, w.p[k], o1) : mul2(rr, w.p[k]);
+                    r.p[k] = fma2(FULL ? add2(h.p[k], nm) : h.p[k], nk, u);
                 }
-                if (p.b && on) {
-                    load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, w);
+                if (p.dsummed.p) {
+                    const V8 q = pairs(ds[i]);
 #pragma unroll
-                    for (int j = 0; j < kVec; ++j) o[j] += w[j];
+                    for (int k = 0; k < 4; ++k) r.p[k] = add2(r.p[k], q.p[k]);
                 }
+                if (p.y.p) {
+                    float b[kVec] = {};
+                    if (p.b) load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, b);
+                    V8 v = pairs_of(b);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v.p[k] = fma2(mul2(add2(h.p[k], nm), rs), w.p[k], v.p[k]);
+                    floats_of(v, o);
+                    store_row(p.y, row, col, p.cols, o);
+                }
+                floats_of(r, o);
+            } else if (p.y.p) {
                 store_row(p.y, row, col, p.cols, o);
             }
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) o[j] = on ? rstd * (g[i][j] - c1 - xh[i][j] * c2) : 0.f;
-            if (on && p.dsummed.p) {
-                float u[kVec];
-                if (p.dsummed.bf16) {
-                    Raw16 r;
-                    Bf16Rows::load(r, p.dsummed, row, col, p.cols);
-                    to_float(r, u);
-                } else {
-                    Raw32 r;
-                    F32Rows::load(r, p.dsummed, row, col, p.cols);
-                    to_float(r, u);
-                }
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) o[j] += u[j];
-            }
-            store_row(p.dx, row, col, p.cols, o);
+            if (XBF16)
+                store_vec(static_cast<__nv_bfloat16 *>(p.dx.p) + row * p.dx.ld, col, p.cols, p.dx.fast, o);
+            else
+                store_vec(static_cast<float *>(p.dx.p) + row * p.dx.ld, col, p.cols, p.dx.fast, o);
         }
     }
-
     if (!p.want_dw && !p.want_db) return;
     float *part = p.partials + (int64_t)blockIdx.x * 2 * p.ld_part;
-    if (LANES > 32) {
+#pragma unroll
+    for (int which = 0; which < (FULL ? 2 : 1); ++which) {
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int col = (t + i * lanes) * kVec;
-            if (col < p.cols) {
-                store_vec(part, col, (int)p.ld_part, true, dw[i]);
-                if (DB) store_vec(part + p.ld_part, col, (int)p.ld_part, true, db[i]);
-            }
-        }
-        return;
-    }
-    // several rows at a time: the groups' sums added in their order
-    __shared__ float s_join[LANES <= 32 ? 128 * kVec : 1];
+            float v[kVec];
+            floats_of(which ? db[FULL ? i : 0] : dw[i], v);
+            for (int off = lanes; off < 32; off <<= 1)  // the warp's rows
 #pragma unroll
-    for (int which = 0; which < (DB ? 2 : 1); ++which) {
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) s_join[threadIdx.x * kVec + j] = which ? db[0][j] : dw[0][j];
-        __syncthreads();
-        for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
-            float s = 0.f;
-            for (int k = 0; k < groups; ++k) s += s_join[k * lanes * kVec + c];
-            part[which * p.ld_part + c] = s;
+                for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], __shfl_xor_sync(0xffffffffu, v[j], off));
+            if (lane < lanes) store_vec(smem_short + warp * width, (t + i * lanes) * kVec, width, true, v);
         }
+        __syncthreads();
+        join_teams(smem_short, kNormWarps, width, p.cols, part + which * p.ld_part);
     }
 }
 
-// Adds the partial sums of a column in a fixed order: eight threads take every eighth, their sums are added in turn.
+// ---------------------------------------------------------------- the sum of the partial sums
+
+// Eight threads take every eighth partial sum of a column, their sums are added in turn.
 __global__ void __launch_bounds__(kJoinCols * kJoinRows) norm_join_kernel(const float *partials, int64_t ld, int parts, int cols, float *dw, float *db, int accumulate) {
     __shared__ float s[kJoinRows][kJoinCols];
     const int c = blockIdx.x * kJoinCols + threadIdx.x, k = threadIdx.y;
     const int which = dw ? (int)blockIdx.y : 1;
     float *out = which ? db : dw;
+    grid_dependency_wait();
     float v = 0.f;
-    if (c < cols)
+    if (c < cols) {
+#pragma unroll 8
         for (int i = k; i < parts; i += kJoinRows) v += partials[((int64_t)i * 2 + which) * ld + c];
+    }
     s[k][threadIdx.x] = v;
     __syncthreads();
     if (k == 0 && c < cols) {
@@ -206,96 +193,115 @@ __global__ void __launch_bounds__(kJoinCols * kJoinRows) norm_join_kernel(const 
 
 cudaError_t launch_join(const NormBackwardParams &p, int parts, cudaStream_t stream) {
     if (!p.want_dw && !p.want_db) return cudaSuccess;
-    const dim3 grid((p.cols + kJoinCols - 1) / kJoinCols, p.want_dw && p.want_db ? 2 : 1);
-    norm_join_kernel<<<grid, dim3(kJoinCols, kJoinRows), 0, stream>>>(p.partials, p.ld_part, parts, p.cols, p.want_dw ? p.dw : nullptr, p.want_db ? p.db : nullptr, p.accumulate);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((p.cols + kJoinCols - 1) / kJoinCols, p.want_dw && p.want_db ? 2 : 1);
+    cfg.blockDim = dim3(kJoinCols, kJoinRows);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_join_kernel, (const float *)p.partials, p.ld_part, parts, (int)p.cols,
+                              p.want_dw ? p.dw : nullptr, p.want_db ? p.db : nullptr, (int)p.accumulate);
+}
+
+// ---------------------------------------------------------------- which kernel
+
+int vectors(int cols) { return (cols + kVec - 1) / kVec; }
+
+// Four vectors a thread where registers hold them (16-bit rows, one sum), two otherwise.
+template <int SRC, bool XBF16, bool DYBF16, bool FULL>
+cudaError_t launch_short(const NormBackwardParams &p, int blocks, cudaStream_t stream) {
+    constexpr int kVecs = DYBF16 && XBF16 && !FULL ? 4 : 2;
+    int lanes = 4;
+    while (lanes * kVecs * kVec < p.cols) lanes *= 2;
+    const size_t smem = (size_t)kNormWarps * lanes * kVecs * kVec * sizeof(float);  // (the sums; the weight before them)
+    norm_backward_short_kernel<SRC, XBF16, DYBF16, kVecs, FULL><<<blocks, kThreads, smem, stream>>>(p, lanes);
     return cudaGetLastError();
 }
 
-// The fewest warps of a block that leave a thread three vectors, 16 at most.
-int fewest_warps(int cols) {
-    const int vecs = (cols + kVec - 1) / kVec;
-    return std::min(16, std::max(1, (vecs + 95) / 96));
-}
+constexpr int kShortCols = 512;  // at most a warp of two vectors, 32 KB of sums
 
-constexpr size_t kSmemOfSM = 228 * 1024;
+constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 512;  // what a block takes beside its rows
 
-// Blocks of up to 16 warps on an SM, 128 registers a thread; the fewest warps a block that leave a thread three
-// vectors (four beyond 12288 columns), and stages of the whole SM's shared memory.
-NormRing ring_of(const NormBackwardParams &p) {
-    NormRing r{};
-    const auto row_bytes = [&](size_t es) { return (p.cols * es + 15) / 16 * 16; };
-    r.h_bytes = row_bytes(!p.x.p ? 1 : p.x.bf16 ? 2 : 4);
-    r.dy_bytes = row_bytes(p.dy.bf16 ? 2 : 4);
-    r.ds_bytes = p.dsummed.p ? row_bytes(p.dsummed.bf16 ? 2 : 4) : 0;
-    const int vecs = (p.cols + kVec - 1) / kVec;
-    r.w_bytes = (size_t)vecs * kVec * 4;
-    const size_t stage = r.h_bytes + r.dy_bytes + r.ds_bytes, fixed = r.w_bytes + 32 + 2048;  // (32: an fp32 vector past the row's end)
-    int blocks = 16 / fewest_warps(p.cols);
-    while (blocks > 1 && blocks * (2 * stage + fixed) > kSmemOfSM) --blocks;
-    r.warps = std::min(16 / blocks, (vecs + 31) / 32);
-    r.vecs = (vecs + r.warps * 32 - 1) / (r.warps * 32);
-    r.warps = (vecs + r.vecs * 32 - 1) / (r.vecs * 32);
-    r.blocks_per_sm = blocks;
-    const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks);
-    if (room < fixed + 2 * stage) return r;
-    r.depth = (int)std::min<size_t>(8, (room - fixed) / stage);
-    r.smem = r.depth * stage + r.w_bytes + 32;
-    return r;
-}
-
-template <typename From, typename Dy, int VPT, int LANES>
-cudaError_t launch(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    const int parts = norm_backward_parts(p.rows, p.cols);
-    if (p.want_db)
-        norm_backward_kernel<From, Dy, VPT, LANES, true><<<parts, s.threads, 0, stream>>>(p);
-    else
-        norm_backward_kernel<From, Dy, VPT, LANES, false><<<parts, s.threads, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? launch_join(p, parts, stream) : e;
-}
-
-template <typename From, typename Dy>
-cudaError_t launch_shape(const NormBackwardParams &p, const NormShape &s, cudaStream_t stream) {
-    switch (s.lanes) {
-        case 8: return launch<From, Dy, 1, 8>(p, s, stream);
-        case 16: return launch<From, Dy, 1, 16>(p, s, stream);
-        case 32: return launch<From, Dy, 1, 32>(p, s, stream);
+// A block per row, 128 registers a thread, so 16 warps on an SM: of the numbers of vectors a thread, the one whose
+// blocks take all rows soonest, by a row's time of its vectors and two more for the exchange of sums. Both sums with
+// four vectors a thread (rows that start anywhere: with three) do not fit the registers, and are taken for the
+// longest rows alone.
+NormTeams teams_of(const NormBackwardParams &p, int mode) {
+    const bool act8 = !p.x.p, full = !p.rms || p.want_db || mode == kAnyRow;
+    const int vecs = vectors(p.cols), pad = mode == kAnyRow ? 16 : 0;
+    const auto bytes = [&](int es) { return (p.cols * es + 15) / 16 * 16 + pad; };
+    NormTeams n{};
+    n.mode = mode;
+    n.at_dy = bytes(act8 ? 1 : p.x.bf16 ? 2 : 4);
+    n.at_ds = n.at_dy + bytes(p.dy.bf16 ? 2 : 4);
+    n.at_scales = n.at_ds + (p.dsummed.p ? bytes(p.dx.bf16 ? 2 : 4) : 0);
+    n.stage_bytes = n.at_scales + (mode == kAnyRow && act8 ? (p.cols / kAct8Block + 1 + 15) / 16 * 16 + pad : 0);
+    if (mode == kWarpRow) {
+        n.warps = 1;
+        n.vecs = vecs > 96 ? 4 : 3;
+        n.blocks_per_sm = 1;
+        n.depth = (int)std::min<size_t>(kNormDepth, kNormRingSmem / (kNormWarps * n.stage_bytes));
+        n.smem = std::max((size_t)kNormWarps * n.depth * n.stage_bytes, (size_t)kNormWarps * n.vecs * 32 * kVec * 4);
+        return n;
     }
-    switch (s.vecs) {
-        case 1: return launch<From, Dy, 1, 64>(p, s, stream);
-        case 2: return launch<From, Dy, 2, 64>(p, s, stream);
-        case 3: return launch<From, Dy, 3, 64>(p, s, stream);
-        default: return launch<From, Dy, 4, 64>(p, s, stream);
+    double best = 0;
+    for (int v = 1; v <= 4; ++v) {
+        const int warps = (vecs + 32 * v - 1) / (32 * v);
+        if (warps > kNormWarps || (v >= (mode == kAnyRow ? 3 : 4) && full && n.warps)) continue;
+        const bool regs = mode == kAnyRow ? v == 1 : v <= 3 || !full;
+        size_t w_bytes = regs ? 0 : (size_t)v * warps * 32 * kVec * 4;
+        int blocks = kNormWarps / warps;
+        while (blocks > 1 && blocks * (kBlockExtra + w_bytes + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
+        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + 2);
+        if (n.warps && time >= best) continue;
+        best = time;
+        const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks - kBlockExtra);
+        n.w_in_smem = w_bytes + n.stage_bytes <= room;
+        if (!n.w_in_smem) w_bytes = 0;
+        n.warps = warps, n.vecs = v, n.blocks_per_sm = blocks;
+        n.depth = (int)std::min<size_t>(kNormDepth, (room - w_bytes) / n.stage_bytes);
+        n.smem = (size_t)n.depth * n.stage_bytes + w_bytes;
     }
+    return n;
 }
 
 }  // namespace
 
+// As many blocks as run at once: one of 16 warps on an SM for rows that warps take, else of the warps that four
+// vectors a thread need.
 int norm_backward_parts(int rows, int cols) {
-    const NormShape s = norm_shape(cols);
-    const int64_t blocks = ((int64_t)rows + s.groups - 1) / s.groups;
-    const int ring = s.groups == 1 ? 16 / fewest_warps(cols) : 0;  // blocks on an SM, of either kernel
-    const int most = kNormSMs * std::max({ring, 512 / s.threads, 1});
-    return (int)(blocks < most ? blocks : most);
+    const int warps = (vectors(cols) + 127) / 128;
+    return (int)std::min<int64_t>(rows, kNormSMs * (kNormWarps / warps));
 }
 
-cudaError_t launch_norm_backward(const NormBackwardParams &q, cudaStream_t stream) {
-    NormBackwardParams p = q;
-    const NormShape s = norm_shape(p.cols);
-    p.lanes = s.lanes;
-    const bool act8 = !p.x.p;
-    if (p.cols > 256 && (p.dx.bf16 <= p.dy.bf16) && p.dy.fast && (act8 ? p.ckpt.fast : p.x.fast) && (!p.dsummed.p || p.dsummed.fast)) {
-        const NormRing r = ring_of(p);
-        if (r.depth >= 2) {
-            const int parts = std::min(p.rows, kNormSMs * r.blocks_per_sm);
-            const cudaError_t e = !act8 ? p.x.bf16 ? launch_norm_ring_bf16(p, r, parts, stream) : launch_norm_ring_f32(p, r, parts, stream)
-                                        : launch_norm_ring_act8(p, r, parts, stream);
-            return e == cudaSuccess ? launch_join(p, parts, stream) : e;
-        }
+cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream) {
+    const bool act8 = !p.x.p, full = !p.rms || p.want_db;
+    const bool fast = p.dy.fast && (act8 ? p.ckpt.fast : p.x.fast) && (!p.dsummed.p || p.dsummed.fast);
+    cudaError_t e = cudaErrorUnknown;
+    int blocks;
+    if (fast && p.cols <= kShortCols && p.dx.bf16 <= p.dy.bf16) {
+        blocks = std::min(p.rows, kNormSMs);
+#define RLK_SHORT(SRC, X, DY) (full ? launch_short<SRC, X, DY, true>(p, blocks, stream) : launch_short<SRC, X, DY, false>(p, blocks, stream))
+        if (act8)
+            e = p.ckpt.e4m3 ? p.dx.bf16 ? RLK_SHORT(kHE4M3, true, true) : p.dy.bf16 ? RLK_SHORT(kHE4M3, false, true) : RLK_SHORT(kHE4M3, false, false)
+                            : p.dx.bf16 ? RLK_SHORT(kHInt8, true, true) : p.dy.bf16 ? RLK_SHORT(kHInt8, false, true) : RLK_SHORT(kHInt8, false, false);
+        else
+            e = p.x.bf16 ? RLK_SHORT(kHBf16, true, true) : p.dy.bf16 ? RLK_SHORT(kHF32, false, true) : RLK_SHORT(kHF32, false, false);
+#undef RLK_SHORT
+    } else {
+        const bool any = !fast || (!act8 && p.x.bf16 && !p.dy.bf16);
+        // a warp per row where there are rows for all warps
+        const bool warp = !any && p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps;
+        const NormTeams n = teams_of(p, any ? kAnyRow : warp ? kWarpRow : kBlockRow);
+        blocks = std::min(p.rows, kNormSMs * n.blocks_per_sm);
+#define RLK_ROWS(H) (p.dy.bf16 ? launch_norm_rows_##H##_bf16(p, n, blocks, stream) : launch_norm_rows_##H##_f32(p, n, blocks, stream))
+        e = act8 ? p.ckpt.e4m3 ? RLK_ROWS(e4m3) : RLK_ROWS(int8) : p.x.bf16 ? RLK_ROWS(bf16) : RLK_ROWS(f32);
+#undef RLK_ROWS
     }
-    if (!p.x.p) return p.dy.bf16 ? launch_shape<FromAct8, Bf16Rows>(p, s, stream) : launch_shape<FromAct8, F32Rows>(p, s, stream);
-    if (p.x.bf16) return p.dy.bf16 ? launch_shape<FromBf16, Bf16Rows>(p, s, stream) : launch_shape<FromBf16, F32Rows>(p, s, stream);
-    return p.dy.bf16 ? launch_shape<FromF32, Bf16Rows>(p, s, stream) : launch_shape<FromF32, F32Rows>(p, s, stream);
+    return e == cudaSuccess ? launch_join(p, blocks, stream) : e;
 }
 
 }  // namespace rlk

@@ -5,6 +5,38 @@ namespace rlk {
 
 namespace {
 
+// Sums over the threads of a row. Inside a warp a butterfly, so that every lane has the same bits; over a
+// block's warps one exchange through shared memory (two buffers in turn: a thread may still read the last
+// one while another writes the next), added in the order of the warps.
+template <int LANES>
+struct RowSum {
+    float (*buf)[2][16];
+    int turn;
+    __device__ __forceinline__ RowSum(float (*b)[2][16]) : buf(b), turn(0) {}
+
+    template <int N>
+    __device__ __forceinline__ void run(float (&v)[N]) {
+        static_assert(N <= 2, "two sums at most");
+#pragma unroll
+        for (int off = (LANES < 32 ? LANES : 32) / 2; off > 0; off >>= 1)
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] = __fadd_rn(v[n], __shfl_xor_sync(0xffffffffu, v[n], off));
+        if (LANES <= 32) return;
+        const int warps = blockDim.x >> 5;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int n = 0; n < N; ++n) buf[turn][n][threadIdx.x >> 5] = v[n];
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            float s = buf[turn][n][0];
+            for (int w = 1; w < warps; ++w) s = __fadd_rn(s, buf[turn][n][w]);
+            v[n] = s;
+        }
+        turn ^= 1;
+    }
+};
+
 template <typename T>
 struct RawOf;
 template <>

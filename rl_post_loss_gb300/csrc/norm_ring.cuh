@@ -1,13 +1,17 @@
-// The backward pass of the norms on rows that start on 16-byte boundaries (mathematics: norm.cuh).
+// The backward pass of the norms with rows brought into shared memory by bulk copies (mathematics: norm.cuh).
 //
-// Bulk copies bring the next rows into shared memory while the block works on one, which it reads twice from
-// there (the sums, then dx), so that a thread holds little more than its sums of dw and db in registers. A
-// row's stage is filled again after the next row's exchange of sums, when every thread has left it: no
-// barrier but that exchange's.
+// While a team of warps works on a row, the copies of its next rows are under way. The row is read twice from
+// shared memory (the sums, then dx), so that a thread holds little more than its sums of dw and db in
+// registers. A row's stage is filled again after the next row's exchange of sums, when every thread of the
+// team has left it: no barrier but that exchange's (with room for one row only, one more after each row).
 //
-// Written with r = dy rstd, u = r w, d = h - mean: xh = d rstd, g = dy w, so dw += r d, mean(g) rstd =
-// mean(u), mean(g xh) = mean(u d), and dx = u - mean(u) - d k + dsummed with k = rstd^2 mean(u d). FULL = false
-// is the RMS form without db, in which mean = 0 and sum(u) is not needed.
+// A team is a block (kBlockRow: two or more on an SM cover each other's exchanges) or, for rows of 1024
+// columns and less, one warp of a block of 16 (kWarpRow: no barriers, and one partial sum for 16 rows at a
+// time). Its threads hold vectors of eight columns, which needs rows on 16-byte boundaries. Rows that start
+// anywhere (kAnyRow) are copied from the 16-byte boundary before them, and column c belongs to thread c mod
+// the team's threads: single loads and stores of a warp then lie side by side.
+//
+// FULL = false is the RMS form without db, in which mean = 0 and sum(u) is not needed.
 #pragma once
 
 #include "norm.cuh"
@@ -15,7 +19,9 @@
 
 namespace rlk {
 
-enum HSource { kHBf16, kHF32, kHAct8 };
+enum HSource { kHBf16, kHF32, kHInt8, kHE4M3 };
+constexpr bool from_act8(int src) { return src >= kHInt8; }
+enum RowMode { kBlockRow, kWarpRow, kAnyRow };
 
 constexpr uint64_t kNormWaitNs = 1000000000ull;
 
@@ -25,105 +31,154 @@ __device__ __forceinline__ V8 read_vec(const char *row, int vec) {
     const uint4 *q = reinterpret_cast<const uint4 *>(row + vec * 32);
     return f32_pairs(q[0], q[1]);
 }
+template <bool BF16>
+__device__ __forceinline__ float read_one(const char *row, int col) {
+    if (BF16) return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(row + col * 2) << 16);
+    return *reinterpret_cast<const float *>(row + col * 4);
+}
 template <int SRC>
-__device__ __forceinline__ V8 read_h(const char *row, int vec, uint32_t scale, bool e4m3) {
-    if (SRC != kHAct8) return read_vec<SRC == kHBf16>(row, vec);
-    return act8_pairs(*reinterpret_cast<const uint2 *>(row + vec * 8), scale, e4m3);
+__device__ __forceinline__ V8 read_h(const char *row, int vec, uint32_t scale) {
+    if (!from_act8(SRC)) return read_vec<SRC == kHBf16>(row, vec);
+    return act8_decode_norm<SRC == kHE4M3>(*reinterpret_cast<const uint2 *>(row + vec * 8), scale);
+}
+__device__ __forceinline__ void store_one(const RowMat &m, int64_t at, float v) {
+    if (m.bf16)
+        static_cast<__nv_bfloat16 *>(m.p)[at] = __float2bfloat16_rn(v);
+    else
+        static_cast<float *>(m.p)[at] = v;
 }
 
-// The block's sums of two values (FULL) or of the second one: a butterfly in each warp, which for two values
-// first gives each half of the warp one of them; then the warps' sums, in their order, from shared memory.
-// Two buffers in turn; unused places hold 0.
-template <bool FULL>
-__device__ __forceinline__ void block_sums(float &a, float &b, float2 *buf, int warps) {
-    const int lane = threadIdx.x & 31;
-    if (FULL) {
-        const float give = lane < 16 ? b : a, keep = lane < 16 ? a : b;
-        float v = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, 16));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-        if ((lane & 15) == 0) reinterpret_cast<float *>(buf + (threadIdx.x >> 5))[lane >> 4] = v;
-    } else {
-        float v = b;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-        if (lane == 0) buf[threadIdx.x >> 5].y = v;
+// A thread's i-th eight columns. Only the last ones may be cut off by the row's end, or not there at all.
+template <int MODE, int VPT>
+struct Columns {
+    int t, T, cols;
+    bool has_last, cut;
+    __device__ __forceinline__ Columns(int t, int T, int cols) : t(t), T(T), cols(cols) {
+        const int vec = t + (VPT - 1) * T;
+        has_last = MODE == kAnyRow || vec * kVec < cols;
+        cut = MODE == kAnyRow || (vec + 1) * kVec > cols;
     }
-    __syncthreads();
-    const float4 *q = reinterpret_cast<const float4 *>(buf);
-    a = b = 0.f;
+    __device__ __forceinline__ bool none(int i) const { return i == VPT - 1 && !has_last; }
+    __device__ __forceinline__ int vec(int i) const { return t + i * T; }
+    __device__ __forceinline__ int col(int i, int j) const { return MODE == kAnyRow ? t + (i * kVec + j) * T : vec(i) * kVec + j; }
+    // eight single values, 0 past the row's end
+    template <typename Get>
+    __device__ __forceinline__ V8 singles(int i, Get get) const {
+        V8 r;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float4 x = q[k];
-        a += x.x + x.z;
-        b += x.y + x.w;
-    }
-    if (warps > 8) {
-#pragma unroll
-        for (int k = 4; k < 8; ++k) {
-            const float4 x = q[k];
-            a += x.x + x.z;
-            b += x.y + x.w;
+        for (int k = 0; k < 4; ++k) {
+            const int a = col(i, 2 * k), b = col(i, 2 * k + 1);
+            r.p[k] = pack2(i < VPT - 1 || a < cols ? get(a) : 0.f, i < VPT - 1 || b < cols ? get(b) : 0.f);
         }
+        return r;
     }
-}
+    template <bool BF16>
+    __device__ __forceinline__ V8 read(const char *row, int i) const {
+        if (MODE == kAnyRow) return singles(i, [&](int c) { return read_one<BF16>(row, c); });
+        return read_vec<BF16>(row, vec(i));
+    }
+    __device__ __forceinline__ V8 params(const void *p, int bf16, int fast, int i, float missing) const {
+        if (!p) return singles(i, [&](int) { return missing; });
+        if (MODE == kAnyRow) return singles(i, [&](int c) { return load_param(p, bf16, c); });
+        float v[kVec];
+        load_params(p, bf16, fast, vec(i) * kVec, cols, v);
+        return pairs_of(v);
+    }
+    __device__ __forceinline__ void store(const RowMat &m, int64_t row, int i, const V8 &a) const {
+        float v[kVec];
+        floats_of(a, v);
+        if (MODE != kAnyRow) {
+            store_row(m, row, vec(i) * kVec, cols, v);
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (i < VPT - 1 || col(i, j) < cols) store_one(m, row * m.ld + col(i, j), v[j]);
+    }
+};
 
-template <int SRC, bool XBF16, bool DYBF16, int VPT, bool FULL>
-__global__ void __launch_bounds__(512) norm_backward_ring_kernel(NormBackwardParams p, NormRing ring) {
-    constexpr bool kWInRegs = VPT <= 3 || !FULL;  // (four vectors with both sums leave no room for it)
+// The bytes that a row's copy starts before the row.
+template <int MODE>
+__device__ __forceinline__ int row_shift(const char *row) { return MODE == kAnyRow ? (int)(reinterpret_cast<uintptr_t>(row) & 15u) : 0; }
+
+template <int SRC, bool DYBF16, int VPT, bool FULL, int MODE>
+__global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(NormBackwardParams p, NormTeams n) {
+    constexpr bool kAct8 = from_act8(SRC), kWInRegs = MODE == kAnyRow ? VPT == 1 : VPT <= 3 || !FULL;  // (else no room is left)
+    constexpr int kTeams = MODE == kWarpRow ? kNormWarps : 1;
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) float2 s_sums[2][16];
-    __shared__ __align__(8) uint64_t s_full[8];
-    const int T = blockDim.x, t = threadIdx.x, S = ring.depth;
-    const int off_dy = (int)ring.h_bytes, off_ds = off_dy + (int)ring.dy_bytes, stage_bytes = off_ds + (int)ring.ds_bytes;
-    const int last_vec = t + (VPT - 1) * T;  // the one vector of a thread that may be short or missing
-    const bool has_last = last_vec * kVec < p.cols, cut = has_last && (last_vec + 1) * kVec > p.cols;
-    if (t < 32) reinterpret_cast<float2 *>(s_sums)[t] = make_float2(0.f, 0.f);
-    if (t == 0) {
-        for (int s = 0; s < S; ++s) ptx::mbar_init(ptx::smem_u32(&s_full[s]), 1);
+    __shared__ __align__(8) uint64_t s_full[kTeams * kNormDepth];
+    const int T = MODE == kWarpRow ? 32 : (int)blockDim.x, team = MODE == kWarpRow ? (int)threadIdx.x >> 5 : 0;
+    const int t = MODE == kWarpRow ? (int)threadIdx.x & 31 : (int)threadIdx.x, S = n.depth;
+    const Columns<MODE, VPT> at(t, T, p.cols);
+    const bool x_bf16 = kAct8 ? p.dx.bf16 : SRC == kHBf16;
+    char *stages = smem + team * S * n.stage_bytes;
+    if (threadIdx.x < 32) (&s_sums[0][0])[threadIdx.x] = make_float2(0.f, 0.f);
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kTeams * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
         ptx::fence_mbar_init();
     }
     __syncthreads();
+    const uint32_t full0 = ptx::smem_u32(&s_full[team * S]);
 
-    const int64_t step = gridDim.x;
-    const auto copy_row = [&](int64_t row, int s) {  // by thread 0
-        char *stage = smem + s * stage_bytes;
-        const uint32_t full = ptx::smem_u32(&s_full[s]);
-        ptx::mbar_arrive_expect_tx(full, (uint32_t)stage_bytes);
-        const char *h = SRC == kHAct8 ? reinterpret_cast<const char *>(p.ckpt.codes) + row * p.ckpt.ld_codes
-                                      : static_cast<const char *>(p.x.p) + row * p.x.ld * (XBF16 ? 2 : 4);
-        ptx::bulk_g2s(ptx::smem_u32(stage), h, (uint32_t)ring.h_bytes, full);
-        ptx::bulk_g2s(ptx::smem_u32(stage + off_dy), static_cast<const char *>(p.dy.p) + row * p.dy.ld * (DYBF16 ? 2 : 4), (uint32_t)ring.dy_bytes, full);
-        if (ring.ds_bytes)
-            ptx::bulk_g2s(ptx::smem_u32(stage + off_ds), static_cast<const char *>(p.dsummed.p) + row * p.dsummed.ld * (XBF16 ? 2 : 4), (uint32_t)ring.ds_bytes, full);
+    const int64_t first = blockIdx.x + (int64_t)team * gridDim.x, step = (int64_t)kTeams * gridDim.x;
+    const auto h_row = [&](int64_t row) -> const char * {
+        return kAct8 ? reinterpret_cast<const char *>(p.ckpt.codes) + row * p.ckpt.ld_codes : static_cast<const char *>(p.x.p) + row * p.x.ld * (SRC == kHBf16 ? 2 : 4);
+    };
+    const auto dy_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.dy.p) + row * p.dy.ld * (DYBF16 ? 2 : 4); };
+    const auto ds_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.dsummed.p) + row * p.dsummed.ld * (x_bf16 ? 2 : 4); };
+    const auto scale_row = [&](int64_t row) -> const char * { return reinterpret_cast<const char *>(p.ckpt.scales) + row * p.ckpt.ld_scales; };
+    // Copies whole 16-byte pieces of memory that hold a row of `bytes` bytes (on 16-byte boundaries: the row rounded up).
+    const auto copy = [&](char *to, const char *from, int bytes, uint32_t full) -> uint32_t {
+        const int shift = row_shift<MODE>(from), size = (shift + bytes + 15) & ~15;
+        ptx::bulk_g2s(ptx::smem_u32(to), from - shift, (uint32_t)size, full);
+        return (uint32_t)size;
+    };
+    const auto copy_row = [&](int64_t row, int s) {  // by the team's thread 0
+        char *stage = stages + s * n.stage_bytes;
+        const uint32_t full = full0 + s * 8;
+        const int h_bytes = p.cols * (kAct8 ? 1 : SRC == kHBf16 ? 2 : 4), dy_bytes = p.cols * (DYBF16 ? 2 : 4);
+        const int ds_bytes = p.cols * (x_bf16 ? 2 : 4), scale_bytes = (p.cols + kAct8Block - 1) / kAct8Block;
+        uint32_t sum;
+        const auto size = [&](const char *from, int bytes) { return (uint32_t)((row_shift<MODE>(from) + bytes + 15) & ~15); };
+        sum = size(h_row(row), h_bytes) + size(dy_row(row), dy_bytes);
+        if (p.dsummed.p) sum += size(ds_row(row), ds_bytes);
+        if (MODE == kAnyRow && kAct8) sum += size(scale_row(row), scale_bytes);
+        ptx::mbar_arrive_expect_tx(full, sum);
+        copy(stage, h_row(row), h_bytes, full);
+        copy(stage + n.at_dy, dy_row(row), dy_bytes, full);
+        if (p.dsummed.p) copy(stage + n.at_ds, ds_row(row), ds_bytes, full);
+        if (MODE == kAnyRow && kAct8) copy(stage + n.at_scales, scale_row(row), scale_bytes, full);
     };
     if (t == 0)
         for (int s = 0; s < S; ++s) {
-            const int64_t row = blockIdx.x + s * step;
+            const int64_t row = first + s * step;
             if (row < p.rows && (!p.mask || p.mask[row])) copy_row(row, s);
         }
 
-    float *w_smem = reinterpret_cast<float *>(smem + S * stage_bytes);  // a thread's own part, read by nobody else
+    float *w_smem = reinterpret_cast<float *>(smem + kTeams * S * n.stage_bytes);  // [VPT T 8], a thread reads its own
     V8 w[kWInRegs ? VPT : 1], dw[VPT], db[FULL ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        float v[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) v[j] = 1.f;
-        if (p.w && (i < VPT - 1 || has_last)) load_params(p.w, p.params_bf16, p.params_fast, (t + i * T) * kVec, p.cols, v);
-        if (kWInRegs)
-            w[i] = pairs_of(v);
-        else if (i < VPT - 1 || has_last)
-            store_vec(w_smem, (t + i * T) * kVec, (t + i * T) * kVec + kVec, true, v);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            dw[i].p[k] = 0ull;
-            if (FULL) db[i].p[k] = 0ull;
+        const V8 v = at.none(i) ? zeros() : at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
+        if (kWInRegs) {
+            w[i] = v;
+        } else if (n.w_in_smem) {
+            float f[kVec];
+            floats_of(v, f);
+            store_vec(w_smem, at.vec(i) * kVec, at.vec(i) * kVec + kVec, true, f);
         }
+        dw[i] = zeros();
+        if (FULL) db[i] = zeros();
     }
+    const auto weight = [&](int i) -> V8 {
+        if constexpr (kWInRegs) return w[i];
+        if (!n.w_in_smem) return at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
+        return read_vec<false>(reinterpret_cast<const char *>(w_smem), at.vec(i));
+    };
 
     // of the row at hand, loaded a row ahead
-    constexpr int kScales = SRC == kHAct8 ? VPT : 1;
+    constexpr int kScales = kAct8 && MODE != kAnyRow ? VPT : 1;
     bool dead = false, on = true;
     float mean = 0.f, rstd = 0.f;
     uint32_t scale[kScales];
@@ -132,29 +187,38 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(NormBackwardPar
         o = !p.mask || p.mask[row];
         r = p.rstd[row];
         if (FULL && !p.rms) m = p.mean[row];
-        if (SRC == kHAct8) {
+        if (kAct8 && MODE != kAnyRow) {
             const uint8_t *q = p.ckpt.scales + row * p.ckpt.ld_scales;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
-                if (i < VPT - 1 || has_last) sc[i] = q[(t + i * T) >> 2];
+                if (!at.none(i)) sc[i] = q[at.vec(i) >> 2];
         }
     };
-    row_data(blockIdx.x, on, mean, rstd, scale);
+    row_data(first, on, mean, rstd, scale);
     uint32_t phases = 0;  // of the stages' barriers
     int s = 0, last = 0, turn = 0;
-    for (int64_t row = blockIdx.x; row < p.rows; row += step) {
+    for (int64_t row = first; row < p.rows; row += step) {
         bool on_next = true;
         float mean_next = 0.f, rstd_next = 0.f;
         uint32_t scale_next[kScales] = {};
         row_data(row + step, on_next, mean_next, rstd_next, scale_next);
-        const int64_t row_more = row + (S - 1) * step;  // takes the last row's stage
-        const bool more = t == 0 && row != blockIdx.x && row_more < p.rows && (!p.mask || p.mask[row_more]);
+        const int64_t row_more = row + (S - 1) * step;  // takes the last row's stage (the only stage: the next row takes it)
+        const bool more = t == 0 && S > 1 && row != first && row_more < p.rows && (!p.mask || p.mask[row_more]);
 
-        const char *stage = smem + s * stage_bytes;
+        const char *stage = stages + s * n.stage_bytes, *sh = stage, *sdy = stage + n.at_dy, *sds = stage + n.at_ds, *ssc = stage + n.at_scales;
+        if (MODE == kAnyRow) {
+            sh += row_shift<MODE>(h_row(row)), sdy += row_shift<MODE>(dy_row(row)), sds += row_shift<MODE>(ds_row(row));
+            if (kAct8) ssc += row_shift<MODE>(scale_row(row));
+        }
+        const auto get_h = [&](int i) -> V8 {
+            if constexpr (MODE != kAnyRow) return read_h<SRC>(sh, at.vec(i), scale[kScales > 1 ? i : 0]);
+            if constexpr (!kAct8) return at.template read<SRC == kHBf16>(sh, i);
+            return at.singles(i, [&](int c) { return act8_value((uint8_t)sh[c], (uint8_t)ssc[c / kAct8Block], SRC == kHE4M3); });
+        };
         float c1 = 0.f, c2 = 0.f;
         const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
         if (on) {
-            if (!dead && !ptx::mbar_wait(ptx::smem_u32(&s_full[s]), (phases >> s) & 1u, kNormWaitNs)) {
+            if (!dead && !ptx::mbar_wait(full0 + s * 8, (phases >> s) & 1u, kNormWaitNs)) {
                 dead = true;
                 if (p.status) raise_status(p.status, RL_ERR_TIMEOUT);
             }
@@ -162,11 +226,10 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(NormBackwardPar
             f32x2 s0 = 0ull, s1 = 0ull;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                if (i == VPT - 1 && !has_last) continue;
-                const int vec = t + i * T;
-                V8 h = read_h<SRC>(stage, vec, scale[SRC == kHAct8 ? i : 0], p.ckpt.e4m3), g = read_vec<DYBF16>(stage + off_dy, vec);
-                if (i == VPT - 1 && cut) h = clipped(h, vec * kVec, p.cols), g = clipped(g, vec * kVec, p.cols);
-                const V8 ww = kWInRegs ? w[kWInRegs ? i : 0] : read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+                if (at.none(i)) continue;
+                V8 h = get_h(i), g = at.template read<DYBF16>(sdy, i);
+                if (MODE != kAnyRow && i == VPT - 1 && at.cut) h = clipped(h, at.vec(i) * kVec, p.cols), g = clipped(g, at.vec(i) * kVec, p.cols);
+                const V8 ww = weight(i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, ww.p[k]);
@@ -179,52 +242,47 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(NormBackwardPar
                 }
             }
             c1 = sum_of(s0), c2 = sum_of(s1);
-            block_sums<FULL>(c1, c2, s_sums[turn], T >> 5);
+            team_sums<FULL, MODE == kWarpRow>(c1, c2, s_sums[turn], T >> 5);
             turn ^= 1;
             if (t == 0 && p.status && !(fabsf(c1) < INFINITY && fabsf(c2) < INFINITY)) raise_status(p.status, RL_ERR_NONFINITE);
             c1 = FULL && !p.rms ? c1 * p.inv_cols : 0.f;
             c2 = c2 * p.inv_cols * rstd * rstd;
-        } else {
+        } else if (MODE != kWarpRow) {
             __syncthreads();
         }
+        if (MODE == kWarpRow) __syncwarp();
         if (more && !dead) copy_row(row_more, last);
         const f32x2 o1 = pack2(-c1, -c1), nk = pack2(-c2, -c2);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if (i == VPT - 1 && !has_last) continue;
-            const int vec = t + i * T, col = vec * kVec;
-            float o[kVec] = {};
+            if (at.none(i)) continue;
+            V8 r = zeros();
             if (on) {
-                const V8 h = read_h<SRC>(stage, vec, scale[SRC == kHAct8 ? i : 0], p.ckpt.e4m3), g = read_vec<DYBF16>(stage + off_dy, vec);
-                const V8 ww = kWInRegs ? w[kWInRegs ? i : 0] : read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
-                V8 r;
+                const V8 h = get_h(i), g = at.template read<DYBF16>(sdy, i), ww = weight(i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 rr = mul2(g.p[k], rs), u = FULL ? fma2(rr, ww.p[k], o1) : mul2(rr, ww.p[k]);
                     r.p[k] = fma2(FULL ? add2(h.p[k], nm) : h.p[k], nk, u);
                 }
-                if (ring.ds_bytes) {
-                    const V8 d = read_vec<XBF16>(stage + off_ds, vec);
+                if (p.dsummed.p) {
+                    const V8 d = x_bf16 ? at.template read<true>(sds, i) : at.template read<false>(sds, i);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) r.p[k] = add2(r.p[k], d.p[k]);
                 }
                 if (p.y.p) {
-                    float b[kVec] = {};
-                    if (p.b) load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, b);
-                    V8 u = pairs_of(b);
+                    V8 u = at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) u.p[k] = fma2(mul2(add2(h.p[k], nm), rs), ww.p[k], u.p[k]);
-                    floats_of(u, o);
-                    store_row(p.y, row, col, p.cols, o);
+                    at.store(p.y, row, i, u);
                 }
-                floats_of(r, o);
             } else if (p.y.p) {
-                store_row(p.y, row, col, p.cols, o);
+                at.store(p.y, row, i, r);
             }
-            if (XBF16)
-                store_vec(static_cast<__nv_bfloat16 *>(p.dx.p) + row * p.dx.ld, col, p.cols, p.dx.fast, o);
-            else
-                store_vec(static_cast<float *>(p.dx.p) + row * p.dx.ld, col, p.cols, p.dx.fast, o);
+            at.store(p.dx, row, i, r);
+        }
+        if (MODE != kWarpRow && S == 1) {
+            __syncthreads();
+            if (t == 0 && row + step < p.rows && on_next && !dead) copy_row(row + step, 0);
         }
         on = on_next, mean = mean_next, rstd = rstd_next;
 #pragma unroll
@@ -232,44 +290,70 @@ __global__ void __launch_bounds__(512) norm_backward_ring_kernel(NormBackwardPar
         last = s;
         s = s + 1 == S ? 0 : s + 1;
     }
-    if (dead) {  // (copies in flight end before the block does, or do not within another wait)
-        if (t == 0)
-            for (int k = 0; k < S; ++k) ptx::mbar_wait(ptx::smem_u32(&s_full[k]), (phases >> k) & 1u, kNormWaitNs);
-        __syncthreads();
-    }
+    if (dead && t == 0)  // (copies in flight end before the block does, or do not within another wait)
+        for (int k = 0; k < S; ++k) ptx::mbar_wait(full0 + k * 8, (phases >> k) & 1u, kNormWaitNs);
     if (!p.want_dw && !p.want_db) return;
+
     float *part = p.partials + (int64_t)blockIdx.x * 2 * p.ld_part;
+    if (MODE != kWarpRow) {
+        const RowMat out{part, p.ld_part, 0, 1};
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        if (i == VPT - 1 && !has_last) continue;
-        float v[kVec];
-        floats_of(dw[i], v);
-        store_vec(part, (t + i * T) * kVec, (int)p.ld_part, true, v);
-        if (FULL) {
-            floats_of(db[i], v);
-            store_vec(part + p.ld_part, (t + i * T) * kVec, (int)p.ld_part, true, v);
+        for (int i = 0; i < VPT; ++i) {
+            if (at.none(i)) continue;
+            at.store(out, 0, i, dw[i]);
+            if (FULL) at.store(out, 1, i, db[i]);
         }
+        return;
+    }
+    // the warps' sums, over the rows' room
+    float *sums = reinterpret_cast<float *>(smem);
+    constexpr int kWidth = VPT * 32 * kVec;
+#pragma unroll
+    for (int which = 0; which < (FULL ? 2 : 1); ++which) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            float v[kVec];
+            floats_of(which ? db[FULL ? i : 0] : dw[i], v);
+            store_vec(sums + team * kWidth, at.vec(i) * kVec, kWidth, true, v);
+        }
+        __syncthreads();
+        join_teams(sums, kTeams, kWidth, p.cols, part + which * p.ld_part);
     }
 }
 
-template <int SRC, bool XBF16, bool DYBF16, int VPT, bool FULL>
-cudaError_t launch_norm_ring(const NormBackwardParams &p, const NormRing &r, int parts, cudaStream_t stream) {
-    auto kernel = norm_backward_ring_kernel<SRC, XBF16, DYBF16, VPT, FULL>;
+template <int SRC, bool DYBF16, int VPT, bool FULL, int MODE>
+cudaError_t launch_norm_ring(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream) {
+    auto kernel = norm_backward_ring_kernel<SRC, DYBF16, VPT, FULL, MODE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<parts, r.warps * 32, r.smem, stream>>>(p, r);
+    kernel<<<blocks, MODE == kWarpRow ? kNormWarps * 32 : n.warps * 32, n.smem, stream>>>(p, n);
     return cudaGetLastError();
 }
 
-template <int SRC, bool XBF16, bool DYBF16>
-cudaError_t launch_norm_ring_shape(const NormBackwardParams &p, const NormRing &r, int parts, cudaStream_t stream) {
-    const bool full = !p.rms || p.want_db;
-    switch (r.vecs) {
-        case 1: return full ? launch_norm_ring<SRC, XBF16, DYBF16, 1, true>(p, r, parts, stream) : launch_norm_ring<SRC, XBF16, DYBF16, 1, false>(p, r, parts, stream);
-        case 2: return full ? launch_norm_ring<SRC, XBF16, DYBF16, 2, true>(p, r, parts, stream) : launch_norm_ring<SRC, XBF16, DYBF16, 2, false>(p, r, parts, stream);
-        case 3: return full ? launch_norm_ring<SRC, XBF16, DYBF16, 3, true>(p, r, parts, stream) : launch_norm_ring<SRC, XBF16, DYBF16, 3, false>(p, r, parts, stream);
-        default: return full ? launch_norm_ring<SRC, XBF16, DYBF16, 4, true>(p, r, parts, stream) : launch_norm_ring<SRC, XBF16, DYBF16, 4, false>(p, r, parts, stream);
+template <int SRC, bool DYBF16>
+cudaError_t launch_norm_rows(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream) {
+#define RLK_RING(V, FULL, MODE) launch_norm_ring<SRC, DYBF16, V, FULL, MODE>(p, n, blocks, stream)
+    if (n.mode == kAnyRow || (SRC == kHBf16 && !DYBF16)) {
+        switch (n.vecs) {
+            case 1: return RLK_RING(1, true, kAnyRow);
+            case 2: return RLK_RING(2, true, kAnyRow);
+            case 3: return RLK_RING(3, true, kAnyRow);
+            default: return RLK_RING(4, true, kAnyRow);
+        }
     }
+    if constexpr (SRC != kHBf16 || DYBF16) {
+        const bool full = !p.rms || p.want_db;
+        if (n.mode == kWarpRow) return full ? RLK_RING(3, true, kWarpRow) : n.vecs == 3 ? RLK_RING(3, false, kWarpRow) : RLK_RING(4, false, kWarpRow);
+        switch (n.vecs) {
+            case 1: return full ? RLK_RING(1, true, kBlockRow) : RLK_RING(1, false, kBlockRow);
+            case 2: return full ? RLK_RING(2, true, kBlockRow) : RLK_RING(2, false, kBlockRow);
+            case 3: return full ? RLK_RING(3, true, kBlockRow) : RLK_RING(3, false, kBlockRow);
+            default: return full ? RLK_RING(4, true, kBlockRow) : RLK_RING(4, false, kBlockRow);
+        }
+    }
+#undef RLK_RING
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace rlk

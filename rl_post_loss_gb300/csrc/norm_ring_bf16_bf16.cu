@@ -1,0 +1,10 @@
+// The norms' backward pass from 16-bit rows and 16-bit dy (norm_ring.cuh); a file of its own, as files compile in parallel.
+#include "norm_ring.cuh"
+
+namespace rlk {
+
+cudaError_t launch_norm_rows_bf16_bf16(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream) {
+    return launch_norm_rows<kHBf16, true>(p, n, blocks, stream);
+}
+
+}  // namespace rlk
