@@ -97,6 +97,15 @@ __device__ __forceinline__ uint2 act8_encode(const float (&v)[kVec], uint32_t b,
     return make_uint2(w[0], w[1]);
 }
 
+__device__ __forceinline__ uint32_t act8_encode_one(float v, uint32_t b, bool e4m3) {
+    if (b == 255u) return 0u;
+    const float inv = __uint_as_float((254u - b) << 23);
+    if (!e4m3) return __float_as_uint(fmaf(v, inv, 12582912.f)) & 0xffu;
+    uint16_t c;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(v * inv));
+    return c & 0xffu;
+}
+
 // What eight codes stand for, as pairs. An int8 code plus 128 in the low byte of 2^23 is 2^23 + 128 + code, and
 // times s the difference is exact. An e4m3 code's 7 low bits, put where fp32 has its exponent and mantissa, are the
 // value times 2^-120 (subnormal codes included). Where products may pass fp32's range (a code can stand for a

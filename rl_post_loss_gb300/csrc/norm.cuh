@@ -27,7 +27,7 @@ struct NormForwardParams {
     int32_t params_bf16, params_fast;
     const uint8_t *mask;
     float *mean, *rstd;        // or nullptr
-    int32_t rows, cols, rms, lanes;
+    int32_t rows, cols, rms;
     float eps, inv_cols;
     uint32_t *status;
 };
@@ -49,15 +49,6 @@ struct NormBackwardParams {
     uint32_t *status;
 };
 
-// How a norm's rows are laid over threads.
-struct NormShape {
-    int lanes;    // threads of a row
-    int vecs;     // vectors of a thread
-    int threads;  // of a block
-    int groups;   // rows that a block works on at a time
-};
-NormShape norm_shape(int cols);
-
 // How the backward pass lays rows over blocks (norm_ring.cuh).
 constexpr int kNormDepth = 8;
 constexpr size_t kNormRingSmem = 225 * 1024;  // of a block, beside its barriers and sums
@@ -74,6 +65,7 @@ struct NormTeams {
 int norm_backward_parts(int rows, int cols);
 
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream);
+cudaError_t launch_norm_forward_any(const NormForwardParams &p, const struct NormTeams &n, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream);
 // The backward pass's kernels by the types of h and dy.
 #define RLK_NORM_ROWS(H, DY) cudaError_t launch_norm_rows_##H##_##DY(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream)

@@ -17,24 +17,6 @@ constexpr int kJoinCols = 32, kJoinRows = 8;
 // Rows on 16-byte boundaries that fit `lanes` threads of a warp (4 to 32) with VPT vectors each, so that a warp
 // works on several rows and a row's sums take few steps; rows are held in registers from one load to the store.
 
-template <bool BF16>
-struct RawMat {
-    using type = Raw16;
-};
-template <>
-struct RawMat<false> {
-    using type = Raw32;
-};
-template <bool BF16>
-__device__ __forceinline__ void load_mat(typename RawMat<BF16>::type &r, const RowMat &m, int64_t row, int col, int cols) {
-    if constexpr (BF16)
-        load_raw(r, static_cast<const __nv_bfloat16 *>(m.p) + row * m.ld, col, cols, true);
-    else
-        load_raw(r, static_cast<const float *>(m.p) + row * m.ld, col, cols, true);
-}
-__device__ __forceinline__ V8 pairs(const Raw16 &r) { return bf16_pairs(r.a); }
-__device__ __forceinline__ V8 pairs(const Raw32 &r) { return f32_pairs(r.a, r.b); }
-
 template <int SRC, bool XBF16, bool DYBF16, int VPT, bool FULL>
 __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBackwardParams p, int lanes) {
     extern __shared__ __align__(16) float smem_short[];
@@ -250,12 +232,13 @@ NormTeams teams_of(const NormBackwardParams &p, int mode) {
     double best = 0;
     for (int v = 1; v <= 4; ++v) {
         const int warps = (vecs + 32 * v - 1) / (32 * v);
+        if ((v - 1) * warps * 32 >= vecs) continue;  // fewer vectors a thread do
         if (warps > kNormWarps || (v >= (mode == kAnyRow ? 3 : 4) && full && n.warps)) continue;
         const bool regs = mode == kAnyRow ? v == 1 : v <= 3 || !full;
         size_t w_bytes = regs ? 0 : (size_t)v * warps * 32 * kVec * 4;
         int blocks = kNormWarps / warps;
         while (blocks > 1 && blocks * (kBlockExtra + w_bytes + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
-        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + 2);
+        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (v == 4 ? 3.5 : 2));
         if (n.warps && time >= best) continue;
         best = time;
         const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks - kBlockExtra);
@@ -294,7 +277,7 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t strea
     } else {
         const bool any = !fast || (!act8 && p.x.bf16 && !p.dy.bf16);
         // a warp per row where there are rows for all warps
-        const bool warp = !any && p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps;
+        const bool warp = !any && p.cols > 512 && p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps;
         const NormTeams n = teams_of(p, any ? kAnyRow : warp ? kWarpRow : kBlockRow);
         blocks = std::min(p.rows, kNormSMs * n.blocks_per_sm);
 #define RLK_ROWS(H) (p.dy.bf16 ? launch_norm_rows_##H##_bf16(p, n, blocks, stream) : launch_norm_rows_##H##_f32(p, n, blocks, stream))

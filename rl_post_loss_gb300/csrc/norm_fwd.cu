@@ -1,233 +1,200 @@
-// The forward pass of the norms (mathematics and layout: norm.cuh).
-#include "norm.cuh"
+// The forward pass of the norms: rows on 16-byte boundaries (norm_fwd.cuh), short ones among them, and which kernel takes a call.
+#include "norm_fwd.cuh"
 
 namespace rlk {
 
 namespace {
 
-// Sums over the threads of a row. Inside a warp a butterfly, so that every lane has the same bits; over a
-// block's warps one exchange through shared memory (two buffers in turn: a thread may still read the last
-// one while another writes the next), added in the order of the warps.
-template <int LANES>
-struct RowSum {
-    float (*buf)[2][16];
-    int turn;
-    __device__ __forceinline__ RowSum(float (*b)[2][16]) : buf(b), turn(0) {}
-
-    template <int N>
-    __device__ __forceinline__ void run(float (&v)[N]) {
-        static_assert(N <= 2, "two sums at most");
-#pragma unroll
-        for (int off = (LANES < 32 ? LANES : 32) / 2; off > 0; off >>= 1)
-#pragma unroll
-            for (int n = 0; n < N; ++n) v[n] = __fadd_rn(v[n], __shfl_xor_sync(0xffffffffu, v[n], off));
-        if (LANES <= 32) return;
-        const int warps = blockDim.x >> 5;
-        if ((threadIdx.x & 31) == 0)
-#pragma unroll
-            for (int n = 0; n < N; ++n) buf[turn][n][threadIdx.x >> 5] = v[n];
-        __syncthreads();
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-            float s = buf[turn][n][0];
-            for (int w = 1; w < warps; ++w) s = __fadd_rn(s, buf[turn][n][w]);
-            v[n] = s;
-        }
-        turn ^= 1;
-    }
-};
-
-template <typename T>
-struct RawOf;
-template <>
-struct RawOf<__nv_bfloat16> { using type = Raw16; };
-template <>
-struct RawOf<float> { using type = Raw32; };
-
-// One row at a time per group of threads, held in registers between the statistics and the output. The
-// variance is a second sum over the registers, of squares of differences from the mean, together with the
-// sum of these differences: what rounding left of the mean is taken off both.
-template <typename T, int VPT, int LANES>
-__global__ void __launch_bounds__(512) norm_forward_kernel(NormForwardParams p) {
-    using Raw = typename RawOf<T>::type;
-    __shared__ float s_buf[2][2][16];
-    RowSum<LANES> sums(s_buf);
-    const int lanes = p.lanes, groups = blockDim.x / lanes, group = threadIdx.x / lanes, t = threadIdx.x - group * lanes;
-    for (int64_t r0 = (int64_t)blockIdx.x * groups; r0 < p.rows; r0 += (int64_t)gridDim.x * groups) {
-        const int64_t row = r0 + group;
-        const bool mine = row < p.rows;
-        const bool on = mine && (!p.mask || p.mask[row]);
-        float v[VPT][kVec];
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int col = (t + i * lanes) * kVec;
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) v[i][j] = 0.f;
-            if (on && col < p.cols) {
-                Raw r;
-                load_raw(r, static_cast<const T *>(p.x.p) + row * p.x.ld, col, p.cols, p.x.fast);
-                to_float(r, v[i]);
-            }
-        }
-        if (p.residual.p) {
+// ---------------------------------------------------------------- short rows
+//
+// Rows on 16-byte boundaries of up to 512 columns: `lanes` threads of a warp (4 to 32) with VPT vectors each, so that
+// a warp works on several rows and a row's sums take few steps. The loads of a row go out together.
+template <bool BF16, int VPT>
+__global__ void __launch_bounds__(256, 4) norm_forward_short_kernel(NormForwardParams p, int lanes) {
+    using Raw = typename RawMat<BF16>::type;
+    const int lane = threadIdx.x & 31, t = lane & (lanes - 1), per_warp = 32 / lanes;
+    const int64_t warp = blockIdx.x + (int64_t)(threadIdx.x >> 5) * gridDim.x, step = (int64_t)gridDim.x * (blockDim.x >> 5) * per_warp;
+    for (int64_t base = warp * per_warp; base < p.rows; base += step) {
+        const int64_t row = base + lane / lanes;
+        const bool mine = row < p.rows, on = mine && (!p.mask || p.mask[row]);
+        Raw x[VPT], r[VPT];
+        V8 v[VPT];
+        if (on) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int col = (t + i * lanes) * kVec;
-                if (on && col < p.cols) {
-                    Raw r;
-                    float u[kVec];
-                    load_raw(r, static_cast<const T *>(p.residual.p) + row * p.residual.ld, col, p.cols, p.residual.fast);
-                    to_float(r, u);
-#pragma unroll
-                    for (int j = 0; j < kVec; ++j) {
-                        v[i][j] += u[j];
-                        if (sizeof(T) == 2) v[i][j] = __bfloat162float(__float2bfloat16_rn(v[i][j]));
-                    }
+                if (col < p.cols) {
+                    load_mat<BF16>(x[i], p.x, row, col, p.cols);
+                    if (p.residual.p) load_mat<BF16>(r[i], p.residual, row, col, p.cols);
                 }
             }
         }
+        f32x2 s0 = 0ull, s1 = 0ull;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) clip_row(v[i], (t + i * lanes) * kVec, p.cols);
-        if (mine && p.h.p)
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int col = (t + i * lanes) * kVec;
-                if (col < p.cols) store_vec(static_cast<T *>(p.h.p) + row * p.h.ld, col, p.cols, p.h.fast, v[i]);
+        for (int i = 0; i < VPT; ++i) {
+            const int vec = t + i * lanes, col = vec * kVec;
+            v[i] = zeros();
+            if (on && col < p.cols) {
+                v[i] = pairs(x[i]);
+                if (p.residual.p) v[i] = add_residual<BF16>(v[i], pairs(r[i]));
+                if (col + kVec > p.cols) v[i] = clipped(v[i], col, p.cols);
             }
-        if (p.ckpt.codes) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int vec = t + i * lanes, col = vec * kVec;
-                const uint32_t b = act8_scale(act8_block_max(act8_amax(v[i])), p.ckpt.e4m3);
+            if (mine && col < p.cols && p.h.p) {
+                float f[kVec];
+                floats_of(v[i], f);
+                store_row(p.h, row, col, p.cols, f);
+            }
+            if (p.ckpt.codes) {
+                float f[kVec];
+                floats_of(v[i], f);
+                const uint32_t b = act8_scale(act8_block_max(act8_amax(f)), p.ckpt.e4m3);
                 if (mine && col < p.cols) {
-                    store_codes(p.ckpt.codes + row * p.ckpt.ld_codes, col, p.cols, p.ckpt.fast, act8_encode(v[i], b, p.ckpt.e4m3));
+                    store_codes(p.ckpt.codes + row * p.ckpt.ld_codes, col, p.cols, p.ckpt.fast, act8_encode(f, b, p.ckpt.e4m3));
                     if ((vec & 3) == 0) p.ckpt.scales[row * p.ckpt.ld_scales + (vec >> 2)] = (uint8_t)b;
                 }
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (p.rms)
+                    s1 = fma2(v[i].p[k], v[i].p[k], s1);
+                else
+                    s0 = add2(s0, v[i].p[k]);
+            }
         }
-
-        float mean = 0.f, var;
+        float b = sum_of(p.rms ? s1 : s0), mean = 0.f, var;
+        for (int off = lanes >> 1; off > 0; off >>= 1) b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, off));
         if (p.rms) {
-            float s[1] = {0.f};
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) s[0] = fmaf(v[i][j], v[i][j], s[0]);
-            sums.run(s);
-            var = s[0] * p.inv_cols;
+            var = b * p.inv_cols;
         } else {
-            float s[1] = {0.f};
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) s[0] += v[i][j];
-            sums.run(s);
-            mean = s[0] * p.inv_cols;
-            float d[2] = {0.f, 0.f};
+            mean = b * p.inv_cols;
+            const f32x2 nm = pack2(-mean, -mean);
+            s0 = s1 = 0ull;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int col = (t + i * lanes) * kVec;
+                if (col >= p.cols) continue;
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) v[i][j] -= mean;
-                if (col + kVec > p.cols) clip_row(v[i], col, p.cols);
+                for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nm);
+                if (col + kVec > p.cols) v[i] = clipped(v[i], col, p.cols);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    d[0] += v[i][j];
-                    d[1] = fmaf(v[i][j], v[i][j], d[1]);
+                for (int k = 0; k < 4; ++k) {
+                    s0 = add2(s0, v[i].p[k]);
+                    s1 = fma2(v[i].p[k], v[i].p[k], s1);
                 }
             }
-            sums.run(d);
-            const float rest = d[0] * p.inv_cols;
-            var = fmaxf(fmaf(-rest, rest, d[1] * p.inv_cols), 0.f) + (d[1] - d[1]);  // (NaN stays)
+            float a = sum_of(s0);
+            b = sum_of(s1);
+            for (int off = lanes >> 1; off > 0; off >>= 1) {
+                a = __fadd_rn(a, __shfl_xor_sync(0xffffffffu, a, off));
+                b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, off));
+            }
+            float rest;
+            var = variance(a, b, p.inv_cols, rest);
             mean += rest;
+            const f32x2 nr = pack2(-rest, -rest);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) v[i][j] -= rest;
+                for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nr);
         }
-        const float rstd = __frsqrt_rn(var + p.eps);
         if (!mine) continue;
-        if (t == 0) {
-            if (on && !(var < INFINITY) && p.status) raise_status(p.status, RL_ERR_NONFINITE);
-            if (p.mean) p.mean[row] = on ? mean : 0.f;
-            if (p.rstd) p.rstd[row] = on ? rstd : 0.f;
+        const float rstd = finish_stats(p, row, t == 0 && on, mean, var);
+        if (t == 0 && !on) {
+            if (p.mean) p.mean[row] = 0.f;
+            if (p.rstd) p.rstd[row] = 0.f;
         }
+        const f32x2 rs = pack2(rstd, rstd);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int col = (t + i * lanes) * kVec;
             if (col >= p.cols) continue;
-            float w[kVec];
+            float f[kVec] = {};
+            if (on) {
+                float u[kVec];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) v[i][j] *= rstd;
-            if (p.w) {
-                load_params(p.w, p.params_bf16, p.params_fast, col, p.cols, w);
+                for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], rs);
+                if (p.w) {
+                    load_params(p.w, p.params_bf16, p.params_fast, col, p.cols, u);
+                    const V8 w = pairs_of(u);
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) v[i][j] *= w[j];
+                    for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], w.p[k]);
+                }
+                if (p.b) {
+                    load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, u);
+                    const V8 c = pairs_of(u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], c.p[k]);
+                }
+                floats_of(v[i], f);
             }
-            if (p.b) {
-                load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, w);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) v[i][j] += w[j];
-            }
-            if (!on)
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) v[i][j] = 0.f;
-            store_row(p.y, row, col, p.cols, v[i]);
+            store_row(p.y, row, col, p.cols, f);
         }
     }
 }
 
-template <typename T, int VPT, int LANES>
-cudaError_t launch(const NormForwardParams &p, const NormShape &s, cudaStream_t stream) {
-    const int64_t blocks = ((int64_t)p.rows + s.groups - 1) / s.groups;
-    const int most = kNormSMs * (2048 / s.threads);
-    norm_forward_kernel<T, VPT, LANES><<<(int)(blocks < most ? blocks : most), s.threads, 0, stream>>>(p);
+constexpr int kShortCols = 512;
+constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 1024;  // what a block takes beside its rows
+
+template <bool BF16>
+cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
+    constexpr int kVecs = 2;
+    int lanes = 4;
+    while (lanes * kVecs * kVec < p.cols) lanes *= 2;
+    const int64_t blocks = ((int64_t)p.rows * lanes + 255) / 256;
+    norm_forward_short_kernel<BF16, kVecs><<<(int)std::min<int64_t>(blocks, kNormSMs * 4), 256, 0, stream>>>(p, lanes);
     return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t launch_shape(const NormForwardParams &p, const NormShape &s, cudaStream_t stream) {
-    switch (s.lanes) {
-        case 8: return launch<T, 1, 8>(p, s, stream);
-        case 16: return launch<T, 1, 16>(p, s, stream);
-        case 32: return launch<T, 1, 32>(p, s, stream);
+// A block per row, 24 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by
+// a row's time of its vectors and two more for each exchange of sums.
+NormTeams teams_of(const NormForwardParams &p, int mode) {
+    const int vecs = (p.cols + kVec - 1) / kVec, pad = mode == kAnyRow ? 16 : 0;
+    NormTeams n{};
+    n.mode = mode;
+    n.at_dy = (p.cols * (p.x.bf16 ? 2 : 4) + 15) / 16 * 16 + pad;
+    n.stage_bytes = n.at_dy * (p.residual.p ? 2 : 1);
+    if (mode == kWarpRow) {
+        n.warps = 1;
+        n.vecs = vecs > 96 ? 4 : 3;
+        n.blocks_per_sm = 2;
+        n.depth = (int)std::min<size_t>(kNormDepth, (kSmemOfSM / 2 - kBlockExtra) / (forward_threads(mode) / 32 * n.stage_bytes));
+        n.smem = (size_t)(forward_threads(mode) / 32) * n.depth * n.stage_bytes;
+        return n;
     }
-    switch (s.vecs) {
-        case 1: return launch<T, 1, 64>(p, s, stream);
-        case 2: return launch<T, 2, 64>(p, s, stream);
-        case 3: return launch<T, 3, 64>(p, s, stream);
-        default: return launch<T, 4, 64>(p, s, stream);
+    double best = 0;
+    for (const int v : {1, 2, 3, 4, 6}) {
+        if (mode == kAnyRow && v > 4) break;
+        const int warps = (vecs + 32 * v - 1) / (32 * v);
+        if (warps > forward_threads(mode) / 32 || (v - 1) * warps * 32 >= vecs) continue;
+        if (mode == kAnyRow && v > 2 && n.warps) continue;  // (single columns take more registers)
+        int blocks = forward_warps(mode) / warps;
+        while (blocks > 1 && blocks * (kBlockExtra + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
+        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : 4));
+        if (n.warps && time >= best) continue;
+        best = time;
+        n.warps = warps, n.vecs = v, n.blocks_per_sm = blocks;
+        n.depth = (int)std::min<size_t>(kNormDepth, std::min(kNormRingSmem, kSmemOfSM / blocks - kBlockExtra) / n.stage_bytes);
+        n.smem = (size_t)n.depth * n.stage_bytes;
     }
+    return n;
 }
 
 }  // namespace
 
-// Rows of up to 256 columns: 8, 16 or 32 lanes, a vector each. Longer rows: the fewest warps that hold them in
-// three vectors a thread, in four beyond 12288 columns (16 warps at most).
-NormShape norm_shape(int cols) {
-    const int vecs = (cols + kVec - 1) / kVec;
-    NormShape s;
-    if (vecs <= 32) {
-        s.lanes = vecs <= 8 ? 8 : vecs <= 16 ? 16 : 32;
-        s.vecs = 1;
-        s.threads = 128;
-        s.groups = s.threads / s.lanes;
-        return s;
+cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream) {
+    const bool fast = p.x.fast && (!p.residual.p || p.residual.fast);
+    if (fast && p.cols <= kShortCols) return p.x.bf16 ? launch_short<true>(p, stream) : launch_short<false>(p, stream);
+    if (!fast) {
+        const NormTeams n = teams_of(p, kAnyRow);
+        return launch_norm_forward_any(p, n, stream);
     }
-    int warps = (vecs + 95) / 96;
-    if (warps > 16) warps = 16;
-    if (warps < 2) warps = 2;
-    s.lanes = s.threads = warps * 32;
-    s.vecs = (vecs + s.lanes - 1) / s.lanes;
-    s.groups = 1;
-    return s;
-}
-
-cudaError_t launch_norm_forward(const NormForwardParams &q, cudaStream_t stream) {
-    NormForwardParams p = q;
-    const NormShape s = norm_shape(p.cols);
-    p.lanes = s.lanes;
-    return p.x.bf16 ? launch_shape<__nv_bfloat16>(p, s, stream) : launch_shape<float>(p, s, stream);
+    if (p.cols <= 1024 && p.rows >= kNormSMs * forward_warps(kWarpRow)) {
+        const NormTeams n = teams_of(p, kWarpRow);
+        if (n.vecs == 3) return p.x.bf16 ? launch_forward_rows<true, 3, kWarpRow>(p, n, stream) : launch_forward_rows<false, 3, kWarpRow>(p, n, stream);
+        return p.x.bf16 ? launch_forward_rows<true, 4, kWarpRow>(p, n, stream) : launch_forward_rows<false, 4, kWarpRow>(p, n, stream);
+    }
+    const NormTeams n = teams_of(p, kBlockRow);
+    return p.x.bf16 ? launch_forward_vecs<true, kBlockRow>(p, n, stream) : launch_forward_vecs<false, kBlockRow>(p, n, stream);
 }
 
 }  // namespace rlk

@@ -1,0 +1,257 @@
+// The forward pass of the norms (mathematics: norm.cuh; how rows are held and brought: norm_rows.cuh).
+//
+// A row is read from shared memory once and held in registers between the statistics and the output; its
+// stage is filled again as soon as the first exchange of sums shows that every thread has read it. The
+// variance is a second sum over the registers, of squares of differences from the mean, together with the sum
+// of these differences: what rounding left of the mean is taken off both.
+#pragma once
+
+#include <algorithm>
+
+#include "norm_rows.cuh"
+
+namespace rlk {
+
+
+// Of a block and of an SM: 80 registers a thread, for single columns 128.
+constexpr int forward_threads(int mode) { return mode == kAnyRow ? 512 : 384; }
+constexpr int forward_warps(int mode) { return mode == kAnyRow ? 16 : 24; }
+
+// h's 8-bit codes. On 16-byte boundaries a block of 32 columns is four lanes' vectors; in rows that start anywhere
+// it is what the warp's lanes hold at one place.
+template <int MODE, int VPT>
+__device__ __forceinline__ void store_act8(const Columns<MODE, VPT> &at, const Act8Mat &a, int64_t row, int i, const V8 &h) {
+    float v[kVec];
+    floats_of(h, v);
+    if (MODE != kAnyRow) {
+        const int vec = at.vec(i), col = vec * kVec;
+        const uint32_t b = act8_scale(act8_block_max(act8_amax(v)), a.e4m3);
+        if (at.none(i)) return;
+        store_codes(a.codes + row * a.ld_codes, col, at.cols, a.fast, act8_encode(v, b, a.e4m3));
+        if ((vec & 3) == 0) a.scales[row * a.ld_scales + (vec >> 2)] = (uint8_t)b;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        const int col = at.col(i, j);
+        const uint32_t b = act8_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu), a.e4m3);
+        if (col >= at.cols) continue;
+        a.codes[row * a.ld_codes + col] = (uint8_t)act8_encode_one(v[j], b, a.e4m3);
+        if ((col & 31) == 0) a.scales[row * a.ld_scales + (col >> 5)] = (uint8_t)b;
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ V8 add_residual(V8 x, const V8 &r) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x.p[k] = add2(x.p[k], r.p[k]);
+        if (BF16) {  // h is what the type of x holds
+            float a, b;
+            unpack2(x.p[k], a, b);
+            const uint32_t w = pack_bf16x2(a, b);
+            x.p[k] = pack2(bf16_lo(w), bf16_hi(w));
+        }
+    }
+    return x;
+}
+
+// What follows from a row's sums: the statistics are written by one thread.
+__device__ __forceinline__ float finish_stats(const NormForwardParams &p, int64_t row, bool one, float mean, float var) {
+    const float rstd = __frsqrt_rn(var + p.eps);
+    if (one) {
+        if (!(var < INFINITY) && p.status) raise_status(p.status, RL_ERR_NONFINITE);
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+    return rstd;
+}
+__device__ __forceinline__ float variance(float sum, float squares, float inv_cols, float &rest) {
+    rest = sum * inv_cols;
+    const float var = fmaf(-rest, rest, squares * inv_cols);
+    return var < 0.f ? 0.f : var;  // (NaN stays)
+}
+
+template <bool BF16, int VPT, int MODE>
+__global__ void __launch_bounds__(forward_threads(MODE), MODE == kAnyRow ? 1 : 2) norm_forward_kernel(NormForwardParams p, NormTeams n) {
+    constexpr int kTeams = MODE == kWarpRow ? forward_threads(MODE) / 32 : 1;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(16) float2 s_sums[2][16];
+    __shared__ __align__(8) uint64_t s_full[kTeams * kNormDepth];
+    const int T = MODE == kWarpRow ? 32 : (int)blockDim.x, team = MODE == kWarpRow ? (int)threadIdx.x >> 5 : 0;
+    const int t = MODE == kWarpRow ? (int)threadIdx.x & 31 : (int)threadIdx.x, S = n.depth;
+    Columns<MODE, VPT> at(t, T, p.cols);
+    char *stages = smem + team * S * n.stage_bytes;
+    if (threadIdx.x < 32) (&s_sums[0][0])[threadIdx.x] = make_float2(0.f, 0.f);
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kTeams * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    const uint32_t full0 = ptx::smem_u32(&s_full[team * S]);
+    const int64_t first = blockIdx.x + (int64_t)team * gridDim.x, step = (int64_t)kTeams * gridDim.x;
+    const auto x_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.x.p) + row * p.x.ld * (BF16 ? 2 : 4); };
+    const auto r_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.residual.p) + row * p.residual.ld * (BF16 ? 2 : 4); };
+    const auto copy_row = [&](int64_t row, int s) {  // by the team's thread 0
+        const uint32_t full = full0 + s * 8, to = ptx::smem_u32(stages + s * n.stage_bytes);
+        if (MODE != kAnyRow) {
+            ptx::mbar_arrive_expect_tx(full, (uint32_t)n.stage_bytes);
+            ptx::bulk_g2s(to, x_row(row), (uint32_t)n.at_dy, full);
+            if (p.residual.p) ptx::bulk_g2s(to + n.at_dy, r_row(row), (uint32_t)n.at_dy, full);
+            return;
+        }
+        const int bytes = p.cols * (BF16 ? 2 : 4);
+        const uint32_t bx = window(x_row(row), bytes), br = p.residual.p ? window(r_row(row), bytes) : 0u;
+        ptx::mbar_arrive_expect_tx(full, bx + br);
+        ptx::bulk_g2s(to, x_row(row) - row_shift<MODE>(x_row(row)), bx, full);
+        if (br) ptx::bulk_g2s(to + n.at_dy, r_row(row) - row_shift<MODE>(r_row(row)), br, full);
+    };
+    if (t == 0)
+        for (int s = 0; s < S; ++s) {
+            const int64_t row = first + s * step;
+            if (row < p.rows && (!p.mask || p.mask[row])) copy_row(row, s);
+        }
+
+    uint32_t phases = 0;  // of the stages' barriers
+    bool dead = false, on = first < p.rows && (!p.mask || p.mask[first]);
+    int s = 0, turn = 0;
+    for (int64_t row = first; row < p.rows; row += step) {
+        at.next_row();
+        const bool on_next = !p.mask || row + step >= p.rows || p.mask[row + step];
+        const int64_t row_more = row + S * step;  // takes this row's stage
+        const bool more = t == 0 && row_more < p.rows && (!p.mask || p.mask[row_more]);
+        V8 v[VPT];
+        if (on) {
+            if (!dead && !ptx::mbar_wait(full0 + s * 8, (phases >> s) & 1u, kNormWaitNs)) {
+                dead = true;
+                if (p.status) raise_status(p.status, RL_ERR_TIMEOUT);
+            }
+            phases ^= 1u << s;
+            const char *sx = stages + s * n.stage_bytes, *sr = sx + n.at_dy;
+            if (MODE == kAnyRow) sx += row_shift<MODE>(x_row(row)), sr += row_shift<MODE>(r_row(row));
+            f32x2 s0 = 0ull, s1 = 0ull;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                v[i] = zeros();
+                if (at.none(i)) continue;
+                v[i] = at.template read<BF16>(sx, i);
+                if (p.residual.p) v[i] = add_residual<BF16>(v[i], at.template read<BF16>(sr, i));
+                if (MODE != kAnyRow && i == VPT - 1 && at.cut) v[i] = clipped(v[i], at.vec(i) * kVec, p.cols);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (p.rms)
+                        s1 = fma2(v[i].p[k], v[i].p[k], s1);
+                    else
+                        s0 = add2(s0, v[i].p[k]);
+                }
+            }
+            float a = 0.f, b = sum_of(p.rms ? s1 : s0), mean = 0.f, var;
+            team_sums<false, MODE == kWarpRow>(a, b, s_sums[turn], T >> 5);
+            turn ^= 1;
+            if (MODE == kWarpRow) __syncwarp();
+            if (more && !dead) copy_row(row_more, s);
+            if (p.h.p)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (!at.none(i)) at.store(p.h, row, i, v[i]);
+            if (p.ckpt.codes)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) store_act8(at, p.ckpt, row, i, v[i]);
+            if (p.rms) {
+                var = b * p.inv_cols;
+            } else {
+                mean = b * p.inv_cols;
+                const f32x2 nm = pack2(-mean, -mean);
+                s0 = s1 = 0ull;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    if (at.none(i)) continue;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nm);
+                    if (i == VPT - 1 && at.cut) v[i] = at.cut_off(v[i], i);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        s0 = add2(s0, v[i].p[k]);
+                        s1 = fma2(v[i].p[k], v[i].p[k], s1);
+                    }
+                }
+                a = sum_of(s0), b = sum_of(s1);
+                team_sums<true, MODE == kWarpRow>(a, b, s_sums[turn], T >> 5);
+                turn ^= 1;
+                float rest;
+                var = variance(a, b, p.inv_cols, rest);
+                mean += rest;
+                const f32x2 nr = pack2(-rest, -rest);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nr);
+            }
+            const float rstd = finish_stats(p, row, t == 0, mean, var);
+            const f32x2 rs = pack2(rstd, rstd);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (at.none(i)) continue;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], rs);
+                if (p.w) {
+                    const V8 w = at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
+                    if (p.b) {
+                        const V8 c = at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[i].p[k] = fma2(v[i].p[k], w.p[k], c.p[k]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], w.p[k]);
+                    }
+                } else if (p.b) {
+                    const V8 c = at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], c.p[k]);
+                }
+                at.store(p.y, row, i, v[i]);
+            }
+        } else {
+            if (more && !dead) copy_row(row_more, s);
+            if (t == 0) {
+                if (p.mean) p.mean[row] = 0.f;
+                if (p.rstd) p.rstd[row] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (!at.none(i)) {
+                    at.store(p.y, row, i, zeros());
+                    if (p.h.p) at.store(p.h, row, i, zeros());
+                }
+                if (p.ckpt.codes) store_act8(at, p.ckpt, row, i, zeros());
+            }
+        }
+        on = on_next;
+        s = s + 1 == S ? 0 : s + 1;
+    }
+    if (dead && t == 0)  // (copies in flight end before the block does, or do not within another wait)
+        for (int k = 0; k < S; ++k) ptx::mbar_wait(full0 + k * 8, (phases >> k) & 1u, kNormWaitNs);
+}
+
+template <bool BF16, int VPT, int MODE>
+cudaError_t launch_forward_rows(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
+    auto kernel = norm_forward_kernel<BF16, VPT, MODE>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<std::min(p.rows, kNormSMs * n.blocks_per_sm), MODE == kWarpRow ? forward_threads(MODE) : n.warps * 32, n.smem, stream>>>(p, n);
+    return cudaGetLastError();
+}
+
+template <bool BF16, int MODE>
+cudaError_t launch_forward_vecs(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
+    switch (n.vecs) {
+        case 1: return launch_forward_rows<BF16, 1, MODE>(p, n, stream);
+        case 2: return launch_forward_rows<BF16, 2, MODE>(p, n, stream);
+        case 3: return launch_forward_rows<BF16, 3, MODE>(p, n, stream);
+        case 4: return launch_forward_rows<BF16, 4, MODE>(p, n, stream);
+    }
+    if constexpr (MODE != kAnyRow) return launch_forward_rows<BF16, 6, MODE>(p, n, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace rlk

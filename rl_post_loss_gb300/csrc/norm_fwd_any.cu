@@ -1,0 +1,10 @@
+// The forward pass of the norms on rows that start anywhere (norm_fwd.cuh); a file of its own, as files compile in parallel.
+#include "norm_fwd.cuh"
+
+namespace rlk {
+
+cudaError_t launch_norm_forward_any(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
+    return p.x.bf16 ? launch_forward_vecs<true, kAnyRow>(p, n, stream) : launch_forward_vecs<false, kAnyRow>(p, n, stream);
+}
+
+}  // namespace rlk

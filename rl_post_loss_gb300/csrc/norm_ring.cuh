@@ -7,100 +7,22 @@
 //
 // A team is a block (kBlockRow: two or more on an SM cover each other's exchanges) or, for rows of 1024
 // columns and less, one warp of a block of 16 (kWarpRow: no barriers, and one partial sum for 16 rows at a
-// time). Its threads hold vectors of eight columns, which needs rows on 16-byte boundaries. Rows that start
-// anywhere (kAnyRow) are copied from the 16-byte boundary before them, and column c belongs to thread c mod
-// the team's threads: single loads and stores of a warp then lie side by side.
+// time); norm_rows.cuh has the third mode, rows that start anywhere.
 //
 // FULL = false is the RMS form without db, in which mean = 0 and sum(u) is not needed.
 #pragma once
 
-#include "norm.cuh"
-#include "ptx.cuh"
+#include "norm_rows.cuh"
 
 namespace rlk {
 
 enum HSource { kHBf16, kHF32, kHInt8, kHE4M3 };
 constexpr bool from_act8(int src) { return src >= kHInt8; }
-enum RowMode { kBlockRow, kWarpRow, kAnyRow };
-
-constexpr uint64_t kNormWaitNs = 1000000000ull;
-
-template <bool BF16>
-__device__ __forceinline__ V8 read_vec(const char *row, int vec) {
-    if (BF16) return bf16_pairs(*reinterpret_cast<const uint4 *>(row + vec * 16));
-    const uint4 *q = reinterpret_cast<const uint4 *>(row + vec * 32);
-    return f32_pairs(q[0], q[1]);
-}
-template <bool BF16>
-__device__ __forceinline__ float read_one(const char *row, int col) {
-    if (BF16) return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(row + col * 2) << 16);
-    return *reinterpret_cast<const float *>(row + col * 4);
-}
 template <int SRC>
 __device__ __forceinline__ V8 read_h(const char *row, int vec, uint32_t scale) {
     if (!from_act8(SRC)) return read_vec<SRC == kHBf16>(row, vec);
     return act8_decode_norm<SRC == kHE4M3>(*reinterpret_cast<const uint2 *>(row + vec * 8), scale);
 }
-__device__ __forceinline__ void store_one(const RowMat &m, int64_t at, float v) {
-    if (m.bf16)
-        static_cast<__nv_bfloat16 *>(m.p)[at] = __float2bfloat16_rn(v);
-    else
-        static_cast<float *>(m.p)[at] = v;
-}
-
-// A thread's i-th eight columns. Only the last ones may be cut off by the row's end, or not there at all.
-template <int MODE, int VPT>
-struct Columns {
-    int t, T, cols;
-    bool has_last, cut;
-    __device__ __forceinline__ Columns(int t, int T, int cols) : t(t), T(T), cols(cols) {
-        const int vec = t + (VPT - 1) * T;
-        has_last = MODE == kAnyRow || vec * kVec < cols;
-        cut = MODE == kAnyRow || (vec + 1) * kVec > cols;
-    }
-    __device__ __forceinline__ bool none(int i) const { return i == VPT - 1 && !has_last; }
-    __device__ __forceinline__ int vec(int i) const { return t + i * T; }
-    __device__ __forceinline__ int col(int i, int j) const { return MODE == kAnyRow ? t + (i * kVec + j) * T : vec(i) * kVec + j; }
-    // eight single values, 0 past the row's end
-    template <typename Get>
-    __device__ __forceinline__ V8 singles(int i, Get get) const {
-        V8 r;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int a = col(i, 2 * k), b = col(i, 2 * k + 1);
-            r.p[k] = pack2(i < VPT - 1 || a < cols ? get(a) : 0.f, i < VPT - 1 || b < cols ? get(b) : 0.f);
-        }
-        return r;
-    }
-    template <bool BF16>
-    __device__ __forceinline__ V8 read(const char *row, int i) const {
-        if (MODE == kAnyRow) return singles(i, [&](int c) { return read_one<BF16>(row, c); });
-        return read_vec<BF16>(row, vec(i));
-    }
-    __device__ __forceinline__ V8 params(const void *p, int bf16, int fast, int i, float missing) const {
-        if (!p) return singles(i, [&](int) { return missing; });
-        if (MODE == kAnyRow) return singles(i, [&](int c) { return load_param(p, bf16, c); });
-        float v[kVec];
-        load_params(p, bf16, fast, vec(i) * kVec, cols, v);
-        return pairs_of(v);
-    }
-    __device__ __forceinline__ void store(const RowMat &m, int64_t row, int i, const V8 &a) const {
-        float v[kVec];
-        floats_of(a, v);
-        if (MODE != kAnyRow) {
-            store_row(m, row, vec(i) * kVec, cols, v);
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (i < VPT - 1 || col(i, j) < cols) store_one(m, row * m.ld + col(i, j), v[j]);
-    }
-};
-
-// The bytes that a row's copy starts before the row.
-template <int MODE>
-__device__ __forceinline__ int row_shift(const char *row) { return MODE == kAnyRow ? (int)(reinterpret_cast<uintptr_t>(row) & 15u) : 0; }
-
 template <int SRC, bool DYBF16, int VPT, bool FULL, int MODE>
 __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(NormBackwardParams p, NormTeams n) {
     constexpr bool kAct8 = from_act8(SRC), kWInRegs = MODE == kAnyRow ? VPT == 1 : VPT <= 3 || !FULL;  // (else no room is left)
@@ -110,7 +32,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     __shared__ __align__(8) uint64_t s_full[kTeams * kNormDepth];
     const int T = MODE == kWarpRow ? 32 : (int)blockDim.x, team = MODE == kWarpRow ? (int)threadIdx.x >> 5 : 0;
     const int t = MODE == kWarpRow ? (int)threadIdx.x & 31 : (int)threadIdx.x, S = n.depth;
-    const Columns<MODE, VPT> at(t, T, p.cols);
+    Columns<MODE, VPT> at(t, T, p.cols);
     const bool x_bf16 = kAct8 ? p.dx.bf16 : SRC == kHBf16;
     char *stages = smem + team * S * n.stage_bytes;
     if (threadIdx.x < 32) (&s_sums[0][0])[threadIdx.x] = make_float2(0.f, 0.f);
@@ -128,27 +50,24 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     const auto dy_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.dy.p) + row * p.dy.ld * (DYBF16 ? 2 : 4); };
     const auto ds_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.dsummed.p) + row * p.dsummed.ld * (x_bf16 ? 2 : 4); };
     const auto scale_row = [&](int64_t row) -> const char * { return reinterpret_cast<const char *>(p.ckpt.scales) + row * p.ckpt.ld_scales; };
-    // Copies whole 16-byte pieces of memory that hold a row of `bytes` bytes (on 16-byte boundaries: the row rounded up).
-    const auto copy = [&](char *to, const char *from, int bytes, uint32_t full) -> uint32_t {
-        const int shift = row_shift<MODE>(from), size = (shift + bytes + 15) & ~15;
-        ptx::bulk_g2s(ptx::smem_u32(to), from - shift, (uint32_t)size, full);
-        return (uint32_t)size;
-    };
     const auto copy_row = [&](int64_t row, int s) {  // by the team's thread 0
         char *stage = stages + s * n.stage_bytes;
-        const uint32_t full = full0 + s * 8;
-        const int h_bytes = p.cols * (kAct8 ? 1 : SRC == kHBf16 ? 2 : 4), dy_bytes = p.cols * (DYBF16 ? 2 : 4);
-        const int ds_bytes = p.cols * (x_bf16 ? 2 : 4), scale_bytes = (p.cols + kAct8Block - 1) / kAct8Block;
-        uint32_t sum;
-        const auto size = [&](const char *from, int bytes) { return (uint32_t)((row_shift<MODE>(from) + bytes + 15) & ~15); };
-        sum = size(h_row(row), h_bytes) + size(dy_row(row), dy_bytes);
-        if (p.dsummed.p) sum += size(ds_row(row), ds_bytes);
-        if (MODE == kAnyRow && kAct8) sum += size(scale_row(row), scale_bytes);
-        ptx::mbar_arrive_expect_tx(full, sum);
-        copy(stage, h_row(row), h_bytes, full);
-        copy(stage + n.at_dy, dy_row(row), dy_bytes, full);
-        if (p.dsummed.p) copy(stage + n.at_ds, ds_row(row), ds_bytes, full);
-        if (MODE == kAnyRow && kAct8) copy(stage + n.at_scales, scale_row(row), scale_bytes, full);
+        const uint32_t full = full0 + s * 8, to = ptx::smem_u32(stage);
+        if (MODE != kAnyRow) {
+            ptx::mbar_arrive_expect_tx(full, (uint32_t)n.stage_bytes);
+            ptx::bulk_g2s(to, h_row(row), (uint32_t)n.at_dy, full);
+            ptx::bulk_g2s(to + n.at_dy, dy_row(row), (uint32_t)(n.at_ds - n.at_dy), full);
+            if (p.dsummed.p) ptx::bulk_g2s(to + n.at_ds, ds_row(row), (uint32_t)(n.stage_bytes - n.at_ds), full);
+            return;
+        }
+        uint32_t bytes[4] = {window(h_row(row), p.cols * (kAct8 ? 1 : SRC == kHBf16 ? 2 : 4)), window(dy_row(row), p.cols * (DYBF16 ? 2 : 4)),
+                             p.dsummed.p ? window(ds_row(row), p.cols * (x_bf16 ? 2 : 4)) : 0u,
+                             kAct8 ? window(scale_row(row), (p.cols + kAct8Block - 1) / kAct8Block) : 0u};
+        ptx::mbar_arrive_expect_tx(full, bytes[0] + bytes[1] + bytes[2] + bytes[3]);
+        ptx::bulk_g2s(to, h_row(row) - row_shift<MODE>(h_row(row)), bytes[0], full);
+        ptx::bulk_g2s(to + n.at_dy, dy_row(row) - row_shift<MODE>(dy_row(row)), bytes[1], full);
+        if (p.dsummed.p) ptx::bulk_g2s(to + n.at_ds, ds_row(row) - row_shift<MODE>(ds_row(row)), bytes[2], full);
+        if (kAct8) ptx::bulk_g2s(to + n.at_scales, scale_row(row) - row_shift<MODE>(scale_row(row)), bytes[3], full);
     };
     if (t == 0)
         for (int s = 0; s < S; ++s) {
@@ -198,6 +117,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     uint32_t phases = 0;  // of the stages' barriers
     int s = 0, last = 0, turn = 0;
     for (int64_t row = first; row < p.rows; row += step) {
+        at.next_row();
         bool on_next = true;
         float mean_next = 0.f, rstd_next = 0.f;
         uint32_t scale_next[kScales] = {};
