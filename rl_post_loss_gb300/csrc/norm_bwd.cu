@@ -2,8 +2,8 @@
 // anywhere, the sum of the blocks' partial sums, and which kernel takes a call.
 #include <algorithm>
 
-#include "norm.cuh"
 #include "norm_ring.cuh"
+#include "norm_short.cuh"
 
 namespace rlk {
 
@@ -12,67 +12,94 @@ namespace {
 constexpr int kThreads = kNormWarps * 32;
 constexpr int kJoinCols = 32, kJoinRows = 8;
 
-// ---------------------------------------------------------------- short rows
-//
-// Rows on 16-byte boundaries that fit `lanes` threads of a warp (4 to 32) with VPT vectors each, so that a warp
-// works on several rows and a row's sums take few steps; rows are held in registers from one load to the store.
+// ---------------------------------------------------------------- short rows (norm_short.cuh)
 
-template <int SRC, bool XBF16, bool DYBF16, int VPT, bool FULL>
-__global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBackwardParams p, int lanes) {
-    extern __shared__ __align__(16) float smem_short[];
-    float *w_smem = smem_short;  // [lanes VPT 8]
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & (lanes - 1), per_warp = 32 / lanes;
+template <int SRC, bool DYBF16, int VPT, bool FULL>
+__global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBackwardParams p, NormShort n) {
+    constexpr bool kAct8 = from_act8(SRC);
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(8) uint64_t s_full[kNormWarps * kNormDepth];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lanes = n.lanes, t = lane & (lanes - 1), slot = lane / lanes, S = n.depth;
     const int width = lanes * VPT * kVec;
+    const bool x_bf16 = kAct8 ? p.dx.bf16 : SRC == kHBf16;
+    float *w_smem = reinterpret_cast<float *>(smem + n.smem) - width;
     for (int c = threadIdx.x; c < width; c += kThreads) w_smem[c] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kNormWarps * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
+        ptx::fence_mbar_init();
+    }
     __syncthreads();
+    ShortRing ring(n);
+    ring.mask = p.mask;
+    ring.base[0] = kAct8 ? reinterpret_cast<const char *>(p.ckpt.codes) : static_cast<const char *>(p.x.p);
+    ring.pitch[0] = kAct8 ? p.ckpt.ld_codes : p.x.ld * (SRC == kHBf16 ? 2 : 4);
+    ring.base[1] = static_cast<const char *>(p.dy.p);
+    ring.pitch[1] = p.dy.ld * (DYBF16 ? 2 : 4);
+    ring.base[2] = static_cast<const char *>(p.dsummed.p);
+    ring.pitch[2] = p.dsummed.ld * (x_bf16 ? 2 : 4);
+    ring.rows = p.rows;
+    char *stages = smem + warp * S * n.stage_bytes;
+    ring.stages = ptx::smem_u32(stages);
+    ring.full = ptx::smem_u32(&s_full[warp * S]);
+    ring.lane = lane;
+    ring.per = 32 / lanes;
+    const int64_t first = blockIdx.x + (int64_t)warp * gridDim.x, step = (int64_t)gridDim.x * kNormWarps;
+    const int64_t batches = ((int64_t)p.rows + ring.per - 1) / ring.per;
+    for (int s = 0; s < S; ++s)
+        if (first + s * step < batches) ring.fetch(first + s * step, s);
+
     V8 dw[VPT], db[FULL ? VPT : 1];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         dw[i] = zeros();
         if (FULL) db[i] = zeros();
     }
-    const int64_t step = (int64_t)gridDim.x * kNormWarps * per_warp;
-    for (int64_t base = (blockIdx.x + (int64_t)warp * gridDim.x) * per_warp; base < p.rows; base += step) {
-        const int64_t row = base + lane / lanes;
-        const bool mine = row < p.rows, on = mine && (!p.mask || p.mask[row]);
-        typename RawMat<DYBF16>::type dy[VPT];
-        typename RawMat<XBF16>::type hx[VPT], ds[VPT];
-        Raw8 h8[VPT];
-        uint32_t scale[VPT];
-        float mean = 0.f, rstd = 0.f;
-        if (on) {
+    constexpr int kScales = kAct8 ? VPT : 1;
+    bool dead = false, mine = false, on = false;  // of the thread's row, loaded a batch ahead
+    float mean = 0.f, rstd = 0.f;
+    uint32_t scale[kScales];
+    const auto row_data = [&](int64_t batch, bool &m, bool &o, float &mu, float &r, uint32_t (&sc)[kScales]) {
+        const int64_t row = batch * ring.per + slot;
+        m = row < p.rows;
+        o = m && (!p.mask || p.mask[row]);
+        mu = r = 0.f;
+        if (!o) return;
+        r = p.rstd[row];
+        if (FULL && !p.rms) mu = p.mean[row];
+        if (kAct8)
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int vec = t + i * lanes, col = vec * kVec;
-                if (col < p.cols) {
-                    if (from_act8(SRC)) {
-                        load_raw(h8[i], p.ckpt.codes + row * p.ckpt.ld_codes, col, p.cols, true);
-                        scale[i] = p.ckpt.scales[row * p.ckpt.ld_scales + (vec >> 2)];
-                    } else {
-                        load_mat<XBF16>(hx[i], p.x, row, col, p.cols);
-                    }
-                    load_mat<DYBF16>(dy[i], p.dy, row, col, p.cols);
-                    if (p.dsummed.p) load_mat<XBF16>(ds[i], p.dsummed, row, col, p.cols);
-                }
+                const int vec = t + i * lanes;
+                sc[kAct8 ? i : 0] = vec * kVec < p.cols ? p.ckpt.scales[row * p.ckpt.ld_scales + (vec >> 2)] : 0;
             }
-            rstd = p.rstd[row];
-            if (FULL && !p.rms) mean = p.mean[row];
+    };
+    if (first < batches) row_data(first, mine, on, mean, rstd, scale);
+    uint32_t phases = 0;
+    int s = 0;
+    for (int64_t batch = first; batch < batches; batch += step) {
+        bool mine_next = false, on_next = false;
+        float mean_next = 0.f, rstd_next = 0.f;
+        uint32_t scale_next[kScales] = {};
+        if (batch + step < batches) row_data(batch + step, mine_next, on_next, mean_next, rstd_next, scale_next);
+        const int64_t row = batch * ring.per + slot;
+        if (__any_sync(0xffffffffu, on)) {
+            if (!dead && !ptx::mbar_wait(ring.full + s * 8, (phases >> s) & 1u, kNormWaitNs)) {
+                dead = true;
+                if (p.status) raise_status(p.status, RL_ERR_TIMEOUT);
+            }
+            phases ^= 1u << s;
         }
+        const char *sh = stages + s * n.stage_bytes + n.at[0] + slot * n.row_bytes[0], *sdy = stages + s * n.stage_bytes + n.at[1] + slot * n.row_bytes[1];
+        const char *sds = stages + s * n.stage_bytes + n.at[2] + slot * n.row_bytes[2];
         const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
-        const auto get_h = [&](int i) -> V8 {
-            if constexpr (from_act8(SRC))
-                return act8_decode_norm<SRC == kHE4M3>(h8[i].a, scale[i]);
-            else
-                return pairs(hx[i]);
-        };
         f32x2 s0 = 0ull, s1 = 0ull;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int col = (t + i * lanes) * kVec;
+            const int vec = t + i * lanes, col = vec * kVec;
             if (!on || col >= p.cols) continue;
-            V8 g = pairs(dy[i]), h = get_h(i);
+            V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec);
             if (col + kVec > p.cols) h = clipped(h, col, p.cols), g = clipped(g, col, p.cols);
-            const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), t + i * lanes);
+            const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, w.p[k]);
@@ -89,26 +116,25 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
             if (FULL) c1 = __fadd_rn(c1, __shfl_xor_sync(0xffffffffu, c1, off));
             c2 = __fadd_rn(c2, __shfl_xor_sync(0xffffffffu, c2, off));
         }
-        if (!mine) continue;
         if (t == 0 && p.status && !(fabsf(c1) < INFINITY && fabsf(c2) < INFINITY)) raise_status(p.status, RL_ERR_NONFINITE);
         c1 = FULL && !p.rms ? c1 * p.inv_cols : 0.f;
         c2 = c2 * p.inv_cols * rstd * rstd;
         const f32x2 o1 = pack2(-c1, -c1), nk = pack2(-c2, -c2);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int col = (t + i * lanes) * kVec;
-            if (col >= p.cols) continue;
-            float o[kVec] = {};
+            const int vec = t + i * lanes, col = vec * kVec;
+            if (!mine || col >= p.cols) continue;
+            V8 r = zeros();
+            float o[kVec];
             if (on) {
-                const V8 g = pairs(dy[i]), h = get_h(i), w = read_vec<false>(reinterpret_cast<const char *>(w_smem), t + i * lanes);
-                V8 r;
+                const V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec), w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 rr = mul2(g.p[k], rs), u = FULL ? fma2(rr, w.p[k], o1) : mul2(rr, w.p[k]);
                     r.p[k] = fma2(FULL ? add2(h.p[k], nm) : h.p[k], nk, u);
                 }
                 if (p.dsummed.p) {
-                    const V8 q = pairs(ds[i]);
+                    const V8 q = x_bf16 ? read_vec<true>(sds, vec) : read_vec<false>(sds, vec);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) r.p[k] = add2(r.p[k], q.p[k]);
                 }
@@ -121,18 +147,24 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
                     floats_of(v, o);
                     store_row(p.y, row, col, p.cols, o);
                 }
-                floats_of(r, o);
             } else if (p.y.p) {
+                floats_of(r, o);
                 store_row(p.y, row, col, p.cols, o);
             }
-            if (XBF16)
-                store_vec(static_cast<__nv_bfloat16 *>(p.dx.p) + row * p.dx.ld, col, p.cols, p.dx.fast, o);
-            else
-                store_vec(static_cast<float *>(p.dx.p) + row * p.dx.ld, col, p.cols, p.dx.fast, o);
+            floats_of(r, o);
+            store_row(p.dx, row, col, p.cols, o);
         }
+        __syncwarp();
+        if (batch + S * step < batches && !__any_sync(0xffffffffu, dead)) ring.fetch(batch + S * step, s);
+        mine = mine_next, on = on_next, mean = mean_next, rstd = rstd_next;
+#pragma unroll
+        for (int i = 0; i < kScales; ++i) scale[i] = scale_next[i];
+        s = s + 1 == S ? 0 : s + 1;
     }
+    if (dead && lane == 0)  // (copies in flight end before the block does, or do not within another wait)
+        for (int k = 0; k < S; ++k) ptx::mbar_wait(ring.full + k * 8, (phases >> k) & 1u, kNormWaitNs);
     if (!p.want_dw && !p.want_db) return;
-    float *part = p.partials + (int64_t)blockIdx.x * 2 * p.ld_part;
+    float *part = p.partials + (int64_t)blockIdx.x * 2 * p.ld_part, *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int which = 0; which < (FULL ? 2 : 1); ++which) {
         __syncthreads();
@@ -143,10 +175,10 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
             for (int off = lanes; off < 32; off <<= 1)  // the warp's rows
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) v[j] = __fadd_rn(v[j], __shfl_xor_sync(0xffffffffu, v[j], off));
-            if (lane < lanes) store_vec(smem_short + warp * width, (t + i * lanes) * kVec, width, true, v);
+            if (lane < lanes) store_vec(sums + warp * width, (t + i * lanes) * kVec, width, true, v);
         }
         __syncthreads();
-        join_teams(smem_short, kNormWarps, width, p.cols, part + which * p.ld_part);
+        join_teams(sums, kNormWarps, width, p.cols, part + which * p.ld_part);
     }
 }
 
@@ -192,18 +224,20 @@ cudaError_t launch_join(const NormBackwardParams &p, int parts, cudaStream_t str
 
 int vectors(int cols) { return (cols + kVec - 1) / kVec; }
 
-// Four vectors a thread where registers hold them (16-bit rows, one sum), two otherwise.
-template <int SRC, bool XBF16, bool DYBF16, bool FULL>
+template <int SRC, bool DYBF16>
 cudaError_t launch_short(const NormBackwardParams &p, int blocks, cudaStream_t stream) {
-    constexpr int kVecs = DYBF16 && XBF16 && !FULL ? 4 : 2;
-    int lanes = 4;
-    while (lanes * kVecs * kVec < p.cols) lanes *= 2;
-    const size_t smem = (size_t)kNormWarps * lanes * kVecs * kVec * sizeof(float);  // (the sums; the weight before them)
-    norm_backward_short_kernel<SRC, XBF16, DYBF16, kVecs, FULL><<<blocks, kThreads, smem, stream>>>(p, lanes);
+    const int es[3] = {from_act8(SRC) ? 1 : SRC == kHBf16 ? 2 : 4, DYBF16 ? 2 : 4, !p.dsummed.p ? 0 : p.dx.bf16 ? 2 : 4};
+    const int64_t ld[3] = {from_act8(SRC) ? p.ckpt.ld_codes : p.x.ld, p.dy.ld, p.dsummed.ld};
+    const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
+    const NormShort n = norm_short(p.cols, es, ld, 3, p.mask != nullptr, (size_t)width * 4, (size_t)kNormWarps * width * 4);
+    const bool full = !p.rms || p.want_db;
+    const auto kernel = n.vecs == 2 ? full ? norm_backward_short_kernel<SRC, DYBF16, 2, true> : norm_backward_short_kernel<SRC, DYBF16, 2, false>
+                                    : full ? norm_backward_short_kernel<SRC, DYBF16, 4, true> : norm_backward_short_kernel<SRC, DYBF16, 4, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, kThreads, n.smem, stream>>>(p, n);
     return cudaGetLastError();
 }
-
-constexpr int kShortCols = 512;  // at most a warp of two vectors, 32 KB of sums
 
 constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 512;  // what a block takes beside its rows
 
@@ -265,19 +299,15 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t strea
     const bool fast = p.dy.fast && (act8 ? p.ckpt.fast : p.x.fast) && (!p.dsummed.p || p.dsummed.fast);
     cudaError_t e = cudaErrorUnknown;
     int blocks;
-    if (fast && p.cols <= kShortCols && p.dx.bf16 <= p.dy.bf16) {
+    if (fast && p.cols <= kShortCols) {
         blocks = std::min(p.rows, kNormSMs);
-#define RLK_SHORT(SRC, X, DY) (full ? launch_short<SRC, X, DY, true>(p, blocks, stream) : launch_short<SRC, X, DY, false>(p, blocks, stream))
-        if (act8)
-            e = p.ckpt.e4m3 ? p.dx.bf16 ? RLK_SHORT(kHE4M3, true, true) : p.dy.bf16 ? RLK_SHORT(kHE4M3, false, true) : RLK_SHORT(kHE4M3, false, false)
-                            : p.dx.bf16 ? RLK_SHORT(kHInt8, true, true) : p.dy.bf16 ? RLK_SHORT(kHInt8, false, true) : RLK_SHORT(kHInt8, false, false);
-        else
-            e = p.x.bf16 ? RLK_SHORT(kHBf16, true, true) : p.dy.bf16 ? RLK_SHORT(kHF32, false, true) : RLK_SHORT(kHF32, false, false);
+#define RLK_SHORT(SRC) (p.dy.bf16 ? launch_short<SRC, true>(p, blocks, stream) : launch_short<SRC, false>(p, blocks, stream))
+        e = act8 ? p.ckpt.e4m3 ? RLK_SHORT(kHE4M3) : RLK_SHORT(kHInt8) : p.x.bf16 ? RLK_SHORT(kHBf16) : RLK_SHORT(kHF32);
 #undef RLK_SHORT
     } else {
         const bool any = !fast || (!act8 && p.x.bf16 && !p.dy.bf16);
         // a warp per row where there are rows for all warps
-        const bool warp = !any && p.cols > 512 && p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps;
+        const bool warp = !any && p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps;
         const NormTeams n = teams_of(p, any ? kAnyRow : warp ? kWarpRow : kBlockRow);
         blocks = std::min(p.rows, kNormSMs * n.blocks_per_sm);
 #define RLK_ROWS(H) (p.dy.bf16 ? launch_norm_rows_##H##_bf16(p, n, blocks, stream) : launch_norm_rows_##H##_f32(p, n, blocks, stream))

@@ -1,69 +1,101 @@
 // The forward pass of the norms: rows on 16-byte boundaries (norm_fwd.cuh), short ones among them, and which kernel takes a call.
 #include "norm_fwd.cuh"
+#include "norm_short.cuh"
 
 namespace rlk {
 
 namespace {
 
-// ---------------------------------------------------------------- short rows
-//
-// Rows on 16-byte boundaries of up to 512 columns: `lanes` threads of a warp (4 to 32) with VPT vectors each, so that
-// a warp works on several rows and a row's sums take few steps. The loads of a row go out together.
-template <bool BF16, int VPT>
-__global__ void __launch_bounds__(256, 4) norm_forward_short_kernel(NormForwardParams p, int lanes) {
-    using Raw = typename RawMat<BF16>::type;
-    const int lane = threadIdx.x & 31, t = lane & (lanes - 1), per_warp = 32 / lanes;
-    const int64_t warp = blockIdx.x + (int64_t)(threadIdx.x >> 5) * gridDim.x, step = (int64_t)gridDim.x * (blockDim.x >> 5) * per_warp;
-    for (int64_t base = warp * per_warp; base < p.rows; base += step) {
-        const int64_t row = base + lane / lanes;
-        const bool mine = row < p.rows, on = mine && (!p.mask || p.mask[row]);
-        Raw x[VPT], r[VPT];
-        V8 v[VPT];
-        if (on) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int col = (t + i * lanes) * kVec;
-                if (col < p.cols) {
-                    load_mat<BF16>(x[i], p.x, row, col, p.cols);
-                    if (p.residual.p) load_mat<BF16>(r[i], p.residual, row, col, p.cols);
-                }
+// ---------------------------------------------------------------- short rows (norm_short.cuh)
+
+template <bool BF16, int VPT, bool FULL>
+__global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kernel(NormForwardParams p, NormShort n) {
+    extern __shared__ __align__(128) char smem[];
+    __shared__ __align__(8) uint64_t s_full[kForwardWarps * kNormDepth];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lanes = n.lanes, t = lane & (lanes - 1), slot = lane / lanes, S = n.depth;
+    const int width = lanes * VPT * kVec;
+    float *w_smem = reinterpret_cast<float *>(smem + n.smem) - 2 * width, *b_smem = w_smem + width;
+    for (int c = threadIdx.x; c < width; c += kForwardWarps * 32) {
+        w_smem[c] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
+        b_smem[c] = c < p.cols && p.b ? load_param(p.b, p.params_bf16, c) : 0.f;
+    }
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < kForwardWarps * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    ShortRing ring(n);
+    ring.mask = p.mask;
+    ring.base[0] = static_cast<const char *>(p.x.p);
+    ring.pitch[0] = p.x.ld * (BF16 ? 2 : 4);
+    ring.base[1] = static_cast<const char *>(p.residual.p);
+    ring.pitch[1] = p.residual.ld * (BF16 ? 2 : 4);
+    ring.base[2] = nullptr;
+    ring.pitch[2] = 0;
+    ring.rows = p.rows;
+    char *stages = smem + warp * S * n.stage_bytes;
+    ring.stages = ptx::smem_u32(stages);
+    ring.full = ptx::smem_u32(&s_full[warp * S]);
+    ring.lane = lane;
+    ring.per = 32 / lanes;
+    const int64_t first = blockIdx.x + (int64_t)warp * gridDim.x, step = (int64_t)gridDim.x * kForwardWarps;
+    const int64_t batches = ((int64_t)p.rows + ring.per - 1) / ring.per;
+    for (int s = 0; s < S; ++s)
+        if (first + s * step < batches) ring.fetch(first + s * step, s);
+    const auto live = [&](int64_t batch) { return batch * ring.per + slot < p.rows && (!p.mask || p.mask[batch * ring.per + slot]); };
+    bool dead = false, on = live(first);
+    uint32_t phases = 0;
+    int s = 0;
+    for (int64_t batch = first; batch < batches; batch += step) {
+        const bool on_next = live(batch + step);
+        const int64_t row = batch * ring.per + slot;
+        const bool mine = row < p.rows;
+        if (__any_sync(0xffffffffu, on)) {
+            if (!dead && !ptx::mbar_wait(ring.full + s * 8, (phases >> s) & 1u, kNormWaitNs)) {
+                dead = true;
+                if (p.status) raise_status(p.status, RL_ERR_TIMEOUT);
             }
+            phases ^= 1u << s;
         }
+        const char *sx = stages + s * n.stage_bytes + slot * n.row_bytes[0], *sr = stages + s * n.stage_bytes + n.at[1] + slot * n.row_bytes[1];
+        V8 v[VPT];
         f32x2 s0 = 0ull, s1 = 0ull;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int vec = t + i * lanes, col = vec * kVec;
             v[i] = zeros();
             if (on && col < p.cols) {
-                v[i] = pairs(x[i]);
-                if (p.residual.p) v[i] = add_residual<BF16>(v[i], pairs(r[i]));
+                v[i] = read_vec<BF16>(sx, vec);
+                if (p.residual.p) v[i] = add_residual<BF16>(v[i], read_vec<BF16>(sr, vec));
                 if (col + kVec > p.cols) v[i] = clipped(v[i], col, p.cols);
             }
-            if (mine && col < p.cols && p.h.p) {
-                float f[kVec];
-                floats_of(v[i], f);
-                store_row(p.h, row, col, p.cols, f);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (!FULL || p.rms)
+                    s1 = fma2(v[i].p[k], v[i].p[k], s1);
+                else
+                    s0 = add2(s0, v[i].p[k]);
             }
-            if (p.ckpt.codes) {
+        }
+        __syncwarp();  // the stage is read
+        if (batch + S * step < batches && !__any_sync(0xffffffffu, dead)) ring.fetch(batch + S * step, s);
+        if (p.h.p || p.ckpt.codes)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int vec = t + i * lanes, col = vec * kVec;
                 float f[kVec];
                 floats_of(v[i], f);
+                if (mine && col < p.cols && p.h.p) store_row(p.h, row, col, p.cols, f);
+                if (!p.ckpt.codes) continue;
                 const uint32_t b = act8_scale(act8_block_max(act8_amax(f)), p.ckpt.e4m3);
                 if (mine && col < p.cols) {
                     store_codes(p.ckpt.codes + row * p.ckpt.ld_codes, col, p.cols, p.ckpt.fast, act8_encode(f, b, p.ckpt.e4m3));
                     if ((vec & 3) == 0) p.ckpt.scales[row * p.ckpt.ld_scales + (vec >> 2)] = (uint8_t)b;
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (p.rms)
-                    s1 = fma2(v[i].p[k], v[i].p[k], s1);
-                else
-                    s0 = add2(s0, v[i].p[k]);
-            }
-        }
-        float b = sum_of(p.rms ? s1 : s0), mean = 0.f, var;
+        float b = sum_of(!FULL || p.rms ? s1 : s0), mean = 0.f, var;
         for (int off = lanes >> 1; off > 0; off >>= 1) b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, off));
-        if (p.rms) {
+        if (!FULL || p.rms) {
             var = b * p.inv_cols;
         } else {
             mean = b * p.inv_cols;
@@ -97,58 +129,61 @@ __global__ void __launch_bounds__(256, 4) norm_forward_short_kernel(NormForwardP
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nr);
         }
-        if (!mine) continue;
-        const float rstd = finish_stats(p, row, t == 0 && on, mean, var);
-        if (t == 0 && !on) {
-            if (p.mean) p.mean[row] = 0.f;
-            if (p.rstd) p.rstd[row] = 0.f;
-        }
-        const f32x2 rs = pack2(rstd, rstd);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int col = (t + i * lanes) * kVec;
-            if (col >= p.cols) continue;
-            float f[kVec] = {};
-            if (on) {
-                float u[kVec];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], rs);
-                if (p.w) {
-                    load_params(p.w, p.params_bf16, p.params_fast, col, p.cols, u);
-                    const V8 w = pairs_of(u);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], w.p[k]);
-                }
-                if (p.b) {
-                    load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, u);
-                    const V8 c = pairs_of(u);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], c.p[k]);
-                }
-                floats_of(v[i], f);
+        if (mine) {
+            const float rstd = finish_stats(p, row, t == 0 && on, mean, var);
+            if (t == 0 && !on) {
+                if (p.mean) p.mean[row] = 0.f;
+                if (p.rstd) p.rstd[row] = 0.f;
             }
-            store_row(p.y, row, col, p.cols, f);
+            const f32x2 rs = pack2(rstd, rstd);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int vec = t + i * lanes, col = vec * kVec;
+                if (col >= p.cols) continue;
+                float f[kVec] = {};
+                if (on) {
+                    const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+                    V8 c;
+                    if (FULL) c = read_vec<false>(reinterpret_cast<const char *>(b_smem), vec);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const f32x2 x = mul2(v[i].p[k], rs);
+                        v[i].p[k] = FULL ? fma2(x, w.p[k], c.p[k]) : mul2(x, w.p[k]);
+                    }
+                    floats_of(v[i], f);
+                }
+                store_row(p.y, row, col, p.cols, f);
+            }
         }
+        on = on_next;
+        s = s + 1 == S ? 0 : s + 1;
     }
+    if (dead && lane == 0)  // (copies in flight end before the block does, or do not within another wait)
+        for (int k = 0; k < S; ++k) ptx::mbar_wait(ring.full + k * 8, (phases >> k) & 1u, kNormWaitNs);
 }
 
-constexpr int kShortCols = 512;
 constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 1024;  // what a block takes beside its rows
 
 template <bool BF16>
 cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
-    constexpr int kVecs = 2;
-    int lanes = 4;
-    while (lanes * kVecs * kVec < p.cols) lanes *= 2;
-    const int64_t blocks = ((int64_t)p.rows * lanes + 255) / 256;
-    norm_forward_short_kernel<BF16, kVecs><<<(int)std::min<int64_t>(blocks, kNormSMs * 4), 256, 0, stream>>>(p, lanes);
+    const int es[2] = {BF16 ? 2 : 4, !p.residual.p ? 0 : BF16 ? 2 : 4};
+    const int64_t ld[2] = {p.x.ld, p.residual.ld};
+    const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
+    const NormShort n = norm_short(p.cols, es, ld, 2, p.mask != nullptr, (size_t)width * 8, 0);
+    const bool full = !p.rms || p.b;
+    const auto kernel = n.vecs == 2 ? full ? norm_forward_short_kernel<BF16, 2, true> : norm_forward_short_kernel<BF16, 2, false>
+                                    : full ? norm_forward_short_kernel<BF16, 4, true> : norm_forward_short_kernel<BF16, 4, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<std::min(p.rows, kNormSMs), kForwardWarps * 32, n.smem, stream>>>(p, n);
     return cudaGetLastError();
 }
 
-// A block per row, 24 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by
-// a row's time of its vectors and two more for each exchange of sums.
+// A block per row, 16 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by
+// a row's time of its vectors and two or three more for its exchanges of sums.
 NormTeams teams_of(const NormForwardParams &p, int mode) {
     const int vecs = (p.cols + kVec - 1) / kVec, pad = mode == kAnyRow ? 16 : 0;
+    const bool full = !p.rms || p.b;
     NormTeams n{};
     n.mode = mode;
     n.at_dy = (p.cols * (p.x.bf16 ? 2 : 4) + 15) / 16 * 16 + pad;
@@ -156,20 +191,19 @@ NormTeams teams_of(const NormForwardParams &p, int mode) {
     if (mode == kWarpRow) {
         n.warps = 1;
         n.vecs = vecs > 96 ? 4 : 3;
-        n.blocks_per_sm = 2;
-        n.depth = (int)std::min<size_t>(kNormDepth, (kSmemOfSM / 2 - kBlockExtra) / (forward_threads(mode) / 32 * n.stage_bytes));
-        n.smem = (size_t)(forward_threads(mode) / 32) * n.depth * n.stage_bytes;
+        n.blocks_per_sm = 1;
+        n.depth = (int)std::min<size_t>(kNormDepth, kNormRingSmem / (kForwardWarps * n.stage_bytes));
+        n.smem = (size_t)(kForwardWarps) * n.depth * n.stage_bytes;
         return n;
     }
     double best = 0;
-    for (const int v : {1, 2, 3, 4, 6}) {
-        if (mode == kAnyRow && v > 4) break;
+    for (int v = 1; v <= 4; ++v) {
         const int warps = (vecs + 32 * v - 1) / (32 * v);
-        if (warps > forward_threads(mode) / 32 || (v - 1) * warps * 32 >= vecs) continue;
-        if (mode == kAnyRow && v > 2 && n.warps) continue;  // (single columns take more registers)
-        int blocks = forward_warps(mode) / warps;
+        if (warps > kForwardWarps || (v - 1) * warps * 32 >= vecs) continue;
+        if (n.warps && (mode == kAnyRow ? v == 4 : full && v == 4)) continue;  // (registers)
+        int blocks = kForwardWarps / warps;
         while (blocks > 1 && blocks * (kBlockExtra + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
-        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : 4));
+        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : 3));
         if (n.warps && time >= best) continue;
         best = time;
         n.warps = warps, n.vecs = v, n.blocks_per_sm = blocks;
@@ -188,13 +222,12 @@ cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream)
         const NormTeams n = teams_of(p, kAnyRow);
         return launch_norm_forward_any(p, n, stream);
     }
-    if (p.cols <= 1024 && p.rows >= kNormSMs * forward_warps(kWarpRow)) {
-        const NormTeams n = teams_of(p, kWarpRow);
-        if (n.vecs == 3) return p.x.bf16 ? launch_forward_rows<true, 3, kWarpRow>(p, n, stream) : launch_forward_rows<false, 3, kWarpRow>(p, n, stream);
-        return p.x.bf16 ? launch_forward_rows<true, 4, kWarpRow>(p, n, stream) : launch_forward_rows<false, 4, kWarpRow>(p, n, stream);
-    }
-    const NormTeams n = teams_of(p, kBlockRow);
-    return p.x.bf16 ? launch_forward_vecs<true, kBlockRow>(p, n, stream) : launch_forward_vecs<false, kBlockRow>(p, n, stream);
+    const bool full = !p.rms || p.b, warp = p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kForwardWarps;  // a warp per row where there are rows for all
+    const NormTeams n = teams_of(p, warp ? kWarpRow : kBlockRow);
+#define RLK_ROWS(BF16) (warp ? full ? launch_forward_rows<BF16, 3, true, kWarpRow>(p, n, stream) : n.vecs == 3 ? launch_forward_rows<BF16, 3, false, kWarpRow>(p, n, stream) : launch_forward_rows<BF16, 4, false, kWarpRow>(p, n, stream) \
+                             : full ? launch_forward_vecs<BF16, true, kBlockRow>(p, n, stream) : launch_forward_vecs<BF16, false, kBlockRow>(p, n, stream))
+    return p.x.bf16 ? RLK_ROWS(true) : RLK_ROWS(false);
+#undef RLK_ROWS
 }
 
 }  // namespace rlk

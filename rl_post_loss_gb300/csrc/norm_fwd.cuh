@@ -13,9 +13,7 @@
 namespace rlk {
 
 
-// Of a block and of an SM: 80 registers a thread, for single columns 128.
-constexpr int forward_threads(int mode) { return mode == kAnyRow ? 512 : 384; }
-constexpr int forward_warps(int mode) { return mode == kAnyRow ? 16 : 24; }
+constexpr int kForwardWarps = 16;  // of a block and of an SM: 128 registers a thread
 
 // h's 8-bit codes. On 16-byte boundaries a block of 32 columns is four lanes' vectors; in rows that start anywhere
 // it is what the warp's lanes hold at one place.
@@ -72,9 +70,11 @@ __device__ __forceinline__ float variance(float sum, float squares, float inv_co
     return var < 0.f ? 0.f : var;  // (NaN stays)
 }
 
-template <bool BF16, int VPT, int MODE>
-__global__ void __launch_bounds__(forward_threads(MODE), MODE == kAnyRow ? 1 : 2) norm_forward_kernel(NormForwardParams p, NormTeams n) {
-    constexpr int kTeams = MODE == kWarpRow ? forward_threads(MODE) / 32 : 1;
+// FULL = false is the RMS form without a bias. A thread's weights and biases stay in registers where there is room.
+template <bool BF16, int VPT, bool FULL, int MODE>
+__global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(NormForwardParams p, NormTeams n) {
+    constexpr int kTeams = MODE == kWarpRow ? kForwardWarps : 1;
+    constexpr bool kHeld = MODE != kAnyRow && VPT <= (FULL ? 3 : 4);
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) float2 s_sums[2][16];
     __shared__ __align__(8) uint64_t s_full[kTeams * kNormDepth];
@@ -112,6 +112,13 @@ __global__ void __launch_bounds__(forward_threads(MODE), MODE == kAnyRow ? 1 : 2
             if (row < p.rows && (!p.mask || p.mask[row])) copy_row(row, s);
         }
 
+    V8 w_held[kHeld ? VPT : 1], b_held[kHeld && FULL ? VPT : 1];
+    if (kHeld)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            w_held[kHeld ? i : 0] = at.none(i) ? zeros() : at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
+            if (FULL) b_held[kHeld && FULL ? i : 0] = at.none(i) ? zeros() : at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
+        }
     uint32_t phases = 0;  // of the stages' barriers
     bool dead = false, on = first < p.rows && (!p.mask || p.mask[first]);
     int s = 0, turn = 0;
@@ -139,13 +146,13 @@ __global__ void __launch_bounds__(forward_threads(MODE), MODE == kAnyRow ? 1 : 2
                 if (MODE != kAnyRow && i == VPT - 1 && at.cut) v[i] = clipped(v[i], at.vec(i) * kVec, p.cols);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (p.rms)
+                    if (!FULL || p.rms)
                         s1 = fma2(v[i].p[k], v[i].p[k], s1);
                     else
                         s0 = add2(s0, v[i].p[k]);
                 }
             }
-            float a = 0.f, b = sum_of(p.rms ? s1 : s0), mean = 0.f, var;
+            float a = 0.f, b = sum_of(!FULL || p.rms ? s1 : s0), mean = 0.f, var;
             team_sums<false, MODE == kWarpRow>(a, b, s_sums[turn], T >> 5);
             turn ^= 1;
             if (MODE == kWarpRow) __syncwarp();
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(forward_threads(MODE), MODE == kAnyRow ? 1 : 2
             if (p.ckpt.codes)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) store_act8(at, p.ckpt, row, i, v[i]);
-            if (p.rms) {
+            if (!FULL || p.rms) {
                 var = b * p.inv_cols;
             } else {
                 mean = b * p.inv_cols;
@@ -194,20 +201,14 @@ __global__ void __launch_bounds__(forward_threads(MODE), MODE == kAnyRow ? 1 : 2
                 if (at.none(i)) continue;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], rs);
-                if (p.w) {
-                    const V8 w = at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
-                    if (p.b) {
-                        const V8 c = at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
+                const V8 w = kHeld ? w_held[kHeld ? i : 0] : at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
+                if (FULL) {
+                    const V8 c = kHeld ? b_held[kHeld && FULL ? i : 0] : at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[i].p[k] = fma2(v[i].p[k], w.p[k], c.p[k]);
-                    } else {
+                    for (int k = 0; k < 4; ++k) v[i].p[k] = fma2(v[i].p[k], w.p[k], c.p[k]);
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], w.p[k]);
-                    }
-                } else if (p.b) {
-                    const V8 c = at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], c.p[k]);
+                    for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], w.p[k]);
                 }
                 at.store(p.y, row, i, v[i]);
             }
@@ -233,25 +234,23 @@ __global__ void __launch_bounds__(forward_threads(MODE), MODE == kAnyRow ? 1 : 2
         for (int k = 0; k < S; ++k) ptx::mbar_wait(full0 + k * 8, (phases >> k) & 1u, kNormWaitNs);
 }
 
-template <bool BF16, int VPT, int MODE>
+template <bool BF16, int VPT, bool FULL, int MODE>
 cudaError_t launch_forward_rows(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
-    auto kernel = norm_forward_kernel<BF16, VPT, MODE>;
+    auto kernel = norm_forward_kernel<BF16, VPT, FULL, MODE>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<std::min(p.rows, kNormSMs * n.blocks_per_sm), MODE == kWarpRow ? forward_threads(MODE) : n.warps * 32, n.smem, stream>>>(p, n);
+    kernel<<<std::min(p.rows, kNormSMs * n.blocks_per_sm), MODE == kWarpRow ? kForwardWarps * 32 : n.warps * 32, n.smem, stream>>>(p, n);
     return cudaGetLastError();
 }
 
-template <bool BF16, int MODE>
+template <bool BF16, bool FULL, int MODE>
 cudaError_t launch_forward_vecs(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
     switch (n.vecs) {
-        case 1: return launch_forward_rows<BF16, 1, MODE>(p, n, stream);
-        case 2: return launch_forward_rows<BF16, 2, MODE>(p, n, stream);
-        case 3: return launch_forward_rows<BF16, 3, MODE>(p, n, stream);
-        case 4: return launch_forward_rows<BF16, 4, MODE>(p, n, stream);
+        case 1: return launch_forward_rows<BF16, 1, FULL, MODE>(p, n, stream);
+        case 2: return launch_forward_rows<BF16, 2, FULL, MODE>(p, n, stream);
+        case 3: return launch_forward_rows<BF16, 3, FULL, MODE>(p, n, stream);
+        default: return launch_forward_rows<BF16, 4, FULL, MODE>(p, n, stream);
     }
-    if constexpr (MODE != kAnyRow) return launch_forward_rows<BF16, 6, MODE>(p, n, stream);
-    return cudaErrorInvalidValue;
 }
 
 }  // namespace rlk

@@ -4,7 +4,7 @@
 namespace rlk {
 
 cudaError_t launch_norm_forward_any(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
-    return p.x.bf16 ? launch_forward_vecs<true, kAnyRow>(p, n, stream) : launch_forward_vecs<false, kAnyRow>(p, n, stream);
+    return p.x.bf16 ? launch_forward_vecs<true, true, kAnyRow>(p, n, stream) : launch_forward_vecs<false, true, kAnyRow>(p, n, stream);
 }
 
 }  // namespace rlk

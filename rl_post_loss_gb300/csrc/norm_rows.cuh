@@ -102,24 +102,4 @@ __device__ __forceinline__ int row_shift(const char *row) { return MODE == kAnyR
 // The bytes of the whole 16-byte pieces of memory that hold a row.
 __device__ __forceinline__ uint32_t window(const char *row, int bytes) { return (uint32_t)(((int)(reinterpret_cast<uintptr_t>(row) & 15u) + bytes + 15) & ~15); }
 
-// ---------------------------------------------------------------- rows straight from memory, on 16-byte boundaries
-
-template <bool BF16>
-struct RawMat {
-    using type = Raw16;
-};
-template <>
-struct RawMat<false> {
-    using type = Raw32;
-};
-template <bool BF16>
-__device__ __forceinline__ void load_mat(typename RawMat<BF16>::type &r, const RowMat &m, int64_t row, int col, int cols) {
-    if constexpr (BF16)
-        load_raw(r, static_cast<const __nv_bfloat16 *>(m.p) + row * m.ld, col, cols, true);
-    else
-        load_raw(r, static_cast<const float *>(m.p) + row * m.ld, col, cols, true);
-}
-__device__ __forceinline__ V8 pairs(const Raw16 &r) { return bf16_pairs(r.a); }
-__device__ __forceinline__ V8 pairs(const Raw32 &r) { return f32_pairs(r.a, r.b); }
-
 }  // namespace rlk

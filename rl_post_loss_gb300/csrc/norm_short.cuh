@@ -1,0 +1,73 @@
+// Short rows of the norms (512 columns and less, on 16-byte boundaries): 4, 8 or 16 threads of a warp take a row,
+// with two or four vectors of eight columns each, so that a warp works on 8, 4 or 2 rows at a time and a row's
+// sums take few steps. Every warp has a ring of its own in shared memory; the copies of its next rows are under
+// way while it works on one batch. Rows that follow one another without a gap come in one copy.
+#pragma once
+
+#include "norm_rows.cuh"
+
+namespace rlk {
+
+constexpr int kShortCols = 512;
+
+// Up to three matrices whose rows come together.
+struct NormShort {
+    int lanes, vecs, depth;
+    int row_bytes[3];  // of a matrix's row in shared memory, 0: no such matrix
+    int at[3];         // where a matrix's rows begin in a stage
+    int whole[3];      // a batch is one copy
+    int stage_bytes;
+    size_t smem;
+};
+
+// `row_bytes`, `ld_bytes` of the matrices; `fixed` bytes of a block's shared memory for something else, after the rings.
+inline NormShort norm_short(int cols, const int *es, const int64_t *ld, int count, bool masked, size_t fixed, size_t least) {
+    NormShort n{};
+    n.vecs = cols <= 64 ? 2 : 4;
+    n.lanes = cols <= 128 ? 4 : cols <= 256 ? 8 : 16;
+    for (int k = 0; k < count; ++k) {
+        if (!es[k]) continue;
+        n.row_bytes[k] = (cols * es[k] + 15) / 16 * 16;
+        n.whole[k] = !masked && ld[k] * es[k] == n.row_bytes[k];
+        n.at[k] = n.stage_bytes;
+        n.stage_bytes += 32 / n.lanes * n.row_bytes[k];
+    }
+    n.depth = (int)((kNormRingSmem - fixed) / ((size_t)kNormWarps * n.stage_bytes));
+    n.depth = n.depth > kNormDepth ? kNormDepth : n.depth;
+    n.smem = (size_t)kNormWarps * n.depth * n.stage_bytes;
+    n.smem = (n.smem > least ? n.smem : least) + fixed;
+    return n;
+}
+
+// A warp's ring. Batch b is rows b (32 / lanes), ...; `base` and `pitch` are the matrices in memory, in bytes.
+struct ShortRing {
+    const NormShort &n;
+    const uint8_t *mask;
+    const char *base[3];
+    int64_t pitch[3];
+    int64_t rows;
+    uint32_t stages, full;  // in shared memory
+    int lane, per;
+    __device__ __forceinline__ ShortRing(const NormShort &n) : n(n) {}
+    // By the whole warp, which has read the stage.
+    __device__ __forceinline__ void fetch(int64_t batch, int s) const {
+        const int64_t row = batch * per + lane;
+        const bool on = lane < per && row < rows && (!mask || mask[row]);
+        const int count = __popc(__ballot_sync(0xffffffffu, on));
+        if (count == 0) return;
+        const uint32_t bar = full + s * 8, to = stages + s * n.stage_bytes;
+        if (lane == 0) ptx::mbar_arrive_expect_tx(bar, (uint32_t)(count * (n.row_bytes[0] + n.row_bytes[1] + n.row_bytes[2])));
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (!n.row_bytes[k]) continue;
+            if (n.whole[k]) {
+                if (lane == 0) ptx::bulk_g2s(to + n.at[k], base[k] + row * pitch[k], (uint32_t)(count * n.row_bytes[k]), bar);
+            } else if (on) {
+                ptx::bulk_g2s(to + n.at[k] + lane * n.row_bytes[k], base[k] + row * pitch[k], (uint32_t)n.row_bytes[k], bar);
+            }
+        }
+    }
+};
+
+}  // namespace rlk
