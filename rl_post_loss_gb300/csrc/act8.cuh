@@ -59,11 +59,12 @@ __device__ __forceinline__ uint32_t act8_scale(uint32_t amax, bool e4m3) {
     return amax >= 0x7f800000u ? 255u : (uint32_t)max(b, 1);
 }
 
+// The bits of the largest |v|; a NaN wins.
 __device__ __forceinline__ uint32_t act8_amax(const float (&v)[kVec]) {
-    uint32_t a = 0;
+    float a = fabsf(v[0]);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) a = max(a, __float_as_uint(v[j]) & 0x7fffffffu);
-    return a;
+    for (int j = 1; j < kVec; ++j) asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(fabsf(v[j])));
+    return __float_as_uint(a);
 }
 
 // The largest of the four lanes that share a block (every lane of the warp takes part).
@@ -177,22 +178,27 @@ __device__ __forceinline__ V8 act8_decode_norm(uint2 c, uint32_t b) {
     return r;
 }
 
-// What one code stands for, in fp32.
-__device__ __forceinline__ float act8_value(uint32_t c, uint32_t b, bool e4m3) {
+// What one code stands for.
+__device__ __forceinline__ float act8_value(uint32_t c, uint32_t b, bool e4m3, float most) {
     const float s = __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
     const float q = e4m3 ? __uint_as_float((uint32_t)((int32_t)(c << 24) >> 4) & 0x87f00000u) * 0x1p120f : (float)(int8_t)c;
-    const float v = q * s, most = __uint_as_float(0x7f7fffffu);
+    const float v = q * s;
     return fabsf(v) > most ? copysignf(most, v) : v;
 }
 
 // ---------------------------------------------------------------- eight columns of a row in memory
 //
-// `fast` (one flag per matrix, from its address and row stride): rows start on 16-byte boundaries (8-byte
-// ones for codes) and are read up to their length rounded up to those; otherwise element by element.
+// `fast` (one flag per matrix, from its address and row stride): rows start on 16-byte boundaries (2: 32-byte ones)
+// and are read up to their length rounded up to those; otherwise single columns are read and written.
+
+__device__ __forceinline__ void ld32(const void *p, uint4 &a, uint4 &b) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(p));
+}
 
 struct Raw16 { uint4 a; };
 struct Raw32 { uint4 a, b; };
-struct Raw8 { uint2 a; };
 
 __device__ __forceinline__ uint4 ld16(const void *p) {
     uint4 r;
@@ -200,43 +206,10 @@ __device__ __forceinline__ uint4 ld16(const void *p) {
     return r;
 }
 
-__device__ __forceinline__ void load_raw(Raw16 &r, const __nv_bfloat16 *row, int col, int cols, bool fast) {
-    if (fast) {
-        r.a = ld16(row + col);
-        return;
-    }
-    const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + col;
-    uint32_t w[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t lo = col + 2 * k < cols ? p[2 * k] : 0u, hi = col + 2 * k + 1 < cols ? p[2 * k + 1] : 0u;
-        w[k] = lo | (hi << 16);
-    }
-    r.a = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void load_raw(Raw32 &r, const float *row, int col, int cols, bool fast) {
-    if (fast) {
-        r.a = *reinterpret_cast<const uint4 *>(row + col);
-        r.b = col + 4 < cols ? *reinterpret_cast<const uint4 *>(row + col + 4) : make_uint4(0u, 0u, 0u, 0u);
-        return;
-    }
-    const uint32_t *p = reinterpret_cast<const uint32_t *>(row) + col;
-    uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k] = col + k < cols ? p[k] : 0u;
-    r.a = make_uint4(w[0], w[1], w[2], w[3]);
-    r.b = make_uint4(w[4], w[5], w[6], w[7]);
-}
-__device__ __forceinline__ void load_raw(Raw8 &r, const uint8_t *row, int col, int cols, bool fast) {
-    if (fast) {
-        r.a = *reinterpret_cast<const uint2 *>(row + col);
-        return;
-    }
-    uint32_t w[2] = {0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (col + k < cols) w[k >> 2] |= (uint32_t)row[col + k] << (8 * (k & 3));
-    r.a = make_uint2(w[0], w[1]);
+__device__ __forceinline__ void load_raw(Raw16 &r, const __nv_bfloat16 *row, int col, int) { r.a = ld16(row + col); }
+__device__ __forceinline__ void load_raw(Raw32 &r, const float *row, int col, int cols) {
+    r.a = *reinterpret_cast<const uint4 *>(row + col);
+    r.b = col + 4 < cols ? *reinterpret_cast<const uint4 *>(row + col + 4) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 __device__ __forceinline__ void to_float(const Raw16 &r, float (&v)[kVec]) {
@@ -286,6 +259,20 @@ __device__ __forceinline__ void store_vec(float *row, int col, int cols, bool fa
     for (int j = 0; j < kVec; ++j)
         if (col + j < cols) row[col + j] = v[j];
 }
+// The same in one store of 32 bytes (rows on 32-byte boundaries): two stores of 16 write every second half of a warp's
+// 32-byte pieces of memory, and each write of half a piece costs as much as a whole one (unpacking to fp32 67% of the
+// copy rate so, @@% in one store).
+__device__ __forceinline__ void st32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                 "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+__device__ __forceinline__ void store_vec32(float *row, int col, const float (&v)[kVec]) {
+    uint32_t w[8];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) w[j] = __float_as_uint(v[j]);
+    st32(row + col, w);
+}
 __device__ __forceinline__ void store_codes(uint8_t *row, int col, int cols, bool fast, uint2 c) {
     if (fast && col + kVec <= cols) {
         *reinterpret_cast<uint2 *>(row + col) = c;
@@ -298,7 +285,7 @@ __device__ __forceinline__ void store_codes(uint8_t *row, int col, int cols, boo
 
 // ---------------------------------------------------------------- parameters
 
-// A matrix: its first element, the row stride in elements, and whether vector accesses are allowed.
+// A matrix: its first element, the row stride in elements, and whether vector accesses are allowed (2: of 32 bytes).
 struct RowMat {
     void *p;
     int64_t ld;
@@ -318,9 +305,9 @@ struct Act8Params {
     Act8Mat a;
     int64_t rows;
     int32_t cols;
-    int32_t row_vecs;       // vectors of a row, whole blocks
-    int64_t step_rows;      // rows and vectors that the grid's threads step over
-    int32_t step_vecs;
+    int32_t row_parts;      // parts of 16 columns of a row, whole blocks
+    int64_t step_rows;      // rows and parts that the grid's threads step over
+    int32_t step_parts;
 };
 
 cudaError_t launch_act8_pack(Act8Params p, cudaStream_t stream);
@@ -330,6 +317,8 @@ cudaError_t launch_act8_unpack(Act8Params p, cudaStream_t stream);
 __device__ __forceinline__ void store_row(const RowMat &m, int64_t row, int col, int cols, const float (&v)[kVec]) {
     if (m.bf16)
         store_vec(static_cast<__nv_bfloat16 *>(m.p) + row * m.ld, col, cols, m.fast, v);
+    else if (m.fast == 2 && col + kVec <= cols)
+        store_vec32(static_cast<float *>(m.p) + row * m.ld, col, v);
     else
         store_vec(static_cast<float *>(m.p) + row * m.ld, col, cols, m.fast, v);
 }

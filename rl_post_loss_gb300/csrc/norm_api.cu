@@ -11,7 +11,8 @@ bool known(int32_t dtype) { return dtype == RL_F32 || dtype == RL_BF16; }
 
 rlk::RowMat mat(const void *p, int64_t ld, int32_t dtype) {
     const int64_t es = dtype == RL_F32 ? 4 : 2;
-    return rlk::RowMat{const_cast<void *>(p), ld, dtype == RL_BF16, aligned(p, 16) && (ld * es) % 16 == 0};
+    const auto rows_on = [&](int64_t to) { return aligned(p, (uintptr_t)to) && (ld * es) % to == 0; };
+    return rlk::RowMat{const_cast<void *>(p), ld, dtype == RL_BF16, rows_on(32) ? 2 : rows_on(16) ? 1 : 0};
 }
 rlk::Act8Mat act8(const rl_act8 &a) {
     return rlk::Act8Mat{static_cast<uint8_t *>(a.codes), static_cast<uint8_t *>(a.scales), a.ld_codes, a.ld_scales,

@@ -14,7 +14,8 @@ constexpr int kJoinCols = 32, kJoinRows = 8;
 
 // ---------------------------------------------------------------- short rows (norm_short.cuh)
 
-template <int SRC, bool DYBF16, int VPT, bool FULL>
+// EXACT: the threads' vectors are the row's columns to the last one, no mask and no output made again.
+template <int SRC, bool DYBF16, int VPT, bool FULL, bool EXACT>
 __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBackwardParams p, NormShort n) {
     constexpr bool kAct8 = from_act8(SRC);
     extern __shared__ __align__(128) char smem[];
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
     const auto row_data = [&](int64_t batch, bool &m, bool &o, float &mu, float &r, uint32_t (&sc)[kScales]) {
         const int64_t row = batch * ring.per + slot;
         m = row < p.rows;
-        o = m && (!p.mask || p.mask[row]);
+        o = m && (EXACT || !p.mask || p.mask[row]);
         mu = r = 0.f;
         if (!o) return;
         r = p.rstd[row];
@@ -93,22 +94,24 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
         const char *sds = stages + s * n.stage_bytes + n.at[2] + slot * n.row_bytes[2];
         const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
         f32x2 s0 = 0ull, s1 = 0ull;
+        if (on) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int vec = t + i * lanes, col = vec * kVec;
-            if (!on || col >= p.cols) continue;
-            V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec);
-            if (col + kVec > p.cols) h = clipped(h, col, p.cols), g = clipped(g, col, p.cols);
-            const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+            for (int i = 0; i < VPT; ++i) {
+                const int vec = t + i * lanes, col = vec * kVec;
+                if (!EXACT && col >= p.cols) continue;
+                V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec);
+                if (!EXACT && col + kVec > p.cols) h = clipped(h, col, p.cols), g = clipped(g, col, p.cols);
+                const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, w.p[k]);
-                dw[i].p[k] = fma2(r, d, dw[i].p[k]);
-                if (FULL) {
-                    db[i].p[k] = add2(db[i].p[k], g.p[k]);
-                    s0 = add2(s0, u);
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, w.p[k]);
+                    dw[i].p[k] = fma2(r, d, dw[i].p[k]);
+                    if (FULL) {
+                        db[i].p[k] = add2(db[i].p[k], g.p[k]);
+                        s0 = add2(s0, u);
+                    }
+                    s1 = fma2(u, d, s1);
                 }
-                s1 = fma2(u, d, s1);
             }
         }
         float c1 = sum_of(s0), c2 = sum_of(s1);
@@ -120,14 +123,15 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
         c1 = FULL && !p.rms ? c1 * p.inv_cols : 0.f;
         c2 = c2 * p.inv_cols * rstd * rstd;
         const f32x2 o1 = pack2(-c1, -c1), nk = pack2(-c2, -c2);
+        if (on) {
+            const int64_t out = row * p.dx.ld;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int vec = t + i * lanes, col = vec * kVec;
-            if (!mine || col >= p.cols) continue;
-            V8 r = zeros();
-            float o[kVec];
-            if (on) {
+            for (int i = 0; i < VPT; ++i) {
+                const int vec = t + i * lanes, col = vec * kVec;
+                if (!EXACT && col >= p.cols) continue;
                 const V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec), w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+                V8 r;
+                float o[kVec];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 rr = mul2(g.p[k], rs), u = FULL ? fma2(rr, w.p[k], o1) : mul2(rr, w.p[k]);
@@ -138,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
 #pragma unroll
                     for (int k = 0; k < 4; ++k) r.p[k] = add2(r.p[k], q.p[k]);
                 }
-                if (p.y.p) {
+                if (!EXACT && p.y.p) {
                     float b[kVec] = {};
                     if (p.b) load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, b);
                     V8 v = pairs_of(b);
@@ -147,12 +151,21 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
                     floats_of(v, o);
                     store_row(p.y, row, col, p.cols, o);
                 }
-            } else if (p.y.p) {
                 floats_of(r, o);
-                store_row(p.y, row, col, p.cols, o);
+                const int end = EXACT ? col + kVec : p.cols;  // (EXACT: no part of a vector)
+                if (x_bf16)
+                    store_vec(static_cast<__nv_bfloat16 *>(p.dx.p) + out, col, end, EXACT || p.dx.fast, o);
+                else if (p.dx.fast == 2 && col + kVec <= end)
+                    store_vec32(static_cast<float *>(p.dx.p) + out, col, o);
+                else
+                    store_vec(static_cast<float *>(p.dx.p) + out, col, end, EXACT || p.dx.fast, o);
             }
-            floats_of(r, o);
-            store_row(p.dx, row, col, p.cols, o);
+        } else if (!EXACT && mine) {
+            const float o[kVec] = {};
+            for (int vec = t; vec * kVec < p.cols; vec += lanes) {
+                store_row(p.dx, row, vec * kVec, p.cols, o);
+                if (p.y.p) store_row(p.y, row, vec * kVec, p.cols, o);
+            }
         }
         __syncwarp();
         if (batch + S * step < batches && !__any_sync(0xffffffffu, dead)) ring.fetch(batch + S * step, s);
@@ -231,8 +244,10 @@ cudaError_t launch_short(const NormBackwardParams &p, int blocks, cudaStream_t s
     const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
     const NormShort n = norm_short(p.cols, es, ld, 3, p.mask != nullptr, (size_t)width * 4, (size_t)kNormWarps * width * 4);
     const bool full = !p.rms || p.want_db;
-    const auto kernel = n.vecs == 2 ? full ? norm_backward_short_kernel<SRC, DYBF16, 2, true> : norm_backward_short_kernel<SRC, DYBF16, 2, false>
-                                    : full ? norm_backward_short_kernel<SRC, DYBF16, 4, true> : norm_backward_short_kernel<SRC, DYBF16, 4, false>;
+    const bool exact = p.cols == width && !p.mask && !p.y.p && p.dx.fast;
+#define RLK_SHORT(V, F) (exact ? norm_backward_short_kernel<SRC, DYBF16, V, F, true> : norm_backward_short_kernel<SRC, DYBF16, V, F, false>)
+    const auto kernel = n.vecs == 2 ? full ? RLK_SHORT(2, true) : RLK_SHORT(2, false) : full ? RLK_SHORT(4, true) : RLK_SHORT(4, false);
+#undef RLK_SHORT
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
     if (e != cudaSuccess) return e;
     kernel<<<blocks, kThreads, n.smem, stream>>>(p, n);

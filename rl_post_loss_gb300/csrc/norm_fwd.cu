@@ -8,7 +8,8 @@ namespace {
 
 // ---------------------------------------------------------------- short rows (norm_short.cuh)
 
-template <bool BF16, int VPT, bool FULL>
+// EXACT: the threads' vectors are the row's columns to the last one, no mask, and rows of y on 16-byte boundaries.
+template <bool BF16, int VPT, bool FULL, bool EXACT>
 __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kernel(NormForwardParams p, NormShort n) {
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(8) uint64_t s_full[kForwardWarps * kNormDepth];
@@ -42,7 +43,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kern
     const int64_t batches = ((int64_t)p.rows + ring.per - 1) / ring.per;
     for (int s = 0; s < S; ++s)
         if (first + s * step < batches) ring.fetch(first + s * step, s);
-    const auto live = [&](int64_t batch) { return batch * ring.per + slot < p.rows && (!p.mask || p.mask[batch * ring.per + slot]); };
+    const auto live = [&](int64_t batch) { return batch * ring.per + slot < p.rows && (EXACT || !p.mask || p.mask[batch * ring.per + slot]); };
     bool dead = false, on = live(first);
     uint32_t phases = 0;
     int s = 0;
@@ -61,20 +62,22 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kern
         V8 v[VPT];
         f32x2 s0 = 0ull, s1 = 0ull;
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int vec = t + i * lanes, col = vec * kVec;
-            v[i] = zeros();
-            if (on && col < p.cols) {
+        for (int i = 0; i < VPT; ++i) v[i] = zeros();
+        if (on) {
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int vec = t + i * lanes, col = vec * kVec;
+                if (!EXACT && col >= p.cols) continue;
                 v[i] = read_vec<BF16>(sx, vec);
                 if (p.residual.p) v[i] = add_residual<BF16>(v[i], read_vec<BF16>(sr, vec));
-                if (col + kVec > p.cols) v[i] = clipped(v[i], col, p.cols);
-            }
+                if (!EXACT && col + kVec > p.cols) v[i] = clipped(v[i], col, p.cols);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (!FULL || p.rms)
-                    s1 = fma2(v[i].p[k], v[i].p[k], s1);
-                else
-                    s0 = add2(s0, v[i].p[k]);
+                for (int k = 0; k < 4; ++k) {
+                    if (!FULL || p.rms)
+                        s1 = fma2(v[i].p[k], v[i].p[k], s1);
+                    else
+                        s0 = add2(s0, v[i].p[k]);
+                }
             }
         }
         __syncwarp();  // the stage is read
@@ -104,10 +107,10 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kern
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int col = (t + i * lanes) * kVec;
-                if (col >= p.cols) continue;
+                if (!EXACT && col >= p.cols) continue;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nm);
-                if (col + kVec > p.cols) v[i] = clipped(v[i], col, p.cols);
+                if (!EXACT && col + kVec > p.cols) v[i] = clipped(v[i], col, p.cols);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     s0 = add2(s0, v[i].p[k]);
@@ -129,31 +132,39 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kern
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nr);
         }
-        if (mine) {
-            const float rstd = finish_stats(p, row, t == 0 && on, mean, var);
-            if (t == 0 && !on) {
-                if (p.mean) p.mean[row] = 0.f;
-                if (p.rstd) p.rstd[row] = 0.f;
-            }
+        if (on) {
+            const float rstd = finish_stats(p, row, t == 0, mean, var);
             const f32x2 rs = pack2(rstd, rstd);
+            const int64_t out = row * p.y.ld;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int vec = t + i * lanes, col = vec * kVec;
-                if (col >= p.cols) continue;
-                float f[kVec] = {};
-                if (on) {
-                    const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
-                    V8 c;
-                    if (FULL) c = read_vec<false>(reinterpret_cast<const char *>(b_smem), vec);
+                if (!EXACT && col >= p.cols) continue;
+                const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+                V8 c;
+                if (FULL) c = read_vec<false>(reinterpret_cast<const char *>(b_smem), vec);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const f32x2 x = mul2(v[i].p[k], rs);
-                        v[i].p[k] = FULL ? fma2(x, w.p[k], c.p[k]) : mul2(x, w.p[k]);
-                    }
-                    floats_of(v[i], f);
+                for (int k = 0; k < 4; ++k) {
+                    const f32x2 x = mul2(v[i].p[k], rs);
+                    v[i].p[k] = FULL ? fma2(x, w.p[k], c.p[k]) : mul2(x, w.p[k]);
                 }
-                store_row(p.y, row, col, p.cols, f);
+                float f[kVec];
+                floats_of(v[i], f);
+                const int end = EXACT ? col + kVec : p.cols;  // (EXACT: no part of a vector)
+                if (p.y.bf16)
+                    store_vec(static_cast<__nv_bfloat16 *>(p.y.p) + out, col, end, EXACT || p.y.fast, f);
+                else if (p.y.fast == 2 && col + kVec <= end)
+                    store_vec32(static_cast<float *>(p.y.p) + out, col, f);
+                else
+                    store_vec(static_cast<float *>(p.y.p) + out, col, end, EXACT || p.y.fast, f);
             }
+        } else if (!EXACT && mine) {
+            if (t == 0) {
+                if (p.mean) p.mean[row] = 0.f;
+                if (p.rstd) p.rstd[row] = 0.f;
+            }
+            const float f[kVec] = {};
+            for (int vec = t; vec * kVec < p.cols; vec += lanes) store_row(p.y, row, vec * kVec, p.cols, f);
         }
         on = on_next;
         s = s + 1 == S ? 0 : s + 1;
@@ -171,8 +182,10 @@ cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
     const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
     const NormShort n = norm_short(p.cols, es, ld, 2, p.mask != nullptr, (size_t)width * 8, 0);
     const bool full = !p.rms || p.b;
-    const auto kernel = n.vecs == 2 ? full ? norm_forward_short_kernel<BF16, 2, true> : norm_forward_short_kernel<BF16, 2, false>
-                                    : full ? norm_forward_short_kernel<BF16, 4, true> : norm_forward_short_kernel<BF16, 4, false>;
+    const bool exact = p.cols == width && !p.mask && p.y.fast;
+#define RLK_SHORT(V, F) (exact ? norm_forward_short_kernel<BF16, V, F, true> : norm_forward_short_kernel<BF16, V, F, false>)
+    const auto kernel = n.vecs == 2 ? full ? RLK_SHORT(2, true) : RLK_SHORT(2, false) : full ? RLK_SHORT(4, true) : RLK_SHORT(4, false);
+#undef RLK_SHORT
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
     if (e != cudaSuccess) return e;
     kernel<<<std::min(p.rows, kNormSMs), kForwardWarps * 32, n.smem, stream>>>(p, n);

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         const auto get_h = [&](int i) -> V8 {
             if constexpr (MODE != kAnyRow) return read_h<SRC>(sh, at.vec(i), scale[kScales > 1 ? i : 0]);
             if constexpr (!kAct8) return at.template read<SRC == kHBf16>(sh, i);
-            return at.singles(i, [&](int c) { return act8_value((uint8_t)sh[c], (uint8_t)ssc[c / kAct8Block], SRC == kHE4M3); });
+            return at.singles(i, [&](int c) { return act8_value((uint8_t)sh[c], (uint8_t)ssc[c / kAct8Block], SRC == kHE4M3, __uint_as_float(0x7f7fffffu)); });
         };
         float c1 = 0.f, c2 = 0.f;
         const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
@@ -173,12 +173,12 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         if (MODE == kWarpRow) __syncwarp();
         if (more && !dead) copy_row(row_more, last);
         const f32x2 o1 = pack2(-c1, -c1), nk = pack2(-c2, -c2);
+        if (on) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (at.none(i)) continue;
-            V8 r = zeros();
-            if (on) {
+            for (int i = 0; i < VPT; ++i) {
+                if (at.none(i)) continue;
                 const V8 h = get_h(i), g = at.template read<DYBF16>(sdy, i), ww = weight(i);
+                V8 r;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 rr = mul2(g.p[k], rs), u = FULL ? fma2(rr, ww.p[k], o1) : mul2(rr, ww.p[k]);
@@ -195,10 +195,14 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                     for (int k = 0; k < 4; ++k) u.p[k] = fma2(mul2(add2(h.p[k], nm), rs), ww.p[k], u.p[k]);
                     at.store(p.y, row, i, u);
                 }
-            } else if (p.y.p) {
-                at.store(p.y, row, i, r);
+                at.store(p.dx, row, i, r);
             }
-            at.store(p.dx, row, i, r);
+        } else {
+            for (int i = 0; i < VPT; ++i) {
+                if (at.none(i)) continue;
+                at.store(p.dx, row, i, zeros());
+                if (p.y.p) at.store(p.y, row, i, zeros());
+            }
         }
         if (MODE != kWarpRow && S == 1) {
             __syncthreads();
