@@ -607,39 +607,64 @@ class Act8:
     """A matrix of activations kept in 8 bits: ``codes`` [rows, columns] and ``scales`` [rows, ceil(columns / 32)], both
     torch.uint8, in the format "int8" or "e4m3" (rl_act8 in the header says what they hold)."""
 
-    __slots__ = ("codes", "scales", "format")
+    __slots__ = ("shape", "format", "device", "_codes", "_scales", "_buffer", "_struct")
 
     def __init__(self, codes, scales, format: str):
+        import torch
         if format not in ACT8_FORMATS:
             raise ValueError("format is 'int8' or 'e4m3'")
-        self.codes, self.scales, self.format = codes, scales, format
+        if codes.dim() != 2 or not codes.is_cuda:
+            raise ValueError("codes is a CUDA tensor [rows, columns]")
+        rows, cols = codes.shape
+        blocks = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
+        c, ld_codes = _like("codes", codes, rows, cols, torch.uint8, codes.device)
+        s, ld_scales = _like("scales", scales, rows, blocks, torch.uint8, codes.device)
+        self.shape, self.format, self.device = codes.shape, format, codes.device
+        self._codes, self._scales, self._buffer = codes, scales, None
+        self._struct = rl_act8(c, s, ld_codes, ld_scales, ACT8_FORMATS[format])
 
     @property
-    def shape(self):
-        return self.codes.shape
+    def codes(self):
+        if self._codes is None:
+            rows, cols = self.shape
+            ld = self._struct.ld_codes
+            self._codes = self._buffer[:rows * ld].view(rows, ld)[:, :cols]
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            rows, first = self.shape[0], self.shape[0] * self._struct.ld_codes
+            self._scales = self._buffer[first:].view(rows, self._struct.ld_scales)
+        return self._scales
 
     @property
     def nbytes(self) -> int:
-        return self.codes.numel() + self.scales.numel()
+        rows, cols = self.shape
+        return rows * (cols + (cols + ACT8_BLOCK - 1) // ACT8_BLOCK)
 
 
 def act8_empty(rows: int, cols: int, format: str = "int8", device="cuda") -> Act8:
-    """Room for rows x cols activations in 8 bits, rows on 16-byte boundaries."""
+    """Room for rows x cols activations in 8 bits, rows of codes on 16-byte boundaries. (One allocation for both
+    tensors, which are made when they are asked for: a tensor costs some 5 us of host time beside a launch.)"""
     import torch
     if format not in ACT8_FORMATS:
         raise ValueError("format is 'int8' or 'e4m3'")
-    codes = torch.empty((rows, (cols + 15) & ~15), dtype=torch.uint8, device=device)
-    scales = torch.empty((rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK), dtype=torch.uint8, device=device)
-    return Act8(codes if cols % 16 == 0 else codes[:, :cols], scales, format)
+    if rows < 0 or cols < 1:
+        raise ValueError("an 8-bit checkpoint has a column at least")
+    ld, blocks = (cols + 15) & ~15, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
+    a = Act8.__new__(Act8)
+    a._buffer = torch.empty(rows * (ld + blocks), dtype=torch.uint8, device=device)
+    a.shape, a.format, a.device, a._codes, a._scales = (rows, cols), format, a._buffer.device, None, None
+    at = a._buffer.data_ptr()
+    a._struct = rl_act8(at, at + rows * ld, ld, blocks, ACT8_FORMATS[format])
+    return a
 
 
 def _act8_struct(a: Act8, rows: int, cols: int, device) -> rl_act8:
-    import torch
-    if not isinstance(a, Act8):
-        raise ValueError("an 8-bit checkpoint is a capi.Act8")
-    codes, ld_codes = _rows("codes", a.codes, rows, cols, torch.uint8, device)
-    scales, ld_scales = _rows("scales", a.scales, rows, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK, torch.uint8, device)
-    return rl_act8(codes, scales, ld_codes, ld_scales, ACT8_FORMATS[a.format])
+    if not isinstance(a, Act8) or a.shape[0] != rows or a.shape[1] != cols or a.device.index != device.index:
+        raise ValueError(f"an 8-bit checkpoint here is a capi.Act8 of [{rows}, {cols}] on {device}")
+    return a._struct
 
 
 def _float_code(name: str, dtype) -> int:
@@ -709,15 +734,19 @@ def layer_norm(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1
     if kind not in LN_KINDS:
         raise ValueError("kind is 'layer' or 'rms'")
     rows, cols, xt, px, ldx = _matrix("x", x)
-    dev, f32 = x.device, torch.float32
+    dev, xdt, f32 = x.device, x.dtype, torch.float32
     pt, pw, pb = _params(weight, bias, cols, dev)
     with _allocations_of(stream, dev):
         if y is None:
-            y = torch.empty((rows, cols), dtype=dtype or x.dtype, device=dev)
-        elif dtype is not None and y.dtype is not dtype:
-            raise ValueError("y has the type that dtype names")
+            y = torch.empty((rows, cols), dtype=dtype or xdt, device=dev)
+            py, ldy, ydt = y.data_ptr(), cols, y.dtype
+        else:
+            ydt = y.dtype
+            if dtype is not None and ydt is not dtype:
+                raise ValueError("y has the type that dtype names")
+            py, ldy = _like("y", y, rows, cols, ydt, dev)
         if summed is None and residual is not None:
-            summed = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+            summed = torch.empty((rows, cols), dtype=xdt, device=dev)
         if want_stats:
             if rstd is None:
                 rstd = torch.empty(rows, dtype=f32, device=dev)
@@ -727,15 +756,16 @@ def layer_norm(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1
             checkpoint = act8_empty(rows, cols, checkpoint, dev)
         if stream is None:
             stream = _current_stream(dev)
-    kept = None if checkpoint is None else ctypes.byref(_act8_struct(checkpoint, rows, cols, dev))
-    cfg = rl_ln_config(LN_KINDS[kind], cols, xt, _float_code("y", y.dtype), pt, eps)
+    pr, ldr = (None, 0) if residual is None else _like("residual", residual, rows, cols, xdt, dev)
+    ps, lds = (None, 0) if summed is None else _like("summed", summed, rows, cols, xdt, dev)
+    cfg = rl_ln_config(LN_KINDS[kind], cols, xt, xt if ydt is xdt else _float_code("y", ydt), pt, eps)
     with _on_device(dev):
-        _check(load().rl_loss_layer_norm(ctypes.byref(cfg), rows, px, ldx, *_like("residual", residual, rows, cols, x.dtype, dev),
-                                         pw, pb, _vector("mask", mask, rows, torch.uint8, dev, True),
-                                         *_like("y", y, rows, cols, y.dtype, dev),
-                                         *_like("summed", summed, rows, cols, x.dtype, dev), kept,
-                                         _vector("mean", mean, rows, f32, dev, True), _vector("rstd", rstd, rows, f32, dev, True),
-                                         _status_word(device_status, dev), stream),
+        _check(load().rl_loss_layer_norm(cfg, rows, px, ldx, pr, ldr, pw, pb,
+                                         None if mask is None else _vector("mask", mask, rows, torch.uint8, dev), py, ldy, ps, lds,
+                                         None if checkpoint is None else _act8_struct(checkpoint, rows, cols, dev),
+                                         None if mean is None else _vector("mean", mean, rows, f32, dev),
+                                         None if rstd is None else _vector("rstd", rstd, rows, f32, dev),
+                                         None if device_status is None else _status_word(device_status, dev), stream),
                "rl_loss_layer_norm")
     return {"y": y, "summed": summed, "mean": mean, "rstd": rstd, "checkpoint": checkpoint}
 
@@ -756,19 +786,22 @@ def layer_norm_backward(dy, weight, mean, rstd, *, x=None, checkpoint=None, kind
     if (x is None) == (checkpoint is None):
         raise ValueError("the norm's input comes as x or as a checkpoint")
     rows, cols, yt, pdy, lddy = _matrix("dy", dy)
-    dev, f32 = dy.device, torch.float32
+    dev, ydt, f32 = dy.device, dy.dtype, torch.float32
     if x is not None:
         if dtype is not None and dtype is not x.dtype:
             raise ValueError("dx has the type of x")
         dtype = x.dtype
     elif dtype is None:
-        dtype = dx.dtype if dx is not None else dy.dtype
+        dtype = dx.dtype if dx is not None else ydt
     pt, pw, pb = _params(weight, bias, cols, dev)
     if accumulate and ((want_dweight and dweight is None) or (want_dbias and dbias is None)):
         raise ValueError("pass the dweight and dbias that are added to")
     with _allocations_of(stream, dev):
         if dx is None:
             dx = torch.empty((rows, cols), dtype=dtype, device=dev)
+            pdx, lddx = dx.data_ptr(), cols
+        else:
+            pdx, lddx = _like("dx", dx, rows, cols, dtype, dev)
         if dweight is None and want_dweight:
             dweight = torch.empty(cols, dtype=f32, device=dev)
         if dbias is None and want_dbias:
@@ -777,17 +810,19 @@ def layer_norm_backward(dy, weight, mean, rstd, *, x=None, checkpoint=None, kind
             stream = _current_stream(dev)
         if workspace is None and (dweight is not None or dbias is not None):
             workspace = _post_workspace(rl_loss_layer_norm_workspace_bytes(rows, cols), dev, stream)
-    kept = None if checkpoint is None else ctypes.byref(_act8_struct(checkpoint, rows, cols, dev))
-    cfg = rl_ln_config(LN_KINDS[kind], cols, _float_code("dx", dtype), yt, pt, 0.0)
+    px, ldx = (None, 0) if x is None else _like("x", x, rows, cols, dtype, dev)
+    ps, lds = (None, 0) if dsummed is None else _like("dsummed", dsummed, rows, cols, dtype, dev)
+    py, ldy = (None, 0) if y is None else _like("y", y, rows, cols, ydt, dev)
+    pws, ws_bytes = (None, 0) if workspace is None else _workspace_of(workspace, dev)
+    cfg = rl_ln_config(LN_KINDS[kind], cols, yt if dtype is ydt else _float_code("dx", dtype), yt, pt, 0.0)
     with _on_device(dev):
         _check(load().rl_loss_layer_norm_backward(
-            ctypes.byref(cfg), rows, pdy, lddy, *_like("x", x, rows, cols, dtype, dev), kept, pw, pb,
-            _vector("mask", mask, rows, torch.uint8, dev, True), _vector("mean", mean, rows, f32, dev, kind == "rms"),
-            _vector("rstd", rstd, rows, f32, dev), *_like("dsummed", dsummed, rows, cols, dtype, dev),
-            *_like("dx", dx, rows, cols, dtype, dev), _vector("dweight", dweight, cols, f32, dev, True),
-            _vector("dbias", dbias, cols, f32, dev, True), int(accumulate), *_like("y", y, rows, cols, dy.dtype, dev),
-            *((None, 0) if workspace is None else _workspace_of(workspace, dev)), _status_word(device_status, dev), stream),
-            "rl_loss_layer_norm_backward")
+            cfg, rows, pdy, lddy, px, ldx, None if checkpoint is None else _act8_struct(checkpoint, rows, cols, dev), pw, pb,
+            None if mask is None else _vector("mask", mask, rows, torch.uint8, dev), _vector("mean", mean, rows, f32, dev, kind == "rms"),
+            _vector("rstd", rstd, rows, f32, dev), ps, lds, pdx, lddx,
+            None if dweight is None else _vector("dweight", dweight, cols, f32, dev),
+            None if dbias is None else _vector("dbias", dbias, cols, f32, dev), int(accumulate), py, ldy, pws, ws_bytes,
+            None if device_status is None else _status_word(device_status, dev), stream), "rl_loss_layer_norm_backward")
     return {"dx": dx, "dweight": dweight, "dbias": dbias, "y": y}
 
 
@@ -801,7 +836,7 @@ def act8_pack(x, *, format: str = "int8", out: Act8 | None = None, stream=None) 
     if stream is None:
         stream = _current_stream(dev)
     with _on_device(dev):
-        _check(load().rl_loss_act8_pack(xt, rows, cols, px, ldx, ctypes.byref(_act8_struct(out, rows, cols, dev)), stream),
+        _check(load().rl_loss_act8_pack(xt, rows, cols, px, ldx, _act8_struct(out, rows, cols, dev), stream),
                "rl_loss_act8_pack")
     return out
 
@@ -809,19 +844,19 @@ def act8_pack(x, *, format: str = "int8", out: Act8 | None = None, stream=None) 
 def act8_unpack(a: Act8, *, dtype=None, out=None, stream=None):
     """The activations that an Act8 stands for, as torch.bfloat16 (or `dtype`), in a new tensor or in `out`."""
     import torch
-    rows, cols = a.codes.shape
-    dev = a.codes.device
+    (rows, cols), dev = a.shape, a.device
     if out is None:
         with _allocations_of(stream, dev):
             out = torch.empty((rows, cols), dtype=dtype or torch.bfloat16, device=dev)
+        po, ldo = out.data_ptr(), cols
     elif dtype is not None and out.dtype is not dtype:
         raise ValueError("out has the type that dtype names")
+    else:
+        po, ldo = _like("out", out, rows, cols, out.dtype, dev)
     if stream is None:
         stream = _current_stream(dev)
     with _on_device(dev):
-        _check(load().rl_loss_act8_unpack(_float_code("out", out.dtype), rows, cols,
-                                          ctypes.byref(_act8_struct(a, rows, cols, dev)),
-                                          *_like("out", out, rows, cols, out.dtype, dev), stream),
+        _check(load().rl_loss_act8_unpack(_float_code("out", out.dtype), rows, cols, a._struct, po, ldo, stream),
                "rl_loss_act8_unpack")
     return out
 

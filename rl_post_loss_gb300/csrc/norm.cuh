@@ -12,6 +12,8 @@
 // of a column; a second launch adds the partial sums.
 #pragma once
 
+#include <atomic>
+
 #include "act8.cuh"
 
 namespace rlk {
@@ -78,6 +80,24 @@ RLK_NORM_ROWS(int8, f32);
 RLK_NORM_ROWS(e4m3, bf16);
 RLK_NORM_ROWS(e4m3, f32);
 #undef RLK_NORM_ROWS
+
+// Launches a kernel that may take `most` bytes of shared memory, which the driver is told once on a device (some 0.5 us of
+// host time).
+template <auto Kernel, typename... Args>
+cudaError_t run_kernel(int blocks, int threads, size_t smem, size_t most, cudaStream_t stream, Args... args) {
+    static std::atomic<uint64_t> told{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (!(told.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+        if (e != cudaSuccess) return e;
+        told.fetch_or(bit, std::memory_order_relaxed);
+    }
+    Kernel<<<blocks, threads, smem, stream>>>(args...);
+    return cudaGetLastError();
+}
 
 // ---------------------------------------------------------------- device helpers
 

@@ -245,13 +245,11 @@ cudaError_t launch_short(const NormBackwardParams &p, int blocks, cudaStream_t s
     const NormShort n = norm_short(p.cols, es, ld, 3, p.mask != nullptr, (size_t)width * 4, (size_t)kNormWarps * width * 4);
     const bool full = !p.rms || p.want_db;
     const bool exact = p.cols == width && !p.mask && !p.y.p && p.dx.fast;
-#define RLK_SHORT(V, F) (exact ? norm_backward_short_kernel<SRC, DYBF16, V, F, true> : norm_backward_short_kernel<SRC, DYBF16, V, F, false>)
-    const auto kernel = n.vecs == 2 ? full ? RLK_SHORT(2, true) : RLK_SHORT(2, false) : full ? RLK_SHORT(4, true) : RLK_SHORT(4, false);
+#define RLK_RUN(V, F, E) run_kernel<norm_backward_short_kernel<SRC, DYBF16, V, F, E>>(blocks, kThreads, n.smem, kNormRingSmem, stream, p, n)
+#define RLK_SHORT(V, F) (exact ? RLK_RUN(V, F, true) : RLK_RUN(V, F, false))
+    return n.vecs == 2 ? full ? RLK_SHORT(2, true) : RLK_SHORT(2, false) : full ? RLK_SHORT(4, true) : RLK_SHORT(4, false);
 #undef RLK_SHORT
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
-    if (e != cudaSuccess) return e;
-    kernel<<<blocks, kThreads, n.smem, stream>>>(p, n);
-    return cudaGetLastError();
+#undef RLK_RUN
 }
 
 constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 512;  // what a block takes beside its rows

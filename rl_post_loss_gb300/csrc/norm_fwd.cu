@@ -183,13 +183,11 @@ cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
     const NormShort n = norm_short(p.cols, es, ld, 2, p.mask != nullptr, (size_t)width * 8, 0);
     const bool full = !p.rms || p.b;
     const bool exact = p.cols == width && !p.mask && p.y.fast;
-#define RLK_SHORT(V, F) (exact ? norm_forward_short_kernel<BF16, V, F, true> : norm_forward_short_kernel<BF16, V, F, false>)
-    const auto kernel = n.vecs == 2 ? full ? RLK_SHORT(2, true) : RLK_SHORT(2, false) : full ? RLK_SHORT(4, true) : RLK_SHORT(4, false);
+#define RLK_RUN(V, F, E) run_kernel<norm_forward_short_kernel<BF16, V, F, E>>(std::min(p.rows, kNormSMs), kForwardWarps * 32, n.smem, kNormRingSmem, stream, p, n)
+#define RLK_SHORT(V, F) (exact ? RLK_RUN(V, F, true) : RLK_RUN(V, F, false))
+    return n.vecs == 2 ? full ? RLK_SHORT(2, true) : RLK_SHORT(2, false) : full ? RLK_SHORT(4, true) : RLK_SHORT(4, false);
 #undef RLK_SHORT
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
-    if (e != cudaSuccess) return e;
-    kernel<<<std::min(p.rows, kNormSMs), kForwardWarps * 32, n.smem, stream>>>(p, n);
-    return cudaGetLastError();
+#undef RLK_RUN
 }
 
 // A block per row, 16 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by
@@ -213,7 +211,7 @@ NormTeams teams_of(const NormForwardParams &p, int mode) {
     for (int v = 1; v <= 4; ++v) {
         const int warps = (vecs + 32 * v - 1) / (32 * v);
         if (warps > kForwardWarps || (v - 1) * warps * 32 >= vecs) continue;
-        if (n.warps && (mode == kAnyRow ? v == 4 : full && v == 4)) continue;  // (registers)
+        if (n.warps && (mode == kAnyRow ? v > 2 : full && v == 4)) continue;  // (registers)
         int blocks = kForwardWarps / warps;
         while (blocks > 1 && blocks * (kBlockExtra + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
         const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : 3));

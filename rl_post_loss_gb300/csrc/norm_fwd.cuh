@@ -74,7 +74,7 @@ __device__ __forceinline__ float variance(float sum, float squares, float inv_co
 template <bool BF16, int VPT, bool FULL, int MODE>
 __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(NormForwardParams p, NormTeams n) {
     constexpr int kTeams = MODE == kWarpRow ? kForwardWarps : 1;
-    constexpr bool kHeld = MODE != kAnyRow && VPT <= (FULL ? 3 : 4);
+    constexpr bool kHeld = VPT <= (MODE == kAnyRow ? 2 : FULL ? 3 : 4);
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) float2 s_sums[2][16];
     __shared__ __align__(8) uint64_t s_full[kTeams * kNormDepth];
@@ -236,11 +236,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
 
 template <bool BF16, int VPT, bool FULL, int MODE>
 cudaError_t launch_forward_rows(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
-    auto kernel = norm_forward_kernel<BF16, VPT, FULL, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
-    if (e != cudaSuccess) return e;
-    kernel<<<std::min(p.rows, kNormSMs * n.blocks_per_sm), MODE == kWarpRow ? kForwardWarps * 32 : n.warps * 32, n.smem, stream>>>(p, n);
-    return cudaGetLastError();
+    return run_kernel<norm_forward_kernel<BF16, VPT, FULL, MODE>>(std::min(p.rows, kNormSMs * n.blocks_per_sm), MODE == kWarpRow ? kForwardWarps * 32 : n.warps * 32, n.smem, kNormRingSmem, stream, p, n);
 }
 
 template <bool BF16, bool FULL, int MODE>

@@ -248,11 +248,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
 
 template <int SRC, bool DYBF16, int VPT, bool FULL, int MODE>
 cudaError_t launch_norm_ring(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream) {
-    auto kernel = norm_backward_ring_kernel<SRC, DYBF16, VPT, FULL, MODE>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
-    if (e != cudaSuccess) return e;
-    kernel<<<blocks, MODE == kWarpRow ? kNormWarps * 32 : n.warps * 32, n.smem, stream>>>(p, n);
-    return cudaGetLastError();
+    return run_kernel<norm_backward_ring_kernel<SRC, DYBF16, VPT, FULL, MODE>>(blocks, MODE == kWarpRow ? kNormWarps * 32 : n.warps * 32, n.smem, kNormRingSmem, stream, p, n);
 }
 
 template <int SRC, bool DYBF16>
