@@ -575,8 +575,8 @@ typedef struct rl_ln_config {
  * and a code for each column. The writer takes the smallest power of two that leaves
  * no value out of range (max |x| <= 127 2^e or 448 2^e, e >= -126) and rounds
  * x / 2^e to the nearest code, ties to even; the values that codes stand for are
- * exact in fp32 and in bf16 (a value that rounding takes past the largest finite one
- * reads as that one). A block that holds NaN or infinity reads back as NaN. 33 bytes
+ * exact in fp32 and, from 2^-133 up, in bf16 (a value that rounding takes past the
+ * largest finite one reads as that one). A block that holds NaN or infinity reads back as NaN. 33 bytes
  * for 32 values. */
 typedef enum rl_act8_format {
     RL_ACT8_INT8 = 0, /* two's complement, -127 .. 127: steps of one size in a block */
@@ -632,6 +632,36 @@ RL_LOSS_API rl_status rl_loss_act8_pack(int32_t x_dtype, int32_t rows, int32_t c
                                         const rl_act8 *out, void *stream);
 RL_LOSS_API rl_status rl_loss_act8_unpack(int32_t x_dtype, int32_t rows, int32_t cols, const rl_act8 *in, void *x,
                                           int64_t ld_x, void *stream);
+
+/* rl_loss_fused_projection_forward_backward with the model's last norm before it:
+ * hidden = norm(x), and instead of dL/dhidden the norm's gradients. hidden and its
+ * gradient exist for one chunk of rows at a time, in the workspace. x [T x ld_x]
+ * and dx (which may be x) are of config->x_dtype, config->cols is the hidden size and
+ * config->y_dtype RL_BF16. dweight and dbias [H] fp32 (or NULL) are overwritten,
+ * summed over the chunks in their order. Results are those of
+ * rl_loss_layer_norm, rl_loss_fused_projection_forward_backward and
+ * rl_loss_layer_norm_backward (the latter summed chunk by chunk). Everything else,
+ * and the errors, as there; the device status is the handle's. `workspace` as for
+ * rl_loss_layer_norm_backward, of rl_loss_normed_projection_workspace_bytes (which is
+ * 0 before rl_loss_projection_setup). */
+typedef struct rl_loss_final_norm {
+    const void *x;
+    int64_t ld_x;
+    const void *weight; /* [H] param_dtype, or NULL */
+    const void *bias;   /* [H] param_dtype, or NULL */
+    void *dx;
+    int64_t ld_dx;
+    float *dweight;     /* [H] or NULL */
+    float *dbias;       /* [H] or NULL */
+} rl_loss_final_norm;
+
+RL_LOSS_API size_t rl_loss_normed_projection_workspace_bytes(rl_loss_t handle);
+RL_LOSS_API rl_status rl_loss_normed_projection_forward_backward(rl_loss_t handle, const rl_ln_config *config,
+                                                                 const rl_loss_final_norm *norm, const void *w_lm,
+                                                                 int64_t ld_w, const rl_loss_inputs *inputs,
+                                                                 float *dw_lm, int64_t ld_dw,
+                                                                 const rl_loss_outputs *outputs, void *workspace,
+                                                                 size_t workspace_bytes, void *stream);
 
 /* Synchronises `stream`, returns the accumulated device status bits
  * (1u << code for each rl_status code raised) in *bits and clears them. */

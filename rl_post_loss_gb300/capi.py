@@ -100,6 +100,12 @@ class rl_act8(ctypes.Structure):
                 ("ld_scales", ctypes.c_int64), ("format", ctypes.c_int32)]
 
 
+class rl_loss_final_norm(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ld_x", ctypes.c_int64), ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("dx", ctypes.c_void_p), ("ld_dx", ctypes.c_int64), ("dweight", ctypes.c_void_p),
+                ("dbias", ctypes.c_void_p)]
+
+
 RL_LN_LAYER, RL_LN_RMS = 0, 1
 RL_ACT8_INT8, RL_ACT8_E4M3 = 0, 1
 LN_KINDS = {"layer": RL_LN_LAYER, "rms": RL_LN_RMS}
@@ -179,6 +185,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
                               st),
         "rl_loss_act8_unpack": ([ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(rl_act8), P, ctypes.c_int64,
                                  P], st),
+        "rl_loss_normed_projection_workspace_bytes": ([P], ctypes.c_size_t),
+        "rl_loss_normed_projection_forward_backward": ([P, ctypes.POINTER(rl_ln_config), ctypes.POINTER(rl_loss_final_norm), P,
+                                                        ctypes.c_int64, ctypes.POINTER(rl_loss_inputs), P, ctypes.c_int64,
+                                                        ctypes.POINTER(rl_loss_outputs), P, ctypes.c_size_t, P], st),
         "rl_loss_projection_logits": ([P, P, ctypes.c_int64, P, ctypes.c_int64, ctypes.c_int32, P, ctypes.c_int64,
                                        P], st),
         "rl_loss_fused_projection_forward_backward": ([P, P, ctypes.c_int64, P, ctypes.c_int64,
@@ -1005,6 +1015,47 @@ class RlLoss:
         self._raise(rl_loss_fused_projection_forward_backward(
             self.handle, _ptr(hidden), hidden.stride(0), _ptr(w_lm), w_lm.stride(0), inp, _ptr(dhidden),
             dhidden.stride(0), _ptr(dw_lm), dw_lm.stride(0), out, stream), "rl_loss_fused_projection_forward_backward")
+
+    def normed_projection_forward_backward(self, x, norm_weight, w_lm, targets, logp_old, logp_infer, mask, cu_seqlens,
+                                           rewards_or_adv, *, loss, dx, dw_lm, dnorm_weight=None, norm_bias=None,
+                                           dnorm_bias=None, kind: str = "rms", eps: float = 1e-5, loss_f64=None, logp=None,
+                                           entropy=None, flags=None, seq_adv=None, counts=None, mean_entropy=None,
+                                           workspace=None, stream=None) -> None:
+        """fused_projection_forward_backward of the model's last norm of x [T, hidden size] (kind "rms" or "layer"), whose output and
+        its gradient exist for one chunk of rows at a time. dx [T, hidden size] (may be x) is the gradient of x,
+        dnorm_weight and dnorm_bias [hidden size] fp32 those of the norm's parameters."""
+        import torch
+        if kind not in LN_KINDS:
+            raise ValueError("kind is 'layer' or 'rms'")
+        T, cols, xt, px, ldx = _matrix("x", x)
+        dev, f32, i32, u8, bf16 = x.device, torch.float32, torch.int32, torch.uint8, torch.bfloat16
+        S, V = cu_seqlens.numel() - 1, self.config.vocab_size
+        pt, pw, pb = _params(norm_weight, norm_bias, cols, dev)
+        pdx, lddx = _like("dx", dx, T, cols, x.dtype, dev)
+        w, ldw = _rows("w_lm", w_lm, V, cols, bf16, dev)
+        dw, lddw = _rows("dw_lm", dw_lm, V, cols, f32, dev)
+        inp = rl_loss_inputs(T, S, 0, None, _vector("targets", targets, T, i32, dev), _vector("logp_old", logp_old, T, f32, dev),
+                             _vector("logp_infer", logp_infer, T, f32, dev), _vector("mask", mask, T, u8, dev),
+                             _vector("cu_seqlens", cu_seqlens, S + 1, i32, dev),
+                             _vector("rewards_or_adv", rewards_or_adv, T if self.config.adv_mode >= RL_ADV_PER_TOKEN else S,
+                                     f32, dev))
+        out = rl_loss_outputs(_vector("loss", loss, 1, f32, dev), _vector("loss_f64", loss_f64, 1, torch.float64, dev, True),
+                              None, 0, _vector("logp", logp, T, f32, dev, True),
+                              _vector("entropy", entropy, T, f32, dev, True), _vector("flags", flags, T, u8, dev, True),
+                              _vector("seq_adv", seq_adv, S, f32, dev, True), _vector("counts", counts, 4, i32, dev, True),
+                              _vector("mean_entropy", mean_entropy, 1, f32, dev, True))
+        norm = rl_loss_final_norm(px, ldx, pw, pb, pdx, lddx, _vector("dnorm_weight", dnorm_weight, cols, f32, dev, True),
+                                  _vector("dnorm_bias", dnorm_bias, cols, f32, dev, True))
+        if stream is None:
+            stream = _current_stream(dev)
+        if workspace is None:
+            with _allocations_of(stream, dev):
+                workspace = _post_workspace(load().rl_loss_normed_projection_workspace_bytes(self.handle), dev, stream)
+        cfg = rl_ln_config(LN_KINDS[kind], cols, xt, RL_BF16, pt, eps)
+        code = load().rl_loss_normed_projection_forward_backward(self.handle, cfg, norm, w, ldw, inp, dw, lddw, out,
+                                                                 *_workspace_of(workspace, dev), stream)
+        if code:
+            self._raise(code, "rl_loss_normed_projection_forward_backward")
 
     def device_status(self, stream=None) -> int:
         import torch

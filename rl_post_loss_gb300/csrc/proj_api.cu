@@ -41,6 +41,44 @@ rl_status cuda_fail(rl_loss_handle_s *h, cudaError_t e) {
     return RL_ERR_CUDA;
 }
 
+// The norm before the projection, chunk by chunk: its output and that output's gradient are one chunk's.
+struct NormStage {
+    const rl_ln_config *config;
+    const rl_loss_final_norm *io;
+    char *hidden, *dhidden;  // [chunk x H] bf16
+    float *mean, *rstd;      // [chunk]
+    void *workspace;
+    size_t workspace_bytes;
+    uint32_t *status;
+
+    const char *x_row(int r) const { return static_cast<const char *>(io->x) + (size_t)r * io->ld_x * (config->x_dtype == RL_BF16 ? 2 : 4); }
+    rl_status forward(int r0, int m, void *stream) const {
+        return rl_loss_layer_norm(config, m, x_row(r0), io->ld_x, nullptr, 0, io->weight, io->bias, nullptr, hidden, config->cols,
+                                  nullptr, 0, nullptr, mean, rstd, status, stream);
+    }
+    rl_status backward(int r0, int m, bool add, void *stream) const {
+        char *dx = static_cast<char *>(io->dx) + (size_t)r0 * io->ld_dx * (config->x_dtype == RL_BF16 ? 2 : 4);
+        return rl_loss_layer_norm_backward(config, m, dhidden, config->cols, x_row(r0), io->ld_x, nullptr, io->weight, nullptr, nullptr,
+                                           mean, rstd, nullptr, 0, dx, io->ld_dx, io->dweight, io->dbias, add, nullptr, 0, workspace,
+                                           workspace_bytes, status, stream);
+    }
+};
+
+size_t norm_stage_layout(const rl_loss_handle_s *h, char *base, NormStage &n) {
+    const size_t rows = (size_t)h->proj_chunk, chunk = align_up(rows * h->proj_hidden * 2, 256), stats = align_up(rows * 4, 256);
+    n.hidden = base;
+    n.dhidden = base + chunk;
+    n.mean = reinterpret_cast<float *>(base + 2 * chunk);
+    n.rstd = reinterpret_cast<float *>(base + 2 * chunk + stats);
+    n.workspace = base + 2 * chunk + 2 * stats;
+    n.workspace_bytes = rl_loss_layer_norm_workspace_bytes(h->proj_chunk, h->proj_hidden);
+    return 2 * chunk + 2 * stats + n.workspace_bytes;
+}
+
+rl_status projection_pass(rl_loss_handle_s *h, const void *hidden, int64_t ld_hidden, const void *w_lm, int64_t ld_w,
+                          const rl_loss_inputs *in, void *dhidden, int64_t ld_dhidden, float *dw_lm, int64_t ld_dw,
+                          const rl_loss_outputs *out, const NormStage *norm, void *stream_ptr);
+
 }  // namespace
 
 extern "C" {
@@ -128,6 +166,70 @@ RL_LOSS_API rl_status rl_loss_fused_projection_forward_backward(
             (ld_hidden * 2) % 16 || (ld_w * 2) % 16 || (ld_dhidden * 2) % 16 || (ld_dw * 4) % 16)
             return RL_ERR_ALIGNMENT;
     }
+    return projection_pass(h, hidden, ld_hidden, w_lm, ld_w, in, dhidden, ld_dhidden, dw_lm, ld_dw, out, nullptr, stream_ptr);
+}
+
+RL_LOSS_API size_t rl_loss_normed_projection_workspace_bytes(rl_loss_t h) {
+    NormStage n{};
+    return h && h->proj_hidden ? norm_stage_layout(h, nullptr, n) : 0;
+}
+
+RL_LOSS_API rl_status rl_loss_normed_projection_forward_backward(rl_loss_t h, const rl_ln_config *config,
+                                                                 const rl_loss_final_norm *norm, const void *w_lm,
+                                                                 int64_t ld_w, const rl_loss_inputs *in, float *dw_lm,
+                                                                 int64_t ld_dw, const rl_loss_outputs *out,
+                                                                 void *workspace, size_t workspace_bytes,
+                                                                 void *stream_ptr) {
+    if (!h || !config || !norm || !in || !out) return RL_ERR_INVALID_ARG;
+    int cur = -1;
+    if (cudaGetDevice(&cur) != cudaSuccess || cur != h->device) return RL_ERR_DEVICE;
+    if (h->proj_hidden == 0) return RL_ERR_INVALID_ARG;
+    const rl_loss_config &c = h->cfg;
+    const int T = in->num_tokens, S = in->num_seqs, H = h->proj_hidden;
+    if (T < 0 || S < 1 || S % c.group_size != 0) return RL_ERR_SHAPE;
+    if (T > c.max_tokens || S > c.max_seqs) return RL_ERR_CAPACITY;
+    if (!in->cu_seqlens || !in->rewards_or_adv || !out->loss) return RL_ERR_INVALID_ARG;
+    if ((config->x_dtype != RL_F32 && config->x_dtype != RL_BF16) || (config->param_dtype != RL_F32 && config->param_dtype != RL_BF16) ||
+        config->y_dtype != RL_BF16)
+        return RL_ERR_DTYPE;
+    if (config->cols != H) return RL_ERR_SHAPE;
+    if (H > rl_loss_layer_norm_max_cols()) return RL_ERR_UNSUPPORTED;
+    if ((config->kind != RL_LN_LAYER && config->kind != RL_LN_RMS) || !(config->eps > 0.f) || !std::isfinite(config->eps))
+        return RL_ERR_INVALID_ARG;
+    NormStage n{};
+    n.config = config;
+    n.io = norm;
+    n.status = h->status;
+    if (T > 0) {
+        if (!norm->x || !norm->dx || !w_lm || !dw_lm || !workspace || !in->targets || !in->logp_old || !in->logp_infer || !in->mask ||
+            (norm->dweight && norm->dweight == norm->dbias) || (norm->x == norm->dx && norm->ld_x != norm->ld_dx))
+            return RL_ERR_INVALID_ARG;
+        if (norm->ld_x < H || norm->ld_dx < H || ld_w < H || ld_dw < H) return RL_ERR_SHAPE;
+        const uintptr_t es = config->x_dtype == RL_F32 ? 4 : 2, ps = config->param_dtype == RL_F32 ? 4 : 2;
+        const auto on = [](const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; };
+        if (!aligned16(w_lm) || !aligned16(dw_lm) || (ld_w * 2) % 16 || (ld_dw * 4) % 16 || !on(norm->x, es) || !on(norm->dx, es) ||
+            !on(norm->weight, ps) || !on(norm->bias, ps) || !on(norm->dweight, 4) || !on(norm->dbias, 4) || !on(workspace, 256))
+            return RL_ERR_ALIGNMENT;
+        if (workspace_bytes < norm_stage_layout(h, static_cast<char *>(workspace), n)) return RL_ERR_CAPACITY;
+    } else {
+        const rl_status st = rl_loss_layer_norm_backward(config, 0, nullptr, H, nullptr, H, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr,
+                                                         nullptr, 0, nullptr, H, norm->dweight, norm->dbias, 0, nullptr, 0, nullptr, 0, nullptr,
+                                                         stream_ptr);
+        if (st != RL_OK) return st;
+    }
+    return projection_pass(h, n.hidden, H, w_lm, ld_w, in, n.dhidden, H, dw_lm, ld_dw, out, &n, stream_ptr);
+}
+
+}  // extern "C"
+
+namespace {
+
+// The chunks of both entry points. With `norm`, hidden and dhidden are one chunk's buffers, filled and emptied by it.
+rl_status projection_pass(rl_loss_handle_s *h, const void *hidden, int64_t ld_hidden, const void *w_lm, int64_t ld_w,
+                          const rl_loss_inputs *in, void *dhidden, int64_t ld_dhidden, float *dw_lm, int64_t ld_dw,
+                          const rl_loss_outputs *out, const NormStage *norm, void *stream_ptr) {
+    const rl_loss_config &c = h->cfg;
+    const int T = in->num_tokens, S = in->num_seqs, V = c.vocab_size, H = h->proj_hidden;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_ptr);
 
     rlk::SeqPrepParams sp{};
@@ -158,7 +260,12 @@ RL_LOSS_API rl_status rl_loss_fused_projection_forward_backward(
     uint8_t *flags = out->flags ? out->flags : h->tok_flags;
     for (int r0 = 0, ci = 0; r0 < T; r0 += h->proj_chunk, ++ci) {
         const int m = T - r0 < h->proj_chunk ? T - r0 : h->proj_chunk;
-        const char *hc = reinterpret_cast<const char *>(hidden) + (size_t)r0 * ld_hidden * 2;
+        const char *hc = reinterpret_cast<const char *>(hidden) + (norm ? 0 : (size_t)r0 * ld_hidden * 2);
+        if (norm) {
+            const rl_status st = norm->forward(r0, m, stream_ptr);
+            if (st != RL_OK) return st == RL_ERR_CUDA ? cuda_fail(h, cudaPeekAtLastError()) : st;
+            launches += 1;
+        }
 
         rlk::GemmProblem fw{};
         fw.M = m;
@@ -238,7 +345,7 @@ RL_LOSS_API rl_status rl_loss_fused_projection_forward_backward(
         bw[0].b = rlk::GemmOperand{w_lm, ld_w, 1};
         bw[0].epi = rlk::GemmProblem::kBf16;
         bw[0].n_fastest = 0;  // pairs running at once share W's column blocks through L2
-        bw[0].d = reinterpret_cast<char *>(dhidden) + (size_t)r0 * ld_dhidden * 2;
+        bw[0].d = reinterpret_cast<char *>(dhidden) + (norm ? 0 : (size_t)r0 * ld_dhidden * 2);
         bw[0].ldd = ld_dhidden;
         bw[1].M = V;
         bw[1].N = H;
@@ -255,6 +362,11 @@ RL_LOSS_API rl_status rl_loss_fused_projection_forward_backward(
         h->prof_end(slot, stream);
         if (e != cudaSuccess) return cuda_fail(h, e);
         launches += 1;
+        if (norm) {
+            const rl_status st = norm->backward(r0, m, ci > 0, stream_ptr);
+            if (st != RL_OK) return st == RL_ERR_CUDA ? cuda_fail(h, cudaPeekAtLastError()) : st;
+            launches += norm->io->dweight || norm->io->dbias ? 2 : 1;
+        }
     }
 
     if (T == 0 && dw_lm) {  // no chunk ran: the weight gradient is zero
@@ -291,4 +403,4 @@ RL_LOSS_API rl_status rl_loss_fused_projection_forward_backward(
     return RL_OK;
 }
 
-}  // extern "C"
+}  // namespace
