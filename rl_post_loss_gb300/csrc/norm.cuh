@@ -101,6 +101,9 @@ cudaError_t run_kernel(int blocks, int threads, size_t smem, size_t most, cudaSt
 
 // ---------------------------------------------------------------- device helpers
 
+// The next launch, if it is one that waits for this one (grid_dependency_wait), may begin.
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 __device__ __forceinline__ V8 clipped(const V8 &a, int col, int cols) {
     float v[kVec];
     floats_of(a, v);
@@ -112,6 +115,8 @@ __device__ __forceinline__ float sum_of(f32x2 a) {
     unpack2(a, x, y);
     return x + y;
 }
+// A thread's sum, kept as two chains of pairs, as one would be waited for.
+__device__ __forceinline__ float sum_of(const f32x2 (&a)[2]) { return sum_of(add2(a[0], a[1])); }
 __device__ __forceinline__ V8 zeros() {
     V8 r;
     r.p[0] = r.p[1] = r.p[2] = r.p[3] = 0ull;

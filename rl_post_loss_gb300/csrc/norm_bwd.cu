@@ -10,7 +10,7 @@ namespace rlk {
 namespace {
 
 constexpr int kThreads = kNormWarps * 32;
-constexpr int kJoinCols = 32, kJoinRows = 8;
+constexpr int kJoin = 32;  // columns and warps of a block that adds partial sums
 
 // ---------------------------------------------------------------- short rows (norm_short.cuh)
 
@@ -30,6 +30,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
         ptx::fence_mbar_init();
     }
     __syncthreads();
+    grid_launch_dependents();
     ShortRing ring(n);
     ring.mask = p.mask;
     ring.base[0] = kAct8 ? reinterpret_cast<const char *>(p.ckpt.codes) : static_cast<const char *>(p.x.p);
@@ -93,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
         const char *sh = stages + s * n.stage_bytes + n.at[0] + slot * n.row_bytes[0], *sdy = stages + s * n.stage_bytes + n.at[1] + slot * n.row_bytes[1];
         const char *sds = stages + s * n.stage_bytes + n.at[2] + slot * n.row_bytes[2];
         const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
-        f32x2 s0 = 0ull, s1 = 0ull;
+        f32x2 s0[2] = {}, s1[2] = {};
         if (on) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -108,9 +109,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
                     dw[i].p[k] = fma2(r, d, dw[i].p[k]);
                     if (FULL) {
                         db[i].p[k] = add2(db[i].p[k], g.p[k]);
-                        s0 = add2(s0, u);
+                        s0[k & 1] = add2(s0[k & 1], u);
                     }
-                    s1 = fma2(u, d, s1);
+                    s1[k & 1] = fma2(u, d, s1[k & 1]);
                 }
             }
         }
@@ -197,25 +198,28 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
 
 // ---------------------------------------------------------------- the sum of the partial sums
 
-// Eight threads take every eighth partial sum of a column, their sums are added in turn.
-__global__ void __launch_bounds__(kJoinCols * kJoinRows) norm_join_kernel(const float *partials, int64_t ld, int parts, int cols, float *dw, float *db, int accumulate) {
-    __shared__ float s[kJoinRows][kJoinCols];
-    const int c = blockIdx.x * kJoinCols + threadIdx.x, k = threadIdx.y;
+// A block adds 32 columns' partial sums: warp k takes every 32nd one, a lane a column, ten loads under way at a time;
+// then warp c adds column c's 32 sums by a butterfly. (Eight warps, each thread a long chain of loads: 4096 x 6144 @@.)
+// The launch begins while the blocks before it still work, and waits for them.
+__global__ void __launch_bounds__(kJoin * kJoin) norm_join_kernel(const float *partials, int64_t ld, int parts, int cols, float *dw, float *db, int accumulate) {
+    __shared__ float s[kJoin][kJoin + 1];
+    const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, c = blockIdx.x * kJoin + lane;
     const int which = dw ? (int)blockIdx.y : 1;
     float *out = which ? db : dw;
     grid_dependency_wait();
     float v = 0.f;
     if (c < cols) {
-#pragma unroll 8
-        for (int i = k; i < parts; i += kJoinRows) v += partials[((int64_t)i * 2 + which) * ld + c];
+        const float *q = partials + which * ld + c;
+#pragma unroll 10
+        for (int i = k; i < parts; i += kJoin) v += q[(int64_t)i * 2 * ld];
     }
-    s[k][threadIdx.x] = v;
+    s[k][lane] = v;
     __syncthreads();
-    if (k == 0 && c < cols) {
+    v = s[lane][k];
 #pragma unroll
-        for (int i = 1; i < kJoinRows; ++i) v += s[i][threadIdx.x];
-        out[c] = accumulate ? out[c] + v : v;
-    }
+    for (int off = 16; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
+    const int mine = blockIdx.x * kJoin + k;
+    if (lane == 0 && mine < cols) out[mine] = accumulate ? out[mine] + v : v;
 }
 
 cudaError_t launch_join(const NormBackwardParams &p, int parts, cudaStream_t stream) {
@@ -224,8 +228,8 @@ cudaError_t launch_join(const NormBackwardParams &p, int parts, cudaStream_t str
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((p.cols + kJoinCols - 1) / kJoinCols, p.want_dw && p.want_db ? 2 : 1);
-    cfg.blockDim = dim3(kJoinCols, kJoinRows);
+    cfg.gridDim = dim3((p.cols + kJoin - 1) / kJoin, p.want_dw && p.want_db ? 2 : 1);
+    cfg.blockDim = dim3(kJoin * kJoin);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -242,7 +246,7 @@ cudaError_t launch_short(const NormBackwardParams &p, int blocks, cudaStream_t s
     const int es[3] = {from_act8(SRC) ? 1 : SRC == kHBf16 ? 2 : 4, DYBF16 ? 2 : 4, !p.dsummed.p ? 0 : p.dx.bf16 ? 2 : 4};
     const int64_t ld[3] = {from_act8(SRC) ? p.ckpt.ld_codes : p.x.ld, p.dy.ld, p.dsummed.ld};
     const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
-    const NormShort n = norm_short(p.cols, es, ld, 3, p.mask != nullptr, (size_t)width * 4, (size_t)kNormWarps * width * 4);
+    const NormShort n = norm_short(p.cols, es, ld, 3, p.mask != nullptr, kNormWarps, (size_t)width * 4, (size_t)kNormWarps * width * 4);
     const bool full = !p.rms || p.want_db;
     const bool exact = p.cols == width && !p.mask && !p.y.p && p.dx.fast;
 #define RLK_RUN(V, F, E) run_kernel<norm_backward_short_kernel<SRC, DYBF16, V, F, E>>(blocks, kThreads, n.smem, kNormRingSmem, stream, p, n)

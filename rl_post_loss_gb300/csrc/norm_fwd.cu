@@ -6,22 +6,24 @@ namespace rlk {
 
 namespace {
 
+constexpr int kShortWarps = 24;  // 80 registers a thread
+
 // ---------------------------------------------------------------- short rows (norm_short.cuh)
 
 // EXACT: the threads' vectors are the row's columns to the last one, no mask, and rows of y on 16-byte boundaries.
 template <bool BF16, int VPT, bool FULL, bool EXACT>
-__global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kernel(NormForwardParams p, NormShort n) {
+__global__ void __launch_bounds__(kShortWarps * 32, 1) norm_forward_short_kernel(NormForwardParams p, NormShort n) {
     extern __shared__ __align__(128) char smem[];
-    __shared__ __align__(8) uint64_t s_full[kForwardWarps * kNormDepth];
+    __shared__ __align__(8) uint64_t s_full[kShortWarps * kNormDepth];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, lanes = n.lanes, t = lane & (lanes - 1), slot = lane / lanes, S = n.depth;
     const int width = lanes * VPT * kVec;
     float *w_smem = reinterpret_cast<float *>(smem + n.smem) - 2 * width, *b_smem = w_smem + width;
-    for (int c = threadIdx.x; c < width; c += kForwardWarps * 32) {
+    for (int c = threadIdx.x; c < width; c += kShortWarps * 32) {
         w_smem[c] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
         b_smem[c] = c < p.cols && p.b ? load_param(p.b, p.params_bf16, c) : 0.f;
     }
     if (threadIdx.x == 0) {
-        for (int k = 0; k < kForwardWarps * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
+        for (int k = 0; k < kShortWarps * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
         ptx::fence_mbar_init();
     }
     __syncthreads();
@@ -39,7 +41,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kern
     ring.full = ptx::smem_u32(&s_full[warp * S]);
     ring.lane = lane;
     ring.per = 32 / lanes;
-    const int64_t first = blockIdx.x + (int64_t)warp * gridDim.x, step = (int64_t)gridDim.x * kForwardWarps;
+    const int64_t first = blockIdx.x + (int64_t)warp * gridDim.x, step = (int64_t)gridDim.x * kShortWarps;
     const int64_t batches = ((int64_t)p.rows + ring.per - 1) / ring.per;
     for (int s = 0; s < S; ++s)
         if (first + s * step < batches) ring.fetch(first + s * step, s);
@@ -96,7 +98,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_short_kern
                     if ((vec & 3) == 0) p.ckpt.scales[row * p.ckpt.ld_scales + (vec >> 2)] = (uint8_t)b;
                 }
             }
-        float b = sum_of(!FULL || p.rms ? s1 : s0), mean = 0.f, var;
+        float b = !FULL || p.rms ? sum_of(s1) : sum_of(s0), mean = 0.f, var;
         for (int off = lanes >> 1; off > 0; off >>= 1) b = __fadd_rn(b, __shfl_xor_sync(0xffffffffu, b, off));
         if (!FULL || p.rms) {
             var = b * p.inv_cols;
@@ -180,10 +182,10 @@ cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
     const int es[2] = {BF16 ? 2 : 4, !p.residual.p ? 0 : BF16 ? 2 : 4};
     const int64_t ld[2] = {p.x.ld, p.residual.ld};
     const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
-    const NormShort n = norm_short(p.cols, es, ld, 2, p.mask != nullptr, (size_t)width * 8, 0);
+    const NormShort n = norm_short(p.cols, es, ld, 2, p.mask != nullptr, kShortWarps, (size_t)width * 8, 0);
     const bool full = !p.rms || p.b;
     const bool exact = p.cols == width && !p.mask && p.y.fast;
-#define RLK_RUN(V, F, E) run_kernel<norm_forward_short_kernel<BF16, V, F, E>>(std::min(p.rows, kNormSMs), kForwardWarps * 32, n.smem, kNormRingSmem, stream, p, n)
+#define RLK_RUN(V, F, E) run_kernel<norm_forward_short_kernel<BF16, V, F, E>>(std::min(p.rows, kNormSMs), kShortWarps * 32, n.smem, kNormRingSmem, stream, p, n)
 #define RLK_SHORT(V, F) (exact ? RLK_RUN(V, F, true) : RLK_RUN(V, F, false))
     return n.vecs == 2 ? full ? RLK_SHORT(2, true) : RLK_SHORT(2, false) : full ? RLK_SHORT(4, true) : RLK_SHORT(4, false);
 #undef RLK_SHORT

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
             phases ^= 1u << s;
             const char *sx = stages + s * n.stage_bytes, *sr = sx + n.at_dy;
             if (MODE == kAnyRow) sx += row_shift<MODE>(x_row(row)), sr += row_shift<MODE>(r_row(row));
-            f32x2 s0 = 0ull, s1 = 0ull;
+            f32x2 s0[2] = {}, s1[2] = {};
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 v[i] = zeros();
@@ -147,12 +147,12 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (!FULL || p.rms)
-                        s1 = fma2(v[i].p[k], v[i].p[k], s1);
+                        s1[k & 1] = fma2(v[i].p[k], v[i].p[k], s1[k & 1]);
                     else
-                        s0 = add2(s0, v[i].p[k]);
+                        s0[k & 1] = add2(s0[k & 1], v[i].p[k]);
                 }
             }
-            float a = 0.f, b = sum_of(!FULL || p.rms ? s1 : s0), mean = 0.f, var;
+            float a = 0.f, b = !FULL || p.rms ? sum_of(s1) : sum_of(s0), mean = 0.f, var;
             team_sums<false, MODE == kWarpRow>(a, b, s_sums[turn], T >> 5);
             turn ^= 1;
             if (MODE == kWarpRow) __syncwarp();
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
             } else {
                 mean = b * p.inv_cols;
                 const f32x2 nm = pack2(-mean, -mean);
-                s0 = s1 = 0ull;
+                s0[0] = s0[1] = s1[0] = s1[1] = 0ull;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     if (at.none(i)) continue;
@@ -178,8 +178,8 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
                     if (i == VPT - 1 && at.cut) v[i] = at.cut_off(v[i], i);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        s0 = add2(s0, v[i].p[k]);
-                        s1 = fma2(v[i].p[k], v[i].p[k], s1);
+                        s0[k & 1] = add2(s0[k & 1], v[i].p[k]);
+                        s1[k & 1] = fma2(v[i].p[k], v[i].p[k], s1[k & 1]);
                     }
                 }
                 a = sum_of(s0), b = sum_of(s1);

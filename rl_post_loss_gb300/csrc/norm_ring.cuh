@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         ptx::fence_mbar_init();
     }
     __syncthreads();
+    grid_launch_dependents();
     const uint32_t full0 = ptx::smem_u32(&s_full[team * S]);
 
     const int64_t first = blockIdx.x + (int64_t)team * gridDim.x, step = (int64_t)kTeams * gridDim.x;
@@ -143,7 +144,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                 if (p.status) raise_status(p.status, RL_ERR_TIMEOUT);
             }
             phases ^= 1u << s;
-            f32x2 s0 = 0ull, s1 = 0ull;
+            f32x2 s0[2] = {}, s1[2] = {};
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (at.none(i)) continue;
@@ -156,9 +157,9 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                     dw[i].p[k] = fma2(r, d, dw[i].p[k]);
                     if (FULL) {
                         db[i].p[k] = add2(db[i].p[k], g.p[k]);
-                        s0 = add2(s0, u);
+                        s0[k & 1] = add2(s0[k & 1], u);
                     }
-                    s1 = fma2(u, d, s1);
+                    s1[k & 1] = fma2(u, d, s1[k & 1]);
                 }
             }
             c1 = sum_of(s0), c2 = sum_of(s1);
@@ -204,8 +205,8 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                 if (p.y.p) at.store(p.y, row, i, zeros());
             }
         }
-        if (MODE != kWarpRow && S == 1) {
-            __syncthreads();
+        if (S == 1) {
+            if (MODE == kWarpRow) __syncwarp(); else __syncthreads();
             if (t == 0 && row + step < p.rows && on_next && !dead) copy_row(row + step, 0);
         }
         on = on_next, mean = mean_next, rstd = rstd_next;

@@ -21,7 +21,7 @@ struct NormShort {
 };
 
 // `row_bytes`, `ld_bytes` of the matrices; `fixed` bytes of a block's shared memory for something else, after the rings.
-inline NormShort norm_short(int cols, const int *es, const int64_t *ld, int count, bool masked, size_t fixed, size_t least) {
+inline NormShort norm_short(int cols, const int *es, const int64_t *ld, int count, bool masked, int warps, size_t fixed, size_t least) {
     NormShort n{};
     n.vecs = cols <= 64 ? 2 : 4;
     n.lanes = cols <= 128 ? 4 : cols <= 256 ? 8 : 16;
@@ -32,9 +32,9 @@ inline NormShort norm_short(int cols, const int *es, const int64_t *ld, int coun
         n.at[k] = n.stage_bytes;
         n.stage_bytes += 32 / n.lanes * n.row_bytes[k];
     }
-    n.depth = (int)((kNormRingSmem - fixed) / ((size_t)kNormWarps * n.stage_bytes));
+    n.depth = (int)((kNormRingSmem - fixed) / ((size_t)warps * n.stage_bytes));
     n.depth = n.depth > kNormDepth ? kNormDepth : n.depth;
-    n.smem = (size_t)kNormWarps * n.depth * n.stage_bytes;
+    n.smem = (size_t)warps * n.depth * n.stage_bytes;
     n.smem = (n.smem > least ? n.smem : least) + fixed;
     return n;
 }

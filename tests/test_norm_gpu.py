@@ -32,6 +32,11 @@ def cases():
     for cols, rows in ((64, 30000), (128, 25000), (512, 9000), (640, 5000), (776, 5000), (1024, 5000), (2056, 2000), (4096, 1300), (6144, 1000)):
         out.append((cols, rows, "layer", BF16, BF16, F32, "pad", True, False, None))
         out.append((cols, rows, "rms", F32, F32, F32, "pad", False, True, "int8"))
+
+    # fp32 rows of which a warp's part of shared memory holds one or two, from the rows themselves
+    for cols, res in ((1024, False), (1024, True), (776, True), (640, True), (512, True), (256, True)):
+        out.append((cols, 6000, "rms", F32, F32, F32, "pad", res, res, None))
+        out.append((cols, 6000, "layer", F32, F32, F32, "pad16", res, False, None))
     return out
 
 
