@@ -558,7 +558,8 @@ RL_LOSS_API rl_status rl_loss_preference(const rl_loss_pref_config *config, int3
  * allocated, no call synchronises, every call can be captured into a CUDA graph;
  * argument errors are returned before anything is launched. `device_status`
  * (optional, device uint32) receives RL_ERR_NONFINITE when a row's statistics, or
- * the sums of its backward pass, are not finite. */
+ * the sums of its backward pass, are not finite, and RL_ERR_TIMEOUT if a bounded
+ * wait inside a kernel ran out (results are then not valid). */
 typedef enum rl_ln_kind { RL_LN_LAYER = 0, RL_LN_RMS = 1 } rl_ln_kind;
 
 typedef struct rl_ln_config {

@@ -691,9 +691,9 @@ def _matrix(name: str, t):
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} is a CUDA tensor [rows, columns]")
     (rows, cols), (ld, step) = t.shape, t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"the rows of {name} are contiguous")
-    return rows, cols, _float_code(name, t.dtype), t.data_ptr(), max(ld, cols)
+    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"the rows of {name} are contiguous and do not overlap")
+    return rows, cols, _float_code(name, t.dtype), t.data_ptr(), ld if rows > 1 else cols
 
 
 def _like(name: str, t, rows: int, cols: int, dtype, device):
@@ -702,9 +702,9 @@ def _like(name: str, t, rows: int, cols: int, dtype, device):
         return None, 0
     if t.dtype is dtype and t.dim() == 2 and t.get_device() == device.index:
         (have, width), (ld, step) = t.shape, t.stride()
-        if have == rows and width == cols and (step == 1 or cols == 1):
-            return t.data_ptr(), max(ld, cols)
-    raise ValueError(f"{name} is a {dtype} tensor [{rows}, {cols}] with contiguous rows on {device}")
+        if have == rows and width == cols and (step == 1 or cols == 1) and (ld >= cols or rows < 2):
+            return t.data_ptr(), ld if rows > 1 else cols
+    raise ValueError(f"{name} is a {dtype} tensor [{rows}, {cols}] with contiguous rows that do not overlap on {device}")
 
 
 def _params(weight, bias, cols: int, device):

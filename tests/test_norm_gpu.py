@@ -252,6 +252,29 @@ def test_every_row_masked(cols):
     assert all((g[k] == 0).all() for k in ("dx", "dweight", "dbias"))
 
 
+def test_broadcast_rows_are_refused_and_single_rows_take_any_stride():
+    x, dy, _, w, b = one(4, 200)
+    f = capi.layer_norm(x, w, b, want_stats=True)
+    row = x[:1]
+    for bad in (lambda: capi.layer_norm(row.expand(4, 200), w, b), lambda: capi.layer_norm(x, w, b, residual=row.expand(4, 200)),
+                lambda: capi.layer_norm_backward(row.expand(4, 200), w, f["mean"], f["rstd"], x=x),
+                lambda: capi.layer_norm_backward(dy, w, f["mean"], f["rstd"], x=x, dsummed=row.expand(4, 200)),
+                lambda: capi.act8_pack(row.expand(4, 200)), lambda: capi.layer_norm(x.as_strided((3, 200), (100, 1)), w, b)):
+        with pytest.raises(ValueError, match="overlap"):
+            bad()
+    alone = x.as_strided((1, 200), (7, 1))
+    assert nh.same(capi.layer_norm(alone, w, b)["y"], f["y"][:1])
+    column = torch.randn((30, 9), device="cuda")[:, 4:5]
+    assert nh.same(capi.layer_norm(column, kind="rms")["y"], capi.layer_norm(column.clone(), kind="rms")["y"])
+
+
+def test_summed_without_a_residual():
+    x, _, _, w, b = one(20, 640, BF16)
+    s = torch.empty_like(x)
+    got = capi.layer_norm(x, w, b, summed=s)
+    assert got["summed"] is s and nh.same(s, x) and nh.same(got["y"], capi.layer_norm(x, w, b)["y"])
+
+
 def test_no_rows():
     x = torch.empty((0, 640), device="cuda")
     w = torch.ones(640, device="cuda")
