@@ -124,23 +124,25 @@ __device__ __forceinline__ V8 zeros() {
 }
 
 // The sums over a block's warps (or, with WARP, over the warp) of two values (BOTH) or of the second one: a
-// butterfly in each warp, which for two values first gives each half of the warp one of them; then the warps'
-// sums, in their order, from shared memory (`buf`: 16 places, the unused ones 0; two buffers in turn, as a
-// thread may still read the last one while another writes the next). Every thread gets the same bits.
-template <bool BOTH, bool WARP>
-__device__ __forceinline__ void team_sums(float &a, float &b, float2 *buf, int warps) {
+// butterfly in each warp, which for two values first gives each half of the warp one of them; then another
+// over the warps' sums from shared memory (`buf`: 16 places, the unused ones 0; two buffers in turn, as a thread may
+// still read the last one while another writes the next). Every thread gets the same bits.
+template <bool BOTH>
+__device__ __forceinline__ float warp_sums(float a, float b) {  // BOTH: a's sum in lanes 0 to 15, b's in the others
     const int lane = threadIdx.x & 31;
-    float v;
+    float v = b;
     if (BOTH) {
         const float give = lane < 16 ? b : a, keep = lane < 16 ? a : b;
         v = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, 16));
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
-    } else {
-        v = b;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
     }
+#pragma unroll
+    for (int off = BOTH ? 8 : 16; off > 0; off >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+template <bool BOTH, bool WARP>
+__device__ __forceinline__ void team_sums(float &a, float &b, float2 *buf, int warps) {
+    const int lane = threadIdx.x & 31;
+    const float v = warp_sums<BOTH>(a, b);
     if (WARP) {
         if (BOTH) a = __shfl_sync(0xffffffffu, v, 0);
         b = BOTH ? __shfl_sync(0xffffffffu, v, 16) : v;
@@ -148,15 +150,18 @@ __device__ __forceinline__ void team_sums(float &a, float &b, float2 *buf, int w
     }
     if (BOTH ? (lane & 15) == 0 : lane == 0) reinterpret_cast<float *>(buf + (threadIdx.x >> 5))[BOTH ? lane >> 4 : 1] = v;
     __syncthreads();
-    const float4 *q = reinterpret_cast<const float4 *>(buf);
-    a = b = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (k == 4 && warps <= 8) break;
-        const float4 x = q[k];
-        if (BOTH) a += x.x + x.z;
-        b += x.y + x.w;
+    float2 x = buf[lane & (warps > 8 ? 15 : 7)];
+    if (warps > 8) {
+        if (BOTH) x.x = __fadd_rn(x.x, __shfl_xor_sync(0xffffffffu, x.x, 8));
+        x.y = __fadd_rn(x.y, __shfl_xor_sync(0xffffffffu, x.y, 8));
     }
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) {
+        if (BOTH) x.x = __fadd_rn(x.x, __shfl_xor_sync(0xffffffffu, x.x, off));
+        x.y = __fadd_rn(x.y, __shfl_xor_sync(0xffffffffu, x.y, off));
+    }
+    if (BOTH) a = x.x;
+    b = x.y;
 }
 
 __device__ __forceinline__ void load_params(const void *p, int bf16, int fast, int col, int cols, float (&v)[kVec]) {

@@ -56,7 +56,7 @@ __device__ __forceinline__ V8 add_residual(V8 x, const V8 &r) {
 
 // What follows from a row's sums: the statistics are written by one thread.
 __device__ __forceinline__ float finish_stats(const NormForwardParams &p, int64_t row, bool one, float mean, float var) {
-    const float rstd = __frsqrt_rn(var + p.eps);
+    const float rstd = rsqrtf(var + p.eps);  // within 2 units in the last place
     if (one) {
         if (!(var < INFINITY) && p.status) raise_status(p.status, RL_ERR_NONFINITE);
         if (p.mean) p.mean[row] = mean;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
                         s0[k & 1] = add2(s0[k & 1], v[i].p[k]);
                 }
             }
-            float a = 0.f, b = !FULL || p.rms ? sum_of(s1) : sum_of(s0), mean = 0.f, var;
+            float a = 0.f, b = !FULL || p.rms ? sum_of(s1) : sum_of(s0), mean = 0.f, rest = 0.f, var;
             team_sums<false, MODE == kWarpRow>(a, b, s_sums[turn], T >> 5);
             turn ^= 1;
             if (MODE == kWarpRow) __syncwarp();
@@ -185,22 +185,16 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
                 a = sum_of(s0), b = sum_of(s1);
                 team_sums<true, MODE == kWarpRow>(a, b, s_sums[turn], T >> 5);
                 turn ^= 1;
-                float rest;
                 var = variance(a, b, p.inv_cols, rest);
                 mean += rest;
-                const f32x2 nr = pack2(-rest, -rest);
-#pragma unroll
-                for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) v[i].p[k] = add2(v[i].p[k], nr);
             }
             const float rstd = finish_stats(p, row, t == 0, mean, var);
-            const f32x2 rs = pack2(rstd, rstd);
+            const f32x2 rs = pack2(rstd, rstd), off = pack2(-rest * rstd, -rest * rstd);  // (v - rest) rstd in one step
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (at.none(i)) continue;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], rs);
+                for (int k = 0; k < 4; ++k) v[i].p[k] = FULL ? fma2(v[i].p[k], rs, off) : mul2(v[i].p[k], rs);
                 const V8 w = kHeld ? w_held[kHeld ? i : 0] : at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
                 if (FULL) {
                     const V8 c = kHeld ? b_held[kHeld && FULL ? i : 0] : at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
