@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
             w_held[kHeld ? i : 0] = at.none(i) ? zeros() : at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
             if (FULL) b_held[kHeld && FULL ? i : 0] = at.none(i) ? zeros() : at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
         }
+    const bool plain = p.y.fast && (p.y.bf16 != 0) == BF16;
     uint32_t phases = 0;  // of the stages' barriers
     bool dead = false, on = first < p.rows && (!p.mask || p.mask[first]);
     int s = 0, turn = 0;
@@ -189,6 +190,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
                 mean += rest;
             }
             const float rstd = finish_stats(p, row, t == 0, mean, var);
+            char *y_row = static_cast<char *>(p.y.p) + row * p.y.ld * (BF16 ? 2 : 4);
             const f32x2 rs = pack2(rstd, rstd), off = pack2(-rest * rstd, -rest * rstd);  // (v - rest) rstd in one step
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -204,7 +206,10 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], w.p[k]);
                 }
-                at.store(p.y, row, i, v[i]);
+                if (MODE != kAnyRow && plain)
+                    at.template store_plain<BF16>(y_row, p.y.fast, i, v[i]);
+                else
+                    at.store(p.y, row, i, v[i]);
             }
         } else {
             if (more && !dead) copy_row(row_more, s);

@@ -33,6 +33,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     const int T = MODE == kWarpRow ? 32 : (int)blockDim.x, team = MODE == kWarpRow ? (int)threadIdx.x >> 5 : 0;
     const int t = MODE == kWarpRow ? (int)threadIdx.x & 31 : (int)threadIdx.x, S = n.depth;
     Columns<MODE, VPT> at(t, T, p.cols);
+    const bool plain = p.dx.fast;
     const bool x_bf16 = kAct8 ? p.dx.bf16 : SRC == kHBf16;
     char *stages = smem + team * S * n.stage_bytes;
     if (threadIdx.x < 32) (&s_sums[0][0])[threadIdx.x] = make_float2(0.f, 0.f);
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         if (MODE == kWarpRow) __syncwarp();
         if (more && !dead) copy_row(row_more, last);
         const f32x2 o1 = pack2(-c1, -c1), nk = pack2(-c2, -c2);
+        char *dx_row = static_cast<char *>(p.dx.p) + row * p.dx.ld * (x_bf16 ? 2 : 4);
         if (on) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
@@ -196,7 +198,12 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                     for (int k = 0; k < 4; ++k) u.p[k] = fma2(mul2(add2(h.p[k], nm), rs), ww.p[k], u.p[k]);
                     at.store(p.y, row, i, u);
                 }
-                at.store(p.dx, row, i, r);
+                if (MODE == kAnyRow || !plain)
+                    at.store(p.dx, row, i, r);
+                else if (x_bf16)
+                    at.template store_plain<true>(dx_row, 1, i, r);
+                else
+                    at.template store_plain<false>(dx_row, p.dx.fast, i, r);
             }
         } else {
             for (int i = 0; i < VPT; ++i) {

@@ -83,6 +83,19 @@ struct Columns {
             if (col(i, j) >= cols) v[j] = 0.f;
         return pairs_of(v);
     }
+    // A row of which `plain` (its type is BF16's, rows on 16-byte boundaries) was found out once for all rows.
+    template <bool BF16>
+    __device__ __forceinline__ void store_plain(void *row, int fast, int i, const V8 &a) const {
+        float v[kVec];
+        floats_of(a, v);
+        const int at = vec(i) * kVec, end = i == VPT - 1 && cut ? cols : at + kVec;
+        if (BF16)
+            store_vec(static_cast<__nv_bfloat16 *>(row), at, end, true, v);
+        else if (fast == 2 && at + kVec <= end)
+            store_vec32(static_cast<float *>(row), at, v);
+        else
+            store_vec(static_cast<float *>(row), at, end, true, v);
+    }
     __device__ __forceinline__ void store(const RowMat &m, int64_t row, int i, const V8 &a) const {
         float v[kVec];
         floats_of(a, v);
