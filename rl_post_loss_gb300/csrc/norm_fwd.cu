@@ -192,8 +192,10 @@ cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
 #undef RLK_RUN
 }
 
-// A block per row, 16 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by
-// a row's time of its vectors and two or three more for its exchanges of sums.
+// A block per row, 16 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by a
+// row's time of its vectors and two or three more for its exchanges of sums and what else is done once a row. (16384 x
+// 8192 bf16: layer norm with two, three, four vectors 141, 147, 136 us, RMS with a residual 180, 174, 181; 20000 x 5120: 156, 92,
+// 108 us; so layer norm with four, whose weights are read from shared memory, counts as 9.8.)
 NormTeams teams_of(const NormForwardParams &p, int mode) {
     const int vecs = (p.cols + kVec - 1) / kVec, pad = mode == kAnyRow ? 16 : 0;
     const bool full = !p.rms || p.b;
@@ -213,15 +215,20 @@ NormTeams teams_of(const NormForwardParams &p, int mode) {
     for (int v = 1; v <= 4; ++v) {
         const int warps = (vecs + 32 * v - 1) / (32 * v);
         if (warps > kForwardWarps || (v - 1) * warps * 32 >= vecs) continue;
-        if (n.warps && (mode == kAnyRow ? v > 2 : full && v == 4)) continue;  // (registers)
+        if (n.warps && mode == kAnyRow && v > 2) continue;  // (registers)
+        // layer norm with four vectors a thread: weight and bias in shared memory, as registers have no room
+        size_t params = mode != kAnyRow && full && v == 4 ? (size_t)2 * v * warps * 32 * kVec * 4 : 0;
         int blocks = kForwardWarps / warps;
-        while (blocks > 1 && blocks * (kBlockExtra + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
-        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : 3));
+        while (blocks > 1 && blocks * (kBlockExtra + params + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
+        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : v == 4 ? 5.8 : 3));
         if (n.warps && time >= best) continue;
         best = time;
+        const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks - kBlockExtra);
+        n.w_in_smem = params + n.stage_bytes <= room;
+        if (!n.w_in_smem) params = 0;
         n.warps = warps, n.vecs = v, n.blocks_per_sm = blocks;
-        n.depth = (int)std::min<size_t>(kNormDepth, std::min(kNormRingSmem, kSmemOfSM / blocks - kBlockExtra) / n.stage_bytes);
-        n.smem = (size_t)n.depth * n.stage_bytes;
+        n.depth = (int)std::min<size_t>(kNormDepth, (room - params) / n.stage_bytes);
+        n.smem = (size_t)n.depth * n.stage_bytes + params;
     }
     return n;
 }

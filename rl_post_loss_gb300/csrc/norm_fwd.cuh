@@ -119,6 +119,23 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
             w_held[kHeld ? i : 0] = at.none(i) ? zeros() : at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
             if (FULL) b_held[kHeld && FULL ? i : 0] = at.none(i) ? zeros() : at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
         }
+    // else in shared memory as fp32, a thread's own beside one another, where that fits
+    float *w_smem = reinterpret_cast<float *>(smem + kTeams * S * n.stage_bytes), *b_smem = w_smem + VPT * T * kVec;
+    if (!kHeld && MODE == kBlockRow && n.w_in_smem)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if (at.none(i)) continue;
+            float f[kVec];
+            floats_of(at.params(p.w, p.params_bf16, p.params_fast, i, 1.f), f);
+            store_vec(w_smem, at.vec(i) * kVec, at.vec(i) * kVec + kVec, true, f);
+            floats_of(at.params(p.b, p.params_bf16, p.params_fast, i, 0.f), f);
+            store_vec(b_smem, at.vec(i) * kVec, at.vec(i) * kVec + kVec, true, f);
+        }
+    const auto param = [&](const V8 &held, const void *q, const float *q_smem, int i, float missing) -> V8 {
+        if (kHeld) return held;
+        if (MODE == kBlockRow && n.w_in_smem) return read_vec<false>(reinterpret_cast<const char *>(q_smem), at.vec(i));
+        return at.params(q, p.params_bf16, p.params_fast, i, missing);
+    };
     const bool plain = p.y.fast && (p.y.bf16 != 0) == BF16;
     uint32_t phases = 0;  // of the stages' barriers
     bool dead = false, on = first < p.rows && (!p.mask || p.mask[first]);
@@ -197,9 +214,9 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
                 if (at.none(i)) continue;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[i].p[k] = FULL ? fma2(v[i].p[k], rs, off) : mul2(v[i].p[k], rs);
-                const V8 w = kHeld ? w_held[kHeld ? i : 0] : at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
+                const V8 w = param(w_held[kHeld ? i : 0], p.w, w_smem, i, 1.f);
                 if (FULL) {
-                    const V8 c = kHeld ? b_held[kHeld && FULL ? i : 0] : at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
+                    const V8 c = param(b_held[kHeld && FULL ? i : 0], p.b, b_smem, i, 0.f);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[i].p[k] = fma2(v[i].p[k], w.p[k], c.p[k]);
                 } else {
