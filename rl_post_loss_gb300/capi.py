@@ -707,6 +707,16 @@ def _like(name: str, t, rows: int, cols: int, dtype, device):
     raise ValueError(f"{name} is a {dtype} tensor [{rows}, {cols}] with contiguous rows that do not overlap on {device}")
 
 
+def _rows_like(t, cols: int, dtype, device):
+    """A new matrix with rows as those of t [rows, columns]: without gaps, or else on 32-byte boundaries."""
+    import torch
+    rows, ld = t.shape[0], t.stride(0)
+    if ld == cols or rows < 2:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    per = 8 if dtype is torch.float32 else 16
+    return torch.empty((rows, (cols + per - 1) // per * per), dtype=dtype, device=device)[:, :cols]
+
+
 def _params(weight, bias, cols: int, device):
     """(dtype code, pointer of weight, pointer of bias) of a norm's parameters."""
     p = weight if weight is not None else bias
@@ -739,7 +749,8 @@ def layer_norm(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1
     where there is one. Returns y (of type `dtype`, that of x unless given), summed (x + residual; None without a
     residual unless a tensor is passed), mean and rstd [rows] (with want_stats; no mean for "rms") and checkpoint: `checkpoint`
     is an Act8, or "int8" or "e4m3" for a new one, that receives the norm's input in 8 bits for layer_norm_backward. Rows whose mask
-    is 0 are not read and give 0. y may be x or the residual, and so may summed."""
+    is 0 are not read and give 0. y may be x or the residual, and so may summed. New matrices have rows like those of x:
+    without gaps, or else on 32-byte boundaries."""
     import torch
     if kind not in LN_KINDS:
         raise ValueError("kind is 'layer' or 'rms'")
@@ -748,15 +759,15 @@ def layer_norm(x, weight=None, bias=None, *, kind: str = "layer", eps: float = 1
     pt, pw, pb = _params(weight, bias, cols, dev)
     with _allocations_of(stream, dev):
         if y is None:
-            y = torch.empty((rows, cols), dtype=dtype or xdt, device=dev)
-            py, ldy, ydt = y.data_ptr(), cols, y.dtype
+            y = _rows_like(x, cols, dtype or xdt, dev)
+            py, ldy, ydt = y.data_ptr(), y.stride(0), y.dtype
         else:
             ydt = y.dtype
             if dtype is not None and ydt is not dtype:
                 raise ValueError("y has the type that dtype names")
             py, ldy = _like("y", y, rows, cols, ydt, dev)
         if summed is None and residual is not None:
-            summed = torch.empty((rows, cols), dtype=xdt, device=dev)
+            summed = _rows_like(x, cols, xdt, dev)
         if want_stats:
             if rstd is None:
                 rstd = torch.empty(rows, dtype=f32, device=dev)
@@ -789,7 +800,7 @@ def layer_norm_backward(dy, weight, mean, rstd, *, x=None, checkpoint=None, kind
     forward pass's. dsummed is the gradient that comes along the residual stream, added to dx. dx has the type of x (from a checkpoint: `dtype`, that of dy unless given). dweight (unless
     want_dweight is False) and dbias (with want_dbias, or where it is passed) are fp32; with accumulate they are
     added to. A tensor y receives the forward pass's output made again (with `bias`, if there was one). Rows whose mask is 0 are not
-    read and give 0. dx may be dy, x or dsummed. A workspace that is passed serves one call at a time."""
+    read and give 0. dx may be dy, x or dsummed (a new one has rows like those of dy). A workspace that is passed serves one call at a time."""
     import torch
     if kind not in LN_KINDS:
         raise ValueError("kind is 'layer' or 'rms'")
@@ -808,8 +819,8 @@ def layer_norm_backward(dy, weight, mean, rstd, *, x=None, checkpoint=None, kind
         raise ValueError("pass the dweight and dbias that are added to")
     with _allocations_of(stream, dev):
         if dx is None:
-            dx = torch.empty((rows, cols), dtype=dtype, device=dev)
-            pdx, lddx = dx.data_ptr(), cols
+            dx = _rows_like(dy, cols, dtype, dev)
+            pdx, lddx = dx.data_ptr(), dx.stride(0)
         else:
             pdx, lddx = _like("dx", dx, rows, cols, dtype, dev)
         if dweight is None and want_dweight:

@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
 // ---------------------------------------------------------------- the sum of the partial sums
 
 // A block adds 32 columns' partial sums: warp k takes every 32nd one, a lane a column, ten loads under way at a time;
-// then warp c adds column c's 32 sums by a butterfly. (Eight warps, each thread a long chain of loads: 4096 x 6144 @@.)
+// then warp c adds column c's 32 sums by a butterfly. (Eight warps, each thread a long chain of loads: 4096 x 6144 41.8 us,
+// against 41.2.)
 // The launch begins while the blocks before it still work, and waits for them.
 __global__ void __launch_bounds__(kJoin * kJoin) norm_join_kernel(const float *partials, int64_t ld, int parts, int cols, float *dw, float *db, int accumulate) {
     __shared__ float s[kJoin][kJoin + 1];
@@ -313,7 +314,7 @@ int norm_backward_parts(int rows, int cols) {
 
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream) {
     const bool act8 = !p.x.p, full = !p.rms || p.want_db;
-    const bool fast = p.dy.fast && (act8 ? p.ckpt.fast : p.x.fast) && (!p.dsummed.p || p.dsummed.fast);
+    const bool fast = p.dy.fast && (act8 ? p.ckpt.fast : p.x.fast) && (!p.dsummed.p || p.dsummed.fast) && p.dx.fast && (!p.y.p || p.y.fast);
     cudaError_t e = cudaErrorUnknown;
     int blocks;
     if (fast && p.cols <= kShortCols) {

@@ -236,7 +236,10 @@ NormTeams teams_of(const NormForwardParams &p, int mode) {
 }  // namespace
 
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream) {
-    const bool fast = p.x.fast && (!p.residual.p || p.residual.fast);
+    // with rows that start anywhere on either side, single columns: what a warp stores one by one has to lie side by side
+    // (8920 x 9118 bf16 with a residual into rows without gaps: 221 us, with vectors cut up at the store 515; into rows on
+    // 16-byte boundaries 112)
+    const bool fast = p.x.fast && (!p.residual.p || p.residual.fast) && p.y.fast && (!p.h.p || p.h.fast) && (!p.ckpt.codes || p.ckpt.fast);
     if (fast && p.cols <= kShortCols) return p.x.bf16 ? launch_short<true>(p, stream) : launch_short<false>(p, stream);
     if (!fast) {
         const NormTeams n = teams_of(p, kAnyRow);

@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         const auto get_h = [&](int i) -> V8 {
             if constexpr (MODE != kAnyRow) return read_h<SRC>(sh, at.vec(i), scale[kScales > 1 ? i : 0]);
             if constexpr (!kAct8) return at.template read<SRC == kHBf16>(sh, i);
-            return at.singles(i, [&](int c) { return act8_value((uint8_t)sh[c], (uint8_t)ssc[c / kAct8Block], SRC == kHE4M3, __uint_as_float(0x7f7fffffu)); });
+            return at.singles(i, [&](int c) { return act8_value_norm<SRC == kHE4M3>((uint8_t)sh[c], (uint8_t)ssc[c / kAct8Block]); });
         };
         float c1 = 0.f, c2 = 0.f;
         const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
