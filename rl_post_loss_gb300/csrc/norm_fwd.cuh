@@ -125,15 +125,12 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (at.none(i)) continue;
-            float f[kVec];
-            floats_of(at.params(p.w, p.params_bf16, p.params_fast, i, 1.f), f);
-            store_vec(w_smem, at.vec(i) * kVec, at.vec(i) * kVec + kVec, true, f);
-            floats_of(at.params(p.b, p.params_bf16, p.params_fast, i, 0.f), f);
-            store_vec(b_smem, at.vec(i) * kVec, at.vec(i) * kVec + kVec, true, f);
+            write_planes(w_smem, at.vec(i), VPT * T, at.params(p.w, p.params_bf16, p.params_fast, i, 1.f));
+            write_planes(b_smem, at.vec(i), VPT * T, at.params(p.b, p.params_bf16, p.params_fast, i, 0.f));
         }
     const auto param = [&](const V8 &held, const void *q, const float *q_smem, int i, float missing) -> V8 {
         if (kHeld) return held;
-        if (MODE == kBlockRow && n.w_in_smem) return read_vec<false>(reinterpret_cast<const char *>(q_smem), at.vec(i));
+        if (MODE == kBlockRow && n.w_in_smem) return read_planes(q_smem, at.vec(i), VPT * T);
         return at.params(q, p.params_bf16, p.params_fast, i, missing);
     };
     const bool plain = p.y.fast && (p.y.bf16 != 0) == BF16;

@@ -85,9 +85,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         if (kWInRegs) {
             w[i] = v;
         } else if (n.w_in_smem) {
-            float f[kVec];
-            floats_of(v, f);
-            store_vec(w_smem, at.vec(i) * kVec, at.vec(i) * kVec + kVec, true, f);
+            write_planes(w_smem, at.vec(i), VPT * T, v);
         }
         dw[i] = zeros();
         if (FULL) db[i] = zeros();
@@ -95,7 +93,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     const auto weight = [&](int i) -> V8 {
         if constexpr (kWInRegs) return w[i];
         if (!n.w_in_smem) return at.params(p.w, p.params_bf16, p.params_fast, i, 1.f);
-        return read_vec<false>(reinterpret_cast<const char *>(w_smem), at.vec(i));
+        return read_planes(w_smem, at.vec(i), VPT * T);
     };
 
     // of the row at hand, loaded a row ahead

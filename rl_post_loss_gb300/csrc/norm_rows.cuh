@@ -33,6 +33,19 @@ __device__ __forceinline__ void store_one(const RowMat &m, int64_t at, float v) 
         static_cast<float *>(m.p)[at] = v;
 }
 
+// Eight fp32 values of a thread that wrote them itself, in two planes of four, so that a warp's accesses of 16 bytes lie
+// side by side (32 bytes apart they meet in the same banks two by two).
+__device__ __forceinline__ void write_planes(float *base, int vec, int vecs, const V8 &a) {
+    float v[kVec];
+    floats_of(a, v);
+    reinterpret_cast<float4 *>(base)[vec] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(base)[vecs + vec] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ V8 read_planes(const float *base, int vec, int vecs) {
+    const uint4 *q = reinterpret_cast<const uint4 *>(base);
+    return f32_pairs(q[vec], q[vecs + vec]);
+}
+
 // A thread's i-th eight columns. Only the last ones may be cut off by the row's end, or not there at all.
 template <int MODE, int VPT>
 struct Columns {
