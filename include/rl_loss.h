@@ -547,8 +547,8 @@ RL_LOSS_API rl_status rl_loss_preference(const rl_loss_pref_config *config, int3
  * back along it, and dx is the gradient of x and of the residual alike.
  * Statistics, sums and products are fp32 (the mean is corrected by the sum of the
  * differences from it), outputs are rounded once; sums over rows go through fp32
- * sums of each block's rows, added in a fixed order that depends on the sizes
- * alone, so results repeat bit for bit.
+ * sums of each block's rows, added in a fixed order that the call's sizes, types,
+ * alignment and choice of outputs set, so the same call repeats bit for bit.
  * Shared rules: rows of any element-aligned address and stride >= C (16-byte
  * aligned ones are read by vectors, up to C rounded up to 16 bytes); nothing past a
  * row's C columns is written. A row whose mask is 0 is not read, its outputs are 0

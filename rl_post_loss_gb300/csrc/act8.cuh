@@ -313,7 +313,7 @@ struct Act8Params {
     Act8Mat a;
     int64_t rows;
     int32_t cols;
-    int32_t row_parts;      // parts of 16 columns of a row, whole blocks
+    int32_t row_parts;      // parts of a row, one thread each
     int64_t step_rows;      // rows and parts that the grid's threads step over
     int32_t step_parts;
 };

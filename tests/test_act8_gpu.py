@@ -72,6 +72,30 @@ def test_codes_in_a_callers_tensors(cols, fmt):
     assert (sc[0] == 200).all() and (sc[-1] == 200).all() and (sc[:, :2] == 200).all() and (sc[:, 2 + blocks:] == 200).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [1, 2, 5, 7, 8, 9, 31, 33, 63, 100, 257])
+def test_rows_at_every_offset(cols, dtype):
+    """Rows that start at every offset in 32 bytes, read and written, with nothing beside them read as theirs or written."""
+    g = torch.Generator().manual_seed(cols)
+    x = (torch.randn((9, cols), generator=g) * torch.exp2(torch.randint(-30, 30, (9, (cols + 31) // 32), generator=g).float()).repeat_interleave(32, 1)[:, :cols]).to(dtype)
+    for fmt in ("int8", "e4m3"):
+        codes, scales = nh.pack64(x, fmt)
+        want = nh.values64(codes, scales, fmt, dtype)
+        for off in range(16):
+            for gap in (0, 1, 5):
+                ld = cols + gap
+                flat = torch.full((9 * ld + 32,), math.nan, dtype=dtype, device="cuda")
+                at = flat[off:off + 9 * ld].view(9, ld)[:, :cols]
+                at.copy_(x)
+                a = capi.act8_pack(at, format=fmt)
+                assert nh.same(a.codes.cpu(), codes) and nh.same(a.scales.cpu(), scales)
+                flat.fill_(7)
+                capi.act8_unpack(a, out=at)
+                assert nh.same(at.double().cpu(), want)
+                at.fill_(7)
+                assert (flat == 7).all()
+
+
 def test_packing_what_was_read_back_changes_nothing():
     x = torch.randn((50, 1000), device="cuda", dtype=BF16) * 30
     for fmt in ("int8", "e4m3"):
