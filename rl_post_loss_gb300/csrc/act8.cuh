@@ -98,15 +98,6 @@ __device__ __forceinline__ uint2 act8_encode(const float (&v)[kVec], uint32_t b,
     return make_uint2(w[0], w[1]);
 }
 
-__device__ __forceinline__ uint32_t act8_encode_one(float v, uint32_t b, bool e4m3) {
-    if (b == 255u) return 0u;
-    const float inv = __uint_as_float((254u - b) << 23);
-    if (!e4m3) return __float_as_uint(fmaf(v, inv, 12582912.f)) & 0xffu;
-    uint16_t c;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(v * inv));
-    return c & 0xffu;
-}
-
 // What eight codes stand for, as pairs. An int8 code plus 128 in the low byte of 2^23 is 2^23 + 128 + code, and
 // times s the difference is exact. An e4m3 code's 7 low bits, put where fp32 has its exponent and mantissa, are the
 // value times 2^-120 (subnormal codes included). Where products may pass fp32's range (a code can stand for a
@@ -176,22 +167,6 @@ __device__ __forceinline__ V8 act8_decode_norm(uint2 c, uint32_t b) {
                                 __uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | ((2 * i + 1) & 3)))), mul, off);
     }
     return r;
-}
-
-// The same for one code.
-template <bool E4M3>
-__device__ __forceinline__ float act8_value_norm(uint32_t c, uint32_t b) {
-    const float s = __uint_as_float(b << 23);
-    if (E4M3) return __uint_as_float((uint32_t)((int32_t)(c << 24) >> 4) & 0x87f00000u) * 0x1p64f * (s * 0x1p56f);
-    return (__uint_as_float(0x4b000000u | (c ^ 0x80u)) - 8388736.f) * s;
-}
-
-// What one code stands for.
-__device__ __forceinline__ float act8_value(uint32_t c, uint32_t b, bool e4m3, float most) {
-    const float s = __uint_as_float(b == 255u ? 0x7fc00000u : (b ? b << 23 : 0x00400000u));
-    const float q = e4m3 ? __uint_as_float((uint32_t)((int32_t)(c << 24) >> 4) & 0x87f00000u) * 0x1p120f : (float)(int8_t)c;
-    const float v = q * s;
-    return fabsf(v) > most ? copysignf(most, v) : v;
 }
 
 // ---------------------------------------------------------------- eight columns of a row in memory

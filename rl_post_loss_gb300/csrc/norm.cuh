@@ -59,7 +59,7 @@ struct NormTeams {
     int warps, vecs, blocks_per_sm;              // of a row; vectors of eight columns of a thread
     int depth;                                   // rows' room of a team in shared memory
     int w_in_smem;                               // the weight beside them, where registers have no room for it
-    int at_dy, at_ds, at_scales, stage_bytes;    // of a row
+    int at_dy, at_ds, stage_bytes;               // of a row
     size_t smem;
 };
 
@@ -67,7 +67,8 @@ struct NormTeams {
 int norm_backward_parts(int rows, int cols);
 
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream);
-cudaError_t launch_norm_forward_any(const NormForwardParams &p, const struct NormTeams &n, cudaStream_t stream);
+cudaError_t launch_norm_forward_any(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream);
+cudaError_t launch_norm_forward_shift(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream);
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream);
 // The backward pass's kernels by the types of h and dy.
 #define RLK_NORM_ROWS(H, DY) cudaError_t launch_norm_rows_##H##_##DY(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream)

@@ -261,18 +261,17 @@ constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 512;  // what a bl
 
 // A block per row, 128 registers a thread, so 16 warps on an SM: of the numbers of vectors a thread, the one whose
 // blocks take all rows soonest, by a row's time of its vectors and two more for the exchange of sums. Both sums with
-// four vectors a thread (rows that start anywhere: with three) do not fit the registers, and are taken for the
+// four vectors a thread (kAnyRow: with three) do not fit the registers, and are taken for the
 // longest rows alone.
 NormTeams teams_of(const NormBackwardParams &p, int mode) {
-    const bool act8 = !p.x.p, full = !p.rms || p.want_db || mode == kAnyRow;
-    const int vecs = vectors(p.cols), pad = mode == kAnyRow ? 16 : 0;
+    const bool act8 = !p.x.p, full = !p.rms || p.want_db || starts_anywhere(mode);
+    const int vecs = vectors(p.cols), pad = starts_anywhere(mode) ? 32 : 0;
     const auto bytes = [&](int es) { return (p.cols * es + 15) / 16 * 16 + pad; };
     NormTeams n{};
     n.mode = mode;
     n.at_dy = bytes(act8 ? 1 : p.x.bf16 ? 2 : 4);
     n.at_ds = n.at_dy + bytes(p.dy.bf16 ? 2 : 4);
-    n.at_scales = n.at_ds + (p.dsummed.p ? bytes(p.dx.bf16 ? 2 : 4) : 0);
-    n.stage_bytes = n.at_scales + (mode == kAnyRow && act8 ? (p.cols / kAct8Block + 1 + 15) / 16 * 16 + pad : 0);
+    n.stage_bytes = n.at_ds + (p.dsummed.p ? bytes(p.dx.bf16 ? 2 : 4) : 0);
     if (mode == kWarpRow) {
         n.warps = 1;
         n.vecs = vecs > 96 ? 4 : 3;
@@ -286,7 +285,7 @@ NormTeams teams_of(const NormBackwardParams &p, int mode) {
         const int warps = (vecs + 32 * v - 1) / (32 * v);
         if ((v - 1) * warps * 32 >= vecs) continue;  // fewer vectors a thread do
         if (warps > kNormWarps || (v >= (mode == kAnyRow ? 3 : 4) && full && n.warps)) continue;
-        const bool regs = mode == kAnyRow ? v == 1 : v <= 3 || !full;
+        const bool regs = mode == kAnyRow ? v == 1 : v <= (mode == kShiftRow ? 2 : 3) || !full;
         size_t w_bytes = regs ? 0 : (size_t)v * warps * 32 * kVec * 4;
         int blocks = kNormWarps / warps;
         while (blocks > 1 && blocks * (kBlockExtra + w_bytes + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
@@ -326,7 +325,7 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t strea
         const bool any = !fast || (!act8 && p.x.bf16 && !p.dy.bf16);
         // a warp per row where there are rows for all warps
         const bool warp = !any && p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps;
-        const NormTeams n = teams_of(p, any ? kAnyRow : warp ? kWarpRow : kBlockRow);
+        const NormTeams n = teams_of(p, any ? act8 ? kShiftRow : kAnyRow : warp ? kWarpRow : kBlockRow);
         blocks = std::min(p.rows, kNormSMs * n.blocks_per_sm);
 #define RLK_ROWS(H) (p.dy.bf16 ? launch_norm_rows_##H##_bf16(p, n, blocks, stream) : launch_norm_rows_##H##_f32(p, n, blocks, stream))
         e = act8 ? p.ckpt.e4m3 ? RLK_ROWS(e4m3) : RLK_ROWS(int8) : p.x.bf16 ? RLK_ROWS(bf16) : RLK_ROWS(f32);

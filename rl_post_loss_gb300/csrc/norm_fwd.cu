@@ -197,8 +197,8 @@ cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
 // 8192 bf16: layer norm with two, three, four vectors 141, 147, 125 us, RMS with a residual 180, 174, 181; 20000 x 5120: 156, 92,
 // 102 us; so layer norm with four, whose weights are read from shared memory, counts as 9.8.)
 NormTeams teams_of(const NormForwardParams &p, int mode) {
-    const int vecs = (p.cols + kVec - 1) / kVec, pad = mode == kAnyRow ? 16 : 0;
-    const bool full = !p.rms || p.b;
+    const int vecs = (p.cols + kVec - 1) / kVec, pad = starts_anywhere(mode) ? 32 : 0;
+    const bool full = starts_anywhere(mode) || !p.rms || p.b;
     NormTeams n{};
     n.mode = mode;
     n.at_dy = (p.cols * (p.x.bf16 ? 2 : 4) + 15) / 16 * 16 + pad;
@@ -236,14 +236,17 @@ NormTeams teams_of(const NormForwardParams &p, int mode) {
 }  // namespace
 
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream) {
-    // with rows that start anywhere on either side, single columns: what a warp stores one by one has to lie side by side
-    // (8920 x 9118 bf16 with a residual into rows without gaps: 221 us, with vectors cut up at the store 515; into rows on
-    // 16-byte boundaries 112)
+    // (with rows that start anywhere on any side: vectors cut up at the store, a warp's stores 16 bytes apart, took 515 us for
+    // 8920 x 9118 bf16 with a residual, which takes 182 so, and 112 between rows on 16-byte boundaries)
     const bool fast = p.x.fast && (!p.residual.p || p.residual.fast) && p.y.fast && (!p.h.p || p.h.fast) && (!p.ckpt.codes || p.ckpt.fast);
     if (fast && p.cols <= kShortCols) return p.x.bf16 ? launch_short<true>(p, stream) : launch_short<false>(p, stream);
     if (!fast) {
-        const NormTeams n = teams_of(p, kAnyRow);
-        return launch_norm_forward_any(p, n, stream);
+        // The pieces shifted into place, where 8-bit codes are made or a thread would hold more than two vectors' single columns,
+        // whose weights have no room in registers: 16000 x 3001 bf16 layer norm to int8 94 us (single columns 199), 8920 x 9118 bf16
+        // with a residual 182 (270), 8192 x 6145 layer norm 95 (99); but 8192 x 4095 61 (52), 30000 x 1031 fp32 with a residual 115 (88).
+        const bool shift = p.ckpt.codes || p.cols > 4096;
+        const NormTeams n = teams_of(p, shift ? kShiftRow : kAnyRow);
+        return shift ? launch_norm_forward_shift(p, n, stream) : launch_norm_forward_any(p, n, stream);
     }
     const bool full = !p.rms || p.b, warp = p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kForwardWarps;  // a warp per row where there are rows for all
     const NormTeams n = teams_of(p, warp ? kWarpRow : kBlockRow);

@@ -15,28 +15,16 @@ namespace rlk {
 
 constexpr int kForwardWarps = 16;  // of a block and of an SM: 128 registers a thread
 
-// h's 8-bit codes. On 16-byte boundaries a block of 32 columns is four lanes' vectors; in rows that start anywhere
-// it is what the warp's lanes hold at one place.
+// h's 8-bit codes; a block of 32 columns is four lanes' vectors.
 template <int MODE, int VPT>
 __device__ __forceinline__ void store_act8(const Columns<MODE, VPT> &at, const Act8Mat &a, int64_t row, int i, const V8 &h) {
     float v[kVec];
     floats_of(h, v);
-    if (MODE != kAnyRow) {
-        const int vec = at.vec(i), col = vec * kVec;
-        const uint32_t b = act8_scale(act8_block_max(act8_amax(v)), a.e4m3);
-        if (at.none(i)) return;
-        store_codes(a.codes + row * a.ld_codes, col, at.cols, a.fast, act8_encode(v, b, a.e4m3));
-        if ((vec & 3) == 0) a.scales[row * a.ld_scales + (vec >> 2)] = (uint8_t)b;
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        const int col = at.col(i, j);
-        const uint32_t b = act8_scale(__reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu), a.e4m3);
-        if (col >= at.cols) continue;
-        a.codes[row * a.ld_codes + col] = (uint8_t)act8_encode_one(v[j], b, a.e4m3);
-        if ((col & 31) == 0) a.scales[row * a.ld_scales + (col >> 5)] = (uint8_t)b;
-    }
+    const int vec = at.vec(i), col = vec * kVec;
+    const uint32_t b = act8_scale(act8_block_max(act8_amax(v)), a.e4m3);
+    if (at.none(i)) return;
+    store_codes(a.codes + row * a.ld_codes, col, at.cols, a.fast, act8_encode(v, b, a.e4m3));
+    if ((vec & 3) == 0) a.scales[row * a.ld_scales + (vec >> 2)] = (uint8_t)b;
 }
 
 template <bool BF16>
@@ -94,7 +82,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
     const auto r_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.residual.p) + row * p.residual.ld * (BF16 ? 2 : 4); };
     const auto copy_row = [&](int64_t row, int s) {  // by the team's thread 0
         const uint32_t full = full0 + s * 8, to = ptx::smem_u32(stages + s * n.stage_bytes);
-        if (MODE != kAnyRow) {
+        if (!starts_anywhere(MODE)) {
             ptx::mbar_arrive_expect_tx(full, (uint32_t)n.stage_bytes);
             ptx::bulk_g2s(to, x_row(row), (uint32_t)n.at_dy, full);
             if (p.residual.p) ptx::bulk_g2s(to + n.at_dy, r_row(row), (uint32_t)n.at_dy, full);
@@ -121,7 +109,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
         }
     // else in shared memory as fp32, a thread's own beside one another, where that fits
     float *w_smem = reinterpret_cast<float *>(smem + kTeams * S * n.stage_bytes), *b_smem = w_smem + VPT * T * kVec;
-    if (!kHeld && MODE == kBlockRow && n.w_in_smem)
+    if (!kHeld && MODE != kAnyRow && n.w_in_smem)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (at.none(i)) continue;
@@ -130,7 +118,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
         }
     const auto param = [&](const V8 &held, const void *q, const float *q_smem, int i, float missing) -> V8 {
         if (kHeld) return held;
-        if (MODE == kBlockRow && n.w_in_smem) return read_planes(q_smem, at.vec(i), VPT * T);
+        if (MODE != kAnyRow && n.w_in_smem) return read_planes(q_smem, at.vec(i), VPT * T);
         return at.params(q, p.params_bf16, p.params_fast, i, missing);
     };
     const bool plain = p.y.fast && (p.y.bf16 != 0) == BF16;
@@ -150,15 +138,15 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
             }
             phases ^= 1u << s;
             const char *sx = stages + s * n.stage_bytes, *sr = sx + n.at_dy;
-            if (MODE == kAnyRow) sx += row_shift<MODE>(x_row(row)), sr += row_shift<MODE>(r_row(row));
+            const int x_shift = row_shift<MODE>(x_row(row)), r_shift = row_shift<MODE>(r_row(row));
             f32x2 s0[2] = {}, s1[2] = {};
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 v[i] = zeros();
                 if (at.none(i)) continue;
-                v[i] = at.template read<BF16>(sx, i);
-                if (p.residual.p) v[i] = add_residual<BF16>(v[i], at.template read<BF16>(sr, i));
-                if (MODE != kAnyRow && i == VPT - 1 && at.cut) v[i] = clipped(v[i], at.vec(i) * kVec, p.cols);
+                v[i] = at.template read<BF16>(sx, x_shift, i);
+                if (p.residual.p) v[i] = add_residual<BF16>(v[i], at.template read<BF16>(sr, r_shift, i));
+                if (MODE != kAnyRow && i == VPT - 1 && at.cut) v[i] = at.cut_off(v[i], i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     if (!FULL || p.rms)
@@ -176,7 +164,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
                     if (!at.none(i)) at.store(p.h, row, i, v[i]);
-            if (p.ckpt.codes)
+            if (MODE != kAnyRow && p.ckpt.codes)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) store_act8(at, p.ckpt, row, i, v[i]);
             if (!FULL || p.rms) {
@@ -220,7 +208,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
 #pragma unroll
                     for (int k = 0; k < 4; ++k) v[i].p[k] = mul2(v[i].p[k], w.p[k]);
                 }
-                if (MODE != kAnyRow && plain)
+                if (!starts_anywhere(MODE) && plain)
                     at.template store_plain<BF16>(y_row, p.y.fast, i, v[i]);
                 else
                     at.store(p.y, row, i, v[i]);
@@ -237,7 +225,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
                     at.store(p.y, row, i, zeros());
                     if (p.h.p) at.store(p.h, row, i, zeros());
                 }
-                if (p.ckpt.codes) store_act8(at, p.ckpt, row, i, zeros());
+                if (MODE != kAnyRow && p.ckpt.codes) store_act8(at, p.ckpt, row, i, zeros());
             }
         }
         on = on_next;

@@ -23,9 +23,14 @@ __device__ __forceinline__ V8 read_h(const char *row, int vec, uint32_t scale) {
     if (!from_act8(SRC)) return read_vec<SRC == kHBf16>(row, vec);
     return act8_decode_norm<SRC == kHE4M3>(*reinterpret_cast<const uint2 *>(row + vec * 8), scale);
 }
+template <int SRC>
+__device__ __forceinline__ V8 read_h_shifted(const char *row, int shift, int vec, uint32_t scale) {
+    if (!from_act8(SRC)) return read_shifted<SRC == kHBf16>(row, shift, vec);
+    return act8_decode_norm<SRC == kHE4M3>(codes_shifted(row, shift, vec), scale);
+}
 template <int SRC, bool DYBF16, int VPT, bool FULL, int MODE>
 __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(NormBackwardParams p, NormTeams n) {
-    constexpr bool kAct8 = from_act8(SRC), kWInRegs = MODE == kAnyRow ? VPT == 1 : VPT <= 3 || !FULL;  // (else no room is left)
+    constexpr bool kAct8 = from_act8(SRC), kWInRegs = MODE == kAnyRow ? VPT == 1 : VPT <= (MODE == kShiftRow ? 2 : 3) || !FULL;  // (else no room is left)
     constexpr int kTeams = MODE == kWarpRow ? kNormWarps : 1;
     extern __shared__ __align__(128) char smem[];
     __shared__ __align__(16) float2 s_sums[2][16];
@@ -51,25 +56,22 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     };
     const auto dy_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.dy.p) + row * p.dy.ld * (DYBF16 ? 2 : 4); };
     const auto ds_row = [&](int64_t row) -> const char * { return static_cast<const char *>(p.dsummed.p) + row * p.dsummed.ld * (x_bf16 ? 2 : 4); };
-    const auto scale_row = [&](int64_t row) -> const char * { return reinterpret_cast<const char *>(p.ckpt.scales) + row * p.ckpt.ld_scales; };
     const auto copy_row = [&](int64_t row, int s) {  // by the team's thread 0
         char *stage = stages + s * n.stage_bytes;
         const uint32_t full = full0 + s * 8, to = ptx::smem_u32(stage);
-        if (MODE != kAnyRow) {
+        if (!starts_anywhere(MODE)) {
             ptx::mbar_arrive_expect_tx(full, (uint32_t)n.stage_bytes);
             ptx::bulk_g2s(to, h_row(row), (uint32_t)n.at_dy, full);
             ptx::bulk_g2s(to + n.at_dy, dy_row(row), (uint32_t)(n.at_ds - n.at_dy), full);
             if (p.dsummed.p) ptx::bulk_g2s(to + n.at_ds, ds_row(row), (uint32_t)(n.stage_bytes - n.at_ds), full);
             return;
         }
-        uint32_t bytes[4] = {window(h_row(row), p.cols * (kAct8 ? 1 : SRC == kHBf16 ? 2 : 4)), window(dy_row(row), p.cols * (DYBF16 ? 2 : 4)),
-                             p.dsummed.p ? window(ds_row(row), p.cols * (x_bf16 ? 2 : 4)) : 0u,
-                             kAct8 ? window(scale_row(row), (p.cols + kAct8Block - 1) / kAct8Block) : 0u};
-        ptx::mbar_arrive_expect_tx(full, bytes[0] + bytes[1] + bytes[2] + bytes[3]);
+        const uint32_t bytes[3] = {window(h_row(row), p.cols * (kAct8 ? 1 : SRC == kHBf16 ? 2 : 4)), window(dy_row(row), p.cols * (DYBF16 ? 2 : 4)),
+                                   p.dsummed.p ? window(ds_row(row), p.cols * (x_bf16 ? 2 : 4)) : 0u};
+        ptx::mbar_arrive_expect_tx(full, bytes[0] + bytes[1] + bytes[2]);
         ptx::bulk_g2s(to, h_row(row) - row_shift<MODE>(h_row(row)), bytes[0], full);
         ptx::bulk_g2s(to + n.at_dy, dy_row(row) - row_shift<MODE>(dy_row(row)), bytes[1], full);
         if (p.dsummed.p) ptx::bulk_g2s(to + n.at_ds, ds_row(row) - row_shift<MODE>(ds_row(row)), bytes[2], full);
-        if (kAct8) ptx::bulk_g2s(to + n.at_scales, scale_row(row) - row_shift<MODE>(scale_row(row)), bytes[3], full);
     };
     if (t == 0)
         for (int s = 0; s < S; ++s) {
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     };
 
     // of the row at hand, loaded a row ahead
-    constexpr int kScales = kAct8 && MODE != kAnyRow ? VPT : 1;
+    constexpr int kScales = kAct8 ? VPT : 1;
     bool dead = false, on = true;
     float mean = 0.f, rstd = 0.f;
     uint32_t scale[kScales];
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         o = !p.mask || p.mask[row];
         r = p.rstd[row];
         if (FULL && !p.rms) m = p.mean[row];
-        if (kAct8 && MODE != kAnyRow) {
+        if (kAct8) {
             const uint8_t *q = p.ckpt.scales + row * p.ckpt.ld_scales;
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
@@ -125,15 +127,12 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         const int64_t row_more = row + (S - 1) * step;  // takes the last row's stage (the only stage: the next row takes it)
         const bool more = t == 0 && S > 1 && row != first && row_more < p.rows && (!p.mask || p.mask[row_more]);
 
-        const char *stage = stages + s * n.stage_bytes, *sh = stage, *sdy = stage + n.at_dy, *sds = stage + n.at_ds, *ssc = stage + n.at_scales;
-        if (MODE == kAnyRow) {
-            sh += row_shift<MODE>(h_row(row)), sdy += row_shift<MODE>(dy_row(row)), sds += row_shift<MODE>(ds_row(row));
-            if (kAct8) ssc += row_shift<MODE>(scale_row(row));
-        }
+        const char *stage = stages + s * n.stage_bytes, *sh = stage, *sdy = stage + n.at_dy, *sds = stage + n.at_ds;
+        const int h_shift = row_shift<MODE>(h_row(row)), dy_shift = row_shift<MODE>(dy_row(row)), ds_shift = row_shift<MODE>(ds_row(row));
         const auto get_h = [&](int i) -> V8 {
-            if constexpr (MODE != kAnyRow) return read_h<SRC>(sh, at.vec(i), scale[kScales > 1 ? i : 0]);
-            if constexpr (!kAct8) return at.template read<SRC == kHBf16>(sh, i);
-            return at.singles(i, [&](int c) { return act8_value_norm<SRC == kHE4M3>((uint8_t)sh[c], (uint8_t)ssc[c / kAct8Block]); });
+            if constexpr (MODE == kAnyRow) return at.template read<SRC == kHBf16>(sh, h_shift, i);  // (no codes)
+            if constexpr (MODE == kShiftRow) return read_h_shifted<SRC>(sh, h_shift, at.vec(i), scale[kScales > 1 ? i : 0]);
+            return read_h<SRC>(sh, at.vec(i), scale[kScales > 1 ? i : 0]);
         };
         float c1 = 0.f, c2 = 0.f;
         const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
@@ -147,8 +146,8 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (at.none(i)) continue;
-                V8 h = get_h(i), g = at.template read<DYBF16>(sdy, i);
-                if (MODE != kAnyRow && i == VPT - 1 && at.cut) h = clipped(h, at.vec(i) * kVec, p.cols), g = clipped(g, at.vec(i) * kVec, p.cols);
+                V8 h = get_h(i), g = at.template read<DYBF16>(sdy, dy_shift, i);
+                if (MODE != kAnyRow && i == VPT - 1 && at.cut) h = at.cut_off(h, i), g = at.cut_off(g, i);
                 const V8 ww = weight(i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (at.none(i)) continue;
-                const V8 h = get_h(i), g = at.template read<DYBF16>(sdy, i), ww = weight(i);
+                const V8 h = get_h(i), g = at.template read<DYBF16>(sdy, dy_shift, i), ww = weight(i);
                 V8 r;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -186,7 +185,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                     r.p[k] = fma2(FULL ? add2(h.p[k], nm) : h.p[k], nk, u);
                 }
                 if (p.dsummed.p) {
-                    const V8 d = x_bf16 ? at.template read<true>(sds, i) : at.template read<false>(sds, i);
+                    const V8 d = x_bf16 ? at.template read<true>(sds, ds_shift, i) : at.template read<false>(sds, ds_shift, i);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) r.p[k] = add2(r.p[k], d.p[k]);
                 }
@@ -196,7 +195,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                     for (int k = 0; k < 4; ++k) u.p[k] = fma2(mul2(add2(h.p[k], nm), rs), ww.p[k], u.p[k]);
                     at.store(p.y, row, i, u);
                 }
-                if (MODE == kAnyRow || !plain)
+                if (starts_anywhere(MODE) || !plain)
                     at.store(p.dx, row, i, r);
                 else if (x_bf16)
                     at.template store_plain<true>(dx_row, 1, i, r);
@@ -260,12 +259,13 @@ cudaError_t launch_norm_ring(const NormBackwardParams &p, const NormTeams &n, in
 template <int SRC, bool DYBF16>
 cudaError_t launch_norm_rows(const NormBackwardParams &p, const NormTeams &n, int blocks, cudaStream_t stream) {
 #define RLK_RING(V, FULL, MODE) launch_norm_ring<SRC, DYBF16, V, FULL, MODE>(p, n, blocks, stream)
-    if (n.mode == kAnyRow || (SRC == kHBf16 && !DYBF16)) {
+    constexpr int kAnywhere = from_act8(SRC) ? kShiftRow : kAnyRow;
+    if (starts_anywhere(n.mode)) {
         switch (n.vecs) {
-            case 1: return RLK_RING(1, true, kAnyRow);
-            case 2: return RLK_RING(2, true, kAnyRow);
-            case 3: return RLK_RING(3, true, kAnyRow);
-            default: return RLK_RING(4, true, kAnyRow);
+            case 1: return RLK_RING(1, true, kAnywhere);
+            case 2: return RLK_RING(2, true, kAnywhere);
+            case 3: return RLK_RING(3, true, kAnywhere);
+            default: return RLK_RING(4, true, kAnywhere);
         }
     }
     if constexpr (SRC != kHBf16 || DYBF16) {

@@ -404,3 +404,56 @@ def test_arguments_are_checked():
         capi.layer_norm_backward(dy, w, None, st["rstd"], x=x)
     with pytest.raises(capi.RlLossError, match="CAPACITY"):
         capi.layer_norm_backward(dy, w, st["mean"], st["rstd"], x=x, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+def at_offset(t, off, gap):
+    """t's rows `gap` elements apart, the first one `off` elements into its memory, and that memory (7 elsewhere)."""
+    rows, cols = t.shape
+    flat = torch.full((rows * (cols + gap) + 64,), 7.0, dtype=torch.float32, device="cuda").to(t.dtype)
+    at = flat[off:off + rows * (cols + gap)].view(rows, cols + gap)[:, :cols]
+    at.copy_(t)
+    return at, flat
+
+
+@pytest.mark.parametrize("cols", [1, 3, 8, 13, 100, 249, 255, 256, 257, 511, 520, 1030, 4097, 4104, 4600])
+@pytest.mark.parametrize("xt,yt", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_rows_at_every_offset(cols, xt, yt):
+    """Inputs and outputs that start at every offset in 32 bytes, each at another one, with and without a checkpoint whose own rows
+    start anywhere; nothing beside an output's rows is written."""
+    g = torch.Generator().manual_seed(cols)
+    rows = 5
+    x, r, ds = (torch.randn((rows, cols), generator=g).to(xt) for _ in range(3))
+    dy = torch.randn((rows, cols), generator=g).to(yt)
+    w, b = torch.randn(cols, generator=g), torch.randn(cols, generator=g)
+    mask = torch.tensor([1, 1, 0, 1, 1], dtype=torch.uint8)
+    wg, bg, mg = w.cuda(), b.cuda(), mask.cuda()
+    y, h, mean, rstd, e_y, e_mean, e_rstd = nh.forward64(x, w, b, "layer", EPS, r, mask)
+    blocks = (cols + 31) // 32
+    for k in range(16):
+        gap = k % 3
+        xg, rg, dyg, dsg = (at_offset(t, (k * m + 1) % 16, gap)[0] for t, m in ((x, 1), (r, 3), (dy, 5), (ds, 7)))
+        out = {n: at_offset(torch.zeros((rows, cols), dtype=t), (k * m + o) % 16, gap)
+               for n, t, m, o in (("y", yt, 1, 1), ("summed", xt, 9, 0), ("dx", xt, 1, 2), ("again", yt, 3, 3))}
+        fmt = (None, "int8", "e4m3", "int8")[k % 4]
+        ck = None
+        if fmt:
+            codes = torch.full((rows, cols + k), 9, dtype=torch.uint8, device="cuda")
+            ck = capi.Act8(codes[:, k // 2:k // 2 + cols], torch.empty((rows, blocks + 1), dtype=torch.uint8, device="cuda")[:, :blocks], fmt)
+        got = capi.layer_norm(xg, wg, bg, residual=rg, mask=mg, eps=EPS, y=out["y"][0], summed=out["summed"][0], want_stats=True, checkpoint=ck)
+        nh.assert_within("y", got["y"], y, e_y, yt)
+        assert nh.same(got["summed"], h)
+        h64 = h
+        if fmt:
+            assert all(nh.same(p, q) for p, q in zip((ck.codes, ck.scales), nh.pack64(h, fmt)))
+            h64 = nh.values64(ck.codes.cpu(), ck.scales.cpu(), fmt, F32)
+            assert (codes[:, :k // 2] == 9).all() and (codes[:, k // 2 + cols:] == 9).all()
+        source = dict(checkpoint=ck) if fmt else dict(x=got["summed"])
+        back = capi.layer_norm_backward(dyg, wg, got["mean"], got["rstd"], mask=mg, dsummed=dsg, dx=out["dx"][0], want_dbias=True, bias=bg,
+                                        y=out["again"][0], **source)
+        dx, dw, db, e_dx, e_dw, e_db = nh.backward64(h64, dy, w, got["mean"].cpu(), got["rstd"].cpu(), "layer", ds, mask)
+        nh.assert_within("dx", back["dx"], dx, e_dx, xt)
+        nh.assert_within("dweight", back["dweight"], dw, e_dw)
+        nh.assert_within("dbias", back["dbias"], db, e_db)
+        for name, (view, flat) in out.items():
+            view.fill_(7)
+            assert (flat == 7).all(), name
