@@ -57,6 +57,7 @@ constexpr size_t kNormRingSmem = 225 * 1024;  // of a block, beside its barriers
 struct NormTeams {
     int mode;                                    // RowMode
     int warps, vecs, blocks_per_sm;              // of a row; vectors of eight columns of a thread
+    int blocks;                                  // of the forward pass
     int depth;                                   // rows' room of a team in shared memory
     int w_in_smem;                               // the weight beside them, where registers have no room for it
     int at_dy, at_ds, stage_bytes;               // of a row

@@ -192,6 +192,22 @@ cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
 #undef RLK_RUN
 }
 
+// Two rows of a block in its ring: with as many as fit, reads far ahead of the writes cost the memory's rate. (65536 x 6144
+// bf16, RMS: 246 us, with eight 281; 32768 x 16384: 317, 367.)
+constexpr int kForwardDepth = 2;
+
+// The blocks that run at once, or, for as many bytes to write as to read, blocks of eight rows for a warp or block, which
+// start when others end: they do not read and write all in step, and a slow SM takes fewer. Where the weights' way into shared memory
+// or arithmetic is what a block waits for, their starts cost more, and masked rows break the step too. (RMS with a
+// residual, us: 65536 x 6144 bf16 with an int8 checkpoint 599 -> 525, 32768 x 6144 fp32 527 -> 471, 8192 x 6144 bf16 72 -> 65; layer norm
+// so 534 -> 466; but with an e4m3 checkpoint 65536 x 5120 489 -> 576, without a residual 16384 x 6144 79 -> 88, with a mask 125 -> 132.)
+int blocks_of(const NormForwardParams &p, int mode, const NormTeams &n, int teams) {
+    const bool full = starts_anywhere(mode) || !p.rms || p.b;
+    const int at_once = std::min(p.rows, kNormSMs * n.blocks_per_sm), short_ones = p.rows / (8 * teams);
+    const bool apart = p.residual.p && !p.mask && !starts_anywhere(mode) && (!full || (mode == kBlockRow && n.vecs < 4 && !p.ckpt.codes));
+    return apart && short_ones >= 3 * at_once ? short_ones : at_once;
+}
+
 // A block per row, 16 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by a
 // row's time of its vectors and two or three more for its exchanges of sums and what else is done once a row. (16384 x
 // 8192 bf16: layer norm with two, three, four vectors 141, 147, 125 us, RMS with a residual 180, 174, 181; 20000 x 5120: 156, 92,
@@ -209,6 +225,7 @@ NormTeams teams_of(const NormForwardParams &p, int mode) {
         n.blocks_per_sm = 1;
         n.depth = (int)std::min<size_t>(kNormDepth, kNormRingSmem / (kForwardWarps * n.stage_bytes));
         n.smem = (size_t)(kForwardWarps) * n.depth * n.stage_bytes;
+        n.blocks = blocks_of(p, mode, n, kForwardWarps);
         return n;
     }
     double best = 0;
@@ -227,9 +244,10 @@ NormTeams teams_of(const NormForwardParams &p, int mode) {
         n.w_in_smem = params + n.stage_bytes <= room;
         if (!n.w_in_smem) params = 0;
         n.warps = warps, n.vecs = v, n.blocks_per_sm = blocks;
-        n.depth = (int)std::min<size_t>(kNormDepth, (room - params) / n.stage_bytes);
+        n.depth = (int)std::min<size_t>(kForwardDepth, (room - params) / n.stage_bytes);
         n.smem = (size_t)n.depth * n.stage_bytes + params;
     }
+    n.blocks = blocks_of(p, mode, n, 1);
     return n;
 }
 

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
 
 template <bool BF16, int VPT, bool FULL, int MODE>
 cudaError_t launch_forward_rows(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream) {
-    return run_kernel<norm_forward_kernel<BF16, VPT, FULL, MODE>>(std::min(p.rows, kNormSMs * n.blocks_per_sm), MODE == kWarpRow ? kForwardWarps * 32 : n.warps * 32, n.smem, kNormRingSmem, stream, p, n);
+    return run_kernel<norm_forward_kernel<BF16, VPT, FULL, MODE>>(n.blocks, MODE == kWarpRow ? kForwardWarps * 32 : n.warps * 32, n.smem, kNormRingSmem, stream, p, n);
 }
 
 template <bool BF16, bool FULL, int MODE>

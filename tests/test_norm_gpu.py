@@ -457,3 +457,22 @@ def test_rows_at_every_offset(cols, xt, yt):
         for name, (view, flat) in out.items():
             view.fill_(7)
             assert (flat == 7).all(), name
+
+
+@pytest.mark.parametrize("rows,cols,kind,dtype,fmt", [(30011, 1032, "rms", BF16, "int8"), (30011, 1032, "layer", BF16, None), (7400, 6144, "rms", F32, None),
+                                                      (60003, 520, "rms", BF16, "e4m3"), (30003, 1024, "rms", F32, None), (30011, 1032, "layer", BF16, "e4m3")])
+def test_rows_do_not_depend_on_the_blocks(rows, cols, kind, dtype, fmt):
+    """Many rows with a residual go to more blocks than run at once, with a mask to no more: the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x, r = (torch.randn((rows, cols), generator=g, device="cuda").to(dtype) for _ in range(2))
+    w = torch.randn(cols, generator=g, device="cuda")
+    b = torch.randn(cols, generator=g, device="cuda") if kind == "layer" else None
+    few, many = (capi.layer_norm(x, w, b, kind=kind, residual=r, want_stats=True, checkpoint=fmt, mask=m)
+                 for m in (torch.ones(rows, dtype=torch.uint8, device="cuda"), None))
+    for name in ("y", "summed", "rstd") + (("mean",) if b is not None else ()):
+        assert torch.equal(few[name], many[name]), name
+    if fmt:
+        assert torch.equal(few["checkpoint"].codes, many["checkpoint"].codes) and torch.equal(few["checkpoint"].scales, many["checkpoint"].scales)
+    some = torch.arange(0, rows, 97)
+    y, h, mean, rstd, e_y, _, _ = nh.forward64(x[some].cpu(), w.cpu(), None if b is None else b.cpu(), kind, EPS, r[some].cpu())
+    nh.assert_within("y", many["y"][some], y, e_y, dtype)
