@@ -2,6 +2,7 @@
 //
 // A thread takes 16 columns, half a block, so that a code store is 16 bytes and what is done once a part is spread
 // over 16 columns: with 8 columns a thread the instructions bound packing (65536 x 6144 bf16: 238 us, against 211 then).
+// 65536 x 6144 bf16 to int8 takes 177 us (101% of the measured copy rate), back 193 us (93%), bound by memory.
 // A row's whole blocks are numbered in parts, so that two neighbouring lanes always hold one block; the threads of
 // the grid step through all rows' parts together.
 #include "act8.cuh"

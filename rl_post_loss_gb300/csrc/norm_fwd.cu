@@ -210,7 +210,7 @@ int blocks_of(const NormForwardParams &p, int mode, const NormTeams &n, int team
 
 // A block per row, 16 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by a
 // row's time of its vectors and two or three more for its exchanges of sums and what else is done once a row. (16384 x
-// 8192 bf16: layer norm with two, three, four vectors 141, 147, 125 us, RMS with a residual 180, 174, 181; 20000 x 5120: 156, 92,
+// 8192 bf16: layer norm with two, three, four vectors 141, 147, 125 us, RMS with a residual 180, 174, 181 (without blocks of eight rows); 20000 x 5120: 156, 92,
 // 102 us; so layer norm with four, whose weights are read from shared memory, counts as 9.8.)
 NormTeams teams_of(const NormForwardParams &p, int mode) {
     const int vecs = (p.cols + kVec - 1) / kVec, pad = starts_anywhere(mode) ? 32 : 0;

