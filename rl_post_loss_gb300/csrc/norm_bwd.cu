@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
     const int width = lanes * VPT * kVec;
     const bool x_bf16 = kAct8 ? p.dx.bf16 : SRC == kHBf16;
     float *w_smem = reinterpret_cast<float *>(smem + n.smem) - width;
-    for (int c = threadIdx.x; c < width; c += kThreads) w_smem[c] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
+    for (int c = threadIdx.x; c < width; c += kThreads) w_smem[plane_of(c, width / kVec)] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
     if (threadIdx.x == 0) {
         for (int k = 0; k < kNormWarps * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
         ptx::fence_mbar_init();
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
                 if (!EXACT && col >= p.cols) continue;
                 V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec);
                 if (!EXACT && col + kVec > p.cols) h = clipped(h, col, p.cols), g = clipped(g, col, p.cols);
-                const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+                const V8 w = read_planes(w_smem, vec, width / kVec);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, w.p[k]);
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
             for (int i = 0; i < VPT; ++i) {
                 const int vec = t + i * lanes, col = vec * kVec;
                 if (!EXACT && col >= p.cols) continue;
-                const V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec), w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+                const V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec), w = read_planes(w_smem, vec, width / kVec);
                 V8 r;
                 float o[kVec];
 #pragma unroll

@@ -19,8 +19,9 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) norm_forward_short_kernel
     const int width = lanes * VPT * kVec;
     float *w_smem = reinterpret_cast<float *>(smem + n.smem) - 2 * width, *b_smem = w_smem + width;
     for (int c = threadIdx.x; c < width; c += kShortWarps * 32) {
-        w_smem[c] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
-        b_smem[c] = c < p.cols && p.b ? load_param(p.b, p.params_bf16, c) : 0.f;
+        const int to = plane_of(c, width / kVec);
+        w_smem[to] = c < p.cols ? (p.w ? load_param(p.w, p.params_bf16, c) : 1.f) : 0.f;
+        b_smem[to] = c < p.cols && p.b ? load_param(p.b, p.params_bf16, c) : 0.f;
     }
     if (threadIdx.x == 0) {
         for (int k = 0; k < kShortWarps * S; ++k) ptx::mbar_init(ptx::smem_u32(&s_full[k]), 1);
@@ -142,9 +143,9 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) norm_forward_short_kernel
             for (int i = 0; i < VPT; ++i) {
                 const int vec = t + i * lanes, col = vec * kVec;
                 if (!EXACT && col >= p.cols) continue;
-                const V8 w = read_vec<false>(reinterpret_cast<const char *>(w_smem), vec);
+                const V8 w = read_planes(w_smem, vec, width / kVec);
                 V8 c;
-                if (FULL) c = read_vec<false>(reinterpret_cast<const char *>(b_smem), vec);
+                if (FULL) c = read_planes(b_smem, vec, width / kVec);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 x = mul2(v[i].p[k], rs);

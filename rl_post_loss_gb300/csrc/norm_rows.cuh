@@ -142,6 +142,8 @@ __device__ __forceinline__ void write_planes(float *base, int vec, int vecs, con
     reinterpret_cast<float4 *>(base)[vec] = make_float4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<float4 *>(base)[vecs + vec] = make_float4(v[4], v[5], v[6], v[7]);
 }
+// Where column c of 8 * vecs stands in planes.
+__device__ __forceinline__ int plane_of(int c, int vecs) { return (c & 4) * vecs + (c >> 3) * 4 + (c & 3); }
 __device__ __forceinline__ V8 read_planes(const float *base, int vec, int vecs) {
     const uint4 *q = reinterpret_cast<const uint4 *>(base);
     return f32_pairs(q[vec], q[vecs + vec]);

@@ -3,8 +3,10 @@
 // sums take few steps. Every warp has a ring of its own in shared memory; the copies of its next rows are under
 // way while it works on one batch. Rows that follow one another without a gap come in one copy.
 //
-// Bound by what a row costs beside its bytes, its shuffles and accesses to shared memory: 202752 x 128 bf16 layer norm 26 us forward
-// (60% of the measured copy rate), 40 us backward (59%).
+// Bound by what a row costs beside its bytes, its shuffles and accesses to shared memory: 202752 x 128 bf16 layer norm 25 us forward
+// (63% of the measured copy rate), 39 us backward (61%); 200000 x 512 78 us (77%) and 107 us (85%). (Two vectors a thread with the weights
+// in registers, twice the lanes a row: 202752 x 128 forward 31 us. Weights that lie as in memory instead of in planes: 26 and 39 us, 93
+// and 114 us; from int8 with a mask, 202752 x 128 backward, 72 against 76.)
 #pragma once
 
 #include "norm_rows.cuh"
