@@ -15,12 +15,11 @@
 #include <atomic>
 
 #include "act8.cuh"
+#include "norm_layout.cuh"
 
 namespace rlk {
 
-constexpr int kNormMaxCols = 16384;
-constexpr int kNormSMs = 152;
-constexpr int kNormWarps = 16;  // of a block of the backward pass, which has an SM for itself
+static_assert(kNormVec == kVec, "");
 
 struct NormForwardParams {
     RowMat x, residual, y, h;  // p = nullptr where there is none
@@ -50,22 +49,6 @@ struct NormBackwardParams {
     int32_t accumulate;  // dw and db are added to
     uint32_t *status;
 };
-
-// How the backward pass lays rows over blocks (norm_ring.cuh).
-constexpr int kNormDepth = 8;
-constexpr size_t kNormRingSmem = 225 * 1024;  // of a block, beside its barriers and sums
-struct NormTeams {
-    int mode;                                    // RowMode
-    int warps, vecs, blocks_per_sm;              // of a row; vectors of eight columns of a thread
-    int blocks;                                  // of the forward pass
-    int depth;                                   // rows' room of a team in shared memory
-    int w_in_smem;                               // the weight beside them, where registers have no room for it
-    int at_dy, at_ds, stage_bytes;               // of a row
-    size_t smem;
-};
-
-// Partial sums of dw and db, at most.
-int norm_backward_parts(int rows, int cols);
 
 cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream);
 cudaError_t launch_norm_forward_any(const NormForwardParams &p, const NormTeams &n, cudaStream_t stream);

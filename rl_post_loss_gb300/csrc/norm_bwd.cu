@@ -240,13 +240,11 @@ cudaError_t launch_join(const NormBackwardParams &p, int parts, cudaStream_t str
 
 // ---------------------------------------------------------------- which kernel
 
-int vectors(int cols) { return (cols + kVec - 1) / kVec; }
-
 template <int SRC, bool DYBF16>
 cudaError_t launch_short(const NormBackwardParams &p, int blocks, cudaStream_t stream) {
     const int es[3] = {from_act8(SRC) ? 1 : SRC == kHBf16 ? 2 : 4, DYBF16 ? 2 : 4, !p.dsummed.p ? 0 : p.dx.bf16 ? 2 : 4};
     const int64_t ld[3] = {from_act8(SRC) ? p.ckpt.ld_codes : p.x.ld, p.dy.ld, p.dsummed.ld};
-    const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
+    const int width = norm_short_width(p.cols);
     const NormShort n = norm_short(p.cols, es, ld, 3, p.mask != nullptr, kNormWarps, (size_t)width * 4, (size_t)kNormWarps * width * 4);
     const bool full = !p.rms || p.want_db;
     const bool exact = p.cols == width && !p.mask && !p.y.p && p.dx.fast;
@@ -257,66 +255,10 @@ cudaError_t launch_short(const NormBackwardParams &p, int blocks, cudaStream_t s
 #undef RLK_RUN
 }
 
-constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 512;  // what a block takes beside its rows
-
-// Three rows of a block in its ring, of which the last one is filled again a row late. (65536 x 6144 bf16, RMS: 389 us, with four
-// 410, with two 419; layer norm 16384 x 8192 164, 164 and 205.)
-constexpr int kBackwardDepth = 3;
-
-// A block per row, 128 registers a thread, so 16 warps on an SM: of the numbers of vectors a thread, the one whose
-// blocks take all rows soonest, by a row's time of its vectors and two more for the exchange of sums. Both sums with
-// four vectors a thread (kAnyRow: with three) do not fit the registers, and are taken for the
-// longest rows alone.
-NormTeams teams_of(const NormBackwardParams &p, int mode) {
-    const bool act8 = !p.x.p, full = !p.rms || p.want_db || starts_anywhere(mode);
-    const int vecs = vectors(p.cols), pad = starts_anywhere(mode) ? 32 : 0;
-    const auto bytes = [&](int es) { return (p.cols * es + 15) / 16 * 16 + pad; };
-    NormTeams n{};
-    n.mode = mode;
-    n.at_dy = bytes(act8 ? 1 : p.x.bf16 ? 2 : 4);
-    n.at_ds = n.at_dy + bytes(p.dy.bf16 ? 2 : 4);
-    n.stage_bytes = n.at_ds + (p.dsummed.p ? bytes(p.dx.bf16 ? 2 : 4) : 0);
-    if (mode == kWarpRow) {
-        n.warps = 1;
-        n.vecs = vecs > 96 ? 4 : 3;
-        n.blocks_per_sm = 1;
-        n.depth = (int)std::min<size_t>(kNormDepth, kNormRingSmem / (kNormWarps * n.stage_bytes));
-        n.smem = std::max((size_t)kNormWarps * n.depth * n.stage_bytes, (size_t)kNormWarps * n.vecs * 32 * kVec * 4);
-        return n;
-    }
-    double best = 0;
-    for (int v = 1; v <= 4; ++v) {
-        const int warps = (vecs + 32 * v - 1) / (32 * v);
-        if ((v - 1) * warps * 32 >= vecs) continue;  // fewer vectors a thread do
-        if (warps > kNormWarps || (v >= (mode == kAnyRow ? 3 : 4) && full && n.warps)) continue;
-        const bool regs = mode == kAnyRow ? v == 1 : v <= (mode == kShiftRow ? 2 : 3) || !full;
-        size_t w_bytes = regs ? 0 : (size_t)v * warps * 32 * kVec * 4;
-        int blocks = kNormWarps / warps;
-        while (blocks > 1 && blocks * (kBlockExtra + w_bytes + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
-        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (v == 4 ? 3.5 : 2));
-        if (n.warps && time >= best) continue;
-        best = time;
-        const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks - kBlockExtra);
-        n.w_in_smem = w_bytes + n.stage_bytes <= room;
-        if (!n.w_in_smem) w_bytes = 0;
-        n.warps = warps, n.vecs = v, n.blocks_per_sm = blocks;
-        n.depth = (int)std::min<size_t>(kBackwardDepth, (room - w_bytes) / n.stage_bytes);
-        n.smem = (size_t)n.depth * n.stage_bytes + w_bytes;
-    }
-    return n;
-}
-
 }  // namespace
 
-// As many blocks as run at once: one of 16 warps on an SM for rows that warps take, else of the warps that four
-// vectors a thread need.
-int norm_backward_parts(int rows, int cols) {
-    const int warps = (vectors(cols) + 127) / 128;
-    return (int)std::min<int64_t>(rows, kNormSMs * (kNormWarps / warps));
-}
-
 cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t stream) {
-    const bool act8 = !p.x.p, full = !p.rms || p.want_db;
+    const bool act8 = !p.x.p;
     const bool fast = p.dy.fast && (act8 ? p.ckpt.fast : p.x.fast) && (!p.dsummed.p || p.dsummed.fast) && p.dx.fast && (!p.y.p || p.y.fast);
     cudaError_t e = cudaErrorUnknown;
     int blocks;
@@ -326,11 +268,10 @@ cudaError_t launch_norm_backward(const NormBackwardParams &p, cudaStream_t strea
         e = act8 ? p.ckpt.e4m3 ? RLK_SHORT(kHE4M3) : RLK_SHORT(kHInt8) : p.x.bf16 ? RLK_SHORT(kHBf16) : RLK_SHORT(kHF32);
 #undef RLK_SHORT
     } else {
-        const bool any = !fast || (!act8 && p.x.bf16 && !p.dy.bf16);
-        // a warp per row where there are rows for all warps
-        const bool warp = !any && p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps;
-        const NormTeams n = teams_of(p, any ? act8 ? kShiftRow : kAnyRow : warp ? kWarpRow : kBlockRow);
-        blocks = std::min(p.rows, kNormSMs * n.blocks_per_sm);
+        const int es[3] = {act8 ? 1 : p.x.bf16 ? 2 : 4, p.dy.bf16 ? 2 : 4, !p.dsummed.p ? 0 : p.dx.bf16 ? 2 : 4};
+        const NormBackwardShape shape{p.rows, p.cols, es[0], es[1], es[2], p.rms != 0, p.want_db != 0};
+        const NormTeams n = norm_backward_teams(shape, norm_backward_mode(shape, fast));
+        blocks = norm_backward_blocks(shape, n);
 #define RLK_ROWS(H) (p.dy.bf16 ? launch_norm_rows_##H##_bf16(p, n, blocks, stream) : launch_norm_rows_##H##_f32(p, n, blocks, stream))
         e = act8 ? p.ckpt.e4m3 ? RLK_ROWS(e4m3) : RLK_ROWS(int8) : p.x.bf16 ? RLK_ROWS(bf16) : RLK_ROWS(f32);
 #undef RLK_ROWS

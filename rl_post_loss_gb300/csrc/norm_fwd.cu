@@ -6,8 +6,6 @@ namespace rlk {
 
 namespace {
 
-constexpr int kShortWarps = 24;  // 80 registers a thread
-
 // ---------------------------------------------------------------- short rows (norm_short.cuh)
 
 // EXACT: the threads' vectors are the row's columns to the last one, no mask, and rows of y on 16-byte boundaries.
@@ -176,13 +174,11 @@ __global__ void __launch_bounds__(kShortWarps * 32, 1) norm_forward_short_kernel
         for (int k = 0; k < S; ++k) ptx::mbar_wait(ring.full + k * 8, (phases >> k) & 1u, kNormWaitNs);
 }
 
-constexpr size_t kSmemOfSM = 228 * 1024, kBlockExtra = 1024 + 1024;  // what a block takes beside its rows
-
 template <bool BF16>
 cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
     const int es[2] = {BF16 ? 2 : 4, !p.residual.p ? 0 : BF16 ? 2 : 4};
     const int64_t ld[2] = {p.x.ld, p.residual.ld};
-    const int width = (p.cols <= 64 ? 2 : 4) * kVec * (p.cols <= 128 ? 4 : p.cols <= 256 ? 8 : 16);
+    const int width = norm_short_width(p.cols);
     const NormShort n = norm_short(p.cols, es, ld, 2, p.mask != nullptr, kShortWarps, (size_t)width * 8, 0);
     const bool full = !p.rms || p.b;
     const bool exact = p.cols == width && !p.mask && p.y.fast;
@@ -193,63 +189,9 @@ cudaError_t launch_short(const NormForwardParams &p, cudaStream_t stream) {
 #undef RLK_RUN
 }
 
-// Two rows of a block in its ring: with as many as fit, reads far ahead of the writes cost the memory's rate. (65536 x 6144
-// bf16, RMS: 246 us, with eight 281; 32768 x 16384: 317, 367.)
-constexpr int kForwardDepth = 2;
-
-// The blocks that run at once, or, for as many bytes to write as to read, blocks of eight rows for a warp or block, which
-// start when others end: they do not read and write all in step, and a slow SM takes fewer. Where the weights' way into shared memory
-// or arithmetic is what a block waits for, their starts cost more, and masked rows break the step too. (RMS with a
-// residual, us: 65536 x 6144 bf16 with an int8 checkpoint 599 -> 525, 32768 x 6144 fp32 527 -> 471, 8192 x 6144 bf16 72 -> 65; layer norm
-// so 534 -> 466; but with an e4m3 checkpoint 65536 x 5120 489 -> 576, without a residual 16384 x 6144 79 -> 88, with a mask 125 -> 132.)
-int blocks_of(const NormForwardParams &p, int mode, const NormTeams &n, int teams) {
-    const bool full = starts_anywhere(mode) || !p.rms || p.b;
-    const int at_once = std::min(p.rows, kNormSMs * n.blocks_per_sm), short_ones = p.rows / (8 * teams);
-    const bool apart = p.residual.p && !p.mask && !starts_anywhere(mode) && (!full || (mode == kBlockRow && n.vecs < 4 && !p.ckpt.codes));
-    return apart && short_ones >= 3 * at_once ? short_ones : at_once;
-}
-
-// A block per row, 16 warps on an SM: of the numbers of vectors a thread, the one whose blocks take all rows soonest, by a
-// row's time of its vectors and two or three more for its exchanges of sums and what else is done once a row. (16384 x
-// 8192 bf16: layer norm with two, three, four vectors 141, 147, 125 us, RMS with a residual 180, 174, 181 (without blocks of eight rows); 20000 x 5120: 156, 92,
-// 102 us; so layer norm with four, whose weights are read from shared memory, counts as 9.8.)
-NormTeams teams_of(const NormForwardParams &p, int mode) {
-    const int vecs = (p.cols + kVec - 1) / kVec, pad = starts_anywhere(mode) ? 32 : 0;
-    const bool full = starts_anywhere(mode) || !p.rms || p.b;
-    NormTeams n{};
-    n.mode = mode;
-    n.at_dy = (p.cols * (p.x.bf16 ? 2 : 4) + 15) / 16 * 16 + pad;
-    n.stage_bytes = n.at_dy * (p.residual.p ? 2 : 1);
-    if (mode == kWarpRow) {
-        n.warps = 1;
-        n.vecs = vecs > 96 ? 4 : 3;
-        n.blocks_per_sm = 1;
-        n.depth = (int)std::min<size_t>(kNormDepth, kNormRingSmem / (kForwardWarps * n.stage_bytes));
-        n.smem = (size_t)(kForwardWarps) * n.depth * n.stage_bytes;
-        n.blocks = blocks_of(p, mode, n, kForwardWarps);
-        return n;
-    }
-    double best = 0;
-    for (int v = 1; v <= 4; ++v) {
-        const int warps = (vecs + 32 * v - 1) / (32 * v);
-        if (warps > kForwardWarps || (v - 1) * warps * 32 >= vecs) continue;
-        if (n.warps && mode == kAnyRow && v > 2) continue;  // (registers)
-        // layer norm with four vectors a thread: weight and bias in shared memory, as registers have no room
-        size_t params = mode != kAnyRow && full && v == 4 ? (size_t)2 * v * warps * 32 * kVec * 4 : 0;
-        int blocks = kForwardWarps / warps;
-        while (blocks > 1 && blocks * (kBlockExtra + params + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
-        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : v == 4 ? 5.8 : 3));
-        if (n.warps && time >= best) continue;
-        best = time;
-        const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks - kBlockExtra);
-        n.w_in_smem = params + n.stage_bytes <= room;
-        if (!n.w_in_smem) params = 0;
-        n.warps = warps, n.vecs = v, n.blocks_per_sm = blocks;
-        n.depth = (int)std::min<size_t>(kForwardDepth, (room - params) / n.stage_bytes);
-        n.smem = (size_t)n.depth * n.stage_bytes + params;
-    }
-    n.blocks = blocks_of(p, mode, n, 1);
-    return n;
+NormForwardShape shape_of(const NormForwardParams &p) {
+    const int es = p.x.bf16 ? 2 : 4;
+    return NormForwardShape{p.rows, p.cols, es, p.residual.p ? es : 0, p.rms != 0, p.b != nullptr, p.mask != nullptr, p.ckpt.codes != nullptr};
 }
 
 }  // namespace
@@ -259,16 +201,11 @@ cudaError_t launch_norm_forward(const NormForwardParams &p, cudaStream_t stream)
     // 8920 x 9118 bf16 with a residual, which takes 182 so, and 112 between rows on 16-byte boundaries)
     const bool fast = p.x.fast && (!p.residual.p || p.residual.fast) && p.y.fast && (!p.h.p || p.h.fast) && (!p.ckpt.codes || p.ckpt.fast);
     if (fast && p.cols <= kShortCols) return p.x.bf16 ? launch_short<true>(p, stream) : launch_short<false>(p, stream);
-    if (!fast) {
-        // The pieces shifted into place, where 8-bit codes are made or a thread would hold more than two vectors' single columns,
-        // whose weights have no room in registers: 16000 x 3001 bf16 layer norm to int8 94 us (single columns 199), 8920 x 9118 bf16
-        // with a residual 182 (270), 8192 x 6145 layer norm 95 (99); but 8192 x 4095 61 (52), 30000 x 1031 fp32 with a residual 115 (88).
-        const bool shift = p.ckpt.codes || p.cols > 4096;
-        const NormTeams n = teams_of(p, shift ? kShiftRow : kAnyRow);
-        return shift ? launch_norm_forward_shift(p, n, stream) : launch_norm_forward_any(p, n, stream);
-    }
-    const bool full = !p.rms || p.b, warp = p.cols <= (full ? 768 : 1024) && p.rows >= kNormSMs * kForwardWarps;  // a warp per row where there are rows for all
-    const NormTeams n = teams_of(p, warp ? kWarpRow : kBlockRow);
+    const NormForwardShape shape = shape_of(p);
+    const RowMode mode = norm_forward_mode(shape, fast);
+    const NormTeams n = norm_forward_teams(shape, mode);
+    if (!fast) return mode == kShiftRow ? launch_norm_forward_shift(p, n, stream) : launch_norm_forward_any(p, n, stream);
+    const bool full = forward_full(shape, mode), warp = mode == kWarpRow;
 #define RLK_ROWS(BF16) (warp ? full ? launch_forward_rows<BF16, 3, true, kWarpRow>(p, n, stream) : n.vecs == 3 ? launch_forward_rows<BF16, 3, false, kWarpRow>(p, n, stream) : launch_forward_rows<BF16, 4, false, kWarpRow>(p, n, stream) \
                              : full ? launch_forward_vecs<BF16, true, kBlockRow>(p, n, stream) : launch_forward_vecs<BF16, false, kBlockRow>(p, n, stream))
     return p.x.bf16 ? RLK_ROWS(true) : RLK_ROWS(false);

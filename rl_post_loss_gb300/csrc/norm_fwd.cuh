@@ -17,8 +17,6 @@
 namespace rlk {
 
 
-constexpr int kForwardWarps = 16;  // of a block and of an SM: 128 registers a thread
-
 // h's 8-bit codes; a block of 32 columns is four lanes' vectors.
 template <int MODE, int VPT>
 __device__ __forceinline__ void store_act8(const Columns<MODE, VPT> &at, const Act8Mat &a, int64_t row, int i, const V8 &h) {
@@ -87,9 +85,9 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(Nor
     const auto copy_row = [&](int64_t row, int s) {  // by the team's thread 0
         const uint32_t full = full0 + s * 8, to = ptx::smem_u32(stages + s * n.stage_bytes);
         if (!starts_anywhere(MODE)) {
-            ptx::mbar_arrive_expect_tx(full, (uint32_t)n.stage_bytes);
-            ptx::bulk_g2s(to, x_row(row), (uint32_t)n.at_dy, full);
-            if (p.residual.p) ptx::bulk_g2s(to + n.at_dy, r_row(row), (uint32_t)n.at_dy, full);
+            ptx::mbar_arrive_expect_tx(full, (uint32_t)(n.copy_bytes[0] + n.copy_bytes[1]));
+            ptx::bulk_g2s(to, x_row(row), (uint32_t)n.copy_bytes[0], full);
+            if (p.residual.p) ptx::bulk_g2s(to + n.at_dy, r_row(row), (uint32_t)n.copy_bytes[1], full);
             return;
         }
         const int bytes = p.cols * (BF16 ? 2 : 4);

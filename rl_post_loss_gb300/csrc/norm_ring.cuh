@@ -64,10 +64,10 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         char *stage = stages + s * n.stage_bytes;
         const uint32_t full = full0 + s * 8, to = ptx::smem_u32(stage);
         if (!starts_anywhere(MODE)) {
-            ptx::mbar_arrive_expect_tx(full, (uint32_t)n.stage_bytes);
-            ptx::bulk_g2s(to, h_row(row), (uint32_t)n.at_dy, full);
-            ptx::bulk_g2s(to + n.at_dy, dy_row(row), (uint32_t)(n.at_ds - n.at_dy), full);
-            if (p.dsummed.p) ptx::bulk_g2s(to + n.at_ds, ds_row(row), (uint32_t)(n.stage_bytes - n.at_ds), full);
+            ptx::mbar_arrive_expect_tx(full, (uint32_t)(n.copy_bytes[0] + n.copy_bytes[1] + n.copy_bytes[2]));
+            ptx::bulk_g2s(to, h_row(row), (uint32_t)n.copy_bytes[0], full);
+            ptx::bulk_g2s(to + n.at_dy, dy_row(row), (uint32_t)n.copy_bytes[1], full);
+            if (p.dsummed.p) ptx::bulk_g2s(to + n.at_ds, ds_row(row), (uint32_t)n.copy_bytes[2], full);
             return;
         }
         const uint32_t bytes[3] = {window(h_row(row), p.cols * (kAct8 ? 1 : SRC == kHBf16 ? 2 : 4)), window(dy_row(row), p.cols * (DYBF16 ? 2 : 4)),

@@ -17,9 +17,6 @@
 
 namespace rlk {
 
-enum RowMode { kBlockRow, kWarpRow, kAnyRow, kShiftRow };
-constexpr bool starts_anywhere(int mode) { return mode == kAnyRow || mode == kShiftRow; }
-
 constexpr uint64_t kNormWaitNs = 1000000000ull;
 
 template <bool BF16>

@@ -13,37 +13,6 @@
 
 namespace rlk {
 
-constexpr int kShortCols = 512;
-
-// Up to three matrices whose rows come together.
-struct NormShort {
-    int lanes, vecs, depth;
-    int row_bytes[3];  // of a matrix's row in shared memory, 0: no such matrix
-    int at[3];         // where a matrix's rows begin in a stage
-    int whole[3];      // a batch is one copy
-    int stage_bytes;
-    size_t smem;
-};
-
-// `row_bytes`, `ld_bytes` of the matrices; `fixed` bytes of a block's shared memory for something else, after the rings.
-inline NormShort norm_short(int cols, const int *es, const int64_t *ld, int count, bool masked, int warps, size_t fixed, size_t least) {
-    NormShort n{};
-    n.vecs = cols <= 64 ? 2 : 4;
-    n.lanes = cols <= 128 ? 4 : cols <= 256 ? 8 : 16;
-    for (int k = 0; k < count; ++k) {
-        if (!es[k]) continue;
-        n.row_bytes[k] = (cols * es[k] + 15) / 16 * 16;
-        n.whole[k] = !masked && ld[k] * es[k] == n.row_bytes[k];
-        n.at[k] = n.stage_bytes;
-        n.stage_bytes += 32 / n.lanes * n.row_bytes[k];
-    }
-    n.depth = (int)((kNormRingSmem - fixed) / ((size_t)warps * n.stage_bytes));
-    n.depth = n.depth > kNormDepth ? kNormDepth : n.depth;
-    n.smem = (size_t)warps * n.depth * n.stage_bytes;
-    n.smem = (n.smem > least ? n.smem : least) + fixed;
-    return n;
-}
-
 // A warp's ring. Batch b is rows b (32 / lanes), ...; `base` and `pitch` are the matrices in memory, in bytes.
 struct ShortRing {
     const NormShort &n;
