@@ -117,7 +117,7 @@ inline NormTeams norm_forward_teams(const NormForwardShape &p, RowMode mode) {
         size_t params = mode != kAnyRow && full && v == 4 ? (size_t)2 * v * warps * 32 * kNormVec * 4 : 0;
         int blocks = kForwardWarps / warps;
         while (blocks > 1 && blocks * (kForwardExtra + params + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
-        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : v == 4 ? 5.8 : 3));
+        const double time = (double)(((int64_t)p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (p.rms ? 2 : v == 4 ? 5.8 : 3));
         if (n.warps && time >= best) continue;
         best = time;
         const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks - kForwardExtra);
@@ -175,7 +175,7 @@ inline NormTeams norm_backward_teams(const NormBackwardShape &p, RowMode mode) {
         size_t w_bytes = regs ? 0 : (size_t)v * warps * 32 * kNormVec * 4;
         int blocks = kNormWarps / warps;
         while (blocks > 1 && blocks * (kBackwardExtra + w_bytes + 2 * n.stage_bytes) > kSmemOfSM) --blocks;
-        const double time = (double)((p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (v == 4 ? 3.5 : 2));
+        const double time = (double)(((int64_t)p.rows + blocks * kNormSMs - 1) / (blocks * kNormSMs)) * (v + (v == 4 ? 3.5 : 2));
         if (n.warps && time >= best) continue;
         best = time;
         const size_t room = std::min(kNormRingSmem, kSmemOfSM / blocks - kBackwardExtra);

@@ -167,3 +167,8 @@ def run(tmp_path, rows, *flags):
 @pytest.mark.parametrize("rows", [(1, 37, 2431), (2432, 20000), (1 << 20,)], ids=str)
 def test_every_access_is_inside_the_allocation(tmp_path, rows):
     assert run(tmp_path, rows) > 1000000
+
+
+def test_the_most_rows_do_not_overflow(tmp_path):
+    """The arithmetic of a layout in range up to 2^31 - 1 rows (an overflow ends the program)."""
+    assert run(tmp_path, [2 ** 31 - 1, 2 ** 31 - 200], "-fsanitize=signed-integer-overflow", "-fsanitize-undefined-trap-on-error") > 1000000
