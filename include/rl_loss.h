@@ -577,8 +577,10 @@ typedef struct rl_ln_config {
  * no value out of range (max |x| <= 127 2^e or 448 2^e, e >= -126) and rounds
  * x / 2^e to the nearest code, ties to even; the values that codes stand for are
  * exact in fp32 and, from 2^-133 up, in bf16 (a value that rounding takes past the
- * largest finite one reads as that one). A block that holds NaN or infinity reads back as NaN. 33 bytes
- * for 32 values. */
+ * largest finite one reads as that one; to rl_loss_layer_norm_backward it is infinite).
+ * A block that holds NaN or infinity reads back as NaN. 33 bytes for 32 values.
+ * What a caller's own codes may hold besides: b = 0 (2^-127), int8 -128, and e4m3
+ * 0x7f and 0xff, which read as 480 and -480; everything under b = 255 is NaN. */
 typedef enum rl_act8_format {
     RL_ACT8_INT8 = 0, /* two's complement, -127 .. 127: steps of one size in a block */
     RL_ACT8_E4M3 = 1  /* 4 exponent and 3 mantissa bits, up to 448: steps relative to the value */

@@ -140,15 +140,17 @@ __device__ __forceinline__ V8 act8_decode(uint2 c, uint32_t b, bool e4m3, float 
     return r;
 }
 
-// act8_decode without branches, right for b <= 198 (and NaN for 255): beyond, values are above 1e21, whose squares
-// pass fp32's range, and a norm's statistics are not finite whatever it reads. (The e4m3 factor 2^120 s comes in
-// two steps, as s may be above 2^7.)
-template <bool E4M3>
-__device__ __forceinline__ V8 act8_decode_norm(uint2 c, uint32_t b) {
-    const float s = __uint_as_float(b << 23);
+// The factor of scale byte b: 2^(b - 127), NaN for 255. (Bit 22 is both 2^-127, for 0, and what makes an infinity NaN.)
+__device__ __forceinline__ float act8_factor(uint32_t b) { return __uint_as_float(b << 23 | (((b + 1u) & 255u) <= 1u ? 1u << 22 : 0u)); }
+
+// What eight codes stand for in fp32, plus `add` (ADD), without branches; a value past fp32's range is infinite. `s` is the
+// block's act8_factor: a code's own value is exact and its product with a power of two is too, so that the sum is rounded once.
+template <bool E4M3, bool ADD>
+__device__ __forceinline__ V8 act8_decode_plus(uint2 c, float s, f32x2 add) {
+    const f32x2 mul = pack2(s, s);
     V8 r;
     if (E4M3) {
-        const f32x2 up = pack2(0x1p64f, 0x1p64f), mul = pack2(s * 0x1p56f, s * 0x1p56f);
+        const f32x2 up = pack2(0x1p120f, 0x1p120f);
         const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -156,16 +158,18 @@ __device__ __forceinline__ V8 act8_decode_norm(uint2 c, uint32_t b) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 x[j] = (uint32_t)((int32_t)__byte_perm(w[i >> 1], 0u, 0x0444u | (uint32_t)((2 * i + j) & 3) << 12) >> 4) & 0x87f00000u;
-            r.p[i] = mul2(mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), up), mul);
+            r.p[i] = mul2(pack2(__uint_as_float(x[0]), __uint_as_float(x[1])), up);
         }
     } else {
-        const f32x2 mul = pack2(s, s), off = pack2(-8388736.f * s, -8388736.f * s);
+        const f32x2 off = pack2(-8388736.f, -8388736.f);
         const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            r.p[i] = fma2(pack2(__uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | (2 * i & 3))),
-                                __uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | ((2 * i + 1) & 3)))), mul, off);
+            r.p[i] = add2(pack2(__uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | (2 * i & 3))),
+                                __uint_as_float(__byte_perm(w[i >> 1], 0x4b000000u, 0x7440u | ((2 * i + 1) & 3)))), off);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = ADD ? fma2(r.p[i], mul, add) : mul2(r.p[i], mul);
     return r;
 }
 

@@ -84,6 +84,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
         uint32_t scale_next[kScales] = {};
         if (batch + step < batches) row_data(batch + step, mine_next, on_next, mean_next, rstd_next, scale_next);
         const int64_t row = batch * ring.per + slot;
+        if (kAct8)
+#pragma unroll
+            for (int i = 0; i < kScales; ++i) scale[i] = __float_as_uint(act8_factor(scale[i]));  // the factors
         if (__any_sync(0xffffffffu, on)) {
             if (!dead && !ptx::mbar_wait(ring.full + s * 8, (phases >> s) & 1u, kNormWaitNs)) {
                 dead = true;
@@ -100,12 +103,12 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
             for (int i = 0; i < VPT; ++i) {
                 const int vec = t + i * lanes, col = vec * kVec;
                 if (!EXACT && col >= p.cols) continue;
-                V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec);
+                V8 h = read_h<SRC, FULL>(sh, vec, __uint_as_float(scale[kAct8 ? i : 0]), nm), g = read_vec<DYBF16>(sdy, vec);
                 if (!EXACT && col + kVec > p.cols) h = clipped(h, col, p.cols), g = clipped(g, col, p.cols);
                 const V8 w = read_planes(w_smem, vec, width / kVec);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, w.p[k]);
+                    const f32x2 d = less_mean<SRC, FULL>(h.p[k], nm), r = mul2(g.p[k], rs), u = mul2(r, w.p[k]);
                     dw[i].p[k] = fma2(r, d, dw[i].p[k]);
                     if (FULL) {
                         db[i].p[k] = add2(db[i].p[k], g.p[k]);
@@ -124,19 +127,22 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
         c1 = FULL && !p.rms ? c1 * p.inv_cols : 0.f;
         c2 = c2 * p.inv_cols * rstd * rstd;
         const f32x2 o1 = pack2(-c1, -c1), nk = pack2(-c2, -c2);
+        if (kAct8)
+#pragma unroll
+            for (int i = 0; i < kScales; ++i) asm volatile("" : "+r"(scale[i]));  // (pairs of it made again, not kept: registers)
         if (on) {
             const int64_t out = row * p.dx.ld;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int vec = t + i * lanes, col = vec * kVec;
                 if (!EXACT && col >= p.cols) continue;
-                const V8 h = read_h<SRC>(sh, vec, scale[kAct8 ? i : 0]), g = read_vec<DYBF16>(sdy, vec), w = read_planes(w_smem, vec, width / kVec);
+                const V8 h = read_h<SRC, FULL>(sh, vec, __uint_as_float(scale[kAct8 ? i : 0]), nm), g = read_vec<DYBF16>(sdy, vec), w = read_planes(w_smem, vec, width / kVec);
                 V8 r;
                 float o[kVec];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 rr = mul2(g.p[k], rs), u = FULL ? fma2(rr, w.p[k], o1) : mul2(rr, w.p[k]);
-                    r.p[k] = fma2(FULL ? add2(h.p[k], nm) : h.p[k], nk, u);
+                    r.p[k] = fma2(less_mean<SRC, FULL>(h.p[k], nm), nk, u);
                 }
                 if (p.dsummed.p) {
                     const V8 q = x_bf16 ? read_vec<true>(sds, vec) : read_vec<false>(sds, vec);
@@ -148,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward_short_kernel(NormBa
                     if (p.b) load_params(p.b, p.params_bf16, p.params_fast, col, p.cols, b);
                     V8 v = pairs_of(b);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v.p[k] = fma2(mul2(add2(h.p[k], nm), rs), w.p[k], v.p[k]);
+                    for (int k = 0; k < 4; ++k) v.p[k] = fma2(mul2(less_mean<SRC, FULL>(h.p[k], nm), rs), w.p[k], v.p[k]);
                     floats_of(v, o);
                     store_row(p.y, row, col, p.cols, o);
                 }

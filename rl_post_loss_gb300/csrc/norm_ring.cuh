@@ -22,16 +22,20 @@ namespace rlk {
 
 enum HSource { kHBf16, kHF32, kHInt8, kHE4M3 };
 constexpr bool from_act8(int src) { return src >= kHInt8; }
-template <int SRC>
-__device__ __forceinline__ V8 read_h(const char *row, int vec, uint32_t scale) {
+// A vector of h, or, from codes, of d = h - mean (FULL = false: h), which takes no more steps than h; `nm` is -mean twice.
+template <int SRC, bool FULL>
+__device__ __forceinline__ V8 read_h(const char *row, int vec, float scale, f32x2 nm) {
     if (!from_act8(SRC)) return read_vec<SRC == kHBf16>(row, vec);
-    return act8_decode_norm<SRC == kHE4M3>(*reinterpret_cast<const uint2 *>(row + vec * 8), scale);
+    return act8_decode_plus<SRC == kHE4M3, FULL>(*reinterpret_cast<const uint2 *>(row + vec * 8), scale, nm);
 }
-template <int SRC>
-__device__ __forceinline__ V8 read_h_shifted(const char *row, int shift, int vec, uint32_t scale) {
+template <int SRC, bool FULL>
+__device__ __forceinline__ V8 read_h_shifted(const char *row, int shift, int vec, float scale, f32x2 nm) {
     if (!from_act8(SRC)) return read_shifted<SRC == kHBf16>(row, shift, vec);
-    return act8_decode_norm<SRC == kHE4M3>(codes_shifted(row, shift, vec), scale);
+    return act8_decode_plus<SRC == kHE4M3, FULL>(codes_shifted(row, shift, vec), scale, nm);
 }
+template <int SRC, bool FULL>
+__device__ __forceinline__ f32x2 less_mean(f32x2 h, f32x2 nm) { return FULL && !from_act8(SRC) ? add2(h, nm) : h; }
+
 template <int SRC, bool DYBF16, int VPT, bool FULL, int MODE>
 __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(NormBackwardParams p, NormTeams n) {
     constexpr bool kAct8 = from_act8(SRC), kWInRegs = MODE == kAnyRow ? VPT == 1 : VPT <= (MODE == kShiftRow ? 2 : 3) || !FULL;  // (else no room is left)
@@ -106,7 +110,8 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
     constexpr int kScales = kAct8 ? VPT : 1;
     bool dead = false, on = true;
     float mean = 0.f, rstd = 0.f;
-    uint32_t scale[kScales];
+    float scale[kScales];
+    uint32_t scale_first[kScales] = {};
     const auto row_data = [&](int64_t row, bool &o, float &m, float &r, uint32_t (&sc)[kScales]) {
         if (row >= p.rows) return;
         o = !p.mask || p.mask[row];
@@ -119,7 +124,9 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                 if (!at.none(i)) sc[i] = q[at.vec(i) >> 2];
         }
     };
-    row_data(first, on, mean, rstd, scale);
+    row_data(first, on, mean, rstd, scale_first);
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) scale[i] = act8_factor(scale_first[i]);
     uint32_t phases = 0;  // of the stages' barriers
     int s = 0, last = 0, turn = 0;
     for (int64_t row = first; row < p.rows; row += step) {
@@ -133,13 +140,13 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
 
         const char *stage = stages + s * n.stage_bytes, *sh = stage, *sdy = stage + n.at_dy, *sds = stage + n.at_ds;
         const int h_shift = row_shift<MODE>(h_row(row)), dy_shift = row_shift<MODE>(dy_row(row)), ds_shift = row_shift<MODE>(ds_row(row));
+        const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
         const auto get_h = [&](int i) -> V8 {
             if constexpr (MODE == kAnyRow) return at.template read<SRC == kHBf16>(sh, h_shift, i);  // (no codes)
-            if constexpr (MODE == kShiftRow) return read_h_shifted<SRC>(sh, h_shift, at.vec(i), scale[kScales > 1 ? i : 0]);
-            return read_h<SRC>(sh, at.vec(i), scale[kScales > 1 ? i : 0]);
+            if constexpr (MODE == kShiftRow) return read_h_shifted<SRC, FULL>(sh, h_shift, at.vec(i), scale[kScales > 1 ? i : 0], nm);
+            return read_h<SRC, FULL>(sh, at.vec(i), scale[kScales > 1 ? i : 0], nm);
         };
         float c1 = 0.f, c2 = 0.f;
-        const f32x2 nm = pack2(-mean, -mean), rs = pack2(rstd, rstd);
         if (on) {
             if (!dead && !ptx::mbar_wait(full0 + s * 8, (phases >> s) & 1u, kNormWaitNs)) {
                 dead = true;
@@ -155,7 +162,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                 const V8 ww = weight(i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const f32x2 d = FULL ? add2(h.p[k], nm) : h.p[k], r = mul2(g.p[k], rs), u = mul2(r, ww.p[k]);
+                    const f32x2 d = less_mean<SRC, FULL>(h.p[k], nm), r = mul2(g.p[k], rs), u = mul2(r, ww.p[k]);
                     dw[i].p[k] = fma2(r, d, dw[i].p[k]);
                     if (FULL) {
                         db[i].p[k] = add2(db[i].p[k], g.p[k]);
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const f32x2 rr = mul2(g.p[k], rs), u = FULL ? fma2(rr, ww.p[k], o1) : mul2(rr, ww.p[k]);
-                    r.p[k] = fma2(FULL ? add2(h.p[k], nm) : h.p[k], nk, u);
+                    r.p[k] = fma2(less_mean<SRC, FULL>(h.p[k], nm), nk, u);
                 }
                 if (p.dsummed.p) {
                     const V8 d = x_bf16 ? at.template read<true>(sds, ds_shift, i) : at.template read<false>(sds, ds_shift, i);
@@ -196,7 +203,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
                 if (p.y.p) {
                     V8 u = at.params(p.b, p.params_bf16, p.params_fast, i, 0.f);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) u.p[k] = fma2(mul2(add2(h.p[k], nm), rs), ww.p[k], u.p[k]);
+                    for (int k = 0; k < 4; ++k) u.p[k] = fma2(mul2(less_mean<SRC, FULL>(h.p[k], nm), rs), ww.p[k], u.p[k]);
                     at.store(p.y, row, i, u);
                 }
                 if (starts_anywhere(MODE) || !plain)
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(kNormWarps * 32, 1) norm_backward_ring_kernel(
         }
         on = on_next, mean = mean_next, rstd = rstd_next;
 #pragma unroll
-        for (int i = 0; i < kScales; ++i) scale[i] = scale_next[i];
+        for (int i = 0; i < kScales; ++i) scale[i] = act8_factor(scale_next[i]);
         last = s;
         s = s + 1 == S ? 0 : s + 1;
     }

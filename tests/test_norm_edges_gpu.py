@@ -37,3 +37,84 @@ def test_fp32_rows_that_end_inside_a_vector(rows, cols, kind, residual):
     nh.assert_within("dweight", back["dweight"], dw, e_dw)
     if b is not None:
         nh.assert_within("dbias", back["dbias"], db, e_db)
+
+
+def any_scale(rows, cols, fmt, at=0):
+    """A checkpoint with every scale byte and every code, as a caller may make one; rows of codes `at` bytes off 16-byte boundaries."""
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    blocks = (cols + 31) // 32
+    ld = (cols + at + 15) // 16 * 16
+    codes = torch.randint(0, 256, (rows, ld), generator=g, device="cuda", dtype=torch.uint8)[:, at:at + cols]
+    scales = (torch.arange(rows * blocks, device="cuda") % 256).to(torch.uint8).view(rows, blocks)
+    return capi.Act8(codes, scales, fmt)
+
+
+@pytest.mark.parametrize("rows,cols,at", [(300, 64, 0), (300, 128, 0), (300, 500, 0), (5000, 640, 0), (5000, 1000, 0), (60, 6144, 0), (60, 16384, 0), (60, 4097, 3),
+                                          (60, 6145, 1)])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_the_backward_pass_reads_what_unpacking_gives(rows, cols, at, kind, fmt):
+    """With mean 0, rstd 1 and no weight the output made again is the norm's input itself: the same bits as act8_unpack's for
+    every scale byte, those that act8_pack does not make among them (but what is past fp32's range stays infinite)."""
+    a = any_scale(rows, cols, fmt, at)
+    dy = torch.zeros((rows, cols), device="cuda")
+    y = torch.empty_like(dy)
+    mean = torch.zeros(rows, device="cuda") if kind == "layer" else None
+    capi.layer_norm_backward(dy, None, mean, torch.ones(rows, device="cuda"), checkpoint=a, kind=kind, want_dweight=False, y=y)
+    want = capi.act8_unpack(a, dtype=F32)
+    assert nh.same(y.clamp(-torch.finfo(F32).max, torch.finfo(F32).max), want)
+    known = torch.ones_like(want, dtype=torch.bool) if fmt == "int8" else (a.codes & 127) != 127
+    exact = nh.values64(a.codes.cpu(), a.scales.cpu(), fmt, F32)
+    assert nh.same(torch.where(known, want, torch.zeros_like(want)), torch.where(known.cpu(), exact, torch.zeros_like(exact)))
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 64), (40, 128), (3000, 1024), (40, 2048), (40, 8192)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("power", [20, 84, 112])
+def test_rows_of_one_large_value_from_a_checkpoint(rows, cols, fmt, power):
+    """Their variance is 0 and everything is finite (the mean of 2^n equal powers of two is exact), so the gradient from
+    the checkpoint, which holds them exactly, is the one from the rows."""
+    x = torch.full((rows, cols), 2.0 ** power, device="cuda")
+    dy = torch.randn((rows, cols), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    f = capi.layer_norm(x, want_stats=True, checkpoint=fmt, eps=EPS, device_status=status)
+    assert nh.same(f["mean"], torch.full((rows,), 2.0 ** power)) and (f["y"] == 0).all()
+    got = capi.layer_norm_backward(dy, None, f["mean"], f["rstd"], checkpoint=f["checkpoint"], want_dbias=True, device_status=status)
+    assert int(status) == 0 and (got["dweight"] == 0).all()
+    dx, _, db, e_dx, _, e_db = nh.backward64(x.cpu(), dy.cpu(), None, f["mean"].cpu(), f["rstd"].cpu(), "layer")
+    nh.assert_within("dx", got["dx"], dx, e_dx, F32)
+    nh.assert_within("dbias", got["dbias"], db, e_db)
+
+
+@pytest.mark.parametrize("rows,cols", [(40, 128), (3000, 640), (40, 6144), (40, 6145)])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_rows_that_are_not_finite_through_a_checkpoint(rows, cols, kind, fmt):
+    """A row that holds NaN or infinity: its gradient is not a number, it is reported, and the other rows have theirs; with
+    the row masked nothing of it is seen."""
+    bit = 1 << capi.CODES["RL_ERR_NONFINITE"]
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x, dy = (torch.randn((rows, cols), generator=g, device="cuda") for _ in range(2))
+    w = torch.randn(cols, generator=g, device="cuda")
+
+    def both(x, mask=None):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        f = capi.layer_norm(x, w, kind=kind, want_stats=True, checkpoint=fmt, mask=mask, device_status=status)
+        first = int(status)
+        status.zero_()
+        b = capi.layer_norm_backward(dy, w, f["mean"], f["rstd"], checkpoint=f["checkpoint"], kind=kind, mask=mask, device_status=status)
+        return b, first, int(status)
+
+    keep = torch.ones(rows, dtype=torch.uint8, device="cuda")
+    keep[7] = 0
+    good, first, second = both(x, keep)
+    assert first == 0 and second == 0
+    for value in (float("nan"), float("inf"), -float("inf")):
+        bad = x.clone()
+        bad[7, cols // 2] = value
+        got, first, second = both(bad)
+        assert first == bit and second == bit
+        assert got["dx"][7].isnan().all() and nh.same(got["dx"][keep != 0], good["dx"][keep != 0])
+        got, first, second = both(bad, keep)
+        assert first == 0 and second == 0
+        assert nh.same(got["dx"], good["dx"]) and nh.same(got["dweight"], good["dweight"])
