@@ -626,6 +626,7 @@ class Act8:
         if codes.dim() != 2 or not codes.is_cuda:
             raise ValueError("codes is a CUDA tensor [rows, columns]")
         rows, cols = codes.shape
+        _check_sizes(rows, cols)
         blocks = (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
         c, ld_codes = _like("codes", codes, rows, cols, torch.uint8, codes.device)
         s, ld_scales = _like("scales", scales, rows, blocks, torch.uint8, codes.device)
@@ -662,6 +663,7 @@ def act8_empty(rows: int, cols: int, format: str = "int8", device="cuda") -> Act
         raise ValueError("format is 'int8' or 'e4m3'")
     if rows < 0 or cols < 1:
         raise ValueError("an 8-bit checkpoint has a column at least")
+    _check_sizes(rows, cols)
     ld, blocks = (cols + 15) & ~15, (cols + ACT8_BLOCK - 1) // ACT8_BLOCK
     a = Act8.__new__(Act8)
     a._buffer = torch.empty(rows * (ld + blocks), dtype=torch.uint8, device=device)
@@ -686,6 +688,12 @@ def _float_code(name: str, dtype) -> int:
     raise ValueError(f"{name} is torch.float32 or torch.bfloat16")
 
 
+def _check_sizes(rows: int, cols: int) -> None:
+    """The C entries take 32-bit sizes, and ctypes passes on the low 32 bits of a longer one."""
+    if rows > 0x7fffffff or cols > 0x7fffffff:
+        raise ValueError("a matrix has fewer than 2^31 rows and columns")
+
+
 def _matrix(name: str, t):
     """(rows, cols, dtype code, pointer, row stride) of a CUDA matrix with contiguous rows."""
     if t.dim() != 2 or not t.is_cuda:
@@ -693,6 +701,7 @@ def _matrix(name: str, t):
     (rows, cols), (ld, step) = t.shape, t.stride()
     if (step != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"the rows of {name} are contiguous and do not overlap")
+    _check_sizes(rows, cols)
     return rows, cols, _float_code(name, t.dtype), t.data_ptr(), ld if rows > 1 else cols
 
 

@@ -197,3 +197,35 @@ def test_normed_projection_refuses_without_a_handle():
 
 def test_struct_sizes_match_the_header():
     assert ctypes.sizeof(capi.rl_ln_config) == 24 and ctypes.sizeof(capi.rl_act8) == 40 and ctypes.sizeof(capi.rl_loss_final_norm) == 64
+
+
+class Tall:
+    """A CUDA matrix of this shape as far as the binding's checks look (no memory: an address that is never followed)."""
+    is_cuda, dtype, device = True, torch.float32, torch.device("cuda", 0)
+
+    def __init__(self, rows, cols, dtype=torch.float32):
+        self.shape, self.dtype = (rows, cols), dtype
+
+    def dim(self):
+        return 2
+
+    def stride(self, k=None):
+        return (self.shape[1], 1) if k is None else (self.shape[1], 1)[k]
+
+    def data_ptr(self):
+        return FAKE
+
+    def get_device(self):
+        return 0
+
+
+@pytest.mark.parametrize("rows,cols", [(2 ** 31, 1), (2 ** 32 + 3, 64), (1, 2 ** 32 + 64)])
+def test_sizes_past_32_bits_are_refused(rows, cols):
+    """The C entries take 32-bit sizes; ctypes would pass the low 32 bits of a longer one without a word."""
+    with pytest.raises(ValueError, match="2\\^31"):
+        capi._matrix("x", Tall(rows, cols))
+    with pytest.raises(ValueError, match="2\\^31"):
+        capi.act8_empty(rows, cols, "int8", "meta")
+    with pytest.raises(ValueError, match="2\\^31"):
+        capi.Act8(Tall(rows, cols, torch.uint8), Tall(rows, (cols + 31) // 32, torch.uint8), "int8")
+    assert capi._matrix("x", Tall(2 ** 31 - 1, 2))[0] == 2 ** 31 - 1
