@@ -20,12 +20,15 @@ enum RlKernelClass {
     kProjBwd,     // both products of the projection backward (one tcgen05 launch per chunk)
     kEntropyFix,  // the entropy of rows holding -inf logits
     kPolicyKl,    // the row kernel of the loss with a KL term
+    kNormForward,   // the norm before the projection
+    kNormBackward,  // and its backward pass, with the sum of its blocks' partial sums
     kNumKernels
 };
 static const char *const kKernelNames[kNumKernels] = {"seg_prep",  "token_prep", "row_loss", "seg_reduce",
                                                       "final_reduce", "proj_gemm", "proj_rows", "proj_bwd",
-                                                      "entropy_fix",  "policy_kl"};
-constexpr size_t kProfSlotsPerCall = 160;  // enough for a projection call of 32 chunks (or a host call of 64 blocks)
+                                                      "entropy_fix",  "policy_kl",  "norm_forward", "norm_backward"};
+static_assert(kNumKernels <= RL_PROFILE_MAX_KERNELS, "");
+constexpr size_t kProfSlotsPerCall = 200;  // enough for a projection call of 32 chunks (or a host call of 64 blocks)
 constexpr int kMaxCopyChunks = 64;         // logits blocks of rl_loss_forward_backward_from_host
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

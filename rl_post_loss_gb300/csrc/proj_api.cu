@@ -262,7 +262,9 @@ rl_status projection_pass(rl_loss_handle_s *h, const void *hidden, int64_t ld_hi
         const int m = T - r0 < h->proj_chunk ? T - r0 : h->proj_chunk;
         const char *hc = reinterpret_cast<const char *>(hidden) + (norm ? 0 : (size_t)r0 * ld_hidden * 2);
         if (norm) {
+            slot = h->prof_begin(kNormForward, stream);
             const rl_status st = norm->forward(r0, m, stream_ptr);
+            h->prof_end(slot, stream);
             if (st != RL_OK) return st == RL_ERR_CUDA ? cuda_fail(h, cudaPeekAtLastError()) : st;
             launches += 1;
         }
@@ -363,7 +365,9 @@ rl_status projection_pass(rl_loss_handle_s *h, const void *hidden, int64_t ld_hi
         if (e != cudaSuccess) return cuda_fail(h, e);
         launches += 1;
         if (norm) {
+            slot = h->prof_begin(kNormBackward, stream);
             const rl_status st = norm->backward(r0, m, ci > 0, stream_ptr);
+            h->prof_end(slot, stream);
             if (st != RL_OK) return st == RL_ERR_CUDA ? cuda_fail(h, cudaPeekAtLastError()) : st;
             launches += norm->io->dweight || norm->io->dbias ? 2 : 1;
         }
