@@ -118,3 +118,52 @@ def test_rows_that_are_not_finite_through_a_checkpoint(rows, cols, kind, fmt):
         got, first, second = both(bad, keep)
         assert first == 0 and second == 0
         assert nh.same(got["dx"], good["dx"]) and nh.same(got["dweight"], good["dweight"])
+
+
+@pytest.mark.parametrize("rows,cols", [(5000, 513), (5000, 600), (20000, 640), (5000, 776), (5000, 1000), (5000, 1024), (1300, 4096), (1000, 6144), (700, 8200),
+                                       (9000, 128), (9000, 200), (2500, 512), (1000, 1031)])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_codes_that_the_norm_writes_for_many_rows(rows, cols, fmt, dtype):
+    """Bit for bit those of act8_pack for the same rows, in the kernels that calls of many rows take, with and without a
+    mask, and (RMS, layer norm) in their two forms."""
+    g = torch.Generator(device="cuda").manual_seed(rows + cols)
+    layout = "tight" if cols % 8 == 0 or cols == 1031 else "pad"
+    spread = torch.exp2(torch.randint(-20, 20, (1, (cols + 31) // 32), generator=g, device="cuda").float()).repeat_interleave(32, 1)[:, :cols]
+    x, res = ((torch.randn((rows, cols), generator=g, device="cuda") * spread).to(dtype) for _ in range(2))
+    h = (x.float() + res.float()).to(dtype)
+    mask = (torch.rand(rows, generator=g, device="cuda") < 0.7).to(torch.uint8)
+    mask[0], mask[-1] = 0, 1
+    w = torch.ones(cols, device="cuda")
+    for kind in ("layer", "rms"):
+        for m in (None, mask):
+            for r in (None, res):
+                if r is None and m is None:
+                    continue  # as with a mask
+                got = capi.layer_norm(nh.on_gpu(x, layout), w, kind=kind, residual=None if r is None else nh.on_gpu(r, layout), mask=m, checkpoint=fmt)
+                want = x if r is None else h
+                if m is not None:
+                    want = torch.where(m[:, None] != 0, want, torch.zeros((), dtype=dtype, device="cuda"))
+                packed = capi.act8_pack(want, format=fmt)
+                assert torch.equal(got["checkpoint"].codes, packed.codes) and torch.equal(got["checkpoint"].scales, packed.scales), (kind, m is None, r is None)
+
+
+@pytest.mark.parametrize("cols", [4, 12, 20, 36, 60, 68, 132, 260, 388, 508])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_short_fp32_rows_that_end_inside_a_vector(cols, kind):
+    """Rows of 16-byte pieces without gaps, whose last vector is read into the row behind it."""
+    rows = 3001
+    g = torch.Generator().manual_seed(cols)
+    x, res, dy = (torch.randn((rows, cols), generator=g) for _ in range(3))
+    w, b = torch.randn(cols, generator=g), torch.randn(cols, generator=g) if kind == "layer" else None
+    wg, bg = w.cuda(), None if b is None else b.cuda()
+    got = capi.layer_norm(x.cuda(), wg, bg, kind=kind, eps=EPS, residual=res.cuda(), want_stats=True)
+    y, h, mean, rstd, e_y, e_mean, e_rstd = nh.forward64(x, w, b, kind, EPS, res)
+    nh.assert_within("y", got["y"], y, e_y, F32)
+    nh.assert_within("rstd", got["rstd"], rstd, e_rstd, F32)
+    back = capi.layer_norm_backward(dy.cuda(), wg, got["mean"], got["rstd"], x=got["summed"], kind=kind, dsummed=res.cuda(), want_dbias=b is not None)
+    dx, dw, db, e_dx, e_dw, e_db = nh.backward64(h, dy, w, None if b is None else got["mean"].cpu(), got["rstd"].cpu(), kind, res)
+    nh.assert_within("dx", back["dx"], dx, e_dx, F32)
+    nh.assert_within("dweight", back["dweight"], dw, e_dw)
+    if b is not None:
+        nh.assert_within("dbias", back["dbias"], db, e_db)
