@@ -643,7 +643,7 @@ RL_LOSS_API rl_status rl_loss_act8_unpack(int32_t x_dtype, int32_t rows, int32_t
  * config->y_dtype RL_BF16. dweight and dbias [H] fp32 (or NULL) are overwritten,
  * summed over the chunks in their order. Results are those of
  * rl_loss_layer_norm, rl_loss_fused_projection_forward_backward and
- * rl_loss_layer_norm_backward (the latter summed chunk by chunk). Everything else,
+ * rl_loss_layer_norm_backward, the norm's called chunk by chunk. Everything else,
  * and the errors, as there; the device status is the handle's. `workspace` as for
  * rl_loss_layer_norm_backward, of rl_loss_normed_projection_workspace_bytes (which is
  * 0 before rl_loss_projection_setup). */
