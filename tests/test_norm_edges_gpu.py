@@ -167,3 +167,70 @@ def test_short_fp32_rows_that_end_inside_a_vector(cols, kind):
     nh.assert_within("dweight", back["dweight"], dw, e_dw)
     if b is not None:
         nh.assert_within("dbias", back["dbias"], db, e_db)
+
+
+@pytest.mark.parametrize("own_stream", [True, False])
+def test_two_threads_at_once(own_stream):
+    """Calls of two threads, on a stream each and on one stream, with the workspaces that the binding keeps."""
+    import threading
+    rows, widths = 700, (640, 6144)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    data = [[torch.randn((rows, c), generator=g, device="cuda").to(BF16) for _ in range(2)] + [torch.randn(c, generator=g, device="cuda")] for c in widths]
+
+    def step(x, dy, w, stream=None):
+        f = capi.layer_norm(x, w, want_stats=True, checkpoint="int8", stream=stream)
+        b = capi.layer_norm_backward(dy, w, f["mean"], f["rstd"], checkpoint=f["checkpoint"], want_dbias=True, stream=stream)
+        return [f["y"], b["dx"], b["dweight"], b["dbias"]]
+
+    want = [[t.clone() for t in step(*d)] for d in data]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in widths]
+    got, errors = [None, None], []
+
+    def work(k):
+        try:
+            with torch.cuda.stream(streams[k if own_stream else 0]):
+                got[k] = [step(*data[k]) for _ in range(30)]
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for k in range(2):
+        assert all(nh.same(a, b) for run in got[k] for a, b in zip(run, want[k]))
+
+
+def test_the_first_call_of_a_process_captured(tmp_path):
+    """Kernels that no call has loaded yet, in a graph."""
+    import subprocess
+    import sys
+    code = """
+import torch
+from rl_post_loss_gb300 import capi
+x, dy = (torch.randn((300, 640), device="cuda") for _ in range(2))
+w = torch.ones(640, device="cuda")
+y, dx, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+mean, rstd = torch.empty(300, device="cuda"), torch.empty(300, device="cuda")
+ws = torch.empty(capi.rl_loss_layer_norm_workspace_bytes(300, 640), dtype=torch.uint8, device="cuda")
+a = capi.act8_empty(300, 640, "int8", x.device)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    capi.layer_norm(x, w, y=y, mean=mean, rstd=rstd, checkpoint=a)
+    capi.layer_norm_backward(dy, w, mean, rstd, checkpoint=a, dx=dx, dweight=dw, workspace=ws)
+graph.replay()
+torch.cuda.synchronize()
+f = capi.layer_norm(x, w, want_stats=True, checkpoint="int8")
+b = capi.layer_norm_backward(dy, w, f["mean"], f["rstd"], checkpoint=f["checkpoint"])
+assert torch.equal(y, f["y"]) and torch.equal(dx, b["dx"]) and torch.equal(dw, b["dweight"])
+print("same")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, timeout=300)
+    assert done.returncode == 0 and b"same" in done.stdout, done.stdout.decode()[-2000:]
