@@ -1,5 +1,5 @@
-// The backward pass of the norms (mathematics: norm.cuh): the kernels for short rows and for rows that start
-// anywhere, the sum of the blocks' partial sums, and which kernel takes a call.
+// The backward pass of the norms (mathematics: norm.cuh): the kernel for short rows, the sum of the blocks' partial sums, and
+// which kernel takes a call (those of longer rows and of rows that start anywhere: norm_ring.cuh).
 #include <algorithm>
 
 #include "norm_ring.cuh"

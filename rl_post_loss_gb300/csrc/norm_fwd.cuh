@@ -7,7 +7,7 @@
 //
 // Bound by memory where a row has one exchange of sums or is short enough for three blocks on an SM (65536 x 6144 bf16, RMS with a
 // residual: 464 us, 102% of the measured copy rate; with an int8 checkpoint 523, 103%); layer norm without a residual waits
-// for its two exchanges (16384 x 6144: 79 us, 76%; 16384 x 8192: 125 us, 63%).
+// for its two exchanges (16384 x 6144: 79 us, 75%; 16384 x 8192: 122 us, 65%; 65536 x 1024: 66 us, 60%).
 #pragma once
 
 #include <algorithm>

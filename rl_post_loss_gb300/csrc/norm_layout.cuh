@@ -140,6 +140,8 @@ constexpr int kBackwardDepth = 3;
 inline bool backward_full(const NormBackwardShape &p, int mode) { return !p.rms || p.want_db || starts_anywhere(mode); }
 
 inline RowMode norm_backward_mode(const NormBackwardShape &p, bool fast) {
+    // bf16 rows with an fp32 dy, a pair that only kAnyRow is built for, go by single columns wherever they start (16384 x 6144
+    // layer norm 232 us, 51% of the measured copy rate; with a bf16 dy 105 us)
     if (!fast || (p.h_es == 2 && p.dy_es == 4)) return p.h_es == 1 ? kShiftRow : kAnyRow;
     // a warp per row where there are rows for all warps
     return p.cols <= (backward_full(p, kBlockRow) ? 768 : 1024) && p.rows >= kNormSMs * kNormWarps ? kWarpRow : kBlockRow;

@@ -7,11 +7,12 @@
 //
 // A team is a block (kBlockRow: two or more on an SM cover each other's exchanges) or, for rows of 1024
 // columns and less, one warp of a block of 16 (kWarpRow: no barriers, and one partial sum for 16 rows at a
-// time); norm_rows.cuh has the third mode, rows that start anywhere.
+// time); of rows that start anywhere a block takes each, in one of two ways (kShiftRow, kAnyRow: norm_rows.cuh).
 //
 // Bound by memory with one exchange a row (65536 x 6144 bf16, RMS with the residual's gradient: 471 us, 101% of the measured copy rate; from
-// int8 416, 100%); reading e4m3 codes costs instructions (65536 x 5120 layer norm 524 us, 66%), and rows of 8192
-// columns leave a block alone on its SM with its exchange (164 us for 16384, 72%).
+// int8 427, 98%); reading e4m3 codes costs instructions (65536 x 5120 layer norm 519 us, 67%), rows of 8192
+// columns leave a block alone on its SM with its exchange (164 us for 16384, 72%), and for the longest fp32 rows with a
+// residual's gradient the weight has room neither in registers nor beside the ring (8192 x 16384 layer norm 468 us, 68%; RMS 341, 93%).
 //
 // FULL = false is the RMS form without db, in which mean = 0 and sum(u) is not needed.
 #pragma once

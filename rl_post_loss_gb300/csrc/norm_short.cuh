@@ -4,9 +4,11 @@
 // way while it works on one batch. Rows that follow one another without a gap come in one copy.
 //
 // Bound by what a row costs beside its bytes, its shuffles and accesses to shared memory: 202752 x 128 bf16 layer norm 25 us forward
-// (63% of the measured copy rate), 39 us backward (61%); 200000 x 512 78 us (77%) and 107 us (85%). (Two vectors a thread with the weights
+// (62% of the measured copy rate), 39 us backward (59%); 200000 x 512 78 us (77%) and 107 us (85%). With a mask every row is a copy of
+// its own and the columns are checked (202752 x 128, a fifth masked: 34 us, 40%, and 58 us, 34%; backward from int8 78 us, 22%), and
+// widths between powers of two leave lanes idle (100000 x 384: 49 us, 47%, and 70 us, 48%). (Two vectors a thread with the weights
 // in registers, twice the lanes a row: 202752 x 128 forward 31 us. Weights that lie as in memory instead of in planes: 26 and 39 us, 93
-// and 114 us; from int8 with a mask, 202752 x 128 backward, 72 against 76.)
+// and 114 us; from int8 with a mask, 202752 x 128 backward, 72 against 76; 78 since every scale byte is read.)
 #pragma once
 
 #include "norm_rows.cuh"
